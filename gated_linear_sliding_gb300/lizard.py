@@ -28,6 +28,10 @@ LIZARD_BF16 = 1
 LIZARD_DECAY_DELAYED = 0
 LIZARD_DECAY_MASKED = 1
 LIZARD_DECAY_LAGGED = 2
+# lizard_act
+LIZARD_ACT_NONE = 0
+LIZARD_ACT_SILU = 1
+LIZARD_ACT_SIGMOID = 2
 
 EXPORTED = ["lizard_attn_fwd_workspace", "lizard_workspace_init", "lizard_attn_fwd",
             "lizard_attn_bwd_workspace", "lizard_attn_bwd", "lizard_decode_workspace",
@@ -38,7 +42,11 @@ EXPORTED = ["lizard_attn_fwd_workspace", "lizard_workspace_init", "lizard_attn_f
             "lizard_attn_fwd_varlen_workspace",
             "lizard_attn_bwd_varlen_workspace", "lizard_attn_bwd_varlen",
             "lizard_attn_fwd_noalloc_scratch", "lizard_read_noalloc_status",
-            "lizard_qkvg_proj", "lizard_qkvg_proj_bwd", "lizard_gate_cache_fill"]
+            "lizard_qkvg_proj", "lizard_qkvg_proj_bwd", "lizard_gate_cache_fill",
+            "lizard_conv_fwd", "lizard_conv_bwd_workspace", "lizard_conv_bwd", "lizard_conv_step",
+            "lizard_scan_fwd_workspace", "lizard_scan_states_bytes", "lizard_scan_fwd",
+            "lizard_scan_bwd_workspace", "lizard_scan_bwd", "lizard_scan_step",
+            "lizard_block_norm_fwd", "lizard_block_norm_bwd_workspace", "lizard_block_norm_bwd"]
 
 
 class lizard_dims(ctypes.Structure):
@@ -46,6 +54,25 @@ class lizard_dims(ctypes.Structure):
                 ("Hkv", ctypes.c_int64), ("d", ctypes.c_int64), ("D", ctypes.c_int64),
                 ("w", ctypes.c_int64), ("M", ctypes.c_int64), ("chunk", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("decay", ctypes.c_int32)]
+
+
+def _fields(int64s: str, floats: str, int32s: str):
+    return [(n, t) for names, t in ((int64s, ctypes.c_int64), (floats, ctypes.c_float),
+                                    (int32s, ctypes.c_int32)) for n in names.split()]
+
+
+class lizard_conv_dims(ctypes.Structure):
+    _fields_ = _fields("B L C K nseq ldx ldy lddx", "", "dtype act")
+
+
+class lizard_scan_dims(ctypes.Structure):
+    _fields_ = _fields("B L C N G nseq ldx lddt ldz ldb ldc ldy lddx ldddt lddz lddb lddc", "",
+                       "dtype softplus")
+
+
+class lizard_norm_dims(ctypes.Structure):
+    _fields_ = _fields("T D groups ldo ldg ldr ldro ldn lddo lddg lddr", "eps_post eps_pre",
+                       "dtype res_dtype act gate_first")
 
 
 class LizardError(RuntimeError):
@@ -115,6 +142,24 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.lizard_status_string.restype = ctypes.c_char_p
     lib.lizard_profile_events.argtypes = [_VP, _VP]
     lib.lizard_profile_events.restype = ctypes.c_int
+    dims_of_call = {"conv": ctypes.POINTER(lizard_conv_dims),
+                    "scan": ctypes.POINTER(lizard_scan_dims),
+                    "block": ctypes.POINTER(lizard_norm_dims)}
+    sz = ctypes.c_size_t
+    for name, rest in (("lizard_conv_fwd", [_VP] * 8 + [sz, _VP]),
+                       ("lizard_conv_bwd", [_VP] * 12 + [sz, _VP]),
+                       ("lizard_conv_step", [_VP] * 4 + [ctypes.c_int64] + [_VP] * 3 + [sz, _VP]),
+                       ("lizard_scan_fwd", [_VP] * 14 + [sz, _VP]),
+                       ("lizard_scan_bwd", [_VP] * 23 + [sz, _VP]),
+                       ("lizard_scan_step", [_VP] * 9 + [ctypes.c_int64] + [_VP] * 3 + [sz, _VP]),
+                       ("lizard_block_norm_fwd", [_VP] * 9),
+                       ("lizard_block_norm_bwd", [_VP] * 15 + [sz, _VP]),
+                       ("lizard_conv_bwd_workspace", None), ("lizard_scan_fwd_workspace", None),
+                       ("lizard_scan_states_bytes", None), ("lizard_scan_bwd_workspace", None),
+                       ("lizard_block_norm_bwd_workspace", None)):
+        fn = getattr(lib, name)
+        fn.argtypes = [dims_of_call[name.split("_")[1]]] + (rest or [])
+        fn.restype = sz if rest is None else ctypes.c_int
     lib.lizard_version.argtypes = []
     lib.lizard_version.restype = ctypes.c_char_p
     _lib = lib
@@ -537,3 +582,354 @@ def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=No
                                      _stream(stream))
     _check(st, "lizard_qkvg_proj_bwd")
     return dx, dW
+
+
+# ---- the selective state space block -----------------------------------------------------
+#
+# Activations are [B, L, width] (dtype fp32 or bf16) and may be column ranges of wider rows: the
+# last axes contiguous, every token the same distance after the one before.  Parameters, scan
+# states and parameter gradients are fp32 and contiguous.  cu_seqlens packs sequences into one row
+# (B = 1): int64 offsets on the device, read when the kernels run, or host integers, which are
+# checked and copied.
+
+
+def _ld(t, name, shape, dtype):
+    """Distance between the token rows of t (0 when dense); t has `shape`, whose leading axes
+    (one for [B, width], else two) count tokens."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.is_contiguous():
+        return 0
+    lead = 1 if len(shape) == 2 else 2
+    width, inner = 1, t.stride()[lead:]
+    for size, stride in zip(reversed(shape[lead:]), reversed(inner)):
+        if size > 1 and stride != width:
+            raise ValueError(f"{name}: the values of a token must be contiguous")
+        width *= size
+    st = t.stride()
+    if lead == 1:
+        ld = st[0]
+        ok = True
+    else:
+        ld = st[1] if shape[1] > 1 else st[0]
+        ok = shape[0] == 1 or shape[1] == 1 or st[0] == shape[1] * st[1]
+    if not ok or ld < width:
+        raise ValueError(f"{name}: token rows must be evenly spaced and not overlap")
+    return ld
+
+
+def _need_same(t, name, shape):
+    """An optional fp32 parameter or state; its address (None when absent)."""
+    if t is None:
+        return None
+    _need(t, name, shape, torch.float32)
+    return t.data_ptr()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _packed(cu_seqlens, B, L, device):
+    """(number of packed sequences, device offsets or None)."""
+    if cu_seqlens is None:
+        return 0, None
+    if B != 1:
+        raise ValueError("cu_seqlens packs sequences into one row: B must be 1")
+    if not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda):
+        cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int64))
+        if cu.ndim != 1 or cu.size < 2 or cu[0] != 0 or cu[-1] != L or (np.diff(cu) < 0).any():
+            raise ValueError("cu_seqlens: inconsistent offsets")
+        cu_seqlens = torch.from_numpy(cu).to(device)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens: at least two offsets in one axis")
+    _need(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int64)
+    return cu_seqlens.numel() - 1, cu_seqlens
+
+
+def _scratch(workspace, nbytes, device):
+    """A workspace of the call's own (its status word is not read by anyone) where none is
+    given."""
+    if workspace is not None:
+        return workspace
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def _slots(slots, B):
+    if slots is None:
+        return None
+    _need(slots, "slots", (B,), torch.int64)
+    return slots.data_ptr()
+
+
+def lizard_conv_fwd(x, w, bias=None, *, act: int = LIZARD_ACT_NONE, state_in=None, state_out=None,
+                    cu_seqlens=None, y=None, workspace=None, stream=None):
+    """Short causal depthwise convolution of x [B, L, C] with w [C, K]; returns y [B, L, C].
+    state_in, state_out [B or sequences, K-1, C]: the inputs before each sequence's first token
+    and its last ones (state_out may be state_in)."""
+    B, L, C = x.shape
+    K, dt = w.shape[1], x.dtype
+    nseq, cu = _packed(cu_seqlens, B, L, x.device)
+    n = nseq or B
+    if y is None:
+        y = torch.empty((B, L, C), dtype=dt, device=x.device)
+    for t, name in ((state_in, "state_in"), (state_out, "state_out")):
+        if t is not None:
+            _need(t, name, (n, K - 1, C), dt)
+    dims = lizard_conv_dims(B, L, C, K, nseq, _ld(x, "x", (B, L, C), dt),
+                            _ld(y, "y", (B, L, C), dt), 0, _dtype_code(x), act)
+    st = load().lizard_conv_fwd(ctypes.byref(dims), x.data_ptr(), _need_same(w, "w", (C, K)),
+                                _need_same(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
+                                y.data_ptr(), _ptr(state_out), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(st, "lizard_conv_fwd")
+    return y
+
+
+def lizard_conv_bwd_workspace(dims) -> int:
+    return int(load().lizard_conv_bwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None,
+                    dstate_out=None, dstate_in=None, cu_seqlens=None, dx=None, workspace=None,
+                    stream=None):
+    """Gradients dx, dw, dbias of lizard_conv_fwd's y against dy (bias and dbias may be None);
+    dstate_out is the gradient of state_out, dstate_in (if given) receives that of state_in."""
+    B, L, C = x.shape
+    K, dt = w.shape[1], x.dtype
+    nseq, cu = _packed(cu_seqlens, B, L, x.device)
+    n = nseq or B
+    if dx is None:
+        dx = torch.empty((B, L, C), dtype=dt, device=x.device)
+    for t, name in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
+        if t is not None:
+            _need(t, name, (n, K - 1, C), dt)
+    dw = torch.empty((C, K), dtype=torch.float32, device=x.device)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dims = lizard_conv_dims(B, L, C, K, nseq, _ld(x, "x", (B, L, C), dt),
+                            _ld(dy, "dy", (B, L, C), dt), _ld(dx, "dx", (B, L, C), dt),
+                            _dtype_code(x), act)
+    workspace = _scratch(workspace, lizard_conv_bwd_workspace(dims), x.device)
+    st = load().lizard_conv_bwd(ctypes.byref(dims), x.data_ptr(), _need_same(w, "w", (C, K)),
+                                _need_same(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
+                                dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dw.data_ptr(),
+                                _ptr(dbias), _ptr(dstate_in), workspace.data_ptr(),
+                                workspace.numel(), _stream(stream))
+    _check(st, "lizard_conv_bwd")
+    return dict(dx=dx, dw=dw, dbias=dbias, dstate_in=dstate_in)
+
+
+def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NONE, y=None,
+                     workspace=None, stream=None):
+    """One token for each of B sequences: y [B, C] from x [B, C]; state [slots, K-1, C] is moved
+    on IN PLACE.  slots: int64 device tensor [B] naming each row's state (negative: an idle row),
+    or None (row b uses entry b)."""
+    B, C = x.shape
+    K, dt = w.shape[1], x.dtype
+    if y is None:
+        y = torch.empty((B, C), dtype=dt, device=x.device)
+    _need(state, "state", (state.shape[0], K - 1, C), dt)
+    dims = lizard_conv_dims(B, 1, C, K, 0, _ld(x, "x", (B, C), dt), _ld(y, "y", (B, C), dt), 0,
+                            _dtype_code(x), act)
+    st = load().lizard_conv_step(ctypes.byref(dims), x.data_ptr(), _need_same(w, "w", (C, K)),
+                                 _need_same(bias, "bias", (C,)), state.data_ptr(), state.shape[0],
+                                 _slots(slots, B), y.data_ptr(), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(st, "lizard_conv_step")
+    return y
+
+
+def _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq):
+    """lizard_scan_dims of the inputs, and the addresses of x, dt, A, Bm, Cm, D, z, dt_bias."""
+    tp, lead = x.dtype, tuple(x.shape[:-1])
+    C, N = A.shape
+    G = Bm.shape[-2]
+    wide, group = lead + (C,), lead + (G, N)
+    dims = lizard_scan_dims(B=lead[0], L=lead[1] if len(lead) == 2 else 1, C=C, N=N, G=G,
+                            nseq=nseq, ldx=_ld(x, "x", wide, tp), lddt=_ld(dt, "dt", wide, tp),
+                            ldz=0 if z is None else _ld(z, "z", wide, tp),
+                            dtype=_dtype_code(x), softplus=int(softplus))
+    if len(lead) == 1:  # [B, G, N]: seen as [B, 1, G, N], so that the groups are not tokens
+        dims.ldb = _ld(Bm.unsqueeze(1), "Bm", (lead[0], 1, G, N), tp)
+        dims.ldc = _ld(Cm.unsqueeze(1), "Cm", (lead[0], 1, G, N), tp)
+    else:
+        dims.ldb = _ld(Bm, "Bm", group, tp)
+        dims.ldc = _ld(Cm, "Cm", group, tp)
+    return dims, (x.data_ptr(), dt.data_ptr(), _need_same(A, "A", (C, N)), Bm.data_ptr(),
+                  Cm.data_ptr(), _need_same(D, "D", (C,)), _ptr(z),
+                  _need_same(dt_bias, "dt_bias", (C,)))
+
+
+def lizard_scan_fwd_workspace(dims) -> int:
+    return int(load().lizard_scan_fwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_scan_bwd_workspace(dims) -> int:
+    return int(load().lizard_scan_bwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_scan_states_bytes(dims) -> int:
+    return int(load().lizard_scan_states_bytes(ctypes.byref(dims)))
+
+
+def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus: bool = True,
+                    h0=None, h_out=None, cu_seqlens=None, y=None, save_states: bool = False,
+                    workspace=None, stream=None):
+    """Selective scan of x [B, L, C] with step sizes dt [B, L, C], rates A [C, N], input and
+    output vectors Bm, Cm [B, L, G, N], skip D [C] and output gate z [B, L, C]; returns y, or
+    (y, states) with save_states, which lizard_scan_bwd takes.  h0, h_out [B or sequences, C, N]
+    fp32: the states before and after (h_out may be h0)."""
+    B, L, C = x.shape
+    nseq, cu = _packed(cu_seqlens, B, L, x.device)
+    dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq)
+    if y is None:
+        y = torch.empty((B, L, C), dtype=x.dtype, device=x.device)
+    dims.ldy = _ld(y, "y", (B, L, C), x.dtype)
+    shape = (nseq or B, C, A.shape[1])
+    lib = load()
+    states = None
+    if save_states:
+        states = torch.empty(lizard_scan_states_bytes(dims), dtype=torch.uint8, device=x.device)
+    workspace = _scratch(workspace, lib.lizard_scan_fwd_workspace(ctypes.byref(dims)), x.device)
+    st = lib.lizard_scan_fwd(ctypes.byref(dims), *ptrs, _need_same(h0, "h0", shape), _ptr(cu),
+                             y.data_ptr(), _need_same(h_out, "h_out", shape), _ptr(states),
+                             workspace.data_ptr(), workspace.numel(), _stream(stream))
+    _check(st, "lizard_scan_fwd")
+    return (y, states) if save_states else y
+
+
+def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=None,
+                    softplus: bool = True, h0=None, dh_out=None, dh0=None, cu_seqlens=None,
+                    dx=None, ddt=None, dz=None, dBm=None, dCm=None, workspace=None, stream=None):
+    """Gradients dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias of lizard_scan_fwd's y against dy, from
+    the same inputs and the states that call returned (None for an absent D, z, dt_bias).
+    dh_out is the gradient of h_out; dh0 (if given) receives that of h0."""
+    B, L, C = x.shape
+    nseq, cu = _packed(cu_seqlens, B, L, x.device)
+    dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq)
+    tp, N, wide = x.dtype, A.shape[1], (B, L, C)
+    group = (B, L, dims.G, N)
+    dims.ldy = _ld(dy, "dy", wide, tp)
+
+    def out(t, shape):
+        return torch.empty(shape, dtype=tp, device=x.device) if t is None else t
+
+    dx, ddt, dBm, dCm = out(dx, wide), out(ddt, wide), out(dBm, group), out(dCm, group)
+    dz = None if z is None else out(dz, wide)
+    dims.lddx, dims.ldddt = _ld(dx, "dx", wide, tp), _ld(ddt, "ddt", wide, tp)
+    dims.lddz = 0 if dz is None else _ld(dz, "dz", wide, tp)
+    dims.lddb, dims.lddc = _ld(dBm, "dBm", group, tp), _ld(dCm, "dCm", group, tp)
+    dA = torch.empty_like(A)
+    dD = None if D is None else torch.empty_like(D)
+    ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
+    _need(states, "states", (lizard_scan_states_bytes(dims),), torch.uint8)
+    shape = (nseq or B, C, N)
+    lib = load()
+    workspace = _scratch(workspace, lib.lizard_scan_bwd_workspace(ctypes.byref(dims)), x.device)
+    st = lib.lizard_scan_bwd(ctypes.byref(dims), *ptrs, _need_same(h0, "h0", shape), _ptr(cu),
+                             states.data_ptr(), dy.data_ptr(),
+                             _need_same(dh_out, "dh_out", shape), dx.data_ptr(), ddt.data_ptr(),
+                             _ptr(dz), dBm.data_ptr(), dCm.data_ptr(), dA.data_ptr(), _ptr(dD),
+                             _ptr(ddt_bias), _need_same(dh0, "dh0", shape), workspace.data_ptr(),
+                             workspace.numel(), _stream(stream))
+    _check(st, "lizard_scan_bwd")
+    return dict(dx=dx, ddt=ddt, dA=dA, dBm=dBm, dCm=dCm, dD=dD, dz=dz, ddt_bias=ddt_bias, dh0=dh0)
+
+
+def lizard_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None,
+                     softplus: bool = True, slots=None, y=None, workspace=None, stream=None):
+    """One token for each of B sequences: y [B, C] from x, dt, z [B, C] and Bm, Cm [B, G, N];
+    state [slots, C, N] fp32 is moved on IN PLACE.  slots as for lizard_conv_step."""
+    dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, 0)
+    B, C = x.shape
+    if y is None:
+        y = torch.empty((B, C), dtype=x.dtype, device=x.device)
+    dims.ldy = _ld(y, "y", (B, C), x.dtype)
+    nslots = state.shape[0]
+    st = load().lizard_scan_step(ctypes.byref(dims), *ptrs,
+                                 _need_same(state, "state", (nslots, C, dims.N)), nslots,
+                                 _slots(slots, B), y.data_ptr(), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(st, "lizard_scan_step")
+    return y
+
+
+def _norm_inputs(o, gate, r, w_post, scale, w_pre, res_dtype, groups, act, gate_first, eps,
+                 eps_pre):
+    """lizard_norm_dims of the inputs, and the addresses of o, gate, r, w_post, scale, w_pre."""
+    shape, tp = tuple(o.shape), o.dtype
+    D = shape[1]
+    dims = lizard_norm_dims(T=shape[0], D=D, groups=groups, ldo=_ld(o, "o", shape, tp),
+                            ldg=0 if gate is None else _ld(gate, "gate", shape, tp),
+                            ldr=0 if r is None else _ld(r, "r", shape, res_dtype),
+                            eps_post=eps, eps_pre=eps if eps_pre is None else eps_pre,
+                            dtype=_dtype_code(o),
+                            res_dtype=LIZARD_F32 if res_dtype == torch.float32 else LIZARD_BF16,
+                            act=act, gate_first=int(gate_first))
+    return dims, (o.data_ptr(), _ptr(gate), _ptr(r), _need_same(w_post, "w_post", (D,)),
+                  _need_same(scale, "scale", (D,)), _need_same(w_pre, "w_pre", (D,)))
+
+
+def lizard_block_norm_fwd(o, *, gate=None, r=None, w_post=None, scale=None, w_pre=None,
+                          groups: int = 1, act: int = LIZARD_ACT_SILU, gate_first: bool = False,
+                          eps: float = 1e-5, eps_pre=None, r_out=None, n_out=None, stream=None):
+    """Norm after a block with its gate, residual scale and add, and the norm before the next
+    block: o [T, D] is the block's output, r [T, D] the residual stream (its dtype or fp32).
+    Returns (r_out, n_out); n_out is None without w_pre.  r_out takes r's dtype, or o's."""
+    shape = tuple(o.shape)
+    if len(shape) != 2:
+        raise ValueError("o must be [T, D]")
+    rtp = r.dtype if r is not None else r_out.dtype if r_out is not None else o.dtype
+    dims, ptrs = _norm_inputs(o, gate, r, w_post, scale, w_pre, rtp, groups, act, gate_first, eps,
+                              eps_pre)
+    if r_out is None:
+        r_out = torch.empty(shape, dtype=rtp, device=o.device)
+    dims.ldro = _ld(r_out, "r_out", shape, rtp)
+    if w_pre is not None:
+        if n_out is None:
+            n_out = torch.empty(shape, dtype=o.dtype, device=o.device)
+        dims.ldn = _ld(n_out, "n_out", shape, o.dtype)
+    elif n_out is not None:
+        raise ValueError("n_out needs w_pre")
+    st = load().lizard_block_norm_fwd(ctypes.byref(dims), *ptrs, r_out.data_ptr(), _ptr(n_out),
+                                      _stream(stream))
+    _check(st, "lizard_block_norm_fwd")
+    return r_out, n_out
+
+
+def lizard_block_norm_bwd_workspace(dims) -> int:
+    return int(load().lizard_block_norm_bwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_post=None,
+                          scale=None, w_pre=None, groups: int = 1, act: int = LIZARD_ACT_SILU,
+                          gate_first: bool = False, eps: float = 1e-5, eps_pre=None,
+                          workspace=None, stream=None):
+    """Gradients do, dgate, dr, dw_post, dscale, dw_pre of lizard_block_norm_fwd against dr_out
+    and dn_out (one may be None; dn_out goes with w_pre), from the forward's inputs; None for an
+    absent input."""
+    shape = tuple(o.shape)
+    rtp = r.dtype if r is not None else dr_out.dtype if dr_out is not None else o.dtype
+    dims, ptrs = _norm_inputs(o, gate, r, w_post, scale, w_pre, rtp, groups, act, gate_first, eps,
+                              eps_pre)
+    if dr_out is not None:
+        dims.ldro = _ld(dr_out, "dr_out", shape, rtp)
+    if dn_out is not None:
+        dims.ldn = _ld(dn_out, "dn_out", shape, o.dtype)
+
+    def like(t, dtype=None):
+        return None if t is None else torch.empty(tuple(t.shape), dtype=dtype or t.dtype, device=o.device)
+
+    do, dgate, dr = like(o), like(gate), like(r)
+    dw_post, dscale, dw_pre = like(w_post), like(scale), like(w_pre)
+    workspace = _scratch(workspace, lizard_block_norm_bwd_workspace(dims), o.device)
+    st = load().lizard_block_norm_bwd(ctypes.byref(dims), *ptrs, _ptr(dr_out), _ptr(dn_out),
+                                      do.data_ptr(), _ptr(dgate), _ptr(dr), _ptr(dw_post),
+                                      _ptr(dscale), _ptr(dw_pre), workspace.data_ptr(),
+                                      workspace.numel(), _stream(stream))
+    _check(st, "lizard_block_norm_bwd")
+    return dict(do=do, dgate=dgate, dr=dr, dw_post=dw_post, dscale=dscale, dw_pre=dw_pre)

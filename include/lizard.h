@@ -340,6 +340,195 @@ lizard_status lizard_decode_step_positions(const lizard_dims* dims, const int64_
                                            void* vcache, void* gcache, void* workspace,
                                            size_t ws_bytes, void* stream);
 
+/* ---- The selective state space block ------------------------------------------------------
+ *
+ * A second constant-memory token mixer next to the one above, and what stands around a mixer:
+ *   lizard_conv_*        the short causal depthwise convolution in front of a scan;
+ *   lizard_scan_*        the selective state space scan (prompts, training, single tokens);
+ *   lizard_block_norm_*  the norm after a block with its gate, residual scale and residual add,
+ *                        and the norm in front of the next block, in one pass.
+ * The conventions at the head of this file hold, with these additions:
+ *   - Element type `dtype` applies to the activations (x, dt, z, Bm, Cm, y, gate, o, the
+ *     convolution's state and the gradients of all of these).  Per-channel parameters (w, bias,
+ *     A, D, dt_bias, w_post, scale, w_pre), scan states and parameter gradients are fp32.
+ *     Sums, states and norms are held in fp32.
+ *   - Token rows may be strided: each activation [B, L, width] has its own distance between
+ *     consecutive tokens, in elements (the ld* fields; 0 means the width, i.e. dense rows), so
+ *     that a call can read a column range of a wider projection.  Row (b, t) is at
+ *     (b L + t) ld.  Base pointers are 16-byte aligned; a distance that is not a whole number of
+ *     16-byte groups, or a width that is not, is served by a slower element-wise path.
+ *   - Packed batches: nseq > 0 selects nseq sequences of different lengths laid one after
+ *     another in one row (B = 1, L = all tokens); cu_seqlens is a DEVICE array of nseq + 1 int64
+ *     offsets (cu[0] = 0, non-decreasing, cu[nseq] = L), read when the kernels run, so that a
+ *     captured CUDA graph can be replayed on other lengths.  nseq = 0: a dense batch of B
+ *     sequences of L tokens, cu_seqlens ignored.  Per-sequence states have B or nseq entries.
+ *     Inconsistent offsets never cause an access out of bounds; they record
+ *     LIZARD_ERR_INVALID_ARG in the workspace's status word where a workspace is given, and the
+ *     results of that call are not defined.
+ *   - L may be 0 (a packed batch of empty sequences): states are passed on, nothing else is
+ *     written; parameter gradients are 0. */
+
+/* act(v): v, v sigmoid(v), or sigmoid(v). */
+typedef enum { LIZARD_ACT_NONE = 0, LIZARD_ACT_SILU = 1, LIZARD_ACT_SIGMOID = 2 } lizard_act;
+
+/* Sizes of the short convolution: B sequences of L tokens (or nseq packed ones), C channels,
+ * K taps, 1 <= K <= 8; act is NONE or SILU. */
+typedef struct {
+    int64_t B, L, C, K, nseq;
+    int64_t ldx, ldy; /* token distances of x; of y and dy */
+    int64_t lddx;     /* of dx (backward) */
+    int32_t dtype, act;
+} lizard_conv_dims;
+
+/* y[t, c] = act(bias[c] + sum_{j < K} w[c, j] x[t - K + 1 + j, c]) within each sequence.
+ *   x, y      [B, L, C];   w [C, K] fp32;   bias [C] fp32 or NULL;
+ *   state_in  [B or nseq, K-1, C] dtype or NULL (zeros): the K-1 inputs before each sequence's
+ *             first token, oldest first;
+ *   state_out likewise, or NULL: the last K-1 inputs of (state_in, x), for the next call or for
+ *             lizard_conv_step; may be the same array as state_in (not a part of it);
+ *   workspace optional (NULL, 0): >= 256 bytes whose status word takes device-side errors. */
+lizard_status lizard_conv_fwd(const lizard_conv_dims* dims, const void* x, const float* w,
+                              const float* bias, const void* state_in, const int64_t* cu_seqlens,
+                              void* y, void* state_out, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* Bytes of device workspace lizard_conv_bwd needs (0 for invalid dims): the status word and
+ * one [K + 1, C] fp32 partial sum of dw and dbias per run of tokens. */
+size_t lizard_conv_bwd_workspace(const lizard_conv_dims* dims);
+
+/* Exact gradient of lizard_conv_fwd's y (and of state_out).
+ *   dy [B, L, C]; dstate_out [B or nseq, K-1, C] dtype or NULL: gradients of y and of state_out;
+ *   dx [B, L, C]; dw [C, K], dbias [C] fp32 (dbias NULL where there is no bias);
+ *   dstate_in [B or nseq, K-1, C] dtype or NULL.  Every output is overwritten; dstate_in is not
+ *   dstate_out.  Reductions use a fixed order (deterministic). */
+lizard_status lizard_conv_bwd(const lizard_conv_dims* dims, const void* x, const float* w,
+                              const float* bias, const void* state_in, const int64_t* cu_seqlens,
+                              const void* dy, const void* dstate_out, void* dx, float* dw,
+                              float* dbias, void* dstate_in, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* One token for each of B sequences (dims.L and nseq are ignored): y [B, C] from x [B, C] and
+ * the state, which is moved on by one token IN PLACE.
+ *   state     [nslots, K-1, C] dtype;
+ *   slots     NULL (sequence b's state is entry b, nslots >= B) or a DEVICE array [B] of int64:
+ *             sequence b's state is entry slots[b].  A negative slot is an idle row: its y is
+ *             zero and no state is touched.  A slot >= nslots does the same and records
+ *             LIZARD_ERR_INVALID_ARG in the status word.  Two rows may not name one slot.
+ *   workspace optional (NULL, 0): >= 256 bytes with a status word. */
+lizard_status lizard_conv_step(const lizard_conv_dims* dims, const void* x, const float* w,
+                               const float* bias, void* state, int64_t nslots,
+                               const int64_t* slots, void* y, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* Sizes of the scan: B sequences of L tokens (or nseq packed ones), C channels with N states
+ * each, 1 <= N <= 64, and G groups of C / G channels that share Bm and Cm.
+ * softplus != 0: the step size is softplus(dt + dt_bias), else dt + dt_bias itself. */
+typedef struct {
+    int64_t B, L, C, N, G, nseq;
+    int64_t ldx, lddt, ldz, ldb, ldc, ldy;   /* token distances of x, dt, z, Bm, Cm; y and dy */
+    int64_t lddx, ldddt, lddz, lddb, lddc;   /* of the gradients dx, ddt, dz, dBm, dCm */
+    int32_t dtype, softplus;
+} lizard_scan_dims;
+
+/* Bytes of device workspace lizard_scan_fwd needs (0 for invalid dims): the status word, plus,
+ * where the batch has too few (sequence, channel) pairs to fill the GPU and the time axis is cut
+ * into segments, one fp32 state and one decay exponent per (segment, channel). */
+size_t lizard_scan_fwd_workspace(const lizard_scan_dims* dims);
+
+/* Bytes of the states that lizard_scan_fwd keeps for lizard_scan_bwd (0 for invalid dims): one
+ * fp32 state [C, N] for every 16 tokens of each row of the batch. */
+size_t lizard_scan_states_bytes(const lizard_scan_dims* dims);
+
+/* The selective scan.  With d[t,c] = softplus(dt[t,c] + dt_bias[c]):
+ *   h[t,c,n] = exp(d[t,c] A[c,n]) h[t-1,c,n] + d[t,c] x[t,c] Bm[t,g(c),n]
+ *   y[t,c]   = (sum_n Cm[t,g(c),n] h[t,c,n] + D[c] x[t,c]) silu(z[t,c]),   g(c) = c / (C / G).
+ *   x, dt, z, y  [B, L, C] (z NULL: no gate);   Bm, Cm [B, L, G, N];
+ *   A [C, N] fp32;   D, dt_bias [C] fp32 or NULL (zero);
+ *   h0     [B or nseq, C, N] fp32 or NULL (zero): the state before each sequence's first token;
+ *   h_out  likewise or NULL: the state after its last token (h0's, or zero, for an empty
+ *          sequence); may be the same array as h0;
+ *   states NULL, or lizard_scan_states_bytes(dims) bytes kept for lizard_scan_bwd;
+ *   workspace, ws_bytes >= lizard_scan_fwd_workspace(dims). */
+lizard_status lizard_scan_fwd(const lizard_scan_dims* dims, const void* x, const void* dt,
+                              const float* A, const void* Bm, const void* Cm, const float* D,
+                              const void* z, const float* dt_bias, const float* h0,
+                              const int64_t* cu_seqlens, void* y, float* h_out, void* states,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace lizard_scan_bwd needs (0 for invalid dims). */
+size_t lizard_scan_bwd_workspace(const lizard_scan_dims* dims);
+
+/* Exact gradient of lizard_scan_fwd's y (and of h_out), from the same inputs, the states that
+ * the forward kept, and h0 and cu_seqlens as then.
+ *   dy [B, L, C]; dh_out [B or nseq, C, N] fp32 or NULL: gradients of y and of h_out;
+ *   dx, ddt, dz [B, L, C] (dz NULL where there is no z); dBm, dCm [B, L, G, N] (the sums over a
+ *   group's channels); dA [C, N], dD, ddt_bias [C] fp32 (dD, ddt_bias NULL where there is no D,
+ *   dt_bias); dh0 [B or nseq, C, N] fp32 or NULL; dh0 is not dh_out.  Every output is
+ *   overwritten.  Reductions use a fixed order (deterministic). */
+lizard_status lizard_scan_bwd(const lizard_scan_dims* dims, const void* x, const void* dt,
+                              const float* A, const void* Bm, const void* Cm, const float* D,
+                              const void* z, const float* dt_bias, const float* h0,
+                              const int64_t* cu_seqlens, const void* states, const void* dy,
+                              const float* dh_out, void* dx, void* ddt, void* dz, void* dBm,
+                              void* dCm, float* dA, float* dD, float* ddt_bias, float* dh0,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* One token for each of B sequences (dims.L and nseq are ignored): x, dt, z, y [B, C], Bm, Cm
+ * [B, G, N]; state [nslots, C, N] fp32 is moved on by one token IN PLACE.  slots, nslots and
+ * workspace as for lizard_conv_step. */
+lizard_status lizard_scan_step(const lizard_scan_dims* dims, const void* x, const void* dt,
+                               const float* A, const void* Bm, const void* Cm, const float* D,
+                               const void* z, const float* dt_bias, float* state, int64_t nslots,
+                               const int64_t* slots, void* y, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* Sizes of the norms around a block: T rows of D values, 1 <= D <= 16384; the norm after the
+ * block runs over `groups` equal parts of a row (1 <= groups, D % groups == 0), the norm in
+ * front of the next block over the whole row.  Rows may be strided (ld*, 0: D).  res_dtype is
+ * the type of the residual stream (r, r_out, dr_out, dr): dtype or LIZARD_F32. */
+typedef struct {
+    int64_t T, D, groups;
+    int64_t ldo, ldg, ldr, ldro, ldn;   /* row distances of o, gate, r; r_out and dr_out; n_out and dn_out */
+    int64_t lddo, lddg, lddr;           /* of do, dgate, dr (backward) */
+    float eps_post, eps_pre;
+    int32_t dtype, res_dtype;
+    int32_t act;        /* lizard_act of the gate: SILU or SIGMOID (ignored without a gate) */
+    int32_t gate_first; /* the gate multiplies before (1) or after (0) the norm after the block */
+} lizard_norm_dims;
+
+/* With norm(v) = v / sqrt(mean(v^2) + eps):
+ *   u = o act(gate)                 if gate_first, else o
+ *   n = w_post norm_groups(u)       (w_post NULL: n = u, no norm)
+ *   n = n act(gate)                 unless gate_first
+ *   rr = r + scale n                (r NULL: 0; scale NULL: 1)
+ *   r_out = rr,   n_out = w_pre norm(rr).
+ * Each output is rounded once, from fp32 values: n_out comes from rr before r_out's rounding.
+ *   o, gate, n_out [T, D] dtype (gate NULL: none); r, r_out [T, D] res_dtype;
+ *   w_post, scale, w_pre [D] fp32 or NULL.  r_out may be NULL, n_out and w_pre may be NULL
+ *   together; one of r_out and n_out is given.  r_out may be r, and n_out may be o or gate
+ *   (same distances); otherwise outputs do not overlap inputs. */
+lizard_status lizard_block_norm_fwd(const lizard_norm_dims* dims, const void* o, const void* gate,
+                                    const void* r, const float* w_post, const float* scale,
+                                    const float* w_pre, void* r_out, void* n_out, void* stream);
+
+/* Bytes of device workspace lizard_block_norm_bwd needs (0 for invalid dims): the status word
+ * and the partial sums of the parameter gradients, whose number does not depend on T once the
+ * rows fill the GPU. */
+size_t lizard_block_norm_bwd_workspace(const lizard_norm_dims* dims);
+
+/* Exact gradient of lizard_block_norm_fwd from its inputs (nothing is kept by the forward).
+ *   dr_out [T, D] res_dtype, dn_out [T, D] dtype: gradients of r_out and n_out (one may be NULL;
+ *   dn_out is given exactly when w_pre is);
+ *   d_o, dgate [T, D] dtype, dr [T, D] res_dtype (dgate NULL exactly when gate is; dr may be
+ *   NULL); dw_post, dscale, dw_pre [D] fp32, NULL exactly when the parameter is.  Every output
+ *   is overwritten.  Reductions use a fixed order (deterministic). */
+lizard_status lizard_block_norm_bwd(const lizard_norm_dims* dims, const void* o, const void* gate,
+                                    const void* r, const float* w_post, const float* scale,
+                                    const float* w_pre, const void* dr_out, const void* dn_out,
+                                    void* d_o, void* dgate, void* dr, float* dw_post,
+                                    float* dscale, float* dw_pre, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read the device status word of `workspace` and clear it.
  * Returns LIZARD_OK or the first error a kernel recorded (e.g. LIZARD_ERR_TIMEOUT). */
 lizard_status lizard_read_device_status(void* workspace, void* stream);
