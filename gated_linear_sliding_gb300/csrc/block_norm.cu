@@ -13,7 +13,9 @@
 namespace lz {
 namespace {
 
-// Sum over a CTA's (TPR > 32) or a warp's threads, the same value in each of them.
+// Sum over a CTA's (TPR > 32) or a warp's threads, the same value in each of them.  Consecutive
+// sums of a CTA alternate between two buffers: the barrier of the one in between is what lets a
+// buffer be written again.
 template <int TPR, int NVAL>
 __device__ __forceinline__ void row_sum(float* v, float (*red)[32]) {
 #pragma unroll
@@ -22,7 +24,6 @@ __device__ __forceinline__ void row_sum(float* v, float (*red)[32]) {
         for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(~0u, v[k], o);
     if constexpr (TPR > 32) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        __syncthreads();  // the last sum's readers are done
         if (lane == 0)
 #pragma unroll
             for (int k = 0; k < NVAL; ++k) red[k][warp] = v[k];
@@ -70,7 +71,6 @@ __device__ __forceinline__ void group_sum(float* p, int nvec, int gv, float* sm,
     }
 }
 
-template <bool FAST>
 __device__ __forceinline__ float act_of(int act, float g, float sg) { return act == LIZARD_ACT_SILU ? g * sg : sg; }
 __device__ __forceinline__ float dact_of(int act, float g, float sg) {
     return act == LIZARD_ACT_SILU ? dsilu(g, sg) : sg * (1.0f - sg);
@@ -81,8 +81,8 @@ template <typename T, typename R, int V, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const NormArgs a) {
     constexpr int RPC = TPR < 128 ? 128 / TPR : 1;
     constexpr bool FAST = is_fast<T>();
-    __shared__ float red[2][32];
-    extern __shared__ float gsm[];
+    __shared__ float red[2][1][32];
+    extern __shared__ __align__(16) float gsm[];
     const int lr = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPC + threadIdx.x / TPR;
     if (TPR == 32 && row >= a.T) return;  // a whole warp
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                ga[i][j] = act_of<FAST>(a.act, ga[i][j], sigm<FAST>(ga[i][j]));
+                ga[i][j] = act_of(a.act, ga[i][j], sigm<FAST>(ga[i][j]));
                 if (a.gate_first) n[i][j] *= ga[i][j];
             }
     }
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
             all[0] += ss[i];
         }
         if (a.groups == 1) {
-            row_sum<TPR, 1>(all, red);
+            row_sum<TPR, 1>(all, red[0]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) ss[i] = all[0];
         } else {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
         if (a.r_out != nullptr) Vec<V>::st((R*)a.r_out + row * a.ldro + vi * V, rr[i]);
     }
     if (a.n_out == nullptr) return;
-    row_sum<TPR, 1>(all, red);
+    row_sum<TPR, 1>(all, red[1]);
     const float rs = rsqrtf(all[0] / (float)D + a.eps_pre);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -168,50 +168,95 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
     }
 }
 
-// One CTA walks rows b, b + grid, ...; the parameter gradients of its columns stay in registers
-// and leave once, as the CTA's partial sums.
+// One CTA walks rows b, b + grid, ..., the next row's values on their way while one is worked on.
+// The parameter gradients of a thread's columns are summed in shared memory, in the thread's own
+// places, and leave once, as the CTA's partial sums.
 template <typename T, typename R, int V, int TPR, int NV>
-__global__ void __launch_bounds__(TPR, TPR == 512 ? 2 : 1) norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TPR, V * NV <= 4 ? 1024 / TPR : 1)
+    norm_bwd_kernel(const NormArgs a) {
     constexpr bool FAST = is_fast<T>();
-    __shared__ float red[2][32];
-    extern __shared__ float gsm[];
+    // hold the next row where registers allow it: 64 a thread at 1024 threads a SM
+    constexpr bool AHEAD = sizeof(T) == 2 && V * NV <= 4;
+    __shared__ float red[2][2][32];
+    extern __shared__ __align__(16) float gsm[];  // [3][D], then the group sums' space
     const int lr = threadIdx.x;
     const int D = (int)a.D, nvec = D / V, gv = nvec / (int)a.groups;
-    float apost[NV][V], ascale[NV][V], apre[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) apost[i][j] = ascale[i][j] = apre[i][j] = 0.0f;
+    float *apost = gsm, *ascale = gsm + D, *apre = gsm + 2 * D, *gspace = gsm + 3 * D;
+    for (int i = lr; i < 3 * D; i += TPR) gsm[i] = 0.0f;
+    __syncthreads();
+    const bool gate = a.gate != nullptr, gfirst = gate && a.gate_first, glast = gate && !a.gate_first;
     const float ginv = 1.0f / (float)(gv * V), dinv = 1.0f / (float)D;
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-        float u[NV][V], ga[NV][V], dr[NV][V];
-        float ss[NV], rs[NV], all[2] = {0.0f, 0.0f};
-        // u: the normalised row (the plain one without a norm)
+    Pack<T, V> po[NV], pg[NV], pn[NV];
+    Pack<R, V> pr[NV], pd[NV];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vi = i * TPR + lr;
-            const bool in = vi < nvec;
+            if (vi >= nvec) continue;
+            po[i] = *reinterpret_cast<const Pack<T, V>*>((const T*)a.o + row * a.ldo + vi * V);
+            if (gate) pg[i] = *reinterpret_cast<const Pack<T, V>*>((const T*)a.gate + row * a.ldg + vi * V);
+            if (a.dr_out != nullptr) pd[i] = *reinterpret_cast<const Pack<R, V>*>((const R*)a.dr_out + row * a.ldro + vi * V);
+            if (a.w_pre != nullptr) {
+                if (a.r != nullptr) pr[i] = *reinterpret_cast<const Pack<R, V>*>((const R*)a.r + row * a.ldr + vi * V);
+                pn[i] = *reinterpret_cast<const Pack<T, V>*>((const T*)a.dn_out + row * a.ldn + vi * V);
+            }
+        }
+    };
+    auto add_to = [](float* sum, const float* v) {
+        float s[V];
+        Vec<V>::ld(sum, s);
 #pragma unroll
-            for (int j = 0; j < V; ++j) u[i][j] = ga[i][j] = dr[i][j] = 0.0f;
-            if (in) Vec<V>::ld((const T*)a.o + row * a.ldo + vi * V, u[i]);
-            if (in && a.gate != nullptr) Vec<V>::ld((const T*)a.gate + row * a.ldg + vi * V, ga[i]);
-            if (in && a.dr_out != nullptr) Vec<V>::ld((const R*)a.dr_out + row * a.ldro + vi * V, dr[i]);
+        for (int j = 0; j < V; ++j) s[j] += v[j];
+        Vec<V>::st(sum, s);
+    };
+    int buf = 0;
+    if (AHEAD && (int64_t)blockIdx.x < a.T) fetch(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        if (!AHEAD) fetch(row);
+        float u[NV][V], ga[NV][V], gd[NV][V], dr[NV][V], rr[NV][V], dn[NV][V];
+        float ss[NV], rs[NV], all[2] = {0.0f, 0.0f};
+        // u: the normalised row (the plain one without a norm); a thread's columns past the row
+        // stay zero and count nowhere
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = i * TPR + lr < nvec;
+#pragma unroll
+            for (int j = 0; j < V; ++j) u[i][j] = ga[i][j] = gd[i][j] = dr[i][j] = rr[i][j] = dn[i][j] = 0.0f;
+            if (in) {
+                po[i].get(u[i]);
+                if (gate) pg[i].get(ga[i]);
+                if (a.dr_out != nullptr) pd[i].get(dr[i]);
+                if (a.w_pre != nullptr) {
+                    if (a.r != nullptr) pr[i].get(rr[i]);
+                    pn[i].get(dn[i]);
+                }
+            }
             ss[i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                if (a.gate != nullptr && a.gate_first) u[i][j] *= act_of<FAST>(a.act, ga[i][j], sigm<FAST>(ga[i][j]));
+                if (gate) {  // ga: act(gate), gd: its derivative
+                    const float g = ga[i][j], sg = sigm<FAST>(g);
+                    ga[i][j] = act_of(a.act, g, sg);
+                    gd[i][j] = dact_of(a.act, g, sg);
+                }
+                if (gfirst) {
+                    gd[i][j] *= u[i][j];
+                    u[i][j] *= ga[i][j];
+                }
                 ss[i] = fmaf(u[i][j], u[i][j], ss[i]);
             }
             all[0] += ss[i];
             rs[i] = 1.0f;
         }
+        if (AHEAD && row + gridDim.x < a.T) fetch(row + gridDim.x);
         if (a.w_post != nullptr) {
             if (a.groups == 1) {
-                row_sum<TPR, 1>(all, red);
+                row_sum<TPR, 1>(all, red[buf]);
+                buf ^= 1;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) ss[i] = all[0];
             } else {
-                group_sum<TPR, NV>(ss, nvec, gv, gsm, lr);
+                group_sum<TPR, NV>(ss, nvec, gv, gspace, lr);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -222,30 +267,34 @@ __global__ void __launch_bounds__(TPR, TPR == 512 ? 2 : 1) norm_bwd_kernel(const
         }
         // the gradient of rr
         if (a.w_pre != nullptr) {
-            float rr[NV][V], dn[NV][V];
             all[0] = all[1] = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int vi = i * TPR + lr;
                 if (vi >= nvec) continue;
-                float wp[V], sc[V], w[V];
-                if (a.r != nullptr) Vec<V>::ld((const R*)a.r + row * a.ldr + vi * V, rr[i]);
-                Vec<V>::ld((const T*)a.dn_out + row * a.ldn + vi * V, dn[i]);
-                if (a.w_post != nullptr) Vec<V>::ld(a.w_post + vi * V, wp);
-                if (a.scale != nullptr) Vec<V>::ld(a.scale + vi * V, sc);
+                float w[V];
+                if (a.w_post != nullptr) Vec<V>::ld(a.w_post + vi * V, w);
+                float n[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    n[j] = a.w_post != nullptr ? u[i][j] * w[j] : u[i][j];
+                    if (glast) n[j] *= ga[i][j];
+                }
+                if (a.scale != nullptr) {
+                    Vec<V>::ld(a.scale + vi * V, w);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) n[j] *= w[j];
+                }
                 Vec<V>::ld(a.w_pre + vi * V, w);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    float n = u[i][j];
-                    if (a.w_post != nullptr) n *= wp[j];
-                    if (a.gate != nullptr && !a.gate_first) n *= act_of<FAST>(a.act, ga[i][j], sigm<FAST>(ga[i][j]));
-                    if (a.scale != nullptr) n *= sc[j];
-                    rr[i][j] = a.r != nullptr ? rr[i][j] + n : n;
+                    rr[i][j] += n[j];
                     all[0] = fmaf(rr[i][j], rr[i][j], all[0]);
                     all[1] = fmaf(dn[i][j] * w[j], rr[i][j], all[1]);
                 }
             }
-            row_sum<TPR, 2>(all, red);
+            row_sum<TPR, 2>(all, red[buf]);
+            buf ^= 1;
             const float rp = rsqrtf(fmaf(all[0], dinv, a.eps_pre)), k = all[1] * dinv * rp * rp;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -255,9 +304,10 @@ __global__ void __launch_bounds__(TPR, TPR == 512 ? 2 : 1) norm_bwd_kernel(const
                 Vec<V>::ld(a.w_pre + vi * V, w);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    apre[i][j] = fmaf(dn[i][j], rr[i][j] * rp, apre[i][j]);
                     dr[i][j] += rp * (dn[i][j] * w[j] - rr[i][j] * k);
+                    dn[i][j] *= rr[i][j] * rp;
                 }
+                add_to(apre + vi * V, dn[i]);
             }
         }
         float dot[NV];
@@ -268,74 +318,98 @@ __global__ void __launch_bounds__(TPR, TPR == 512 ? 2 : 1) norm_bwd_kernel(const
             dot[i] = 0.0f;
             if (vi >= nvec) continue;
             if (a.dr != nullptr) Vec<V>::st((R*)a.dr + row * a.lddr + vi * V, dr[i]);
-            float wp[V], sc[V], dg[V];
-            if (a.w_post != nullptr) Vec<V>::ld(a.w_post + vi * V, wp);
-            if (a.scale != nullptr) Vec<V>::ld(a.scale + vi * V, sc);
+            float w[V], t[V];
+            if (a.w_post != nullptr) Vec<V>::ld(a.w_post + vi * V, w);
+            if (a.scale != nullptr) {
+                float sc[V];
+                Vec<V>::ld(a.scale + vi * V, sc);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float n = a.w_post != nullptr ? u[i][j] * wp[j] : u[i][j];  // before a later gate
-                float act = 1.0f, dact = 0.0f;
-                if (a.gate != nullptr && !a.gate_first) {
-                    const float sg = sigm<FAST>(ga[i][j]);
-                    act = act_of<FAST>(a.act, ga[i][j], sg);
-                    dact = dact_of(a.act, ga[i][j], sg);
+                for (int j = 0; j < V; ++j) {
+                    float n = a.w_post != nullptr ? u[i][j] * w[j] : u[i][j];
+                    if (glast) n *= ga[i][j];
+                    t[j] = dr[i][j] * n;
+                    dr[i][j] *= sc[j];
                 }
-                ascale[i][j] = fmaf(dr[i][j], n * act, ascale[i][j]);
-                float dm = a.scale != nullptr ? dr[i][j] * sc[j] : dr[i][j];
-                dg[j] = dm * n * dact;
-                dm *= act;
-                apost[i][j] = fmaf(dm, u[i][j], apost[i][j]);
-                if (a.w_post != nullptr) dm *= wp[j];
-                dr[i][j] = dm;
-                dot[i] = fmaf(dm, u[i][j], dot[i]);
+                add_to(ascale + vi * V, t);
             }
-            if (a.gate != nullptr && !a.gate_first) Vec<V>::st((T*)a.dgate + row * a.lddg + vi * V, dg);
+            if (glast) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float n = a.w_post != nullptr ? u[i][j] * w[j] : u[i][j];
+                    t[j] = dr[i][j] * n * gd[i][j];
+                    dr[i][j] *= ga[i][j];
+                }
+                Vec<V>::st((T*)a.dgate + row * a.lddg + vi * V, t);
+            }
+            if (a.w_post != nullptr) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    t[j] = dr[i][j] * u[i][j];
+                    dr[i][j] *= w[j];
+                    dot[i] = fmaf(dr[i][j], u[i][j], dot[i]);
+                }
+                add_to(apost + vi * V, t);
+            }
             all[0] += dot[i];
         }
         if (a.w_post != nullptr) {
             if (a.groups == 1) {
-                row_sum<TPR, 1>(all, red);
+                row_sum<TPR, 1>(all, red[buf]);
+                buf ^= 1;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) dot[i] = all[0];
             } else {
-                group_sum<TPR, NV>(dot, nvec, gv, gsm, lr);
+                group_sum<TPR, NV>(dot, nvec, gv, gspace, lr);
             }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vi = i * TPR + lr;
             if (vi >= nvec) continue;
-            float dg[V], ov[V];
-            if (a.gate != nullptr && a.gate_first) Vec<V>::ld((const T*)a.o + row * a.ldo + vi * V, ov);
+            float dg[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (a.w_post != nullptr) dr[i][j] = rs[i] * (dr[i][j] - u[i][j] * (dot[i] * ginv));
-                if (a.gate != nullptr && a.gate_first) {
-                    const float sg = sigm<FAST>(ga[i][j]);
-                    dg[j] = dr[i][j] * ov[j] * dact_of(a.act, ga[i][j], sg);
-                    dr[i][j] *= act_of<FAST>(a.act, ga[i][j], sg);
+                if (gfirst) {
+                    dg[j] = dr[i][j] * gd[i][j];
+                    dr[i][j] *= ga[i][j];
                 }
             }
             Vec<V>::st((T*)a.d_o + row * a.lddo + vi * V, dr[i]);
-            if (a.gate != nullptr && a.gate_first) Vec<V>::st((T*)a.dgate + row * a.lddg + vi * V, dg);
+            if (gfirst) Vec<V>::st((T*)a.dgate + row * a.lddg + vi * V, dg);
         }
     }
     float* p = a.partial + (int64_t)blockIdx.x * 3 * D;
+    __syncthreads();
+    for (int i = lr; i < 3 * D; i += TPR) p[i] = gsm[i];
+}
+
+// dw_post, dscale and dw_pre from the CTAs' partial sums [n][3][D], each added in the same order.
+__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const NormArgs a, int64_t n) {
+    // 32 columns a CTA, eight threads a column: thread k adds partials k, k + 8, ..., then the
+    // eight are added in order
+    __shared__ float part[8][33];
+    const int col = threadIdx.x & 31, k = threadIdx.x >> 5, m = blockIdx.y;
+    float* out = m == 0 ? a.dw_post : m == 1 ? a.dscale : a.dw_pre;
+    if (out == nullptr) return;
+    const int64_t i = (int64_t)blockIdx.x * 32 + col;
+    float s = 0.0f;
+    if (i < a.D) {
+#pragma unroll 8
+        for (int64_t p = k; p < n; p += 8) s += a.partial[(p * 3 + m) * a.D + i];
+    }
+    part[k][col] = s;
+    __syncthreads();
+    if (k == 0 && i < a.D) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int vi = i * TPR + lr;
-        if (vi >= nvec) continue;
-        Vec<V>::st(p + vi * V, apost[i]);
-        Vec<V>::st(p + D + vi * V, ascale[i]);
-        Vec<V>::st(p + 2 * D + vi * V, apre[i]);
+        for (int j = 1; j < 8; ++j) s += part[j][col];
+        out[i] = s;
     }
 }
 
-constexpr int kBwdCtas = 304;  // two a SM
-
 template <typename K>
 cudaError_t group_smem(K kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
+    if (bytes <= 40 * 1024) return cudaSuccess;  // with the static part below the default 48 KB
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
@@ -358,7 +432,8 @@ cudaError_t fwd_go(const NormArgs& a, cudaStream_t s) {
 
 template <typename T, typename R, int V, int TPR, int NV>
 cudaError_t bwd_go(const NormArgs& a, cudaStream_t s) {
-    const size_t sm = group_bytes(a, V);
+    const size_t sm = sizeof(float) * 3 * (size_t)a.D + group_bytes(a, V);
+    // the odd-width path at its widest, with both the sums and one value a column
     const cudaError_t e = group_smem(norm_bwd_kernel<T, R, V, TPR, NV>, sm);
     if (e != cudaSuccess) return e;
     norm_bwd_kernel<T, R, V, TPR, NV><<<(unsigned)norm_bwd_ctas(a.T, a.D), TPR, sm, s>>>(a);
@@ -385,35 +460,32 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
 
 template <typename T, typename R>
 cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
-    const bool v8 = a.D % 8 == 0 && (a.D / a.groups) % 8 == 0 && a.ldo % 8 == 0 && a.ldg % 8 == 0 &&
-                    a.ldr % 8 == 0 && a.ldro % 8 == 0 && a.ldn % 8 == 0 && a.lddo % 8 == 0 &&
-                    a.lddg % 8 == 0 && a.lddr % 8 == 0;
+    const bool v4 = a.D % 4 == 0 && (a.D / a.groups) % 4 == 0 && a.ldo % 4 == 0 && a.ldg % 4 == 0 &&
+                    a.ldr % 4 == 0 && a.ldro % 4 == 0 && a.ldn % 4 == 0 && a.lddo % 4 == 0 &&
+                    a.lddg % 4 == 0 && a.lddr % 4 == 0;
     cudaError_t e;
-    if (v8) {
-        if (a.D <= 1024) e = bwd_go<T, R, 8, 128, 1>(a, s);
-        else if (a.D <= 2048) e = bwd_go<T, R, 8, 256, 1>(a, s);
-        else if (a.D <= 4096) e = bwd_go<T, R, 8, 512, 1>(a, s);
-        else if (a.D <= 8192) e = bwd_go<T, R, 8, 1024, 1>(a, s);
-        else e = bwd_go<T, R, 8, 1024, 2>(a, s);
+    if (v4) {
+        if (a.D <= 512) e = bwd_go<T, R, 4, 128, 1>(a, s);
+        else if (a.D <= 1024) e = bwd_go<T, R, 4, 256, 1>(a, s);
+        else if (a.D <= 2048) e = bwd_go<T, R, 4, 512, 1>(a, s);
+        else if (a.D <= 4096) e = bwd_go<T, R, 4, 1024, 1>(a, s);
+        else if (a.D <= 8192) e = bwd_go<T, R, 4, 1024, 2>(a, s);
+        else e = bwd_go<T, R, 4, 1024, 4>(a, s);
     } else {
         if (a.D <= 1024) e = bwd_go<T, R, 1, 256, 4>(a, s);
         else if (a.D <= 8192) e = bwd_go<T, R, 1, 1024, 8>(a, s);
         else e = bwd_go<T, R, 1, 1024, 16>(a, s);
     }
-    const int64_t n = norm_bwd_ctas(a.T, a.D);
-    if (e == cudaSuccess && a.dw_post != nullptr)
-        e = launch_sum_partials(a.partial, n, 3 * a.D, a.dw_post, a.D, s);
-    if (e == cudaSuccess && a.dscale != nullptr)
-        e = launch_sum_partials(a.partial + a.D, n, 3 * a.D, a.dscale, a.D, s);
-    if (e == cudaSuccess && a.dw_pre != nullptr)
-        e = launch_sum_partials(a.partial + 2 * a.D, n, 3 * a.D, a.dw_pre, a.D, s);
-    return e;
+    if (e != cudaSuccess) return e;
+    norm_bwd_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 3), 256, 0, s>>>(a, norm_bwd_ctas(a.T, a.D));
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 int64_t norm_bwd_ctas(int64_t T, int64_t D) {
-    const int64_t most = D <= 1024 ? 8 * 152 : D <= 2048 ? 4 * 152 : kBwdCtas;
+    // 1024 threads a SM, as far as the widths' CTAs go
+    const int64_t most = 152 * (D <= 512 ? 8 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1);
     return T < 1 ? 1 : T < most ? T : most;
 }
 

@@ -13,6 +13,7 @@ namespace lz {
 namespace {
 
 constexpr int kNT = 128;
+constexpr int TX = 32, TY = kNT / TX;  // a CTA: TX threads along the channels, TY runs of tokens
 
 // The K - 1 inputs before token t of its sequence, from the row or the sequence's state.
 template <typename T, int K, int V>
@@ -32,13 +33,25 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const SeqAt& q, i
     }
 }
 
+// The taps of a CTA's TX V channels go through shared memory, transposed: each thread reading
+// its own channels' rows of w costs more than the inputs of a run.
 template <int K, int V>
-__device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t c, float (*w)[V], float* bias) {
+struct Taps {
+    float w[K][TX * V], bias[TX * V];
+    __device__ __forceinline__ void fill(const ConvArgs& a, int64_t c0) {
+        const int n = (int)min64(TX * V, a.C - c0);
+        for (int e = threadIdx.x; e < n * K; e += kNT) w[e % K][e / K] = a.w[c0 * K + e];
+        for (int e = threadIdx.x; e < n; e += kNT) bias[e] = a.bias != nullptr ? a.bias[c0 + e] : 0.0f;
+        __syncthreads();
+    }
+};
+template <int K, int V>
+__device__ __forceinline__ void load_taps(const Taps<K, V>& t, int tx, float (*w)[V], float* bias) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = a.w[(c + i) * K + j];
-        bias[i] = a.bias != nullptr ? a.bias[c + i] : 0.0f;
+        for (int j = 0; j < K; ++j) w[j][i] = t.w[j][tx * V + i];
+        bias[i] = t.bias[tx * V + i];
     }
 }
 
@@ -74,38 +87,50 @@ __global__ void __launch_bounds__(kNT) conv_tail_kernel(const ConvArgs a) {
 }
 
 // One thread: V channels, `run` tokens of one row of the batch.  Bound by HBM: x is read and y
-// written once; U rows are in flight per thread.
+// written once; the next U rows are on their way while U are computed.
 template <typename T, int K, int V>
-__global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t runs, int run) {
-    constexpr int U = 4;
+__global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
+    constexpr int U = 8;
     const bool silu = a.act == LIZARD_ACT_SILU;
-    const int64_t nv = a.C / V, id = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    __shared__ Taps<K, V> taps;
+    const int tx = threadIdx.x % TX;
+    const int64_t c0 = blockIdx.x % cbs * (TX * V), c = c0 + tx * V;
+    const int64_t rr = blockIdx.x / cbs * TY + threadIdx.x / TX, b = rr / runs;
     check_offsets(a.seqs, a.header);
-    if (id >= a.B * runs * nv) return;
-    const int64_t c = id % nv * V, rr = id / nv, b = rr / runs;
+    taps.fill(a, c0);
+    if (rr >= a.B * runs || c >= a.C) return;
     const int64_t t0 = rr % runs * run, t1 = min64(t0 + run, a.seqs.L), row0 = b * a.seqs.L;
     float w[K][V], bias[V], win[K][V];
-    load_taps<K, V>(a, c, w, bias);
+    load_taps<K, V>(taps, tx, w, bias);
     SeqAt q = seq_at(a.seqs, b, t0);
     load_window<T, K, V>(a, q, row0, t0, c, win);
-    const T* x = (const T*)a.x + row0 * a.ldx + c;
-    T* y = (T*)a.y + row0 * a.ldy + c;
-    for (int64_t t = t0; t < t1; t += U) {
-        float in[U][V];
+    const T* x = (const T*)a.x + (row0 + t0) * a.ldx + c;
+    T* y = (T*)a.y + (row0 + t0) * a.ldy + c;
+    const int n = (int)(t1 - t0);
+    Pack<T, V> in[U], next[U];
+    auto fetch = [&](int t) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < t1) Vec<V>::ld(x + (t + u) * a.ldx, in[u]);
+            if (t + u < n) next[u] = *reinterpret_cast<const Pack<T, V>*>(x + (int64_t)(t + u) * a.ldx);
+    };
+    fetch(0);
+    int change = (int)min64(q.end - t0, n);  // where the next sequence begins
+    for (int t = 0; t < n; t += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) in[u] = next[u];
+        fetch(t + U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (t + u >= t1) break;
-            if (t + u == q.end) {
-                q = seq_at(a.seqs, b, t + u);
-                load_window<T, K, V>(a, q, row0, t + u, c, win);
+            if (t + u >= n) break;
+            if (t + u == change) {
+                q = seq_at(a.seqs, b, t0 + t + u);
+                load_window<T, K, V>(a, q, row0, t0 + t + u, c, win);
+                change = (int)min64(q.end - t0, n);
             }
             float o[V];
+            in[u].get(win[K - 1]);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                win[K - 1][i] = in[u][i];
                 float p = bias[i];
 #pragma unroll
                 for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
@@ -113,34 +138,41 @@ __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t
 #pragma unroll
                 for (int j = 0; j + 1 < K; ++j) win[j][i] = win[j + 1][i];
             }
-            Vec<V>::st(y + (t + u) * a.ldy, o);
+            Vec<V>::st(y, o);
+            y += a.ldy;
         }
     }
 }
 
 // One token a sequence: the state's K - 1 rows are read, moved up by one and written back.
 template <typename T, int K, int V>
-__global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a, int64_t cbs) {
     const bool silu = a.act == LIZARD_ACT_SILU;
-    const int64_t nv = a.C / V, id = (int64_t)blockIdx.x * kNT + threadIdx.x;
-    if (id >= a.B * nv) return;
-    const int64_t c = id % nv * V, b = id / nv;
-    int64_t slot = a.slots != nullptr ? a.slots[b] : b;
+    __shared__ Taps<K, V> taps;
+    const int tx = threadIdx.x % TX;
+    const int64_t c0 = blockIdx.x % cbs * (TX * V), c = c0 + tx * V;
+    const int64_t b = blockIdx.x / cbs * TY + threadIdx.x / TX;
+    const bool in = b < a.B && c < a.C;
+    const int64_t slot = !in ? -1 : a.slots != nullptr ? a.slots[b] : b;
+    const bool live = slot >= 0 && slot < a.nslots;
+    float w[K][V], bias[V], win[K][V], o[V];
+    T* st = (T*)a.state + slot * (K - 1) * a.C + c;
+    if (live) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) Vec<V>::ld(st + j * a.C, win[j]);
+        Vec<V>::ld((const T*)a.x + b * a.ldx + c, win[K - 1]);
+    }
+    taps.fill(a, c0);
+    if (!in) return;
     T* y = (T*)a.y + b * a.ldy + c;
-    float o[V];
-    if (slot < 0 || slot >= a.nslots) {
+    if (!live) {
         if (slot >= 0) report(a.header, LIZARD_ERR_INVALID_ARG, 33);
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = 0.0f;
         Vec<V>::st(y, o);
         return;
     }
-    float w[K][V], bias[V], win[K][V];
-    T* st = (T*)a.state + slot * (K - 1) * a.C + c;
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) Vec<V>::ld(st + j * a.C, win[j]);
-    Vec<V>::ld((const T*)a.x + b * a.ldx + c, win[K - 1]);
-    load_taps<K, V>(a, c, w, bias);
+    load_taps<K, V>(taps, tx, w, bias);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float p = bias[i];
@@ -160,54 +192,78 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a) {
 // sequence's first token are its state, whose gradient is written by the run that holds that
 // token.
 template <typename T, int K, int V>
-__global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t runs, int run) {
+__global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
     constexpr int U = 4;
     const bool silu = a.act == LIZARD_ACT_SILU;
-    const int64_t nv = a.C / V, id = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    __shared__ Taps<K, V> taps;
+    const int tx = threadIdx.x % TX;
+    const int64_t c0 = blockIdx.x % cbs * (TX * V), c = c0 + tx * V;
+    const int64_t rr = blockIdx.x / cbs * TY + threadIdx.x / TX, b = rr / runs;
     check_offsets(a.seqs, a.header);
-    if (id >= a.B * runs * nv) return;
-    const int64_t c = id % nv * V, rr = id / nv, b = rr / runs;
-    const int64_t t0 = rr % runs * run, t1 = min64(t0 + run, a.seqs.L), row0 = b * a.seqs.L;
+    taps.fill(a, c0);
+    if (rr >= a.B * runs || c >= a.C) return;
+    const int64_t t0 = rr % runs * run, row0 = b * a.seqs.L;
+    const int n = (int)min64(run, a.seqs.L - t0);
     float w[K][V], bias[V], win[K][V], acc[K][V], dw[K][V], db[V];
-    load_taps<K, V>(a, c, w, bias);
+    load_taps<K, V>(taps, tx, w, bias);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         db[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < K; ++j) dw[j][i] = acc[j][i] = 0.0f;
     }
-    const T* x = (const T*)a.x + row0 * a.ldx + c;
-    const T* dy = (const T*)a.dy + row0 * a.ldy + c;
-    T* dx = (T*)a.dx + row0 * a.lddx + c;
-    SeqAt q = seq_at(a.seqs, b, t0);
-    load_window<T, K, V>(a, q, row0, t0, c, win);
+    // tokens count from t0 from here on; a begin before -K and an end past n + K count as those
+    const T* x = (const T*)a.x + (row0 + t0) * a.ldx + c;
+    const T* dy = (const T*)a.dy + (row0 + t0) * a.ldy + c;
+    T* dx = (T*)a.dx + (row0 + t0) * a.lddx + c;
+    SeqAt q;
+    int begin, end;
+    auto enter = [&](int t) {
+        q = seq_at(a.seqs, b, t0 + t);
+        begin = (int)max64(q.begin - t0, -K);
+        end = (int)min64(q.end - t0, n + K);
+        load_window<T, K, V>(a, q, row0, t0 + t, c, win);
+    };
+    enter(0);
     // the gradient of token u (or of a place before the sequence's first token)
-    auto put = [&](int64_t u, const float* v) {
-        if (u >= q.begin) {
-            if (u >= t0 && u < t1) Vec<V>::st(dx + u * a.lddx, v);
-        } else if (a.dstate_in != nullptr && q.begin >= t0 && q.begin < t1) {
-            Vec<V>::st((T*)a.dstate_in + (q.seq * (K - 1) + (K - 1) + u - q.begin) * a.C + c, v);
+    auto put = [&](int u, const float* v) {
+        if (u >= begin) {
+            if (u >= 0 && u < n) Vec<V>::st(dx + u * a.lddx, v);
+        } else if (a.dstate_in != nullptr && begin >= 0 && begin < n) {
+            Vec<V>::st((T*)a.dstate_in + (q.seq * (K - 1) + (K - 1) + u - begin) * a.C + c, v);
         }
     };
-    int64_t t = t0;
+    int t = 0;
     while (true) {
-        const int64_t lim = min64(q.end, t1 + K - 1);
-        for (; t < lim; t += U) {
-            float in[U][V], g[U][V];
+        const int lim = min(end, n + K - 1);
+        Pack<T, V> in[U], g[U], nin[U], ng[U];  // the next U tokens are on their way
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (t + u < lim) {
-                    Vec<V>::ld(x + (t + u) * a.ldx, in[u]);
-                    Vec<V>::ld(dy + (t + u) * a.ldy, g[u]);
+                    nin[u] = *reinterpret_cast<const Pack<T, V>*>(x + (t + u) * a.ldx);
+                    ng[u] = *reinterpret_cast<const Pack<T, V>*>(dy + (t + u) * a.ldy);
                 }
+        };
+        fetch(t);
+#pragma unroll 1
+        for (; t < lim; t += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                in[u] = nin[u];
+                g[u] = ng[u];
+            }
+            fetch(t + U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t + u >= lim) break;
-                const float own = t + u < t1 ? 1.0f : 0.0f;  // the halo belongs to the next run
+                float gy[V];
+                in[u].get(win[K - 1]);
+                g[u].get(gy);
+                const float own = t + u < n ? 1.0f : 0.0f;  // the halo belongs to the next run
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    win[K - 1][i] = in[u][i];
-                    float dp = g[u][i];
+                    float dp = gy[i];
                     if (silu) {
                         float p = bias[i];
 #pragma unroll
@@ -235,7 +291,7 @@ __global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t
             }
         }
         t = lim;
-        if (t == q.end) {  // the sequence's last K - 1 places: no later token adds to them
+        if (t == end) {  // the sequence's last K - 1 places: no later token adds to them
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 if (a.dstate_out != nullptr) {
@@ -247,21 +303,38 @@ __global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t
                 put(t - (K - 1) + j, acc[j]);
             }
         }
-        if (t >= t1) break;
-        q = seq_at(a.seqs, b, t);
-        load_window<T, K, V>(a, q, row0, t, c, win);
+        if (t >= n) break;
+        enter(t);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < K; ++j) acc[j][i] = 0.0f;
     }
-    float* p = a.partial + rr * (K + 1) * a.C;  // [C, K], then [C]
+    float* p = a.partial + rr * (K + 1) * a.C + c;  // [K + 1, C]
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < K; ++j) p[(c + i) * K + j] = dw[j][i];
-        p[a.C * K + c + i] = db[i];
+    for (int j = 0; j < K; ++j) Vec<V>::st(p + j * a.C, dw[j]);
+    Vec<V>::st(p + K * a.C, db);
+}
+
+// dw [C, K] and dbias [C] from the runs' sums [n, K + 1, C]: 32 channels a CTA, eight threads a
+// channel; thread k adds runs k, k + 8, ..., then the eight are added in order.
+__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const ConvArgs a, int64_t n) {
+    __shared__ float part[8][33];
+    const int col = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + col, count = (a.K + 1) * a.C;
+    float s = 0.0f;
+    if (i < count) {
+#pragma unroll 8
+        for (int64_t p = k; p < n; p += 8) s += a.partial[p * count + i];
     }
+    part[k][col] = s;
+    __syncthreads();
+    if (k != 0 || i >= count) return;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) s += part[j][col];
+    const int64_t j = i / a.C, c = i % a.C;
+    if (j < a.K) a.dw[c * a.K + j] = s;
+    else if (a.dbias != nullptr) a.dbias[c] = s;
 }
 
 // Sequences without tokens pass the gradient of their state on.
@@ -324,8 +397,8 @@ cudaError_t conv_fwd(const ConvArgs& a, cudaStream_t s) {
         if (a.seqs.L > 0) {
             const int run = run_tokens(a.B, a.seqs.L, nv, 32);
             const int64_t runs = (a.seqs.L + run - 1) / run;
-            const unsigned g = blocks_for(a.B * runs * nv);
-            conv_fwd_kernel<T, K, V><<<g, kNT, 0, s>>>(a, runs, run);
+            const int64_t cbs = (nv + TX - 1) / TX;
+            conv_fwd_kernel<T, K, V><<<(unsigned)(cbs * ((a.B * runs + TY - 1) / TY)), kNT, 0, s>>>(a, runs, run, cbs);
         }
         if (K > 1 && a.state_out != nullptr)
             conv_tail_kernel<T, K, V><<<blocks_for(a.nstate * nv), kNT, 0, s>>>(a);
@@ -337,8 +410,8 @@ template <typename T, int V>
 cudaError_t conv_step(const ConvArgs& a, cudaStream_t s) {
     return with_taps(a.K, [&](auto kk) {
         constexpr int K = decltype(kk)::value;
-        const unsigned g = blocks_for(a.B * (a.C / V));
-        conv_step_kernel<T, K, V><<<g, kNT, 0, s>>>(a);
+        const int64_t cbs = (a.C / V + TX - 1) / TX;
+        conv_step_kernel<T, K, V><<<(unsigned)(cbs * ((a.B + TY - 1) / TY)), kNT, 0, s>>>(a, cbs);
         return cudaGetLastError();
     });
 }
@@ -354,8 +427,8 @@ cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
     cudaError_t e = with_taps(a.K, [&](auto kk) {
         constexpr int K = decltype(kk)::value;
         if (runs > 0) {
-            const unsigned g = blocks_for(a.B * runs * nv);
-            conv_bwd_kernel<T, K, V><<<g, kNT, 0, s>>>(a, runs, run);
+            const int64_t cbs = (nv + TX - 1) / TX;
+            conv_bwd_kernel<T, K, V><<<(unsigned)(cbs * ((a.B * runs + TY - 1) / TY)), kNT, 0, s>>>(a, runs, run, cbs);
         }
         return cudaGetLastError();
     });
@@ -365,11 +438,8 @@ cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const int64_t n = a.B * runs, stride = (a.K + 1) * a.C;
-    e = launch_sum_partials(a.partial, n, stride, a.dw, a.K * a.C, s);
-    if (e == cudaSuccess && a.dbias != nullptr)
-        e = launch_sum_partials(a.partial + a.K * a.C, n, stride, a.dbias, a.C, s);
-    return e;
+    conv_bwd_sum_kernel<<<(unsigned)(((a.K + 1) * a.C + 31) / 32), 256, 0, s>>>(a, a.B * runs);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -387,14 +457,14 @@ int64_t conv_bwd_runs(int64_t B, int64_t L, int64_t C) {
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) {
     if (a.dtype == LIZARD_BF16)
-        return rows_of(a.ldx, a.C, 8) && a.ldy % 8 == 0 ? conv_fwd<__nv_bfloat16, 8>(a, s)
+        return rows_of(a.ldx, a.C, 4) && a.ldy % 4 == 0 ? conv_fwd<__nv_bfloat16, 4>(a, s)
                                                         : conv_fwd<__nv_bfloat16, 1>(a, s);
     return rows_of(a.ldx, a.C, 4) && a.ldy % 4 == 0 ? conv_fwd<float, 4>(a, s) : conv_fwd<float, 1>(a, s);
 }
 
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s) {
     if (a.dtype == LIZARD_BF16)
-        return rows_of(a.ldx, a.C, 8) && a.ldy % 8 == 0 ? conv_step<__nv_bfloat16, 8>(a, s)
+        return rows_of(a.ldx, a.C, 4) && a.ldy % 4 == 0 ? conv_step<__nv_bfloat16, 4>(a, s)
                                                         : conv_step<__nv_bfloat16, 1>(a, s);
     return rows_of(a.ldx, a.C, 4) && a.ldy % 4 == 0 ? conv_step<float, 4>(a, s) : conv_step<float, 1>(a, s);
 }

@@ -15,77 +15,64 @@ namespace lz {
 namespace scan {
 namespace {
 
-template <int LPC, int CPT>
+template <int LPC, int NS>
 struct Lay {
-    static constexpr int TT = LPC == 1 ? 16 : 32;    // tokens a tile
-    static constexpr int LC = 32 / LPC;              // channels side by side in a warp
-    static constexpr int CH = NT / 32 * LC * CPT;    // channels a CTA
-    static constexpr int NP = NS * LPC;              // states, padded
-    static constexpr int NV = CH / 8;                // 8-channel pieces of a row
-    static constexpr int PX = (TT * NV + NT - 1) / NT;       // pieces a thread stages of x, dt, z
-    static constexpr int PB = (TT * (NP + 7) / 8 + NT - 1) / NT;  // and of Bm, Cm
-    static constexpr int YS = CH + 8;                // row stride of the outputs' tile: four
-                                                     // rows x eight channels in distinct banks
+    static constexpr int LC = 32 / LPC;            // channels side by side in a warp
+    static constexpr int CH = NT / 32 * LC;        // channels a CTA
+    static constexpr int NP = NS * LPC;            // states, padded
+    static constexpr int NV = CH / 8;              // 8-channel pieces of a row
+    // tokens a tile: one piece of x, dt and z a thread where Bm and Cm leave room for it
+    static constexpr int TT = 1024 / CH < 2048 / NP ? 1024 / CH : 2048 / NP;
+    static constexpr int NQ = (NP + 7) / 8;        // 8-state pieces of a row of Bm
+    static constexpr int PB = (TT * NQ + NT - 1) / NT;  // of which a thread stages so many
+    static constexpr int U = LPC > 4 ? 8 : 4;      // tokens whose outputs are summed together
+    using P = Plane<TT, CH, LC>;
 };
 
-template <int LPC, int CPT>
+template <int LPC, int NS>
 struct Smem {
-    using L = Lay<LPC, CPT>;
-    static constexpr int TT = L::TT;
-    float2 dx[TT][L::CH];          // d, d x
-    float2 b[TT][2][LPC], c[TT][2][LPC];  // [half][lane]: states 4 lane + 2 half + {0, 1}
-    float y[TT][L::YS];
+    using L = Lay<LPC, NS>;
+    f2 d[L::P::SIZE], dx[L::P::SIZE];        // (d, d), (d x, d x)
+    f2 b[L::TT][NS / 2 * LPC], c[L::TT][NS / 2 * LPC];
+    float y[L::P::SIZE];
 };
 
 // MAIN: the outputs (and states).  Otherwise only a segment's own end state from a zero start and
 // the sum of its step sizes, for the join.
-template <typename T, int LPC, int CPT, bool MAIN>
+template <typename T, int LPC, int NS, bool MAIN>
 __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cut cut,
                                                       float* rec_h, float* rec_d,
                                                       const float* h0) {
-    using L = Lay<LPC, CPT>;
-    constexpr int TT = L::TT, LC = L::LC, CH = L::CH, NP = L::NP, NV = L::NV, PX = L::PX, PB = L::PB;
-    constexpr int NQ = (NP + 7) / 8;  // 8-state pieces of a row of Bm
-    __shared__ __align__(16) Smem<LPC, CPT> sm;
+    using L = Lay<LPC, NS>;
+    using P = typename L::P;
+    constexpr int TT = L::TT, LC = L::LC, CH = L::CH, NV = L::NV, PB = L::PB, NQ = L::NQ, U = L::U;
+    constexpr int H = NS / 2;
+    __shared__ __align__(16) Smem<LPC, NS> sm;
     const Where<CH> w(a, cut);
     if (MAIN) check_offsets(a.seqs, a.header);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int q = lane & (LPC - 1), cl = lane / LPC;
+    const int q = lane & (LPC - 1), lch = warp * LC + lane / LPC;
     const int N = (int)a.N, nn = max(0, min(NS, N - NS * q));  // this lane's states
-    const bool v4 = N % 4 == 0;
+    const bool vn = N % (NS < 4 ? NS : 4) == 0;
     const int64_t t0 = w.seg * cut.seg_len, t1 = min64(t0 + cut.seg_len, a.seqs.L);
-    const int64_t row0 = w.b * a.seqs.L;
-    const int64_t C = a.C;
+    const int64_t row0 = w.b * a.seqs.L, C = a.C, c = w.c0 + lch;
+    const bool own = c < w.clim;
+    const int64_t off = c * N + NS * q;  // of this lane's states in [C, N]
 
-    float A2[CPT][NS], h[CPT][NS], sd[CPT];
-    int64_t ch[CPT];
-    bool own[CPT];
+    f2 A2[H], h[H];
+    float sd = 0.0f;
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-        ch[k] = w.c0 + warp * (LC * CPT) + k * LC + cl;
-        own[k] = ch[k] < w.clim;
-        sd[k] = 0.0f;
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (own[k]) load4(a.A + ch[k] * N + NS * q, nn, v4, f);
+    for (int i = 0; i < H; ++i) A2[i] = h[i] = 0;
+    if (own) load_pairs<NS>(a.A + off, nn, vn, A2);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            A2[k][i] = f[i] * kLog2e;
-            h[k][i] = 0.0f;
-        }
-    }
-    // a sequence's first state
-    auto begin_state = [&](int64_t seq) {
+    for (int i = 0; i < H; ++i) A2[i] = mul2(A2[i], pack(kLog2e, kLog2e));
+    auto begin_state = [&](int64_t seq) {  // a sequence's first state
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-#pragma unroll
-            for (int i = 0; i < NS; ++i) h[k][i] = 0.0f;
-            if (h0 != nullptr && own[k]) load4(h0 + (seq * C + ch[k]) * N + NS * q, nn, v4, h[k]);
-        }
+        for (int i = 0; i < H; ++i) h[i] = 0;
+        if (h0 != nullptr && own) load_pairs<NS>(h0 + seq * C * N + off, nn, vn, h);
     };
     auto put_state = [&](float* p) {  // p: [C, N]
-#pragma unroll
-        for (int k = 0; k < CPT; ++k)
-            if (own[k]) store4(p + ch[k] * N + NS * q, nn, v4, h[k]);
+        if (own) store_pairs<NS>(p + off, nn, vn, h);
     };
     SeqAt sq = seq_at(a.seqs, w.b, t0);
     bool cutoff = false;  // a sequence begins in this segment: nothing before it reaches its end
@@ -93,61 +80,76 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
     if (t0 == sq.begin) {
         begin_state(sq.seq);
         cutoff = true;
-    } else if (MAIN) {
-#pragma unroll
-        for (int k = 0; k < CPT; ++k)
-            if (own[k]) load4(rec_h + (rec + ch[k]) * N + NS * q, nn, v4, h[k]);
+    } else if (MAIN && own) {
+        load_pairs<NS>(rec_h + rec * N + off, nn, vn, h);
     }
 
-    // staging: thread's pieces of a tile
-    const bool vec = a.C % 8 == 0 && (C / a.G) % 8 == 0 && a.ldx % 8 == 0 && a.lddt % 8 == 0 &&
+    // staging: one piece of eight channels of one token
+    const bool vec = C % 8 == 0 && (C / a.G) % 8 == 0 && a.ldx % 8 == 0 && a.lddt % 8 == 0 &&
                      a.ldz % 8 == 0 && a.ldy % 8 == 0;
     const bool vecb = N % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0;
-    const int pc = tid % NV * 8, pt = tid / NV;  // channel and first token of the x pieces
-    const int64_t pch = w.c0 + pc;
-    const int pn = (int)max64(0, min64(8, w.clim - pch));
-    constexpr int DT = NT / NV;  // tokens between a thread's pieces
-    Raw<T> rx[PX], rdt[PX], rz[PX], rb[PB], rc[PB];
-    auto fetch = [&](int64_t tt) {
+    const int pv = tid % NV, pt = tid / NV;
+    const bool stages = pt < TT;
+    const int64_t pch = w.c0 + pv * 8;
+    const int pn = stages ? (int)max64(0, min64(8, w.clim - pch)) : 0;
+    float bias[8], skip[8];
 #pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int64_t t = tt + pt + i * DT;
-            const int n = t < t1 && pt + i * DT < TT ? pn : 0;
-            const int64_t r = row0 + t;
-            rx[i].load((const T*)a.x + r * a.ldx + pch, n, vec);
-            rdt[i].load((const T*)a.dt + r * a.lddt + pch, n, vec);
-            if (MAIN && a.z != nullptr) rz[i].load((const T*)a.z + r * a.ldz + pch, n, vec);
+    for (int j = 0; j < 8; ++j) {
+        bias[j] = a.dt_bias != nullptr && j < pn ? a.dt_bias[pch + j] : 0.0f;
+        skip[j] = MAIN && a.D != nullptr && j < pn ? a.D[pch + j] : 0.0f;
+    }
+    const T *px = (const T*)a.x + (row0 + t0 + pt) * a.ldx + pch;
+    const T *pdt = (const T*)a.dt + (row0 + t0 + pt) * a.lddt + pch;
+    const T *pz = (const T*)a.z + (row0 + t0 + pt) * a.ldz + pch;
+    T* py = (T*)a.y + (row0 + t0 + pt) * a.ldy + pch;
+    const T *pb[PB], *pc[PB];
+    int bn[PB], bt[PB];  // states of a piece of Bm and Cm, its token in a tile
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+        const int e = tid + i * NT, n0 = e % NQ * 8;
+        bt[i] = e / NQ;
+        bn[i] = bt[i] < TT ? max(0, min(8, N - n0)) : 0;
+        pb[i] = (const T*)a.Bm + (row0 + t0 + bt[i]) * a.ldb + w.grp * N + n0;
+        pc[i] = (const T*)a.Cm + (row0 + t0 + bt[i]) * a.ldc + w.grp * N + n0;
+    }
+    Raw<T> rx, rdt, rz, rb[PB], rc[PB];
+    auto fetch = [&](int left) {  // the next tile, of which `left` tokens are the segment's
+        const int n = pt < left ? pn : 0;
+        rx.load(px, n, vec);
+        rdt.load(pdt, n, vec);
+        px += TT * a.ldx;
+        pdt += TT * a.lddt;
+        if (MAIN && a.z != nullptr) {
+            rz.load(pz, n, vec);
+            pz += TT * a.ldz;
         }
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
-            const int e = tid + i * NT, tl = e / NQ, n0 = e % NQ * 8;
-            const int n = tl < TT && tt + tl < t1 ? max(0, min(8, N - n0)) : 0;
-            const int64_t r = row0 + tt + tl;
-            rb[i].load((const T*)a.Bm + r * a.ldb + w.grp * N + n0, n, vecb);
-            if (MAIN) rc[i].load((const T*)a.Cm + r * a.ldc + w.grp * N + n0, n, vecb);
+            const int m = bt[i] < left ? bn[i] : 0;
+            rb[i].load(pb[i], m, vecb);
+            pb[i] += TT * a.ldb;
+            if (MAIN) {
+                rc[i].load(pc[i], m, vecb);
+                pc[i] += TT * a.ldc;
+            }
         }
     };
-    Raw<T> kx[PX], kz[PX];  // the current tile's x and z, for its outputs
+    Raw<T> kx, kz;  // the current tile's x and z, for its outputs
     auto commit = [&]() {
-        float bias[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = a.dt_bias != nullptr && i < pn ? a.dt_bias[pch + i] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            if (pt + i * DT >= TT) break;
+        if (stages) {
             float fx[8], fd[8];
-            rx[i].get(fx);
-            rdt[i].get(fd);
-            float2* o = &sm.dx[pt + i * DT][pc];
+            rx.get(fx);
+            rdt.get(fd);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = fd[j] + bias[j], d = a.softplus ? softplus_(v) : v;
-                o[j] = make_float2(d, d * fx[j]);
+                const float v = fd[j] + bias[j], d = a.softplus ? softplus_(v) : v, dx = d * fx[j];
+                sm.d[P::at(pt, pv * 8 + j)] = pack(d, d);
+                sm.dx[P::at(pt, pv * 8 + j)] = pack(dx, dx);
             }
-            if (MAIN) {
-                kx[i] = rx[i];
-                kz[i] = rz[i];
-            }
+        }
+        if (MAIN) {
+            kx = rx;
+            kz = rz;
         }
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
@@ -155,134 +157,101 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
             if (tl >= TT) break;
             float f[8];
             rb[i].get(f);
-#pragma unroll
-            for (int j = 0; j < 8 && j < NP; j += 2)
-                sm.b[tl][j / 2 % 2][(n0 + j) / 4] = make_float2(f[j], f[j + 1]);
+            put_states<NS, LPC>(sm.b[tl], n0, f);
             if (MAIN) {
                 rc[i].get(f);
-#pragma unroll
-                for (int j = 0; j < 8 && j < NP; j += 2)
-                    sm.c[tl][j / 2 % 2][(n0 + j) / 4] = make_float2(f[j], f[j + 1]);
+                put_states<NS, LPC>(sm.c[tl], n0, f);
             }
         }
     };
     // one token: the recurrence, and this lane's part of the output
-    auto step = [&](int tl, float* part) {
-        const float2 b0 = sm.b[tl][0][q], b1 = sm.b[tl][1][q];
-        const float bb[4] = {b0.x, b0.y, b1.x, b1.y};
-        float cc[4];
-        if (MAIN) {
-            const float2 c0 = sm.c[tl][0][q], c1 = sm.c[tl][1][q];
-            cc[0] = c0.x, cc[1] = c0.y, cc[2] = c1.x, cc[3] = c1.y;
-        }
+    auto step = [&](int tl) {
+        const f2 d = sm.d[P::at(tl, lch)], dx = sm.dx[P::at(tl, lch)];
+        f2 part = 0;
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const float2 d = sm.dx[tl][warp * (LC * CPT) + k * LC + cl];
-            float p = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                h[k][i] = fmaf(ex2(d.x * A2[k][i]), h[k][i], d.y * bb[i]);
-                if (MAIN) p = fmaf(cc[i], h[k][i], p);
-            }
-            if (MAIN) part[k] = p;
-            else sd[k] += d.x;
+        for (int i = 0; i < H; ++i) {
+            h[i] = fma2(exp2_2(mul2(d, A2[i])), h[i], mul2(dx, sm.b[tl][i * LPC + q]));
+            if (MAIN) part = i == 0 ? mul2(h[i], sm.c[tl][q]) : fma2(h[i], sm.c[tl][i * LPC + q], part);
         }
+        if (!MAIN) {
+            float u, v;
+            unpack(d, u, v);
+            sd += u;
+        }
+        return sum2(part);
     };
-    // sums over a channel's lanes of four tokens' parts; each lane keeps one token of four
-    // (two of four with two lanes a channel)
-    auto reduce = [&](float (*p)[CPT], int tl) {
+
+    auto outputs = [&](float* part, int tl) {  // over the channel's lanes; a lane keeps some of the tokens
+        if (MAIN) {
+            const int at = spread_sum<U, 1, LPC>(part, lane);
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            float* yc = &sm.y[tl][warp * (LC * CPT) + k * LC + cl];
-            if constexpr (LPC == 1) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) yc[i * L::YS] = p[i][k];
-            } else {
-                const bool b0 = q & 1;
-                float u = b0 ? p[1][k] : p[0][k], v = b0 ? p[3][k] : p[2][k];
-                u += __shfl_xor_sync(~0u, b0 ? p[0][k] : p[1][k], 1);
-                v += __shfl_xor_sync(~0u, b0 ? p[2][k] : p[3][k], 1);
-                if constexpr (LPC == 2) {
-                    yc[(q & 1) * L::YS] = u;
-                    yc[(2 + (q & 1)) * L::YS] = v;
-                } else {
-                    const bool b1 = q & 2;
-                    float s = b1 ? v : u;
-                    s += __shfl_xor_sync(~0u, b1 ? u : v, 2);
-#pragma unroll
-                    for (int o = 4; o < LPC; o *= 2) s += __shfl_xor_sync(~0u, s, o);
-                    if (q < 4) yc[(q & 3) * L::YS] = s;
-                }
-            }
+            for (int i = 0; i < spread_left(U, LPC); ++i)
+                if (LPC <= U || q < U) sm.y[P::at(tl + at + i, lch)] = part[i];
         }
     };
 
-    fetch(t0);
+    fetch((int)min64(TT, t1 - t0));
     for (int64_t tt = t0; tt < t1; tt += TT) {
         commit();
         __syncthreads();
-        if (tt + TT < t1) fetch(tt + TT);
-        const int n = (int)min64(TT, t1 - tt);
-        for (int tl = 0; tl < n; tl += 4) {
-            const int64_t t = tt + tl;
-            if (MAIN && a.states != nullptr && tl % CK == 0)
-                put_state(a.states + (w.b * ((a.seqs.L + CK - 1) / CK) + t / CK) * C * N);
-            float part[4][CPT];
-            if (t + 4 <= sq.end) {  // then t + 4 <= t1 too: a segment ends on a group or with its row
+        if (tt + TT < t1) fetch((int)min64(TT, t1 - tt - TT));
+        const int n = (int)min64(TT, t1 - tt), inside = (int)min64(TT, sq.end - tt);
+        // where the states of the tile's 16-token chunks go
+        float* keep = MAIN && a.states != nullptr ? a.states + (w.b * ((a.seqs.L + CK - 1) / CK) + tt / CK) * C * N : nullptr;
+        const int lead = TT % CK == 0 ? 0 : (int)(tt % CK);
+        if (n == TT && inside == TT) {
+#pragma unroll 1
+            for (int tl = 0; tl < TT; tl += U) {
+                if (MAIN && keep != nullptr && (lead + tl) % CK == 0) put_state(keep + tl / CK * C * N);
+                float part[U];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) step(tl + i, part[i]);
-            } else {
+                for (int i = 0; i < U; ++i) part[i] = step(tl + i);
+                outputs(part, tl);
+            }
+        } else {
+#pragma unroll 1
+            for (int tl = 0; tl < n; tl += U) {
+                if (MAIN && keep != nullptr && (lead + tl) % CK == 0) put_state(keep + tl / CK * C * N);
+                float part[U];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int k = 0; k < CPT; ++k) part[i][k] = 0.0f;
-                    if (t + i >= t1) continue;
-                    if (t + i == sq.end) {
+                for (int i = 0; i < U; ++i) part[i] = 0.0f;
+#pragma unroll 1
+                for (int i = 0; i < U && tl + i < n; ++i) {
+                    if (tt + tl + i == sq.end) {
                         if (MAIN && a.h_out != nullptr) put_state(a.h_out + sq.seq * C * N);
-                        sq = seq_at(a.seqs, w.b, t + i);
+                        sq = seq_at(a.seqs, w.b, tt + tl + i);
                         begin_state(sq.seq);
                         cutoff = true;
                     }
-                    step(tl + i, part[i]);
+                    const float p = step(tl + i);
+#pragma unroll
+                    for (int k = 0; k < U; ++k)
+                        if (k == i) part[k] = p;
                 }
+                outputs(part, tl);
             }
-            if (MAIN) reduce(part, tl);
         }
-        if (MAIN) {
-            __syncthreads();
-            float dd[8];
+        __syncthreads();
+        if (MAIN && stages) {
+            float fx[8], o[8];
+            kx.get(fx);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dd[i] = a.D != nullptr && i < pn ? a.D[pch + i] : 0.0f;
+            for (int j = 0; j < 8; ++j) o[j] = fmaf(skip[j], fx[j], sm.y[P::at(pt, pv * 8 + j)]);
+            if (a.z != nullptr) {
+                float fz[8];
+                kz.get(fz);
 #pragma unroll
-            for (int i = 0; i < PX; ++i) {
-                const int tl = pt + i * DT;
-                if (tl >= TT) break;
-                float fx[8], o[8];
-                kx[i].get(fx);
-                const float4 y0 = *reinterpret_cast<const float4*>(&sm.y[tl][pc]);
-                const float4 y1 = *reinterpret_cast<const float4*>(&sm.y[tl][pc + 4]);
-                const float yy[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = fmaf(dd[j], fx[j], yy[j]);
-                if (a.z != nullptr) {
-                    float fz[8];
-                    kz[i].get(fz);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] *= fz[j] * sigm<is_fast<T>()>(fz[j]);
-                }
-                store8((T*)a.y + (row0 + tt + tl) * a.ldy + pch, o, tt + tl < t1 ? pn : 0, vec);
+                for (int j = 0; j < 8; ++j) o[j] *= fz[j] * sigm<is_fast<T>()>(fz[j]);
             }
-        } else {
-            __syncthreads();
+            store8(py, o, pt < n ? pn : 0, vec);
+            py += TT * a.ldy;
         }
     }
     if (MAIN) {
         if (t1 == sq.end && a.h_out != nullptr) put_state(a.h_out + sq.seq * C * N);
     } else {
         put_state(rec_h + rec * N);
-#pragma unroll
-        for (int k = 0; k < CPT; ++k)
-            if (own[k] && q == 0) rec_d[rec + ch[k]] = cutoff ? __int_as_float(0x7fc00000) : sd[k];
+        if (own && q == 0) rec_d[rec + c] = cutoff ? __int_as_float(0x7fc00000) : sd;
     }
 }
 
@@ -320,6 +289,7 @@ __global__ void __launch_bounds__(256) scan_pass_kernel(Seqs seqs, int64_t nstat
 // One token a sequence.  Bound by reading and writing the state once.
 template <typename T, int LPC>
 __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanArgs a) {
+    constexpr int NS = 4;
     constexpr int LC = NT / LPC;
     const int q = threadIdx.x & (LPC - 1);
     const int64_t cbs = (a.C + LC - 1) / LC, b = blockIdx.x / cbs;
@@ -335,8 +305,8 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanArgs a) {
     float h[NS] = {}, A[NS] = {}, bb[NS] = {}, cc[NS] = {}, d = 0.0f, x = 0.0f;
     if (own) {
         const bool v4 = N % 4 == 0;
-        load4(a.state + (slot * a.C + c) * N + NS * q, nn, v4, h);
-        load4(a.A + c * N + NS * q, nn, v4, A);
+        load_n<NS>(a.state + (slot * a.C + c) * N + NS * q, nn, v4, h);
+        load_n<NS>(a.A + c * N + NS * q, nn, v4, A);
         const int64_t grp = c / (a.C / a.G);
         const T* pb = (const T*)a.Bm + b * a.ldb + grp * N + NS * q;
         const T* pc = (const T*)a.Cm + b * a.ldc + grp * N + NS * q;
@@ -362,7 +332,7 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanArgs a) {
 #pragma unroll
     for (int o = 1; o < LPC; o *= 2) y += __shfl_xor_sync(~0u, y, o);
     if (!own) return;
-    store4(a.state + (slot * a.C + c) * N + NS * q, nn, N % 4 == 0, h);
+    store_n<NS>(a.state + (slot * a.C + c) * N + NS * q, nn, N % 4 == 0, h);
     if (q != 0) return;
     if (a.D != nullptr) y = fmaf(a.D[c], x, y);
     if (a.z != nullptr) {
@@ -378,10 +348,35 @@ cudaError_t with_lanes(int l, F&& f) {
     else return l == LPC ? f(std::integral_constant<int, LPC>()) : with_lanes<LPC * 2>(l, f);
 }
 
+// States a lane holds.  Eight keep a channel on few lanes, whose sums cost the least, and need
+// many channels to fill the GPU; with few channels fewer states a lane make more warps.
+int fwd_states(const ScanArgs& a) {
+    const int np = padded_states(a.N);
+    if (np < 16) return 4;
+    const int64_t warps = a.B * a.C * np / (8 * 32);
+    if (warps >= 1500) return 8;
+    if (np == 16 && warps >= 200 && warps < 400) return 2;
+    return 4;
+}
+
+// Calls f with the lanes a channel and the states a lane, as constants.
+template <typename F>
+cudaError_t with_lay(const ScanArgs& a, F&& f) {
+    const int np = padded_states(a.N), ns = fwd_states(a);
+    auto go = [&](auto l, auto n) { return f(l, n); };
+    using std::integral_constant;
+    if (ns == 2) return go(integral_constant<int, 8>(), integral_constant<int, 2>());
+    if (ns == 4)
+        return with_lanes(np / 4, [&](auto l) { return go(l, integral_constant<int, 4>()); });
+    if (np == 16) return go(integral_constant<int, 2>(), integral_constant<int, 8>());
+    if (np == 32) return go(integral_constant<int, 4>(), integral_constant<int, 8>());
+    return go(integral_constant<int, 8>(), integral_constant<int, 8>());
+}
+
 // The forward's cut.  One pass over the whole time axis costs the least; where that leaves too
 // few warps, the axis is cut into segments, whose end states take a pass of their own.
 Cut fwd_cut(const ScanArgs& a) {
-    const int lanes = lanes_for(a.N), ch = NT / lanes;
+    const int ch = NT * fwd_states(a) / padded_states(a.N);
     Cut k;
     k.cbg = (a.C / a.G + ch - 1) / ch;
     k.cblocks = k.cbg * a.G;
@@ -415,21 +410,21 @@ cudaError_t scan_fwd(const ScanArgs& a, cudaStream_t s) {
     if (a.h_out != nullptr && a.h_out != a.h0 && (a.seqs.cu != nullptr || a.seqs.L == 0))
         scan_pass_kernel<<<gs, 256, 0, s>>>(a.seqs, a.nstate, w, a.h0, a.h_out, false);
     if (a.seqs.L == 0) return cudaGetLastError();
-    return with_lanes(lanes_for(a.N), [&](auto ll) {
-        constexpr int LPC = decltype(ll)::value;
+    return with_lay(a, [&](auto ll, auto nn) {
+        constexpr int LPC = decltype(ll)::value, NS = decltype(nn)::value;
         const unsigned g = (unsigned)(a.B * k.segs * k.cblocks);
         if (k.segs > 1) {
-            scan_fwd_kernel<T, LPC, 1, false><<<g, NT, 0, s>>>(a, k, rec_h, rec_d, h0);
+            scan_fwd_kernel<T, LPC, NS, false><<<g, NT, 0, s>>>(a, k, rec_h, rec_d, h0);
             scan_join_kernel<<<(unsigned)((a.B * w + 255) / 256), 256, 0, s>>>(a, k.segs, rec_h, rec_d);
         }
-        scan_fwd_kernel<T, LPC, 1, true><<<g, NT, 0, s>>>(a, k, rec_h, rec_d, h0);
+        scan_fwd_kernel<T, LPC, NS, true><<<g, NT, 0, s>>>(a, k, rec_h, rec_d, h0);
         return cudaGetLastError();
     });
 }
 
 template <typename T>
 cudaError_t scan_step(const ScanArgs& a, cudaStream_t s) {
-    return with_lanes(lanes_for(a.N), [&](auto ll) {
+    return with_lanes(padded_states(a.N) / 4, [&](auto ll) {
         constexpr int LPC = decltype(ll)::value, LC = NT / LPC;
         scan_step_kernel<T, LPC><<<(unsigned)(a.B * ((a.C + LC - 1) / LC)), NT, 0, s>>>(a);
         return cudaGetLastError();

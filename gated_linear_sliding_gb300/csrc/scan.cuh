@@ -7,7 +7,6 @@ namespace lz {
 namespace scan {
 
 constexpr int NT = 128;      // threads a CTA
-constexpr int NS = 4;        // states a thread holds for each of its channels
 constexpr int CK = 16;       // tokens between the states kept for the backward
 constexpr int SEG = 64;      // segments are whole multiples of this many tokens
 
@@ -18,12 +17,58 @@ __device__ __forceinline__ float ex2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Two fp32 values in a register pair, and the paired instructions on them.  One issue slot does
+// two operations; measured, a pair takes 2.1 cycles of a scheduler with up to two operands of its
+// own and 3.1 with three, against 1.03 for each single fused multiply-add, so that pairs cost the
+// same multiplier time and leave slots for the loads, exponentials and shuffles between them.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pack(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 exp2_2(f2 v) {
+    float a, b;
+    unpack(v, a, b);
+    return pack(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    unpack(v, a, b);
+    return a + b;
+}
+
+// rcp.approx of a value in [1, 2^126): within one ulp
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| <= 1, and log1p(u) = 2 atanh(s) with
 // s = u / (2 + u) <= 1/3: the odd series to s^13 leaves 2 (1/3)^15 / 15, below 2^-26 of the
 // result.  (A logarithm of 1 + u would lose the digits of a small step size.)
 __device__ __forceinline__ float softplus_(float x) {
     const float u = ex2(-kLog2e * fabsf(x));
-    const float s = __fdividef(u, 2.0f + u), s2 = s * s;
+    const float s = u * rcp(2.0f + u), s2 = s * s;
     float p = 1.0f / 13.0f;
     p = fmaf(p, s2, 1.0f / 11.0f);
     p = fmaf(p, s2, 1.0f / 9.0f);
@@ -87,32 +132,107 @@ __device__ __forceinline__ void store8(T* p, const float* f, int n, bool vec) {
         if (i < n) lz::st(p + i, f[i]);
 }
 
-// Up to four consecutive fp32 values (n of them; the rest read as zero).
-__device__ __forceinline__ void load4(const float* p, int n, bool vec, float* f) {
-    if (vec && n == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+// NS consecutive fp32 values, n of them in the array (the rest read as zero); vec: p is aligned
+// to min(NS, 4) values.
+template <int NS>
+__device__ __forceinline__ void load_n(const float* p, int n, bool vec, float* f) {
+    if (vec && n == NS) {
+        if constexpr (NS % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i) {
+                const float4 v = reinterpret_cast<const float4*>(p)[i];
+                f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+            }
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(p);
+            f[0] = v.x, f[1] = v.y;
+        }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = i < n ? p[i] : 0.0f;
+    for (int i = 0; i < NS; ++i) f[i] = i < n ? p[i] : 0.0f;
 }
-__device__ __forceinline__ void store4(float* p, int n, bool vec, const float* f) {
-    if (vec && n == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+template <int NS>
+__device__ __forceinline__ void store_n(float* p, int n, bool vec, const float* f) {
+    if (vec && n == NS) {
+        if constexpr (NS % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i)
+                reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else {
+            *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+        }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NS; ++i)
         if (i < n) p[i] = f[i];
 }
-
-// Lanes that share a channel: the power of two that holds N states, four a lane.
-inline int lanes_for(int64_t N) {
-    int l = 1;
-    while (l * NS < N) l *= 2;
-    return l;
+// The same as pairs.
+template <int NS>
+__device__ __forceinline__ void load_pairs(const float* p, int n, bool vec, f2* f) {
+    float v[NS];
+    load_n<NS>(p, n, vec, v);
+#pragma unroll
+    for (int i = 0; i < NS / 2; ++i) f[i] = pack(v[2 * i], v[2 * i + 1]);
 }
+template <int NS>
+__device__ __forceinline__ void store_pairs(float* p, int n, bool vec, const f2* f) {
+    float v[NS];
+#pragma unroll
+    for (int i = 0; i < NS / 2; ++i) unpack(f[i], v[2 * i], v[2 * i + 1]);
+    store_n<NS>(p, n, vec, v);
+}
+
+// A row of Bm or Cm, eight states from n0 on, into a tile of pairs [state pair of a lane][lane].
+template <int NS, int LPC>
+__device__ __forceinline__ void put_states(f2* row, int n0, const float* f) {
+#pragma unroll
+    for (int j = 0; j < 8 && j < NS * LPC; j += 2) {
+        const int n = n0 + j;
+        row[n % NS / 2 * LPC + n / NS] = pack(f[j], f[j + 1]);
+    }
+}
+
+// States of a channel, padded: the power of two from 4 that holds N.
+inline int padded_states(int64_t N) {
+    int n = 4;
+    while (n < N) n *= 2;
+    return n;
+}
+
+// Values of a tile by (token, channel), staged by the thread that loads eight neighbouring
+// channels of a token and read by the lanes of a warp's LC channels: index [channel of eight]
+// [token][piece of eight], so that the writing lanes are neighbours and, with PAD more values
+// after each of the eight planes, the reading ones fall into different banks.
+template <int TT, int CH, int LC>
+struct Plane {
+    static constexpr int NV = CH / 8, PAD = LC >= 8 ? LC / 8 : 1, STEP = TT * NV + PAD, SIZE = 8 * STEP;
+    static __device__ __forceinline__ int at(int t, int c) { return (c & 7) * STEP + t * NV + (c >> 3); }
+};
+
+// Sums over the lanes `o`, 2 o, ... < END of U values at once: each stage hands half of the
+// values to the other lane.  Leaves CNT values in v[0 .. CNT), those from index `at` on, the same
+// in the lanes of any further stages.
+template <int U, int O, int END, int CNT = U>
+__device__ __forceinline__ int spread_sum(float* v, int lane, int at = 0) {
+    if constexpr (O >= END) return at;
+    else if constexpr (CNT > 1) {
+        constexpr int H = CNT / 2;
+        const bool up = lane & O;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float send = up ? v[i] : v[H + i], keep = up ? v[H + i] : v[i];
+            v[i] = keep + __shfl_xor_sync(~0u, send, O);
+        }
+        return spread_sum<U, O * 2, END, H>(v, lane, at + (up ? H : 0));
+    } else {
+        v[0] += __shfl_xor_sync(~0u, v[0], O);
+        return spread_sum<U, O * 2, END, 1>(v, lane, at);
+    }
+}
+// How many values spread_sum leaves: U over the lanes' number, at least one.
+constexpr int spread_left(int U, int lanes) { return U > lanes ? U / lanes : 1; }
 
 // How a call is cut into CTAs: blocks of channels (none across two groups) x segments of the
 // time axis x rows of the batch.

@@ -6,13 +6,21 @@
 //   gb = sum_n G Bm,   dx = d gb + D e,   dd = x gb + sum_n q A,   ddt = dd sigmoid(dt + bias),
 //   dz = dy (sum_n Cm h + D x) silu'(z),   dh0 = a[first] G[first].
 //
-// A CTA of 128 threads owns a block of channels (lanes and states as in the forward) and walks a
-// segment backwards, 16 tokens at a time from the state the forward kept at their start: the
-// second eight tokens' states are recomputed into registers and walked backwards, then the first
-// eight's.  The decays are computed again on the way back, which costs less than holding them.
-// Sums over states go over a channel's lanes, sums over channels over the other lanes and then
-// over the CTA's warps in shared memory; the CTA's part of dBm and dCm, of dA, dD and ddt_bias
-// goes to the workspace and is added in a fixed order.
+// A CTA of 128 threads owns a block of channels and walks a segment backwards, 16 tokens at a time
+// from the state the forward kept at their start: one walk forward leaves the states before each
+// four tokens in shared memory, then four tokens at a time, from the last, are walked forward
+// again into registers and backwards.  The decays are computed again on the way back, which costs
+// less than holding them.  A thread holds four states of two channels.
+//
+// What bounds it is the number of instructions, and of those a third are the sums that cross
+// lanes: over states (three values a token and channel) and over channels (dBm and dCm).  Each
+// stage of such a sum hands half of the values to another lane.  Which half is free of selects
+// where it goes by an order that the lanes do not share: neighbouring lanes of a channel hold the
+// two channels in opposite order, and neighbouring channels hold the two pairs of states in
+// opposite order, so that every lane sends its second one and keeps its first.
+//
+// The CTA's parts of dBm and dCm, of dA, dD and ddt_bias go to the workspace and are added in a
+// fixed order.
 #include <type_traits>
 
 #include "scan.cuh"
@@ -21,37 +29,45 @@ namespace lz {
 namespace scan {
 namespace {
 
-constexpr int HB = CK / 2;  // tokens whose states are held at once
+constexpr int QT = 4, QN = CK / QT;  // tokens whose states are held at once, and how often a chunk
+constexpr int NS = 4, H = 2;  // states a lane holds of a channel, and pairs of them
 
 template <int LPC>
 struct Lay {
-    static constexpr int CPT = LPC >= 4 ? 2 : 1;  // channels a thread
+    static constexpr int CPT = LPC > 1 ? 2 : 1;  // channels a thread
     static constexpr int LC = 32 / LPC;
-    static constexpr int CH = NT / 32 * LC * CPT;
+    static constexpr int CW = LC * CPT;          // channels a warp
+    static constexpr int CH = NT / 32 * CW;
     static constexpr int NP = NS * LPC;
     static constexpr int NV = CH / 8;
     static constexpr int PX = (CK * NV + NT - 1) / NT;
-    static constexpr int PB = (CK * (NP + 7) / 8 + NT - 1) / NT;
-    static constexpr int OS = CH + 8;  // row stride of the outputs' tiles
+    static constexpr int NQ = (NP + 7) / 8;
+    static constexpr int PB = (CK * NQ + NT - 1) / NT;
+    static constexpr int KEEP = spread_left(16, 32 / NV > 1 ? 32 / NV : 1);
+    using P = Plane<CK, CH, CW>;
 };
 
 template <int LPC>
 struct Smem {
     using L = Lay<LPC>;
-    float2 dx[CK][L::CH];  // d, d x
-    float e[CK][L::CH];
-    float2 b[CK][2][LPC], c[CK][2][LPC];
-    float gb[CK][L::OS], qa[CK][L::OS], ch[CK][L::OS];  // sums over states
-    float bc[NT / 32][CK][2][L::NP];                    // a warp's sums over channels
+    // (d, d), (d x, d x), (e, e); once a token has been walked back, the second becomes its sums
+    // over states (gb, qa) and the last one's first half that of Cm h
+    f2 d[L::P::SIZE], dx[L::P::SIZE], e[L::P::SIZE];
+    f2 b[CK][H * LPC], c[CK][H * LPC];
+    float bc[NT / 32][CK][2][L::NP];         // a warp's sums over channels
+    float bias[L::CH], skip[L::CH];          // dt_bias and D of the channels
+    f2 start[QN][L::CPT * H][NT];            // a thread's states before each four tokens
+    f2 dA[L::CPT * H][NT];                   // a thread's dA: a chunk's terms are added up first
 };
 
 template <typename T, int LPC>
-__global__ void __launch_bounds__(NT) scan_bwd_kernel(const ScanArgs a, const Cut cut,
+__global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const ScanArgs a, const Cut cut,
                                                       const float* rec_g, float* pbc, float* pA,
                                                       float* pD, float* pbias) {
     using L = Lay<LPC>;
+    using P = typename L::P;
     constexpr int CPT = L::CPT, LC = L::LC, CH = L::CH, NP = L::NP, NV = L::NV, PX = L::PX, PB = L::PB;
-    constexpr int NQ = (NP + 7) / 8;
+    constexpr int NQ = L::NQ, KEEP = L::KEEP;
     constexpr bool FAST = is_fast<T>();
     extern __shared__ __align__(16) unsigned char smraw[];
     Smem<LPC>& sm = *reinterpret_cast<Smem<LPC>*>(smraw);
@@ -59,42 +75,43 @@ __global__ void __launch_bounds__(NT) scan_bwd_kernel(const ScanArgs a, const Cu
     check_offsets(a.seqs, a.header);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane & (LPC - 1), cl = lane / LPC;
+    const bool swap = cl & 1;  // this lane's pairs of states are held in reverse order
     const int N = (int)a.N, nn = max(0, min(NS, N - NS * q));
     const bool v4 = N % 4 == 0;
     const int64_t t0 = w.seg * cut.seg_len, t1 = min64(t0 + cut.seg_len, a.seqs.L);
     const int64_t row0 = w.b * a.seqs.L, C = a.C, nck = (a.seqs.L + CK - 1) / CK;
-    const int lch = warp * (LC * CPT) + cl;  // channel k of this thread: lch + k LC
-
-    float A2[CPT][NS], dA[CPT][NS], gn[CPT][NS];
-    int64_t ch[CPT];
-    bool own[CPT];
-    auto load_state = [&](const float* p, float (*f)[NS]) {  // p: [C, N] or null
-#pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-#pragma unroll
-            for (int i = 0; i < NS; ++i) f[k][i] = 0.0f;
-            if (p != nullptr && own[k]) load4(p + ch[k] * N + NS * q, nn, v4, f[k]);
-        }
-    };
-    auto put_state = [&](float* p, float (*f)[NS]) {
-#pragma unroll
-        for (int k = 0; k < CPT; ++k)
-            if (own[k]) store4(p + ch[k] * N + NS * q, nn, v4, f[k]);
-    };
-    auto seq_state = [&](const float* p, int64_t seq) { return p == nullptr ? p : p + seq * C * N; };
+    int lch[CPT], pl[CPT];  // channel k of this thread (the order goes by the lane), its place in a plane
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-        ch[k] = w.c0 + lch + k * LC;
-        own[k] = ch[k] < w.clim;
+        lch[k] = warp * L::CW + (CPT == 2 ? (k ^ (q & 1)) * LC : 0) + cl;
+        pl[k] = P::at(0, lch[k]);
     }
+    const int pair0 = (swap ? LPC : 0) + q, pair1 = (swap ? 0 : LPC) + q;  // of a row of b and c
+
+    auto load_state = [&](const float* p, f2 (*f)[H]) {  // p: [C, N] or null
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            f2 v[H] = {0, 0};
+            if (p != nullptr && w.c0 + lch[k] < w.clim)
+                load_pairs<NS>(p + (w.c0 + lch[k]) * N + NS * q, nn, v4, v);
+            f[k][0] = swap ? v[1] : v[0];
+            f[k][1] = swap ? v[0] : v[1];
+        }
+    };
+    auto put_state = [&](float* p, f2 (*f)[H]) {
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            const f2 v[H] = {swap ? f[k][1] : f[k][0], swap ? f[k][0] : f[k][1]};
+            if (w.c0 + lch[k] < w.clim) store_pairs<NS>(p + (w.c0 + lch[k]) * N + NS * q, nn, v4, v);
+        }
+    };
+    auto seq_state = [&](const float* p, int64_t seq) { return p == nullptr ? p : p + seq * C * N; };
+    f2 A2[CPT][H], gn[CPT][H];
     load_state(a.A, A2);
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            A2[k][i] *= kLog2e;
-            dA[k][i] = 0.0f;
-        }
+        for (int i = 0; i < H; ++i) A2[k][i] = mul2(A2[k][i], pack(kLog2e, kLog2e));
     // gn: the gradient that reaches the state after a token from later ones
     SeqAt sq = seq_at(a.seqs, w.b, t1 - 1);
     if (t1 == sq.end) load_state(seq_state(a.dh_out, sq.seq), gn);
@@ -104,215 +121,219 @@ __global__ void __launch_bounds__(NT) scan_bwd_kernel(const ScanArgs a, const Cu
                      a.ldz % 8 == 0 && a.ldy % 8 == 0 && a.lddx % 8 == 0 && a.ldddt % 8 == 0 &&
                      a.lddz % 8 == 0;
     const bool vecb = N % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0;
-    const int pc = tid % NV * 8, pt = tid / NV;
-    const int64_t pch = w.c0 + pc;
+    const int pv = tid % NV, pt = tid / NV;
+    const int64_t pch = w.c0 + pv * 8;
     const int pn = (int)max64(0, min64(8, w.clim - pch));
     constexpr int DT = NT / NV;
-    float sD[8], sbias[8];
+    for (int c = tid; c < CH; c += NT) {
+        const bool in = w.c0 + c < w.clim;
+        sm.bias[c] = in && a.dt_bias != nullptr ? a.dt_bias[w.c0 + c] : 0.0f;
+        sm.skip[c] = in && a.D != nullptr ? a.D[w.c0 + c] : 0.0f;
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sD[j] = sbias[j] = 0.0f;
+    for (int i = 0; i < CPT * H; ++i) sm.dA[i][tid] = 0;
+    float keep[KEEP];  // sums of dD's and ddt_bias's terms: see below
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) keep[i] = 0.0f;
+    // places of this lane's shares of the sums across lanes
+    float dummy[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int at_t = spread_sum<4, 2, LPC>(dummy, lane), at_n = spread_sum<4, LPC * 2, 32>(dummy, lane);
+    constexpr int LEFT_T = spread_left(4, LPC / 2 > 0 ? LPC / 2 : 1), LEFT_N = spread_left(4, LC / 2);
+    const bool put_t = LPC <= 8 || q < 8, put_n = LC <= 8 || cl < 8;
 
-    auto step = [&](int tl, float (*h)[NS]) {  // the recurrence, one token on
-        const float2 b0 = sm.b[tl][0][q], b1 = sm.b[tl][1][q];
-        const float bb[4] = {b0.x, b0.y, b1.x, b1.y};
+    auto step = [&](int tl, f2 (*h)[H]) {  // the recurrence, one token on
+        const f2 b[H] = {sm.b[tl][pair0], sm.b[tl][pair1]};
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
-            const float2 d = sm.dx[tl][lch + k * LC];
+            const f2 d = sm.d[pl[k] + tl * NV], dx = sm.dx[pl[k] + tl * NV];
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[k][i] = fmaf(ex2(d.x * A2[k][i]), h[k][i], d.y * bb[i]);
+            for (int i = 0; i < H; ++i) h[k][i] = fma2(exp2_2(mul2(d, A2[k][i])), h[k][i], mul2(dx, b[i]));
         }
     };
 
+    // The tokens [tt, tt + 16) of which those before t1 are walked.  PLAIN: none of them begins a
+    // sequence.
+    f2 dA[CPT][H];
+    auto chunk = [&](int64_t tt, auto plain) {
+        constexpr bool PLAIN = decltype(plain)::value;
+        f2 h[CPT][H];
+        load_state(a.states + (w.b * nck + tt / CK) * C * N, h);
+        auto enter = [&](int tl) {  // the state before a token
+            if (PLAIN || tt + tl >= t1) return;
+            const SeqAt s = seq_at(a.seqs, w.b, tt + tl);
+            if (s.begin == tt + tl) load_state(seq_state(a.h0, s.seq), h);
+        };
+        // the last token's step is not needed; a segment's short last chunk stops at its end
+        const int quarters = (int)((min64(tt + CK, t1) - tt + QT - 1) / QT);
+#pragma unroll 1
+        for (int j = 0; j < quarters; ++j) {
+#pragma unroll
+            for (int k = 0; k < CPT; ++k)
+#pragma unroll
+                for (int i = 0; i < H; ++i) sm.start[j][k * H + i][tid] = h[k][i];
+            if (j + 1 == quarters) break;
+#pragma unroll
+            for (int u = 0; u < QT; ++u) {
+                enter(j * QT + u);
+                step(j * QT + u, h);
+            }
+        }
+#pragma unroll 1
+        for (int j = quarters - 1; j >= 0; --j) {
+            const int l0 = j * QT;
+            f2 hist[QT + 1][CPT][H];
+#pragma unroll
+            for (int k = 0; k < CPT; ++k)
+#pragma unroll
+                for (int i = 0; i < H; ++i) h[k][i] = hist[0][k][i] = sm.start[j][k * H + i][tid];
+#pragma unroll
+            for (int u = 0; u < QT; ++u) {
+                enter(l0 + u);
+                step(l0 + u, h);
+#pragma unroll
+                for (int k = 0; k < CPT; ++k)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) hist[u + 1][k][i] = h[k][i];
+            }
+            float pgb[QT], pqa[QT], pch[QT];  // of the first channel in this lane's order
+#pragma unroll
+            for (int u = QT - 1; u >= 0; --u) {
+                const int tl = l0 + u;
+                const f2 b[H] = {sm.b[tl][pair0], sm.b[tl][pair1]};
+                const f2 c[H] = {sm.c[tl][pair0], sm.c[tl][pair1]};
+                const bool first = !PLAIN && tt + tl == sq.begin && tt + tl < t1;
+                f2 hp[CPT][H];  // the state before the token
+#pragma unroll
+                for (int k = 0; k < CPT; ++k)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) hp[k][i] = hist[u][k][i];
+                if (first) load_state(seq_state(a.h0, sq.seq), hp);
+                f2 vb[H], vc[H];  // dBm, dCm of this lane's states, over its channels
+                float gb[CPT], qa[CPT], cs[CPT];
+#pragma unroll
+                for (int k = 0; k < CPT; ++k) {
+                    const f2 d = sm.d[pl[k] + tl * NV], dx = sm.dx[pl[k] + tl * NV], e = sm.e[pl[k] + tl * NV];
+                    f2 sgb, sqa, scs;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const f2 g = fma2(c[i], e, gn[k][i]), hh = hist[u + 1][k][i];
+                        const f2 ag = mul2(exp2_2(mul2(d, A2[k][i])), g), qq = mul2(ag, hp[k][i]);
+                        gn[k][i] = ag;
+                        dA[k][i] = fma2(qq, d, dA[k][i]);
+                        sqa = i == 0 ? mul2(qq, A2[k][i]) : fma2(qq, A2[k][i], sqa);
+                        sgb = i == 0 ? mul2(g, b[i]) : fma2(g, b[i], sgb);
+                        scs = i == 0 ? mul2(c[i], hh) : fma2(c[i], hh, scs);
+                        vb[i] = k == 0 ? mul2(g, dx) : fma2(g, dx, vb[i]);
+                        vc[i] = k == 0 ? mul2(hh, e) : fma2(hh, e, vc[i]);
+                    }
+                    gb[k] = sum2(sgb);
+                    qa[k] = sum2(sqa);
+                    cs[k] = sum2(scs);
+                }
+                if (first) {
+                    if (a.dh0 != nullptr) put_state(a.dh0 + sq.seq * C * N, gn);
+                    if (tt + tl > t0) {
+                        sq = seq_at(a.seqs, w.b, tt + tl - 1);
+                        load_state(seq_state(a.dh_out, sq.seq), gn);
+                    }
+                }
+                // over states, first stage: the second channel goes to the neighbouring lane,
+                // whose first it is
+                if constexpr (CPT == 2) {
+                    gb[0] += __shfl_xor_sync(~0u, gb[1], 1);
+                    qa[0] += __shfl_xor_sync(~0u, qa[1], 1);
+                    cs[0] += __shfl_xor_sync(~0u, cs[1], 1);
+                }
+                pgb[u] = gb[0];
+                pqa[u] = qa[0];
+                pch[u] = cs[0];
+                // over channels: the second pair of states goes to the lane that has it first
+                float v[4], s0, s1;
+                unpack(vb[1], s0, s1);
+                f2 x = pack(__shfl_xor_sync(~0u, s0, LPC), __shfl_xor_sync(~0u, s1, LPC));
+                unpack(add2(vb[0], x), v[0], v[1]);
+                unpack(vc[1], s0, s1);
+                x = pack(__shfl_xor_sync(~0u, s0, LPC), __shfl_xor_sync(~0u, s1, LPC));
+                unpack(add2(vc[0], x), v[2], v[3]);
+                spread_sum<4, LPC * 2, 32>(v, lane);
+#pragma unroll
+                for (int i = 0; i < LEFT_N; ++i)
+                    if (put_n) sm.bc[warp][tl][(at_n + i) / 2][NS * q + (swap ? 2 : 0) + (at_n + i) % 2] = v[i];
+            }
+            // over states, the other stages: four tokens together, of which a lane keeps some.
+            // All lanes of a channel have read the tokens' planes by now.
+            spread_sum<4, 2, LPC>(pgb, lane);
+            spread_sum<4, 2, LPC>(pqa, lane);
+            spread_sum<4, 2, LPC>(pch, lane);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < LEFT_T; ++i)
+                if (put_t) {
+                    const int o = pl[0] + (l0 + at_t + i) * NV;
+                    sm.dx[o] = pack(pgb[i], pqa[i]);
+                    reinterpret_cast<float*>(&sm.e[o])[0] = pch[i];
+                }
+        }
+    };
+
+#pragma unroll 1
     for (int64_t tt = t0 + (t1 - 1 - t0) / CK * CK; tt >= t0; tt -= CK) {
-        Raw<T> rx[PX], rdt[PX], rz[PX], rdy[PX];
+        __syncthreads();  // the last chunk's tiles have been read
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int tl = pt + i * DT;
-            const int n = tl < CK && tt + tl < t1 ? pn : 0;
+            if (tl >= CK) break;
+            const bool live = tt + tl < t1;
+            const int n = live ? pn : 0;
             const int64_t r = row0 + tt + tl;
-            rx[i].load((const T*)a.x + r * a.ldx + pch, n, vec);
-            rdt[i].load((const T*)a.dt + r * a.lddt + pch, n, vec);
-            rdy[i].load((const T*)a.dy + r * a.ldy + pch, n, vec);
-            if (a.z != nullptr) rz[i].load((const T*)a.z + r * a.ldz + pch, n, vec);
+            Raw<T> rx, rdt, rz, rdy;
+            rx.load((const T*)a.x + r * a.ldx + pch, n, vec);
+            rdt.load((const T*)a.dt + r * a.lddt + pch, n, vec);
+            rdy.load((const T*)a.dy + r * a.ldy + pch, n, vec);
+            if (a.z != nullptr) rz.load((const T*)a.z + r * a.ldz + pch, n, vec);
+            float fx[8], fd[8], fe[8], fz[8];
+            rx.get(fx);
+            rdt.get(fd);
+            rdy.get(fe);
+            if (a.z != nullptr) rz.get(fz);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int o = P::at(tl, pv * 8 + j);
+                const float v = fd[j] + sm.bias[pv * 8 + j];
+                // a place past the segment's end must leave the state and its gradient as they are
+                const float d = live ? (a.softplus ? softplus_(v) : v) : 0.0f, dx = d * fx[j];
+                const float e = a.z != nullptr ? fe[j] * (fz[j] * sigm<FAST>(fz[j])) : fe[j];
+                sm.d[o] = pack(d, d);
+                sm.dx[o] = pack(dx, dx);
+                sm.e[o] = pack(e, e);
+            }
         }
-        float hs[CPT][NS];  // the state before the chunk
-        load_state(a.states + (w.b * nck + tt / CK) * C * N, hs);
-        __syncthreads();  // the last chunk's tiles have been read
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
             const int e = tid + i * NT, tl = e / NQ, n0 = e % NQ * 8;
             if (tl >= CK) break;
             const int n = tt + tl < t1 ? max(0, min(8, N - n0)) : 0;
             const int64_t r = row0 + tt + tl;
-            Raw<T> v;
+            Raw<T> rb, rc;
             float f[8];
-            v.load((const T*)a.Bm + r * a.ldb + w.grp * N + n0, n, vecb);
-            v.get(f);
-#pragma unroll
-            for (int j = 0; j < 8 && j < NP; j += 2)
-                sm.b[tl][j / 2 % 2][(n0 + j) / 4] = make_float2(f[j], f[j + 1]);
-            v.load((const T*)a.Cm + r * a.ldc + w.grp * N + n0, n, vecb);
-            v.get(f);
-#pragma unroll
-            for (int j = 0; j < 8 && j < NP; j += 2)
-                sm.c[tl][j / 2 % 2][(n0 + j) / 4] = make_float2(f[j], f[j + 1]);
-        }
-#pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int tl = pt + i * DT;
-            if (tl >= CK) break;
-            const bool live = tt + tl < t1;
-            float fx[8], fd[8], fe[8], fz[8];
-            rx[i].get(fx);
-            rdt[i].get(fd);
-            rdy[i].get(fe);
-            if (a.z != nullptr) rz[i].get(fz);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = fd[j] + (a.dt_bias != nullptr && j < pn ? a.dt_bias[pch + j] : 0.0f);
-                // a place past the segment's end must leave the state and its gradient as they are
-                const float d = live ? (a.softplus ? softplus_(v) : v) : 0.0f;
-                sm.dx[tl][pc + j] = make_float2(d, d * fx[j]);
-                sm.e[tl][pc + j] = a.z != nullptr ? fe[j] * (fz[j] * sigm<FAST>(fz[j])) : fe[j];
-            }
+            rb.load((const T*)a.Bm + r * a.ldb + w.grp * N + n0, n, vecb);
+            rc.load((const T*)a.Cm + r * a.ldc + w.grp * N + n0, n, vecb);
+            rb.get(f);
+            put_states<NS, LPC>(sm.b[tl], n0, f);
+            rc.get(f);
+            put_states<NS, LPC>(sm.c[tl], n0, f);
         }
         __syncthreads();
-#pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-            const int l0 = half * HB;
-            if (tt + l0 >= t1) continue;
-            float h[CPT][NS], hist[HB][CPT][NS];
 #pragma unroll
-            for (int k = 0; k < CPT; ++k)
+        for (int k = 0; k < CPT; ++k)
 #pragma unroll
-                for (int i = 0; i < NS; ++i) h[k][i] = hs[k][i];
-            // whether a sequence begins among the chunk's tokens up to the half's end
-            const bool plain = sq.begin < tt;
-            auto enter = [&](int64_t t) {  // the state before token t
-                const SeqAt s = seq_at(a.seqs, w.b, t);
-                if (s.begin == t) load_state(seq_state(a.h0, s.seq), h);
-            };
-            for (int tl = 0; tl < l0; ++tl) {
-                if (!plain) enter(tt + tl);
-                step(tl, h);
-            }
-            float hb0[CPT][NS];  // the state before the half
+            for (int i = 0; i < H; ++i) dA[k][i] = 0;
+        if (sq.begin < tt) chunk(tt, std::true_type());
+        else chunk(tt, std::false_type());
 #pragma unroll
-            for (int k = 0; k < CPT; ++k)
+        for (int k = 0; k < CPT; ++k)
 #pragma unroll
-                for (int i = 0; i < NS; ++i) hb0[k][i] = h[k][i];
-#pragma unroll
-            for (int u = 0; u < HB; ++u) {
-                if (!plain && tt + l0 + u < t1) enter(tt + l0 + u);
-                step(l0 + u, h);
-#pragma unroll
-                for (int k = 0; k < CPT; ++k)
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) hist[u][k][i] = h[k][i];
-            }
-#pragma unroll
-            for (int u4 = HB - 4; u4 >= 0; u4 -= 4) {
-                float pgb[4][CPT], pqa[4][CPT], pch[4][CPT];
-#pragma unroll
-                for (int u3 = 3; u3 >= 0; --u3) {
-                    const int u = u4 + u3, tl = l0 + u;
-                    const int64_t t = tt + tl;
-                    const float2 b0 = sm.b[tl][0][q], b1 = sm.b[tl][1][q];
-                    const float2 c0 = sm.c[tl][0][q], c1 = sm.c[tl][1][q];
-                    const float bb[4] = {b0.x, b0.y, b1.x, b1.y}, cc[4] = {c0.x, c0.y, c1.x, c1.y};
-                    const bool first = !plain && t == sq.begin && t < t1;
-                    float hp[CPT][NS];
-#pragma unroll
-                    for (int k = 0; k < CPT; ++k)
-#pragma unroll
-                        for (int i = 0; i < NS; ++i) hp[k][i] = u > 0 ? hist[u > 0 ? u - 1 : 0][k][i] : hb0[k][i];
-                    if (first) load_state(seq_state(a.h0, sq.seq), hp);
-                    float v[8];  // dBm, dCm of this lane's states, over its channels
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < CPT; ++k) {
-                        const float2 d = sm.dx[tl][lch + k * LC];
-                        const float e = sm.e[tl][lch + k * LC];
-                        float gb = 0.0f, qa = 0.0f, cs = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < NS; ++i) {
-                            const float g = fmaf(cc[i], e, gn[k][i]);
-                            const float ag = ex2(d.x * A2[k][i]) * g;
-                            const float qq = ag * hp[k][i];
-                            gn[k][i] = ag;
-                            dA[k][i] = fmaf(qq, d.x, dA[k][i]);
-                            qa = fmaf(qq, A2[k][i], qa);
-                            gb = fmaf(g, bb[i], gb);
-                            cs = fmaf(cc[i], hist[u][k][i], cs);
-                            v[i] = fmaf(g, d.y, v[i]);
-                            v[4 + i] = fmaf(e, hist[u][k][i], v[4 + i]);
-                        }
-                        pgb[u3][k] = gb;
-                        pqa[u3][k] = qa;
-                        pch[u3][k] = cs;
-                    }
-                    if (first) {
-                        if (a.dh0 != nullptr) put_state(a.dh0 + sq.seq * C * N, gn);
-                        if (t > t0) {
-                            sq = seq_at(a.seqs, w.b, t - 1);
-                            load_state(seq_state(a.dh_out, sq.seq), gn);
-                        }
-                    }
-                    // over the lanes with the same states: each stage hands half of the values
-                    // over, and a lane ends with one (or, with few such lanes, some) of the eight
-                    int at = 0, cnt = 8;
-#pragma unroll
-                    for (int o = LPC; o < 32; o *= 2) {
-                        const bool up = lane & o;
-                        if (cnt > 1) {
-                            cnt /= 2;
-#pragma unroll
-                            for (int i = 0; i < cnt; ++i) {
-                                const float send = up ? v[i] : v[cnt + i], keep = up ? v[cnt + i] : v[i];
-                                v[i] = keep + __shfl_xor_sync(~0u, send, o);
-                            }
-                            at += up ? cnt : 0;
-                        } else {
-                            v[0] += __shfl_xor_sync(~0u, v[0], o);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < cnt; ++i)
-                        if (LPC >= 4 || cl < 8) sm.bc[warp][tl][(at + i) / 4][NS * q + (at + i) % 4] = v[i];
-                }
-                // over a channel's lanes, four tokens together; a lane keeps one token of four
-                auto put = [&](float (*p)[CPT], float* o) {
-#pragma unroll
-                    for (int k = 0; k < CPT; ++k) {
-                        float* y = o + k * LC;
-                        if constexpr (LPC == 1) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) y[i * L::OS] = p[i][k];
-                        } else {
-                            const bool b0 = q & 1;
-                            float u = b0 ? p[1][k] : p[0][k], v = b0 ? p[3][k] : p[2][k];
-                            u += __shfl_xor_sync(~0u, b0 ? p[0][k] : p[1][k], 1);
-                            v += __shfl_xor_sync(~0u, b0 ? p[2][k] : p[3][k], 1);
-                            if constexpr (LPC == 2) {
-                                y[(q & 1) * L::OS] = u;
-                                y[(2 + (q & 1)) * L::OS] = v;
-                            } else {
-                                const bool b1 = q & 2;
-                                float s = b1 ? v : u;
-                                s += __shfl_xor_sync(~0u, b1 ? u : v, 2);
-#pragma unroll
-                                for (int x = 4; x < LPC; x *= 2) s += __shfl_xor_sync(~0u, s, x);
-                                if (q < 4) y[(q & 3) * L::OS] = s;
-                            }
-                        }
-                    }
-                };
-                put(pgb, &sm.gb[l0 + u4][lch]);
-                put(pqa, &sm.qa[l0 + u4][lch]);
-                if (a.z != nullptr) put(pch, &sm.ch[l0 + u4][lch]);
-            }
-        }
+            for (int i = 0; i < H; ++i) sm.dA[k * H + i][tid] = add2(sm.dA[k * H + i][tid], dA[k][i]);
         __syncthreads();
         // the CTA's part of dBm and dCm
         float* o = pbc + (((w.cb % cut.cbg) * a.B * a.seqs.L + row0 + tt) * a.G + w.grp) * 2 * N;
@@ -325,59 +346,82 @@ __global__ void __launch_bounds__(NT) scan_bwd_kernel(const ScanArgs a, const Cu
             o[((int64_t)tl * a.G * 2 + m) * N + n] = s;
         }
         // the gradients of x, dt and z
+        float terms[16];  // of dD and ddt_bias, this thread's channels
+#pragma unroll
+        for (int j = 0; j < 16; ++j) terms[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int tl = pt + i * DT;
             if (tl >= CK) break;
             const int n = tt + tl < t1 ? pn : 0;
+            const int64_t r = row0 + tt + tl;
+            Raw<T> rx, rdt, rz, rdy;
+            rx.load((const T*)a.x + r * a.ldx + pch, n, vec);
+            rdt.load((const T*)a.dt + r * a.lddt + pch, n, vec);
+            rdy.load((const T*)a.dy + r * a.ldy + pch, n, vec);
+            if (a.z != nullptr) rz.load((const T*)a.z + r * a.ldz + pch, n, vec);
             float fx[8], fd[8], fy[8], fz[8], ox[8], ot[8], oz[8];
-            rx[i].get(fx);
-            rdt[i].get(fd);
-            rdy[i].get(fy);
-            if (a.z != nullptr) rz[i].get(fz);
+            rx.get(fx);
+            rdt.get(fd);
+            rdy.get(fy);
+            if (a.z != nullptr) rz.get(fz);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float D = a.D != nullptr && j < n ? a.D[pch + j] : 0.0f;
-                const float d = sm.dx[tl][pc + j].x, e = sm.e[tl][pc + j], gb = sm.gb[tl][pc + j];
-                ox[j] = fmaf(d, gb, D * e);
-                // qa was summed with A log2(e)
-                float dd = fmaf(fx[j], gb, sm.qa[tl][pc + j] * 0.69314718055994531f);
-                if (a.softplus) {
-                    const float v = fd[j] + (a.dt_bias != nullptr && j < n ? a.dt_bias[pch + j] : 0.0f);
-                    dd *= sigm<FAST>(v);
-                }
-                ot[j] = dd;
-                if (j < n) {
-                    sD[j] = fmaf(e, fx[j], sD[j]);
-                    sbias[j] += dd;
-                }
+                const int at = P::at(tl, pv * 8 + j);
+                const float D = sm.skip[pv * 8 + j];
+                float d, gb, qa, e = fy[j], ch, x;
+                unpack(sm.d[at], d, x);
+                unpack(sm.dx[at], gb, qa);
+                unpack(sm.e[at], ch, x);
                 if (a.z != nullptr) {
                     const float sg = sigm<FAST>(fz[j]);
-                    oz[j] = fy[j] * fmaf(D, fx[j], sm.ch[tl][pc + j]) * dsilu(fz[j], sg);
+                    e *= fz[j] * sg;
+                    oz[j] = fy[j] * fmaf(D, fx[j], ch) * dsilu(fz[j], sg);
+                }
+                ox[j] = fmaf(d, gb, D * e);
+                // qa was summed with A log2(e)
+                float dd = fmaf(fx[j], gb, qa * 0.69314718055994531f);
+                if (a.softplus) dd *= sigm<FAST>(fd[j] + sm.bias[pv * 8 + j]);
+                ot[j] = dd;
+                if (j < n) {
+                    terms[j] = fmaf(e, fx[j], terms[j]);
+                    terms[8 + j] += dd;
                 }
             }
-            const int64_t r = row0 + tt + tl;
             store8((T*)a.dx + r * a.lddx + pch, ox, n, vec);
             store8((T*)a.ddt + r * a.ldddt + pch, ot, n, vec);
             if (a.z != nullptr) store8((T*)a.dz + r * a.lddz + pch, oz, n, vec);
         }
+        // over the warp's threads of the same channels; a thread keeps KEEP of the sixteen sums
+        spread_sum<16, NV, 32>(terms, lane);
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) keep[i] += terms[i];
     }
     // the CTA's part of dA, dD and ddt_bias
     const int64_t part = w.b * cut.segs + w.seg;
-    put_state(pA + part * C * N, dA);
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(smraw);  // [2][DT][CH]
+    f2 tA[CPT][H];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        red[pt * CH + pc + j] = sD[j];
-        red[(DT + pt) * CH + pc + j] = sbias[j];
+    for (int k = 0; k < CPT; ++k)
+#pragma unroll
+        for (int i = 0; i < H; ++i) tA[k][i] = sm.dA[k * H + i][tid];
+    put_state(pA + part * C * N, tA);
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smraw);  // [warps][2][CH]
+    {
+        float none[16] = {};
+        const int at = spread_sum<16, NV, 32>(none, lane);
+        // where a warp holds a channel's threads once or less often than its lanes, every lane has
+        // its own sums; else lanes that ended with the same ones write the same values
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            red[(warp * 2 + (at + i) / 8) * CH + pv * 8 + (at + i) % 8] = keep[i];
     }
     __syncthreads();
     for (int e = tid; e < 2 * CH; e += NT) {
         const int c = e % CH, m = e / CH;
         if (w.c0 + c >= w.clim) continue;
         float s = 0.0f;
-        for (int k = 0; k < DT; ++k) s += red[(m * DT + k) * CH + c];
+        for (int k = 0; k < NT / 32; ++k) s += red[(k * 2 + m) * CH + c];
         (m == 0 ? pD : pbias)[part * C + w.c0 + c] = s;
     }
 }
@@ -389,37 +433,40 @@ template <typename T, int LPC>
 __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cut cut, float* rec_g,
                                                       float* rec_d) {
     using L = Lay<LPC>;
-    constexpr int CPT = L::CPT, LC = L::LC, CH = L::CH, NP = L::NP, NV = L::NV, PX = L::PX, PB = L::PB;
-    constexpr int NQ = (NP + 7) / 8, DT = NT / NV;
+    using P = typename L::P;
+    constexpr int CPT = L::CPT, LC = L::LC, CH = L::CH, NV = L::NV, PX = L::PX, PB = L::PB, NQ = L::NQ;
+    constexpr int DT = NT / NV;
     constexpr bool FAST = is_fast<T>();
-    __shared__ float2 sde[CK][CH];  // d, e
-    __shared__ float2 sc[CK][2][LPC];
+    __shared__ __align__(16) f2 sd[P::SIZE];  // (d, d)
+    __shared__ __align__(16) f2 se[P::SIZE];  // (e, e)
+    __shared__ __align__(16) f2 sc[CK][H * LPC];
     const Where<CH> w(a, cut);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int q = lane & (LPC - 1), lch = warp * (LC * CPT) + lane / LPC;
+    const int q = lane & (LPC - 1), lch = warp * L::CW + lane / LPC;
     const int N = (int)a.N, nn = max(0, min(NS, N - NS * q));
     const bool v4 = N % 4 == 0;
     const int64_t t0 = w.seg * cut.seg_len, t1 = min64(t0 + cut.seg_len, a.seqs.L);
     const int64_t row0 = w.b * a.seqs.L, C = a.C;
-    float A2[CPT][NS], p[CPT][NS], acc[CPT][NS], sd[CPT];
+    f2 A2[CPT][H], p[CPT][H], acc[CPT][H];
+    float sum[CPT];
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const int64_t c = w.c0 + lch + k * LC;
-        if (c < w.clim) load4(a.A + c * N + NS * q, nn, v4, f);
-        sd[k] = 0.0f;
+        A2[k][0] = A2[k][1] = 0;
+        if (c < w.clim) load_pairs<NS>(a.A + c * N + NS * q, nn, v4, A2[k]);
+        sum[k] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            A2[k][i] = f[i] * kLog2e;
-            p[k][i] = 1.0f;
-            acc[k][i] = 0.0f;
+        for (int i = 0; i < H; ++i) {
+            A2[k][i] = mul2(A2[k][i], pack(kLog2e, kLog2e));
+            p[k][i] = pack(1.0f, 1.0f);
+            acc[k][i] = 0;
         }
     }
     const SeqAt sq = seq_at(a.seqs, w.b, t0);
     const bool vec = C % 8 == 0 && (C / a.G) % 8 == 0 && a.lddt % 8 == 0 && a.ldz % 8 == 0 && a.ldy % 8 == 0;
     const bool vecb = N % 8 == 0 && a.ldc % 8 == 0;
-    const int pc = tid % NV * 8, pt = tid / NV;
-    const int64_t pch = w.c0 + pc;
+    const int pv = tid % NV, pt = tid / NV;
+    const int64_t pch = w.c0 + pv * 8;
     const int pn = (int)max64(0, min64(8, w.clim - pch));
     // a segment that begins a sequence hands nothing on
     const int64_t stop = sq.begin == t0 ? t0 : min64(t1, sq.end);
@@ -431,21 +478,23 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
             if (tl >= CK) break;
             const bool live = tt + tl < stop;
             const int64_t r = row0 + tt + tl;
-            Raw<T> v;
+            Raw<T> rdt, rdy, rz;
             float fd[8], fe[8], fz[8];
-            v.load((const T*)a.dt + r * a.lddt + pch, live ? pn : 0, vec);
-            v.get(fd);
-            v.load((const T*)a.dy + r * a.ldy + pch, live ? pn : 0, vec);
-            v.get(fe);
+            rdt.load((const T*)a.dt + r * a.lddt + pch, live ? pn : 0, vec);
+            rdy.load((const T*)a.dy + r * a.ldy + pch, live ? pn : 0, vec);
             if (a.z != nullptr) {
-                v.load((const T*)a.z + r * a.ldz + pch, live ? pn : 0, vec);
-                v.get(fz);
+                rz.load((const T*)a.z + r * a.ldz + pch, live ? pn : 0, vec);
+                rz.get(fz);
             }
+            rdt.get(fd);
+            rdy.get(fe);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float x = fd[j] + (a.dt_bias != nullptr && j < pn ? a.dt_bias[pch + j] : 0.0f);
                 const float d = live ? (a.softplus ? softplus_(x) : x) : 0.0f;
-                sde[tl][pc + j] = make_float2(d, a.z != nullptr ? fe[j] * (fz[j] * sigm<FAST>(fz[j])) : fe[j]);
+                const float e = a.z != nullptr ? fe[j] * (fz[j] * sigm<FAST>(fz[j])) : fe[j];
+                sd[P::at(tl, pv * 8 + j)] = pack(d, d);
+                se[P::at(tl, pv * 8 + j)] = pack(e, e);
             }
         }
 #pragma unroll
@@ -457,23 +506,22 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
             v.load((const T*)a.Cm + (row0 + tt + tl) * a.ldc + w.grp * N + n0,
                    tt + tl < stop ? max(0, min(8, N - n0)) : 0, vecb);
             v.get(f);
-#pragma unroll
-            for (int j = 0; j < 8 && j < NP; j += 2)
-                sc[tl][j / 2 % 2][(n0 + j) / 4] = make_float2(f[j], f[j + 1]);
+            put_states<NS, LPC>(sc[tl], n0, f);
         }
         __syncthreads();
 #pragma unroll 4
         for (int tl = 0; tl < CK; ++tl) {
-            const float2 c0 = sc[tl][0][q], c1 = sc[tl][1][q];
-            const float cc[4] = {c0.x, c0.y, c1.x, c1.y};
+            const f2 c[H] = {sc[tl][q], sc[tl][LPC + q]};
 #pragma unroll
             for (int k = 0; k < CPT; ++k) {
-                const float2 d = sde[tl][lch + k * LC];
-                sd[k] += d.x;
+                const f2 d = sd[P::at(tl, lch + k * LC)], e = se[P::at(tl, lch + k * LC)];
+                float u, v;
+                unpack(d, u, v);
+                sum[k] += u;
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    p[k][i] *= ex2(d.x * A2[k][i]);
-                    acc[k][i] = fmaf(p[k][i], cc[i] * d.y, acc[k][i]);
+                for (int i = 0; i < H; ++i) {
+                    p[k][i] = mul2(p[k][i], exp2_2(mul2(d, A2[k][i])));
+                    acc[k][i] = fma2(p[k][i], mul2(c[i], e), acc[k][i]);
                 }
             }
         }
@@ -485,13 +533,13 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
         const int64_t c = w.c0 + lch + k * LC;
         if (c >= w.clim) continue;
         if (ends && a.dh_out != nullptr) {
-            float g[4];
-            load4(a.dh_out + (sq.seq * C + c) * N + NS * q, nn, v4, g);
+            f2 g[H];
+            load_pairs<NS>(a.dh_out + (sq.seq * C + c) * N + NS * q, nn, v4, g);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) acc[k][i] = fmaf(p[k][i], g[i], acc[k][i]);
+            for (int i = 0; i < H; ++i) acc[k][i] = fma2(p[k][i], g[i], acc[k][i]);
         }
-        store4(rec_g + (rec + c) * N + NS * q, nn, v4, acc[k]);
-        if (q == 0) rec_d[rec + c] = stop < t1 || ends ? __int_as_float(0x7fc00000) : sd[k];
+        store_pairs<NS>(rec_g + (rec + c) * N + NS * q, nn, v4, acc[k]);
+        if (q == 0) rec_d[rec + c] = stop < t1 || ends ? __int_as_float(0x7fc00000) : sum[k];
     }
 }
 
@@ -539,7 +587,7 @@ cudaError_t with_lanes(int l, F&& f) {
 }
 
 Cut bwd_cut(const ScanArgs& a) {
-    const int lanes = lanes_for(a.N), ch = NT / lanes * (lanes >= 4 ? 2 : 1);
+    const int lanes = padded_states(a.N) / NS, ch = NT / lanes * (lanes > 1 ? 2 : 1);
     Cut k;
     k.cbg = (a.C / a.G + ch - 1) / ch;
     k.cblocks = k.cbg * a.G;
@@ -583,7 +631,7 @@ cudaError_t scan_bwd(const ScanArgs& a, cudaStream_t s) {
     int64_t parts = 0;
     if (a.seqs.L > 0) {
         parts = a.B * k.segs;
-        e = with_lanes(lanes_for(a.N), [&](auto ll) {
+        e = with_lanes(padded_states(a.N) / NS, [&](auto ll) {
             constexpr int LPC = decltype(ll)::value;
             const unsigned g = (unsigned)(parts * k.cblocks);
             if (k.segs > 1) {

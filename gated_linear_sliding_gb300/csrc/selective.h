@@ -128,6 +128,13 @@ struct Vec<1> {
     static __device__ __forceinline__ void st(T* p, const float* f) { lz::st(p, f[0]); }
 };
 
+// Vec<V>'s elements as they lie in memory.
+template <typename T, int V>
+struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+    T e[V];
+    __device__ __forceinline__ void get(float* f) const { Vec<V>::ld(e, f); }
+};
+
 // sigmoid(v), and the derivative of v sigmoid(v) given it.  The fp32 path divides, takes expf and
 // never e^|v|, which overflows where the sigmoid is still a number; the bf16 path takes the fast
 // exponential and division, whose error (a few 2^-23) is far below bf16's step.
