@@ -25,7 +25,7 @@ struct Lay {
     static constexpr int TT = 1024 / CH < 2048 / NP ? 1024 / CH : 2048 / NP;
     static constexpr int NQ = (NP + 7) / 8;        // 8-state pieces of a row of Bm
     static constexpr int PB = (TT * NQ + NT - 1) / NT;  // of which a thread stages so many
-    static constexpr int U = LPC > 4 ? 8 : 4;      // tokens whose outputs are summed together
+    static constexpr int U = 8;                    // tokens whose outputs are summed together
     using P = Plane<TT, CH, LC>;
 };
 
@@ -35,12 +35,13 @@ struct Smem {
     f2 d[L::P::SIZE], dx[L::P::SIZE];        // (d, d), (d x, d x)
     f2 b[L::TT][NS / 2 * LPC], c[L::TT][NS / 2 * LPC];
     float y[L::P::SIZE];
+    __align__(8) float bias[L::CH], skip[L::CH];  // dt_bias and D of the channels
 };
 
 // MAIN: the outputs (and states).  Otherwise only a segment's own end state from a zero start and
 // the sum of its step sizes, for the join.
 template <typename T, int LPC, int NS, bool MAIN>
-__global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cut cut,
+__global__ void __launch_bounds__(NT, 4) scan_fwd_kernel(const ScanArgs a, const Cut cut,
                                                       float* rec_h, float* rec_d,
                                                       const float* h0) {
     using L = Lay<LPC, NS>;
@@ -92,12 +93,12 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
     const bool stages = pt < TT;
     const int64_t pch = w.c0 + pv * 8;
     const int pn = stages ? (int)max64(0, min64(8, w.clim - pch)) : 0;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        bias[j] = a.dt_bias != nullptr && j < pn ? a.dt_bias[pch + j] : 0.0f;
-        skip[j] = MAIN && a.D != nullptr && j < pn ? a.D[pch + j] : 0.0f;
+    for (int k = tid; k < CH; k += NT) {
+        const bool in = w.c0 + k < w.clim;
+        sm.bias[k] = in && a.dt_bias != nullptr ? a.dt_bias[w.c0 + k] : 0.0f;
+        sm.skip[k] = MAIN && in && a.D != nullptr ? a.D[w.c0 + k] : 0.0f;
     }
+    __syncthreads();
     const T *px = (const T*)a.x + (row0 + t0 + pt) * a.ldx + pch;
     const T *pdt = (const T*)a.dt + (row0 + t0 + pt) * a.lddt + pch;
     const T *pz = (const T*)a.z + (row0 + t0 + pt) * a.ldz + pch;
@@ -137,14 +138,15 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
     Raw<T> kx, kz;  // the current tile's x and z, for its outputs
     auto commit = [&]() {
         if (stages) {
-            float fx[8], fd[8];
+            f2 fx[4], fd[4];
             rx.get(fx);
             rdt.get(fd);
+            const f2* bias = reinterpret_cast<const f2*>(&sm.bias[pv * 8]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = fd[j] + bias[j], d = a.softplus ? softplus_(v) : v, dx = d * fx[j];
-                sm.d[P::at(pt, pv * 8 + j)] = pack(d, d);
-                sm.dx[P::at(pt, pv * 8 + j)] = pack(dx, dx);
+            for (int j = 0; j < 4; ++j) {
+                const f2 v = add2(fd[j], bias[j]), d = a.softplus ? softplus2(v) : v;
+                put_doubled<P>(sm.d, pt, pv * 8 + 2 * j, d);
+                put_doubled<P>(sm.dx, pt, pv * 8 + 2 * j, mul2(d, fx[j]));
             }
         }
         if (MAIN) {
@@ -167,12 +169,16 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
     // one token: the recurrence, and this lane's part of the output
     auto step = [&](int tl) {
         const f2 d = sm.d[P::at(tl, lch)], dx = sm.dx[P::at(tl, lch)];
-        f2 part = 0;
+        f2 part = 0, half = 0;  // two chains of sums
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            h[i] = fma2(exp2_2(mul2(d, A2[i])), h[i], mul2(dx, sm.b[tl][i * LPC + q]));
-            if (MAIN) part = i == 0 ? mul2(h[i], sm.c[tl][q]) : fma2(h[i], sm.c[tl][i * LPC + q], part);
+            h[i] = fma2(decay2(d, A2[i]), h[i], mul2(dx, sm.b[tl][i * LPC + q]));
+            if (MAIN) {
+                f2& p = i < (H + 1) / 2 ? part : half;
+                p = i == 0 || i == (H + 1) / 2 ? mul2(h[i], sm.c[tl][i * LPC + q]) : fma2(h[i], sm.c[tl][i * LPC + q], p);
+            }
         }
+        if (H > 1) part = add2(part, half);
         if (!MAIN) {
             float u, v;
             unpack(d, u, v);
@@ -190,36 +196,50 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
         }
     };
 
-    fetch((int)min64(TT, t1 - t0));
-    for (int64_t tt = t0; tt < t1; tt += TT) {
+    // tokens left in the segment and in the sequence (a row has less than 2^31)
+    int left = (int)(t1 - t0), inside = (int)(sq.end - t0);
+    // where the states before each 16 tokens go
+    float* keep = MAIN && a.states != nullptr
+                      ? a.states + (w.b * ((a.seqs.L + CK - 1) / CK) + t0 / CK) * C * N + off : nullptr;
+    int until = 0;  // tokens until the next of them
+    auto keep_state = [&]() {
+        if (!MAIN || keep == nullptr) return;
+        if (until == 0) {
+            if (own) store_pairs<NS>(keep, nn, vn, h);
+            keep += C * N;
+            until = CK;
+        }
+        until -= U;
+    };
+    fetch(left);
+    for (; left > 0; left -= TT, inside -= TT) {
         commit();
         __syncthreads();
-        if (tt + TT < t1) fetch((int)min64(TT, t1 - tt - TT));
-        const int n = (int)min64(TT, t1 - tt), inside = (int)min64(TT, sq.end - tt);
-        // where the states of the tile's 16-token chunks go
-        float* keep = MAIN && a.states != nullptr ? a.states + (w.b * ((a.seqs.L + CK - 1) / CK) + tt / CK) * C * N : nullptr;
-        const int lead = TT % CK == 0 ? 0 : (int)(tt % CK);
-        if (n == TT && inside == TT) {
+        if (left > TT) fetch(left - TT);
+        if (left >= TT && inside >= TT) {
 #pragma unroll 1
             for (int tl = 0; tl < TT; tl += U) {
-                if (MAIN && keep != nullptr && (lead + tl) % CK == 0) put_state(keep + tl / CK * C * N);
+                keep_state();
                 float part[U];
 #pragma unroll
                 for (int i = 0; i < U; ++i) part[i] = step(tl + i);
                 outputs(part, tl);
             }
         } else {
+            const int n = min(TT, left);
 #pragma unroll 1
             for (int tl = 0; tl < n; tl += U) {
-                if (MAIN && keep != nullptr && (lead + tl) % CK == 0) put_state(keep + tl / CK * C * N);
+                keep_state();
                 float part[U];
 #pragma unroll
                 for (int i = 0; i < U; ++i) part[i] = 0.0f;
 #pragma unroll 1
                 for (int i = 0; i < U && tl + i < n; ++i) {
-                    if (tt + tl + i == sq.end) {
+                    if (tl + i == inside) {
                         if (MAIN && a.h_out != nullptr) put_state(a.h_out + sq.seq * C * N);
-                        sq = seq_at(a.seqs, w.b, tt + tl + i);
+                        const int64_t at = sq.end;
+                        sq = seq_at(a.seqs, w.b, at);
+                        inside += (int)(sq.end - at);
                         begin_state(sq.seq);
                         cutoff = true;
                     }
@@ -233,17 +253,21 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(const ScanArgs a, const Cu
         }
         __syncthreads();
         if (MAIN && stages) {
-            float fx[8], o[8];
+            f2 fx[4], o[4];
             kx.get(fx);
+            const f2* skip = reinterpret_cast<const f2*>(&sm.skip[pv * 8]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = fmaf(skip[j], fx[j], sm.y[P::at(pt, pv * 8 + j)]);
+            for (int j = 0; j < 4; ++j) {
+                const int k = pv * 8 + 2 * j;
+                o[j] = fma2(skip[j], fx[j], pack(sm.y[P::at(pt, k)], sm.y[P::at(pt, k + 1)]));
+            }
             if (a.z != nullptr) {
-                float fz[8];
+                f2 fz[4];
                 kz.get(fz);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] *= fz[j] * sigm<is_fast<T>()>(fz[j]);
+                for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], mul2(fz[j], sigm2<is_fast<T>()>(fz[j])));
             }
-            store8(py, o, pt < n ? pn : 0, vec);
+            store8(py, o, pt < left ? pn : 0, vec);
             py += TT * a.ldy;
         }
     }
@@ -264,15 +288,23 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanArgs a, int64_
     const int64_t b = id / CN, cn = id % CN, c = cn / a.N;
     const float A2 = a.A[cn] * kLog2e;
     float h = 0.0f;
-    for (int64_t s = 0; s < segs; ++s) {
-        float* p = rec_h + (b * segs + s) * CN + cn;
-        float own = 0.0f, d = 0.0f;
-        if (s + 1 < segs) {  // the last segment's own end state is not needed
-            own = *p;
-            d = rec_d[(b * segs + s) * a.C + c];
+    float* p = rec_h + b * segs * CN + cn;
+    const float* pd = rec_d + b * segs * a.C + c;
+    constexpr int U = 8;  // records read together: each is a trip to memory
+    for (int64_t s = 0; s < segs; s += U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = s + u + 1 < segs;  // the last segment's own end state is not needed
+            own[u] = in ? p[(s + u) * CN] : 0.0f;
+            d[u] = in ? pd[(s + u) * a.C] : 0.0f;
         }
-        *p = h;
-        h = isnan(d) ? own : fmaf(ex2(d * A2), h, own);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u >= segs) break;
+            p[(s + u) * CN] = h;
+            h = isnan(d[u]) ? own[u] : fmaf(ex2(d[u] * A2), h, own[u]);
+        }
     }
 }
 
@@ -348,43 +380,36 @@ cudaError_t with_lanes(int l, F&& f) {
     else return l == LPC ? f(std::integral_constant<int, LPC>()) : with_lanes<LPC * 2>(l, f);
 }
 
-// States a lane holds.  Eight keep a channel on few lanes, whose sums cost the least, and need
-// many channels to fill the GPU; with few channels fewer states a lane make more warps.
-int fwd_states(const ScanArgs& a) {
-    const int np = padded_states(a.N);
-    if (np < 16) return 4;
-    const int64_t warps = a.B * a.C * np / (8 * 32);
-    if (warps >= 1500) return 8;
-    if (np == 16 && warps >= 200 && warps < 400) return 2;
-    return 4;
-}
-
-// Calls f with the lanes a channel and the states a lane, as constants.
+// Calls f with the lanes a channel and the states a lane, as constants.  Eight states a lane keep
+// the sums over a channel's lanes cheapest (8 x 2048 x 4096 x 16: 451 us, with four a lane 490).
 template <typename F>
 cudaError_t with_lay(const ScanArgs& a, F&& f) {
-    const int np = padded_states(a.N), ns = fwd_states(a);
-    auto go = [&](auto l, auto n) { return f(l, n); };
     using std::integral_constant;
-    if (ns == 2) return go(integral_constant<int, 8>(), integral_constant<int, 2>());
-    if (ns == 4)
-        return with_lanes(np / 4, [&](auto l) { return go(l, integral_constant<int, 4>()); });
-    if (np == 16) return go(integral_constant<int, 2>(), integral_constant<int, 8>());
-    if (np == 32) return go(integral_constant<int, 4>(), integral_constant<int, 8>());
-    return go(integral_constant<int, 8>(), integral_constant<int, 8>());
+    const int np = padded_states(a.N);
+    if (np == 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>());
+    if (np == 8) return f(integral_constant<int, 2>(), integral_constant<int, 4>());
+    return with_lanes(np / 8, [&](auto l) { return f(l, integral_constant<int, 8>()); });
+}
+int channels_of(const ScanArgs& a) {
+    const int np = padded_states(a.N);
+    return NT * (np >= 16 ? 8 : 4) / np;
 }
 
-// The forward's cut.  One pass over the whole time axis costs the least; where that leaves too
-// few warps, the axis is cut into segments, whose end states take a pass of their own.
+// The forward's cut.  One pass over the whole time axis computes the least; where that leaves
+// about a CTA for each of 152 SMs or fewer, the axis is cut into segments for two rounds of the
+// four CTAs a SM holds, although their end states then take a pass of their own, half as long as
+// the outputs' (8192 x 4096 x 16: 64 CTAs 1000 us, cut into 16 x 64 335 us; 65536 x 1024 x 16:
+// 16 CTAs cut into 32 x 16 793 us, 64 x 16 686 us, 128 x 16 717 us).
 Cut fwd_cut(const ScanArgs& a) {
-    const int ch = NT * fwd_states(a) / padded_states(a.N);
+    const int ch = channels_of(a);
     Cut k;
     k.cbg = (a.C / a.G + ch - 1) / ch;
     k.cblocks = k.cbg * a.G;
     k.segs = 1;
     k.seg_len = a.seqs.L;
     const int64_t ctas = a.B * k.cblocks;
-    if (ctas >= 96 || a.seqs.L <= 4 * SEG) return k;
-    int64_t want = (4 * 152 + ctas - 1) / ctas;
+    if (ctas > 180 || a.seqs.L <= 4 * SEG) return k;
+    const int64_t want = (8 * 152 + ctas - 1) / ctas;
     k.seg_len = ((a.seqs.L + want - 1) / want + SEG - 1) / SEG * SEG;
     k.segs = (a.seqs.L + k.seg_len - 1) / k.seg_len;
     return k;

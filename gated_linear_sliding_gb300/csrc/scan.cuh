@@ -50,13 +50,24 @@ __device__ __forceinline__ f2 exp2_2(f2 v) {
     unpack(v, a, b);
     return pack(ex2(a), ex2(b));
 }
+// The decays exp(d A) of two states, A2 = A log2(e).  ex2.approx errs downwards: by 2e-8 of the
+// result on average over exponents from -1 to -0.01, 1.7e-8 to -0.001, 0.6e-8 above (2^24
+// arguments each).  A state that remembers a thousand tokens multiplies a thousand of them, so the
+// exponent is moved up by as much, on the product's own instruction: the error of dA against 64
+// bits falls from 1.9e-6 to 0.9e-6 on 8 x 2048 tokens, of the last states from 4.5e-7 to 2.5e-7
+// on 8192.
+__device__ __forceinline__ f2 decay2(f2 d, f2 A2) { return exp2_2(fma2(d, A2, pack(2e-8f, 2e-8f))); }
 __device__ __forceinline__ float sum2(f2 v) {
     float a, b;
     unpack(v, a, b);
     return a + b;
 }
 
-// rcp.approx of a value in [1, 2^126): within one ulp
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// 1 / x of a value from 1 on, within one ulp (0 from 2^126 on)
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -65,18 +76,40 @@ __device__ __forceinline__ float rcp(float x) {
 
 // log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| <= 1, and log1p(u) = 2 atanh(s) with
 // s = u / (2 + u) <= 1/3: the odd series to s^13 leaves 2 (1/3)^15 / 15, below 2^-26 of the
-// result.  (A logarithm of 1 + u would lose the digits of a small step size.)
-__device__ __forceinline__ float softplus_(float x) {
-    const float u = ex2(-kLog2e * fabsf(x));
-    const float s = u * rcp(2.0f + u), s2 = s * s;
-    float p = 1.0f / 13.0f;
-    p = fmaf(p, s2, 1.0f / 11.0f);
-    p = fmaf(p, s2, 1.0f / 9.0f);
-    p = fmaf(p, s2, 1.0f / 7.0f);
-    p = fmaf(p, s2, 1.0f / 5.0f);
-    p = fmaf(p, s2, 1.0f / 3.0f);
-    p = fmaf(p, s2, 1.0f);
-    return fmaf(2.0f * s, p, fmaxf(x, 0.0f));
+// result.  (A logarithm of 1 + u would lose the digits of a small step size.)  Two at a time.
+__device__ __forceinline__ f2 softplus2(f2 v) {
+    float x, y;
+    unpack(v, x, y);
+    const f2 u = pack(ex2(-kLog2e * fabsf(x)), ex2(-kLog2e * fabsf(y)));
+    float m, n;
+    unpack(add2(u, pack(2.0f, 2.0f)), m, n);
+    const f2 s = mul2(u, pack(rcp(m), rcp(n))), s2 = mul2(s, s);
+    const float c[7] = {2.0f / 13.0f, 2.0f / 11.0f, 2.0f / 9.0f, 2.0f / 7.0f, 2.0f / 5.0f, 2.0f / 3.0f, 2.0f};
+    f2 p = pack(c[0], c[0]);
+#pragma unroll
+    for (int i = 1; i < 7; ++i) p = fma2(p, s2, pack(c[i], c[i]));
+    return fma2(s, p, pack(fmaxf(x, 0.0f), fmaxf(y, 0.0f)));
+}
+
+__device__ __forceinline__ float softplus_(float v) {
+    float x, y;
+    unpack(softplus2(pack(v, 0.0f)), x, y);
+    return x;
+}
+
+// sigmoid of two values.  As sigm: the fast form where bf16's step hides its error of a few
+// 2^-23, the exact one for fp32.
+template <bool FAST>
+__device__ __forceinline__ f2 sigm2(f2 v) {
+    float x, y;
+    if constexpr (FAST) {
+        unpack(mul2(v, pack(-kLog2e, -kLog2e)), x, y);
+        unpack(add2(pack(ex2(x), ex2(y)), pack(1.0f, 1.0f)), x, y);
+        return pack(rcp(x), rcp(y));
+    } else {
+        unpack(v, x, y);
+        return pack(sigm<false>(x), sigm<false>(y));
+    }
 }
 
 // Eight storage elements in registers.
@@ -84,6 +117,12 @@ template <typename T>
 struct Raw {
     uint4 v[sizeof(T) / 2];
     __device__ __forceinline__ void get(float* f) const { Vec<8>::ld(reinterpret_cast<const T*>(v), f); }
+    __device__ __forceinline__ void get(f2* f) const {
+        float v[8];
+        get(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pack(v[2 * i], v[2 * i + 1]);
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = make_uint4(0, 0, 0, 0);
@@ -122,7 +161,10 @@ struct Raw {
 };
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* f, int n, bool vec) {
+__device__ __forceinline__ void store8(T* p, const f2* v, int n, bool vec) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack(v[i], f[2 * i], f[2 * i + 1]);
     if (vec) {
         if (n > 0) Vec<8>::st(p, f);
         return;
@@ -210,6 +252,16 @@ struct Plane {
     static constexpr int NV = CH / 8, PAD = LC >= 8 ? LC / 8 : 1, STEP = TT * NV + PAD, SIZE = 8 * STEP;
     static __device__ __forceinline__ int at(int t, int c) { return (c & 7) * STEP + t * NV + (c >> 3); }
 };
+
+// Puts two neighbouring channels' values (channels 2 j and 2 j + 1 of a piece) into a plane of
+// pairs, each doubled, as the recurrence's paired instructions want them.
+template <typename P>
+__device__ __forceinline__ void put_doubled(f2* plane, int t, int c, f2 v) {
+    float x, y;
+    unpack(v, x, y);
+    plane[P::at(t, c)] = pack(x, x);
+    plane[P::at(t, c + 1)] = pack(y, y);
+}
 
 // Sums over the lanes `o`, 2 o, ... < END of U values at once: each stage hands half of the
 // values to the other lane.  Leaves CNT values in v[0 .. CNT), those from index `at` on, the same

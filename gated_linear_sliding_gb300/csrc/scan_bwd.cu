@@ -55,13 +55,13 @@ struct Smem {
     f2 d[L::P::SIZE], dx[L::P::SIZE], e[L::P::SIZE];
     f2 b[CK][H * LPC], c[CK][H * LPC];
     float bc[NT / 32][CK][2][L::NP];         // a warp's sums over channels
-    float bias[L::CH], skip[L::CH];          // dt_bias and D of the channels
+    __align__(8) float bias[L::CH], skip[L::CH];  // dt_bias and D of the channels
     f2 start[QN][L::CPT * H][NT];            // a thread's states before each four tokens
     f2 dA[L::CPT * H][NT];                   // a thread's dA: a chunk's terms are added up first
 };
 
 template <typename T, int LPC>
-__global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const ScanArgs a, const Cut cut,
+__global__ void __launch_bounds__(NT, LPC > 2 ? 4 : 2) scan_bwd_kernel(const ScanArgs a, const Cut cut,
                                                       const float* rec_g, float* pbc, float* pA,
                                                       float* pD, float* pbias) {
     using L = Lay<LPC>;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const Sc
         for (int k = 0; k < CPT; ++k) {
             const f2 d = sm.d[pl[k] + tl * NV], dx = sm.dx[pl[k] + tl * NV];
 #pragma unroll
-            for (int i = 0; i < H; ++i) h[k][i] = fma2(exp2_2(mul2(d, A2[k][i])), h[k][i], mul2(dx, b[i]));
+            for (int i = 0; i < H; ++i) h[k][i] = fma2(decay2(d, A2[k][i]), h[k][i], mul2(dx, b[i]));
         }
     };
 
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const Sc
             const SeqAt s = seq_at(a.seqs, w.b, tt + tl);
             if (s.begin == tt + tl) load_state(seq_state(a.h0, s.seq), h);
         };
-        // the last token's step is not needed; a segment's short last chunk stops at its end
+        // a segment's short last chunk stops at its end
         const int quarters = (int)((min64(tt + CK, t1) - tt + QT - 1) / QT);
 #pragma unroll 1
         for (int j = 0; j < quarters; ++j) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const Sc
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         const f2 g = fma2(c[i], e, gn[k][i]), hh = hist[u + 1][k][i];
-                        const f2 ag = mul2(exp2_2(mul2(d, A2[k][i])), g), qq = mul2(ag, hp[k][i]);
+                        const f2 ag = mul2(decay2(d, A2[k][i]), g), qq = mul2(ag, hp[k][i]);
                         gn[k][i] = ag;
                         dA[k][i] = fma2(qq, d, dA[k][i]);
                         sqa = i == 0 ? mul2(qq, A2[k][i]) : fma2(qq, A2[k][i], sqa);
@@ -278,6 +278,22 @@ __global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const Sc
 
 #pragma unroll 1
     for (int64_t tt = t0 + (t1 - 1 - t0) / CK * CK; tt >= t0; tt -= CK) {
+        // the chunk before is fetched into L2 meanwhile: registers for it are not to be had
+        if (tt > t0 && vec && pn > 0) {
+#pragma unroll
+            for (int i = 0; i < PX; ++i) {
+                const int tl = pt + i * DT - CK;
+                if (tl >= 0) break;
+                const int64_t r = row0 + tt + tl;
+                prefetch_l2((const T*)a.x + r * a.ldx + pch);
+                prefetch_l2((const T*)a.dt + r * a.lddt + pch);
+                prefetch_l2((const T*)a.dy + r * a.ldy + pch);
+                if (a.z != nullptr) prefetch_l2((const T*)a.z + r * a.ldz + pch);
+            }
+            // and the state before it, a 128-byte line each
+            if (tid < CH * N / 32 && w.c0 * N + tid * 32 < w.clim * N)
+                prefetch_l2(a.states + (w.b * nck + tt / CK - 1) * C * N + w.c0 * N + tid * 32);
+        }
         __syncthreads();  // the last chunk's tiles have been read
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
@@ -291,21 +307,21 @@ __global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const Sc
             rdt.load((const T*)a.dt + r * a.lddt + pch, n, vec);
             rdy.load((const T*)a.dy + r * a.ldy + pch, n, vec);
             if (a.z != nullptr) rz.load((const T*)a.z + r * a.ldz + pch, n, vec);
-            float fx[8], fd[8], fe[8], fz[8];
+            f2 fx[4], fd[4], fe[4], fz[4];
             rx.get(fx);
             rdt.get(fd);
             rdy.get(fe);
             if (a.z != nullptr) rz.get(fz);
+            const f2* bias = reinterpret_cast<const f2*>(&sm.bias[pv * 8]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int o = P::at(tl, pv * 8 + j);
-                const float v = fd[j] + sm.bias[pv * 8 + j];
+            for (int j = 0; j < 4; ++j) {
+                const f2 v = add2(fd[j], bias[j]);
                 // a place past the segment's end must leave the state and its gradient as they are
-                const float d = live ? (a.softplus ? softplus_(v) : v) : 0.0f, dx = d * fx[j];
-                const float e = a.z != nullptr ? fe[j] * (fz[j] * sigm<FAST>(fz[j])) : fe[j];
-                sm.d[o] = pack(d, d);
-                sm.dx[o] = pack(dx, dx);
-                sm.e[o] = pack(e, e);
+                const f2 d = live ? (a.softplus ? softplus2(v) : v) : 0;
+                if (a.z != nullptr) fe[j] = mul2(fe[j], mul2(fz[j], sigm2<FAST>(fz[j])));
+                put_doubled<P>(sm.d, tl, pv * 8 + 2 * j, d);
+                put_doubled<P>(sm.dx, tl, pv * 8 + 2 * j, mul2(d, fx[j]));
+                put_doubled<P>(sm.e, tl, pv * 8 + 2 * j, fe[j]);
             }
         }
 #pragma unroll
@@ -360,33 +376,43 @@ __global__ void __launch_bounds__(NT, LPC == 1 ? 2 : 3) scan_bwd_kernel(const Sc
             rdt.load((const T*)a.dt + r * a.lddt + pch, n, vec);
             rdy.load((const T*)a.dy + r * a.ldy + pch, n, vec);
             if (a.z != nullptr) rz.load((const T*)a.z + r * a.ldz + pch, n, vec);
-            float fx[8], fd[8], fy[8], fz[8], ox[8], ot[8], oz[8];
+            f2 fx[4], fd[4], fy[4], fz[4], ox[4], ot[4], oz[4];
             rx.get(fx);
             rdt.get(fd);
             rdy.get(fy);
             if (a.z != nullptr) rz.get(fz);
+            const f2* bias = reinterpret_cast<const f2*>(&sm.bias[pv * 8]);
+            const f2* skip = reinterpret_cast<const f2*>(&sm.skip[pv * 8]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = P::at(tl, pv * 8 + j);
-                const float D = sm.skip[pv * 8 + j];
-                float d, gb, qa, e = fy[j], ch, x;
-                unpack(sm.d[at], d, x);
-                unpack(sm.dx[at], gb, qa);
-                unpack(sm.e[at], ch, x);
+            for (int j = 0; j < 4; ++j) {
+                const int o0 = P::at(tl, pv * 8 + 2 * j), o1 = P::at(tl, pv * 8 + 2 * j + 1);
+                float d0, d1, g0, g1, q0, q1, x;
+                unpack(sm.d[o0], d0, x);
+                unpack(sm.d[o1], d1, x);
+                unpack(sm.dx[o0], g0, q0);
+                unpack(sm.dx[o1], g1, q1);
+                const f2 d = pack(d0, d1), gb = pack(g0, g1), D = skip[j];
+                f2 e = fy[j];
                 if (a.z != nullptr) {
-                    const float sg = sigm<FAST>(fz[j]);
-                    e *= fz[j] * sg;
-                    oz[j] = fy[j] * fmaf(D, fx[j], ch) * dsilu(fz[j], sg);
+                    const f2 sg = sigm2<FAST>(fz[j]);
+                    float c0, c1;
+                    unpack(sm.e[o0], c0, x);
+                    unpack(sm.e[o1], c1, x);
+                    // silu' = sg + z sg (1 - sg)
+                    const f2 zs = mul2(fz[j], sg), ds = fma2(zs, fma2(sg, pack(-1.0f, -1.0f), pack(1.0f, 1.0f)), sg);
+                    oz[j] = mul2(mul2(fy[j], fma2(D, fx[j], pack(c0, c1))), ds);
+                    e = mul2(e, zs);
                 }
-                ox[j] = fmaf(d, gb, D * e);
+                ox[j] = fma2(d, gb, mul2(D, e));
                 // qa was summed with A log2(e)
-                float dd = fmaf(fx[j], gb, qa * 0.69314718055994531f);
-                if (a.softplus) dd *= sigm<FAST>(fd[j] + sm.bias[pv * 8 + j]);
+                f2 dd = fma2(fx[j], gb, mul2(pack(q0, q1), pack(0.69314718055994531f, 0.69314718055994531f)));
+                if (a.softplus) dd = mul2(dd, sigm2<FAST>(add2(fd[j], bias[j])));
                 ot[j] = dd;
-                if (j < n) {
-                    terms[j] = fmaf(e, fx[j], terms[j]);
-                    terms[8 + j] += dd;
-                }
+                float e0, e1;
+                unpack(mul2(e, fx[j]), e0, e1);
+                unpack(dd, d0, d1);
+                if (2 * j < n) terms[2 * j] += e0, terms[8 + 2 * j] += d0;
+                if (2 * j + 1 < n) terms[2 * j + 1] += e1, terms[9 + 2 * j] += d1;
             }
             store8((T*)a.dx + r * a.lddx + pch, ox, n, vec);
             store8((T*)a.ddt + r * a.ldddt + pch, ot, n, vec);
@@ -479,7 +505,7 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
             const bool live = tt + tl < stop;
             const int64_t r = row0 + tt + tl;
             Raw<T> rdt, rdy, rz;
-            float fd[8], fe[8], fz[8];
+            f2 fd[4], fe[4], fz[4];
             rdt.load((const T*)a.dt + r * a.lddt + pch, live ? pn : 0, vec);
             rdy.load((const T*)a.dy + r * a.ldy + pch, live ? pn : 0, vec);
             if (a.z != nullptr) {
@@ -489,12 +515,16 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
             rdt.get(fd);
             rdy.get(fe);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = fd[j] + (a.dt_bias != nullptr && j < pn ? a.dt_bias[pch + j] : 0.0f);
-                const float d = live ? (a.softplus ? softplus_(x) : x) : 0.0f;
-                const float e = a.z != nullptr ? fe[j] * (fz[j] * sigm<FAST>(fz[j])) : fe[j];
-                sd[P::at(tl, pv * 8 + j)] = pack(d, d);
-                se[P::at(tl, pv * 8 + j)] = pack(e, e);
+            for (int j = 0; j < 4; ++j) {
+                float b0 = 0.0f, b1 = 0.0f;
+                if (a.dt_bias != nullptr) {
+                    if (2 * j < pn) b0 = a.dt_bias[pch + 2 * j];
+                    if (2 * j + 1 < pn) b1 = a.dt_bias[pch + 2 * j + 1];
+                }
+                const f2 v = add2(fd[j], pack(b0, b1));
+                if (a.z != nullptr) fe[j] = mul2(fe[j], mul2(fz[j], sigm2<FAST>(fz[j])));
+                put_doubled<P>(sd, tl, pv * 8 + 2 * j, live ? (a.softplus ? softplus2(v) : v) : 0);
+                put_doubled<P>(se, tl, pv * 8 + 2 * j, fe[j]);
             }
         }
 #pragma unroll
@@ -520,7 +550,7 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
                 sum[k] += u;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    p[k][i] = mul2(p[k][i], exp2_2(mul2(d, A2[k][i])));
+                    p[k][i] = mul2(p[k][i], decay2(d, A2[k][i]));
                     acc[k][i] = fma2(p[k][i], mul2(c[i], e), acc[k][i]);
                 }
             }
@@ -551,11 +581,22 @@ __global__ void __launch_bounds__(256) scan_adj_join_kernel(const ScanArgs a, in
     const int64_t b = id / CN, cn = id % CN, c = cn / a.N;
     const float A2 = a.A[cn] * kLog2e;
     float g = 0.0f;
-    for (int64_t s = segs - 1; s >= 0; --s) {
-        float* p = rec_g + (b * segs + s) * CN + cn;
-        const float own = *p, d = rec_d[(b * segs + s) * a.C + c];
-        *p = g;
-        g = isnan(d) ? own : fmaf(ex2(d * A2), g, own);
+    float* p = rec_g + b * segs * CN + cn;
+    const float* pd = rec_d + b * segs * a.C + c;
+    constexpr int U = 8;  // records read together
+    for (int64_t s = segs - 1; s >= 0; s -= U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            own[u] = s >= u ? p[(s - u) * CN] : 0.0f;
+            d[u] = s >= u ? pd[(s - u) * a.C] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s < u) break;
+            p[(s - u) * CN] = g;
+            g = isnan(d[u]) ? own[u] : fmaf(ex2(d[u] * A2), g, own[u]);
+        }
     }
 }
 
@@ -586,6 +627,8 @@ cudaError_t with_lanes(int l, F&& f) {
     else return l == LPC ? f(std::integral_constant<int, LPC>()) : with_lanes<LPC * 2>(l, f);
 }
 
+// As the forward's cut: segments where there are fewer than two CTAs a SM.  The pass over the
+// segments' gradients costs about a fifth of the walk.
 Cut bwd_cut(const ScanArgs& a) {
     const int lanes = padded_states(a.N) / NS, ch = NT / lanes * (lanes > 1 ? 2 : 1);
     Cut k;
@@ -594,8 +637,8 @@ Cut bwd_cut(const ScanArgs& a) {
     k.segs = 1;
     k.seg_len = a.seqs.L;
     const int64_t ctas = a.B * k.cblocks;
-    if (ctas >= 304 || a.seqs.L <= SEG) return k;
-    const int64_t want = (3 * 152 + ctas - 1) / ctas;
+    if (ctas > 304 || a.seqs.L <= SEG) return k;
+    const int64_t want = (4 * 152 + ctas - 1) / ctas;
     k.seg_len = ((a.seqs.L + want - 1) / want + SEG - 1) / SEG * SEG;
     k.segs = (a.seqs.L + k.seg_len - 1) / k.seg_len;
     return k;

@@ -41,6 +41,7 @@ bool header_of(void* ws, size_t bytes, WsHeader** h) {
 
 bool batch_ok(int64_t B, int64_t L, int64_t C, int64_t nseq) {
     if (!extent(B, 1) || !extent(L, 0) || !extent(C, 1) || nseq < 0 || nseq > kMaxExtent) return false;
+    if (L > 0x7fff0000) return false;  // the kernels count a row's tokens in 32 bits
     if (nseq > 0 && B != 1) return false;
     return (double)B * (double)(L > 0 ? L : 1) * (double)C < 9e15;
 }

@@ -593,41 +593,52 @@ def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=No
 # checked and copied.
 
 
-def _ld(t, name, shape, dtype):
-    """Distance between the token rows of t (0 when dense); t has `shape`, whose leading axes
-    (one for [B, width], else two) count tokens."""
-    if tuple(t.shape) != shape:
+def _ld(t, name, shape, dtype, lead=2):
+    """Distance between the token rows of t (0 when dense); the first `lead` axes of `shape`
+    count tokens."""
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return 0
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.is_contiguous():
-        return 0
-    lead = 1 if len(shape) == 2 else 2
-    width, inner = 1, t.stride()[lead:]
-    for size, stride in zip(reversed(shape[lead:]), reversed(inner)):
+    st, width = t.stride(), 1
+    for size, stride in zip(reversed(shape[lead:]), reversed(st[lead:])):
         if size > 1 and stride != width:
             raise ValueError(f"{name}: the values of a token must be contiguous")
         width *= size
-    st = t.stride()
     if lead == 1:
-        ld = st[0]
-        ok = True
+        ld, even = st[0], True
     else:
         ld = st[1] if shape[1] > 1 else st[0]
-        ok = shape[0] == 1 or shape[1] == 1 or st[0] == shape[1] * st[1]
-    if not ok or ld < width:
+        even = shape[0] == 1 or shape[1] == 1 or st[0] == shape[1] * st[1]
+    if not even or ld < width:
         raise ValueError(f"{name}: token rows must be evenly spaced and not overlap")
     return ld
 
 
-def _need_same(t, name, shape):
+def _need_f32(t, name, shape):
     """An optional fp32 parameter or state; its address (None when absent)."""
     if t is None:
         return None
-    _need(t, name, shape, torch.float32)
+    if t.shape != shape or t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous():
+        _need(t, name, shape, torch.float32)
     return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t):
+    """Handle of `stream`, or of the current stream of t's device (without making the Stream
+    object, which costs as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _ptr(t):
@@ -662,7 +673,8 @@ def _scratch(workspace, nbytes, device):
 def _slots(slots, B):
     if slots is None:
         return None
-    _need(slots, "slots", (B,), torch.int64)
+    if slots.shape != (B,) or slots.dtype is not torch.int64 or not slots.is_cuda or not slots.is_contiguous():
+        _need(slots, "slots", (B,), torch.int64)
     return slots.data_ptr()
 
 
@@ -676,16 +688,16 @@ def lizard_conv_fwd(x, w, bias=None, *, act: int = LIZARD_ACT_NONE, state_in=Non
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
     n = nseq or B
     if y is None:
-        y = torch.empty((B, L, C), dtype=dt, device=x.device)
+        y = x.new_empty((B, L, C))
     for t, name in ((state_in, "state_in"), (state_out, "state_out")):
         if t is not None:
             _need(t, name, (n, K - 1, C), dt)
     dims = lizard_conv_dims(B, L, C, K, nseq, _ld(x, "x", (B, L, C), dt),
                             _ld(y, "y", (B, L, C), dt), 0, _dtype_code(x), act)
-    st = load().lizard_conv_fwd(ctypes.byref(dims), x.data_ptr(), _need_same(w, "w", (C, K)),
-                                _need_same(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
+    st = load().lizard_conv_fwd(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
+                                _need_f32(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
                                 y.data_ptr(), _ptr(state_out), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _stream(stream))
+                                0 if workspace is None else workspace.numel(), _stream_of(stream, x))
     _check(st, "lizard_conv_fwd")
     return y
 
@@ -704,7 +716,7 @@ def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
     n = nseq or B
     if dx is None:
-        dx = torch.empty((B, L, C), dtype=dt, device=x.device)
+        dx = x.new_empty((B, L, C))
     for t, name in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
         if t is not None:
             _need(t, name, (n, K - 1, C), dt)
@@ -714,11 +726,11 @@ def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None
                             _ld(dy, "dy", (B, L, C), dt), _ld(dx, "dx", (B, L, C), dt),
                             _dtype_code(x), act)
     workspace = _scratch(workspace, lizard_conv_bwd_workspace(dims), x.device)
-    st = load().lizard_conv_bwd(ctypes.byref(dims), x.data_ptr(), _need_same(w, "w", (C, K)),
-                                _need_same(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
+    st = load().lizard_conv_bwd(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
+                                _need_f32(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
                                 dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dw.data_ptr(),
                                 _ptr(dbias), _ptr(dstate_in), workspace.data_ptr(),
-                                workspace.numel(), _stream(stream))
+                                workspace.numel(), _stream_of(stream, x))
     _check(st, "lizard_conv_bwd")
     return dict(dx=dx, dw=dw, dbias=dbias, dstate_in=dstate_in)
 
@@ -730,15 +742,18 @@ def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NON
     or None (row b uses entry b)."""
     B, C = x.shape
     K, dt = w.shape[1], x.dtype
+    ldy = 0
     if y is None:
-        y = torch.empty((B, C), dtype=dt, device=x.device)
-    _need(state, "state", (state.shape[0], K - 1, C), dt)
-    dims = lizard_conv_dims(B, 1, C, K, 0, _ld(x, "x", (B, C), dt), _ld(y, "y", (B, C), dt), 0,
-                            _dtype_code(x), act)
-    st = load().lizard_conv_step(ctypes.byref(dims), x.data_ptr(), _need_same(w, "w", (C, K)),
-                                 _need_same(bias, "bias", (C,)), state.data_ptr(), state.shape[0],
+        y = x.new_empty((B, C))
+    else:
+        ldy = _ld(y, "y", (B, C), dt, 1)
+    if _ld(state, "state", (state.shape[0], K - 1, C), dt, 1):
+        raise ValueError("state must be a contiguous CUDA tensor")
+    dims = lizard_conv_dims(B, 1, C, K, 0, _ld(x, "x", (B, C), dt, 1), ldy, 0, _dtype_code(x), act)
+    st = load().lizard_conv_step(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
+                                 _need_f32(bias, "bias", (C,)), state.data_ptr(), state.shape[0],
                                  _slots(slots, B), y.data_ptr(), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream(stream))
+                                 0 if workspace is None else workspace.numel(), _stream_of(stream, x))
     _check(st, "lizard_conv_step")
     return y
 
@@ -746,22 +761,18 @@ def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NON
 def _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq):
     """lizard_scan_dims of the inputs, and the addresses of x, dt, A, Bm, Cm, D, z, dt_bias."""
     tp, lead = x.dtype, tuple(x.shape[:-1])
+    n = len(lead)
     C, N = A.shape
     G = Bm.shape[-2]
     wide, group = lead + (C,), lead + (G, N)
-    dims = lizard_scan_dims(B=lead[0], L=lead[1] if len(lead) == 2 else 1, C=C, N=N, G=G,
-                            nseq=nseq, ldx=_ld(x, "x", wide, tp), lddt=_ld(dt, "dt", wide, tp),
-                            ldz=0 if z is None else _ld(z, "z", wide, tp),
-                            dtype=_dtype_code(x), softplus=int(softplus))
-    if len(lead) == 1:  # [B, G, N]: seen as [B, 1, G, N], so that the groups are not tokens
-        dims.ldb = _ld(Bm.unsqueeze(1), "Bm", (lead[0], 1, G, N), tp)
-        dims.ldc = _ld(Cm.unsqueeze(1), "Cm", (lead[0], 1, G, N), tp)
-    else:
-        dims.ldb = _ld(Bm, "Bm", group, tp)
-        dims.ldc = _ld(Cm, "Cm", group, tp)
-    return dims, (x.data_ptr(), dt.data_ptr(), _need_same(A, "A", (C, N)), Bm.data_ptr(),
-                  Cm.data_ptr(), _need_same(D, "D", (C,)), _ptr(z),
-                  _need_same(dt_bias, "dt_bias", (C,)))
+    dims = lizard_scan_dims(lead[0], lead[1] if n == 2 else 1, C, N, G, nseq,
+                            _ld(x, "x", wide, tp, n), _ld(dt, "dt", wide, tp, n),
+                            0 if z is None else _ld(z, "z", wide, tp, n),
+                            _ld(Bm, "Bm", group, tp, n), _ld(Cm, "Cm", group, tp, n), 0, 0, 0, 0, 0, 0,
+                            _dtype_code(x), 1 if softplus else 0)
+    return dims, (x.data_ptr(), dt.data_ptr(), _need_f32(A, "A", (C, N)), Bm.data_ptr(),
+                  Cm.data_ptr(), _need_f32(D, "D", (C,)), _ptr(z),
+                  _need_f32(dt_bias, "dt_bias", (C,)))
 
 
 def lizard_scan_fwd_workspace(dims) -> int:
@@ -787,17 +798,18 @@ def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus:
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
     dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq)
     if y is None:
-        y = torch.empty((B, L, C), dtype=x.dtype, device=x.device)
-    dims.ldy = _ld(y, "y", (B, L, C), x.dtype)
+        y = x.new_empty((B, L, C))
+    else:
+        dims.ldy = _ld(y, "y", (B, L, C), x.dtype)
     shape = (nseq or B, C, A.shape[1])
     lib = load()
     states = None
     if save_states:
         states = torch.empty(lizard_scan_states_bytes(dims), dtype=torch.uint8, device=x.device)
     workspace = _scratch(workspace, lib.lizard_scan_fwd_workspace(ctypes.byref(dims)), x.device)
-    st = lib.lizard_scan_fwd(ctypes.byref(dims), *ptrs, _need_same(h0, "h0", shape), _ptr(cu),
-                             y.data_ptr(), _need_same(h_out, "h_out", shape), _ptr(states),
-                             workspace.data_ptr(), workspace.numel(), _stream(stream))
+    st = lib.lizard_scan_fwd(ctypes.byref(dims), *ptrs, _need_f32(h0, "h0", shape), _ptr(cu),
+                             y.data_ptr(), _need_f32(h_out, "h_out", shape), _ptr(states),
+                             workspace.data_ptr(), workspace.numel(), _stream_of(stream, x))
     _check(st, "lizard_scan_fwd")
     return (y, states) if save_states else y
 
@@ -830,12 +842,12 @@ def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=Non
     shape = (nseq or B, C, N)
     lib = load()
     workspace = _scratch(workspace, lib.lizard_scan_bwd_workspace(ctypes.byref(dims)), x.device)
-    st = lib.lizard_scan_bwd(ctypes.byref(dims), *ptrs, _need_same(h0, "h0", shape), _ptr(cu),
+    st = lib.lizard_scan_bwd(ctypes.byref(dims), *ptrs, _need_f32(h0, "h0", shape), _ptr(cu),
                              states.data_ptr(), dy.data_ptr(),
-                             _need_same(dh_out, "dh_out", shape), dx.data_ptr(), ddt.data_ptr(),
+                             _need_f32(dh_out, "dh_out", shape), dx.data_ptr(), ddt.data_ptr(),
                              _ptr(dz), dBm.data_ptr(), dCm.data_ptr(), dA.data_ptr(), _ptr(dD),
-                             _ptr(ddt_bias), _need_same(dh0, "dh0", shape), workspace.data_ptr(),
-                             workspace.numel(), _stream(stream))
+                             _ptr(ddt_bias), _need_f32(dh0, "dh0", shape), workspace.data_ptr(),
+                             workspace.numel(), _stream_of(stream, x))
     _check(st, "lizard_scan_bwd")
     return dict(dx=dx, ddt=ddt, dA=dA, dBm=dBm, dCm=dCm, dD=dD, dz=dz, ddt_bias=ddt_bias, dh0=dh0)
 
@@ -847,13 +859,14 @@ def lizard_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None,
     dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, 0)
     B, C = x.shape
     if y is None:
-        y = torch.empty((B, C), dtype=x.dtype, device=x.device)
-    dims.ldy = _ld(y, "y", (B, C), x.dtype)
+        y = x.new_empty((B, C))
+    else:
+        dims.ldy = _ld(y, "y", (B, C), x.dtype, 1)
     nslots = state.shape[0]
     st = load().lizard_scan_step(ctypes.byref(dims), *ptrs,
-                                 _need_same(state, "state", (nslots, C, dims.N)), nslots,
+                                 _need_f32(state, "state", (nslots, C, dims.N)), nslots,
                                  _slots(slots, B), y.data_ptr(), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream(stream))
+                                 0 if workspace is None else workspace.numel(), _stream_of(stream, x))
     _check(st, "lizard_scan_step")
     return y
 
@@ -862,16 +875,17 @@ def _norm_inputs(o, gate, r, w_post, scale, w_pre, res_dtype, groups, act, gate_
                  eps_pre):
     """lizard_norm_dims of the inputs, and the addresses of o, gate, r, w_post, scale, w_pre."""
     shape, tp = tuple(o.shape), o.dtype
+    if len(shape) != 2:
+        raise ValueError("o must be [T, D]")
     D = shape[1]
-    dims = lizard_norm_dims(T=shape[0], D=D, groups=groups, ldo=_ld(o, "o", shape, tp),
-                            ldg=0 if gate is None else _ld(gate, "gate", shape, tp),
-                            ldr=0 if r is None else _ld(r, "r", shape, res_dtype),
-                            eps_post=eps, eps_pre=eps if eps_pre is None else eps_pre,
-                            dtype=_dtype_code(o),
-                            res_dtype=LIZARD_F32 if res_dtype == torch.float32 else LIZARD_BF16,
-                            act=act, gate_first=int(gate_first))
-    return dims, (o.data_ptr(), _ptr(gate), _ptr(r), _need_same(w_post, "w_post", (D,)),
-                  _need_same(scale, "scale", (D,)), _need_same(w_pre, "w_pre", (D,)))
+    dims = lizard_norm_dims(shape[0], D, groups, _ld(o, "o", shape, tp, 1),
+                            0 if gate is None else _ld(gate, "gate", shape, tp, 1),
+                            0 if r is None else _ld(r, "r", shape, res_dtype, 1), 0, 0, 0, 0, 0,
+                            eps, eps if eps_pre is None else eps_pre, _dtype_code(o),
+                            LIZARD_F32 if res_dtype is torch.float32 else LIZARD_BF16, act,
+                            1 if gate_first else 0)
+    return dims, (o.data_ptr(), _ptr(gate), _ptr(r), _need_f32(w_post, "w_post", (D,)),
+                  _need_f32(scale, "scale", (D,)), _need_f32(w_pre, "w_pre", (D,)))
 
 
 def lizard_block_norm_fwd(o, *, gate=None, r=None, w_post=None, scale=None, w_pre=None,
@@ -881,22 +895,22 @@ def lizard_block_norm_fwd(o, *, gate=None, r=None, w_post=None, scale=None, w_pr
     block: o [T, D] is the block's output, r [T, D] the residual stream (its dtype or fp32).
     Returns (r_out, n_out); n_out is None without w_pre.  r_out takes r's dtype, or o's."""
     shape = tuple(o.shape)
-    if len(shape) != 2:
-        raise ValueError("o must be [T, D]")
     rtp = r.dtype if r is not None else r_out.dtype if r_out is not None else o.dtype
     dims, ptrs = _norm_inputs(o, gate, r, w_post, scale, w_pre, rtp, groups, act, gate_first, eps,
                               eps_pre)
     if r_out is None:
-        r_out = torch.empty(shape, dtype=rtp, device=o.device)
-    dims.ldro = _ld(r_out, "r_out", shape, rtp)
-    if w_pre is not None:
-        if n_out is None:
-            n_out = torch.empty(shape, dtype=o.dtype, device=o.device)
-        dims.ldn = _ld(n_out, "n_out", shape, o.dtype)
-    elif n_out is not None:
-        raise ValueError("n_out needs w_pre")
+        r_out = o.new_empty(shape, dtype=rtp)
+    else:
+        dims.ldro = _ld(r_out, "r_out", shape, rtp, 1)
+    if w_pre is None:
+        if n_out is not None:
+            raise ValueError("n_out needs w_pre")
+    elif n_out is None:
+        n_out = o.new_empty(shape)
+    else:
+        dims.ldn = _ld(n_out, "n_out", shape, o.dtype, 1)
     st = load().lizard_block_norm_fwd(ctypes.byref(dims), *ptrs, r_out.data_ptr(), _ptr(n_out),
-                                      _stream(stream))
+                                      _stream_of(stream, o))
     _check(st, "lizard_block_norm_fwd")
     return r_out, n_out
 
@@ -917,9 +931,9 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
     dims, ptrs = _norm_inputs(o, gate, r, w_post, scale, w_pre, rtp, groups, act, gate_first, eps,
                               eps_pre)
     if dr_out is not None:
-        dims.ldro = _ld(dr_out, "dr_out", shape, rtp)
+        dims.ldro = _ld(dr_out, "dr_out", shape, rtp, 1)
     if dn_out is not None:
-        dims.ldn = _ld(dn_out, "dn_out", shape, o.dtype)
+        dims.ldn = _ld(dn_out, "dn_out", shape, o.dtype, 1)
 
     def like(t, dtype=None):
         return None if t is None else torch.empty(tuple(t.shape), dtype=dtype or t.dtype, device=o.device)
@@ -930,6 +944,6 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
     st = load().lizard_block_norm_bwd(ctypes.byref(dims), *ptrs, _ptr(dr_out), _ptr(dn_out),
                                       do.data_ptr(), _ptr(dgate), _ptr(dr), _ptr(dw_post),
                                       _ptr(dscale), _ptr(dw_pre), workspace.data_ptr(),
-                                      workspace.numel(), _stream(stream))
+                                      workspace.numel(), _stream_of(stream, o))
     _check(st, "lizard_block_norm_bwd")
     return dict(do=do, dgate=dgate, dr=dr, dw_post=dw_post, dscale=dscale, dw_pre=dw_pre)

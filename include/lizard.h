@@ -365,6 +365,7 @@ lizard_status lizard_decode_step_positions(const lizard_dims* dims, const int64_
  *     Inconsistent offsets never cause an access out of bounds; they record
  *     LIZARD_ERR_INVALID_ARG in the workspace's status word where a workspace is given, and the
  *     results of that call are not defined.
+ *   - A row of a batch has fewer than 2^31 tokens (offsets of elements are 64 bits wide).
  *   - L may be 0 (a packed batch of empty sequences): states are passed on, nothing else is
  *     written; parameter gradients are 0. */
 
