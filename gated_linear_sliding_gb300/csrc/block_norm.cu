@@ -13,6 +13,8 @@
 namespace lz {
 namespace {
 
+constexpr int kSumsWidth = 8192;  // widest row whose parameter sums fit into shared memory
+
 // Sum over a CTA's (TPR > 32) or a warp's threads, the same value in each of them.  Consecutive
 // sums of a CTA alternate between two buffers: the barrier of the one in between is what lets a
 // buffer be written again.
@@ -71,317 +73,420 @@ __device__ __forceinline__ void group_sum(float* p, int nvec, int gv, float* sm,
     }
 }
 
-__device__ __forceinline__ float act_of(int act, float g, float sg) { return act == LIZARD_ACT_SILU ? g * sg : sg; }
-__device__ __forceinline__ float dact_of(int act, float g, float sg) {
-    return act == LIZARD_ACT_SILU ? dsilu(g, sg) : sg * (1.0f - sg);
+// A thread's columns of a row, in pairs: NV pieces of V neighbouring columns each, piece i at
+// column (i TPR + lane) V.  With V = 1 a pair is two pieces.
+template <int V, int TPR, int NV>
+struct Cols {
+    static constexpr int NP = V * NV / 2;
+    template <typename T>
+    static __device__ __forceinline__ void ld(const T* row, int lr, int nvec, f2* f) {
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int c = 2 * k * TPR + lr;
+                f[k] = pack(c < nvec ? lz::ld(row + c) : 0.0f, c + TPR < nvec ? lz::ld(row + c + TPR) : 0.0f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i * TPR + lr < nvec) {
+                    get2(*reinterpret_cast<const Pack<T, V>*>(row + (i * TPR + lr) * V), f + i * V / 2);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V / 2; ++k) f[i * V / 2 + k] = 0;
+                }
+            }
+        }
+    }
+    template <typename T>
+    static __device__ __forceinline__ void st(T* row, int lr, int nvec, const f2* f) {
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int c = 2 * k * TPR + lr;
+                float x, y;
+                unpack(f[k], x, y);
+                if (c < nvec) lz::st(row + c, x);
+                if (c + TPR < nvec) lz::st(row + c + TPR, y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i * TPR + lr >= nvec) continue;
+                float v[V];
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) unpack(f[i * V / 2 + k], v[2 * k], v[2 * k + 1]);
+                Vec<V>::st(row + (i * TPR + lr) * V, v);
+            }
+        }
+    }
+    // the sum of a b over each piece
+    static __device__ __forceinline__ void pieces(const f2* a, const f2* b, float* p) {
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) unpack(mul2(a[k], b[k]), p[2 * k], p[2 * k + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                f2 s = mul2(a[i * V / 2], b[i * V / 2]);
+#pragma unroll
+                for (int k = 1; k < V / 2; ++k) s = fma2(a[i * V / 2 + k], b[i * V / 2 + k], s);
+                p[i] = sum2(s);
+            }
+        }
+    }
+    // piece i's value at pair k
+    static __device__ __forceinline__ f2 at(const float* p, int k) {
+        if constexpr (V == 1) return pack(p[2 * k], p[2 * k + 1]);
+        else return pack(p[k / (V / 2)], p[k / (V / 2)]);
+    }
+};
+
+// The next row's pieces of one tensor on their way into shared memory, each thread's own; not ON:
+// rows are read directly.
+template <typename T, int V, int TPR, int NV, bool ON>
+struct Ahead {
+    T* at;  // [nvec V]
+    __device__ __forceinline__ void fetch(const T* row, int lr, int nvec) const {
+        if constexpr (ON) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + lr) * V;
+                if (i * TPR + lr < nvec) copy_async<T, V>(at + c, row + c);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const T* row, int lr, int nvec, f2* f) const {
+        Cols<V, TPR, NV>::ld(ON ? at : row, lr, nvec, f);
+    }
+};
+
+// Whether the backward's rows fit ahead, next to the parameter sums, into a SM's 227 KB.
+template <typename T, int V, int TPR>
+constexpr bool rows_ahead() { return V > 1 && (TPR < 512 || (TPR == 512 && sizeof(T) == 2)); }
+
+template <int NP>
+__device__ __forceinline__ float dot_of(const f2* a, const f2* b) {
+    f2 s = mul2(a[0], b[0]);
+#pragma unroll
+    for (int k = 1; k < NP; ++k) s = fma2(a[k], b[k], s);
+    return sum2(s);
 }
 
-// TPR threads a row; 32: four rows a CTA of 128, else one row a CTA.
+// TPR threads a row (32: four rows a CTA of 128, else one row a CTA), which walk rows at a distance
+// of all rows that are worked on at once, the next row's values on their way meanwhile.
 template <typename T, typename R, int V, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const NormArgs a) {
-    constexpr int RPC = TPR < 128 ? 128 / TPR : 1;
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 768 ? 768 / (TPR < 128 ? 128 : TPR) : 1)
+    norm_fwd_kernel(const NormArgs a) {
+    using C = Cols<V, TPR, NV>;
+    constexpr int NP = C::NP, RPC = TPR < 128 ? 128 / TPR : 1;
     constexpr bool FAST = is_fast<T>();
     __shared__ float red[2][1][32];
-    extern __shared__ __align__(16) float gsm[];
-    const int lr = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPC + threadIdx.x / TPR;
-    if (TPR == 32 && row >= a.T) return;  // a whole warp
+    extern __shared__ __align__(16) float gsm[];  // the group sums' space, then the rows ahead
+    const int lr = threadIdx.x % TPR, rc = threadIdx.x / TPR;
     const int D = (int)a.D, nvec = D / V, gv = nvec / (int)a.groups;
-    const T* o = (const T*)a.o + row * a.ldo;
-    const T* gate = (const T*)a.gate + row * a.ldg;
-    const R* r = (const R*)a.r + row * a.ldr;
-    float n[NV][V], ga[NV][V], rr[NV][V];
+    char* ahead = (char*)gsm + a.group_bytes + (size_t)rc * D * (2 * sizeof(T) + sizeof(R));
+    const Ahead<R, V, TPR, NV, (V > 1)> ar{(R*)ahead};
+    const Ahead<T, V, TPR, NV, (V > 1)> ao{(T*)(ahead + D * sizeof(R))}, ag{ao.at + D};
+    const int64_t step = (int64_t)gridDim.x * RPC;
+    auto fetch = [&](int64_t row) {  // two groups: what a row begins with, and its residual
+        if (row < a.T) {
+            ao.fetch((const T*)a.o + row * a.ldo, lr, nvec);
+            if (a.gate != nullptr) ag.fetch((const T*)a.gate + row * a.ldg, lr, nvec);
+        }
+        copy_commit();
+    };
+    auto fetch_r = [&](int64_t row) {
+        if (row < a.T && a.r != nullptr) ar.fetch((const R*)a.r + row * a.ldr, lr, nvec);
+        copy_commit();
+    };
+    int64_t row = (int64_t)blockIdx.x * RPC + rc;
+    fetch(row);
+    fetch_r(row);
+    int buf = 0;
+    for (; row < a.T; row += step) {
+        f2 n[NP], ga[NP], rr[NP], w[NP];
+        copy_wait<1>();
+        ao.get((const T*)a.o + row * a.ldo, lr, nvec, n);
+        if (a.gate != nullptr) ag.get((const T*)a.gate + row * a.ldg, lr, nvec, ga);
+        fetch(row + step);
+        if (a.gate != nullptr) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int vi = i * TPR + lr;
-        const bool in = vi < nvec;
-#pragma unroll
-        for (int j = 0; j < V; ++j) n[i][j] = ga[i][j] = rr[i][j] = 0.0f;
-        if (in) Vec<V>::ld(o + vi * V, n[i]);
-        if (in && a.gate != nullptr) Vec<V>::ld(gate + vi * V, ga[i]);
-        if (in && a.r != nullptr) Vec<V>::ld(r + vi * V, rr[i]);
-    }
-    if (a.gate != nullptr) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                ga[i][j] = act_of(a.act, ga[i][j], sigm<FAST>(ga[i][j]));
-                if (a.gate_first) n[i][j] *= ga[i][j];
+            for (int k = 0; k < NP; ++k) {
+                const f2 sg = sigm2<FAST>(ga[k]);
+                ga[k] = a.act == LIZARD_ACT_SILU ? mul2(ga[k], sg) : sg;
+                if (a.gate_first) n[k] = mul2(n[k], ga[k]);
             }
-    }
-    if (a.w_post != nullptr) {
-        float ss[NV];
-        float all[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            ss[i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) ss[i] = fmaf(n[i][j], n[i][j], ss[i]);
-            all[0] += ss[i];
         }
-        if (a.groups == 1) {
-            row_sum<TPR, 1>(all, red[0]);
+        if (a.w_post != nullptr) {
+            C::ld(a.w_post, lr, nvec, w);
+            if (a.groups == 1) {
+                float all[1] = {dot_of<NP>(n, n)};
+                row_sum<TPR, 1>(all, red[buf]);
+                buf ^= 1;
+                const float rs = rsqrtf(all[0] / (float)D + a.eps_post);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) ss[i] = all[0];
-        } else {
-            group_sum<TPR, NV>(ss, nvec, gv, gsm, lr);
+                for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], mul2(w[k], pack(rs, rs)));
+            } else {
+                float p[NV];
+                C::pieces(n, n, p);
+                group_sum<TPR, NV>(p, nvec, gv, gsm, lr);
+                const float inv = 1.0f / (float)(gv * V);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)  // columns past the row stay zero, whatever eps is
+                    p[i] = i * TPR + lr < nvec ? rsqrtf(fmaf(p[i], inv, a.eps_post)) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], mul2(w[k], C::at(p, k)));
+            }
         }
-        const float inv = 1.0f / (float)(gv * V);
+        if (a.gate != nullptr && !a.gate_first) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vi = i * TPR + lr;
-            const float rs = rsqrtf(fmaf(ss[i], inv, a.eps_post));
-            float w[V];
-            if (vi < nvec) Vec<V>::ld(a.w_post + vi * V, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) n[i][j] *= rs * w[j];
+            for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], ga[k]);
         }
-    }
-    float all[1] = {0.0f};
+        copy_wait<1>();
+        if (a.r != nullptr) ar.get((const R*)a.r + row * a.ldr, lr, nvec, rr);
+        fetch_r(row + step);
+        if (a.scale != nullptr) {
+            C::ld(a.scale, lr, nvec, w);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int vi = i * TPR + lr;
-        if (vi >= nvec) continue;
-        float w[V];
-        if (a.scale != nullptr) Vec<V>::ld(a.scale + vi * V, w);
+            for (int k = 0; k < NP; ++k) n[k] = a.r != nullptr ? fma2(w[k], n[k], rr[k]) : mul2(w[k], n[k]);
+        } else if (a.r != nullptr) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            if (a.gate != nullptr && !a.gate_first) n[i][j] *= ga[i][j];
-            rr[i][j] = a.scale != nullptr ? fmaf(w[j], n[i][j], rr[i][j]) : rr[i][j] + n[i][j];
-            all[0] = fmaf(rr[i][j], rr[i][j], all[0]);
+            for (int k = 0; k < NP; ++k) n[k] = add2(n[k], rr[k]);
         }
-        if (a.r_out != nullptr) Vec<V>::st((R*)a.r_out + row * a.ldro + vi * V, rr[i]);
-    }
-    if (a.n_out == nullptr) return;
-    row_sum<TPR, 1>(all, red[1]);
-    const float rs = rsqrtf(all[0] / (float)D + a.eps_pre);
+        if (a.r_out != nullptr) C::st((R*)a.r_out + row * a.ldro, lr, nvec, n);
+        if (a.n_out == nullptr) continue;
+        C::ld(a.w_pre, lr, nvec, w);
+        float all[1] = {dot_of<NP>(n, n)};
+        row_sum<TPR, 1>(all, red[buf]);
+        buf ^= 1;
+        const float rs = rsqrtf(all[0] / (float)D + a.eps_pre);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int vi = i * TPR + lr;
-        if (vi >= nvec) continue;
-        float w[V];
-        Vec<V>::ld(a.w_pre + vi * V, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) rr[i][j] *= rs * w[j];
-        Vec<V>::st((T*)a.n_out + row * a.ldn + vi * V, rr[i]);
+        for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], mul2(w[k], pack(rs, rs)));
+        C::st((T*)a.n_out + row * a.ldn, lr, nvec, n);
     }
+    copy_wait<0>();
 }
 
-// One CTA walks rows b, b + grid, ..., the next row's values on their way while one is worked on.
-// The parameter gradients of a thread's columns are summed in shared memory, in the thread's own
-// places, and leave once, as the CTA's partial sums.
+// One CTA walks rows b, b + grid, ...  The parameter gradients of a thread's columns are summed in
+// shared memory (the widest rows: in the CTA's partial sums themselves), in the thread's own
+// places, and leave once.  Sixteen columns a thread: with fewer the sums over the row cost more
+// than the row's arithmetic (four columns: 402 us on 16384 x 4096).
 template <typename T, typename R, int V, int TPR, int NV>
-__global__ void __launch_bounds__(TPR, V * NV <= 4 ? 1024 / TPR : 1)
-    norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kernel(const NormArgs a) {
+    using C = Cols<V, TPR, NV>;
+    constexpr int NP = C::NP;
+    constexpr bool ON = rows_ahead<T, V, TPR>();
     constexpr bool FAST = is_fast<T>();
-    // hold the next row where registers allow it: 64 a thread at 1024 threads a SM
-    constexpr bool AHEAD = sizeof(T) == 2 && V * NV <= 4;
     __shared__ float red[2][2][32];
-    extern __shared__ __align__(16) float gsm[];  // [3][D], then the group sums' space
+    // [3][D] up to kSumsWidth columns, the group sums' space, the row ahead
+    extern __shared__ __align__(16) float gsm[];
     const int lr = threadIdx.x;
     const int D = (int)a.D, nvec = D / V, gv = nvec / (int)a.groups;
-    float *apost = gsm, *ascale = gsm + D, *apre = gsm + 2 * D, *gspace = gsm + 3 * D;
-    for (int i = lr; i < 3 * D; i += TPR) gsm[i] = 0.0f;
-    __syncthreads();
+    float* partial = a.partial + (int64_t)blockIdx.x * 3 * D;
+    const bool near = D <= kSumsWidth;
+    float *sums = near ? gsm : partial, *gspace = near ? gsm + 3 * D : gsm;
+    {
+        f2 zero[NP];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) zero[k] = 0;
+        for (int m = 0; m < 3; ++m) C::st(sums + m * D, lr, nvec, zero);
+    }
+    auto add_to = [&](int m, const f2* v) {
+        f2 s[NP];
+        C::ld(sums + m * D, lr, nvec, s);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) s[k] = add2(s[k], v[k]);
+        C::st(sums + m * D, lr, nvec, s);
+    };
     const bool gate = a.gate != nullptr, gfirst = gate && a.gate_first, glast = gate && !a.gate_first;
     const float ginv = 1.0f / (float)(gv * V), dinv = 1.0f / (float)D;
-    Pack<T, V> po[NV], pg[NV], pn[NV];
-    Pack<R, V> pr[NV], pd[NV];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vi = i * TPR + lr;
-            if (vi >= nvec) continue;
-            po[i] = *reinterpret_cast<const Pack<T, V>*>((const T*)a.o + row * a.ldo + vi * V);
-            if (gate) pg[i] = *reinterpret_cast<const Pack<T, V>*>((const T*)a.gate + row * a.ldg + vi * V);
-            if (a.dr_out != nullptr) pd[i] = *reinterpret_cast<const Pack<R, V>*>((const R*)a.dr_out + row * a.ldro + vi * V);
+    char* ahead = (char*)gspace + a.group_bytes;
+    const Ahead<R, V, TPR, NV, ON> ad{(R*)ahead}, ar{ad.at + D};
+    const Ahead<T, V, TPR, NV, ON> ao{(T*)(ar.at + D)}, ag{ao.at + D}, an{ag.at + D};
+    auto fetch = [&](int64_t row) {  // two groups: what a row begins with, and what comes later
+        if (row < a.T) {
+            ao.fetch((const T*)a.o + row * a.ldo, lr, nvec);
+            if (gate) ag.fetch((const T*)a.gate + row * a.ldg, lr, nvec);
+        }
+        copy_commit();
+    };
+    auto fetch_later = [&](int64_t row) {
+        if (row < a.T) {
+            if (a.dr_out != nullptr) ad.fetch((const R*)a.dr_out + row * a.ldro, lr, nvec);
             if (a.w_pre != nullptr) {
-                if (a.r != nullptr) pr[i] = *reinterpret_cast<const Pack<R, V>*>((const R*)a.r + row * a.ldr + vi * V);
-                pn[i] = *reinterpret_cast<const Pack<T, V>*>((const T*)a.dn_out + row * a.ldn + vi * V);
+                if (a.r != nullptr) ar.fetch((const R*)a.r + row * a.ldr, lr, nvec);
+                an.fetch((const T*)a.dn_out + row * a.ldn, lr, nvec);
             }
         }
+        copy_commit();
     };
-    auto add_to = [](float* sum, const float* v) {
-        float s[V];
-        Vec<V>::ld(sum, s);
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] += v[j];
-        Vec<V>::st(sum, s);
-    };
+    fetch(blockIdx.x);
+    fetch_later(blockIdx.x);
     int buf = 0;
-    if (AHEAD && (int64_t)blockIdx.x < a.T) fetch(blockIdx.x);
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-        if (!AHEAD) fetch(row);
-        float u[NV][V], ga[NV][V], gd[NV][V], dr[NV][V], rr[NV][V], dn[NV][V];
-        float ss[NV], rs[NV], all[2] = {0.0f, 0.0f};
-        // u: the normalised row (the plain one without a norm); a thread's columns past the row
-        // stay zero and count nowhere
+        // u: the normalised row (the plain one without a norm); ga, gd: act(gate), its derivative
+        f2 u[NP], ga[NP], gd[NP], dr[NP], w[NP];
+        copy_wait<1>();
+        ao.get((const T*)a.o + row * a.ldo, lr, nvec, u);
+        if (gate) ag.get((const T*)a.gate + row * a.ldg, lr, nvec, ga);
+        fetch(row + gridDim.x);
+        if (gate) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = i * TPR + lr < nvec;
-#pragma unroll
-            for (int j = 0; j < V; ++j) u[i][j] = ga[i][j] = gd[i][j] = dr[i][j] = rr[i][j] = dn[i][j] = 0.0f;
-            if (in) {
-                po[i].get(u[i]);
-                if (gate) pg[i].get(ga[i]);
-                if (a.dr_out != nullptr) pd[i].get(dr[i]);
-                if (a.w_pre != nullptr) {
-                    if (a.r != nullptr) pr[i].get(rr[i]);
-                    pn[i].get(dn[i]);
-                }
-            }
-            ss[i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (gate) {  // ga: act(gate), gd: its derivative
-                    const float g = ga[i][j], sg = sigm<FAST>(g);
-                    ga[i][j] = act_of(a.act, g, sg);
-                    gd[i][j] = dact_of(a.act, g, sg);
+            for (int k = 0; k < NP; ++k) {
+                const f2 sg = sigm2<FAST>(ga[k]);
+                if (a.act == LIZARD_ACT_SILU) {
+                    gd[k] = dsilu2(ga[k], sg);
+                    ga[k] = mul2(ga[k], sg);
+                } else {
+                    gd[k] = mul2(sg, fma2(sg, pack(-1.0f, -1.0f), pack(1.0f, 1.0f)));
+                    ga[k] = sg;
                 }
                 if (gfirst) {
-                    gd[i][j] *= u[i][j];
-                    u[i][j] *= ga[i][j];
+                    gd[k] = mul2(gd[k], u[k]);
+                    u[k] = mul2(u[k], ga[k]);
                 }
-                ss[i] = fmaf(u[i][j], u[i][j], ss[i]);
             }
-            all[0] += ss[i];
-            rs[i] = 1.0f;
         }
-        if (AHEAD && row + gridDim.x < a.T) fetch(row + gridDim.x);
+        float rs[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) rs[i] = 1.0f;
         if (a.w_post != nullptr) {
             if (a.groups == 1) {
+                float all[1] = {dot_of<NP>(u, u)};
                 row_sum<TPR, 1>(all, red[buf]);
                 buf ^= 1;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) ss[i] = all[0];
+                for (int i = 0; i < NV; ++i) rs[i] = rsqrtf(fmaf(all[0], ginv, a.eps_post));
             } else {
-                group_sum<TPR, NV>(ss, nvec, gv, gspace, lr);
+                C::pieces(u, u, rs);
+                group_sum<TPR, NV>(rs, nvec, gv, gspace, lr);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)  // columns past the row stay zero, whatever eps is
+                    rs[i] = i * TPR + lr < nvec ? rsqrtf(fmaf(rs[i], ginv, a.eps_post)) : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                rs[i] = rsqrtf(fmaf(ss[i], ginv, a.eps_post));
-#pragma unroll
-                for (int j = 0; j < V; ++j) u[i][j] *= rs[i];
-            }
+            for (int k = 0; k < NP; ++k) u[k] = mul2(u[k], C::at(rs, k));
         }
         // the gradient of rr
-        if (a.w_pre != nullptr) {
-            all[0] = all[1] = 0.0f;
+        copy_wait<1>();
+        if (a.dr_out != nullptr) {
+            ad.get((const R*)a.dr_out + row * a.ldro, lr, nvec, dr);
+        } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int vi = i * TPR + lr;
-                if (vi >= nvec) continue;
-                float w[V];
-                if (a.w_post != nullptr) Vec<V>::ld(a.w_post + vi * V, w);
-                float n[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    n[j] = a.w_post != nullptr ? u[i][j] * w[j] : u[i][j];
-                    if (glast) n[j] *= ga[i][j];
-                }
-                if (a.scale != nullptr) {
-                    Vec<V>::ld(a.scale + vi * V, w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) n[j] *= w[j];
-                }
-                Vec<V>::ld(a.w_pre + vi * V, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    rr[i][j] += n[j];
-                    all[0] = fmaf(rr[i][j], rr[i][j], all[0]);
-                    all[1] = fmaf(dn[i][j] * w[j], rr[i][j], all[1]);
-                }
-            }
-            row_sum<TPR, 2>(all, red[buf]);
-            buf ^= 1;
-            const float rp = rsqrtf(fmaf(all[0], dinv, a.eps_pre)), k = all[1] * dinv * rp * rp;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int vi = i * TPR + lr;
-                if (vi >= nvec) continue;
-                float w[V];
-                Vec<V>::ld(a.w_pre + vi * V, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    dr[i][j] += rp * (dn[i][j] * w[j] - rr[i][j] * k);
-                    dn[i][j] *= rr[i][j] * rp;
-                }
-                add_to(apre + vi * V, dn[i]);
-            }
+            for (int k = 0; k < NP; ++k) dr[k] = 0;
         }
-        float dot[NV];
-        all[0] = 0.0f;
+        // what the block adds to the residual, before its scale, times f
+        auto added = [&](const f2* f, f2* n) {
+            if (a.w_post != nullptr) {
+                C::ld(a.w_post, lr, nvec, n);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vi = i * TPR + lr;
-            dot[i] = 0.0f;
-            if (vi >= nvec) continue;
-            if (a.dr != nullptr) Vec<V>::st((R*)a.dr + row * a.lddr + vi * V, dr[i]);
-            float w[V], t[V];
-            if (a.w_post != nullptr) Vec<V>::ld(a.w_post + vi * V, w);
-            if (a.scale != nullptr) {
-                float sc[V];
-                Vec<V>::ld(a.scale + vi * V, sc);
+                for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], mul2(u[k], f[k]));
+            } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float n = a.w_post != nullptr ? u[i][j] * w[j] : u[i][j];
-                    if (glast) n *= ga[i][j];
-                    t[j] = dr[i][j] * n;
-                    dr[i][j] *= sc[j];
-                }
-                add_to(ascale + vi * V, t);
+                for (int k = 0; k < NP; ++k) n[k] = mul2(u[k], f[k]);
             }
             if (glast) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float n = a.w_post != nullptr ? u[i][j] * w[j] : u[i][j];
-                    t[j] = dr[i][j] * n * gd[i][j];
-                    dr[i][j] *= ga[i][j];
-                }
-                Vec<V>::st((T*)a.dgate + row * a.lddg + vi * V, t);
+                for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], ga[k]);
             }
-            if (a.w_post != nullptr) {
+        };
+        if (a.w_pre != nullptr) {
+            f2 rr[NP], dn[NP];
+            if (a.scale != nullptr) {
+                C::ld(a.scale, lr, nvec, w);
+            } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    t[j] = dr[i][j] * u[i][j];
-                    dr[i][j] *= w[j];
-                    dot[i] = fmaf(dr[i][j], u[i][j], dot[i]);
-                }
-                add_to(apost + vi * V, t);
+                for (int k = 0; k < NP; ++k) w[k] = pack(1.0f, 1.0f);
             }
-            all[0] += dot[i];
+            added(w, rr);
+            if (a.r != nullptr) {
+                ar.get((const R*)a.r + row * a.ldr, lr, nvec, w);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) rr[k] = add2(rr[k], w[k]);
+            }
+            an.get((const T*)a.dn_out + row * a.ldn, lr, nvec, dn);
+            C::ld(a.w_pre, lr, nvec, w);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) w[k] = mul2(w[k], dn[k]);
+            float all[2] = {dot_of<NP>(rr, rr), dot_of<NP>(w, rr)};
+            row_sum<TPR, 2>(all, red[buf]);
+            buf ^= 1;
+            const float rp = rsqrtf(fmaf(all[0], dinv, a.eps_pre)), c = -all[1] * dinv * rp * rp;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                dr[k] = fma2(fma2(rr[k], pack(c, c), w[k]), pack(rp, rp), dr[k]);
+                dn[k] = mul2(dn[k], mul2(rr[k], pack(rp, rp)));
+            }
+            add_to(2, dn);
+        }
+        fetch_later(row + gridDim.x);
+        if (a.dr != nullptr) C::st((R*)a.dr + row * a.lddr, lr, nvec, dr);
+        f2 t[NP];
+        if (a.scale != nullptr) {
+            added(dr, t);
+            add_to(1, t);
+            C::ld(a.scale, lr, nvec, w);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) dr[k] = mul2(dr[k], w[k]);
+        }
+        if (glast) {
+            if (a.w_post != nullptr) {
+                C::ld(a.w_post, lr, nvec, t);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) t[k] = mul2(t[k], u[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NP; ++k) t[k] = u[k];
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                t[k] = mul2(t[k], mul2(dr[k], gd[k]));
+                dr[k] = mul2(dr[k], ga[k]);
+            }
+            C::st((T*)a.dgate + row * a.lddg, lr, nvec, t);
         }
         if (a.w_post != nullptr) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) t[k] = mul2(dr[k], u[k]);
+            add_to(0, t);
+            C::ld(a.w_post, lr, nvec, w);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) dr[k] = mul2(dr[k], w[k]);
+            float dot[NV];
             if (a.groups == 1) {
+                float all[1] = {dot_of<NP>(dr, u)};
                 row_sum<TPR, 1>(all, red[buf]);
                 buf ^= 1;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) dot[i] = all[0];
             } else {
+                C::pieces(dr, u, dot);
                 group_sum<TPR, NV>(dot, nvec, gv, gspace, lr);
             }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) dot[i] *= -ginv;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) dr[k] = mul2(fma2(u[k], C::at(dot, k), dr[k]), C::at(rs, k));
         }
+        if (gfirst) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vi = i * TPR + lr;
-            if (vi >= nvec) continue;
-            float dg[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (a.w_post != nullptr) dr[i][j] = rs[i] * (dr[i][j] - u[i][j] * (dot[i] * ginv));
-                if (gfirst) {
-                    dg[j] = dr[i][j] * gd[i][j];
-                    dr[i][j] *= ga[i][j];
-                }
+            for (int k = 0; k < NP; ++k) {
+                t[k] = mul2(dr[k], gd[k]);
+                dr[k] = mul2(dr[k], ga[k]);
             }
-            Vec<V>::st((T*)a.d_o + row * a.lddo + vi * V, dr[i]);
-            if (gfirst) Vec<V>::st((T*)a.dgate + row * a.lddg + vi * V, dg);
+            C::st((T*)a.dgate + row * a.lddg, lr, nvec, t);
+        }
+        C::st((T*)a.d_o + row * a.lddo, lr, nvec, dr);
+    }
+    copy_wait<0>();
+    if (near) {
+        f2 s[NP];
+        for (int m = 0; m < 3; ++m) {
+            C::ld(sums + m * D, lr, nvec, s);
+            C::st(partial + m * D, lr, nvec, s);
         }
     }
-    float* p = a.partial + (int64_t)blockIdx.x * 3 * D;
-    __syncthreads();
-    for (int i = lr; i < 3 * D; i += TPR) p[i] = gsm[i];
 }
 
 // dw_post, dscale and dw_pre from the CTAs' partial sums [n][3][D], each added in the same order.
@@ -417,23 +522,28 @@ cudaError_t group_smem(K kernel, size_t bytes) {
 size_t group_bytes(const NormArgs& a, int V) {
     const int64_t nvec = a.D / V, gv = nvec / a.groups;
     if (a.groups == 1 || a.w_post == nullptr || (gv <= 32 && (gv & (gv - 1)) == 0)) return 0;
-    return sizeof(float) * (size_t)(nvec + a.groups);
+    return (sizeof(float) * (size_t)(nvec + a.groups) + 15) / 16 * 16;
 }
 
 template <typename T, typename R, int V, int TPR, int NV>
-cudaError_t fwd_go(const NormArgs& a, cudaStream_t s) {
+cudaError_t fwd_go(NormArgs a, cudaStream_t s) {
     constexpr int RPC = TPR < 128 ? 128 / TPR : 1;
-    const size_t sm = group_bytes(a, V);
-    const cudaError_t e = group_smem(norm_fwd_kernel<T, R, V, TPR, NV>, sm);
+    a.group_bytes = group_bytes(a, V);
+    const size_t sm = a.group_bytes + (V > 1 ? RPC * (size_t)a.D * (2 * sizeof(T) + sizeof(R)) : 0);
+    const auto kernel = norm_fwd_kernel<T, R, V, TPR, NV>;
+    const cudaError_t e = group_smem(kernel, sm);
     if (e != cudaSuccess) return e;
-    norm_fwd_kernel<T, R, V, TPR, NV><<<(unsigned)((a.T + RPC - 1) / RPC), TPR * RPC, sm, s>>>(a);
+    // as many CTAs as are resident: 768 threads a SM
+    const int64_t ctas = (a.T + RPC - 1) / RPC, most = 152 * (TPR >= 768 ? 1 : 768 / (TPR < 128 ? 128 : TPR));
+    kernel<<<(unsigned)(ctas < most ? ctas : most), TPR * RPC, sm, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, typename R, int V, int TPR, int NV>
-cudaError_t bwd_go(const NormArgs& a, cudaStream_t s) {
-    const size_t sm = sizeof(float) * 3 * (size_t)a.D + group_bytes(a, V);
-    // the odd-width path at its widest, with both the sums and one value a column
+cudaError_t bwd_go(NormArgs a, cudaStream_t s) {
+    a.group_bytes = group_bytes(a, V);
+    const size_t sm = sizeof(float) * (a.D <= kSumsWidth ? 3 * (size_t)a.D : 0) + a.group_bytes +
+                      (rows_ahead<T, V, TPR>() ? (size_t)a.D * (3 * sizeof(T) + 2 * sizeof(R)) : 0);
     const cudaError_t e = group_smem(norm_bwd_kernel<T, R, V, TPR, NV>, sm);
     if (e != cudaSuccess) return e;
     norm_bwd_kernel<T, R, V, TPR, NV><<<(unsigned)norm_bwd_ctas(a.T, a.D), TPR, sm, s>>>(a);
@@ -446,34 +556,34 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
     const bool v8 = a.D % 8 == 0 && (a.D / a.groups) % 8 == 0 && a.ldo % 8 == 0 && a.ldg % 8 == 0 &&
                     a.ldr % 8 == 0 && a.ldro % 8 == 0 && a.ldn % 8 == 0;
     if (v8) {
-        if (a.D <= 256 && a.groups == 1) return fwd_go<T, R, 8, 32, 1>(a, s);
+        if (a.D <= 512 && a.groups == 1) return fwd_go<T, R, 8, 32, 2>(a, s);
         if (a.D <= 1024) return fwd_go<T, R, 8, 128, 1>(a, s);
-        if (a.D <= 2048) return fwd_go<T, R, 8, 256, 1>(a, s);
+        if (a.D <= 2048) return fwd_go<T, R, 8, 128, 2>(a, s);
         if (a.D <= 4096) return fwd_go<T, R, 8, 256, 2>(a, s);
         if (a.D <= 8192) return fwd_go<T, R, 8, 512, 2>(a, s);
         return fwd_go<T, R, 8, 1024, 2>(a, s);
     }
     if (a.D <= 1024) return fwd_go<T, R, 1, 256, 4>(a, s);
-    if (a.D <= 8192) return fwd_go<T, R, 1, 1024, 8>(a, s);
+    if (a.D <= 4096) return fwd_go<T, R, 1, 512, 8>(a, s);
     return fwd_go<T, R, 1, 1024, 16>(a, s);
 }
 
 template <typename T, typename R>
 cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
-    const bool v4 = a.D % 4 == 0 && (a.D / a.groups) % 4 == 0 && a.ldo % 4 == 0 && a.ldg % 4 == 0 &&
-                    a.ldr % 4 == 0 && a.ldro % 4 == 0 && a.ldn % 4 == 0 && a.lddo % 4 == 0 &&
-                    a.lddg % 4 == 0 && a.lddr % 4 == 0;
+    const bool v8 = a.D % 8 == 0 && (a.D / a.groups) % 8 == 0 && a.ldo % 8 == 0 && a.ldg % 8 == 0 &&
+                    a.ldr % 8 == 0 && a.ldro % 8 == 0 && a.ldn % 8 == 0 && a.lddo % 8 == 0 &&
+                    a.lddg % 8 == 0 && a.lddr % 8 == 0;
     cudaError_t e;
-    if (v4) {
-        if (a.D <= 512) e = bwd_go<T, R, 4, 128, 1>(a, s);
-        else if (a.D <= 1024) e = bwd_go<T, R, 4, 256, 1>(a, s);
-        else if (a.D <= 2048) e = bwd_go<T, R, 4, 512, 1>(a, s);
-        else if (a.D <= 4096) e = bwd_go<T, R, 4, 1024, 1>(a, s);
-        else if (a.D <= 8192) e = bwd_go<T, R, 4, 1024, 2>(a, s);
-        else e = bwd_go<T, R, 4, 1024, 4>(a, s);
+    if (v8) {
+        if (a.D <= 512) e = bwd_go<T, R, 8, 32, 2>(a, s);
+        else if (a.D <= 1024) e = bwd_go<T, R, 8, 64, 2>(a, s);
+        else if (a.D <= 2048) e = bwd_go<T, R, 8, 128, 2>(a, s);
+        else if (a.D <= 4096) e = bwd_go<T, R, 8, 256, 2>(a, s);
+        else if (a.D <= 8192) e = bwd_go<T, R, 8, 512, 2>(a, s);
+        else e = bwd_go<T, R, 8, 1024, 2>(a, s);
     } else {
-        if (a.D <= 1024) e = bwd_go<T, R, 1, 256, 4>(a, s);
-        else if (a.D <= 8192) e = bwd_go<T, R, 1, 1024, 8>(a, s);
+        if (a.D <= 1024) e = bwd_go<T, R, 1, 64, 16>(a, s);
+        else if (a.D <= 4096) e = bwd_go<T, R, 1, 256, 16>(a, s);
         else e = bwd_go<T, R, 1, 1024, 16>(a, s);
     }
     if (e != cudaSuccess) return e;
@@ -484,8 +594,8 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
 }  // namespace
 
 int64_t norm_bwd_ctas(int64_t T, int64_t D) {
-    // 1024 threads a SM, as far as the widths' CTAs go
-    const int64_t most = 152 * (D <= 512 ? 8 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1);
+    // 512 threads a SM, sixteen columns a thread
+    const int64_t most = 152 * (D <= 512 ? 16 : D <= 1024 ? 8 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1);
     return T < 1 ? 1 : T < most ? T : most;
 }
 

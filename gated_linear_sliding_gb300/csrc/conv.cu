@@ -15,20 +15,52 @@ namespace {
 constexpr int kNT = 128;
 constexpr int TX = 32, TY = kNT / TX;  // a CTA: TX threads along the channels, TY runs of tokens
 
+// V neighbouring channels as pairs (one channel: a pair with an idle half).
+template <int V>
+struct Chan {
+    static constexpr int NP = (V + 1) / 2;
+    static __device__ __forceinline__ void pairs(const float* f, f2* o) {
+        if constexpr (V == 1) o[0] = pack(f[0], 0.0f);
+        else {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) o[i] = pack(f[2 * i], f[2 * i + 1]);
+        }
+    }
+    template <typename T>
+    static __device__ __forceinline__ void ld(const T* p, f2* o) {
+        float f[V];
+        Vec<V>::ld(p, f);
+        pairs(f, o);
+    }
+    template <typename T>
+    static __device__ __forceinline__ void get(const Pack<T, V>& p, f2* o) {
+        float f[V];
+        p.get(f);
+        pairs(f, o);
+    }
+    template <typename T>
+    static __device__ __forceinline__ void st(T* p, const f2* v) {
+        float f[2 * NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) unpack(v[i], f[2 * i], f[2 * i + 1]);
+        Vec<V>::st(p, f);
+    }
+};
+
 // The K - 1 inputs before token t of its sequence, from the row or the sequence's state.
 template <typename T, int K, int V>
 __device__ __forceinline__ void load_window(const ConvArgs& a, const SeqAt& q, int64_t row0,
-                                            int64_t t, int64_t c, float (*win)[V]) {
+                                            int64_t t, int64_t c, f2 (*win)[Chan<V>::NP]) {
     const T* x = (const T*)a.x;
     const T* st = (const T*)a.state_in;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int64_t u = t - (K - 1) + j;  // token of win[j]
-        if (u >= q.begin) Vec<V>::ld(x + (row0 + u) * a.ldx + c, win[j]);
-        else if (st != nullptr) Vec<V>::ld(st + (q.seq * (K - 1) + (K - 1) + u - q.begin) * a.C + c, win[j]);
+        if (u >= q.begin) Chan<V>::ld(x + (row0 + u) * a.ldx + c, win[j]);
+        else if (st != nullptr) Chan<V>::ld(st + (q.seq * (K - 1) + (K - 1) + u - q.begin) * a.C + c, win[j]);
         else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = 0.0f;
+            for (int i = 0; i < Chan<V>::NP; ++i) win[j][i] = 0;
         }
     }
 }
@@ -37,7 +69,7 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const SeqAt& q, i
 // its own channels' rows of w costs more than the inputs of a run.
 template <int K, int V>
 struct Taps {
-    float w[K][TX * V], bias[TX * V];
+    __align__(16) float w[K][TX * V], bias[TX * V];
     __device__ __forceinline__ void fill(const ConvArgs& a, int64_t c0) {
         const int n = (int)min64(TX * V, a.C - c0);
         for (int e = threadIdx.x; e < n * K; e += kNT) w[e % K][e / K] = a.w[c0 * K + e];
@@ -46,12 +78,19 @@ struct Taps {
     }
 };
 template <int K, int V>
-__device__ __forceinline__ void load_taps(const Taps<K, V>& t, int tx, float (*w)[V], float* bias) {
+__device__ __forceinline__ void load_taps(const Taps<K, V>& t, int tx, f2 (*w)[Chan<V>::NP], f2* bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int j = 0; j < K; ++j) Chan<V>::ld(&t.w[j][tx * V], w[j]);
+    Chan<V>::ld(&t.bias[tx * V], bias);
+}
+// pre-activations, and act of them
+template <int K, int NP>
+__device__ __forceinline__ void taps_of(const f2 (*w)[NP], const f2* bias, const f2 (*win)[NP], f2* p) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = t.w[j][tx * V + i];
-        bias[i] = t.bias[tx * V + i];
+    for (int i = 0; i < NP; ++i) {
+        p[i] = bias[i];
+#pragma unroll
+        for (int j = 0; j < K; ++j) p[i] = fma2(w[j][i], win[j][i], p[i]);
     }
 }
 
@@ -90,35 +129,40 @@ __global__ void __launch_bounds__(kNT) conv_tail_kernel(const ConvArgs a) {
 // written once; the next U rows are on their way while U are computed.
 template <typename T, int K, int V>
 __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
-    constexpr int U = 8;
+    constexpr int U = 8, S = 2;  // rows a group, groups on their way
     const bool silu = a.act == LIZARD_ACT_SILU;
     __shared__ Taps<K, V> taps;
     const int tx = threadIdx.x % TX;
     const int64_t c0 = blockIdx.x % cbs * (TX * V), c = c0 + tx * V;
     const int64_t rr = blockIdx.x / cbs * TY + threadIdx.x / TX, b = rr / runs;
     check_offsets(a.seqs, a.header);
-    taps.fill(a, c0);
-    if (rr >= a.B * runs || c >= a.C) return;
-    const int64_t t0 = rr % runs * run, t1 = min64(t0 + run, a.seqs.L), row0 = b * a.seqs.L;
-    float w[K][V], bias[V], win[K][V];
-    load_taps<K, V>(taps, tx, w, bias);
-    SeqAt q = seq_at(a.seqs, b, t0);
-    load_window<T, K, V>(a, q, row0, t0, c, win);
+    const bool in_range = rr < a.B * runs && c < a.C;
+    const int64_t t0 = rr % runs * run, row0 = b * a.seqs.L;
+    const int n = in_range ? (int)min64(run, a.seqs.L - t0) : 0;
     const T* x = (const T*)a.x + (row0 + t0) * a.ldx + c;
     T* y = (T*)a.y + (row0 + t0) * a.ldy + c;
-    const int n = (int)(t1 - t0);
-    Pack<T, V> in[U], next[U];
-    auto fetch = [&](int t) {
+    __shared__ Pack<T, V> rows[S][U][kNT];
+    auto fetch = [&](int t) {  // the group from token t on
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < n) next[u] = *reinterpret_cast<const Pack<T, V>*>(x + (int64_t)(t + u) * a.ldx);
+            if (t + u < n) copy_async<T, V>(rows[t / U % S][u][threadIdx.x].e, x + (int64_t)(t + u) * a.ldx);
+        copy_commit();
     };
-    fetch(0);
+    constexpr int NP = Chan<V>::NP;
+    f2 w[K][NP], bias[NP], win[K][NP];
+    SeqAt q;
+#pragma unroll
+    for (int g = 0; g < S; ++g) fetch(g * U);  // on their way while the taps are
+    if (in_range) {
+        q = seq_at(a.seqs, b, t0);
+        load_window<T, K, V>(a, q, row0, t0, c, win);
+    }
+    taps.fill(a, c0);
+    if (!in_range) return;
+    load_taps<K, V>(taps, tx, w, bias);
     int change = (int)min64(q.end - t0, n);  // where the next sequence begins
     for (int t = 0; t < n; t += U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) in[u] = next[u];
-        fetch(t + U);
+        copy_wait<S - 1>();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= n) break;
@@ -127,21 +171,23 @@ __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t
                 load_window<T, K, V>(a, q, row0, t0 + t + u, c, win);
                 change = (int)min64(q.end - t0, n);
             }
-            float o[V];
-            in[u].get(win[K - 1]);
+            f2 o[NP];
+            Chan<V>::get(rows[t / U % S][u][threadIdx.x], win[K - 1]);
+            taps_of<K, NP>(w, bias, win, o);
+            if (silu) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float p = bias[i];
+                for (int i = 0; i < NP; ++i) o[i] = mul2(o[i], sigm2<is_fast<T>()>(o[i]));
+            }
 #pragma unroll
-                for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-                o[i] = silu ? p * sigm<is_fast<T>()>(p) : p;
+            for (int i = 0; i < NP; ++i)
 #pragma unroll
                 for (int j = 0; j + 1 < K; ++j) win[j][i] = win[j + 1][i];
-            }
-            Vec<V>::st(y, o);
+            Chan<V>::st(y, o);
             y += a.ldy;
         }
+        fetch(t + S * U);
     }
+    copy_wait<0>();
 }
 
 // One token a sequence: the state's K - 1 rows are read, moved up by one and written back.
@@ -155,12 +201,13 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a, int64_
     const bool in = b < a.B && c < a.C;
     const int64_t slot = !in ? -1 : a.slots != nullptr ? a.slots[b] : b;
     const bool live = slot >= 0 && slot < a.nslots;
-    float w[K][V], bias[V], win[K][V], o[V];
+    constexpr int NP = Chan<V>::NP;
+    f2 w[K][NP], bias[NP], win[K][NP], o[NP];
     T* st = (T*)a.state + slot * (K - 1) * a.C + c;
     if (live) {
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) Vec<V>::ld(st + j * a.C, win[j]);
-        Vec<V>::ld((const T*)a.x + b * a.ldx + c, win[K - 1]);
+        for (int j = 0; j < K - 1; ++j) Chan<V>::ld(st + j * a.C, win[j]);
+        Chan<V>::ld((const T*)a.x + b * a.ldx + c, win[K - 1]);
     }
     taps.fill(a, c0);
     if (!in) return;
@@ -168,21 +215,19 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a, int64_
     if (!live) {
         if (slot >= 0) report(a.header, LIZARD_ERR_INVALID_ARG, 33);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = 0.0f;
-        Vec<V>::st(y, o);
+        for (int i = 0; i < NP; ++i) o[i] = 0;
+        Chan<V>::st(y, o);
         return;
     }
     load_taps<K, V>(taps, tx, w, bias);
+    taps_of<K, NP>(w, bias, win, o);
+    if (silu) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float p = bias[i];
-#pragma unroll
-        for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-        o[i] = silu ? p * sigm<is_fast<T>()>(p) : p;
+        for (int i = 0; i < NP; ++i) o[i] = mul2(o[i], sigm2<is_fast<T>()>(o[i]));
     }
-    Vec<V>::st(y, o);
+    Chan<V>::st(y, o);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) Vec<V>::st(st + j * a.C, win[j + 1]);
+    for (int j = 0; j < K - 1; ++j) Chan<V>::st(st + j * a.C, win[j + 1]);
 }
 
 // Backward, one thread: V channels, the tokens [t0, t1) of a run.  Walking forward, token t gives
@@ -193,127 +238,132 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a, int64_
 // token.
 template <typename T, int K, int V>
 __global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
-    constexpr int U = 4;
+    constexpr int U = 4, S = 2;  // rows a group, groups on their way
     const bool silu = a.act == LIZARD_ACT_SILU;
     __shared__ Taps<K, V> taps;
     const int tx = threadIdx.x % TX;
     const int64_t c0 = blockIdx.x % cbs * (TX * V), c = c0 + tx * V;
     const int64_t rr = blockIdx.x / cbs * TY + threadIdx.x / TX, b = rr / runs;
     check_offsets(a.seqs, a.header);
-    taps.fill(a, c0);
-    if (rr >= a.B * runs || c >= a.C) return;
+    const bool in_range = rr < a.B * runs && c < a.C;
     const int64_t t0 = rr % runs * run, row0 = b * a.seqs.L;
     const int n = (int)min64(run, a.seqs.L - t0);
-    float w[K][V], bias[V], win[K][V], acc[K][V], dw[K][V], db[V];
-    load_taps<K, V>(taps, tx, w, bias);
+    constexpr int NP = Chan<V>::NP;
+    f2 w[K][NP], bias[NP], win[K][NP], acc[K][NP], dw[K][NP], db[NP];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.0f;
+    for (int i = 0; i < NP; ++i) {
+        db[i] = 0;
 #pragma unroll
-        for (int j = 0; j < K; ++j) dw[j][i] = acc[j][i] = 0.0f;
+        for (int j = 0; j < K; ++j) dw[j][i] = acc[j][i] = 0;
     }
     // tokens count from t0 from here on; a begin before -K and an end past n + K count as those
     const T* x = (const T*)a.x + (row0 + t0) * a.ldx + c;
     const T* dy = (const T*)a.dy + (row0 + t0) * a.ldy + c;
     T* dx = (T*)a.dx + (row0 + t0) * a.lddx + c;
     SeqAt q;
-    int begin, end;
+    int begin = 0, end = 0, lim = 0;  // lim: end of the tokens walked of this sequence
+    __shared__ Pack<T, V> rows[S][2][U][kNT];
+    int groups = 0;  // fetched so far
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < lim) {
+                copy_async<T, V>(rows[groups % S][0][u][threadIdx.x].e, x + (t + u) * a.ldx);
+                copy_async<T, V>(rows[groups % S][1][u][threadIdx.x].e, dy + (t + u) * a.ldy);
+            }
+        copy_commit();
+        ++groups;
+    };
     auto enter = [&](int t) {
         q = seq_at(a.seqs, b, t0 + t);
         begin = (int)max64(q.begin - t0, -K);
         end = (int)min64(q.end - t0, n + K);
+        lim = min(end, n + K - 1);
+#pragma unroll
+        for (int g = 0; g < S; ++g) fetch(t + g * U);
         load_window<T, K, V>(a, q, row0, t0 + t, c, win);
     };
-    enter(0);
+    if (in_range) enter(0);  // on their way while the taps are
+    taps.fill(a, c0);
+    if (!in_range) return;
+    load_taps<K, V>(taps, tx, w, bias);
     // the gradient of token u (or of a place before the sequence's first token)
-    auto put = [&](int u, const float* v) {
+    auto put = [&](int u, const f2* v) {
         if (u >= begin) {
-            if (u >= 0 && u < n) Vec<V>::st(dx + u * a.lddx, v);
+            if (u >= 0 && u < n) Chan<V>::st(dx + u * a.lddx, v);
         } else if (a.dstate_in != nullptr && begin >= 0 && begin < n) {
-            Vec<V>::st((T*)a.dstate_in + (q.seq * (K - 1) + (K - 1) + u - begin) * a.C + c, v);
+            Chan<V>::st((T*)a.dstate_in + (q.seq * (K - 1) + (K - 1) + u - begin) * a.C + c, v);
         }
     };
     int t = 0;
     while (true) {
-        const int lim = min(end, n + K - 1);
-        Pack<T, V> in[U], g[U], nin[U], ng[U];  // the next U tokens are on their way
-        auto fetch = [&](int t) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < lim) {
-                    nin[u] = *reinterpret_cast<const Pack<T, V>*>(x + (t + u) * a.ldx);
-                    ng[u] = *reinterpret_cast<const Pack<T, V>*>(dy + (t + u) * a.ldy);
-                }
-        };
-        fetch(t);
 #pragma unroll 1
         for (; t < lim; t += U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                in[u] = nin[u];
-                g[u] = ng[u];
-            }
-            fetch(t + U);
+            copy_wait<S - 1>();
+            const int at = groups % S;  // the oldest group
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t + u >= lim) break;
-                float gy[V];
-                in[u].get(win[K - 1]);
-                g[u].get(gy);
-                const float own = t + u < n ? 1.0f : 0.0f;  // the halo belongs to the next run
+                f2 dp[NP];
+                Chan<V>::get(rows[at][0][u][threadIdx.x], win[K - 1]);
+                Chan<V>::get(rows[at][1][u][threadIdx.x], dp);
+                if (silu) {
+                    f2 p[NP];
+                    taps_of<K, NP>(w, bias, win, p);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float dp = gy[i];
-                    if (silu) {
-                        float p = bias[i];
+                    for (int i = 0; i < NP; ++i) dp[i] = mul2(dp[i], dsilu2(p[i], sigm2<is_fast<T>()>(p[i])));
+                }
 #pragma unroll
-                        for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-                        dp *= dsilu(p, sigm<is_fast<T>()>(p));
-                    }
-                    const float od = own * dp;
-                    db[i] += od;
+                for (int i = 0; i < NP; ++i)
 #pragma unroll
-                    for (int j = 0; j < K; ++j) {
-                        dw[j][i] = fmaf(od, win[j][i], dw[j][i]);
-                        acc[j][i] = fmaf(w[j][i], dp, acc[j][i]);
+                    for (int j = 0; j < K; ++j) acc[j][i] = fma2(w[j][i], dp[i], acc[j][i]);
+                if (t + u < n) {  // the halo belongs to the next run
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        db[i] = add2(db[i], dp[i]);
+#pragma unroll
+                        for (int j = 0; j < K; ++j) dw[j][i] = fma2(dp[i], win[j][i], dw[j][i]);
                     }
                 }
                 put(t + u - (K - 1), acc[0]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
+                for (int i = 0; i < NP; ++i) {
 #pragma unroll
                     for (int j = 0; j + 1 < K; ++j) {
                         acc[j][i] = acc[j + 1][i];
                         win[j][i] = win[j + 1][i];
                     }
-                    acc[K - 1][i] = 0.0f;
+                    acc[K - 1][i] = 0;
                 }
             }
+            fetch(t + S * U);
         }
         t = lim;
         if (t == end) {  // the sequence's last K - 1 places: no later token adds to them
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 if (a.dstate_out != nullptr) {
-                    float d[V];
-                    Vec<V>::ld((const T*)a.dstate_out + (q.seq * (K - 1) + j) * a.C + c, d);
+                    f2 d[NP];
+                    Chan<V>::ld((const T*)a.dstate_out + (q.seq * (K - 1) + j) * a.C + c, d);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[j][i] += d[i];
+                    for (int i = 0; i < NP; ++i) acc[j][i] = add2(acc[j][i], d[i]);
                 }
                 put(t - (K - 1) + j, acc[j]);
             }
         }
         if (t >= n) break;
+        copy_wait<0>();
         enter(t);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < NP; ++i)
 #pragma unroll
-            for (int j = 0; j < K; ++j) acc[j][i] = 0.0f;
+            for (int j = 0; j < K; ++j) acc[j][i] = 0;
     }
+    copy_wait<0>();
     float* p = a.partial + rr * (K + 1) * a.C + c;  // [K + 1, C]
 #pragma unroll
-    for (int j = 0; j < K; ++j) Vec<V>::st(p + j * a.C, dw[j]);
-    Vec<V>::st(p + K * a.C, db);
+    for (int j = 0; j < K; ++j) Chan<V>::st(p + j * a.C, dw[j]);
+    Chan<V>::st(p + K * a.C, db);
 }
 
 // dw [C, K] and dbias [C] from the runs' sums [n, K + 1, C]: 32 channels a CTA, eight threads a

@@ -10,46 +10,6 @@ constexpr int NT = 128;      // threads a CTA
 constexpr int CK = 16;       // tokens between the states kept for the backward
 constexpr int SEG = 64;      // segments are whole multiples of this many tokens
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Two fp32 values in a register pair, and the paired instructions on them.  One issue slot does
-// two operations; measured, a pair takes 2.1 cycles of a scheduler with up to two operands of its
-// own and 3.1 with three, against 1.03 for each single fused multiply-add, so that pairs cost the
-// same multiplier time and leave slots for the loads, exponentials and shuffles between them.
-typedef uint64_t f2;
-__device__ __forceinline__ f2 pack(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack(f2 v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 exp2_2(f2 v) {
-    float a, b;
-    unpack(v, a, b);
-    return pack(ex2(a), ex2(b));
-}
 // The decays exp(d A) of two states, A2 = A log2(e).  ex2.approx errs downwards: by 2e-8 of the
 // result on average over exponents from -1 to -0.01, 1.7e-8 to -0.001, 0.6e-8 above (2^24
 // arguments each).  A state that remembers a thousand tokens multiplies a thousand of them, so the
@@ -57,21 +17,9 @@ __device__ __forceinline__ f2 exp2_2(f2 v) {
 // bits falls from 1.9e-6 to 0.9e-6 on 8 x 2048 tokens, of the last states from 4.5e-7 to 2.5e-7
 // on 8192.
 __device__ __forceinline__ f2 decay2(f2 d, f2 A2) { return exp2_2(fma2(d, A2, pack(2e-8f, 2e-8f))); }
-__device__ __forceinline__ float sum2(f2 v) {
-    float a, b;
-    unpack(v, a, b);
-    return a + b;
-}
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-// 1 / x of a value from 1 on, within one ulp (0 from 2^126 on)
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| <= 1, and log1p(u) = 2 atanh(s) with
@@ -95,21 +43,6 @@ __device__ __forceinline__ float softplus_(float v) {
     float x, y;
     unpack(softplus2(pack(v, 0.0f)), x, y);
     return x;
-}
-
-// sigmoid of two values.  As sigm: the fast form where bf16's step hides its error of a few
-// 2^-23, the exact one for fp32.
-template <bool FAST>
-__device__ __forceinline__ f2 sigm2(f2 v) {
-    float x, y;
-    if constexpr (FAST) {
-        unpack(mul2(v, pack(-kLog2e, -kLog2e)), x, y);
-        unpack(add2(pack(ex2(x), ex2(y)), pack(1.0f, 1.0f)), x, y);
-        return pack(rcp(x), rcp(y));
-    } else {
-        unpack(v, x, y);
-        return pack(sigm<false>(x), sigm<false>(y));
-    }
 }
 
 // Eight storage elements in registers.

@@ -398,10 +398,8 @@ __global__ void __launch_bounds__(NT, LPC > 2 ? 4 : 2) scan_bwd_kernel(const Sca
                     float c0, c1;
                     unpack(sm.e[o0], c0, x);
                     unpack(sm.e[o1], c1, x);
-                    // silu' = sg + z sg (1 - sg)
-                    const f2 zs = mul2(fz[j], sg), ds = fma2(zs, fma2(sg, pack(-1.0f, -1.0f), pack(1.0f, 1.0f)), sg);
-                    oz[j] = mul2(mul2(fy[j], fma2(D, fx[j], pack(c0, c1))), ds);
-                    e = mul2(e, zs);
+                    oz[j] = mul2(mul2(fy[j], fma2(D, fx[j], pack(c0, c1))), dsilu2(fz[j], sg));
+                    e = mul2(e, mul2(fz[j], sg));
                 }
                 ox[j] = fma2(d, gb, mul2(D, e));
                 // qa was summed with A log2(e)

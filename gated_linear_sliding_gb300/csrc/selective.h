@@ -135,19 +135,121 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
     __device__ __forceinline__ void get(float* f) const { Vec<V>::ld(e, f); }
 };
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Two fp32 values in a register pair, and the paired instructions on them.  One issue slot does
+// two operations; measured, a pair takes 2.1 cycles of a scheduler with up to two operands of its
+// own and 3.1 with three, against 1.03 for each single fused multiply-add, so that pairs cost the
+// same multiplier time and leave slots for the loads, exponentials and shuffles between them.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pack(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 exp2_2(f2 v) {
+    float a, b;
+    unpack(v, a, b);
+    return pack(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    unpack(v, a, b);
+    return a + b;
+}
+
+// 1 / x of a value from 1 on, within one ulp (0 from 2^126 on)
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // sigmoid(v), and the derivative of v sigmoid(v) given it.  The fp32 path divides, takes expf and
-// never e^|v|, which overflows where the sigmoid is still a number; the bf16 path takes the fast
-// exponential and division, whose error (a few 2^-23) is far below bf16's step.
+// never e^|v|, which overflows where the sigmoid is still a number; the bf16 path takes the
+// hardware's exponential and reciprocal, whose error (a few 2^-23) is far below bf16's step.
 template <bool FAST>
 __device__ __forceinline__ float sigm(float v) {
-    if constexpr (FAST) return __fdividef(1.0f, 1.0f + __expf(-v));
+    if constexpr (FAST) return rcp(1.0f + ex2(-kLog2e * v));
     const float e = expf(-fabsf(v));
     return (v >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 __device__ __forceinline__ float dsilu(float v, float sg) { return sg * fmaf(v, 1.0f - sg, 1.0f); }
 
+// The same for two values, and the derivative of v sigmoid(v) given the sigmoid.
+template <bool FAST>
+__device__ __forceinline__ f2 sigm2(f2 v) {
+    float x, y;
+    if constexpr (FAST) {
+        unpack(mul2(v, pack(-kLog2e, -kLog2e)), x, y);
+        unpack(add2(pack(ex2(x), ex2(y)), pack(1.0f, 1.0f)), x, y);
+        return pack(rcp(x), rcp(y));
+    } else {
+        unpack(v, x, y);
+        return pack(sigm<false>(x), sigm<false>(y));
+    }
+}
+__device__ __forceinline__ f2 dsilu2(f2 v, f2 sg) {
+    const f2 one = pack(1.0f, 1.0f), less = fma2(sg, pack(-1.0f, -1.0f), one);
+    return fma2(mul2(v, sg), less, sg);
+}
+// V consecutive elements as V / 2 pairs, for V of 2 or more.
+template <typename T, int V>
+__device__ __forceinline__ void get2(const Pack<T, V>& p, f2* f) {
+    float v[V];
+    p.get(v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = pack(v[2 * i], v[2 * i + 1]);
+}
+
 template <typename T>
 constexpr bool is_fast() { return sizeof(T) == 2; }
+
+// A thread's own copy of V elements from global to shared memory, asynchronous where its size
+// allows it (4, 8, 16 or 32 bytes): rows ahead wait in shared memory and not in registers, and
+// since each thread reads back only what it copied, waiting for its own copies is enough.
+template <typename T, int V>
+__device__ __forceinline__ void copy_async(T* to, const T* from) {
+    constexpr int bytes = sizeof(T) * V;
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (bytes == 32) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s + 16), "l"((const char*)from + 16) : "memory");
+    } else if constexpr (bytes == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    } else if constexpr (bytes >= 4) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(bytes) : "memory");
+    } else {
+        *to = *from;
+    }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most LEFT of the thread's committed groups are under way.
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 struct ConvArgs {
     int64_t B, C;
@@ -214,6 +316,7 @@ struct NormArgs {
     void *d_o, *dgate, *dr;
     float *dw_post, *dscale, *dw_pre;
     float* partial;  // backward: [CTAs, 3, D]
+    size_t group_bytes;  // set by the launch: shared memory of the group sums
 };
 int64_t norm_bwd_ctas(int64_t T, int64_t D);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s);
