@@ -147,17 +147,17 @@ struct Cols {
 template <typename T, int V, int TPR, int NV, bool ON>
 struct Ahead {
     T* at;  // [nvec V]
-    __device__ __forceinline__ void fetch(const T* row, int lr, int nvec) const {
+    __device__ __forceinline__ void fetch(const T* row, int lr, int nvec, size_t offset = 0) const {
         if constexpr (ON) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TPR + lr) * V;
-                if (i * TPR + lr < nvec) copy_async<T, V>(at + c, row + c);
+                if (i * TPR + lr < nvec) copy_async<T, V>((T*)((char*)at + offset) + c, row + c);
             }
         }
     }
-    __device__ __forceinline__ void get(const T* row, int lr, int nvec, f2* f) const {
-        Cols<V, TPR, NV>::ld(ON ? at : row, lr, nvec, f);
+    __device__ __forceinline__ void get(const T* row, int lr, int nvec, f2* f, size_t offset = 0) const {
+        Cols<V, TPR, NV>::ld(ON ? (const T*)((const char*)at + offset) : row, lr, nvec, f);
     }
 };
 
@@ -268,15 +268,17 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 768 ? 768 / (TPR 
     copy_wait<0>();
 }
 
-// One CTA walks rows b, b + grid, ...  The parameter gradients of a thread's columns are summed in
-// shared memory (the widest rows: in the CTA's partial sums themselves), in the thread's own
-// places, and leave once.  Sixteen columns a thread: with fewer the sums over the row cost more
-// than the row's arithmetic (four columns: 402 us on 16384 x 4096).
-template <typename T, typename R, int V, int TPR, int NV>
+// One CTA walks rows b, b + grid, ...  The parameter gradients of a thread's columns are summed as
+// the rows go by and leave once.  HOLD (rows up to 4096 columns, eight a thread): the parameters
+// and their sums stay in registers, and two rows are on their way in shared memory.  Otherwise
+// sixteen columns a thread, the sums in shared memory (the widest rows: in the CTA's partial sums
+// themselves), in the thread's own places, the parameters read again for each row.
+template <typename T, typename R, int V, int TPR, int NV, bool HOLD>
 __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kernel(const NormArgs a) {
     using C = Cols<V, TPR, NV>;
     constexpr int NP = C::NP;
-    constexpr bool ON = rows_ahead<T, V, TPR>();
+    constexpr bool ON = HOLD || rows_ahead<T, V, TPR>();
+    constexpr int S = HOLD ? 2 : 1;  // rows on their way
     constexpr bool FAST = is_fast<T>();
     __shared__ float red[2][2][32];
     // [3][D] up to kSumsWidth columns, the group sums' space, the row ahead
@@ -284,15 +286,41 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
     const int lr = threadIdx.x;
     const int D = (int)a.D, nvec = D / V, gv = nvec / (int)a.groups;
     float* partial = a.partial + (int64_t)blockIdx.x * 3 * D;
-    const bool near = D <= kSumsWidth;
+    const bool near = !HOLD && D <= kSumsWidth;
     float *sums = near ? gsm : partial, *gspace = near ? gsm + 3 * D : gsm;
-    {
-        f2 zero[NP];
+    f2 held[3][HOLD ? NP : 1], param[3][HOLD ? NP : 1];  // sums of, and w_post, scale, w_pre
+    const float* const params[3] = {a.w_post, a.scale, a.w_pre};
 #pragma unroll
-        for (int k = 0; k < NP; ++k) zero[k] = 0;
-        for (int m = 0; m < 3; ++m) C::st(sums + m * D, lr, nvec, zero);
+    for (int m = 0; m < 3; ++m) {
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) held[m][k] = 0;
+            if (params[m] != nullptr) C::ld(params[m], lr, nvec, param[m]);
+        } else {
+            f2 zero[NP];
+#pragma unroll
+            for (int k = 0; k < NP; ++k) zero[k] = 0;
+            C::st(sums + m * D, lr, nvec, zero);
+        }
     }
-    auto add_to = [&](int m, const f2* v) {
+    auto get_param = [&](auto m, f2* w) {
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) w[k] = param[decltype(m)::value][k];
+        } else {
+            C::ld(params[decltype(m)::value], lr, nvec, w);
+        }
+    };
+    using W0 = std::integral_constant<int, 0>;  // w_post
+    using W1 = std::integral_constant<int, 1>;  // scale
+    using W2 = std::integral_constant<int, 2>;  // w_pre
+    auto add_to = [&](auto mm, const f2* v) {
+        constexpr int m = decltype(mm)::value;
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) held[m][k] = add2(held[m][k], v[k]);
+            return;
+        }
         f2 s[NP];
         C::ld(sums + m * D, lr, nvec, s);
 #pragma unroll
@@ -302,35 +330,41 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
     const bool gate = a.gate != nullptr, gfirst = gate && a.gate_first, glast = gate && !a.gate_first;
     const float ginv = 1.0f / (float)(gv * V), dinv = 1.0f / (float)D;
     char* ahead = (char*)gspace + a.group_bytes;
+    const size_t row_bytes = (size_t)D * (3 * sizeof(T) + 2 * sizeof(R));
     const Ahead<R, V, TPR, NV, ON> ad{(R*)ahead}, ar{ad.at + D};
     const Ahead<T, V, TPR, NV, ON> ao{(T*)(ar.at + D)}, ag{ao.at + D}, an{ag.at + D};
-    auto fetch = [&](int64_t row) {  // two groups: what a row begins with, and what comes later
+    // two groups of a row: what it begins with, and what comes later
+    auto fetch = [&](int64_t row, int slot) {
         if (row < a.T) {
-            ao.fetch((const T*)a.o + row * a.ldo, lr, nvec);
-            if (gate) ag.fetch((const T*)a.gate + row * a.ldg, lr, nvec);
+            ao.fetch((const T*)a.o + row * a.ldo, lr, nvec, slot * row_bytes);
+            if (gate) ag.fetch((const T*)a.gate + row * a.ldg, lr, nvec, slot * row_bytes);
         }
         copy_commit();
     };
-    auto fetch_later = [&](int64_t row) {
+    auto fetch_later = [&](int64_t row, int slot) {
         if (row < a.T) {
-            if (a.dr_out != nullptr) ad.fetch((const R*)a.dr_out + row * a.ldro, lr, nvec);
+            if (a.dr_out != nullptr) ad.fetch((const R*)a.dr_out + row * a.ldro, lr, nvec, slot * row_bytes);
             if (a.w_pre != nullptr) {
-                if (a.r != nullptr) ar.fetch((const R*)a.r + row * a.ldr, lr, nvec);
-                an.fetch((const T*)a.dn_out + row * a.ldn, lr, nvec);
+                if (a.r != nullptr) ar.fetch((const R*)a.r + row * a.ldr, lr, nvec, slot * row_bytes);
+                an.fetch((const T*)a.dn_out + row * a.ldn, lr, nvec, slot * row_bytes);
             }
         }
         copy_commit();
     };
-    fetch(blockIdx.x);
-    fetch_later(blockIdx.x);
+    const int64_t next = (int64_t)gridDim.x * S;  // from a row to the one its place is for next
+    for (int k = 0; k < S; ++k) {
+        fetch(blockIdx.x + (int64_t)k * gridDim.x, k);
+        fetch_later(blockIdx.x + (int64_t)k * gridDim.x, k);
+    }
+    int slot = 0;
     int buf = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         // u: the normalised row (the plain one without a norm); ga, gd: act(gate), its derivative
         f2 u[NP], ga[NP], gd[NP], dr[NP], w[NP];
-        copy_wait<1>();
-        ao.get((const T*)a.o + row * a.ldo, lr, nvec, u);
-        if (gate) ag.get((const T*)a.gate + row * a.ldg, lr, nvec, ga);
-        fetch(row + gridDim.x);
+        copy_wait<2 * S - 1>();
+        ao.get((const T*)a.o + row * a.ldo, lr, nvec, u, slot * row_bytes);
+        if (gate) ag.get((const T*)a.gate + row * a.ldg, lr, nvec, ga, slot * row_bytes);
+        fetch(row + next, slot);
         if (gate) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
@@ -369,9 +403,9 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
             for (int k = 0; k < NP; ++k) u[k] = mul2(u[k], C::at(rs, k));
         }
         // the gradient of rr
-        copy_wait<1>();
+        copy_wait<2 * S - 1>();
         if (a.dr_out != nullptr) {
-            ad.get((const R*)a.dr_out + row * a.ldro, lr, nvec, dr);
+            ad.get((const R*)a.dr_out + row * a.ldro, lr, nvec, dr, slot * row_bytes);
         } else {
 #pragma unroll
             for (int k = 0; k < NP; ++k) dr[k] = 0;
@@ -379,7 +413,7 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
         // what the block adds to the residual, before its scale, times f
         auto added = [&](const f2* f, f2* n) {
             if (a.w_post != nullptr) {
-                C::ld(a.w_post, lr, nvec, n);
+                get_param(W0(), n);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) n[k] = mul2(n[k], mul2(u[k], f[k]));
             } else {
@@ -394,19 +428,19 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
         if (a.w_pre != nullptr) {
             f2 rr[NP], dn[NP];
             if (a.scale != nullptr) {
-                C::ld(a.scale, lr, nvec, w);
+                get_param(W1(), w);
             } else {
 #pragma unroll
                 for (int k = 0; k < NP; ++k) w[k] = pack(1.0f, 1.0f);
             }
             added(w, rr);
             if (a.r != nullptr) {
-                ar.get((const R*)a.r + row * a.ldr, lr, nvec, w);
+                ar.get((const R*)a.r + row * a.ldr, lr, nvec, w, slot * row_bytes);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) rr[k] = add2(rr[k], w[k]);
             }
-            an.get((const T*)a.dn_out + row * a.ldn, lr, nvec, dn);
-            C::ld(a.w_pre, lr, nvec, w);
+            an.get((const T*)a.dn_out + row * a.ldn, lr, nvec, dn, slot * row_bytes);
+            get_param(W2(), w);
 #pragma unroll
             for (int k = 0; k < NP; ++k) w[k] = mul2(w[k], dn[k]);
             float all[2] = {dot_of<NP>(rr, rr), dot_of<NP>(w, rr)};
@@ -418,21 +452,22 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
                 dr[k] = fma2(fma2(rr[k], pack(c, c), w[k]), pack(rp, rp), dr[k]);
                 dn[k] = mul2(dn[k], mul2(rr[k], pack(rp, rp)));
             }
-            add_to(2, dn);
+            add_to(W2(), dn);
         }
-        fetch_later(row + gridDim.x);
+        fetch_later(row + next, slot);
+        if (S > 1) slot ^= 1;
         if (a.dr != nullptr) C::st((R*)a.dr + row * a.lddr, lr, nvec, dr);
         f2 t[NP];
         if (a.scale != nullptr) {
             added(dr, t);
-            add_to(1, t);
-            C::ld(a.scale, lr, nvec, w);
+            add_to(W1(), t);
+            get_param(W1(), w);
 #pragma unroll
             for (int k = 0; k < NP; ++k) dr[k] = mul2(dr[k], w[k]);
         }
         if (glast) {
             if (a.w_post != nullptr) {
-                C::ld(a.w_post, lr, nvec, t);
+                get_param(W0(), t);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) t[k] = mul2(t[k], u[k]);
             } else {
@@ -449,8 +484,8 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
         if (a.w_post != nullptr) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) t[k] = mul2(dr[k], u[k]);
-            add_to(0, t);
-            C::ld(a.w_post, lr, nvec, w);
+            add_to(W0(), t);
+            get_param(W0(), w);
 #pragma unroll
             for (int k = 0; k < NP; ++k) dr[k] = mul2(dr[k], w[k]);
             float dot[NV];
@@ -480,7 +515,10 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
         C::st((T*)a.d_o + row * a.lddo, lr, nvec, dr);
     }
     copy_wait<0>();
-    if (near) {
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int m = 0; m < 3; ++m) C::st(partial + m * D, lr, nvec, held[m]);
+    } else if (near) {
         f2 s[NP];
         for (int m = 0; m < 3; ++m) {
             C::ld(sums + m * D, lr, nvec, s);
@@ -539,14 +577,17 @@ cudaError_t fwd_go(NormArgs a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename T, typename R, int V, int TPR, int NV>
+template <typename T, typename R, int V, int TPR, int NV, bool HOLD = false>
 cudaError_t bwd_go(NormArgs a, cudaStream_t s) {
     a.group_bytes = group_bytes(a, V);
-    const size_t sm = sizeof(float) * (a.D <= kSumsWidth ? 3 * (size_t)a.D : 0) + a.group_bytes +
-                      (rows_ahead<T, V, TPR>() ? (size_t)a.D * (3 * sizeof(T) + 2 * sizeof(R)) : 0);
-    const cudaError_t e = group_smem(norm_bwd_kernel<T, R, V, TPR, NV>, sm);
+    const size_t row = (size_t)a.D * (3 * sizeof(T) + 2 * sizeof(R));
+    const size_t sm = a.group_bytes + (HOLD ? 2 * row
+                                            : sizeof(float) * (a.D <= kSumsWidth ? 3 * (size_t)a.D : 0) +
+                                                  (rows_ahead<T, V, TPR>() ? row : 0));
+    const auto kernel = norm_bwd_kernel<T, R, V, TPR, NV, HOLD>;
+    const cudaError_t e = group_smem(kernel, sm);
     if (e != cudaSuccess) return e;
-    norm_bwd_kernel<T, R, V, TPR, NV><<<(unsigned)norm_bwd_ctas(a.T, a.D), TPR, sm, s>>>(a);
+    kernel<<<(unsigned)norm_bwd_ctas(a.T, a.D), TPR, sm, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -575,10 +616,10 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
                     a.lddg % 8 == 0 && a.lddr % 8 == 0;
     cudaError_t e;
     if (v8) {
-        if (a.D <= 512) e = bwd_go<T, R, 8, 32, 2>(a, s);
-        else if (a.D <= 1024) e = bwd_go<T, R, 8, 64, 2>(a, s);
-        else if (a.D <= 2048) e = bwd_go<T, R, 8, 128, 2>(a, s);
-        else if (a.D <= 4096) e = bwd_go<T, R, 8, 256, 2>(a, s);
+        if (a.D <= 512) e = bwd_go<T, R, 8, 64, 1, true>(a, s);
+        else if (a.D <= 1024) e = bwd_go<T, R, 8, 128, 1, true>(a, s);
+        else if (a.D <= 2048) e = bwd_go<T, R, 8, 256, 1, true>(a, s);
+        else if (a.D <= 4096) e = bwd_go<T, R, 8, 512, 1, true>(a, s);
         else if (a.D <= 8192) e = bwd_go<T, R, 8, 512, 2>(a, s);
         else e = bwd_go<T, R, 8, 1024, 2>(a, s);
     } else {
@@ -594,8 +635,8 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
 }  // namespace
 
 int64_t norm_bwd_ctas(int64_t T, int64_t D) {
-    // 512 threads a SM, sixteen columns a thread
-    const int64_t most = 152 * (D <= 512 ? 16 : D <= 1024 ? 8 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1);
+    // 512 threads a SM, eight columns a thread
+    const int64_t most = 152 * (D <= 512 ? 8 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1);
     return T < 1 ? 1 : T < most ? T : most;
 }
 
