@@ -86,9 +86,9 @@ __global__ void __launch_bounds__(NT, 4) scan_fwd_kernel(const ScanArgs a, const
     }
 
     // staging: one piece of eight channels of one token
-    const bool vec = C % 8 == 0 && (C / a.G) % 8 == 0 && a.ldx % 8 == 0 && a.lddt % 8 == 0 &&
-                     a.ldz % 8 == 0 && a.ldy % 8 == 0;
-    const bool vecb = N % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0;
+    const int64_t cg = C / a.G;
+    const bool vec = rows16<T>(cg, a.ldx) && rows16<T>(cg, a.lddt) && rows16<T>(cg, a.ldz) && rows16<T>(cg, a.ldy);
+    const bool vecb = rows16<T>(N, a.ldb) && rows16<T>(N, a.ldc);
     const int pv = tid % NV, pt = tid / NV;
     const bool stages = pt < TT;
     const int64_t pch = w.c0 + pv * 8;

@@ -60,15 +60,15 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = make_uint4(0, 0, 0, 0);
     }
-    // n (0..8) elements at p, zeros after them; vec: p is 16-byte aligned and n is 0 or 8
+    // n (0..8) elements at p, zeros after them; vec: p is 16-byte aligned
     __device__ __forceinline__ void load(const T* p, int n, bool vec) {
-        if (vec) {
-            if (n > 0) {
+        if (vec && n == 8) {
 #pragma unroll
-                for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-            } else {
-                zero();
-            }
+            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+            return;
+        }
+        if (n <= 0) {
+            zero();
             return;
         }
         T e[8];
@@ -98,8 +98,8 @@ __device__ __forceinline__ void store8(T* p, const f2* v, int n, bool vec) {
     float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack(v[i], f[2 * i], f[2 * i + 1]);
-    if (vec) {
-        if (n > 0) Vec<8>::st(p, f);
+    if (vec && n == 8) {
+        Vec<8>::st(p, f);
         return;
     }
 #pragma unroll
@@ -218,6 +218,14 @@ __device__ __forceinline__ int spread_sum(float* v, int lane, int at = 0) {
 }
 // How many values spread_sum leaves: U over the lanes' number, at least one.
 constexpr int spread_left(int U, int lanes) { return U > lanes ? U / lanes : 1; }
+
+// Whether rows of this width and distance keep 16-byte alignment at every eighth element (of each
+// of their groups).
+template <typename T>
+__device__ __forceinline__ bool rows16(int64_t width, int64_t ld) {
+    constexpr int E = 16 / sizeof(T);
+    return width % E == 0 && ld % E == 0;
+}
 
 // How a call is cut into CTAs: blocks of channels (none across two groups) x segments of the
 // time axis x rows of the batch.

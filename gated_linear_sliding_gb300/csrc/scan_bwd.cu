@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(NT, LPC > 2 ? 4 : 2) scan_bwd_kernel(const Sca
     if (t1 == sq.end) load_state(seq_state(a.dh_out, sq.seq), gn);
     else load_state(rec_g + (w.b * cut.segs + w.seg) * C * N, gn);
 
-    const bool vec = C % 8 == 0 && (C / a.G) % 8 == 0 && a.ldx % 8 == 0 && a.lddt % 8 == 0 &&
-                     a.ldz % 8 == 0 && a.ldy % 8 == 0 && a.lddx % 8 == 0 && a.ldddt % 8 == 0 &&
-                     a.lddz % 8 == 0;
-    const bool vecb = N % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0;
+    const int64_t cg = C / a.G;
+    const bool vec = rows16<T>(cg, a.ldx) && rows16<T>(cg, a.lddt) && rows16<T>(cg, a.ldz) && rows16<T>(cg, a.ldy) &&
+                     rows16<T>(cg, a.lddx) && rows16<T>(cg, a.ldddt) && rows16<T>(cg, a.lddz);
+    const bool vecb = rows16<T>(N, a.ldb) && rows16<T>(N, a.ldc);
     const int pv = tid % NV, pt = tid / NV;
     const int64_t pch = w.c0 + pv * 8;
     const int pn = (int)max64(0, min64(8, w.clim - pch));
@@ -487,8 +487,9 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
         }
     }
     const SeqAt sq = seq_at(a.seqs, w.b, t0);
-    const bool vec = C % 8 == 0 && (C / a.G) % 8 == 0 && a.lddt % 8 == 0 && a.ldz % 8 == 0 && a.ldy % 8 == 0;
-    const bool vecb = N % 8 == 0 && a.ldc % 8 == 0;
+    const int64_t cg = C / a.G;
+    const bool vec = rows16<T>(cg, a.lddt) && rows16<T>(cg, a.ldz) && rows16<T>(cg, a.ldy);
+    const bool vecb = rows16<T>(N, a.ldc);
     const int pv = tid % NV, pt = tid / NV;
     const int64_t pch = w.c0 + pv * 8;
     const int pn = (int)max64(0, min64(8, w.clim - pch));
