@@ -4,8 +4,13 @@
 //   u = o [act(gate)],  n = w_post u / rms_group(u),  n [act(gate)],  rr = r + scale n,
 //   r_out = rr,  n_out = w_pre rr / rms(rr)
 //
-// Bound by HBM: each row is read once into registers (V neighbouring columns a piece, NV pieces a
-// thread), the sums of squares are reduced inside the CTA, and both outputs leave from registers.
+// Bound by HBM: each row is read once (V neighbouring columns a piece, NV pieces a thread), the sums
+// of squares are reduced inside the CTA, and both outputs leave from registers.  16384 x 4096 bf16
+// with gate, residual and both norms: 133 us, 5.05 TB/s; without the next row on its way 153 us; the
+// norm over 32 heads with its gate, 8192 x 4096: 38 us, 5.3 TB/s.  Backward of the former: 286 us,
+// 3.75 TB/s: one row at a time a SM, three sums over the row, each with a barrier, between its loads
+// and its stores; with the parameters read again for each row and their sums in shared memory
+// 366 us, with four columns a thread 402 us.
 #include <type_traits>
 
 #include "selective.h"

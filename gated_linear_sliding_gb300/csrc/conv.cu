@@ -125,8 +125,10 @@ __global__ void __launch_bounds__(kNT) conv_tail_kernel(const ConvArgs a) {
     }
 }
 
-// One thread: V channels, `run` tokens of one row of the batch.  Bound by HBM: x is read and y
-// written once; the next U rows are on their way while U are computed.
+// One thread: V channels, `run` tokens of one row of the batch.  x is read and y written once;
+// bound by HBM with the instruction issue close behind (20 instructions an element).  8 x 2048 x
+// 4096 bf16, K = 4: 53 us, 5.05 TB/s.  With the rows ahead in registers (104 of them, 20 warps a
+// SM) 96 us: the loads in flight were too few; taps read by each thread from global memory 161 us.
 template <typename T, int K, int V>
 __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
     constexpr int U = 8, S = 2;  // rows a group, groups on their way
@@ -235,7 +237,8 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a, int64_
 // those sums, and the oldest is complete once t has been added.  The walk goes K - 1 tokens past
 // the run (or to the sequence's end) to complete the run's own last tokens.  Places before a
 // sequence's first token are its state, whose gradient is written by the run that holds that
-// token.
+// token.  8 x 2048 x 4096 bf16, K = 4: 105 us for x, dy and dx, 3.8 TB/s; 36 instructions an element
+// on 122 registers (16 warps a SM) share the bound with HBM.
 template <typename T, int K, int V>
 __global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
     constexpr int U = 4, S = 2;  // rows a group, groups on their way

@@ -3,10 +3,19 @@
 //   h[t, c, n] = exp(d A[c, n]) h[t-1, c, n] + d x[t, c] Bm[t, n],   d = softplus(dt + bias)
 //   y[t, c]    = (sum_n Cm[t, n] h[t, c, n] + D[c] x[t, c]) silu(z[t, c])
 //
-// Four lanes (N = 16) share a channel, four states each in registers; a CTA of 128 threads walks
-// its channels through a segment of the time axis, a tile of 32 tokens at a time: the tile's step sizes and
-// d x are computed once and put into shared memory with Bm and Cm in fp32, while the next tile's
-// rows are already on their way into registers.
+// Two lanes (N = 16) share a channel, eight states each in registers; a CTA of 128 threads walks its
+// channels through a segment of the time axis, a tile of tokens at a time: the tile's step sizes
+// and d x are computed once and put into shared memory with Bm and Cm in fp32, while the next
+// tile's rows are already on their way into registers.
+//
+// The floor is the exponentials: one for each token, channel and state, 32 a cycle and SM (57 us
+// for 8192 x 4096 x 16; the bytes take 40 us).  An element takes nine instruction slots: the
+// exponential, two products, two multiply-adds (paired, half a slot each), a quarter each of four
+// loads from shared memory and its share of the staging (softplus, gate, conversions: 25 slots a
+// token and channel).  8 x 2048 x 4096 x 16 bf16: 445 us at 56% of the issue slots, no pipe above
+// 60%: the warps wait for one another's shared-memory loads and for the fixed latency of dependent
+// instructions; more warps with fewer registers, exponentials ahead by a group of tokens, tiles by
+// asynchronous copies, and single instead of paired arithmetic all measured the same or slower.
 #include <type_traits>
 
 #include "scan.cuh"
