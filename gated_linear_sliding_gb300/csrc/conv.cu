@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kNT) conv_tail_kernel(const ConvArgs a) {
 // bound by HBM with the instruction issue close behind (20 instructions an element).  8 x 2048 x
 // 4096 bf16, K = 4: 53 us, 5.05 TB/s.  With the rows ahead in registers (104 of them, 20 warps a
 // SM) 96 us: the loads in flight were too few; taps read by each thread from global memory 161 us.
-template <typename T, int K, int V>
+template <typename T, int K, int V, bool STATES>
 __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
     constexpr int U = 8, S = 2;  // rows a group, groups on their way
     const bool silu = a.act == LIZARD_ACT_SILU;
@@ -162,6 +162,11 @@ __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t
     taps.fill(a, c0);
     if (!in_range) return;
     load_taps<K, V>(taps, tx, w, bias);
+    // the window after a sequence's last token is what its state holds then
+    auto put_state = [&]() {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) Chan<V>::st((T*)a.state_out + (q.seq * (K - 1) + j) * a.C + c, win[j]);
+    };
     int change = (int)min64(q.end - t0, n);  // where the next sequence begins
     for (int t = 0; t < n; t += U) {
         copy_wait<S - 1>();
@@ -190,6 +195,7 @@ __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t
         fetch(t + S * U);
     }
     copy_wait<0>();
+    if (STATES && t0 + n == q.end) put_state();
 }
 
 // One token a sequence: the state's K - 1 rows are read, moved up by one and written back.
@@ -427,11 +433,12 @@ unsigned blocks_for(int64_t n) { return (unsigned)((n + kNT - 1) / kNT); }
 
 bool rows_of(int64_t ld, int64_t width, int64_t v) { return ld % v == 0 && width % v == 0; }
 
-// Tokens a thread walks: long runs read little halo, short ones fill the GPU (152 SMs, 2048
-// threads each) on small batches.
+// Tokens a thread walks: long runs read little halo and begin seldom (8 x 2048 x 4096, backward with
+// its sums: 64 tokens 117 us, 128 109 us, 256 119 us), short ones fill the GPU on small batches.
+constexpr int kFwdRun = 128, kBwdRun = 128;
 int run_tokens(int64_t B, int64_t L, int64_t nv, int longest) {
     int run = longest;
-    while (run > 8 && B * ((L + run - 1) / run) * nv < 152 * 1024) run /= 2;
+    while (run > 8 && B * ((L + run - 1) / run) * nv < 152 * 512) run /= 2;
     return run;
 }
 
@@ -447,13 +454,18 @@ cudaError_t conv_fwd(const ConvArgs& a, cudaStream_t s) {
     const int64_t nv = a.C / V;
     return with_taps(a.K, [&](auto kk) {
         constexpr int K = decltype(kk)::value;
+        // The pass over the rows writes a dense batch's states too, unless they are those that its
+        // other threads begin with; sequences of a packed batch may be empty, and meet no pass.
+        const bool states = K > 1 && a.state_out != nullptr && a.state_out != a.state_in &&
+                            a.seqs.cu == nullptr && a.seqs.L > 0;
         if (a.seqs.L > 0) {
-            const int run = run_tokens(a.B, a.seqs.L, nv, 32);
+            const int run = run_tokens(a.B, a.seqs.L, nv, kFwdRun);
             const int64_t runs = (a.seqs.L + run - 1) / run;
             const int64_t cbs = (nv + TX - 1) / TX;
-            conv_fwd_kernel<T, K, V><<<(unsigned)(cbs * ((a.B * runs + TY - 1) / TY)), kNT, 0, s>>>(a, runs, run, cbs);
+            const auto kernel = states ? conv_fwd_kernel<T, K, V, true> : conv_fwd_kernel<T, K, V, false>;
+            kernel<<<(unsigned)(cbs * ((a.B * runs + TY - 1) / TY)), kNT, 0, s>>>(a, runs, run, cbs);
         }
-        if (K > 1 && a.state_out != nullptr)
+        if (K > 1 && a.state_out != nullptr && !states)
             conv_tail_kernel<T, K, V><<<blocks_for(a.nstate * nv), kNT, 0, s>>>(a);
         return cudaGetLastError();
     });
@@ -469,7 +481,6 @@ cudaError_t conv_step(const ConvArgs& a, cudaStream_t s) {
     });
 }
 
-constexpr int kBwdRun = 64;
 int bwd_run(int64_t B, int64_t L, int64_t C) { return run_tokens(B, L, (C + 3) / 4, kBwdRun); }
 
 template <typename T, int V>

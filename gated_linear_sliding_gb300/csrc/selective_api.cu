@@ -76,7 +76,7 @@ bool conv_args(const lizard_conv_dims* d, bool step, ConvArgs* a) {
 
 // CTAs of 128 threads of the largest conv launch, at one channel and eight tokens a thread.
 bool conv_grid_ok(const ConvArgs& a) {
-    return grid_ok(((double)a.B * (double)(a.seqs.L / 8 + 1) * (double)a.C) / 128 + 1) &&
+    return grid_ok(((double)a.C / 32 + 1) * ((double)a.B * (double)(a.seqs.L / 8 + 1) / 4 + 1)) &&
            grid_ok((double)a.nstate * (double)a.C * a.K / 128 + 1);
 }
 
