@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kNT) conv_tail_kernel(const ConvArgs a) {
 
 // One thread: V channels, `run` tokens of one row of the batch.  x is read and y written once;
 // bound by HBM with the instruction issue close behind (20 instructions an element).  8 x 2048 x
-// 4096 bf16, K = 4: 53 us, 5.05 TB/s.  With the rows ahead in registers (104 of them, 20 warps a
+// 4096 bf16, K = 4: 52 us, 5.15 TB/s.  With the rows ahead in registers (104 of them, 20 warps a
 // SM) 96 us: the loads in flight were too few; taps read by each thread from global memory 161 us.
 template <typename T, int K, int V, bool STATES>
 __global__ void __launch_bounds__(kNT) conv_fwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(const ConvArgs a, int64_
 // those sums, and the oldest is complete once t has been added.  The walk goes K - 1 tokens past
 // the run (or to the sequence's end) to complete the run's own last tokens.  Places before a
 // sequence's first token are its state, whose gradient is written by the run that holds that
-// token.  8 x 2048 x 4096 bf16, K = 4: 105 us for x, dy and dx, 3.8 TB/s; 36 instructions an element
+// token.  8 x 2048 x 4096 bf16, K = 4: 102 us for x, dy and dx, 3.95 TB/s; 36 instructions an element
 // on 122 registers (16 warps a SM) share the bound with HBM.
 template <typename T, int K, int V>
 __global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t runs, int run, int64_t cbs) {
@@ -455,7 +455,7 @@ cudaError_t conv_fwd(const ConvArgs& a, cudaStream_t s) {
     return with_taps(a.K, [&](auto kk) {
         constexpr int K = decltype(kk)::value;
         // The pass over the rows writes a dense batch's states too, unless they are those that its
-        // other threads begin with; sequences of a packed batch may be empty, and meet no pass.
+        // other threads begin with; a packed batch's sequences may be empty, and no thread's.
         const bool states = K > 1 && a.state_out != nullptr && a.state_out != a.state_in &&
                             a.seqs.cu == nullptr && a.seqs.L > 0;
         if (a.seqs.L > 0) {
