@@ -532,27 +532,16 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
     }
 }
 
-// dw_post, dscale and dw_pre from the CTAs' partial sums [n][3][D], each added in the same order.
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const NormArgs a, int64_t n) {
-    // 32 columns a CTA, eight threads a column: thread k adds partials k, k + 8, ..., then the
-    // eight are added in order
-    __shared__ float part[8][33];
-    const int col = threadIdx.x & 31, k = threadIdx.x >> 5, m = blockIdx.y;
+// dw_post, dscale and dw_pre from the CTAs' partial sums [n][3][D].
+template <int KT>
+__global__ void __launch_bounds__(32 * KT) norm_bwd_sum_kernel(const NormArgs a, int64_t n) {
+    const int m = blockIdx.y;
     float* out = m == 0 ? a.dw_post : m == 1 ? a.dscale : a.dw_pre;
     if (out == nullptr) return;
-    const int64_t i = (int64_t)blockIdx.x * 32 + col;
-    float s = 0.0f;
-    if (i < a.D) {
-#pragma unroll 8
-        for (int64_t p = k; p < n; p += 8) s += a.partial[(p * 3 + m) * a.D + i];
-    }
-    part[k][col] = s;
-    __syncthreads();
-    if (k == 0 && i < a.D) {
-#pragma unroll
-        for (int j = 1; j < 8; ++j) s += part[j][col];
-        out[i] = s;
-    }
+    const int64_t i0 = (int64_t)blockIdx.x * 32;
+    sum_columns<KT>(
+        n, (int)min64(32, a.D - i0), [&](int64_t p, int i) { return a.partial[(p * 3 + m) * a.D + i0 + i]; },
+        [&](int i, float s) { out[i0 + i] = s; });
 }
 
 template <typename K>
@@ -633,7 +622,10 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
         else e = bwd_go<T, R, 1, 1024, 16>(a, s);
     }
     if (e != cudaSuccess) return e;
-    norm_bwd_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 3), 256, 0, s>>>(a, norm_bwd_ctas(a.T, a.D));
+    const int64_t n = norm_bwd_ctas(a.T, a.D);
+    const dim3 g((unsigned)((a.D + 31) / 32), 3);
+    if (many_partials(n, 3 * (int64_t)g.x)) norm_bwd_sum_kernel<32><<<g, 1024, 0, s>>>(a, n);
+    else norm_bwd_sum_kernel<8><<<g, 256, 0, s>>>(a, n);
     return cudaGetLastError();
 }
 

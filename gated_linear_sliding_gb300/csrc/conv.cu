@@ -375,25 +375,17 @@ __global__ void __launch_bounds__(kNT) conv_bwd_kernel(const ConvArgs a, int64_t
     Chan<V>::st(p + K * a.C, db);
 }
 
-// dw [C, K] and dbias [C] from the runs' sums [n, K + 1, C]: 32 channels a CTA, eight threads a
-// channel; thread k adds runs k, k + 8, ..., then the eight are added in order.
-__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const ConvArgs a, int64_t n) {
-    __shared__ float part[8][33];
-    const int col = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + col, count = (a.K + 1) * a.C;
-    float s = 0.0f;
-    if (i < count) {
-#pragma unroll 8
-        for (int64_t p = k; p < n; p += 8) s += a.partial[p * count + i];
-    }
-    part[k][col] = s;
-    __syncthreads();
-    if (k != 0 || i >= count) return;
-#pragma unroll
-    for (int j = 1; j < 8; ++j) s += part[j][col];
-    const int64_t j = i / a.C, c = i % a.C;
-    if (j < a.K) a.dw[c * a.K + j] = s;
-    else if (a.dbias != nullptr) a.dbias[c] = s;
+// dw [C, K] and dbias [C] from the runs' sums [n, K + 1, C].
+template <int KT>
+__global__ void __launch_bounds__(32 * KT) conv_bwd_sum_kernel(const ConvArgs a, int64_t n) {
+    const int64_t i0 = (int64_t)blockIdx.x * 32, count = (a.K + 1) * a.C;
+    sum_columns<KT>(
+        n, (int)min64(32, count - i0), [&](int64_t p, int i) { return a.partial[p * count + i0 + i]; },
+        [&](int i, float s) {
+            const int64_t j = (i0 + i) / a.C, c = (i0 + i) % a.C;
+            if (j < a.K) a.dw[c * a.K + j] = s;
+            else if (a.dbias != nullptr) a.dbias[c] = s;
+        });
 }
 
 // Sequences without tokens pass the gradient of their state on.
@@ -407,26 +399,13 @@ __global__ void __launch_bounds__(kNT) conv_bwd_empty_kernel(const ConvArgs a) {
     st((T*)a.dstate_in + id, g != nullptr ? ld(g + id) : 0.0f);
 }
 
-__global__ void __launch_bounds__(256) sum_partials_kernel(const float* in, int64_t n,
-                                                           int64_t stride, float* out,
-                                                           int64_t count) {
-    // 32 columns a CTA, eight threads a column: thread k adds partials k, k + 8, ..., then the
-    // eight are added in order
-    __shared__ float part[8][33];
-    const int col = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + col;
-    float s = 0.0f;
-    if (i < count) {
-#pragma unroll 4
-        for (int64_t p = k; p < n; p += 8) s += in[p * stride + i];
-    }
-    part[k][col] = s;
-    __syncthreads();
-    if (k == 0 && i < count) {
-#pragma unroll
-        for (int j = 1; j < 8; ++j) s += part[j][col];
-        out[i] = s;
-    }
+template <int KT>
+__global__ void __launch_bounds__(32 * KT) sum_partials_kernel(const float* in, int64_t n, int64_t stride, float* out,
+                                                               int64_t count) {
+    const int64_t i0 = (int64_t)blockIdx.x * 32;
+    sum_columns<KT>(
+        n, (int)min64(32, count - i0), [&](int64_t p, int i) { return in[p * stride + i0 + i]; },
+        [&](int i, float s) { out[i0 + i] = s; });
 }
 
 unsigned blocks_for(int64_t n) { return (unsigned)((n + kNT - 1) / kNT); }
@@ -438,7 +417,8 @@ bool rows_of(int64_t ld, int64_t width, int64_t v) { return ld % v == 0 && width
 constexpr int kFwdRun = 128, kBwdRun = 128;
 int run_tokens(int64_t B, int64_t L, int64_t nv, int longest) {
     int run = longest;
-    while (run > 8 && B * ((L + run - 1) / run) * nv < 152 * 512) run /= 2;
+    const int64_t warps = (nv + TX - 1) / TX;  // of a run
+    while (run > 8 && B * ((L + run - 1) / run) * warps < 152 * 16) run /= 2;
     return run;
 }
 
@@ -502,7 +482,9 @@ cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    conv_bwd_sum_kernel<<<(unsigned)(((a.K + 1) * a.C + 31) / 32), 256, 0, s>>>(a, a.B * runs);
+    const unsigned g = (unsigned)(((a.K + 1) * a.C + 31) / 32);
+    if (many_partials(a.B * runs, g)) conv_bwd_sum_kernel<32><<<g, 1024, 0, s>>>(a, a.B * runs);
+    else conv_bwd_sum_kernel<8><<<g, 256, 0, s>>>(a, a.B * runs);
     return cudaGetLastError();
 }
 
@@ -510,7 +492,9 @@ cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
 
 cudaError_t launch_sum_partials(const float* in, int64_t n, int64_t stride, float* out,
                                 int64_t count, cudaStream_t s) {
-    sum_partials_kernel<<<(unsigned)((count + 31) / 32), 256, 0, s>>>(in, n, stride, out, count);
+    const unsigned g = (unsigned)((count + 31) / 32);
+    if (many_partials(n, g)) sum_partials_kernel<32><<<g, 1024, 0, s>>>(in, n, stride, out, count);
+    else sum_partials_kernel<8><<<g, 256, 0, s>>>(in, n, stride, out, count);
     return cudaGetLastError();
 }
 
