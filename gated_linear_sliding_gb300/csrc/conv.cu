@@ -399,15 +399,6 @@ __global__ void __launch_bounds__(kNT) conv_bwd_empty_kernel(const ConvArgs a) {
     st((T*)a.dstate_in + id, g != nullptr ? ld(g + id) : 0.0f);
 }
 
-template <int KT>
-__global__ void __launch_bounds__(32 * KT) sum_partials_kernel(const float* in, int64_t n, int64_t stride, float* out,
-                                                               int64_t count) {
-    const int64_t i0 = (int64_t)blockIdx.x * 32;
-    sum_columns<KT>(
-        n, (int)min64(32, count - i0), [&](int64_t p, int i) { return in[p * stride + i0 + i]; },
-        [&](int i, float s) { out[i0 + i] = s; });
-}
-
 unsigned blocks_for(int64_t n) { return (unsigned)((n + kNT - 1) / kNT); }
 
 bool rows_of(int64_t ld, int64_t width, int64_t v) { return ld % v == 0 && width % v == 0; }
@@ -489,14 +480,6 @@ cudaError_t conv_bwd(const ConvArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
-
-cudaError_t launch_sum_partials(const float* in, int64_t n, int64_t stride, float* out,
-                                int64_t count, cudaStream_t s) {
-    const unsigned g = (unsigned)((count + 31) / 32);
-    if (many_partials(n, g)) sum_partials_kernel<32><<<g, 1024, 0, s>>>(in, n, stride, out, count);
-    else sum_partials_kernel<8><<<g, 256, 0, s>>>(in, n, stride, out, count);
-    return cudaGetLastError();
-}
 
 int64_t conv_bwd_runs(int64_t B, int64_t L, int64_t C) {
     const int run = bwd_run(B, L, C);

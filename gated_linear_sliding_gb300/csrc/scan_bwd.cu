@@ -67,8 +67,8 @@ struct Smem {
 
 template <typename T, int LPC>
 __global__ void __launch_bounds__(NT, LPC > 2 ? 4 : 2) scan_bwd_kernel(const ScanArgs a, const Cut cut,
-                                                      const float* rec_g, float* pbc, float* pA,
-                                                      float* pD, float* pbias) {
+                                                      const float* rec_g, float* pbc, float* pparam,
+                                                      int64_t param_stride) {
     using L = Lay<LPC>;
     using P = typename L::P;
     constexpr int CPT = L::CPT, LC = L::LC, CH = L::CH, NP = L::NP, NV = L::NV, PX = L::PX, PB = L::PB;
@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(NT, LPC > 2 ? 4 : 2) scan_bwd_kernel(const Sca
     for (int k = 0; k < CPT; ++k)
 #pragma unroll
         for (int i = 0; i < H; ++i) tA[k][i] = sm.dA[k * H + i][tid];
-    put_state(pA + part * C * N, tA);
+    float* pp = pparam + part * param_stride;  // dA [C, N], dD [C], ddt_bias [C]
+    put_state(pp, tA);
     __syncthreads();
     float* red = reinterpret_cast<float*>(smraw);  // [warps][2][CH]
     {
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(NT, LPC > 2 ? 4 : 2) scan_bwd_kernel(const Sca
         if (w.c0 + c >= w.clim) continue;
         float s = 0.0f;
         for (int k = 0; k < NT / 32; ++k) s += red[(k * 2 + m) * CH + c];
-        (m == 0 ? pD : pbias)[part * C + w.c0 + c] = s;
+        pp[C * N + m * C + w.c0 + c] = s;
     }
 }
 
@@ -617,6 +618,23 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, int64_t 
     else st((T*)a.dCm + row * a.lddc + g * a.N + n, s);
 }
 
+// dA, dD and ddt_bias from the CTAs' parts [n][stride].
+template <int KT>
+__global__ void __launch_bounds__(32 * KT) scan_param_kernel(const ScanArgs a, int64_t n, const float* in, int64_t stride) {
+    const int64_t i0 = (int64_t)blockIdx.x * 32, CN = a.C * a.N;
+    sum_columns<KT>(
+        n, (int)min64(32, CN + 2 * a.C - i0), [&](int64_t p, int i) { return in[p * stride + i0 + i]; },
+        [&](int k, float s) {
+            const int64_t i = i0 + k;
+            if (i < CN) a.dA[i] = s;
+            else if (i < CN + a.C) {
+                if (a.dD != nullptr) a.dD[i - CN] = s;
+            } else if (a.ddt_bias != nullptr) {
+                a.ddt_bias[i - CN - a.C] = s;
+            }
+        });
+}
+
 __global__ void __launch_bounds__(256) scan_bwd_empty_kernel(const ScanArgs a) {
     const int64_t CN = a.C * a.N, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >= a.nstate * CN) return;
@@ -649,7 +667,7 @@ Cut bwd_cut(const ScanArgs& a) {
 }
 
 struct BwdWs {
-    size_t rec_g, rec_d, bc, A, D, bias, total;
+    size_t rec_g, rec_d, bc, param, param_stride, total;
 };
 BwdWs bwd_ws(const ScanArgs& a, const Cut& k) {
     BwdWs o;
@@ -659,9 +677,8 @@ BwdWs bwd_ws(const ScanArgs& a, const Cut& k) {
     o.rec_g = at, at += k.segs > 1 ? up(parts * CN) : 0;
     o.rec_d = at, at += k.segs > 1 ? up(parts * a.C) : 0;
     o.bc = at, at += up((size_t)(k.cbg * a.B * a.seqs.L * a.G * 2 * a.N));
-    o.A = at, at += up(parts * CN);
-    o.D = at, at += up(parts * a.C);
-    o.bias = at, at += up(parts * a.C);
+    o.param_stride = up(CN + 2 * (size_t)a.C);
+    o.param = at, at += parts * o.param_stride;
     o.total = at;
     return o;
 }
@@ -688,18 +705,17 @@ cudaError_t scan_bwd(const ScanArgs& a, cudaStream_t s) {
             const int bytes = (int)sizeof(Smem<LPC>);
             cudaError_t r = cudaFuncSetAttribute(scan_bwd_kernel<T, LPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (r != cudaSuccess) return r;
-            scan_bwd_kernel<T, LPC><<<g, NT, bytes, s>>>(a, k, f + o.rec_g, f + o.bc, f + o.A, f + o.D, f + o.bias);
+            scan_bwd_kernel<T, LPC><<<g, NT, bytes, s>>>(a, k, f + o.rec_g, f + o.bc, f + o.param, (int64_t)o.param_stride);
             const int64_t n = a.B * a.seqs.L * a.G * 2 * a.N;
             scan_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, k.cbg, f + o.bc);
             return cudaGetLastError();
         });
         if (e != cudaSuccess) return e;
     }
-    e = launch_sum_partials(f + o.A, parts, CN, a.dA, CN, s);
-    if (e == cudaSuccess && a.dD != nullptr) e = launch_sum_partials(f + o.D, parts, a.C, a.dD, a.C, s);
-    if (e == cudaSuccess && a.ddt_bias != nullptr)
-        e = launch_sum_partials(f + o.bias, parts, a.C, a.ddt_bias, a.C, s);
-    return e;
+    const unsigned g = (unsigned)((CN + 2 * a.C + 31) / 32);
+    if (many_partials(parts, g)) scan_param_kernel<32><<<g, 1024, 0, s>>>(a, parts, f + o.param, o.param_stride);
+    else scan_param_kernel<8><<<g, 256, 0, s>>>(a, parts, f + o.param, o.param_stride);
+    return cudaGetLastError();
 }
 
 }  // namespace

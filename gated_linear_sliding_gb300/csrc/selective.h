@@ -349,8 +349,4 @@ int64_t norm_bwd_ctas(int64_t T, int64_t D);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
 
-// out[i] = sum over p < n of in[p * stride + i], i < count, in the order of p.
-cudaError_t launch_sum_partials(const float* in, int64_t n, int64_t stride, float* out,
-                                int64_t count, cudaStream_t s);
-
 }  // namespace lz
