@@ -827,14 +827,17 @@ def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=Non
     group = (B, L, dims.G, N)
     dims.ldy = _ld(dy, "dy", wide, tp)
 
-    def out(t, shape):
-        return torch.empty(shape, dtype=tp, device=x.device) if t is None else t
+    def out(t, name, shape):
+        return (x.new_empty(shape), 0) if t is None else (t, _ld(t, name, shape, tp))
 
-    dx, ddt, dBm, dCm = out(dx, wide), out(ddt, wide), out(dBm, group), out(dCm, group)
-    dz = None if z is None else out(dz, wide)
-    dims.lddx, dims.ldddt = _ld(dx, "dx", wide, tp), _ld(ddt, "ddt", wide, tp)
-    dims.lddz = 0 if dz is None else _ld(dz, "dz", wide, tp)
-    dims.lddb, dims.lddc = _ld(dBm, "dBm", group, tp), _ld(dCm, "dCm", group, tp)
+    dx, dims.lddx = out(dx, "dx", wide)
+    ddt, dims.ldddt = out(ddt, "ddt", wide)
+    dBm, dims.lddb = out(dBm, "dBm", group)
+    dCm, dims.lddc = out(dCm, "dCm", group)
+    if z is None:
+        dz = None
+    else:
+        dz, dims.lddz = out(dz, "dz", wide)
     dA = torch.empty_like(A)
     dD = None if D is None else torch.empty_like(D)
     ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
