@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(NT, 4) scan_fwd_kernel(const ScanArgs a, const
     __shared__ __align__(16) Smem<LPC, NS> sm;
     const Where<CH> w(a, cut);
     if (MAIN) check_offsets(a.seqs, a.header);
+    else if (w.seg + 1 == cut.segs) return;  // nothing follows the last segment
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane & (LPC - 1), lch = warp * LC + lane / LPC;
     const int N = (int)a.N, nn = max(0, min(NS, N - NS * q));  // this lane's states

@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(NT) scan_adj_kernel(const ScanArgs a, const Cu
     __shared__ __align__(16) f2 se[P::SIZE];  // (e, e)
     __shared__ __align__(16) f2 sc[CK][H * LPC];
     const Where<CH> w(a, cut);
+    if (w.seg == 0) return;  // nothing is before the first segment
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane & (LPC - 1), lch = warp * L::CW + lane / LPC;
     const int N = (int)a.N, nn = max(0, min(NS, N - NS * q));
@@ -593,8 +594,8 @@ __global__ void __launch_bounds__(256) scan_adj_join_kernel(const ScanArgs a, in
         float own[U], d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            own[u] = s >= u ? p[(s - u) * CN] : 0.0f;
-            d[u] = s >= u ? pd[(s - u) * a.C] : 0.0f;
+            own[u] = s > u ? p[(s - u) * CN] : 0.0f;  // the first segment's own is not needed
+            d[u] = s > u ? pd[(s - u) * a.C] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
