@@ -35,11 +35,27 @@ __device__ __forceinline__ void row_sum(float* v, float (*red)[32]) {
 #pragma unroll
             for (int k = 0; k < NVAL; ++k) red[k][warp] = v[k];
         __syncthreads();
+        constexpr int W = TPR / 32;
 #pragma unroll
         for (int k = 0; k < NVAL; ++k) {
-            v[k] = lane < TPR / 32 ? red[k][lane] : 0.0f;
+            if constexpr (W >= 4 && W <= 16) {  // broadcast loads and a tree: shorter than a second round of shuffles
+                f2 t[W / 2];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(~0u, v[k], o);
+                for (int i = 0; i < W / 4; ++i) {
+                    const float4 q = reinterpret_cast<const float4*>(red[k])[i];
+                    t[2 * i] = pack(q.x, q.y);
+                    t[2 * i + 1] = pack(q.z, q.w);
+                }
+#pragma unroll
+                for (int o = W / 4; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < o; ++i) t[i] = add2(t[i], t[i + o]);
+                v[k] = sum2(t[0]);
+            } else {
+                v[k] = lane < W ? red[k][lane] : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(~0u, v[k], o);
+            }
         }
     }
 }
@@ -186,7 +202,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 768 ? 768 / (TPR 
     using C = Cols<V, TPR, NV>;
     constexpr int NP = C::NP, RPC = TPR < 128 ? 128 / TPR : 1;
     constexpr bool FAST = is_fast<T>();
-    __shared__ float red[2][1][32];
+    __shared__ __align__(16) float red[2][1][32];
     extern __shared__ __align__(16) float gsm[];  // the group sums' space, then the rows ahead
     const int lr = threadIdx.x % TPR, rc = threadIdx.x / TPR;
     const int D = (int)a.D, nvec = D / V, gv = nvec / (int)a.groups;
@@ -285,7 +301,7 @@ __global__ void __launch_bounds__(TPR, TPR >= 512 ? 1 : 512 / TPR) norm_bwd_kern
     constexpr bool ON = HOLD || rows_ahead<T, V, TPR>();
     constexpr int S = HOLD ? 2 : 1;  // rows on their way
     constexpr bool FAST = is_fast<T>();
-    __shared__ float red[2][2][32];
+    __shared__ __align__(16) float red[2][2][32];
     // [3][D] up to kSumsWidth columns, the group sums' space, the row ahead
     extern __shared__ __align__(16) float gsm[];
     const int lr = threadIdx.x;
