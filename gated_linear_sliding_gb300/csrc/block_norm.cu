@@ -6,9 +6,9 @@
 //
 // Bound by HBM: each row is read once (V neighbouring columns a piece, NV pieces a thread), the sums
 // of squares are reduced inside the CTA, and both outputs leave from registers.  16384 x 4096 bf16
-// with gate, residual and both norms: 133 us, 5.05 TB/s; without the next row on its way 153 us; the
-// norm over 32 heads with its gate, 8192 x 4096: 38 us, 5.3 TB/s.  Backward of the former: 286 us,
-// 3.75 TB/s: one row at a time a SM, three sums over the row, each with a barrier, between its loads
+// with gate, residual and both norms: 129 us, 5.2 TB/s; without the next row on its way 153 us; the
+// norm over 32 heads with its gate, 8192 x 4096: 38 us, 5.3 TB/s.  Backward of the former: 283 us,
+// 3.8 TB/s: one row at a time a SM, three sums over the row, each with a barrier, between its loads
 // and its stores; with the parameters read again for each row and their sums in shared memory
 // 366 us, with four columns a thread 402 us.
 #include <type_traits>
