@@ -425,8 +425,10 @@ Cut fwd_cut(const ScanArgs& a) {
     return k;
 }
 
+// The segments' records, rounded up to 16 bytes: the copy of the first states after them is read in
+// pieces of four values.
 size_t rec_floats(const ScanArgs& a, const Cut& k) {
-    return k.segs > 1 ? (size_t)(a.B * k.segs * a.C) * (a.N + 1) : 0;
+    return k.segs > 1 ? ((size_t)(a.B * k.segs * a.C) * (a.N + 1) + 3) & ~(size_t)3 : 0;
 }
 
 template <typename T>

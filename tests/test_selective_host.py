@@ -1,0 +1,25 @@
+"""The selective block without a GPU: workspace layouts and what the binding checks and does before a
+launch."""
+import pytest
+
+from gated_linear_sliding_gb300 import _build
+from gated_linear_sliding_gb300 import lizard as lz
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return lz.load()
+
+
+@pytest.mark.parametrize("B,C,N,L", [(1, 1001, 16, 600), (1, 9, 4, 600), (3, 37, 8, 1500), (2, 5, 64, 700), (1, 7, 3, 400),
+                                     (1, 1000, 16, 600)])
+def test_copied_states_begin_on_16_bytes(lib, B, C, N, L):
+    """Where h_out is h0 and the time axis is cut, the states are copied to the workspace's end and
+    read from there in pieces of four values."""
+    d = lz.lizard_scan_dims(B=B, L=L, C=C, N=N, G=1, dtype=0, softplus=1)
+    ws = lz.lizard_scan_fwd_workspace(d)
+    assert ws > 256 + 4 * B * C * N  # cut into segments
+    assert (ws - 4 * B * C * N) % 16 == 0
