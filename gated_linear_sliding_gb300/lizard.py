@@ -880,6 +880,8 @@ def _norm_inputs(o, gate, r, w_post, scale, w_pre, res_dtype, groups, act, gate_
     shape, tp = tuple(o.shape), o.dtype
     if len(shape) != 2:
         raise ValueError("o must be [T, D]")
+    if res_dtype not in (tp, torch.float32):
+        raise ValueError(f"residual stream: dtype {res_dtype} is neither o's ({tp}) nor float32")
     D = shape[1]
     dims = lizard_norm_dims(shape[0], D, groups, _ld(o, "o", shape, tp, 1),
                             0 if gate is None else _ld(gate, "gate", shape, tp, 1),

@@ -23,3 +23,18 @@ def test_copied_states_begin_on_16_bytes(lib, B, C, N, L):
     ws = lz.lizard_scan_fwd_workspace(d)
     assert ws > 256 + 4 * B * C * N  # cut into segments
     assert (ws - 4 * B * C * N) % 16 == 0
+
+
+@pytest.mark.parametrize("dtype,res", [(torch.bfloat16, torch.float16), (torch.bfloat16, torch.float64),
+                                       (torch.bfloat16, torch.int16), (torch.float32, torch.bfloat16),
+                                       (torch.float32, torch.float64)])
+def test_residual_stream_of_another_type_is_refused(dtype, res):
+    """The library knows the residual stream as o's type or fp32; anything else would be read as one
+    of them."""
+    o, r = torch.zeros(3, 8, dtype=dtype), torch.zeros(3, 8, dtype=res)
+    for call in (lambda: lz.lizard_block_norm_fwd(o, r=r),
+                 lambda: lz.lizard_block_norm_fwd(o, r_out=r),
+                 lambda: lz.lizard_block_norm_bwd(o, r=r, dr_out=r),
+                 lambda: lz.lizard_block_norm_bwd(o, dr_out=r)):
+        with pytest.raises(ValueError, match="residual stream: dtype"):
+            call()
