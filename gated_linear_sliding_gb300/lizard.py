@@ -8,6 +8,7 @@ path.  If the library has not been built, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -584,13 +585,30 @@ def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=No
     return dx, dW
 
 
+def _on_stream(fn):
+    """Runs a call that is given a stream under it, so that what the call allocates (workspaces,
+    copies of offsets, outputs) belongs to that stream: memory of the current stream's pool may still
+    be in use there, and goes back to it while the kernels on the other stream run.  (The function's
+    own `stream` is for its signature.)"""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 # ---- the selective state space block -----------------------------------------------------
 #
 # Activations are [B, L, width] (dtype fp32 or bf16) and may be column ranges of wider rows: the
 # last axes contiguous, every token the same distance after the one before.  Parameters, scan
 # states and parameter gradients are fp32 and contiguous.  cu_seqlens packs sequences into one row
 # (B = 1): int64 offsets on the device, read when the kernels run, or host integers, which are
-# checked and copied.
+# checked and copied (the host waits for the copy).  What a call allocates belongs to the stream it
+# runs on: `stream`, or the current one.
 
 
 def _ld(t, name, shape, dtype, lead=2):
@@ -631,11 +649,9 @@ def _need_f32(t, name, shape):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_of(stream, t):
-    """Handle of `stream`, or of the current stream of t's device (without making the Stream
-    object, which costs as much as a launch)."""
-    if stream is not None:
-        return stream.cuda_stream
+def _stream_of(t):
+    """Handle of the current stream of t's device (without making the Stream object, which costs
+    as much as a launch)."""
     if _raw_stream is not None:
         return _raw_stream(t.device.index)
     return torch.cuda.current_stream(t.device).cuda_stream
@@ -678,6 +694,7 @@ def _slots(slots, B):
     return slots.data_ptr()
 
 
+@_on_stream
 def lizard_conv_fwd(x, w, bias=None, *, act: int = LIZARD_ACT_NONE, state_in=None, state_out=None,
                     cu_seqlens=None, y=None, workspace=None, stream=None):
     """Short causal depthwise convolution of x [B, L, C] with w [C, K]; returns y [B, L, C].
@@ -697,7 +714,7 @@ def lizard_conv_fwd(x, w, bias=None, *, act: int = LIZARD_ACT_NONE, state_in=Non
     st = load().lizard_conv_fwd(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
                                 _need_f32(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
                                 y.data_ptr(), _ptr(state_out), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _stream_of(stream, x))
+                                0 if workspace is None else workspace.numel(), _stream_of(x))
     _check(st, "lizard_conv_fwd")
     return y
 
@@ -706,6 +723,7 @@ def lizard_conv_bwd_workspace(dims) -> int:
     return int(load().lizard_conv_bwd_workspace(ctypes.byref(dims)))
 
 
+@_on_stream
 def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None,
                     dstate_out=None, dstate_in=None, cu_seqlens=None, dx=None, workspace=None,
                     stream=None):
@@ -730,11 +748,12 @@ def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None
                                 _need_f32(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
                                 dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dw.data_ptr(),
                                 _ptr(dbias), _ptr(dstate_in), workspace.data_ptr(),
-                                workspace.numel(), _stream_of(stream, x))
+                                workspace.numel(), _stream_of(x))
     _check(st, "lizard_conv_bwd")
     return dict(dx=dx, dw=dw, dbias=dbias, dstate_in=dstate_in)
 
 
+@_on_stream
 def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NONE, y=None,
                      workspace=None, stream=None):
     """One token for each of B sequences: y [B, C] from x [B, C]; state [slots, K-1, C] is moved
@@ -753,7 +772,7 @@ def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NON
     st = load().lizard_conv_step(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
                                  _need_f32(bias, "bias", (C,)), state.data_ptr(), state.shape[0],
                                  _slots(slots, B), y.data_ptr(), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream_of(stream, x))
+                                 0 if workspace is None else workspace.numel(), _stream_of(x))
     _check(st, "lizard_conv_step")
     return y
 
@@ -787,6 +806,7 @@ def lizard_scan_states_bytes(dims) -> int:
     return int(load().lizard_scan_states_bytes(ctypes.byref(dims)))
 
 
+@_on_stream
 def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus: bool = True,
                     h0=None, h_out=None, cu_seqlens=None, y=None, save_states: bool = False,
                     workspace=None, stream=None):
@@ -809,11 +829,12 @@ def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus:
     workspace = _scratch(workspace, lib.lizard_scan_fwd_workspace(ctypes.byref(dims)), x.device)
     st = lib.lizard_scan_fwd(ctypes.byref(dims), *ptrs, _need_f32(h0, "h0", shape), _ptr(cu),
                              y.data_ptr(), _need_f32(h_out, "h_out", shape), _ptr(states),
-                             workspace.data_ptr(), workspace.numel(), _stream_of(stream, x))
+                             workspace.data_ptr(), workspace.numel(), _stream_of(x))
     _check(st, "lizard_scan_fwd")
     return (y, states) if save_states else y
 
 
+@_on_stream
 def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=None,
                     softplus: bool = True, h0=None, dh_out=None, dh0=None, cu_seqlens=None,
                     dx=None, ddt=None, dz=None, dBm=None, dCm=None, workspace=None, stream=None):
@@ -850,11 +871,12 @@ def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=Non
                              _need_f32(dh_out, "dh_out", shape), dx.data_ptr(), ddt.data_ptr(),
                              _ptr(dz), dBm.data_ptr(), dCm.data_ptr(), dA.data_ptr(), _ptr(dD),
                              _ptr(ddt_bias), _need_f32(dh0, "dh0", shape), workspace.data_ptr(),
-                             workspace.numel(), _stream_of(stream, x))
+                             workspace.numel(), _stream_of(x))
     _check(st, "lizard_scan_bwd")
     return dict(dx=dx, ddt=ddt, dA=dA, dBm=dBm, dCm=dCm, dD=dD, dz=dz, ddt_bias=ddt_bias, dh0=dh0)
 
 
+@_on_stream
 def lizard_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None,
                      softplus: bool = True, slots=None, y=None, workspace=None, stream=None):
     """One token for each of B sequences: y [B, C] from x, dt, z [B, C] and Bm, Cm [B, G, N];
@@ -869,7 +891,7 @@ def lizard_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None,
     st = load().lizard_scan_step(ctypes.byref(dims), *ptrs,
                                  _need_f32(state, "state", (nslots, C, dims.N)), nslots,
                                  _slots(slots, B), y.data_ptr(), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream_of(stream, x))
+                                 0 if workspace is None else workspace.numel(), _stream_of(x))
     _check(st, "lizard_scan_step")
     return y
 
@@ -893,6 +915,7 @@ def _norm_inputs(o, gate, r, w_post, scale, w_pre, res_dtype, groups, act, gate_
                   _need_f32(scale, "scale", (D,)), _need_f32(w_pre, "w_pre", (D,)))
 
 
+@_on_stream
 def lizard_block_norm_fwd(o, *, gate=None, r=None, w_post=None, scale=None, w_pre=None,
                           groups: int = 1, act: int = LIZARD_ACT_SILU, gate_first: bool = False,
                           eps: float = 1e-5, eps_pre=None, r_out=None, n_out=None, stream=None):
@@ -915,7 +938,7 @@ def lizard_block_norm_fwd(o, *, gate=None, r=None, w_post=None, scale=None, w_pr
     else:
         dims.ldn = _ld(n_out, "n_out", shape, o.dtype, 1)
     st = load().lizard_block_norm_fwd(ctypes.byref(dims), *ptrs, r_out.data_ptr(), _ptr(n_out),
-                                      _stream_of(stream, o))
+                                      _stream_of(o))
     _check(st, "lizard_block_norm_fwd")
     return r_out, n_out
 
@@ -924,6 +947,7 @@ def lizard_block_norm_bwd_workspace(dims) -> int:
     return int(load().lizard_block_norm_bwd_workspace(ctypes.byref(dims)))
 
 
+@_on_stream
 def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_post=None,
                           scale=None, w_pre=None, groups: int = 1, act: int = LIZARD_ACT_SILU,
                           gate_first: bool = False, eps: float = 1e-5, eps_pre=None,
@@ -949,6 +973,6 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
     st = load().lizard_block_norm_bwd(ctypes.byref(dims), *ptrs, _ptr(dr_out), _ptr(dn_out),
                                       do.data_ptr(), _ptr(dgate), _ptr(dr), _ptr(dw_post),
                                       _ptr(dscale), _ptr(dw_pre), workspace.data_ptr(),
-                                      workspace.numel(), _stream_of(stream, o))
+                                      workspace.numel(), _stream_of(o))
     _check(st, "lizard_block_norm_bwd")
     return dict(do=do, dgate=dgate, dr=dr, dw_post=dw_post, dscale=dscale, dw_pre=dw_pre)

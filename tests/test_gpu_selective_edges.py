@@ -36,3 +36,119 @@ def test_scan_in_place_state_of_odd_channels(lz, B, L, C, N, lens):
     y2 = lz.lizard_scan_fwd(x, dt, A, Bm, Cm, h0=st, h_out=st, cu_seqlens=cu)
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(h, st)
+
+
+# ------------------------------------------------------------------------------------- streams
+
+
+def block_calls(lz, host=False):
+    """Each call of the block as f(**more) -> its outputs; the packed ones with offsets on the device or
+    as host integers."""
+    d = Draw(21, "bf16")
+    L, C, N = 640, 64, 16
+    cu = [0, 300, 640] if host else offsets([300, 340])
+    x, dt, dy = (d(1, L, C)[0] for _ in range(3))
+    Bm, Cm = d(1, L, 1, N)[0], d(1, L, 1, N)[0]
+    A = d.dev(-np.exp(d.rng.normal(size=(C, N))))[0]
+    w = d(C, 4, dtype=torch.float32)[0]
+    v = d(C, dtype=torch.float32)[0]
+    state, h = d(3, 3, C)[0], d(3, C, N, dtype=torch.float32)[0]
+    _, st = lz.lizard_scan_fwd(x, dt, A, Bm, Cm, cu_seqlens=cu, save_states=True)
+    rows, last = x[0], (x[0, :3], dt[0, :3], A, Bm[0, :3], Cm[0, :3])
+
+    kept = []
+
+    def own(t):  # a step's state, the caller's: made before the call and alive after it
+        kept.append(t.clone())
+        torch.cuda.current_stream().synchronize()
+        return kept[-1]
+
+    def flat(f):
+        def call(**more):
+            out = f(**more)
+            out = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,)
+            return [t for t in out if t is not None]
+        return call
+
+    return {k: flat(f) for k, f in dict(
+        conv_fwd=lambda **m: lz.lizard_conv_fwd(x, w, v, act=1, cu_seqlens=cu, **m),
+        conv_bwd=lambda **m: lz.lizard_conv_bwd(x, w, v, dy, act=1, cu_seqlens=cu, **m),
+        conv_step=lambda **m: lz.lizard_conv_step(rows[:3], w, v, own(state), act=1, **m),
+        scan_fwd=lambda **m: lz.lizard_scan_fwd(x, dt, A, Bm, Cm, cu_seqlens=cu, save_states=True, **m),
+        scan_bwd=lambda **m: lz.lizard_scan_bwd(x, dt, A, Bm, Cm, dy, st, cu_seqlens=cu, **m),
+        scan_step=lambda **m: lz.lizard_scan_step(*last, own(h), **m),
+        norm_fwd=lambda **m: lz.lizard_block_norm_fwd(rows, r=rows, w_post=v, w_pre=v, **m),
+        norm_bwd=lambda **m: lz.lizard_block_norm_bwd(rows, r=rows, w_post=v, w_pre=v, dr_out=rows, dn_out=rows, **m),
+    ).items()}
+
+
+CALLS = ["conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_memory_of_a_call_on_another_stream(lz, name):
+    """A call on another stream, which is still busy, takes no memory back to the current stream
+    before its kernels are done: neither does it see what is written there meanwhile, nor does it
+    write there."""
+    f = block_calls(lz)[name]
+    want = f()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    sizes = (512, 4096, 1 << 14, 1 << 16, 1 << 18, 1 << 20, 2 << 20, 5 << 20, 20 << 20)
+
+    def filled():
+        return [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(24 if n <= 1 << 16 else 4)]
+
+    # the streams' pools have blocks of these sizes from here on, and the kernels are loaded: nothing
+    # below makes the host wait
+    filled()
+    f(stream=s)
+    f()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # 0.1 s
+    got = f(stream=s)
+    fill = filled()
+    torch.cuda.current_stream().synchronize()
+    assert not s.query()  # the call's kernels are still to come
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+    assert all(bool((t == 0x5A).all()) for t in fill)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_of_a_call_on_another_stream(lz, name):
+    """A call on another stream writes no memory that pending work of the current stream still reads."""
+    f = block_calls(lz)[name]
+    want = f()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    keep = [torch.full(t.shape, 7, dtype=t.dtype, device="cuda") for t in want for _ in range(2)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    late = [t.clone() for t in keep]
+    del keep
+    got = f(stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in late)
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("name", ["conv_fwd", "conv_bwd", "scan_fwd", "scan_bwd"])
+def test_host_offsets_on_another_stream(lz, name):
+    """Offsets copied for a call on another stream (the host waits for the copy) are not overwritten by
+    the current stream."""
+    f = block_calls(lz, host=True)[name]
+    want = f()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = f(stream=s)
+        fill = [torch.full((3,), -1, dtype=torch.int64, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), i
+        del fill
