@@ -7,6 +7,7 @@ path.  If the library has not been built, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -190,6 +191,29 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _under(stream):
+    """Context in which `stream` (None: the current one) is the current stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _on_stream(fn):
+    """Runs a call that is given a stream under it, so that what the call allocates (workspaces,
+    copies of offsets, outputs) belongs to that stream: memory of the current stream's pool may still
+    be in use there, and goes back to it while the kernels on the other stream run.  (The function's
+    own `stream` is for its signature.)"""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with _under(stream):
+            return fn(*args, **kw)
+    return call
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return LIZARD_F32
@@ -242,8 +266,10 @@ def lizard_decode_workspace(dims: lizard_dims) -> int:
 
 
 def new_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
-    """Allocate a workspace (torch owns the memory) and zero its status word."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    """Allocate a workspace (torch owns the memory, which belongs to the stream) and zero its status
+    word."""
+    with _under(stream):
+        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     _check(load().lizard_workspace_init(_p(ws), ws.numel(), _stream(stream)),
            "lizard_workspace_init")
     return ws
@@ -284,6 +310,7 @@ def lizard_read_device_status(workspace: torch.Tensor, stream=None) -> int:
     return int(load().lizard_read_device_status(_p(workspace), _stream(stream)))
 
 
+@_on_stream
 def lizard_attn_fwd(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0, y=None, lse=None,
                     S_out=None, z_out=None, kcache_out=None, vcache_out=None, workspace=None,
                     stream=None, decay: int = LIZARD_DECAY_DELAYED):
@@ -326,6 +353,7 @@ def lizard_attn_fwd_varlen_workspace(dims, cu_seqlens) -> int:
     return int(load().lizard_attn_fwd_varlen_workspace(ctypes.byref(dims), cu.ctypes.data))
 
 
+@_on_stream
 def lizard_attn_fwd_varlen(q, k, v, g, Wf, sinks, w: int, cu_seqlens, *, scale: float = 0.0,
                            y=None, lse=None, S_out=None, z_out=None, kcache_out=None,
                            vcache_out=None, workspace=None, stream=None,
@@ -366,6 +394,7 @@ def lizard_attn_fwd_varlen(q, k, v, g, Wf, sinks, w: int, cu_seqlens, *, scale: 
     return y
 
 
+@_on_stream
 def lizard_attn_fwd_noalloc(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0, y=None,
                             lse=None, S_out=None, z_out=None, kcache_out=None, vcache_out=None,
                             stream=None, decay: int = LIZARD_DECAY_DELAYED):
@@ -394,6 +423,7 @@ def lizard_attn_fwd_noalloc(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0
     return y
 
 
+@_on_stream
 def lizard_attn_bwd(q, k, v, g, Wf, sinks, y, lse, dy, w: int, *, scale: float = 0.0,
                     dq=None, dk=None, dv=None, dg=None, dWf=None, dsinks=None, workspace=None,
                     stream=None, decay: int = LIZARD_DECAY_DELAYED):
@@ -431,6 +461,7 @@ def lizard_attn_bwd_varlen_workspace(dims, cu_seqlens) -> int:
     return int(load().lizard_attn_bwd_varlen_workspace(ctypes.byref(dims), cu.ctypes.data))
 
 
+@_on_stream
 def lizard_attn_bwd_varlen(q, k, v, g, Wf, sinks, y, lse, dy, w: int, cu_seqlens, *,
                            scale: float = 0.0, workspace=None, stream=None,
                            decay: int = LIZARD_DECAY_DELAYED):
@@ -482,6 +513,7 @@ def _decode_common(q, k, v, g, Wf, sinks, S, z, kcache, vcache, gcache, w, decay
     return B, Hq, Hkv, d, D, M
 
 
+@_on_stream
 def lizard_decode_step(pos: int, q, k, v, g, Wf, sinks, S, z, kcache, vcache, w: int, *,
                        scale: float = 0.0, y=None, workspace=None, stream=None, gcache=None,
                        decay: int = LIZARD_DECAY_DELAYED):
@@ -501,6 +533,7 @@ def lizard_decode_step(pos: int, q, k, v, g, Wf, sinks, S, z, kcache, vcache, w:
     return y
 
 
+@_on_stream
 def lizard_decode_step_positions(pos, q, k, v, g, Wf, sinks, S, z, kcache, vcache, w: int, *,
                                  scale: float = 0.0, y=None, workspace=None, stream=None,
                                  gcache=None, decay: int = LIZARD_DECAY_DELAYED):
@@ -534,6 +567,7 @@ def lizard_gate_cache_fill(g, gcache, w: int, *, stream=None):
            "lizard_gate_cache_fill")
 
 
+@_on_stream
 def lizard_qkvg_proj(x, W, Hq: int, Hkv: int, d: int, D: int, *, q=None, k=None, v=None,
                      g=None, workspace=None, stream=None):
     """[q | k | v | g] = x W^T on the tensor cores.  x [B, L, dm], W [N, dm] (bf16).
@@ -557,6 +591,7 @@ def lizard_qkvg_proj(x, W, Hq: int, Hkv: int, d: int, D: int, *, q=None, k=None,
     return tuple(outs)
 
 
+@_on_stream
 def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=None,
                          stream=None):
     """dx = dY W (bf16) and dW = dY^T x (fp32) for dY = [dq | dk | dv | dg]."""
@@ -583,22 +618,6 @@ def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=No
                                      _stream(stream))
     _check(st, "lizard_qkvg_proj_bwd")
     return dx, dW
-
-
-def _on_stream(fn):
-    """Runs a call that is given a stream under it, so that what the call allocates (workspaces,
-    copies of offsets, outputs) belongs to that stream: memory of the current stream's pool may still
-    be in use there, and goes back to it while the kernels on the other stream run.  (The function's
-    own `stream` is for its signature.)"""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
 
 
 # ---- the selective state space block -----------------------------------------------------

@@ -85,12 +85,10 @@ def block_calls(lz, host=False):
 CALLS = ["conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd"]
 
 
-@pytest.mark.parametrize("name", CALLS)
-def test_memory_of_a_call_on_another_stream(lz, name):
-    """A call on another stream, which is still busy, takes no memory back to the current stream
+def memory_stays(f):
+    """A call f on another stream, which is still busy, takes no memory back to the current stream
     before its kernels are done: neither does it see what is written there meanwhile, nor does it
     write there."""
-    f = block_calls(lz)[name]
     want = f()
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -117,10 +115,8 @@ def test_memory_of_a_call_on_another_stream(lz, name):
     assert all(bool((t == 0x5A).all()) for t in fill)
 
 
-@pytest.mark.parametrize("name", CALLS)
-def test_outputs_of_a_call_on_another_stream(lz, name):
-    """A call on another stream writes no memory that pending work of the current stream still reads."""
-    f = block_calls(lz)[name]
+def outputs_stay(f):
+    """A call f on another stream writes no memory that pending work of the current stream still reads."""
     want = f()
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -135,6 +131,16 @@ def test_outputs_of_a_call_on_another_stream(lz, name):
     assert all(bool((t == 7).all()) for t in late)
     for i, (a, b) in enumerate(zip(got, want)):
         assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_memory_of_a_call_on_another_stream(lz, name):
+    memory_stays(block_calls(lz)[name])
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_of_a_call_on_another_stream(lz, name):
+    outputs_stay(block_calls(lz)[name])
 
 
 @pytest.mark.parametrize("name", ["conv_fwd", "conv_bwd", "scan_fwd", "scan_bwd"])
