@@ -560,10 +560,15 @@ __global__ void __launch_bounds__(32 * KT) norm_bwd_sum_kernel(const NormArgs a,
         [&](int i, float s) { out[i0 + i] = s; });
 }
 
-template <typename K>
-cudaError_t group_smem(K kernel, size_t bytes) {
+// Raises a kernel's limit of dynamic shared memory where this launch's bytes need it, always to the
+// most that any of its launches takes: the limit is the process's, and another thread may launch the
+// same kernel with other sizes between this call and the launch.
+template <size_t most, typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    static_assert(most <= 226 * 1024, "with the static part within a SM's 227 KB");
     if (bytes <= 40 * 1024) return cudaSuccess;  // with the static part below the default 48 KB
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (bytes > most) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 // Shared memory of the group sums that neighbouring lanes cannot do.
@@ -572,6 +577,8 @@ size_t group_bytes(const NormArgs& a, int V) {
     if (a.groups == 1 || a.w_post == nullptr || (gv <= 32 && (gv & (gv - 1)) == 0)) return 0;
     return (sizeof(float) * (size_t)(nvec + a.groups) + 15) / 16 * 16;
 }
+// The most of it for rows of nvec pieces: such groups have three pieces or more.
+constexpr size_t most_group_bytes(size_t nvec) { return (sizeof(float) * (nvec + nvec / 3) + 15) / 16 * 16; }
 
 template <typename T, typename R, int V, int TPR, int NV>
 cudaError_t fwd_go(NormArgs a, cudaStream_t s) {
@@ -579,7 +586,9 @@ cudaError_t fwd_go(NormArgs a, cudaStream_t s) {
     a.group_bytes = group_bytes(a, V);
     const size_t sm = a.group_bytes + (V > 1 ? RPC * (size_t)a.D * (2 * sizeof(T) + sizeof(R)) : 0);
     const auto kernel = norm_fwd_kernel<T, R, V, TPR, NV>;
-    const cudaError_t e = group_smem(kernel, sm);
+    constexpr size_t D = V * TPR * NV;  // widest row
+    constexpr size_t most_smem = most_group_bytes(D / V) + (V > 1 ? RPC * D * (2 * sizeof(T) + sizeof(R)) : 0);
+    const cudaError_t e = allow_smem<most_smem>(kernel, sm);
     if (e != cudaSuccess) return e;
     // as many CTAs as are resident: 768 threads a SM
     const int64_t ctas = (a.T + RPC - 1) / RPC, most = 152 * (TPR >= 768 ? 1 : 768 / (TPR < 128 ? 128 : TPR));
@@ -595,7 +604,11 @@ cudaError_t bwd_go(NormArgs a, cudaStream_t s) {
                                             : sizeof(float) * (a.D <= kSumsWidth ? 3 * (size_t)a.D : 0) +
                                                   (rows_ahead<T, V, TPR>() ? row : 0));
     const auto kernel = norm_bwd_kernel<T, R, V, TPR, NV, HOLD>;
-    const cudaError_t e = group_smem(kernel, sm);
+    constexpr size_t D = V * TPR * NV, wide = D * (3 * sizeof(T) + 2 * sizeof(R));  // widest row
+    constexpr size_t most_smem = most_group_bytes(D / V) + (HOLD ? 2 * wide
+                                                            : sizeof(float) * 3 * (D < kSumsWidth ? D : kSumsWidth) +
+                                                                  (rows_ahead<T, V, TPR>() ? wide : 0));
+    const cudaError_t e = allow_smem<most_smem>(kernel, sm);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)norm_bwd_ctas(a.T, a.D), TPR, sm, s>>>(a);
     return cudaGetLastError();

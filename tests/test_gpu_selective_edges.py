@@ -1,5 +1,8 @@
 """The selective block on the GPU where its calls meet odd sizes, other streams and threads, and values
 far out."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 
@@ -158,3 +161,50 @@ def test_host_offsets_on_another_stream(lz, name):
         for i, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a, b), i
         del fill
+
+
+# ------------------------------------------------------------------------------- host threads
+
+
+@pytest.mark.parametrize("widths", [(8192, 5120), (4096, 2056)])
+def test_norms_of_two_host_threads(lz, widths):
+    """Two host threads whose rows take the same kernels with different amounts of shared memory: every
+    call succeeds and gives the bits it gives alone.  The library is called without the binding, so
+    that the threads spend their time inside it."""
+    d = Draw(31, "f32")
+    T, data, want = 4, [], []
+    for D in widths:
+        o, r, w = d(T, D)[0], d(T, D)[0], d(D)[0]
+        how = dict(r=r, w_post=w, w_pre=w)
+        g = lz.lizard_block_norm_bwd(o, **how, dr_out=r, dn_out=o)
+        want.append([*lz.lizard_block_norm_fwd(o, **how), g["do"], g["dr"], g["dw_post"], g["dw_pre"]])
+        data.append((o, r, w))
+    torch.cuda.synchronize()
+    lib, got, bad, start = lz.load(), [None, None], [0, 0], threading.Barrier(2)
+
+    def work(i):
+        (o, r, w), D, s = data[i], widths[i], torch.cuda.Stream()
+        dims = lz.lizard_norm_dims(T=T, D=D, groups=1, eps_post=1e-5, eps_pre=1e-5, dtype=0, res_dtype=0, act=1)
+        out = [torch.zeros_like(t) for t in want[i]]
+        ws = lz.new_workspace(lz.lizard_block_norm_bwd_workspace(dims), "cuda")
+        torch.cuda.synchronize()
+        p, po, pr, pw = [t.data_ptr() for t in out], o.data_ptr(), r.data_ptr(), w.data_ptr()
+        ref, st = ctypes.byref(dims), s.cuda_stream
+        start.wait()
+        for _ in range(10000):
+            bad[i] += lib.lizard_block_norm_fwd(ref, po, None, pr, pw, None, pw, p[0], p[1], st) != 0
+            bad[i] += lib.lizard_block_norm_bwd(ref, po, None, pr, pw, None, pw, pr, po, p[2], None, p[3], p[4], None, p[5],
+                                                ws.data_ptr(), ws.numel(), st) != 0
+        s.synchronize()
+        got[i] = out
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert bad == [0, 0]
+    for a, b in zip(got, want):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
