@@ -200,6 +200,19 @@ def _under(stream):
     return torch.cuda.stream(stream)
 
 
+@functools.cache
+def _gpus() -> int:
+    return torch.cuda.device_count()
+
+
+def _one_device(args):
+    """Launches go to the current device: tensors of another one are refused."""
+    here = torch.cuda.current_device()
+    for t in args:
+        if getattr(t, "is_cuda", False) and t.device.index != here:
+            raise ValueError(f"a tensor is on device {t.device}, the current device is cuda:{here}")
+
+
 def _on_stream(fn):
     """Runs a call that is given a stream under it, so that what the call allocates (workspaces,
     copies of offsets, outputs) belongs to that stream: memory of the current stream's pool may still
@@ -207,10 +220,12 @@ def _on_stream(fn):
     own `stream` is for its signature.)"""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with _under(stream):
-            return fn(*args, **kw)
+        if stream is not None:
+            with _under(stream):
+                return call(*args, **kw)
+        if _gpus() > 1:
+            _one_device((*args, *kw.values()))
+        return fn(*args, **kw)
     return call
 
 

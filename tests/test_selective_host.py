@@ -38,3 +38,40 @@ def test_residual_stream_of_another_type_is_refused(dtype, res):
                  lambda: lz.lizard_block_norm_bwd(o, dr_out=r)):
         with pytest.raises(ValueError, match="residual stream: dtype"):
             call()
+
+
+class OnDevice:
+    """Stands for a CUDA tensor of a device."""
+    is_cuda = True
+
+    def __init__(self, index, *shape):
+        self.device, self.shape, self.dtype = torch.device("cuda", index), torch.Size(shape), torch.float32
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Kernels are launched on the current device; a tensor of another one must not get there."""
+    monkeypatch.setattr(lz, "_gpus", lambda: 2, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def no_launch(*a):
+        raise AssertionError("reached the library")
+
+    monkeypatch.setattr(lz, "load", no_launch)
+    x0, x1 = OnDevice(0, 1, 5, 8), OnDevice(1, 1, 5, 8)
+    w0, w1 = OnDevice(0, 8, 4), OnDevice(1, 8, 4)
+    b0, b1 = OnDevice(0, 1, 5, 1, 4), OnDevice(1, 1, 5, 1, 4)
+    o0, o1 = OnDevice(0, 5, 8), OnDevice(1, 5, 8)
+    q0, q1 = OnDevice(0, 1, 5, 2, 64), OnDevice(1, 1, 5, 2, 64)
+    for call in (lambda: lz.lizard_conv_fwd(x1, w1),
+                 lambda: lz.lizard_conv_fwd(x0, w1),
+                 lambda: lz.lizard_conv_fwd(x0, w0, workspace=w1),
+                 lambda: lz.lizard_conv_bwd(x0, w0, None, x1),
+                 lambda: lz.lizard_conv_step(o0, w0, None, OnDevice(1, 5, 3, 8)),
+                 lambda: lz.lizard_scan_fwd(x0, x0, w0, b0, b0, z=x1),
+                 lambda: lz.lizard_scan_bwd(x0, x0, w0, b0, b1, x0, w0),
+                 lambda: lz.lizard_scan_step(o0, o0, w0, b0, b0, OnDevice(1, 5, 8, 4)),
+                 lambda: lz.lizard_block_norm_fwd(o0, r=o1),
+                 lambda: lz.lizard_block_norm_bwd(o1, dr_out=o1),
+                 lambda: lz.lizard_attn_fwd(q0, q0, q0, q1, w0, w0, 4)):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
