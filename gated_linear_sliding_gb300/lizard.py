@@ -217,12 +217,15 @@ def _on_stream(fn):
     """Runs a call that is given a stream under it, so that what the call allocates (workspaces,
     copies of offsets, outputs) belongs to that stream: memory of the current stream's pool may still
     be in use there, and goes back to it while the kernels on the other stream run.  (The function's
-    own `stream` is for its signature.)"""
+    own `stream` is for its signature.)  Checks where the workspace and the tensors are."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is not None:
             with _under(stream):
                 return call(*args, **kw)
+        workspace = kw.get("workspace")
+        if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous CUDA tensor")
         if _gpus() > 1:
             _one_device((*args, *kw.values()))
         return fn(*args, **kw)

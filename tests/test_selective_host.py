@@ -47,6 +47,9 @@ class OnDevice:
     def __init__(self, index, *shape):
         self.device, self.shape, self.dtype = torch.device("cuda", index), torch.Size(shape), torch.float32
 
+    def is_contiguous(self):
+        return True
+
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
     """Kernels are launched on the current device; a tensor of another one must not get there."""
@@ -74,4 +77,28 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                  lambda: lz.lizard_block_norm_bwd(o1, dr_out=o1),
                  lambda: lz.lizard_attn_fwd(q0, q0, q0, q1, w0, w0, 4)):
         with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
+
+
+@pytest.mark.parametrize("workspace", ["host", "strided"])
+def test_workspaces_that_kernels_cannot_use_are_refused(monkeypatch, workspace):
+    """The library takes a workspace's address and size; it cannot see that it is on the host or has
+    gaps."""
+    class Strided(OnDevice):
+        def is_contiguous(self):
+            return False
+
+    ws = torch.zeros(1 << 16, dtype=torch.uint8) if workspace == "host" else Strided(0, 1 << 16)
+    monkeypatch.setattr(lz, "load", lambda *a: pytest.fail("reached the library"))
+    x, w, b = OnDevice(0, 1, 5, 8), OnDevice(0, 8, 4), OnDevice(0, 1, 5, 1, 4)
+    o, q = OnDevice(0, 5, 8), OnDevice(0, 1, 5, 2, 64)
+    for call in (lambda: lz.lizard_conv_fwd(x, w, workspace=ws),
+                 lambda: lz.lizard_conv_bwd(x, w, None, x, workspace=ws),
+                 lambda: lz.lizard_conv_step(o, w, None, x, workspace=ws),
+                 lambda: lz.lizard_scan_fwd(x, x, w, b, b, workspace=ws),
+                 lambda: lz.lizard_scan_bwd(x, x, w, b, b, x, w, workspace=ws),
+                 lambda: lz.lizard_scan_step(o, o, w, b, b, x, workspace=ws),
+                 lambda: lz.lizard_block_norm_bwd(o, dr_out=o, workspace=ws),
+                 lambda: lz.lizard_attn_fwd(q, q, q, q, w, w, 4, workspace=ws)):
+        with pytest.raises(ValueError, match="workspace must be"):
             call()
