@@ -22,20 +22,36 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// The smaller of the two, NaN where one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| <= 1, and log1p(u) = 2 atanh(s) with
-// s = u / (2 + u) <= 1/3: the odd series to s^13 leaves 2 (1/3)^15 / 15, below 2^-26 of the
-// result.  (A logarithm of 1 + u would lose the digits of a small step size.)  Two at a time.
+// s = u / (2 + u) <= 1/3: s times a polynomial in s^2, five coefficients fitted for the least
+// relative error on [0, 1/9], which rounded to fp32 is 2^-26.9.  (A logarithm of 1 + u would lose the digits of a small step size.)  For a small step size
+// the result is u itself, whose exponent |x| log2(e) would bring |x| 2^-24 of it as the product's
+// rounding and as much as that of the constant: what the product leaves, by the multiply-add, and
+// the constant's second part are put back to first order.  Two at a time.
 __device__ __forceinline__ f2 softplus2(f2 v) {
     float x, y;
     unpack(v, x, y);
-    const f2 u = pack(ex2(-kLog2e * fabsf(x)), ex2(-kLog2e * fabsf(y)));
+    // from 128 on, infinity included, e^-|x| is 0
+    const f2 a = pack(min_nan(fabsf(x), 128.0f), min_nan(fabsf(y), 128.0f));
+    const f2 p2 = mul2(a, pack(-kLog2e, -kLog2e));  // -|x| log2(e) = p2 - left
+    const float low = 1.9259629911e-8f;             // log2(e) - kLog2e
+    const f2 left = fma2(a, pack(low, low), fma2(a, pack(kLog2e, kLog2e), p2));
+    f2 u = exp2_2(p2);
+    u = fma2(mul2(u, left), pack(-0.69314718055994531f, -0.69314718055994531f), u);
     float m, n;
     unpack(add2(u, pack(2.0f, 2.0f)), m, n);
     const f2 s = mul2(u, pack(rcp(m), rcp(n))), s2 = mul2(s, s);
-    const float c[7] = {2.0f / 13.0f, 2.0f / 11.0f, 2.0f / 9.0f, 2.0f / 7.0f, 2.0f / 5.0f, 2.0f / 3.0f, 2.0f};
+    const float c[5] = {0.281783342f, 0.279606014f, 0.400249094f, 0.66666317f, 2.0f};
     f2 p = pack(c[0], c[0]);
 #pragma unroll
-    for (int i = 1; i < 7; ++i) p = fma2(p, s2, pack(c[i], c[i]));
+    for (int i = 1; i < 5; ++i) p = fma2(p, s2, pack(c[i], c[i]));
     return fma2(s, p, pack(fmaxf(x, 0.0f), fmaxf(y, 0.0f)));
 }
 

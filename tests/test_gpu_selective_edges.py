@@ -208,3 +208,50 @@ def test_norms_of_two_host_threads(lz, widths):
     for a, b in zip(got, want):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------------------- step sizes
+
+
+def step_sizes(lz, dt, way):
+    """softplus(dt) as the state after one token of x = Bm = 1 from zero."""
+    n = dt.numel()
+    one = torch.ones(1, 1, n, dtype=dt.dtype, device="cuda")
+    A, h = -torch.ones(n, 1, device="cuda"), torch.zeros(1, n, 1, device="cuda")
+    bc = torch.ones(1, 1, 1, 1, dtype=dt.dtype, device="cuda")
+    if way == "prompt":
+        lz.lizard_scan_fwd(one, dt.view(1, 1, n), A, bc, bc, h_out=h)
+    else:
+        lz.lizard_scan_step(one[0], dt.view(1, n), A, bc[0], bc[0], h)
+    torch.cuda.synchronize()
+    return h.view(n).double().cpu().numpy()
+
+
+@pytest.mark.parametrize("way", ["prompt", "step"])
+def test_softplus_keeps_its_digits(lz, way):
+    """Relative error over arguments from -87 to 20.  In units of 2^-24: four for ex2.approx (2^-22), two
+    for rcp.approx (one ulp), one each for the correction's last step, u + 2, u / (2 + u) and the last
+    multiply-add, two for the polynomial: twelve.  The remainder's own rounding is below 2^-40."""
+    rng = np.random.default_rng(0)
+    v = np.concatenate([rng.uniform(-87, 20, 200_000), rng.uniform(-1, 1, 50_000), rng.uniform(-20, -5, 50_000)])
+    v = v.astype(np.float32)
+    got = step_sizes(lz, torch.from_numpy(v).cuda(), way)
+    w = v.astype(np.float64)
+    want = np.maximum(w, 0) + np.log1p(np.exp(-np.abs(w)))
+    err = np.abs(got - want) / want * 2.0 ** 24
+    assert err.max() <= 12, (err.max(), w[err.argmax()])
+
+
+@pytest.mark.parametrize("way", ["prompt", "step"])
+def test_softplus_far_out(lz, way):
+    """A token whose step is masked by the lowest value or minus infinity passes nothing; below 2^-126 a
+    step size is zero; NaN stays."""
+    f = np.float32
+    v = np.array([-np.inf, np.finfo(f).min, -1e30, -200, -128, -103, -88, -87.5, 88, 128, 129, 1e30, np.inf, np.nan, 0], f)
+    got = step_sizes(lz, torch.from_numpy(v).cuda(), way)
+    w = v.astype(np.float64)
+    want = np.maximum(w, 0) + np.log1p(np.exp(-np.abs(w)))
+    assert np.isnan(got[13]) and got[12] == np.inf
+    assert (got[:5] == 0).all()
+    assert (np.abs(got[:8] - want[:8]) <= 2.0 ** -126).all()
+    assert (np.abs(got[8:12] / want[8:12] - 1) <= 12 * 2.0 ** -24).all() and abs(got[14] / want[14] - 1) <= 12 * 2.0 ** -24
