@@ -186,14 +186,14 @@ def _p(t):
 
 
 def _stream(stream):
-    if stream is None:
+    if stream is None or stream is _HERE:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _under(stream):
     """Context in which `stream` (None: the current one) is the current stream."""
-    if stream is None:
+    if stream is None or stream is _HERE:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
@@ -213,23 +213,27 @@ def _one_device(args):
             raise ValueError(f"a tensor is on device {t.device}, the current device is cuda:{here}")
 
 
-def _on_stream(fn):
-    """Runs a call that is given a stream under it, so that what the call allocates (workspaces,
-    copies of offsets, outputs) belongs to that stream: memory of the current stream's pool may still
-    be in use there, and goes back to it while the kernels on the other stream run.  (The function's
-    own `stream` is for its signature.)  Checks where the workspace and the tensors are."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is not None:
-            with _under(stream):
-                return call(*args, **kw)
-        workspace = kw.get("workspace")
-        if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous CUDA tensor")
+_HERE = object()  # for `stream`: the current stream, everything has been looked at
+
+
+def _placed(fn, given):
+    """Runs a call, given its arguments by name, under the stream it is given, so that what it
+    allocates (workspaces, copies of offsets, outputs) belongs to that stream: memory of the current
+    stream's pool may still be in use there, and goes back to it while the kernels on the other stream
+    run."""
+    with _under(given["stream"]):
         if _gpus() > 1:
-            _one_device((*args, *kw.values()))
-        return fn(*args, **kw)
-    return call
+            _one_device(given.values())
+        return fn(**dict(given, stream=_HERE))
+
+
+def _ws(workspace):
+    """Address and bytes of an optional workspace."""
+    if workspace is None:
+        return None, 0
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -328,12 +332,13 @@ def lizard_read_device_status(workspace: torch.Tensor, stream=None) -> int:
     return int(load().lizard_read_device_status(_p(workspace), _stream(stream)))
 
 
-@_on_stream
 def lizard_attn_fwd(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0, y=None, lse=None,
                     S_out=None, z_out=None, kcache_out=None, vcache_out=None, workspace=None,
                     stream=None, decay: int = LIZARD_DECAY_DELAYED):
     """Forward over L tokens.  Returns y [B, L, Hq, d] (allocated if not given).  `decay`
     selects the decay reading (LIZARD_DECAY_*)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_attn_fwd, locals())
     B, L, Hq, d = q.shape
     Hkv, D, M = k.shape[2], g.shape[-1], sinks.shape[1]
     dt = q.dtype
@@ -359,7 +364,7 @@ def lizard_attn_fwd(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0, y=None
         workspace = new_workspace(lizard_attn_fwd_workspace(dims), q.device, stream)
     st = load().lizard_attn_fwd(ctypes.byref(dims), _p(q), _p(k), _p(v), _p(g), _p(Wf),
                                 _p(sinks), _p(y), _p(lse), _p(S_out), _p(z_out), _p(kcache_out),
-                                _p(vcache_out), _p(workspace), workspace.numel(),
+                                _p(vcache_out), *_ws(workspace),
                                 _stream(stream))
     _check(st, "lizard_attn_fwd")
     return y
@@ -371,7 +376,6 @@ def lizard_attn_fwd_varlen_workspace(dims, cu_seqlens) -> int:
     return int(load().lizard_attn_fwd_varlen_workspace(ctypes.byref(dims), cu.ctypes.data))
 
 
-@_on_stream
 def lizard_attn_fwd_varlen(q, k, v, g, Wf, sinks, w: int, cu_seqlens, *, scale: float = 0.0,
                            y=None, lse=None, S_out=None, z_out=None, kcache_out=None,
                            vcache_out=None, workspace=None, stream=None,
@@ -379,6 +383,8 @@ def lizard_attn_fwd_varlen(q, k, v, g, Wf, sinks, w: int, cu_seqlens, *, scale: 
     """Forward over a packed batch: q [T, Hq, d], k, v [T, Hkv, d], g [T, Hkv, D], and
     cu_seqlens (host integers, B + 1 offsets) delimiting B sequences.  Returns y [T, Hq, d];
     S_out, z_out, kcache_out, vcache_out hold one entry per sequence."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_attn_fwd_varlen, locals())
     T, Hq, d = q.shape
     Hkv, D, M = k.shape[1], g.shape[-1], sinks.shape[1]
     cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int64))
@@ -406,13 +412,11 @@ def lizard_attn_fwd_varlen(q, k, v, g, Wf, sinks, w: int, cu_seqlens, *, scale: 
         workspace = new_workspace(lizard_attn_fwd_varlen_workspace(dims, cu), q.device, stream)
     st = load().lizard_attn_fwd_varlen(ctypes.byref(dims), cu.ctypes.data, _p(q), _p(k), _p(v),
                                        _p(g), _p(Wf), _p(sinks), _p(y), _p(lse), _p(S_out),
-                                       _p(z_out), _p(kcache_out), _p(vcache_out), _p(workspace),
-                                       workspace.numel(), _stream(stream))
+                                       _p(z_out), _p(kcache_out), _p(vcache_out), *_ws(workspace), _stream(stream))
     _check(st, "lizard_attn_fwd_varlen")
     return y
 
 
-@_on_stream
 def lizard_attn_fwd_noalloc(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0, y=None,
                             lse=None, S_out=None, z_out=None, kcache_out=None, vcache_out=None,
                             stream=None, decay: int = LIZARD_DECAY_DELAYED):
@@ -421,6 +425,8 @@ def lizard_attn_fwd_noalloc(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0
     Same arguments and result as lizard_attn_fwd; the library keeps the scratch in a
     fixed 32 MiB device array (see include/lizard.h for the limit and the sharing rules).
     `y` is allocated here only for the Python caller's convenience when not given."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_attn_fwd_noalloc, locals())
     B, L, Hq, d = q.shape
     Hkv, D, M = k.shape[2], g.shape[-1], sinks.shape[1]
     dt = q.dtype
@@ -441,12 +447,13 @@ def lizard_attn_fwd_noalloc(q, k, v, g, Wf, sinks, w: int, *, scale: float = 0.0
     return y
 
 
-@_on_stream
 def lizard_attn_bwd(q, k, v, g, Wf, sinks, y, lse, dy, w: int, *, scale: float = 0.0,
                     dq=None, dk=None, dv=None, dg=None, dWf=None, dsinks=None, workspace=None,
                     stream=None, decay: int = LIZARD_DECAY_DELAYED):
     """Gradients (dq, dk, dv, dg, dWf, dsinks) of y against dy (same decay reading as the
     forward that made y)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_attn_bwd, locals())
     B, L, Hq, d = q.shape
     Hkv, D, M = k.shape[2], g.shape[-1], sinks.shape[1]
     dt = q.dtype
@@ -467,7 +474,7 @@ def lizard_attn_bwd(q, k, v, g, Wf, sinks, y, lse, dy, w: int, *, scale: float =
         workspace = new_workspace(lizard_attn_bwd_workspace(dims), q.device, stream)
     st = load().lizard_attn_bwd(ctypes.byref(dims), _p(q), _p(k), _p(v), _p(g), _p(Wf),
                                 _p(sinks), _p(y), _p(lse), _p(dy), _p(dq), _p(dk), _p(dv),
-                                _p(dg), _p(dWf), _p(dsinks), _p(workspace), workspace.numel(),
+                                _p(dg), _p(dWf), _p(dsinks), *_ws(workspace),
                                 _stream(stream))
     _check(st, "lizard_attn_bwd")
     return dict(dq=dq, dk=dk, dv=dv, dg=dg, dWf=dWf, dsinks=dsinks)
@@ -479,12 +486,13 @@ def lizard_attn_bwd_varlen_workspace(dims, cu_seqlens) -> int:
     return int(load().lizard_attn_bwd_varlen_workspace(ctypes.byref(dims), cu.ctypes.data))
 
 
-@_on_stream
 def lizard_attn_bwd_varlen(q, k, v, g, Wf, sinks, y, lse, dy, w: int, cu_seqlens, *,
                            scale: float = 0.0, workspace=None, stream=None,
                            decay: int = LIZARD_DECAY_DELAYED):
     """Gradients of lizard_attn_fwd_varlen's y against dy for a packed batch: dq, dk, dv,
     dg packed like the inputs; dWf and dsinks summed over the sequences."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_attn_bwd_varlen, locals())
     T, Hq, d = q.shape
     Hkv, D, M = k.shape[1], g.shape[-1], sinks.shape[1]
     cu = np.asarray(cu_seqlens, dtype=np.int64)
@@ -508,7 +516,7 @@ def lizard_attn_bwd_varlen(q, k, v, g, Wf, sinks, y, lse, dy, w: int, cu_seqlens
     st = load().lizard_attn_bwd_varlen(ctypes.byref(dims), cu.ctypes.data, _p(q), _p(k), _p(v),
                                        _p(g), _p(Wf), _p(sinks), _p(y), _p(lse), _p(dy),
                                        _p(dq), _p(dk), _p(dv), _p(dg), _p(dWf), _p(dsinks),
-                                       _p(workspace), workspace.numel(), _stream(stream))
+                                       *_ws(workspace), _stream(stream))
     _check(st, "lizard_attn_bwd_varlen")
     return dict(dq=dq, dk=dk, dv=dv, dg=dg, dWf=dWf, dsinks=dsinks)
 
@@ -531,12 +539,13 @@ def _decode_common(q, k, v, g, Wf, sinks, S, z, kcache, vcache, gcache, w, decay
     return B, Hq, Hkv, d, D, M
 
 
-@_on_stream
 def lizard_decode_step(pos: int, q, k, v, g, Wf, sinks, S, z, kcache, vcache, w: int, *,
                        scale: float = 0.0, y=None, workspace=None, stream=None, gcache=None,
                        decay: int = LIZARD_DECAY_DELAYED):
     """One decode step at position pos; S, z, kcache, vcache (and gcache, the gate ring the
     MASKED and LAGGED readings need) are updated in place."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_decode_step, locals())
     B, Hq, Hkv, d, D, M = _decode_common(q, k, v, g, Wf, sinks, S, z, kcache, vcache, gcache,
                                          w, decay)
     y = torch.empty_like(q) if y is None else y
@@ -545,19 +554,20 @@ def lizard_decode_step(pos: int, q, k, v, g, Wf, sinks, S, z, kcache, vcache, w:
         workspace = new_workspace(lizard_decode_workspace(dims), q.device, stream)
     st = load().lizard_decode_step(ctypes.byref(dims), int(pos), _p(q), _p(k), _p(v), _p(g),
                                    _p(Wf), _p(sinks), _p(y), _p(S), _p(z), _p(kcache),
-                                   _p(vcache), _p(gcache), _p(workspace), workspace.numel(),
+                                   _p(vcache), _p(gcache), *_ws(workspace),
                                    _stream(stream))
     _check(st, "lizard_decode_step")
     return y
 
 
-@_on_stream
 def lizard_decode_step_positions(pos, q, k, v, g, Wf, sinks, S, z, kcache, vcache, w: int, *,
                                  scale: float = 0.0, y=None, workspace=None, stream=None,
                                  gcache=None, decay: int = LIZARD_DECAY_DELAYED):
     """One decode step with a position per sequence: pos is an int64 device tensor [B],
     read when the kernel runs.  A negative entry is reported through the workspace status
     (lizard_read_device_status) and leaves that sequence untouched."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_decode_step_positions, locals())
     B = q.shape[0]
     _need(pos, "pos", (B,), torch.int64)
     B, Hq, Hkv, d, D, M = _decode_common(q, k, v, g, Wf, sinks, S, z, kcache, vcache, gcache,
@@ -568,8 +578,7 @@ def lizard_decode_step_positions(pos, q, k, v, g, Wf, sinks, S, z, kcache, vcach
         workspace = new_workspace(lizard_decode_workspace(dims), q.device, stream)
     st = load().lizard_decode_step_positions(ctypes.byref(dims), _p(pos), _p(q), _p(k), _p(v),
                                              _p(g), _p(Wf), _p(sinks), _p(y), _p(S), _p(z),
-                                             _p(kcache), _p(vcache), _p(gcache), _p(workspace),
-                                             workspace.numel(), _stream(stream))
+                                             _p(kcache), _p(vcache), _p(gcache), *_ws(workspace), _stream(stream))
     _check(st, "lizard_decode_step_positions")
     return y
 
@@ -585,11 +594,12 @@ def lizard_gate_cache_fill(g, gcache, w: int, *, stream=None):
            "lizard_gate_cache_fill")
 
 
-@_on_stream
 def lizard_qkvg_proj(x, W, Hq: int, Hkv: int, d: int, D: int, *, q=None, k=None, v=None,
                      g=None, workspace=None, stream=None):
     """[q | k | v | g] = x W^T on the tensor cores.  x [B, L, dm], W [N, dm] (bf16).
     Returns (q, k, v, g) in the mixer's layouts (allocated if not given)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_qkvg_proj, locals())
     B, L, dm = x.shape
     N = Hq * d + 2 * Hkv * d + Hkv * D
     _need(x, "x", (B, L, dm), torch.bfloat16)
@@ -602,17 +612,17 @@ def lizard_qkvg_proj(x, W, Hq: int, Hkv: int, d: int, D: int, *, q=None, k=None,
         _need(t, name, shape, torch.bfloat16)
         outs.append(t)
     dims = make_dims(B, L, Hq, Hkv, d, D, 1, 0, LIZARD_BF16)
-    nb = 0 if workspace is None else workspace.numel()
     st = load().lizard_qkvg_proj(ctypes.byref(dims), dm, _p(x), _p(W), *[_p(t) for t in outs],
-                                 _p(workspace), nb, _stream(stream))
+                                 *_ws(workspace), _stream(stream))
     _check(st, "lizard_qkvg_proj")
     return tuple(outs)
 
 
-@_on_stream
 def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=None,
                          stream=None):
     """dx = dY W (bf16) and dW = dY^T x (fp32) for dY = [dq | dk | dv | dg]."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_qkvg_proj_bwd, locals())
     B, L, dm = x.shape
     Hq, d = dq.shape[2], dq.shape[3]
     Hkv, D = dg.shape[2], dg.shape[3]
@@ -630,9 +640,8 @@ def lizard_qkvg_proj_bwd(x, W, dq, dk, dv, dg, *, dx=None, dW=None, workspace=No
     _need(dx, "dx", (B, L, dm), torch.bfloat16)
     _need(dW, "dW", (N, dm), torch.float32)
     dims = make_dims(B, L, Hq, Hkv, d, D, 1, 0, LIZARD_BF16)
-    nb = 0 if workspace is None else workspace.numel()
     st = load().lizard_qkvg_proj_bwd(ctypes.byref(dims), dm, _p(x), _p(W), _p(dq), _p(dk),
-                                     _p(dv), _p(dg), _p(dx), _p(dW), _p(workspace), nb,
+                                     _p(dv), _p(dg), _p(dx), _p(dW), *_ws(workspace),
                                      _stream(stream))
     _check(st, "lizard_qkvg_proj_bwd")
     return dx, dW
@@ -731,12 +740,13 @@ def _slots(slots, B):
     return slots.data_ptr()
 
 
-@_on_stream
 def lizard_conv_fwd(x, w, bias=None, *, act: int = LIZARD_ACT_NONE, state_in=None, state_out=None,
                     cu_seqlens=None, y=None, workspace=None, stream=None):
     """Short causal depthwise convolution of x [B, L, C] with w [C, K]; returns y [B, L, C].
     state_in, state_out [B or sequences, K-1, C]: the inputs before each sequence's first token
     and its last ones (state_out may be state_in)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_conv_fwd, locals())
     B, L, C = x.shape
     K, dt = w.shape[1], x.dtype
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
@@ -750,8 +760,8 @@ def lizard_conv_fwd(x, w, bias=None, *, act: int = LIZARD_ACT_NONE, state_in=Non
                             _ld(y, "y", (B, L, C), dt), 0, _dtype_code(x), act)
     st = load().lizard_conv_fwd(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
                                 _need_f32(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
-                                y.data_ptr(), _ptr(state_out), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _stream_of(x))
+                                y.data_ptr(), _ptr(state_out), *_ws(workspace),
+                                _stream_of(x))
     _check(st, "lizard_conv_fwd")
     return y
 
@@ -760,12 +770,13 @@ def lizard_conv_bwd_workspace(dims) -> int:
     return int(load().lizard_conv_bwd_workspace(ctypes.byref(dims)))
 
 
-@_on_stream
 def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None,
                     dstate_out=None, dstate_in=None, cu_seqlens=None, dx=None, workspace=None,
                     stream=None):
     """Gradients dx, dw, dbias of lizard_conv_fwd's y against dy (bias and dbias may be None);
     dstate_out is the gradient of state_out, dstate_in (if given) receives that of state_in."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_conv_bwd, locals())
     B, L, C = x.shape
     K, dt = w.shape[1], x.dtype
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
@@ -784,18 +795,19 @@ def lizard_conv_bwd(x, w, bias, dy, *, act: int = LIZARD_ACT_NONE, state_in=None
     st = load().lizard_conv_bwd(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
                                 _need_f32(bias, "bias", (C,)), _ptr(state_in), _ptr(cu),
                                 dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dw.data_ptr(),
-                                _ptr(dbias), _ptr(dstate_in), workspace.data_ptr(),
-                                workspace.numel(), _stream_of(x))
+                                _ptr(dbias), _ptr(dstate_in), *_ws(workspace),
+                                _stream_of(x))
     _check(st, "lizard_conv_bwd")
     return dict(dx=dx, dw=dw, dbias=dbias, dstate_in=dstate_in)
 
 
-@_on_stream
 def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NONE, y=None,
                      workspace=None, stream=None):
     """One token for each of B sequences: y [B, C] from x [B, C]; state [slots, K-1, C] is moved
     on IN PLACE.  slots: int64 device tensor [B] naming each row's state (negative: an idle row),
     or None (row b uses entry b)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_conv_step, locals())
     B, C = x.shape
     K, dt = w.shape[1], x.dtype
     ldy = 0
@@ -808,8 +820,8 @@ def lizard_conv_step(x, w, bias, state, *, slots=None, act: int = LIZARD_ACT_NON
     dims = lizard_conv_dims(B, 1, C, K, 0, _ld(x, "x", (B, C), dt, 1), ldy, 0, _dtype_code(x), act)
     st = load().lizard_conv_step(ctypes.byref(dims), x.data_ptr(), _need_f32(w, "w", (C, K)),
                                  _need_f32(bias, "bias", (C,)), state.data_ptr(), state.shape[0],
-                                 _slots(slots, B), y.data_ptr(), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream_of(x))
+                                 _slots(slots, B), y.data_ptr(), *_ws(workspace),
+                                 _stream_of(x))
     _check(st, "lizard_conv_step")
     return y
 
@@ -843,7 +855,6 @@ def lizard_scan_states_bytes(dims) -> int:
     return int(load().lizard_scan_states_bytes(ctypes.byref(dims)))
 
 
-@_on_stream
 def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus: bool = True,
                     h0=None, h_out=None, cu_seqlens=None, y=None, save_states: bool = False,
                     workspace=None, stream=None):
@@ -851,6 +862,8 @@ def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus:
     output vectors Bm, Cm [B, L, G, N], skip D [C] and output gate z [B, L, C]; returns y, or
     (y, states) with save_states, which lizard_scan_bwd takes.  h0, h_out [B or sequences, C, N]
     fp32: the states before and after (h_out may be h0)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_scan_fwd, locals())
     B, L, C = x.shape
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
     dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq)
@@ -866,18 +879,19 @@ def lizard_scan_fwd(x, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus:
     workspace = _scratch(workspace, lib.lizard_scan_fwd_workspace(ctypes.byref(dims)), x.device)
     st = lib.lizard_scan_fwd(ctypes.byref(dims), *ptrs, _need_f32(h0, "h0", shape), _ptr(cu),
                              y.data_ptr(), _need_f32(h_out, "h_out", shape), _ptr(states),
-                             workspace.data_ptr(), workspace.numel(), _stream_of(x))
+                             *_ws(workspace), _stream_of(x))
     _check(st, "lizard_scan_fwd")
     return (y, states) if save_states else y
 
 
-@_on_stream
 def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=None,
                     softplus: bool = True, h0=None, dh_out=None, dh0=None, cu_seqlens=None,
                     dx=None, ddt=None, dz=None, dBm=None, dCm=None, workspace=None, stream=None):
     """Gradients dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias of lizard_scan_fwd's y against dy, from
     the same inputs and the states that call returned (None for an absent D, z, dt_bias).
     dh_out is the gradient of h_out; dh0 (if given) receives that of h0."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_scan_bwd, locals())
     B, L, C = x.shape
     nseq, cu = _packed(cu_seqlens, B, L, x.device)
     dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, nseq)
@@ -907,17 +921,17 @@ def lizard_scan_bwd(x, dt, A, Bm, Cm, dy, states, *, D=None, z=None, dt_bias=Non
                              states.data_ptr(), dy.data_ptr(),
                              _need_f32(dh_out, "dh_out", shape), dx.data_ptr(), ddt.data_ptr(),
                              _ptr(dz), dBm.data_ptr(), dCm.data_ptr(), dA.data_ptr(), _ptr(dD),
-                             _ptr(ddt_bias), _need_f32(dh0, "dh0", shape), workspace.data_ptr(),
-                             workspace.numel(), _stream_of(x))
+                             _ptr(ddt_bias), _need_f32(dh0, "dh0", shape), *_ws(workspace), _stream_of(x))
     _check(st, "lizard_scan_bwd")
     return dict(dx=dx, ddt=ddt, dA=dA, dBm=dBm, dCm=dCm, dD=dD, dz=dz, ddt_bias=ddt_bias, dh0=dh0)
 
 
-@_on_stream
 def lizard_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None,
                      softplus: bool = True, slots=None, y=None, workspace=None, stream=None):
     """One token for each of B sequences: y [B, C] from x, dt, z [B, C] and Bm, Cm [B, G, N];
     state [slots, C, N] fp32 is moved on IN PLACE.  slots as for lizard_conv_step."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_scan_step, locals())
     dims, ptrs = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, 0)
     B, C = x.shape
     if y is None:
@@ -927,8 +941,8 @@ def lizard_scan_step(x, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None,
     nslots = state.shape[0]
     st = load().lizard_scan_step(ctypes.byref(dims), *ptrs,
                                  _need_f32(state, "state", (nslots, C, dims.N)), nslots,
-                                 _slots(slots, B), y.data_ptr(), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream_of(x))
+                                 _slots(slots, B), y.data_ptr(), *_ws(workspace),
+                                 _stream_of(x))
     _check(st, "lizard_scan_step")
     return y
 
@@ -952,13 +966,14 @@ def _norm_inputs(o, gate, r, w_post, scale, w_pre, res_dtype, groups, act, gate_
                   _need_f32(scale, "scale", (D,)), _need_f32(w_pre, "w_pre", (D,)))
 
 
-@_on_stream
 def lizard_block_norm_fwd(o, *, gate=None, r=None, w_post=None, scale=None, w_pre=None,
                           groups: int = 1, act: int = LIZARD_ACT_SILU, gate_first: bool = False,
                           eps: float = 1e-5, eps_pre=None, r_out=None, n_out=None, stream=None):
     """Norm after a block with its gate, residual scale and add, and the norm before the next
     block: o [T, D] is the block's output, r [T, D] the residual stream (its dtype or fp32).
     Returns (r_out, n_out); n_out is None without w_pre.  r_out takes r's dtype, or o's."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_block_norm_fwd, locals())
     shape = tuple(o.shape)
     rtp = r.dtype if r is not None else r_out.dtype if r_out is not None else o.dtype
     dims, ptrs = _norm_inputs(o, gate, r, w_post, scale, w_pre, rtp, groups, act, gate_first, eps,
@@ -984,7 +999,6 @@ def lizard_block_norm_bwd_workspace(dims) -> int:
     return int(load().lizard_block_norm_bwd_workspace(ctypes.byref(dims)))
 
 
-@_on_stream
 def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_post=None,
                           scale=None, w_pre=None, groups: int = 1, act: int = LIZARD_ACT_SILU,
                           gate_first: bool = False, eps: float = 1e-5, eps_pre=None,
@@ -992,6 +1006,8 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
     """Gradients do, dgate, dr, dw_post, dscale, dw_pre of lizard_block_norm_fwd against dr_out
     and dn_out (one may be None; dn_out goes with w_pre), from the forward's inputs; None for an
     absent input."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_block_norm_bwd, locals())
     shape = tuple(o.shape)
     rtp = r.dtype if r is not None else dr_out.dtype if dr_out is not None else o.dtype
     dims, ptrs = _norm_inputs(o, gate, r, w_post, scale, w_pre, rtp, groups, act, gate_first, eps,
@@ -1009,7 +1025,6 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
     workspace = _scratch(workspace, lizard_block_norm_bwd_workspace(dims), o.device)
     st = load().lizard_block_norm_bwd(ctypes.byref(dims), *ptrs, _ptr(dr_out), _ptr(dn_out),
                                       do.data_ptr(), _ptr(dgate), _ptr(dr), _ptr(dw_post),
-                                      _ptr(dscale), _ptr(dw_pre), workspace.data_ptr(),
-                                      workspace.numel(), _stream_of(o))
+                                      _ptr(dscale), _ptr(dw_pre), *_ws(workspace), _stream_of(o))
     _check(st, "lizard_block_norm_bwd")
     return dict(do=do, dgate=dgate, dr=dr, dw_post=dw_post, dscale=dscale, dw_pre=dw_pre)

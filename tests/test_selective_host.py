@@ -80,25 +80,43 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
             call()
 
 
-@pytest.mark.parametrize("workspace", ["host", "strided"])
-def test_workspaces_that_kernels_cannot_use_are_refused(monkeypatch, workspace):
+class AsCuda(torch.Tensor):
+    """A host tensor that says it is on a GPU."""
+    is_cuda = True
+
+
+def as_cuda(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(AsCuda)
+
+
+@pytest.mark.parametrize("kind", ["host", "strided"])
+def test_workspaces_that_kernels_cannot_use_are_refused(monkeypatch, kind):
     """The library takes a workspace's address and size; it cannot see that it is on the host or has
     gaps."""
-    class Strided(OnDevice):
-        def is_contiguous(self):
-            return False
+    u8 = torch.uint8
+    ws = torch.zeros(1 << 16, dtype=u8) if kind == "host" else as_cuda(1 << 17, dtype=u8)[::2]
 
-    ws = torch.zeros(1 << 16, dtype=torch.uint8) if workspace == "host" else Strided(0, 1 << 16)
-    monkeypatch.setattr(lz, "load", lambda *a: pytest.fail("reached the library"))
-    x, w, b = OnDevice(0, 1, 5, 8), OnDevice(0, 8, 4), OnDevice(0, 1, 5, 1, 4)
-    o, q = OnDevice(0, 5, 8), OnDevice(0, 1, 5, 2, 64)
+    class Library:  # sizes are asked for, launches are not to come
+        def __getattr__(self, name):
+            return lambda *a: 0 if name.endswith(("_workspace", "_bytes")) else pytest.fail(f"reached {name}")
+
+    monkeypatch.setattr(lz, "load", Library)
+    x, w, b = as_cuda(1, 5, 8), as_cuda(8, 4), as_cuda(1, 5, 1, 4)
+    o, state, bs, h = as_cuda(5, 8), as_cuda(5, 3, 8), as_cuda(5, 1, 4), as_cuda(5, 8, 4)
+    q, Wf, sinks = as_cuda(1, 5, 2, 64), as_cuda(2, 64, 32), as_cuda(2, 4)
+    t, S, z, kc = as_cuda(1, 2, 64), as_cuda(1, 2, 64, 64), as_cuda(1, 2, 64), as_cuda(1, 2, 5, 64)
+    xb, W, qb = (as_cuda(*n, dtype=torch.bfloat16) for n in ((1, 5, 16), (512, 16), (1, 5, 2, 64)))
     for call in (lambda: lz.lizard_conv_fwd(x, w, workspace=ws),
                  lambda: lz.lizard_conv_bwd(x, w, None, x, workspace=ws),
-                 lambda: lz.lizard_conv_step(o, w, None, x, workspace=ws),
+                 lambda: lz.lizard_conv_step(o, w, None, state, workspace=ws),
                  lambda: lz.lizard_scan_fwd(x, x, w, b, b, workspace=ws),
-                 lambda: lz.lizard_scan_bwd(x, x, w, b, b, x, w, workspace=ws),
-                 lambda: lz.lizard_scan_step(o, o, w, b, b, x, workspace=ws),
+                 lambda: lz.lizard_scan_bwd(x, x, w, b, b, x, as_cuda(0, dtype=u8), workspace=ws),
+                 lambda: lz.lizard_scan_step(o, o, w, bs, bs, h, workspace=ws),
                  lambda: lz.lizard_block_norm_bwd(o, dr_out=o, workspace=ws),
-                 lambda: lz.lizard_attn_fwd(q, q, q, q, w, w, 4, workspace=ws)):
+                 lambda: lz.lizard_attn_fwd(q, q, q, q, Wf, sinks, 4, workspace=ws),
+                 lambda: lz.lizard_attn_bwd(q, q, q, q, Wf, sinks, q, as_cuda(1, 5, 2), q, 4, workspace=ws),
+                 lambda: lz.lizard_decode_step(0, t, t, t, t, Wf, sinks, S, z, kc, kc, 4, workspace=ws),
+                 lambda: lz.lizard_qkvg_proj(xb, W, 2, 2, 64, 64, q=qb, k=qb, v=qb, g=qb, workspace=ws),
+                 lambda: lz.lizard_qkvg_proj_bwd(xb, W, qb, qb, qb, qb, dW=as_cuda(512, 16), workspace=ws)):
         with pytest.raises(ValueError, match="workspace must be"):
             call()
