@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanArgs a) {
     float y = 0.0f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        h[i] = fmaf(ex2(d * (A[i] * kLog2e)), h[i], dx * bb[i]);
+        h[i] = fmaf(ex2(fmaf(d, A[i] * kLog2e, kDecayShift)), h[i], dx * bb[i]);
         y = fmaf(cc[i], h[i], y);
     }
 #pragma unroll

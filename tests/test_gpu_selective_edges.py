@@ -255,3 +255,27 @@ def test_softplus_far_out(lz, way):
     assert (got[:5] == 0).all()
     assert (np.abs(got[:8] - want[:8]) <= 2.0 ** -126).all()
     assert (np.abs(got[8:12] / want[8:12] - 1) <= 12 * 2.0 ** -24).all() and abs(got[14] / want[14] - 1) <= 12 * 2.0 ** -24
+
+
+# ------------------------------------------------------------------------------- long memory
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C,N,G", [(24, 16, 1), (10, 5, 2), (7, 1, 1)])
+def test_states_token_by_token_are_the_prompts(lz, dtype, C, N, G):
+    """250 single tokens move a state to the bits that a prompt of them (one segment) moves it to: the
+    same decays, products and sums in the same order.  (A bias of the decays adds up over tokens.)"""
+    d = Draw(41, dtype)
+    L = 250
+    x, dt = d(2, L, C)[0], d(2, L, C, shift=-5.0)[0]
+    Bm, Cm = d(2, L, G, N)[0], d(2, L, G, N)[0]
+    A = d.dev(-np.exp(d.rng.normal(size=(C, N))))[0]
+    bias = d(C, dtype=torch.float32, scale=0.3)[0]
+    h0 = d(2, C, N, dtype=torch.float32)[0]
+    h, st = torch.empty_like(h0), h0.clone()
+    lz.lizard_scan_fwd(x, dt, A, Bm, Cm, dt_bias=bias, h0=h0, h_out=h)
+    for t in range(L):
+        lz.lizard_scan_step(x[:, t].contiguous(), dt[:, t].contiguous(), A, Bm[:, t].contiguous(), Cm[:, t].contiguous(), st,
+                            dt_bias=bias)
+    torch.cuda.synchronize()
+    assert torch.equal(h, st)
