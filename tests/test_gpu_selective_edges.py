@@ -6,7 +6,8 @@ import threading
 import numpy as np
 import pytest
 
-from test_gpu_selective import Draw, check, offsets
+from oracle import selective as S
+from test_gpu_selective import Draw, check, offsets, tdt
 
 pytestmark = pytest.mark.gpu
 
@@ -279,3 +280,61 @@ def test_states_token_by_token_are_the_prompts(lz, dtype, C, N, G):
                             dt_bias=bias)
     torch.cuda.synchronize()
     assert torch.equal(h, st)
+
+
+# ------------------------------------------------------------------------------- parameter gradients
+
+PARAM = [  # T, D, groups, gate ("", first, last), residual: more rows than CTAs, so that each adds up several
+    (1300, 16, 1, "last", "same"),
+    (2000, 128, 1, "", "f32"),
+    (400, 37, 1, "last", "same"),
+    (1400, 1023, 3, "first", "f32"),   # one column a piece, group sums through shared memory
+    (1400, 512, 2, "last", "same"),
+    (700, 1040, 8, "first", "same"),
+    (700, 2050, 2, "last", "same"),
+    (400, 2048, 1, "last", "f32"),
+    (400, 3840, 3, "first", "same"),   # eight columns a piece, group sums through shared memory
+    (400, 4096, 1, "last", "same"),
+    (400, 5000, 1, "last", "f32"),     # sums in shared memory from here on
+    (400, 8184, 3, "first", "same"),
+    (330, 9000, 3, "last", "f32"),     # in the CTAs' partial sums from here on
+    (330, 9001, 1, "first", "same"),
+    (310, 16384, 8, "last", "same"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", range(len(PARAM)))
+def test_parameter_gradients_of_many_rows(lz, dtype, case):
+    """dw_post, dscale and dw_pre where a CTA walks several rows.  A term passes at most 128 roundings
+    before the sums over rows (a row's sum: 16 of a thread, ten of the lanes and warps, three such sums;
+    the gate's exponential and reciprocal eight; two dozen products), which have T / 8 in a chain at
+    most; each is 2^-24 of the term's magnitude, added up over a column's rows.  A lost row is about
+    1 / T of that sum, more than twenty times as much."""
+    T, D, groups, gate, res = PARAM[case]
+    d = Draw(case, dtype)
+    rtp = tdt(dtype) if res == "same" else torch.float32
+    vec = lambda: d(D, dtype=torch.float32, scale=0.3, shift=1.0)  # noqa: E731
+    v = dict(o=d(T, D), gate=d(T, D) if gate else (None, None), r=d(T, D, dtype=rtp), w_post=vec(), scale=vec(), w_pre=vec())
+    dr, dn = d(T, D, dtype=rtp), d(T, D)
+    t, f = {k: a[0] for k, a in v.items()}, {k: a[1] for k, a in v.items()}
+    o = t.pop("o")
+    how = dict(groups=groups, gate_first=gate == "first", eps=1e-4)
+    g = lz.lizard_block_norm_bwd(o, **t, **how, dr_out=dr[0], dn_out=dn[0])
+    torch.cuda.synchronize()
+    ref = S.norm_bwd(**f, **how, act="silu", dr_out=dr[1], dn_out=dn[1])
+    # the terms' magnitudes
+    a = np.abs(S.silu(f["gate"])) if gate else np.ones((T, D))
+    u = np.abs(f["o"]) * (a if gate == "first" else 1)
+    parts = u.reshape(T, groups, -1)
+    unit = (parts / np.sqrt((parts ** 2).mean(-1, keepdims=True) + 1e-4)).reshape(T, D)
+    n = unit * np.abs(f["w_post"]) * (a if gate == "last" else 1)
+    rr_out, _ = S.norm_fwd(**f, **how, act="silu")
+    q = np.sqrt((rr_out ** 2).mean(-1, keepdims=True) + 1e-4)
+    rr = np.abs(f["r"]) + np.abs(f["scale"]) * n
+    w = np.abs(dn[1] * f["w_pre"])
+    grad = np.abs(dr[1]) + w / q + rr * (w * rr).mean(-1, keepdims=True) / q ** 3
+    mags = dict(dw_pre=np.abs(dn[1]) * rr / q, dscale=grad * n,
+                dw_post=grad * np.abs(f["scale"]) * unit * (a if gate == "last" else 1))
+    for k, m in mags.items():
+        check(g[k], ref[k], m.sum(0), 128 + T / 8, k)
