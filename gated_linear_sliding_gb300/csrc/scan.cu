@@ -384,10 +384,11 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanArgs a) {
     st((T*)a.y + b * a.ldy + c, y);
 }
 
-template <int LPC = 1, typename F>
+// Calls f with l, one of LPC, 2 LPC, ... MOST, as a constant.
+template <int LPC, int MOST, typename F>
 cudaError_t with_lanes(int l, F&& f) {
-    if constexpr (LPC > 16) return cudaErrorInvalidValue;
-    else return l == LPC ? f(std::integral_constant<int, LPC>()) : with_lanes<LPC * 2>(l, f);
+    if constexpr (LPC > MOST) return cudaErrorInvalidValue;
+    else return l == LPC ? f(std::integral_constant<int, LPC>()) : with_lanes<LPC * 2, MOST>(l, f);
 }
 
 // Calls f with the lanes a channel and the states a lane, as constants.  Eight states a lane keep
@@ -398,7 +399,7 @@ cudaError_t with_lay(const ScanArgs& a, F&& f) {
     const int np = padded_states(a.N);
     if (np == 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>());
     if (np == 8) return f(integral_constant<int, 2>(), integral_constant<int, 4>());
-    return with_lanes(np / 8, [&](auto l) { return f(l, integral_constant<int, 8>()); });
+    return with_lanes<2, 8>(np / 8, [&](auto l) { return f(l, integral_constant<int, 8>()); });
 }
 int channels_of(const ScanArgs& a) {
     const int np = padded_states(a.N);
@@ -461,7 +462,7 @@ cudaError_t scan_fwd(const ScanArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t scan_step(const ScanArgs& a, cudaStream_t s) {
-    return with_lanes(padded_states(a.N) / 4, [&](auto ll) {
+    return with_lanes<1, 16>(padded_states(a.N) / 4, [&](auto ll) {
         constexpr int LPC = decltype(ll)::value, LC = NT / LPC;
         scan_step_kernel<T, LPC><<<(unsigned)(a.B * ((a.C + LC - 1) / LC)), NT, 0, s>>>(a);
         return cudaGetLastError();
