@@ -338,3 +338,39 @@ def test_parameter_gradients_of_many_rows(lz, dtype, case):
                 dw_post=grad * np.abs(f["scale"]) * unit * (a if gate == "last" else 1))
     for k, m in mags.items():
         check(g[k], ref[k], m.sum(0), 128 + T / 8, k)
+
+
+# ------------------------------------------------------------------------------- captured steps
+
+
+def test_captured_token_replays_on_new_tokens_and_slots(lz):
+    """A token's three calls captured into a graph, replayed on other tokens and slots (one idle, others
+    in another order), give the eager calls' bits in outputs and states."""
+    d = Draw(51, "bf16")
+    B, C, N, slots = 6, 40, 16, 9
+    w, v = d(C, 4, dtype=torch.float32)[0], d(C, dtype=torch.float32, shift=1.0)[0]
+    A = d.dev(-np.exp(d.rng.normal(size=(C, N))))[0]
+    conv, state = d(slots, 3, C)[0], d(slots, C, N, dtype=torch.float32)[0]
+    tokens = [dict(x=d(B, C)[0], dt=d(B, C, shift=-2.0)[0], Bm=d(B, 1, N)[0], Cm=d(B, 1, N)[0], z=d(B, C)[0], r=d(B, C)[0],
+                   slots=torch.tensor(d.rng.permutation(slots)[:B], device="cuda")) for _ in range(5)]
+    tokens[3]["slots"][2] = -1
+
+    def run(t, conv, state):
+        x = lz.lizard_conv_step(t["x"], w, v, conv, slots=t["slots"], act=1)
+        y = lz.lizard_scan_step(x, t["dt"], A, t["Bm"], t["Cm"], state, D=v, z=t["z"], slots=t["slots"])
+        return lz.lizard_block_norm_fwd(y, r=t["r"], w_post=v, scale=v, w_pre=v)
+
+    ec, es = conv.clone(), state.clone()
+    want = [run(t, ec, es) for t in tokens]
+    gc, gs = conv.clone(), state.clone()
+    at = {k: a.clone() for k, a in tokens[0].items()}
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(at, gc, gs)
+    for t, ref in zip(tokens, want):
+        for k in at:
+            at[k].copy_(t[k])
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert torch.equal(gc, ec) and torch.equal(gs, es)
