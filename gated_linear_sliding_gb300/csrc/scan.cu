@@ -9,11 +9,11 @@
 // tile's rows are already on their way into registers.
 //
 // The floor is the exponentials: one for each token, channel and state, 32 a cycle and SM (57 us
-// for 8192 x 4096 x 16; the bytes take 40 us).  An element takes nine instruction slots: the
+// for 8192 x 4096 x 16; the bytes take 40 us).  An element takes 8.5 instruction slots: the
 // exponential, two products, two multiply-adds (paired, half a slot each), a quarter each of four
-// loads from shared memory and its share of the staging (softplus, gate, conversions: 25 slots a
-// token and channel).  8 x 2048 x 4096 x 16 bf16: 445 us at 56% of the issue slots, no pipe above
-// 60%: the warps wait for one another's shared-memory loads and for the fixed latency of dependent
+// loads from shared memory and its share of the staging (softplus, gate, conversions: about 27 slots a
+// token and channel).  8 x 2048 x 4096 x 16 bf16: 453 us at 55% of the issue slots, no pipe above
+// 63%: the warps wait for one another's shared-memory loads and for the fixed latency of dependent
 // instructions; more warps with fewer registers, exponentials ahead by a group of tokens, tiles by
 // asynchronous copies, and single instead of paired arithmetic all measured the same or slower.
 #include <type_traits>

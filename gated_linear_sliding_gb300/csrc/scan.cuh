@@ -18,8 +18,8 @@ constexpr int SEG = 64;      // segments are whole multiples of this many tokens
 // so from 1e-4 to 1e-3 it errs upwards by a little more than the exponential alone errs downwards, and
 // elsewhere less.  With step sizes from 0.001 to 0.1 and rates from 1 to 16 the error of dA against
 // 64 bits falls from 1.9e-6 to 0.9e-6 on 8 x 2048 tokens, of the last states from 4.5e-7 to 2.5e-7 on
-// 8192.  Prompts, training and single tokens take the same decays, so that a state does not depend on
-// which of them moved it.
+// 8192.  Prompts, training and single tokens take the same decays, so that a state drifts alike
+// whichever of them moves it.
 constexpr float kDecayShift = 2e-8f;
 __device__ __forceinline__ f2 decay2(f2 d, f2 A2) { return exp2_2(fma2(d, A2, pack(kDecayShift, kDecayShift))); }
 

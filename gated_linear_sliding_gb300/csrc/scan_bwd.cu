@@ -19,8 +19,8 @@
 // two channels in opposite order, and neighbouring channels hold the two pairs of states in
 // opposite order, so that every lane sends its second one and keeps its first.
 //
-// 8 x 2048 x 4096 x 16 bf16: 1648 us, 235 instructions for the eight elements of a thread's token
-// at half of the issue slots; the floor is 218 us of bytes or 114 us of exponentials (each is taken
+// 8 x 2048 x 4096 x 16 bf16: 1656 us, 239 instructions for the eight elements of a thread's token
+// at half of the issue slots; the floor is 139 us of bytes or 114 us of exponentials (each is taken
 // 2.75 times).  Before: states of eight tokens in registers (two CTAs a SM) 2850 us, unpaired 3056
 // us.  The chunk ahead by asynchronous copies 1702 us, in registers 1853 us (spilled).
 //
