@@ -366,10 +366,11 @@ lizard_status lizard_decode_step_positions(const lizard_dims* dims, const int64_
  *     LIZARD_ERR_INVALID_ARG in the workspace's status word where a workspace is given, and the
  *     results of that call are not defined.
  *   - Outputs overlap neither inputs nor one another, but where a call says that they may.
- *   - A value that is not finite reaches only results of its own sequence and channel (Bm, Cm: of their
- *     group; dBm, dCm are sums over a group); these may be NaN where the formula gives an infinity.
- *     A step size of 0, as softplus gives for dt of minus infinity or the type's lowest value, lets
- *     the state pass unchanged.
+ *   - In the convolution and the scan, a value of a channel that is not finite reaches that channel's
+ *     results in its own sequence, its parameter gradients, and dBm and dCm (sums over a group); in
+ *     the norms, its row's results and the parameter gradients.  These may be NaN where the formula
+ *     gives an infinity.  A step size of 0, as softplus gives for dt of minus infinity or the type's
+ *     lowest value, lets the state pass unchanged.
  *   - A row of a batch has fewer than 2^31 tokens (offsets of elements are 64 bits wide).
  *   - L may be 0 (a packed batch of empty sequences): states are passed on, nothing else is
  *     written; parameter gradients are 0. */

@@ -374,3 +374,73 @@ def test_captured_token_replays_on_new_tokens_and_slots(lz):
         g.replay()
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
     assert torch.equal(gc, ec) and torch.equal(gs, es)
+
+
+# ------------------------------------------------------------------------------- values not finite
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("L,C,N", [(70, 37, 5), (600, 24, 16)])
+def test_a_channel_that_is_not_finite_stays_alone(lz, bad, L, C, N):
+    """One channel's inputs hold such values at some tokens: every other channel's results, forward and
+    backward, are the bits they are without them, over one segment and over several."""
+    d = Draw(61, "bf16")
+    t = {k: d(2, L, C)[0] for k in ("x", "dt", "z", "dy")}
+    Bm, Cm = d(2, L, 1, N)[0], d(2, L, 1, N)[0]
+    A = d.dev(-np.exp(d.rng.normal(size=(C, N))))[0]
+    w, v = d(C, 4, dtype=torch.float32)[0], d(C, dtype=torch.float32)[0]
+
+    def results(t):
+        h = torch.empty(2, C, N, device="cuda")
+        how = dict(D=v, z=t["z"], dt_bias=v)
+        y, st = lz.lizard_scan_fwd(t["x"], t["dt"], A, Bm, Cm, h_out=h, save_states=True, **how)
+        g = lz.lizard_scan_bwd(t["x"], t["dt"], A, Bm, Cm, t["dy"], st, **how)
+        c = lz.lizard_conv_fwd(t["x"], w, v, act=1)
+        gc = lz.lizard_conv_bwd(t["x"], w, v, t["dy"], act=1)
+        wide = [y, g["dx"], g["ddt"], g["dz"], c, gc["dx"]]
+        return wide, [h.transpose(0, 1), g["dA"], g["dD"], g["ddt_bias"], gc["dw"], gc["dbias"]]
+
+    want = results(t)
+    channel, keep = 11, [c for c in range(C) if c != 11]
+    for k in t:
+        t[k][:, ::13, channel] = bad
+    got = results(t)
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got[0], want[0])):
+        assert torch.equal(a[..., keep], b[..., keep]), i
+        assert not torch.isfinite(a[..., channel]).all(), i
+    for i, (a, b) in enumerate(zip(got[1], want[1])):
+        assert torch.equal(a[keep], b[keep]), i
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mask", ["inf", "lowest"])
+def test_masked_tokens(lz, dtype, mask):
+    """Tokens whose dt is minus infinity or the lowest value, all of a sequence's among them: outputs,
+    states and gradients against 64 bits, with the counts of roundings of the scan's tests."""
+    B, L, C, N = 3, 330, 16, 16
+    d = Draw(71, dtype)
+    low = -np.inf if mask == "inf" else torch.finfo(tdt(dtype)).min
+    raw = d.rng.normal(size=(B, L, C)).astype(np.float32)
+    raw[d.rng.random((B, L)) < 0.3] = low
+    raw[2] = low
+    dt, dtv = d.dev(raw, tdt(dtype))
+    (x, xv), (z, zv), (dy, dyv) = (d(B, L, C) for _ in range(3))
+    (Bm, Bv), (Cm, Cv) = d(B, L, 1, N), d(B, L, 1, N)
+    A, Av = d.dev(-np.exp(d.rng.normal(size=(C, N))))
+    (b, bv), (h0, hv) = d(C, dtype=torch.float32), d(B, C, N, dtype=torch.float32)
+    h = torch.empty_like(h0)
+    how = dict(z=z, dt_bias=b, h0=h0)
+    y, st = lz.lizard_scan_fwd(x, dt, A, Bm, Cm, h_out=h, save_states=True, **how)
+    g = lz.lizard_scan_bwd(x, dt, A, Bm, Cm, dy, st, **how)
+    torch.cuda.synchronize()
+    assert torch.equal(h[2], h0[2])
+    for i in range(B):
+        a = (xv[i], dtv[i], Av, Bv[i], Cv[i], np.zeros(C), zv[i], bv, hv[i])
+        up = (dyv[i], np.zeros((C, N)))
+        (ry, rh), (my, mh) = S.scan_fwd(*a), S.scan_fwd(*a, absolute=True)
+        check(y[i], ry, my, 16 * L + 64 + N, f"y {i}")
+        check(h[i], rh[-1], mh[-1], 16 * L + 64 + N, f"h {i}")
+        r, m = S.scan_bwd(*a, *up), S.scan_bwd(*a, *up, absolute=True)
+        for k, gk in (("dx", "dx"), ("ddt", "ddt"), ("dz", "dz"), ("dB", "dBm"), ("dC", "dCm")):
+            check(g[gk][i], r[k], m[k], 32 * L + 128 + N + 2 * C, f"{gk} {i}")
