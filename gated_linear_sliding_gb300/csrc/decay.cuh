@@ -1,0 +1,81 @@
+// Device helpers that the kernels of the linear attention with a decay for each head share: the walk
+// over a segment's tiles and the powers of a decay.
+#pragma once
+
+#include "heads.h"
+
+namespace lz {
+
+constexpr int kTile = 64;  // tokens of a tile: all pairs inside it are formed
+
+// log2 of a head's decay.  Minus infinity becomes a number whose every power but the 0th is 0 (0 times
+// infinity would be NaN); NaN stays.
+__device__ __forceinline__ float log2_decay(const float* log_decay, int64_t h) {
+    const float l = log_decay[h] * kLog2e;
+    return l < -1e4f ? -1e4f : l;
+}
+__device__ __forceinline__ float power(float l2, int64_t n) { return exp2f(l2 * (float)n); }
+
+// Up to kTile consecutive tokens of one sequence, in a row of the batch.
+struct Tile {
+    int64_t t0;
+    int n;
+    bool first, last;  // the walk enters the sequence with this tile, leaves it after it
+    int64_t seq;
+};
+
+// The tiles of a segment [lo, hi) of row b, forwards or backwards in time.  A tile ends where its
+// sequence does.
+struct Walk {
+    int64_t lo, hi, at, begin, end, seq;
+    bool rev;
+    __device__ __forceinline__ Walk(const Seqs& s, int64_t b, int64_t lo_, int64_t hi_, bool rev_)
+        : lo(lo_), hi(hi_), at(rev_ ? hi_ : lo_), begin(0), end(0), seq(0), rev(rev_) {
+        if (lo < hi) enter(s, b);
+    }
+    __device__ __forceinline__ void enter(const Seqs& s, int64_t b) {
+        const SeqAt q = seq_at(s, b, rev ? at - 1 : at);
+        begin = q.begin;
+        end = q.end;
+        seq = q.seq;
+    }
+    __device__ __forceinline__ bool next(const Seqs& s, int64_t b, Tile* t) {
+        if (rev ? at <= lo : at >= hi) return false;
+        if (rev ? at <= begin : at >= end) enter(s, b);
+        t->seq = seq;
+        if (!rev) {
+            const int64_t to = min64(min64(at + kTile, end), hi);
+            t->t0 = at;
+            t->n = (int)(to - at);
+            t->first = at == begin;
+            t->last = to == end;
+            at = to;
+        } else {
+            const int64_t from = max64(max64(at - kTile, begin), lo);
+            t->t0 = from;
+            t->n = (int)(at - from);
+            t->first = at == end;
+            t->last = from == begin;
+            at = from;
+        }
+        return true;
+    }
+};
+
+// The part of a segment whose tokens reach the state that leaves it: tokens [from, to), and whether
+// the sequence's own first state (not the segment before) is what they begin with.
+struct Reach {
+    int64_t from, to, seq;
+    bool whole;
+};
+__device__ __forceinline__ Reach reach(const Seqs& s, int64_t b, int64_t lo, int64_t hi, bool rev) {
+    Reach r;
+    const SeqAt q = seq_at(s, b, rev ? lo : hi - 1);
+    r.seq = q.seq;
+    r.from = rev ? lo : max64(q.begin, lo);
+    r.to = rev ? min64(q.end, hi) : hi;
+    r.whole = rev ? q.end <= hi : q.begin >= lo;
+    return r;
+}
+
+}  // namespace lz

@@ -48,7 +48,10 @@ EXPORTED = ["lizard_attn_fwd_workspace", "lizard_workspace_init", "lizard_attn_f
             "lizard_conv_fwd", "lizard_conv_bwd_workspace", "lizard_conv_bwd", "lizard_conv_step",
             "lizard_scan_fwd_workspace", "lizard_scan_states_bytes", "lizard_scan_fwd",
             "lizard_scan_bwd_workspace", "lizard_scan_bwd", "lizard_scan_step",
-            "lizard_block_norm_fwd", "lizard_block_norm_bwd_workspace", "lizard_block_norm_bwd"]
+            "lizard_block_norm_fwd", "lizard_block_norm_bwd_workspace", "lizard_block_norm_bwd",
+            "lizard_qk_rope_fwd", "lizard_qk_rope_bwd_workspace", "lizard_qk_rope_bwd",
+            "lizard_decay_attn_kernel", "lizard_decay_attn_fwd_workspace", "lizard_decay_attn_fwd",
+            "lizard_decay_attn_bwd_workspace", "lizard_decay_attn_bwd", "lizard_decay_attn_step"]
 
 
 class lizard_dims(ctypes.Structure):
@@ -75,6 +78,15 @@ class lizard_scan_dims(ctypes.Structure):
 class lizard_norm_dims(ctypes.Structure):
     _fields_ = _fields("T D groups ldo ldg ldr ldro ldn lddo lddg lddr", "eps_post eps_pre",
                        "dtype res_dtype act gate_first")
+
+
+class lizard_rope_dims(ctypes.Structure):
+    _fields_ = (_fields("B L Hq Hkv d rot axes", "", "") + [("section", ctypes.c_int64 * 4)]
+                + _fields("start ldq ldk ldqo ldko lddq lddk", "eps", "dtype norm neighbours"))
+
+
+class lizard_decay_dims(ctypes.Structure):
+    _fields_ = _fields("B L Hq Hkv dk dv nseq ldq ldk ldv ldo lddq lddk lddv", "scale", "dtype")
 
 
 class LizardError(RuntimeError):
@@ -146,7 +158,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.lizard_profile_events.restype = ctypes.c_int
     dims_of_call = {"conv": ctypes.POINTER(lizard_conv_dims),
                     "scan": ctypes.POINTER(lizard_scan_dims),
-                    "block": ctypes.POINTER(lizard_norm_dims)}
+                    "block": ctypes.POINTER(lizard_norm_dims),
+                    "qk": ctypes.POINTER(lizard_rope_dims),
+                    "decay": ctypes.POINTER(lizard_decay_dims)}
     sz = ctypes.c_size_t
     for name, rest in (("lizard_conv_fwd", [_VP] * 8 + [sz, _VP]),
                        ("lizard_conv_bwd", [_VP] * 12 + [sz, _VP]),
@@ -158,7 +172,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
                        ("lizard_block_norm_bwd", [_VP] * 15 + [sz, _VP]),
                        ("lizard_conv_bwd_workspace", None), ("lizard_scan_fwd_workspace", None),
                        ("lizard_scan_states_bytes", None), ("lizard_scan_bwd_workspace", None),
-                       ("lizard_block_norm_bwd_workspace", None)):
+                       ("lizard_block_norm_bwd_workspace", None),
+                       ("lizard_qk_rope_fwd", [_VP] * 9), ("lizard_qk_rope_bwd_workspace", None),
+                       ("lizard_qk_rope_bwd", [_VP] * 13 + [sz, _VP]),
+                       ("lizard_decay_attn_fwd_workspace", None),
+                       ("lizard_decay_attn_bwd_workspace", None),
+                       ("lizard_decay_attn_kernel", []),
+                       ("lizard_decay_attn_fwd", [_VP] * 9 + [sz, _VP]),
+                       ("lizard_decay_attn_bwd", [_VP] * 13 + [sz, _VP]),
+                       ("lizard_decay_attn_step", [_VP] * 5 + [ctypes.c_int64] + [_VP] * 3 + [sz, _VP])):
         fn = getattr(lib, name)
         fn.argtypes = [dims_of_call[name.split("_")[1]]] + (rest or [])
         fn.restype = sz if rest is None else ctypes.c_int
@@ -1028,3 +1050,203 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
                                       _ptr(dscale), _ptr(dw_pre), *_ws(workspace), _stream_of(o))
     _check(st, "lizard_block_norm_bwd")
     return dict(do=do, dgate=dgate, dr=dr, dw_post=dw_post, dscale=dscale, dw_pre=dw_pre)
+
+
+# ---- queries and keys in front of a mixer, and linear attention with a decay for each head ----------
+
+
+def _qk_rope_inputs(q, k, freqs, positions, sections, start, w_q, w_k, norm, eps, neighbours):
+    """lizard_rope_dims of the inputs, the shapes of q and k, and the addresses of w_q, w_k, freqs,
+    positions."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, L, heads, d]")
+    shape = tuple(q.shape)
+    B, L, Hq, d = shape
+    kshape = (B, L, 0, d) if k is None else (B, L, k.shape[-2], d)
+    rot = 0 if freqs is None else 2 * freqs.shape[0]
+    axes = 1 if sections is None else len(sections)
+    if not 1 <= axes <= 4:
+        raise ValueError("sections: one to four axes")
+    if positions is not None:
+        want = (B, L) if sections is None else (B, L, axes)
+        if positions.shape != want or positions.dtype is not torch.int64 or not positions.is_cuda or not positions.is_contiguous():
+            _need(positions, "positions", want, torch.int64)
+    dims = lizard_rope_dims(B, L, Hq, kshape[2], d, rot, axes, start=start, eps=eps, dtype=_dtype_code(q),
+                            norm=1 if norm else 0, neighbours=1 if neighbours else 0)
+    if sections is not None:
+        dims.section[:axes] = [int(n) for n in sections]
+    return dims, shape, kshape, (_need_f32(w_q, "w_q", (d,)), _need_f32(w_k, "w_k", (d,)),
+                                 _need_f32(freqs, "freqs", (rot // 2,)), _ptr(positions))
+
+
+def lizard_qk_rope_fwd(q, k, freqs, *, positions=None, sections=None, start: int = 0, w_q=None, w_k=None,
+                       norm: bool = True, eps: float = 1e-6, neighbours: bool = False, q_out=None,
+                       k_out=None, stream=None):
+    """Norm of each head's query and key and rotation by position: q [B, L, Hq, d], k [B, L, Hkv, d] (or
+    None); freqs [rot / 2] fp32 (None: no rotation), radians a position.  positions [B, L] int64, or
+    [B, L, axes] with sections (the number of pairs that turn with each axis); None: token t of a row is
+    at start + t.  w_q, w_k [d] fp32.  Returns (q_out, k_out), which may be q and k."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_qk_rope_fwd, locals())
+    dims, shape, kshape, params = _qk_rope_inputs(q, k, freqs, positions, sections, start, w_q, w_k, norm, eps, neighbours)
+    tp = q.dtype
+    dims.ldq = _ld(q, "q", shape, tp)
+    if q_out is None:
+        q_out = q.new_empty(shape)
+    else:
+        dims.ldqo = _ld(q_out, "q_out", shape, tp)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out needs k")
+    else:
+        dims.ldk = _ld(k, "k", kshape, tp)
+        if k_out is None:
+            k_out = q.new_empty(kshape)
+        else:
+            dims.ldko = _ld(k_out, "k_out", kshape, tp)
+    st = load().lizard_qk_rope_fwd(ctypes.byref(dims), q.data_ptr(), _ptr(k), *params, q_out.data_ptr(),
+                                   _ptr(k_out), _stream_of(q))
+    _check(st, "lizard_qk_rope_fwd")
+    return q_out, k_out
+
+
+def lizard_qk_rope_bwd_workspace(dims) -> int:
+    return int(load().lizard_qk_rope_bwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_qk_rope_bwd(q, k, freqs, dq_out, dk_out, *, positions=None, sections=None, start: int = 0,
+                       w_q=None, w_k=None, norm: bool = True, eps: float = 1e-6, neighbours: bool = False,
+                       dq=None, dk=None, workspace=None, stream=None):
+    """Gradients dq, dk, dw_q, dw_k of lizard_qk_rope_fwd against dq_out and dk_out, from the forward's
+    inputs (None for an absent k or weight).  dq may be dq_out, dk may be dk_out."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_qk_rope_bwd, locals())
+    dims, shape, kshape, params = _qk_rope_inputs(q, k, freqs, positions, sections, start, w_q, w_k, norm, eps, neighbours)
+    tp = q.dtype
+    if (k is None) != (dk_out is None) or (k is None and dk is not None):
+        raise ValueError("dk_out and dk go with k")
+    dims.ldq, dims.ldqo = _ld(q, "q", shape, tp), _ld(dq_out, "dq_out", shape, tp)
+    if dq is None:
+        dq = q.new_empty(shape)
+    else:
+        dims.lddq = _ld(dq, "dq", shape, tp)
+    if k is not None:
+        dims.ldk, dims.ldko = _ld(k, "k", kshape, tp), _ld(dk_out, "dk_out", kshape, tp)
+        if dk is None:
+            dk = q.new_empty(kshape)
+        else:
+            dims.lddk = _ld(dk, "dk", kshape, tp)
+    dw_q = None if w_q is None else torch.empty_like(w_q)
+    dw_k = None if w_k is None else torch.empty_like(w_k)
+    lib = load()
+    workspace = _scratch(workspace, lib.lizard_qk_rope_bwd_workspace(ctypes.byref(dims)), q.device)
+    st = lib.lizard_qk_rope_bwd(ctypes.byref(dims), q.data_ptr(), _ptr(k), *params, dq_out.data_ptr(), _ptr(dk_out),
+                                dq.data_ptr(), _ptr(dk), _ptr(dw_q), _ptr(dw_k), *_ws(workspace), _stream_of(q))
+    _check(st, "lizard_qk_rope_bwd")
+    return dict(dq=dq, dk=dk, dw_q=dw_q, dw_k=dw_k)
+
+
+def _decay_inputs(q, k, v, log_decay, scale, nseq):
+    """lizard_decay_dims of the inputs, and the addresses of q, k, v, log_decay."""
+    tp, lead = q.dtype, tuple(q.shape[:-2])
+    n = len(lead)
+    Hq, dk = q.shape[-2:]
+    Hkv, dv = v.shape[-2:]
+    dims = lizard_decay_dims(lead[0], lead[1] if n == 2 else 1, Hq, Hkv, dk, dv, nseq,
+                             _ld(q, "q", lead + (Hq, dk), tp, n), _ld(k, "k", lead + (Hkv, dk), tp, n),
+                             _ld(v, "v", lead + (Hkv, dv), tp, n), 0, 0, 0, 0,
+                             dk ** -0.5 if scale is None else scale, _dtype_code(q))
+    return dims, (q.data_ptr(), k.data_ptr(), v.data_ptr(), _need_f32(log_decay, "log_decay", (Hkv,)))
+
+
+def lizard_decay_attn_kernel(dims) -> int:
+    return int(load().lizard_decay_attn_kernel(ctypes.byref(dims)))
+
+
+def lizard_decay_attn_fwd_workspace(dims) -> int:
+    return int(load().lizard_decay_attn_fwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_decay_attn_bwd_workspace(dims) -> int:
+    return int(load().lizard_decay_attn_bwd_workspace(ctypes.byref(dims)))
+
+
+def lizard_decay_attn_fwd(q, k, v, log_decay, *, scale=None, s0=None, s_out=None, cu_seqlens=None, o=None,
+                          workspace=None, stream=None):
+    """Linear attention with a decay for each head, S[t] = exp(log_decay) S[t-1] + k[t] v[t]^T and o[t] =
+    scale q[t] S[t]: q [B, L, Hq, dk], k [B, L, Hkv, dk], v [B, L, Hkv, dv], log_decay [Hkv] fp32 (at most
+    0); scale is 1 / sqrt(dk) unless given.  Returns o [B, L, Hq, dv].  s0, s_out [B or sequences, Hkv,
+    dk, dv] fp32: the states before and after (s_out may be s0)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_decay_attn_fwd, locals())
+    if q.dim() != 4:
+        raise ValueError("q must be [B, L, heads, dk]")
+    B, L = q.shape[:2]
+    nseq, cu = _packed(cu_seqlens, B, L, q.device)
+    dims, ptrs = _decay_inputs(q, k, v, log_decay, scale, nseq)
+    shape = (B, L, dims.Hq, dims.dv)
+    if o is None:
+        o = q.new_empty(shape)
+    else:
+        dims.ldo = _ld(o, "o", shape, q.dtype)
+    states = (nseq or B, dims.Hkv, dims.dk, dims.dv)
+    lib = load()
+    workspace = _scratch(workspace, lib.lizard_decay_attn_fwd_workspace(ctypes.byref(dims)), q.device)
+    st = lib.lizard_decay_attn_fwd(ctypes.byref(dims), *ptrs, _need_f32(s0, "s0", states), _ptr(cu), o.data_ptr(),
+                                   _need_f32(s_out, "s_out", states), *_ws(workspace), _stream_of(q))
+    _check(st, "lizard_decay_attn_fwd")
+    return o
+
+
+def lizard_decay_attn_bwd(q, k, v, log_decay, do, *, scale=None, s0=None, ds_out=None, ds0=None,
+                          cu_seqlens=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients dq, dk, dv of lizard_decay_attn_fwd's o against do [B, L, Hq, dv], from the same inputs
+    (log_decay has none).  ds_out is the gradient of s_out, ds0 (if given) receives that of s0 (it may be
+    ds_out)."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_decay_attn_bwd, locals())
+    if q.dim() != 4:
+        raise ValueError("q must be [B, L, heads, dk]")
+    B, L = q.shape[:2]
+    nseq, cu = _packed(cu_seqlens, B, L, q.device)
+    dims, ptrs = _decay_inputs(q, k, v, log_decay, scale, nseq)
+    tp = q.dtype
+    dims.ldo = _ld(do, "do", (B, L, dims.Hq, dims.dv), tp)
+
+    def out(t, name, like):
+        shape = tuple(like.shape)
+        return (like.new_empty(shape), 0) if t is None else (t, _ld(t, name, shape, tp))
+
+    dq, dims.lddq = out(dq, "dq", q)
+    dk, dims.lddk = out(dk, "dk", k)
+    dv, dims.lddv = out(dv, "dv", v)
+    states = (nseq or B, dims.Hkv, dims.dk, dims.dv)
+    lib = load()
+    workspace = _scratch(workspace, lib.lizard_decay_attn_bwd_workspace(ctypes.byref(dims)), q.device)
+    st = lib.lizard_decay_attn_bwd(ctypes.byref(dims), *ptrs, _need_f32(s0, "s0", states), _ptr(cu), do.data_ptr(),
+                                   _need_f32(ds_out, "ds_out", states), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                   _need_f32(ds0, "ds0", states), *_ws(workspace), _stream_of(q))
+    _check(st, "lizard_decay_attn_bwd")
+    return dict(dq=dq, dk=dk, dv=dv, ds0=ds0)
+
+
+def lizard_decay_attn_step(q, k, v, log_decay, state, *, scale=None, slots=None, o=None, workspace=None,
+                           stream=None):
+    """One token for each of B sequences: o [B, Hq, dv] from q [B, Hq, dk], k [B, Hkv, dk], v [B, Hkv, dv];
+    state [slots, Hkv, dk, dv] fp32 is moved on IN PLACE.  slots as for lizard_conv_step."""
+    if stream is not _HERE and (stream is not None or _gpus() > 1):
+        return _placed(lizard_decay_attn_step, locals())
+    if q.dim() != 3:
+        raise ValueError("q must be [B, heads, dk]")
+    dims, ptrs = _decay_inputs(q, k, v, log_decay, scale, 0)
+    B = dims.B
+    if o is None:
+        o = q.new_empty((B, dims.Hq, dims.dv))
+    else:
+        dims.ldo = _ld(o, "o", (B, dims.Hq, dims.dv), q.dtype, 1)
+    nslots = state.shape[0]
+    st = load().lizard_decay_attn_step(ctypes.byref(dims), *ptrs,
+                                       _need_f32(state, "state", (nslots, dims.Hkv, dims.dk, dims.dv)), nslots,
+                                       _slots(slots, B), o.data_ptr(), *_ws(workspace), _stream_of(q))
+    _check(st, "lizard_decay_attn_step")
+    return o

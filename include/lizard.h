@@ -540,6 +540,119 @@ lizard_status lizard_block_norm_bwd(const lizard_norm_dims* dims, const void* o,
                                     float* dscale, float* dw_pre, void* workspace,
                                     size_t ws_bytes, void* stream);
 
+/* ---- Queries and keys in front of a mixer, and linear attention with a decay for each head ----
+ *
+ * lizard_qk_rope_* stands between lizard_qkvg_proj and a mixer: the norm of each head's query and key
+ * and the rotation by its position, in one pass.  lizard_decay_attn_* is a third constant-memory
+ * mixer: linear attention whose state decays by a constant rate for each head.  The conventions of
+ * the selective block hold (strided token rows with dense heads, packed batches, slots, status words,
+ * outputs that overlap nothing but where a call says so). */
+
+/* Sizes of the norms and the rotation: B rows of L tokens with Hq query and Hkv key heads (Hkv may be
+ * 0) of d values, 1 <= d <= 512.  The first `rot` values of a head are rotated in pairs (even, 0 <=
+ * rot <= d): (i, i + rot/2), or (2i, 2i+1) with neighbours != 0.  Positions have `axes` coordinates, 1
+ * to 4: pairs [0, section[0]) turn with the first one, the next section[1] with the second, and so
+ * on; the sections add up to rot / 2 (with one axis they are not read).  norm != 0: the RMS norm over
+ * a head's d values comes first. */
+typedef struct {
+    int64_t B, L, Hq, Hkv, d, rot, axes;
+    int64_t section[4];
+    int64_t start;              /* without positions: token t of each row is at start + t */
+    int64_t ldq, ldk;           /* token distances of q and k */
+    int64_t ldqo, ldko;         /* of q_out and k_out (backward: of dq_out and dk_out) */
+    int64_t lddq, lddk;         /* of dq and dk (backward) */
+    float eps;
+    int32_t dtype, norm, neighbours;
+} lizard_rope_dims;
+
+/* For each head x of q (and of k, with w_k), with a[i] = positions[axis(i)] freqs[i]:
+ *   n = w x / sqrt(mean(x^2) + eps)      (w NULL: 1; without norm n = x, and w must be NULL)
+ *   (y1, y2) = (n1 cos a - n2 sin a, n2 cos a + n1 sin a) for each pair;   y = n beyond rot.
+ *   q, q_out   [B, L, Hq, d];   k, k_out [B, L, Hkv, d] (NULL exactly when Hkv is 0);
+ *   w_q, w_k   [d] fp32 or NULL;   freqs [rot / 2] fp32, radians a position (NULL when rot is 0);
+ *   positions  NULL, or a DEVICE array [B, L, axes] of int64 (any sign), read when the kernel runs.
+ * The angle is formed modulo one turn from the product of the position and the frequency as a 64-bit
+ * fraction of a turn: far positions lose nothing.  A frequency that is not finite gives NaN.
+ * q_out may be q and k_out may be k (same distances).  Values are rounded once, at the end. */
+lizard_status lizard_qk_rope_fwd(const lizard_rope_dims* dims, const void* q, const void* k,
+                                 const float* w_q, const float* w_k, const float* freqs,
+                                 const int64_t* positions, void* q_out, void* k_out, void* stream);
+
+/* Bytes of device workspace lizard_qk_rope_bwd needs (0 for invalid dims): the status word and the
+ * partial sums of the weights' gradients. */
+size_t lizard_qk_rope_bwd_workspace(const lizard_rope_dims* dims);
+
+/* Exact gradient of lizard_qk_rope_fwd from its inputs (nothing is kept by the forward; without norm
+ * q and k are not read and may be NULL).
+ *   dq_out, dk_out  gradients of q_out, k_out;   dq, dk  as q, k (dq may be dq_out, dk may be dk_out,
+ *   same distances);   dw_q, dw_k [d] fp32, NULL exactly when the weight is.  Every output is
+ *   overwritten.  Reductions use a fixed order (deterministic). */
+lizard_status lizard_qk_rope_bwd(const lizard_rope_dims* dims, const void* q, const void* k,
+                                 const float* w_q, const float* w_k, const float* freqs,
+                                 const int64_t* positions, const void* dq_out, const void* dk_out,
+                                 void* dq, void* dk, float* dw_q, float* dw_k, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* Sizes of linear attention with a decay for each head: B sequences of L tokens (or nseq packed
+ * ones), Hq query heads on Hkv states (Hq % Hkv == 0; query head h reads state h / (Hq / Hkv)), keys
+ * of dk and values of dv values, 1 <= dk, dv <= 192; scale multiplies the outputs (any finite number). */
+typedef struct {
+    int64_t B, L, Hq, Hkv, dk, dv, nseq;
+    int64_t ldq, ldk, ldv, ldo;     /* token distances of q, k, v; o and do */
+    int64_t lddq, lddk, lddv;       /* of dq, dk, dv (backward) */
+    float scale;
+    int32_t dtype;
+} lizard_decay_dims;
+
+/* Which kernels serve these sizes: 1 = tensor cores (bf16, dk and dv multiples of 8 up to 128, token
+ * distances multiples of 8), 0 = fp32 arithmetic (every other shape), -1 = invalid sizes.  Pure host
+ * query. */
+int lizard_decay_attn_kernel(const lizard_decay_dims* dims);
+
+/* Bytes of device workspace lizard_decay_attn_fwd needs (0 for invalid dims): the status word, plus,
+ * where there are too few sequences and heads to fill the GPU and the time axis is cut into segments,
+ * one fp32 state for each of them. */
+size_t lizard_decay_attn_fwd_workspace(const lizard_decay_dims* dims);
+
+/* For each sequence and state head h, with query heads q of that state:
+ *   S[t] = exp(log_decay[h]) S[t-1] + k[t] v[t]^T,      o[t] = scale q[t] S[t].
+ *   q [B, L, Hq, dk];  k [B, L, Hkv, dk];  v [B, L, Hkv, dv];  o [B, L, Hq, dv];
+ *   log_decay [Hkv] fp32, at most 0 (constants of the model; minus infinity: a token sees itself
+ *            only; above 0 states grow and may overflow);
+ *   s0       [B or nseq, Hkv, dk, dv] fp32 or NULL (zero): the state before each first token;
+ *   s_out    likewise or NULL: the state after the last token (s0's, or zero, for an empty
+ *            sequence); may be the same array as s0;
+ *   workspace, ws_bytes >= lizard_decay_attn_fwd_workspace(dims).
+ * A value that is not finite reaches results of its own sequence and state head only, and there
+ * those of up to 63 tokens before it (all products of a chunk of 64 tokens are formed). */
+lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q, const void* k,
+                                    const void* v, const float* log_decay, const float* s0,
+                                    const int64_t* cu_seqlens, void* o, float* s_out,
+                                    void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace lizard_decay_attn_bwd needs (0 for invalid dims). */
+size_t lizard_decay_attn_bwd_workspace(const lizard_decay_dims* dims);
+
+/* Exact gradient of lizard_decay_attn_fwd's o (and of s_out) from its inputs (nothing is kept by the
+ * forward; s0 and cu_seqlens as then; log_decay has no gradient).
+ *   d_o [B, L, Hq, dv]; ds_out [B or nseq, Hkv, dk, dv] fp32 or NULL: gradients of o and of s_out;
+ *   dq, dk, dv as q, k, v (dk, dv: the sums over the query heads of a state); ds0 [B or nseq, Hkv, dk,
+ *   dv] fp32 or NULL; may be the same array as ds_out.  Every output is overwritten.  Results do not
+ *   depend on the order in which CTAs run (deterministic). */
+lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q, const void* k,
+                                    const void* v, const float* log_decay, const float* s0,
+                                    const int64_t* cu_seqlens, const void* d_o, const float* ds_out,
+                                    void* dq, void* dk, void* dv, float* ds0, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
+/* One token for each of B sequences (dims.L and nseq are ignored): q [B, Hq, dk], k [B, Hkv, dk],
+ * v [B, Hkv, dv], o [B, Hq, dv]; state [nslots, Hkv, dk, dv] fp32 is moved on by one token IN PLACE.
+ * slots, nslots and workspace as for lizard_conv_step. */
+lizard_status lizard_decay_attn_step(const lizard_decay_dims* dims, const void* q, const void* k,
+                                     const void* v, const float* log_decay, float* state,
+                                     int64_t nslots, const int64_t* slots, void* o,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read the device status word of `workspace` and clear it.
  * Returns LIZARD_OK or the first error a kernel recorded (e.g. LIZARD_ERR_TIMEOUT). */
 lizard_status lizard_read_device_status(void* workspace, void* stream);
