@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
         const int64_t lo = s * p.seg_len, hi = min64(lo + p.seg_len, p.seqs.L);
         pass[s] = reach(p.seqs, b, lo, hi, p.rev).whole ? -1.0f : power(l2, hi - lo);
     }
+    grid_dep_launch();
     grid_dep_wait();
     __syncthreads();
     if (e >= size) return;
@@ -343,18 +344,22 @@ cudaError_t run_pass(const DecayPass& p, cudaStream_t s) {
 
 cudaError_t run_join(const DecayPass& p, float* recs, cudaStream_t s) {
     const int64_t size = (int64_t)p.dx * p.dz;
-    decay_join_kernel<<<(unsigned)(p.units * ((size + 255) / 256)), 256, sizeof(float) * p.nseg, s>>>(p, recs);
-    return cudaGetLastError();
+    const cudaError_t e = launch_dependent(decay_join_kernel, dim3((unsigned)(p.units * ((size + 255) / 256))), dim3(256),
+                                           sizeof(float) * p.nseg, s, p, recs);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // The states in front of the segments, [units, nseg, dk, dv], from a pass that is not transposed.
 cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, cudaStream_t s) {
     if (p.nseg == 1) return cudaSuccess;
-    const cudaError_t e = a.dtype == LIZARD_F32 ? run_ends<float>(p, recs, s) : run_ends<__nv_bfloat16>(p, recs, s);
+    const cudaError_t e = decay_uses_tc(a)          ? decay_tc_ends(p, recs, s)
+                          : a.dtype == LIZARD_F32 ? run_ends<float>(p, recs, s)
+                                                  : run_ends<__nv_bfloat16>(p, recs, s);
     return e != cudaSuccess ? e : run_join(p, recs, s);
 }
 
 cudaError_t outputs(const DecayArgs& a, const DecayPass& p, cudaStream_t s) {
+    if (decay_uses_tc(a)) return decay_tc_pass(p, s);
     return a.dtype == LIZARD_F32 ? run_pass<float>(p, s) : run_pass<__nv_bfloat16>(p, s);
 }
 
@@ -377,10 +382,11 @@ cudaError_t own_first_states(const DecayArgs& a, DecayPass* p, float* copy, cuda
 }
 
 // Segments of whole tiles: one where sequences, heads and slices already make a CTA a SM, else as many
-// as that takes.
+// as that takes (fp32 arithmetic: two CTAs a SM).
 void cut(const DecayArgs& a, DecayPass* p) {
-    const int64_t ctas = p->units * ((a.dv + ZS - 1) / ZS), tiles = (a.seqs.L + kTile - 1) / kTile;
-    int64_t n = ctas >= 152 ? 1 : 304 / ctas;
+    const bool tensor = decay_uses_tc(a);
+    const int64_t ctas = tensor ? p->units : p->units * ((a.dv + ZS - 1) / ZS), tiles = (a.seqs.L + kTile - 1) / kTile;
+    int64_t n = tensor ? 152 / ctas : ctas >= 152 ? 1 : 304 / ctas;
     n = n < tiles ? n : tiles;
     n = n < 1 ? 1 : n;
     const int64_t per = (tiles + n - 1) / n;
@@ -553,8 +559,6 @@ cudaError_t step_typed(const DecayArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
-
-bool decay_uses_tc(const DecayArgs&) { return false; }
 
 // Forward: the states of its segments; backward: those of S and of dS.  Behind them, with segments, a
 // copy of the sequences' first states for calls whose last states overwrite them.

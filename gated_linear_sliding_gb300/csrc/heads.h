@@ -83,5 +83,8 @@ struct DecayPass {
     Seqs seqs;
     WsHeader* header;
 };
+// On the tensor cores: the segments' own end states (of a pass that is not transposed), and a pass.
+cudaError_t decay_tc_ends(const DecayPass& p, float* recs, cudaStream_t s);
+cudaError_t decay_tc_pass(const DecayPass& p, cudaStream_t s);
 
 }  // namespace lz
