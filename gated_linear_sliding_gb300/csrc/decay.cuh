@@ -16,44 +16,43 @@ __device__ __forceinline__ float log2_decay(const float* log_decay, int64_t h) {
 }
 __device__ __forceinline__ float power(float l2, int64_t n) { return exp2f(l2 * (float)n); }
 
-// Up to kTile consecutive tokens of one sequence, in a row of the batch.
+// Up to a tile's length of consecutive tokens of one sequence, in a row of the batch.
 struct Tile {
-    int64_t t0;
-    int n;
+    int t0, n;
     bool first, last;  // the walk enters the sequence with this tile, leaves it after it
-    int64_t seq;
+    int seq;
 };
 
 // The tiles of a segment [lo, hi) of row b, forwards or backwards in time.  A tile ends where its
-// sequence does.
+// sequence does.  (A row has fewer than 2^31 tokens, and so has a batch sequences.)
 struct Walk {
-    int64_t lo, hi, at, begin, end, seq;
+    int lo, hi, at, begin, end, seq, tile;
     bool rev;
-    __device__ __forceinline__ Walk(const Seqs& s, int64_t b, int64_t lo_, int64_t hi_, bool rev_)
-        : lo(lo_), hi(hi_), at(rev_ ? hi_ : lo_), begin(0), end(0), seq(0), rev(rev_) {
+    __device__ __forceinline__ Walk(const Seqs& s, int64_t b, int64_t lo_, int64_t hi_, bool rev_, int tile_ = kTile)
+        : lo((int)lo_), hi((int)hi_), at((int)(rev_ ? hi_ : lo_)), begin(0), end(0), seq(0), tile(tile_), rev(rev_) {
         if (lo < hi) enter(s, b);
     }
     __device__ __forceinline__ void enter(const Seqs& s, int64_t b) {
         const SeqAt q = seq_at(s, b, rev ? at - 1 : at);
-        begin = q.begin;
-        end = q.end;
-        seq = q.seq;
+        begin = (int)q.begin;
+        end = (int)q.end;
+        seq = (int)q.seq;
     }
     __device__ __forceinline__ bool next(const Seqs& s, int64_t b, Tile* t) {
         if (rev ? at <= lo : at >= hi) return false;
         if (rev ? at <= begin : at >= end) enter(s, b);
         t->seq = seq;
         if (!rev) {
-            const int64_t to = min64(min64(at + kTile, end), hi);
+            const int to = min(min(at + tile, end), hi);
             t->t0 = at;
-            t->n = (int)(to - at);
+            t->n = to - at;
             t->first = at == begin;
             t->last = to == end;
             at = to;
         } else {
-            const int64_t from = max64(max64(at - kTile, begin), lo);
+            const int from = max(max(at - tile, begin), lo);
             t->t0 = from;
-            t->n = (int)(at - from);
+            t->n = at - from;
             t->first = at == end;
             t->last = from == begin;
             at = from;

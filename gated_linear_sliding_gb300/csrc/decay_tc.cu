@@ -2,20 +2,24 @@
 // keys and values of up to 128 values.
 //
 // One kernel runs every pass (DecayPass: the outputs, dq, and backwards in time dv and dk).  A CTA walks a
-// segment of one state head in tiles of 64 tokens.  With X up to two query heads of a tile as 128 rows, Y and
-// Z the tile's 64 tokens and S the state in front of it, an item is
-//   P = (X Y^T) (.) e^(l |i - j|)          [128 x 64], masked to the tokens before (rev: behind)
-//   O = e^(l (i+1)) (X S) + P Z            [128 x dz]
-// and a tile moves the state on:  S' = e^(l n) S + Y~^T Z,  Y~[j] = e^(l (n-1-j)) Y[j].
-// Every power is of a difference of places, so all factors lie in [0, 1].
+// segment of one state head in chunks.  128 rows of x make an item with 64 of y and z: two query heads of
+// a chunk of 64 tokens, or one head of a chunk of 128 tokens where a state has one head of x (so that the MMAs'
+// 128 rows are used), with 64 of the chunk's tokens of y and z in turn.  With S the state in front of the chunk
+//   P = (X Y^T) (.) e^(l |i - j|), masked to the tokens before (rev: behind),   O = e^(l (i+1)) X S + P Z
+// and a chunk of n tokens moves the state on:  S' = e^(l n) S + Y~^T Z,  Y~[j] = e^(l (n-1-j)) Y[j].
+//
+// The decay of a pair is e^(l (i-r)) e^(l (r-j)) with r in the middle of the chunk: the second factor is a
+// constant for each column of P, the first one scales the finished row of O, and the operand copy of S takes
+// e^(l (r+1)).  Where all of these lie within 2^32 of 1, as they do while a token keeps 0.71 of the state (a
+// half, in chunks of 64), nothing else is needed.  Heads that decay faster take each pair's power of the difference (at most 1) and scale X S before P Z is added.
 //
 // Roundings: P and the operand copy of S are bf16 (a relative 2^-8 of the terms, as the output's own).  S itself
 // stays in fp32 in TMEM, and Y~ goes in as a high and a low bf16 part (2^-17), since S leaves the call in fp32
 // and what is rounded there would stay for the rest of the sequence.
 //
-// Warps: 0-7 the pairs' weights, the state part's scale and the outputs (a thread holds one row's 32 of the 64
-// pairs and 64 of the 128 output columns); 8-11 the state (a row of S to a thread; Y~); 12 the copies; 13 the
-// MMAs of the items; 14 those of the state.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
+// Warps: 0-7 the pairs' weights and the outputs (a thread holds one row's 32 of 64 pairs and 64 of 128 output
+// columns); 8-11 the state (a row of S to a thread; Y~); 12 the copies; 13 the MMAs of the scores, 14 of the
+// state, 15 of the outputs.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -31,31 +35,34 @@ using tc::kdesc;
 using tc::mndesc;
 
 constexpr int kMathWarps = 8;
-constexpr int kThreads = 32 * 15;
+constexpr int kThreads = 32 * 16;
 constexpr uint32_t kBox = 8192;  // a box of 64 rows x 64 columns of bf16
 
 struct TcArgs {
-    CUtensorMap x, y, z;
+    CUtensorMap x, y, z, out;
     DecayPass p;
 };
 
-// Shared memory: XST stages of XB boxes of x, YST of y and z, Y~, the state's operand copy.
-template <int XST_, int XB_, int YST_, bool REV_>
+// Shared memory: XST stages of x, YST of y and z, Y~, the state's operand copy, and rows of the output on
+// their way out (OWN), which otherwise go through the stage that x came in.
+template <int XST_, int YST_, bool OWN_, bool REV_>
 struct Layout {
-    static constexpr int XST = XST_, XB = XB_, YST = YST_;
-    static constexpr bool REV = REV_;
+    static constexpr int XST = XST_, YST = YST_;
+    static constexpr bool OWN = OWN_, REV = REV_;
     static constexpr uint32_t X = 0;
-    static constexpr uint32_t YZ = XST * XB * kBox;
+    static constexpr uint32_t OUT = XST * 4 * kBox;
+    static constexpr uint32_t YZ = OUT + (OWN ? 4 * kBox : 0);
     static constexpr uint32_t KT = YZ + YST * 4 * kBox;  // high part, low part
     static constexpr uint32_t ST = KT + 4 * kBox;
-    static constexpr uint32_t TABLE = ST + 4 * kBox;     // powers 0 .. 64, and times in_scale
-    static constexpr uint32_t BARS = TABLE + 2 * 72 * 4;
-    static constexpr uint32_t BYTES = BARS + 320 + 1024;
+    static constexpr uint32_t TABLE = ST + 4 * kBox;     // powers 0 .. 128, and the columns' factors
+    static constexpr uint32_t BARS = TABLE + (132 + 128) * 4;
+    static constexpr uint32_t BYTES = BARS + 304 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
-// forwards: tiles of two heads of x stream past one of y and z; backwards: heads of y and z past one of x
-using Forwards = Layout<3, 4, 2, false>;
-using Backwards = Layout<2, 2, 4, true>;
+// many rows of x for each of y and z; many of y and z for each of x (a sum over heads)
+template <bool REV>
+using Wide = Layout<2, 2, true, REV>;
+using Deep = Layout<2, 3, false, true>;
 
 // Waits with a limit.  When one runs out it is reported once and every role leaves.
 struct Waiter {
@@ -99,13 +106,19 @@ __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
 __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt, int n, float f, int tid) {
     const int tok = tid & 63, half = tid >> 6;
     const uint32_t from = ys + half * kBox, to = kt + half * kBox;
+    uint32_t w[8][4];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[c][i] = 0;
+        if (tok < n) ld_shared_v4(from + sw128(tok, c), w[c][0], w[c][1], w[c][2], w[c][3]);
+    }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         const uint32_t off = sw128(tok, c);
-        uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
-        if (tok < n) ld_shared_v4(from + off, w[0], w[1], w[2], w[3]);
+        uint32_t hi[4], lo[4];
         float v[8];
-        tc::unpack8(w[0], w[1], w[2], w[3], v);
+        tc::unpack8(w[c][0], w[c][1], w[c][2], w[c][3], v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::split2(v[2 * i] * f, v[2 * i + 1] * f, hi[i], lo[i]);
         st_shared_v4(to + off, hi[0], hi[1], hi[2], hi[3]);
@@ -114,47 +127,79 @@ __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt
     }
 }
 
-// S += Y~^T Z over a tile's 64 tokens, both parts; one thread.
-__device__ __forceinline__ void state_mmas(uint32_t d, uint32_t kt, uint32_t zs, uint32_t idesc, bool fresh) {
+// A value that all lanes of a warp hold, as one the compiler knows to be such: operands of an MMA that are
+// known to be uniform cost a fraction of the issue time.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(~0u, v, 0); }
+
+// An MMA by the lane for which `leader` holds, in code that the whole warp runs.
+__device__ __forceinline__ void mma_bf16_one(bool leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts_one(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)leader)
+        : "memory");
+}
+
+// S += Y~^T Z over a tile's 64 tokens, both parts; by a warp.
+__device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, uint32_t zs, uint32_t idesc, bool fresh) {
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        const uint64_t a = mndesc(kt + part * 2 * kBox, kBox), b = mndesc(zs, kBox);
+    for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_bf16(d, a + ((j * 2048) >> 4), b + ((j * 2048) >> 4), idesc, fresh && part == 0 && j == 0 ? 0u : 1u);
-    }
+        for (int j = 0; j < 4; ++j)
+            mma_bf16_one(leader, d, mndesc(kt + part * 2 * kBox + j * 2048, kBox), mndesc(zs + j * 2048, kBox), idesc,
+                         fresh && part == 0 && j == 0 ? 0u : 1u);
+}
+
+// Eight bf16 of a row, packed.
+__device__ __forceinline__ void st_pack8(uint32_t to, const float* v) {
+    st_shared_v4(to, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 template <typename SM>
 __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs g) {
-    constexpr int XST = SM::XST, XB = SM::XB, YST = SM::YST;
-    constexpr bool rev = SM::REV;
+    constexpr int XST = SM::XST, YST = SM::YST;
+    constexpr bool rev = SM::REV, own = SM::OWN;
     extern __shared__ uint8_t smem_raw[];
     const DecayPass& p = g.p;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
     float* pw = reinterpret_cast<float*>(sm + SM::TABLE);  // powers of the decay
-    float* pws = pw + 72;                                  // times in_scale
+    float* col = pw + 132;                                 // factors of the columns of P
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BARS);
     uint64_t *x_full = bar, *x_free = bar + 3, *yz_full = bar + 6, *yz_free = bar + 10, *zz_full = bar + 14, *s_full = bar + 18,
              *p_full = bar + 20, *xs_full = bar + 22, *pv_done = bar + 24, *o_free = bar + 26, *kt_full = bar + 28,
-             *h_done = bar + 29, *st_full = bar + 30, *xs_done = bar + 31;
-    uint64_t *pair = bar + 32, *drained = bar + 36;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 37);
+             *h_done = bar + 29, *st_full = bar + 30, *xs_done = bar + 31, *drained = bar + 32;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 34);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool leader = lane == 0;
     const Seg w = seg_of(p);
     check_offsets(p.seqs, p.header);
+    const bool tall = p.gx == 1;                 // a tile of x: 128 tokens of a head, or 64 of two
+    const int chunk = tall ? 128 : 64, mid = chunk / 2 - 1;
     const float l2 = log2_decay(p.log_decay, w.h);
-    for (int i = tid; i <= kTile; i += kThreads) {
+    const bool slow = l2 * (float)chunk >= -64.0f;  // factors of rows and columns (see above)
+    for (int i = tid; i < 129; i += kThreads) {
         pw[i] = power(l2, i);
-        pws[i] = pw[i] * p.in_scale;
+        if (i < 128) col[i] = p.in_scale * power(l2, rev ? i - mid : mid - i);
     }
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < XST; ++i) {
             mbar_init(&x_full[i], 1);
-            mbar_init(&x_free[i], 32 * kMathWarps);
+            mbar_init(&x_free[i], own ? 2 : kMathWarps);  // scores and X S, or the outputs' last warps
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < YST; ++i) {
             mbar_init(&yz_full[i], 1);
             mbar_init(&yz_free[i], 2);
             mbar_init(&zz_full[i], 128);
@@ -170,8 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         mbar_init(h_done, 1);
         mbar_init(st_full, 128);
         mbar_init(xs_done, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 64);
-        mbar_init(drained, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drained[i], 1);
         *abort = 0;
         fence_mbar_init();
     }
@@ -189,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     const int kx = (p.dx + 15) / 16;                 // K steps over dx
     const int nz = (p.dz + 15) / 16 * 16;            // N over dz
     const int ntx = (p.gx + 1) / 2;                  // tiles of x heads
-    constexpr uint32_t xhalf = (XB / 2) * kBox;      // from the first 64 columns of x to the next
+    constexpr uint32_t kHalf = 2 * kBox;             // from the first 64 columns of x, or of S, to the next
 
-    Walk walk(p.seqs, w.b, w.lo, w.hi, rev);
+    Walk walk(p.seqs, w.b, w.lo, w.hi, rev, chunk);
     Tile t;
 
     if (warp == 12) {
@@ -203,32 +247,33 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             bool ok = true;
             while (ok && walk.next(p.seqs, w.b, &t)) {
                 const int row = (int)(w.b * p.seqs.L + t.t0);
+                const int nsub = t.n > 64 ? 2 : 1, ny = p.gy * nsub;
                 for (int a = 0; a < ntx && ok; ++a) {
-                    for (int gh = 0; gh < p.gy && ok; ++gh) {
+                    for (int q = 0; q < ny && ok; ++q) {
                         if (a == 0) {
-                            const int s = yi % YST;
+                            const int s = yi % YST, head = (int)(w.h * p.gy) + q / nsub, at = row + 64 * (q % nsub);
                             if (yi >= YST && !wait(&yz_free[s], ((yi / YST) & 1) ^ 1, 100)) {
                                 ok = false;
                                 break;
                             }
                             uint8_t* to = sm + SM::YZ + s * 4 * kBox;
                             mbar_arrive_expect_tx(&yz_full[s], (nhx + nhz) * kBox);
-                            const int head = (int)(w.h * p.gy + gh);
-                            for (int h = 0; h < nhx; ++h) tma_load_3d(to + h * kBox, &g.y, &yz_full[s], 64 * h, head, row);
-                            for (int h = 0; h < nhz; ++h) tma_load_3d(to + (2 + h) * kBox, &g.z, &yz_full[s], 64 * h, head, row);
+                            for (int h = 0; h < nhx; ++h) tma_load_3d(to + h * kBox, &g.y, &yz_full[s], 64 * h, head, at);
+                            for (int h = 0; h < nhz; ++h) tma_load_3d(to + (2 + h) * kBox, &g.z, &yz_full[s], 64 * h, head, at);
                             ++yi;
                         }
-                        if (gh == 0) {
-                            const int s = xt % XST, heads = p.gx - 2 * a < 2 ? 1 : 2;
+                        if (q == 0) {
+                            const int s = xt % XST, parts = tall ? nsub : p.gx - 2 * a < 2 ? 1 : 2;
                             if (xt >= XST && !wait(&x_free[s], ((xt / XST) & 1) ^ 1, 101)) {
                                 ok = false;
                                 break;
                             }
-                            uint8_t* to = sm + SM::X + s * XB * kBox;
-                            mbar_arrive_expect_tx(&x_full[s], heads * nhx * kBox);
-                            for (int k = 0; k < heads; ++k)
+                            uint8_t* to = sm + SM::X + s * 4 * kBox;
+                            mbar_arrive_expect_tx(&x_full[s], parts * nhx * kBox);
+                            for (int k = 0; k < parts; ++k)
                                 for (int h = 0; h < nhx; ++h)
-                                    tma_load_3d(to + h * xhalf + k * kBox, &g.x, &x_full[s], 64 * h, (int)(w.h * p.gx) + 2 * a + k, row);
+                                    tma_load_3d(to + h * kHalf + k * kBox, &g.x, &x_full[s], 64 * h, (int)(w.h * p.gx) + (tall ? 0 : 2 * a + k),
+                                                row + (tall ? 64 * k : 0));
                             ++xt;
                         }
                     }
@@ -241,111 +286,129 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         }
         __syncwarp();
     } else if (warp == 13) {
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16(128, 64, false, false), id_o = idesc_bf16(128, nz, false, true);
-            uint32_t it = 0, xt = 0, yi = 0, ci = 0;
-            int pending = -1, pending_y = 0, pending_x = 0;
-            bool pending_last = false, ok = true;
-            // O += P Z of the item before
-            auto values = [&]() -> bool {
-                const int s = pending & 1, ys = pending_y % YST;
-                if (!wait(&p_full[s], (pending >> 1) & 1, 102) || !wait(&zz_full[ys], (pending_y / YST) & 1, 103)) return false;
-                tc_fence_after();
-                const uint64_t b = mndesc(base + SM::YZ + (ys * 4 + 2) * kBox, kBox);
+        // scores: X Y^T
+        const uint32_t id_s = idesc_bf16(128, 64, false, false);
+        uint32_t it = 0, xt = 0, yi = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            for (int a = 0; a < ntx && ok; ++a) {
+                for (int q = 0; q < ny && ok; ++q, ++it) {
+                    const int s = it & 1, xs = xt % XST;
+                    const uint32_t y = yi + q;
+                    const int ys = y % YST;
+                    if (q == 0 && !wait.all(&x_full[xs], (xt / XST) & 1, 104)) { ok = false; break; }
+                    if (a == 0 && !wait.all(&yz_full[ys], (y / YST) & 1, 105)) { ok = false; break; }
+                    if (it >= 2 && !wait.all(&pv_done[s], ((it >> 1) & 1) ^ 1, 106)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t xa = uniform(base + SM::X + xs * 4 * kBox), ya = uniform(base + SM::YZ + ys * 4 * kBox), to = uniform(tS + s * 64);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_bf16_ts(tO + (pending_x & 1) * 128, tS + s * 64 + j * 8, b + ((j * 2048) >> 4), id_o, 1u);
-                mma_commit(&pv_done[s]);
-                if (pending_last) mma_commit(&yz_free[ys]);
-                pending = -1;
-                return true;
-            };
-            while (ok && walk.next(p.seqs, w.b, &t)) {
-                const uint32_t y0 = yi;
-                for (int a = 0; a < ntx && ok; ++a) {
-                    for (int gh = 0; gh < p.gy && ok; ++gh, ++it) {
-                        const int s = it & 1, xs = xt % XST;
-                        const uint32_t y = y0 + gh;
-                        const int ys = y % YST;
-                        if (gh == 0 && !wait(&x_full[xs], (xt / XST) & 1, 104)) { ok = false; break; }
-                        if (a == 0 && !wait(&yz_full[ys], (y / YST) & 1, 105)) { ok = false; break; }
-                        if (it >= 2 && !wait(&pv_done[s], ((it >> 1) & 1) ^ 1, 106)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t xa = base + SM::X + xs * XB * kBox, ya = base + SM::YZ + ys * 4 * kBox;
-                        for (int k = 0; k < kx; ++k) {
-                            const uint32_t in = (k & 3) * 32;
-                            mma_bf16(tS + s * 64, kdesc(xa + (k >> 2) * xhalf + in), kdesc(ya + (k >> 2) * kBox + in), id_s, k > 0);
-                        }
+                    for (int k = 0; k < 8; ++k)
+                        if (k < kx)
+                            mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
+                    if (leader) {
                         mma_commit(&s_full[s]);
-                        // what does not wait for the state of a new tile goes first
-                        if (pending >= 0 && a == 0 && gh == 0 && !values()) { ok = false; break; }
-                        if (gh == 0) {
-                            if (xt >= 2 && !wait(&o_free[xt & 1], ((xt >> 1) & 1) ^ 1, 107)) { ok = false; break; }
-                            if (a == 0 && !wait(st_full, ci & 1, 108)) { ok = false; break; }
-                            tc_fence_after();
-                            for (int k = 0; k < kx; ++k)
-                                mma_bf16(tO + (xt & 1) * 128, kdesc(xa + (k >> 2) * xhalf + (k & 3) * 32),
-                                         mndesc(base + SM::ST + k * 2048, 2 * kBox), id_o, k > 0);
-                            mma_commit(&xs_full[xt & 1]);
+                        if (own && q == ny - 1) mma_commit(&x_free[xs]);
+                    }
+                    if (q == ny - 1) ++xt;
+                }
+            }
+            yi += ny;
+        }
+        if (!ok) {  // every MMA that was issued ends before the CTA leaves: they read shared memory
+            if (leader) mma_commit(&drained[0]);
+            mbar_wait(&drained[0], 0, tc::kTimeout);
+        }
+    } else if (warp == 15) {
+        // outputs: X S, and P Z after it in the same accumulator
+        const uint32_t id_o = idesc_bf16(128, nz, false, true);
+        uint32_t it = 0, xt = 0, yi = 0, ci = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            for (int a = 0; a < ntx && ok; ++a) {
+                for (int q = 0; q < ny && ok; ++q, ++it) {
+                    const int s = it & 1, xs = xt % XST;
+                    const uint32_t y = yi + q;
+                    const int ys = y % YST;
+                    const uint32_t to = uniform(tO + (xt & 1) * 128);
+                    if (q == 0) {
+                        if (!wait.all(&x_full[xs], (xt / XST) & 1, 107)) { ok = false; break; }
+                        if (xt >= 2 && !wait.all(&o_free[xt & 1], ((xt >> 1) & 1) ^ 1, 119)) { ok = false; break; }
+                        if (a == 0 && !wait.all(st_full, ci & 1, 108)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t xa = uniform(base + SM::X + xs * 4 * kBox);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < kx)
+                                mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), mndesc(base + SM::ST + k * 2048, kHalf), id_o, k > 0);
+                        if (leader) {
+                            if (!slow) mma_commit(&xs_full[xt & 1]);
+                            if (own) mma_commit(&x_free[xs]);
                             if (a == ntx - 1) mma_commit(xs_done);
                         }
-                        if (pending >= 0 && !values()) { ok = false; break; }
-                        pending = (int)it;
-                        pending_y = (int)y;
-                        pending_x = (int)xt;
-                        pending_last = a == ntx - 1;
-                        if (gh == p.gy - 1) ++xt;
                     }
-                }
-                yi += p.gy;
-                ++ci;
-            }
-            if (ok && pending >= 0) ok = values();
-            if (!ok) {  // every MMA that was issued ends before the CTA leaves: they read shared memory
-                mma_commit(drained);
-                mbar_wait(drained, 0, tc::kTimeout);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 14) {
-        if (lane == 0) {
-            const uint32_t id_h = idesc_bf16(128, nz, true, true);
-            uint32_t yi = 0;
-            bool ok = true;
-            while (ok && walk.next(p.seqs, w.b, &t)) {
-                for (int gh = 0; gh < p.gy; ++gh, ++yi) {
-                    if (!wait(kt_full, yi & 1, 109)) { ok = false; break; }
+                    if (!wait.all(&zz_full[ys], (y / YST) & 1, 103) || !wait.all(&p_full[s], (it >> 1) & 1, 102)) { ok = false; break; }
                     tc_fence_after();
-                    state_mmas(tH, base + SM::KT, base + SM::YZ + ((yi % YST) * 4 + 2) * kBox, id_h, false);
+                    const uint32_t za = uniform(base + SM::YZ + (ys * 4 + 2) * kBox), from = uniform(tS + s * 64);
+                    // the weights of each 32 columns lie at the beginning of their scores
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_bf16_ts_one(leader, to, from + (j >> 1) * 32 + (j & 1) * 8, mndesc(za + j * 2048, kBox), id_o, 1u);
+                    if (leader) {
+                        mma_commit(&pv_done[s]);
+                        if (a == ntx - 1) mma_commit(&yz_free[ys]);
+                    }
+                    if (q == ny - 1) ++xt;
+                }
+            }
+            yi += ny;
+            ++ci;
+        }
+        if (!ok) {
+            if (leader) mma_commit(&drained[1]);
+            mbar_wait(&drained[1], 0, tc::kTimeout);
+        }
+    } else if (warp == 14) {
+        const uint32_t id_h = idesc_bf16(128, nz, true, true);
+        uint32_t yi = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            for (int q = 0; q < ny; ++q, ++yi) {
+                if (!wait.all(kt_full, yi & 1, 109)) { ok = false; break; }
+                tc_fence_after();
+                state_mmas(leader, tH, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), id_h, false);
+                if (leader) {
                     mma_commit(h_done);
                     mma_commit(&yz_free[yi % YST]);
                 }
             }
-            if (!ok && yi > 0) mbar_wait(h_done, (yi - 1) & 1, tc::kTimeout);
         }
-        __syncwarp();
+        if (!ok && yi > 0) mbar_wait(h_done, (yi - 1) & 1, tc::kTimeout);
     } else if (warp >= 8) {
         // the state: row `row` of S
         const int row = tid - 256;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int64_t size = (int64_t)p.dx * p.dz;
-        const int64_t step = p.transposed ? p.dx : 1, at = p.transposed ? row : (int64_t)row * p.dz;
+        const int step = p.transposed ? p.dx : 1;
+        const int64_t at = p.transposed ? row : (int64_t)row * p.dz;
         uint32_t yi = 0, ci = 0;
         bool ok = true, was_last = false;
-        int64_t was_seq = 0;
+        int was_seq = 0;
         grid_dep_wait();
         // the state behind a sequence's last tile
-        auto leave = [&](int64_t seq) {
+        auto leave = [&](int seq) {
             if (p.fin == nullptr) return;
-            float* to = p.fin + (seq * p.Hkv + w.h) * size;
-            for (int c = 0; c < p.dz; c += 32) {
-                float v[32];
-                tmem_ld32(tH + lanes + c, v);
+            float* to = p.fin + (seq * p.Hkv + w.h) * size + at;
+#pragma unroll 1
+            for (int c = 0; c < p.dz; c += 8, to += 8 * step) {
+                float v[8];
+                tmem_ld8(tH + lanes + c, v);
                 tmem_wait_ld();
                 if (row < p.dx)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i < p.dz) to[at + (c + i) * step] = v[i];
+                    for (int i = 0; i < 8; ++i) to[i * step] = v[i];
             }
         };
         while (ok && walk.next(p.seqs, w.b, &t)) {
@@ -354,25 +417,33 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tc_fence_after();
                 if (was_last) leave(was_seq);
             }
-            const float keep = pw[t.n];
+            const float keep = pw[t.n], seen = !slow ? 1.0f : rev ? power(l2, t.n - 1 - mid) : pw[mid + 1];
             const bool from_memory = t.first || ci == 0;
             const float* from = !from_memory ? nullptr
                                 : t.first    ? (p.init == nullptr ? nullptr : p.init + (t.seq * p.Hkv + w.h) * size)
                                              : p.recs + (w.unit * p.nseg + w.seg) * size;
+            if (from_memory) {
+                if (from != nullptr) from += at;
+#pragma unroll 1
+                for (int c = 0; c < nz; c += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = from != nullptr && row < p.dx && c < p.dz ? from[(c + i) * step] : 0.0f;
+                    tmem_st8(tH + lanes + c, reinterpret_cast<const uint32_t*>(v));
+                }
+                tmem_wait_st();
+            }
+#pragma unroll 1
             for (int c = 0; c < nz; c += 32) {
                 float v[32];
-                if (from_memory) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = from != nullptr && row < p.dx && c + i < p.dz ? from[at + (c + i) * step] : 0.0f;
-                } else {
-                    tmem_ld32(tH + lanes + c, v);
-                    tmem_wait_ld();
-                }
+                tmem_ld32(tH + lanes + c, v);
+                tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int col = c + 8 * i;
-                    st_shared_v4(base + SM::ST + (col >> 6) * 2 * kBox + sw128(row, (col & 63) >> 3), pack_bf16(v[8 * i], v[8 * i + 1]),
-                                 pack_bf16(v[8 * i + 2], v[8 * i + 3]), pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                    float u[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[k] = v[8 * i + k] * seen;
+                    st_pack8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), u);
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= keep;
@@ -382,13 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(st_full);
-            for (int gh = 0; gh < p.gy; ++gh, ++yi) {
-                const int ys = yi % YST;
+            const int nsub = t.n > 64 ? 2 : 1, ny = p.gy * nsub;
+            for (int q = 0; q < ny; ++q, ++yi) {
+                const int ys = yi % YST, j0 = 64 * (q % nsub);
                 if (!wait.all(&yz_full[ys], (yi / YST) & 1, 112)) { ok = false; break; }
-                if (gh > 0 && !wait.all(h_done, (yi - 1) & 1, 113)) { ok = false; break; }
-                const int tok = row & 63, far = rev ? tok + 1 : t.n - 1 - tok;
+                if (q > 0 && !wait.all(h_done, (yi - 1) & 1, 113)) { ok = false; break; }
+                const int m = min(64, t.n - j0), tok = row & 63, far = rev ? j0 + tok + 1 : t.n - 1 - j0 - tok;
                 const uint32_t ya = base + SM::YZ + ys * 4 * kBox;
-                scale_rows(ya, ya + 2 * kBox, base + SM::KT, t.n, tok < t.n ? pws[far] : 0.0f, row);
+                scale_rows(ya, ya + 2 * kBox, base + SM::KT, m, tok < m ? pw[far] * p.in_scale : 0.0f, row);
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&zz_full[ys]);
@@ -405,110 +477,123 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             }
         }
     } else {
-        // weights of pairs, the state part's scale, outputs: row `r` of the tile of x heads
+        // weights of pairs and outputs: row `r` of the tile of x
         const int quad = warp & 3, half = warp >> 2;
-        const int r = 32 * quad + lane, i = r & 63, hs = r >> 6;  // token in the tile, head of the two
+        const int r = 32 * quad + lane, i = tall ? r : r & 63;  // token in the chunk
+        const int tq = tall ? quad : quad & 1;                  // its block of 32 tokens
+        const int slot = tall ? 0 : quad >> 1;                  // head of the two
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const int ib = quad & 1;                     // the row's block of 32 tokens; the columns' is `half`
         const bool z_on = 64 * half < p.dz;
-        const int zc = z_on ? (nz - 64 * half < 64 ? nz - 64 * half : 64) : 0;  // output columns of this warp
-        uint32_t it = 0, xt = 0, pairs = 0;
+        const float rowf = p.out_scale * (slow ? power(l2, rev ? mid - i : i - mid) : 1.0f);
+        const uint32_t c0 = base + SM::TABLE + 132 * 4;
+        uint32_t it = 0, xt = 0;
         bool ok = true;
         // the tile whose outputs are still to be stored
-        int held = -1, held_x = 0, held_n = 0, held_heads = 0, held_a = 0;
-        int64_t held_t0 = 0;
+        int held = -1, held_x = 0, held_n = 0, held_head = 0;
+        bool held_live = false;
+        int held_t0 = 0;
         auto store = [&]() -> bool {
             if (!wait.all(&pv_done[held & 1], (held >> 1) & 1, 115)) return false;
             tc_fence_after();
-            const uint32_t stage = base + SM::X + (held_x % XST) * XB * kBox + half * xhalf;
-            const bool live = hs < held_heads && z_on;  // one answer for a warp
+            const uint32_t off = own ? SM::OUT : SM::X + (held_x % XST) * 4 * kBox;
+            const uint32_t stage = base + off + half * kHalf + quad * 4096;
+            const bool live = held_live && z_on;  // one answer for a warp
             if (live) {
-                for (int c = 0; c < zc; c += 32) {
+                if (own && lane == 0) bulk_wait_read();  // the rows before have left
+                __syncwarp();
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 32) {
                     float v[32];
                     tmem_ld32(tO + (held_x & 1) * 128 + lanes + 64 * half + c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] *= p.out_scale;
+                    for (int k = 0; k < 32; ++k) v[k] *= rowf;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        st_shared_v4(stage + sw128(r, (c >> 3) + k), pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
-                                     pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
+                    for (int k = 0; k < 4; ++k) st_pack8(stage + sw128(lane, (c >> 3) + k), v + 8 * k);
                 }
+                fence_async_smem();
             }
             tc_fence_before();
             mbar_arrive(&o_free[held_x & 1]);
             __syncwarp();
             if (live) {
-                const int chunk = lane & 7;
-                const int64_t head = w.h * p.gx + 2 * held_a + hs;
-                __nv_bfloat16* out = (__nv_bfloat16*)p.out + (w.b * p.seqs.L + held_t0) * p.ldout + head * p.dz + 64 * half + 8 * chunk;
-                if (64 * half + 8 * chunk < p.dz) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int row = 4 * k + (lane >> 3), tok = (32 * quad + row) & 63;
-                        uint32_t v[4];
-                        ld_shared_v4(stage + sw128(32 * quad + row, chunk), v[0], v[1], v[2], v[3]);
-                        if (tok < held_n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
+                if (32 * tq + 32 <= held_n) {
+                    if (lane == 0) {
+                        tma_store_3d(&g.out, sm + off + half * kHalf + quad * 4096, 64 * half, held_head, (int)(w.b * p.seqs.L + held_t0) + 32 * tq);
+                        bulk_commit();
+                        if (!own) bulk_wait_read();
                     }
+                } else if (32 * tq < held_n) {
+                    const int c = lane & 7;
+                    __nv_bfloat16* out = (__nv_bfloat16*)p.out + (w.b * p.seqs.L + held_t0) * p.ldout + (int64_t)held_head * p.dz + 64 * half + 8 * c;
+                    if (64 * half + 8 * c < p.dz) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int row = 4 * k + (lane >> 3), tok = 32 * tq + row;
+                            uint32_t v[4];
+                            ld_shared_v4(stage + sw128(row, c), v[0], v[1], v[2], v[3]);
+                            if (tok < held_n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                    fence_async_smem();
                 }
             }
-            fence_async_smem();
-            mbar_arrive(&x_free[held_x % XST]);
+            __syncwarp();
+            if (!own && lane == 0) mbar_arrive(&x_free[held_x % XST]);
             held = -1;
             return true;
         };
         while (ok && walk.next(p.seqs, w.b, &t)) {
+            const int nsub = t.n > 64 ? 2 : 1, ny = p.gy * nsub;
             for (int a = 0; a < ntx && ok; ++a) {
-                const int heads = p.gx - 2 * a < 2 ? 1 : 2;
-                const bool live = hs < heads;
-                for (int gh = 0; gh < p.gy && ok; ++gh, ++it) {
-                    const int s = it & 1;
+                const bool live = tall ? 32 * tq < t.n : 2 * a + slot < p.gx;
+                for (int q = 0; q < ny && ok; ++q, ++it) {
+                    const int s = it & 1, cb = 2 * (q % nsub) + half;  // block of the columns
                     if (!wait.all(&s_full[s], (it >> 1) & 1, 116)) { ok = false; break; }
                     tc_fence_after();
                     if (live) {
-                        const uint32_t to = tS + s * 64 + lanes + half * 16;
                         uint32_t o[16];
-                        if (rev ? ib > half : ib < half) {
+                        if (rev ? tq > cb : tq < cb) {
 #pragma unroll
                             for (int k = 0; k < 16; ++k) o[k] = 0;
                         } else {
                             float v[32];
                             tmem_ld32(tS + s * 64 + lanes + half * 32, v);
                             tmem_wait_ld();
-                            if (ib != half) {
-                                // |i - j| as steps to the border between the blocks and beyond it
-                                const float far = pw[rev ? 32 - (i & 31) : (i & 31) + 1];
+                            if (slow) {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] *= far * pws[rev ? k : 31 - k];
-                                if (rev && t.n < kTile) {
+                                for (int k = 0; k < 8; ++k) {
+                                    uint32_t f[4];
+                                    ld_shared_v4(c0 + (32 * cb + 4 * k) * 4, f[0], f[1], f[2], f[3]);
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k) v[k] = 32 * half + k < t.n ? v[k] : 0.0f;
+                                    for (int m = 0; m < 4; ++m) v[4 * k + m] *= __uint_as_float(f[m]);
                                 }
                             } else {
-                                const int d0 = i & 31;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
-                                    const int d = rev ? k - d0 : d0 - k;
-                                    v[k] = d >= 0 && 32 * half + k < t.n ? v[k] * pws[d & 63] : 0.0f;
+                                    const int d = rev ? 32 * cb + k - i : i - 32 * cb - k;
+                                    v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
                                 }
+                            }
+                            if (tq == cb) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = (rev ? k >= lane : k <= lane) ? v[k] : 0.0f;
+                            }
+                            if (rev && 32 * cb + 32 > t.n) {  // tokens behind the last one
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = 32 * cb + k < t.n ? v[k] : 0.0f;
                             }
 #pragma unroll
                             for (int k = 0; k < 16; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
                         }
-                        // both halves of a row's scores are read before its weights overwrite them
-                        tc_fence_before();
-                        mbar_arrive(&pair[quad]);
-                        if (!wait.all(&pair[quad], pairs & 1, 118)) { ok = false; break; }
-                        tc_fence_after();
-                        ++pairs;
-                        tmem_st16(to, o);
+                        tmem_st16(tS + s * 64 + lanes + half * 32, o);
                     }
-                    if (gh == 0) {
+                    if (!slow && q == 0) {  // e^(l (i+1)) X S
                         if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) { ok = false; break; }
                         tc_fence_after();
                         if (live && z_on) {
                             const float f = i < t.n ? pw[rev ? t.n - 1 - i : i + 1] : 0.0f;
-                            for (int c = 0; c < zc; c += 32) {
+                            for (int c = 0; c < 64; c += 32) {
                                 float v[32];
                                 tmem_ld32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
                                 tmem_wait_ld();
@@ -522,12 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     tc_fence_before();
                     mbar_arrive(&p_full[s]);
                     if (held >= 0 && !store()) { ok = false; break; }
-                    if (gh == p.gy - 1) {
+                    if (q == ny - 1) {
                         held = (int)it;
                         held_x = (int)xt;
                         held_n = t.n;
-                        held_heads = heads;
-                        held_a = a;
+                        held_head = (int)(w.h * p.gx) + (tall ? 0 : 2 * a + slot);
+                        held_live = live;
                         held_t0 = t.t0;
                         ++xt;
                     }
@@ -535,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             }
         }
         if (ok && held >= 0) store();
+        if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -623,21 +709,22 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
         }
         __syncwarp();
     } else if (warp == 9) {
-        if (lane == 0) {
-            const uint32_t id_h = idesc_bf16(128, nz, true, true);
-            uint32_t it = 0;
-            for (; it < items; ++it) {
-                const int k = it & 1;
-                if (!wait(&kt_full[k], (it >> 1) & 1, 121)) break;
-                tc_fence_after();
-                state_mmas(tb, base + EndsSmem::KT + k * 4 * kBox, base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox, id_h, it == 0);
+        const bool leader = lane == 0;
+        const uint32_t id_h = idesc_bf16(128, nz, true, true);
+        uint32_t it = 0;
+        for (; it < items; ++it) {
+            const int k = it & 1;
+            if (!wait.all(&kt_full[k], (it >> 1) & 1, 121)) break;
+            tc_fence_after();
+            state_mmas(leader, tb, uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), id_h,
+                       it == 0);
+            if (leader) {
                 mma_commit(&kt_free[k]);
                 mma_commit(&yz_free[it % kEndsStages]);
             }
-            mma_commit(done);
-            if (it < items) mbar_wait(done, 0, tc::kTimeout);
         }
-        __syncwarp();
+        if (leader) mma_commit(done);
+        if (it < items) mbar_wait(done, 0, tc::kTimeout);
     } else {
         const int group = warp >> 2, in = tid & 127, tok = in & 63;
         uint32_t it = 0;
@@ -690,11 +777,11 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
     }
 }
 
-// [rows, heads, width] of a tensor with token distance ld, boxes of 64 rows x 64 columns of one head.
-bool map_of(CUtensorMap* m, const void* ptr, int64_t rows, int64_t heads, int64_t width, int64_t ld) {
+// [rows, heads, width] of a tensor with token distance ld, boxes of `box_rows` x 64 columns of one head.
+bool map_of(CUtensorMap* m, const void* ptr, int64_t rows, int64_t heads, int64_t width, int64_t ld, int box_rows = 64) {
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, 1, 64};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
     return tc::make_map(m, ptr, 3, dims, strides, box);
 }
 
@@ -702,7 +789,8 @@ bool args_of(const DecayPass& p, TcArgs* a) {
     a->p = p;
     const int64_t rows = p.units / p.Hkv * p.seqs.L;
     return map_of(&a->x, p.x, rows, p.Hkv * p.gx, p.dx, p.ldx) && map_of(&a->y, p.y, rows, p.Hkv * p.gy, p.dx, p.ldy) &&
-           map_of(&a->z, p.z, rows, p.Hkv * p.gy, p.dz, p.ldz);
+           map_of(&a->z, p.z, rows, p.Hkv * p.gy, p.dz, p.ldz) &&
+           (p.out == nullptr || map_of(&a->out, p.out, rows, p.Hkv * p.gx, p.dz, p.ldout, 32));
 }
 
 template <typename SM>
@@ -746,7 +834,8 @@ cudaError_t decay_tc_ends(const DecayPass& p, float* recs, cudaStream_t s) {
 cudaError_t decay_tc_pass(const DecayPass& p, cudaStream_t s) {
     TcArgs a;
     if (!args_of(p, &a)) return cudaErrorInvalidValue;
-    return p.rev ? go<Backwards>(a, s) : go<Forwards>(a, s);
+    if (!p.rev) return go<Wide<false>>(a, s);
+    return p.gy > 1 ? go<Deep>(a, s) : go<Wide<true>>(a, s);
 }
 
 }  // namespace lz
