@@ -105,25 +105,26 @@ __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
 // behind the tile's last token become zeros: 0 times what lies there may be NaN.
 __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt, int n, float f, int tid) {
     const int tok = tid & 63, half = tid >> 6;
-    const uint32_t from = ys + half * kBox, to = kt + half * kBox;
-    uint32_t w[8][4];
-#pragma unroll
+    const uint32_t row = half * kBox + tok * 128;
+    const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
+    // two pieces at a time: a loop that stays in the instruction cache beats a longer one without branches
+#pragma unroll 2
     for (int c = 0; c < 8; ++c) {
+        const uint32_t off = row + ((c ^ (tok & 7)) << 4);
+        uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
+        if (tok < n) ld_shared_v4(ys + off, w[0], w[1], w[2], w[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[c][i] = 0;
-        if (tok < n) ld_shared_v4(from + sw128(tok, c), w[c][0], w[c][1], w[c][2], w[c][3]);
-    }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t off = sw128(tok, c);
-        uint32_t hi[4], lo[4];
-        float v[8];
-        tc::unpack8(w[c][0], w[c][1], w[c][2], w[c][3], v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc::split2(v[2 * i] * f, v[2 * i + 1] * f, hi[i], lo[i]);
-        st_shared_v4(to + off, hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(to + 2 * kBox + off, lo[0], lo[1], lo[2], lo[3]);
-        if (tok >= n) st_shared_v4(zs + half * kBox + off, 0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            const f2 v = mul2(pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), ff);
+            unpack(v, a, b);
+            hi[i] = pack_bf16(a, b);
+            unpack(fma2(pack(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xffff0000u)), minus, v), a, b);
+            lo[i] = pack_bf16(a, b);
+        }
+        st_shared_v4(kt + off, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(kt + 2 * kBox + off, lo[0], lo[1], lo[2], lo[3]);
+        if (tok >= n) st_shared_v4(zs + off, 0, 0, 0, 0);
     }
 }
 
@@ -161,9 +162,16 @@ __device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt,
                          fresh && part == 0 && j == 0 ? 0u : 1u);
 }
 
-// Eight bf16 of a row, packed.
-__device__ __forceinline__ void st_pack8(uint32_t to, const float* v) {
-    st_shared_v4(to, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+// Eight values of a row times f as bf16.
+__device__ __forceinline__ void st_scaled8(uint32_t to, const float* v, f2 f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack(mul2(pack(v[2 * i], v[2 * i + 1]), f), a, b);
+        w[i] = pack_bf16(a, b);
+    }
+    st_shared_v4(to, w[0], w[1], w[2], w[3]);
 }
 
 template <typename SM>
@@ -418,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (was_last) leave(was_seq);
             }
             const float keep = pw[t.n], seen = !slow ? 1.0f : rev ? power(l2, t.n - 1 - mid) : pw[mid + 1];
+            const f2 keep2 = pack(keep, keep), seen2 = pack(seen, seen);
             const bool from_memory = t.first || ci == 0;
             const float* from = !from_memory ? nullptr
                                 : t.first    ? (p.init == nullptr ? nullptr : p.init + (t.seq * p.Hkv + w.h) * size)
@@ -439,14 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tmem_ld32(tH + lanes + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float u[8];
+                for (int i = 0; i < 4; ++i) st_scaled8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), v + 8 * i, seen2);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) u[k] = v[8 * i + k] * seen;
-                    st_pack8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), u);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= keep;
+                for (int i = 0; i < 16; ++i) unpack(mul2(pack(v[2 * i], v[2 * i + 1]), keep2), v[2 * i], v[2 * i + 1]);
                 tmem_st32(tH + lanes + c, v);
             }
             tmem_wait_st();
@@ -485,141 +489,145 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         const bool z_on = 64 * half < p.dz;
         const float rowf = p.out_scale * (slow ? power(l2, rev ? mid - i : i - mid) : 1.0f);
+        const f2 rowf2 = pack(rowf, rowf);
         const uint32_t c0 = base + SM::TABLE + 132 * 4;
+        bool have = walk.next(p.seqs, w.b, &t);
         uint32_t it = 0, xt = 0;
-        bool ok = true;
+        int a = 0, q = 0;
         // the tile whose outputs are still to be stored
-        int held = -1, held_x = 0, held_n = 0, held_head = 0;
-        bool held_live = false;
-        int held_t0 = 0;
-        auto store = [&]() -> bool {
-            if (!wait.all(&pv_done[held & 1], (held >> 1) & 1, 115)) return false;
-            tc_fence_after();
-            const uint32_t off = own ? SM::OUT : SM::X + (held_x % XST) * 4 * kBox;
-            const uint32_t stage = base + off + half * kHalf + quad * 4096;
-            const bool live = held_live && z_on;  // one answer for a warp
-            if (live) {
-                if (own && lane == 0) bulk_wait_read();  // the rows before have left
-                __syncwarp();
-#pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                    float v[32];
-                    tmem_ld32(tO + (held_x & 1) * 128 + lanes + 64 * half + c, v);
-                    tmem_wait_ld();
+        bool held = false, held_live = false;
+        int held_n = 0, held_head = 0, held_t0 = 0;
+        // an item's weights, then the outputs of the tile of x before, whose products end meanwhile
+        while (true) {
+            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            const bool live = tall ? 32 * tq < t.n : 2 * a + slot < p.gx;
+            if (have) {
+                const int s = it & 1, cb = 2 * (t.n > 64 ? q & 1 : 0) + half;  // block of the columns
+                if (!wait.all(&s_full[s], (it >> 1) & 1, 116)) break;
+                tc_fence_after();
+                if (live) {
+                    const uint32_t at = tS + s * 64 + lanes + half * 32;
+                    uint32_t o[16];
+                    if (rev ? tq > cb : tq < cb) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] *= rowf;
+                        for (int k = 0; k < 16; ++k) o[k] = 0;
+                    } else {
+                        float v[32];
+                        tmem_ld32(at, v);
+                        tmem_wait_ld();
+                        if (slow) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) st_pack8(stage + sw128(lane, (c >> 3) + k), v + 8 * k);
-                }
-                fence_async_smem();
-            }
-            tc_fence_before();
-            mbar_arrive(&o_free[held_x & 1]);
-            __syncwarp();
-            if (live) {
-                if (32 * tq + 32 <= held_n) {
-                    if (lane == 0) {
-                        tma_store_3d(&g.out, sm + off + half * kHalf + quad * 4096, 64 * half, held_head, (int)(w.b * p.seqs.L + held_t0) + 32 * tq);
-                        bulk_commit();
-                        if (!own) bulk_wait_read();
-                    }
-                } else if (32 * tq < held_n) {
-                    const int c = lane & 7;
-                    __nv_bfloat16* out = (__nv_bfloat16*)p.out + (w.b * p.seqs.L + held_t0) * p.ldout + (int64_t)held_head * p.dz + 64 * half + 8 * c;
-                    if (64 * half + 8 * c < p.dz) {
+                            for (int k = 0; k < 8; ++k) {
+                                uint32_t f[4];
+                                ld_shared_v4(c0 + (32 * cb + 4 * k) * 4, f[0], f[1], f[2], f[3]);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int row = 4 * k + (lane >> 3), tok = 32 * tq + row;
-                            uint32_t v[4];
-                            ld_shared_v4(stage + sw128(row, c), v[0], v[1], v[2], v[3]);
-                            if (tok < held_n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
+                                for (int m = 0; m < 2; ++m)
+                                    unpack(mul2(pack(v[4 * k + 2 * m], v[4 * k + 2 * m + 1]), pack(__uint_as_float(f[2 * m]), __uint_as_float(f[2 * m + 1]))),
+                                           v[4 * k + 2 * m], v[4 * k + 2 * m + 1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int d = rev ? 32 * cb + k - i : i - 32 * cb - k;
+                                v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
+                            }
                         }
+                        if (tq == cb || (rev && 32 * cb + 32 > t.n)) {
+                            // places on the wrong side, and of tokens behind the last one, are left out whatever they hold
+                            const int lo = rev && tq == cb ? lane : 0, hi = rev ? t.n - 32 * cb - 1 : lane;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = (!rev || k >= lo) && k <= hi ? v[k] : 0.0f;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+                    }
+                    tmem_st16(at, o);
+                }
+                if (!slow && q == 0) {  // e^(l (i+1)) X S
+                    if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) break;
+                    tc_fence_after();
+                    if (live && z_on) {
+                        const float f = i < t.n ? pw[rev ? t.n - 1 - i : i + 1] : 0.0f;
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 32) {
+                            float v[32];
+                            tmem_ld32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] *= f;
+                            tmem_st32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[s]);
+            }
+            if (held) {  // item it - 1 was the last of tile xt - 1
+                const uint32_t hx = xt - 1, hi = it - 1;
+                if (!wait.all(&pv_done[hi & 1], (hi >> 1) & 1, 115)) break;
+                tc_fence_after();
+                const uint32_t off = own ? SM::OUT : SM::X + (hx % XST) * 4 * kBox;
+                const uint32_t stage = base + off + half * kHalf + quad * 4096;
+                const bool out_live = held_live && z_on;  // one answer for a warp
+                if (out_live) {
+                    if (own && lane == 0) bulk_wait_read();  // the rows before have left
+                    __syncwarp();
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        float v[32];
+                        tmem_ld32(tO + (hx & 1) * 128 + lanes + 64 * half + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) st_scaled8(stage + sw128(lane, (c >> 3) + k), v + 8 * k, rowf2);
                     }
                     fence_async_smem();
                 }
+                tc_fence_before();
+                mbar_arrive(&o_free[hx & 1]);
+                __syncwarp();
+                if (out_live) {
+                    if (32 * tq + 32 <= held_n) {
+                        if (lane == 0) {
+                            tma_store_3d(&g.out, sm + off + half * kHalf + quad * 4096, 64 * half, held_head, (int)(w.b * p.seqs.L) + held_t0 + 32 * tq);
+                            bulk_commit();
+                            if (!own) bulk_wait_read();
+                        }
+                    } else if (32 * tq < held_n) {
+                        const int c = lane & 7;
+                        __nv_bfloat16* out = (__nv_bfloat16*)p.out + (w.b * p.seqs.L + held_t0) * p.ldout + (int64_t)held_head * p.dz + 64 * half + 8 * c;
+                        if (64 * half + 8 * c < p.dz) {
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                const int row = 4 * k + (lane >> 3), tok = 32 * tq + row;
+                                uint32_t v[4];
+                                ld_shared_v4(stage + sw128(row, c), v[0], v[1], v[2], v[3]);
+                                if (tok < held_n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
+                            }
+                        }
+                        fence_async_smem();
+                    }
+                }
+                __syncwarp();
+                if (!own && lane == 0) mbar_arrive(&x_free[hx % XST]);
+                held = false;
             }
-            __syncwarp();
-            if (!own && lane == 0) mbar_arrive(&x_free[held_x % XST]);
-            held = -1;
-            return true;
-        };
-        while (ok && walk.next(p.seqs, w.b, &t)) {
-            const int nsub = t.n > 64 ? 2 : 1, ny = p.gy * nsub;
-            for (int a = 0; a < ntx && ok; ++a) {
-                const bool live = tall ? 32 * tq < t.n : 2 * a + slot < p.gx;
-                for (int q = 0; q < ny && ok; ++q, ++it) {
-                    const int s = it & 1, cb = 2 * (q % nsub) + half;  // block of the columns
-                    if (!wait.all(&s_full[s], (it >> 1) & 1, 116)) { ok = false; break; }
-                    tc_fence_after();
-                    if (live) {
-                        uint32_t o[16];
-                        if (rev ? tq > cb : tq < cb) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = 0;
-                        } else {
-                            float v[32];
-                            tmem_ld32(tS + s * 64 + lanes + half * 32, v);
-                            tmem_wait_ld();
-                            if (slow) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    uint32_t f[4];
-                                    ld_shared_v4(c0 + (32 * cb + 4 * k) * 4, f[0], f[1], f[2], f[3]);
-#pragma unroll
-                                    for (int m = 0; m < 4; ++m) v[4 * k + m] *= __uint_as_float(f[m]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const int d = rev ? 32 * cb + k - i : i - 32 * cb - k;
-                                    v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
-                                }
-                            }
-                            if (tq == cb) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = (rev ? k >= lane : k <= lane) ? v[k] : 0.0f;
-                            }
-                            if (rev && 32 * cb + 32 > t.n) {  // tokens behind the last one
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = 32 * cb + k < t.n ? v[k] : 0.0f;
-                            }
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-                        }
-                        tmem_st16(tS + s * 64 + lanes + half * 32, o);
-                    }
-                    if (!slow && q == 0) {  // e^(l (i+1)) X S
-                        if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) { ok = false; break; }
-                        tc_fence_after();
-                        if (live && z_on) {
-                            const float f = i < t.n ? pw[rev ? t.n - 1 - i : i + 1] : 0.0f;
-                            for (int c = 0; c < 64; c += 32) {
-                                float v[32];
-                                tmem_ld32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] *= f;
-                                tmem_st32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
-                            }
-                        }
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&p_full[s]);
-                    if (held >= 0 && !store()) { ok = false; break; }
-                    if (q == ny - 1) {
-                        held = (int)it;
-                        held_x = (int)xt;
-                        held_n = t.n;
-                        held_head = (int)(w.h * p.gx) + (tall ? 0 : 2 * a + slot);
-                        held_live = live;
-                        held_t0 = t.t0;
-                        ++xt;
-                    }
+            if (!have) break;
+            ++it;
+            if (++q == ny) {
+                q = 0;
+                held = true;
+                held_live = live;
+                held_n = t.n;
+                held_head = (int)(w.h * p.gx) + (tall ? 0 : 2 * a + slot);
+                held_t0 = t.t0;
+                ++xt;
+                if (++a == ntx) {
+                    a = 0;
+                    have = walk.next(p.seqs, w.b, &t);
                 }
             }
         }
-        if (ok && held >= 0) store();
         if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
