@@ -107,8 +107,7 @@ __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt
     const int tok = tid & 63, half = tid >> 6;
     const uint32_t row = half * kBox + tok * 128;
     const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
-    // two pieces at a time: a loop that stays in the instruction cache beats a longer one without branches
-#pragma unroll 2
+#pragma unroll 1
     for (int c = 0; c < 8; ++c) {
         const uint32_t off = row + ((c ^ (tok & 7)) << 4);
         uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
@@ -154,12 +153,9 @@ __device__ __forceinline__ void mma_bf16_ts_one(bool leader, uint32_t d_tmem, ui
 
 // S += Y~^T Z over a tile's 64 tokens, both parts; by a warp.
 __device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, uint32_t zs, uint32_t idesc, bool fresh) {
-#pragma unroll
-    for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            mma_bf16_one(leader, d, mndesc(kt + part * 2 * kBox + j * 2048, kBox), mndesc(zs + j * 2048, kBox), idesc,
-                         fresh && part == 0 && j == 0 ? 0u : 1u);
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j)
+        mma_bf16_one(leader, d, mndesc(kt + (j >> 2) * 2 * kBox + (j & 3) * 2048, kBox), mndesc(zs + (j & 3) * 2048, kBox), idesc, fresh && j == 0 ? 0u : 1u);
 }
 
 // Eight values of a row times f as bf16.
@@ -310,10 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     if (it >= 2 && !wait.all(&pv_done[s], ((it >> 1) & 1) ^ 1, 106)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t xa = uniform(base + SM::X + xs * 4 * kBox), ya = uniform(base + SM::YZ + ys * 4 * kBox), to = uniform(tS + s * 64);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < kx)
-                            mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
+#pragma unroll 1
+                    for (int k = 0; k < kx; ++k)
+                        mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
                     if (leader) {
                         mma_commit(&s_full[s]);
                         if (own && q == ny - 1) mma_commit(&x_free[xs]);
@@ -346,10 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                         if (a == 0 && !wait.all(st_full, ci & 1, 108)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t xa = uniform(base + SM::X + xs * 4 * kBox);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < kx)
-                                mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), mndesc(base + SM::ST + k * 2048, kHalf), id_o, k > 0);
+#pragma unroll 1
+                        for (int k = 0; k < kx; ++k)
+                            mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), mndesc(base + SM::ST + k * 2048, kHalf), id_o, k > 0);
                         if (leader) {
                             if (!slow) mma_commit(&xs_full[xt & 1]);
                             if (own) mma_commit(&x_free[xs]);
@@ -360,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     tc_fence_after();
                     const uint32_t za = uniform(base + SM::YZ + (ys * 4 + 2) * kBox), from = uniform(tS + s * 64);
                     // the weights of each 32 columns lie at the beginning of their scores
-#pragma unroll
+#pragma unroll 1
                     for (int j = 0; j < 4; ++j)
                         mma_bf16_ts_one(leader, to, from + (j >> 1) * 32 + (j & 1) * 8, mndesc(za + j * 2048, kBox), id_o, 1u);
                     if (leader) {
@@ -443,15 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tmem_wait_st();
             }
 #pragma unroll 1
-            for (int c = 0; c < nz; c += 32) {
-                float v[32];
-                tmem_ld32(tH + lanes + c, v);
+            for (int c = 0; c < nz; c += 16) {
+                float v[16];
+                tmem_ld16(tH + lanes + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) st_scaled8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), v + 8 * i, seen2);
+                for (int i = 0; i < 2; ++i) st_scaled8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), v + 8 * i, seen2);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) unpack(mul2(pack(v[2 * i], v[2 * i + 1]), keep2), v[2 * i], v[2 * i + 1]);
-                tmem_st32(tH + lanes + c, v);
+                for (int i = 0; i < 8; ++i) unpack(mul2(pack(v[2 * i], v[2 * i + 1]), keep2), v[2 * i], v[2 * i + 1]);
+                tmem_st16(tH + lanes + c, reinterpret_cast<const uint32_t*>(v));
             }
             tmem_wait_st();
             fence_async_smem();
@@ -507,41 +501,45 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tc_fence_after();
                 if (live) {
                     const uint32_t at = tS + s * 64 + lanes + half * 32;
-                    uint32_t o[16];
-                    if (rev ? tq > cb : tq < cb) {
+                    const bool none = rev ? tq > cb : tq < cb, some = tq == cb || (rev && 32 * cb + 32 > t.n);
+#pragma unroll 1
+                    for (int c = 0; c < 32; c += 16) {
+                        uint32_t o[8];
+                        if (none) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = 0;
-                    } else {
-                        float v[32];
-                        tmem_ld32(at, v);
-                        tmem_wait_ld();
-                        if (slow) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                uint32_t f[4];
-                                ld_shared_v4(c0 + (32 * cb + 4 * k) * 4, f[0], f[1], f[2], f[3]);
-#pragma unroll
-                                for (int m = 0; m < 2; ++m)
-                                    unpack(mul2(pack(v[4 * k + 2 * m], v[4 * k + 2 * m + 1]), pack(__uint_as_float(f[2 * m]), __uint_as_float(f[2 * m + 1]))),
-                                           v[4 * k + 2 * m], v[4 * k + 2 * m + 1]);
-                            }
+                            for (int k = 0; k < 8; ++k) o[k] = 0;
                         } else {
+                            float v[16];
+                            tmem_ld16(at + c, v);
+                            tmem_wait_ld();
+                            if (slow) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int d = rev ? 32 * cb + k - i : i - 32 * cb - k;
-                                v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
+                                for (int k = 0; k < 4; ++k) {
+                                    uint32_t f[4];
+                                    ld_shared_v4(c0 + (32 * cb + c + 4 * k) * 4, f[0], f[1], f[2], f[3]);
+#pragma unroll
+                                    for (int m = 0; m < 2; ++m)
+                                        unpack(mul2(pack(v[4 * k + 2 * m], v[4 * k + 2 * m + 1]), pack(__uint_as_float(f[2 * m]), __uint_as_float(f[2 * m + 1]))),
+                                               v[4 * k + 2 * m], v[4 * k + 2 * m + 1]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const int d = rev ? 32 * cb + c + k - i : i - 32 * cb - c - k;
+                                    v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
+                                }
                             }
-                        }
-                        if (tq == cb || (rev && 32 * cb + 32 > t.n)) {
-                            // places on the wrong side, and of tokens behind the last one, are left out whatever they hold
-                            const int lo = rev && tq == cb ? lane : 0, hi = rev ? t.n - 32 * cb - 1 : lane;
+                            if (some) {
+                                // places on the wrong side, and of tokens behind the last one, are left out whatever they hold
+                                const int lo = (rev && tq == cb ? lane : 0) - c, hi = (rev ? t.n - 32 * cb - 1 : lane) - c;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = (!rev || k >= lo) && k <= hi ? v[k] : 0.0f;
-                        }
+                                for (int k = 0; k < 16; ++k) v[k] = (!rev || k >= lo) && k <= hi ? v[k] : 0.0f;
+                            }
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+                            for (int k = 0; k < 8; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+                        }
+                        tmem_st8(at + c / 2, o);  // over scores that this thread has read
                     }
-                    tmem_st16(at, o);
                 }
                 if (!slow && q == 0) {  // e^(l (i+1)) X S
                     if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) break;
@@ -549,13 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     if (live && z_on) {
                         const float f = i < t.n ? pw[rev ? t.n - 1 - i : i + 1] : 0.0f;
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 32) {
-                            float v[32];
-                            tmem_ld32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
+                        for (int c = 0; c < 64; c += 16) {
+                            float v[16];
+                            tmem_ld16(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] *= f;
-                            tmem_st32(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
+                            for (int k = 0; k < 16; ++k) v[k] *= f;
+                            tmem_st16(tO + (xt & 1) * 128 + lanes + 64 * half + c, reinterpret_cast<const uint32_t*>(v));
                         }
                     }
                 }
@@ -574,12 +572,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     if (own && lane == 0) bulk_wait_read();  // the rows before have left
                     __syncwarp();
 #pragma unroll 1
-                    for (int c = 0; c < 64; c += 32) {
-                        float v[32];
-                        tmem_ld32(tO + (hx & 1) * 128 + lanes + 64 * half + c, v);
+                    for (int c = 0; c < 64; c += 16) {
+                        float v[16];
+                        tmem_ld16(tO + (hx & 1) * 128 + lanes + 64 * half + c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) st_scaled8(stage + sw128(lane, (c >> 3) + k), v + 8 * k, rowf2);
+                        for (int k = 0; k < 2; ++k) st_scaled8(stage + sw128(lane, (c >> 3) + k), v + 8 * k, rowf2);
                     }
                     fence_async_smem();
                 }
