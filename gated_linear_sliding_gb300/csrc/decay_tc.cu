@@ -18,8 +18,8 @@
 // and what is rounded there would stay for the rest of the sequence.
 //
 // Warps: 0-7 the pairs' weights and the outputs (a thread holds one row's 32 of 64 pairs and 64 of 128 output
-// columns); 8-11 the state (a row of S to a thread; Y~); 12 the copies; 13 the MMAs of the scores, 14 of the
-// state, 15 of the outputs.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
+// columns); 8-15 the state (half a row of S to a thread; Y~); 16 the copies; 17 the MMAs of the scores, 18 of
+// the state, 19 of the outputs.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -35,7 +35,8 @@ using tc::kdesc;
 using tc::mndesc;
 
 constexpr int kMathWarps = 8;
-constexpr int kThreads = 32 * 16;
+constexpr int kStateWarps = 8;
+constexpr int kThreads = 32 * 20;
 constexpr uint32_t kBox = 8192;  // a box of 64 rows x 64 columns of bf16
 
 struct TcArgs {
@@ -64,21 +65,24 @@ template <bool REV>
 using Wide = Layout<2, 2, true, REV>;
 using Deep = Layout<2, 3, false, true>;
 
-// Waits with a limit.  When one runs out it is reported once and every role leaves.
+// Waits with a limit.  When one runs out it is reported once and every role leaves.  What happens while a
+// wait lasts is one function for all of them: in line, the waits would fill the instruction cache.
+__device__ __noinline__ bool spin(uint64_t* bar, uint32_t parity, unsigned where, volatile int* abort, WsHeader* header) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (clock64() - t0 > tc::kTimeout) {
+            if (atomicExch((int*)abort, 1) == 0) report(header, LIZARD_ERR_TIMEOUT, where);
+            return false;
+        }
+    }
+    return true;
+}
 struct Waiter {
     volatile int* abort;
     WsHeader* header;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, unsigned where) const {
-        if (mbar_try_wait(bar, parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity)) {
-            if (*abort) return false;
-            if (clock64() - t0 > tc::kTimeout) {
-                if (atomicExch((int*)abort, 1) == 0) report(header, LIZARD_ERR_TIMEOUT, where);
-                return false;
-            }
-        }
-        return true;
+        return mbar_try_wait(bar, parity) || spin(bar, parity, where, abort, header);
     }
     // by all lanes of a warp: one answer
     __device__ __forceinline__ bool all(uint64_t* bar, uint32_t parity, unsigned where) const {
@@ -101,15 +105,15 @@ __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
     return s;
 }
 
-// The tile of Y~ from y's, as high and low parts, by 128 threads (token, half of the columns); and rows of z
-// behind the tile's last token become zeros: 0 times what lies there may be NaN.
+// The tile of Y~ from y's, as high and low parts, by 64 PARTS threads (token, part of the columns); and rows
+// of z behind the tile's last token become zeros: 0 times what lies there may be NaN.
+template <int PARTS>
 __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt, int n, float f, int tid) {
-    const int tok = tid & 63, half = tid >> 6;
-    const uint32_t row = half * kBox + tok * 128;
+    const int tok = tid & 63, part = tid >> 6;
     const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t off = row + ((c ^ (tok & 7)) << 4);
+    for (int c = 16 / PARTS * part; c < 16 / PARTS * (part + 1); ++c) {
+        const uint32_t off = (c >> 3) * kBox + sw128(tok, c & 7);
         uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
         if (tok < n) ld_shared_v4(ys + off, w[0], w[1], w[2], w[3]);
 #pragma unroll
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         for (int i = 0; i < YST; ++i) {
             mbar_init(&yz_full[i], 1);
             mbar_init(&yz_free[i], 2);
-            mbar_init(&zz_full[i], 128);
+            mbar_init(&zz_full[i], 32 * kStateWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -215,15 +219,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             mbar_init(&pv_done[i], 1);
             mbar_init(&o_free[i], 32 * kMathWarps);
         }
-        mbar_init(kt_full, 128);
+        mbar_init(kt_full, 32 * kStateWarps);
         mbar_init(h_done, 1);
-        mbar_init(st_full, 128);
+        mbar_init(st_full, 32 * kStateWarps);
         mbar_init(xs_done, 1);
         for (int i = 0; i < 2; ++i) mbar_init(&drained[i], 1);
         *abort = 0;
         fence_mbar_init();
     }
-    if (warp == 13) {
+    if (warp == 17) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     Walk walk(p.seqs, w.b, w.lo, w.hi, rev, chunk);
     Tile t;
 
-    if (warp == 12) {
+    if (warp == 16) {
         if (lane == 0) {
             prefetch_tmap(&g.x);
             prefetch_tmap(&g.y);
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             }
         }
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 17) {
         // scores: X Y^T
         const uint32_t id_s = idesc_bf16(128, 64, false, false);
         uint32_t it = 0, xt = 0, yi = 0;
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             if (leader) mma_commit(&drained[0]);
             mbar_wait(&drained[0], 0, tc::kTimeout);
         }
-    } else if (warp == 15) {
+    } else if (warp == 19) {
         // outputs: X S, and P Z after it in the same accumulator
         const uint32_t id_o = idesc_bf16(128, nz, false, true);
         uint32_t it = 0, xt = 0, yi = 0, ci = 0;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             if (leader) mma_commit(&drained[1]);
             mbar_wait(&drained[1], 0, tc::kTimeout);
         }
-    } else if (warp == 14) {
+    } else if (warp == 18) {
         const uint32_t id_h = idesc_bf16(128, nz, true, true);
         uint32_t yi = 0;
         bool ok = true;
@@ -389,29 +393,49 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         }
         if (!ok && yi > 0) mbar_wait(h_done, (yi - 1) & 1, tc::kTimeout);
     } else if (warp >= 8) {
-        // the state: row `row` of S
-        const int row = tid - 256;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        // the state: row `row` of S, one half of its columns
+        const int in = tid - 32 * kMathWarps, row = in & 127, z0 = (in >> 7) * 64, z1 = min(z0 + 64, p.dz);
+        const uint32_t at = tH + ((uint32_t)(32 * (warp & 3)) << 16);
         const int64_t size = (int64_t)p.dx * p.dz;
-        const int step = p.transposed ? p.dx : 1;
-        const int64_t at = p.transposed ? row : (int64_t)row * p.dz;
         uint32_t yi = 0, ci = 0;
         bool ok = true, was_last = false;
         int was_seq = 0;
         grid_dep_wait();
-        // the state behind a sequence's last tile
+        // the state behind a sequence's last tile (a pass whose states are transposed leaves none)
         auto leave = [&](int seq) {
             if (p.fin == nullptr) return;
-            float* to = p.fin + (seq * p.Hkv + w.h) * size + at;
+            float* to = p.fin + (seq * p.Hkv + w.h) * size + (int64_t)row * p.dz;
 #pragma unroll 1
-            for (int c = 0; c < p.dz; c += 8, to += 8 * step) {
-                float v[8];
-                tmem_ld8(tH + lanes + c, v);
+            for (int c = z0; c < z1; c += 16) {
+                float v[16];
+                tmem_ld16(at + c, v);
                 tmem_wait_ld();
-                if (row < p.dx)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) to[i * step] = v[i];
+                for (int i = 0; i < 16; i += 4)
+                    if (row < p.dx && c + i < z1) *reinterpret_cast<float4*>(to + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
+        };
+        // a state from memory
+        auto fetch = [&](const float* from) {
+#pragma unroll 1
+            for (int c = z0; c < z0 + 64; c += 32) {
+                float v[32];
+                if (p.transposed) {
+                    const float* f = from + (int64_t)c * p.dx + row;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = from != nullptr && row < p.dx && c + (i & ~7) < z1 ? f[i * p.dx] : 0.0f;
+                } else {
+                    const float* f = from + (int64_t)row * p.dz + c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (from != nullptr && row < p.dx && c + i < z1) u = *reinterpret_cast<const float4*>(f + i);
+                        v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+                    }
+                }
+                tmem_st32(at + c, v);
+            }
+            tmem_wait_st();
         };
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (ci > 0) {
@@ -419,33 +443,22 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tc_fence_after();
                 if (was_last) leave(was_seq);
             }
+            if (t.first || ci == 0)
+                fetch(!t.first            ? p.recs + (w.unit * p.nseg + w.seg) * size
+                      : p.init == nullptr ? nullptr
+                                          : p.init + (t.seq * p.Hkv + w.h) * size);
             const float keep = pw[t.n], seen = !slow ? 1.0f : rev ? power(l2, t.n - 1 - mid) : pw[mid + 1];
             const f2 keep2 = pack(keep, keep), seen2 = pack(seen, seen);
-            const bool from_memory = t.first || ci == 0;
-            const float* from = !from_memory ? nullptr
-                                : t.first    ? (p.init == nullptr ? nullptr : p.init + (t.seq * p.Hkv + w.h) * size)
-                                             : p.recs + (w.unit * p.nseg + w.seg) * size;
-            if (from_memory) {
-                if (from != nullptr) from += at;
 #pragma unroll 1
-                for (int c = 0; c < nz; c += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = from != nullptr && row < p.dx && c < p.dz ? from[(c + i) * step] : 0.0f;
-                    tmem_st8(tH + lanes + c, reinterpret_cast<const uint32_t*>(v));
-                }
-                tmem_wait_st();
-            }
-#pragma unroll 1
-            for (int c = 0; c < nz; c += 16) {
+            for (int c = z0; c < z0 + 64 && c < nz; c += 16) {
                 float v[16];
-                tmem_ld16(tH + lanes + c, v);
+                tmem_ld16(at + c, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) st_scaled8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), v + 8 * i, seen2);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) unpack(mul2(pack(v[2 * i], v[2 * i + 1]), keep2), v[2 * i], v[2 * i + 1]);
-                tmem_st16(tH + lanes + c, reinterpret_cast<const uint32_t*>(v));
+                tmem_st16(at + c, reinterpret_cast<const uint32_t*>(v));
             }
             tmem_wait_st();
             fence_async_smem();
@@ -456,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 const int ys = yi % YST, j0 = 64 * (q % nsub);
                 if (!wait.all(&yz_full[ys], (yi / YST) & 1, 112)) { ok = false; break; }
                 if (q > 0 && !wait.all(h_done, (yi - 1) & 1, 113)) { ok = false; break; }
-                const int m = min(64, t.n - j0), tok = row & 63, far = rev ? j0 + tok + 1 : t.n - 1 - j0 - tok;
+                const int m = min(64, t.n - j0), tok = in & 63, far = rev ? j0 + tok + 1 : t.n - 1 - j0 - tok;
                 const uint32_t ya = base + SM::YZ + ys * 4 * kBox;
-                scale_rows(ya, ya + 2 * kBox, base + SM::KT, m, tok < m ? pw[far] * p.in_scale : 0.0f, row);
+                scale_rows<4>(ya, ya + 2 * kBox, base + SM::KT, m, tok < m ? pw[far] * p.in_scale : 0.0f, in);
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&zz_full[ys]);
@@ -630,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
@@ -744,7 +757,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 if (it >= 2 && !wait.all(&kt_free[group], ((it >> 1) & 1) ^ 1, 123)) { ok = false; break; }
                 const float f = tok < n ? power(l2, rev ? t0 + tok - r.from + 1 : r.to - 1 - t0 - tok) * p.in_scale : 0.0f;
                 const uint32_t ya = base + EndsSmem::YZ + s * 4 * kBox;
-                scale_rows(ya, ya + 2 * kBox, base + EndsSmem::KT + group * 4 * kBox, n, f, in);
+                scale_rows<2>(ya, ya + 2 * kBox, base + EndsSmem::KT + group * 4 * kBox, n, f, in);
                 fence_async_smem();
                 mbar_arrive(&kt_full[group]);
             }
