@@ -30,6 +30,7 @@ struct Where {  // of a CTA's segment
     int64_t unit, b, h, lo, hi;
     int seg, slice;
 };
+template <bool ENDS>
 __device__ __forceinline__ Where where_of(const DecayPass& p, int slices) {
     Where w;
     int64_t id = blockIdx.x;
@@ -37,6 +38,7 @@ __device__ __forceinline__ Where where_of(const DecayPass& p, int slices) {
     id /= slices;
     w.unit = id % p.units;
     w.seg = (int)(id / p.units);
+    if (ENDS) w.seg = ending_segment(p, w.seg);
     w.b = w.unit / p.Hkv;
     w.h = w.unit - w.b * p.Hkv;
     w.lo = (int64_t)w.seg * p.seg_len;
@@ -54,7 +56,7 @@ template <typename T, int NI>
 __global__ void __launch_bounds__(NT) decay_ends_kernel(const DecayPass p, float* recs) {
     extern __shared__ float sm[];
     const int slices = (p.dz + ZS - 1) / ZS;
-    const Where w = where_of(p, slices);
+    const Where w = where_of<true>(p, slices);
     check_offsets(p.seqs, p.header);
     const int ldx = (p.dx + 3) / 4 * 4 + 4;
     float *ys = sm, *zs = ys + kTile * ldx;
@@ -108,15 +110,16 @@ __global__ void __launch_bounds__(NT) decay_ends_kernel(const DecayPass p, float
         }
 }
 
-// The states in front of the segments from their own contributions, in place: an element a thread,
+// The states in front of the segments from their own contributions, in place: V elements a thread,
 // segments in the order of time (rev: against it).
-__global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, float* recs) {
+template <int V>
+__global__ void __launch_bounds__(128) decay_join_kernel(const DecayPass p, float* recs) {
     extern __shared__ float pass[];  // [nseg]: what of the state in front of a segment leaves it
-    const int64_t size = (int64_t)p.dx * p.dz, blocks = (size + 255) / 256;
-    const int64_t unit = blockIdx.x / blocks, e = (blockIdx.x % blocks) * 256 + threadIdx.x;
+    const int64_t size = (int64_t)p.dx * p.dz, blocks = (size / V + 127) / 128;
+    const int64_t unit = blockIdx.x / blocks, e = ((blockIdx.x % blocks) * 128 + threadIdx.x) * V;
     const int64_t b = unit / p.Hkv;
     const float l2 = log2_decay(p.log_decay, unit - b * p.Hkv);
-    for (int s = threadIdx.x; s < p.nseg; s += 256) {
+    for (int s = threadIdx.x; s < p.nseg; s += 128) {
         const int64_t lo = s * p.seg_len, hi = min64(lo + p.seg_len, p.seqs.L);
         pass[s] = reach(p.seqs, b, lo, hi, p.rev).whole ? -1.0f : power(l2, hi - lo);
     }
@@ -125,22 +128,24 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
     __syncthreads();
     if (e >= size) return;
     float* r = recs + unit * p.nseg * size + e;
-    float carry = 0.0f;
+    float carry[V] = {};
     constexpr int AHEAD = 8;
     for (int s0 = 0; s0 < p.nseg; s0 += AHEAD) {
-        float own[AHEAD];
+        float own[AHEAD][V];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int s = p.rev ? p.nseg - 1 - s0 - k : s0 + k;
-            if (s0 + k < p.nseg) own[k] = r[s * size];
+            if (s0 + k < p.nseg - 1) Vec<V>::ld(r + s * size, own[k]);  // the last segment's is nobody's first state
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int s = p.rev ? p.nseg - 1 - s0 - k : s0 + k;
             if (s0 + k < p.nseg) {
-                r[s * size] = carry;
+                Vec<V>::st(r + s * size, carry);
                 // a sequence that begins in the segment lets nothing pass, not even NaN
-                carry = pass[s] < 0.0f ? own[k] : fmaf(pass[s], carry, own[k]);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (s0 + k < p.nseg - 1) carry[i] = pass[s] < 0.0f ? own[k][i] : fmaf(pass[s], carry[i], own[k][i]);
             }
         }
     }
@@ -151,7 +156,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     extern __shared__ float sm[];
     const int slices = (p.dz + ZS - 1) / ZS;
-    const Where w = where_of(p, slices);
+    const Where w = where_of<false>(p, slices);
     check_offsets(p.seqs, p.header);
     const int dxp = (p.dx + 3) / 4 * 4, ldx = dxp + 4;
     float* xs = sm;
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
         __syncthreads();
         if (t.first || !begun) {
             const float* from = t.first ? (p.init == nullptr ? nullptr : p.init + (t.seq * p.Hkv + w.h) * size)
-                                        : p.recs + (w.unit * p.nseg + w.seg) * size;
+                                        : first_state(p, w.unit, w.seg);
             for (int e = threadIdx.x; e < dxp * ZS; e += NT) {
                 const int i = e / ZS, j = e % ZS;
                 st[e] = from != nullptr && i < p.dx && j < zn ? from[state_at(p, i, z0 + j)] : 0.0f;
@@ -305,13 +310,17 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     }
 }
 
-// States of empty sequences: what they begin with.
+// States of empty sequences: what they begin with.  1024 elements to a CTA.
 __global__ void __launch_bounds__(256) decay_empty_kernel(const Seqs s, const float* init, float* fin, int64_t Hkv, int64_t size) {
-    const int64_t seq = blockIdx.x / Hkv;
+    const int64_t blocks = (size + 1023) / 1024, state = blockIdx.x / blocks, seq = state / Hkv;
     int64_t end;
     if (s.cu != nullptr ? s.cu[seq + 1] != s.cu[seq] : seq_tokens(s, seq, &end) != 0) return;
-    const int64_t base = blockIdx.x * size;
-    for (int64_t e = threadIdx.x; e < size; e += 256) fin[base + e] = init != nullptr ? init[base + e] : 0.0f;
+    const int64_t first = blockIdx.x % blocks * 1024, base = state * size;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t e = first + k * 256 + threadIdx.x;
+        if (e < size) fin[base + e] = init != nullptr ? init[base + e] : 0.0f;
+    }
 }
 
 size_t ends_smem(int dx) { return sizeof(float) * (size_t)(kTile * ((dx + 3) / 4 * 4 + 4) + kTile * ZS); }
@@ -324,7 +333,7 @@ static_assert(kMostSmem <= 226 * 1024, "within a SM's shared memory");
 
 template <typename T>
 cudaError_t run_ends(const DecayPass& p, float* recs, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.units * p.nseg * ((p.dz + ZS - 1) / ZS));
+    const unsigned grid = (unsigned)(p.units * (p.nseg - 1) * ((p.dz + ZS - 1) / ZS));
     const auto kernel = p.dx <= 64 ? decay_ends_kernel<T, 4> : p.dx <= 128 ? decay_ends_kernel<T, 8> : decay_ends_kernel<T, 12>;
     const size_t sm = ends_smem(p.dx);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ends_smem(192));
@@ -342,12 +351,16 @@ cudaError_t run_pass(const DecayPass& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <int V>
 cudaError_t run_join(const DecayPass& p, float* recs, cudaStream_t s) {
-    const int64_t size = (int64_t)p.dx * p.dz;
-    const cudaError_t e = launch_dependent(decay_join_kernel, dim3((unsigned)(p.units * ((size + 255) / 256))), dim3(256),
+    const int64_t size = (int64_t)p.dx * p.dz / V;
+    const cudaError_t e = launch_dependent(decay_join_kernel<V>, dim3((unsigned)(p.units * ((size + 127) / 128))), dim3(128),
                                            sizeof(float) * p.nseg, s, p, recs);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+// Of two segments of a dense batch the one's end state is the other's first: nothing to join.
+int shift_of(const DecayPass& p) { return p.nseg == 2 && p.seqs.cu == nullptr ? (p.rev ? 1 : -1) : 0; }
 
 // The states in front of the segments, [units, nseg, dk, dv], from a pass that is not transposed.
 cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, cudaStream_t s) {
@@ -355,7 +368,8 @@ cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, 
     const cudaError_t e = decay_uses_tc(a)          ? decay_tc_ends(p, recs, s)
                           : a.dtype == LIZARD_F32 ? run_ends<float>(p, recs, s)
                                                   : run_ends<__nv_bfloat16>(p, recs, s);
-    return e != cudaSuccess ? e : run_join(p, recs, s);
+    if (e != cudaSuccess || shift_of(p) != 0) return e;
+    return a.dk * a.dv % 4 == 0 ? run_join<4>(p, recs, s) : run_join<1>(p, recs, s);
 }
 
 cudaError_t outputs(const DecayArgs& a, const DecayPass& p, cudaStream_t s) {
@@ -365,7 +379,7 @@ cudaError_t outputs(const DecayArgs& a, const DecayPass& p, cudaStream_t s) {
 
 cudaError_t empty_states(const DecayArgs& a, const float* init, float* fin, cudaStream_t s) {
     if (fin == nullptr || fin == init || (a.seqs.cu == nullptr && a.seqs.L > 0)) return cudaSuccess;
-    decay_empty_kernel<<<(unsigned)(a.nstate * a.Hkv), 256, 0, s>>>(a.seqs, init, fin, a.Hkv, a.dk * a.dv);
+    decay_empty_kernel<<<(unsigned)(a.nstate * a.Hkv * ((a.dk * a.dv + 1023) / 1024)), 256, 0, s>>>(a.seqs, init, fin, a.Hkv, a.dk * a.dv);
     return cudaGetLastError();
 }
 
@@ -403,6 +417,7 @@ DecayPass base_pass(const DecayArgs& a) {
     p.header = a.header;
     p.in_scale = p.out_scale = 1.0f;
     cut(a, &p);
+    p.rec_shift = shift_of(p);
     return p;
 }
 
@@ -435,6 +450,7 @@ DecayPass dv_pass(const DecayArgs& a) {
     p.dx = (int)a.dk, p.dz = (int)a.dv;
     p.gx = 1, p.gy = (int)(a.Hq / a.Hkv);
     p.rev = true;
+    p.rec_shift = shift_of(p);
     p.in_scale = a.scale;
     p.init = a.ds_out;
     p.fin = a.ds0;

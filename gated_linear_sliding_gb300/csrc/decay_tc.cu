@@ -60,9 +60,12 @@ struct Layout {
     static constexpr uint32_t BYTES = BARS + 304 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
-// many rows of x for each of y and z; many of y and z for each of x (a sum over heads)
+// several tiles of x for each of y and z; one of each; several of y and z for each of x (a sum over heads).
+// One stage of x is enough where its last reader is done long before the chunk is, and leaves room for a third
+// of y and z, whose copies otherwise wait for the chunk before.
+using Wide = Layout<2, 2, true, false>;
 template <bool REV>
-using Wide = Layout<2, 2, true, REV>;
+using Even = Layout<1, 3, true, REV>;
 using Deep = Layout<2, 3, false, true>;
 
 // Waits with a limit.  When one runs out it is reported once and every role leaves.  What happens while a
@@ -94,10 +97,12 @@ struct Seg {
     int64_t unit, b, h, lo, hi;
     int seg;
 };
+template <bool ENDS>
 __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
     Seg s;
     s.unit = blockIdx.x % p.units;
     s.seg = (int)(blockIdx.x / p.units);
+    if (ENDS) s.seg = ending_segment(p, s.seg);
     s.b = s.unit / p.Hkv;
     s.h = s.unit - s.b * p.Hkv;
     s.lo = (int64_t)s.seg * p.seg_len;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
-    const Seg w = seg_of(p);
+    const Seg w = seg_of<false>(p);
     check_offsets(p.seqs, p.header);
     const bool tall = p.gx == 1;                 // a tile of x: 128 tokens of a head, or 64 of two
     const int chunk = tall ? 128 : 64, mid = chunk / 2 - 1;
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (was_last) leave(was_seq);
             }
             if (t.first || ci == 0)
-                fetch(!t.first            ? p.recs + (w.unit * p.nseg + w.seg) * size
+                fetch(!t.first            ? first_state(p, w.unit, w.seg)
                       : p.init == nullptr ? nullptr
                                           : p.init + (t.seq * p.Hkv + w.h) * size);
             const float keep = pw[t.n], seen = !slow ? 1.0f : rev ? power(l2, t.n - 1 - mid) : pw[mid + 1];
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 13);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Seg w = seg_of(p);
+    const Seg w = seg_of<true>(p);
     check_offsets(p.seqs, p.header);
     const float l2 = log2_decay(p.log_decay, w.h);
     if (tid == 0) {
@@ -831,7 +836,7 @@ cudaError_t go_ends(const TcArgs& a, float* recs, cudaStream_t s) {
     const auto kernel = decay_tc_ends_kernel<rev>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)EndsSmem::BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.p.units * a.p.nseg), kEndsThreads, EndsSmem::BYTES, s>>>(a, recs);
+    kernel<<<(unsigned)(a.p.units * (a.p.nseg - 1)), kEndsThreads, EndsSmem::BYTES, s>>>(a, recs);
     return cudaGetLastError();
 }
 
@@ -853,8 +858,9 @@ cudaError_t decay_tc_ends(const DecayPass& p, float* recs, cudaStream_t s) {
 cudaError_t decay_tc_pass(const DecayPass& p, cudaStream_t s) {
     TcArgs a;
     if (!args_of(p, &a)) return cudaErrorInvalidValue;
-    if (!p.rev) return go<Wide<false>>(a, s);
-    return p.gy > 1 ? go<Deep>(a, s) : go<Wide<true>>(a, s);
+    if (p.gx > 1) return go<Wide>(a, s);
+    if (p.gy > 1) return go<Deep>(a, s);
+    return p.rev ? go<Even<true>>(a, s) : go<Even<false>>(a, s);
 }
 
 }  // namespace lz

@@ -77,9 +77,9 @@ struct DecayPass {
     float out_scale, in_scale;
     const float *log_decay, *init;
     float* fin;
-    const float* recs;  // state in front of each segment, [units, nseg, dk, dv]; null with one segment
+    const float* recs;  // a segment's first state is entry seg + rec_shift of [units, nseg, dk, dv]
     int64_t units, Hkv, seg_len;
-    int nseg;
+    int nseg, rec_shift;
     Seqs seqs;
     WsHeader* header;
 };

@@ -85,7 +85,7 @@ bool decay_args(const lizard_decay_dims* d, bool step, DecayArgs* a) {
 // Sizes the kernels are compiled for, and grids that fit.
 bool decay_compiled(const DecayArgs& a) {
     return a.dk <= 192 && a.dv <= 192 && a.Hq / a.Hkv <= 1 << 16 && grid_ok((double)a.B * (double)a.Hkv * 1024.0) &&
-           grid_ok((double)a.nstate * (double)a.Hkv * 8.0);
+           grid_ok((double)a.nstate * (double)a.Hkv * 64.0);
 }
 
 }  // namespace
