@@ -110,16 +110,17 @@ __global__ void __launch_bounds__(NT) decay_ends_kernel(const DecayPass p, float
         }
 }
 
-// The states in front of the segments from their own contributions, in place: V elements a thread,
-// segments in the order of time (rev: against it).
-template <int V>
-__global__ void __launch_bounds__(128) decay_join_kernel(const DecayPass p, float* recs) {
+// The states in front of the segments from their own contributions, in place: an element a thread,
+// segments in the order of time (rev: against it).  Bound by latency, so single elements, many threads, and
+// some segments' loads ahead (19 segments of 8 heads: 12 us with four elements a thread, 11 with 32 segments ahead,
+// whose registers cost threads).
+__global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, float* recs) {
     extern __shared__ float pass[];  // [nseg]: what of the state in front of a segment leaves it
-    const int64_t size = (int64_t)p.dx * p.dz, blocks = (size / V + 127) / 128;
-    const int64_t unit = blockIdx.x / blocks, e = ((blockIdx.x % blocks) * 128 + threadIdx.x) * V;
+    const int64_t size = (int64_t)p.dx * p.dz, blocks = (size + 255) / 256;
+    const int64_t unit = blockIdx.x / blocks, e = (blockIdx.x % blocks) * 256 + threadIdx.x;
     const int64_t b = unit / p.Hkv;
     const float l2 = log2_decay(p.log_decay, unit - b * p.Hkv);
-    for (int s = threadIdx.x; s < p.nseg; s += 128) {
+    for (int s = threadIdx.x; s < p.nseg; s += 256) {
         const int64_t lo = s * p.seg_len, hi = min64(lo + p.seg_len, p.seqs.L);
         pass[s] = reach(p.seqs, b, lo, hi, p.rev).whole ? -1.0f : power(l2, hi - lo);
     }
@@ -128,24 +129,22 @@ __global__ void __launch_bounds__(128) decay_join_kernel(const DecayPass p, floa
     __syncthreads();
     if (e >= size) return;
     float* r = recs + unit * p.nseg * size + e;
-    float carry[V] = {};
-    constexpr int AHEAD = 8;
+    float carry = 0.0f;
+    constexpr int AHEAD = 10;
     for (int s0 = 0; s0 < p.nseg; s0 += AHEAD) {
-        float own[AHEAD][V];
+        float own[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int s = p.rev ? p.nseg - 1 - s0 - k : s0 + k;
-            if (s0 + k < p.nseg - 1) Vec<V>::ld(r + s * size, own[k]);  // the last segment's is nobody's first state
+            if (s0 + k < p.nseg - 1) own[k] = r[s * size];  // the last segment's is nobody's first state
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int s = p.rev ? p.nseg - 1 - s0 - k : s0 + k;
             if (s0 + k < p.nseg) {
-                Vec<V>::st(r + s * size, carry);
+                r[s * size] = carry;
                 // a sequence that begins in the segment lets nothing pass, not even NaN
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (s0 + k < p.nseg - 1) carry[i] = pass[s] < 0.0f ? own[k][i] : fmaf(pass[s], carry[i], own[k][i]);
+                if (s0 + k < p.nseg - 1) carry = pass[s] < 0.0f ? own[k] : fmaf(pass[s], carry, own[k]);
             }
         }
     }
@@ -351,10 +350,9 @@ cudaError_t run_pass(const DecayPass& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int V>
 cudaError_t run_join(const DecayPass& p, float* recs, cudaStream_t s) {
-    const int64_t size = (int64_t)p.dx * p.dz / V;
-    const cudaError_t e = launch_dependent(decay_join_kernel<V>, dim3((unsigned)(p.units * ((size + 127) / 128))), dim3(128),
+    const int64_t size = (int64_t)p.dx * p.dz;
+    const cudaError_t e = launch_dependent(decay_join_kernel, dim3((unsigned)(p.units * ((size + 255) / 256))), dim3(256),
                                            sizeof(float) * p.nseg, s, p, recs);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -369,7 +367,7 @@ cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, 
                           : a.dtype == LIZARD_F32 ? run_ends<float>(p, recs, s)
                                                   : run_ends<__nv_bfloat16>(p, recs, s);
     if (e != cudaSuccess || shift_of(p) != 0) return e;
-    return a.dk * a.dv % 4 == 0 ? run_join<4>(p, recs, s) : run_join<1>(p, recs, s);
+    return run_join(p, recs, s);
 }
 
 cudaError_t outputs(const DecayArgs& a, const DecayPass& p, cudaStream_t s) {

@@ -112,11 +112,11 @@ __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
 
 // The tile of Y~ from y's, as high and low parts, by 64 PARTS threads (token, part of the columns); and rows
 // of z behind the tile's last token become zeros: 0 times what lies there may be NaN.
-template <int PARTS>
+template <int PARTS, int UNROLL>
 __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt, int n, float f, int tid) {
     const int tok = tid & 63, part = tid >> 6;
     const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int c = 16 / PARTS * part; c < 16 / PARTS * (part + 1); ++c) {
         const uint32_t off = (c >> 3) * kBox + sw128(tok, c & 7);
         uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (q > 0 && !wait.all(h_done, (yi - 1) & 1, 113)) { ok = false; break; }
                 const int m = min(64, t.n - j0), tok = in & 63, far = rev ? j0 + tok + 1 : t.n - 1 - j0 - tok;
                 const uint32_t ya = base + SM::YZ + ys * 4 * kBox;
-                scale_rows<4>(ya, ya + 2 * kBox, base + SM::KT, m, tok < m ? pw[far] * p.in_scale : 0.0f, in);
+                scale_rows<4, 1>(ya, ya + 2 * kBox, base + SM::KT, m, tok < m ? pw[far] * p.in_scale : 0.0f, in);
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&zz_full[ys]);
@@ -657,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 // ------------------------------------------------------------------------- segments' end states
 
 // A segment's own contribution to the state that leaves it, from all tokens that reach it, each with its
-// whole power of the decay: S stays in TMEM and nothing is scaled on the way.  Two groups of four warps make
-// Y~ in turn, warp 8 copies, warp 9 issues the MMAs.
-constexpr int kEndsThreads = 320, kEndsStages = 4;
+// whole power of the decay: S stays in TMEM and nothing is scaled on the way.  Two groups of eight warps make
+// Y~ in turn, warp 16 copies, warp 17 issues the MMAs.
+constexpr int kEndsThreads = 576, kEndsStages = 4;
 struct EndsSmem {
     static constexpr uint32_t YZ = 0;
     static constexpr uint32_t KT = kEndsStages * 4 * kBox;
@@ -688,14 +688,14 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             mbar_init(&yz_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kt_full[i], 128);
+            mbar_init(&kt_full[i], 256);
             mbar_init(&kt_free[i], 1);
         }
         mbar_init(done, 1);
         *abort = 0;
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(tmem_slot, 128);
         tmem_relinquish();
     }
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
     const Reach r = reach(p.seqs, w.b, w.lo, w.hi, rev);
     const uint32_t items = (uint32_t)((r.to - r.from + kTile - 1) / kTile) * p.gy;
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             prefetch_tmap(&g.y);
             prefetch_tmap(&g.z);
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                     mbar_wait(&yz_full[q % kEndsStages], (q / kEndsStages) & 1, tc::kTimeout);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         const bool leader = lane == 0;
         const uint32_t id_h = idesc_bf16(128, nz, true, true);
         uint32_t it = 0;
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
         if (leader) mma_commit(done);
         if (it < items) mbar_wait(done, 0, tc::kTimeout);
     } else {
-        const int group = warp >> 2, in = tid & 127, tok = in & 63;
+        const int group = warp >> 3, in = tid & 255, tok = in & 63;
         uint32_t it = 0;
         bool ok = true;
         for (int64_t t0 = r.from; t0 < r.to && ok; t0 += kTile) {
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 if (it >= 2 && !wait.all(&kt_free[group], ((it >> 1) & 1) ^ 1, 123)) { ok = false; break; }
                 const float f = tok < n ? power(l2, rev ? t0 + tok - r.from + 1 : r.to - 1 - t0 - tok) * p.in_scale : 0.0f;
                 const uint32_t ya = base + EndsSmem::YZ + s * 4 * kBox;
-                scale_rows<2>(ya, ya + 2 * kBox, base + EndsSmem::KT + group * 4 * kBox, n, f, in);
+                scale_rows<4, 4>(ya, ya + 2 * kBox, base + EndsSmem::KT + group * 4 * kBox, n, f, in);
                 fence_async_smem();
                 mbar_arrive(&kt_full[group]);
             }
@@ -774,28 +774,27 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             float* to = recs + (w.unit * p.nseg + w.seg) * size + (int64_t)row * p.dz;
             const float* from = r.whole && p.init != nullptr ? p.init + (r.seq * p.Hkv + w.h) * size + (int64_t)row * p.dz : nullptr;
             const float f = from != nullptr ? power(l2, r.to - r.from) : 0.0f;
-            for (int c = 64 * group; c < 64 * group + 64 && c < p.dz; c += 32) {
-                float v[32];
-                tmem_ld32(tb + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
-                tmem_wait_ld();
-                if (row < p.dx) {
+            const int c = 32 * (warp >> 2);  // 32 of the row's columns
+            float v[32];
+            tmem_ld32(tb + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
+            tmem_wait_ld();
+            if (row < p.dx) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        if (c + k >= p.dz) continue;
-                        float4 u = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                        if (from != nullptr) {
-                            const float4 i = *reinterpret_cast<const float4*>(from + c + k);
-                            u.x = fmaf(f, i.x, u.x), u.y = fmaf(f, i.y, u.y), u.z = fmaf(f, i.z, u.z), u.w = fmaf(f, i.w, u.w);
-                        }
-                        *reinterpret_cast<float4*>(to + c + k) = u;
+                for (int k = 0; k < 32; k += 4) {
+                    if (c + k >= p.dz) continue;
+                    float4 u = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    if (from != nullptr) {
+                        const float4 i = *reinterpret_cast<const float4*>(from + c + k);
+                        u.x = fmaf(f, i.x, u.x), u.y = fmaf(f, i.y, u.y), u.z = fmaf(f, i.z, u.z), u.w = fmaf(f, i.w, u.w);
                     }
+                    *reinterpret_cast<float4*>(to + c + k) = u;
                 }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tb, 128);
     }
