@@ -64,7 +64,7 @@ struct Walk {
 // Segments whose end state another one begins with: all but the last in the order of time.
 __device__ __forceinline__ int ending_segment(const DecayPass& p, int i) { return p.rev ? i + 1 : i; }
 __device__ __forceinline__ const float* first_state(const DecayPass& p, int64_t unit, int seg) {
-    return p.recs + (unit * p.nseg + seg + p.rec_shift) * p.dx * p.dz;
+    return p.recs + (unit * p.nseg + (p.parts > 0 ? 0 : seg)) * p.dx * p.dz;
 }
 
 // The part of a segment whose tokens reach the state that leaves it: tokens [from, to), and whether

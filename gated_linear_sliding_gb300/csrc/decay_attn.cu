@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(NT) decay_ends_kernel(const DecayPass p, float
             }
         }
     }
-    float* out = recs + (w.unit * p.nseg + w.seg) * p.dx * p.dz;
+    float* out = recs + (w.unit * p.nseg + (p.parts > 0 ? 0 : w.seg)) * p.dx * p.dz;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -357,8 +357,12 @@ cudaError_t run_join(const DecayPass& p, float* recs, cudaStream_t s) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Of two segments of a dense batch the one's end state is the other's first: nothing to join.
-int shift_of(const DecayPass& p) { return p.nseg == 2 && p.seqs.cu == nullptr ? (p.rev ? 1 : -1) : 0; }
+// Of two segments of a dense batch the one's end state is the other's first: nothing to join.  On the tensor
+// cores two CTAs share such a segment where that keeps within a CTA a SM.
+int parts_of(const DecayArgs& a, const DecayPass& p) {
+    if (p.nseg != 2 || a.seqs.cu != nullptr) return 0;
+    return decay_uses_tc(a) && p.units <= 76 ? 2 : 1;
+}
 
 // The states in front of the segments, [units, nseg, dk, dv], from a pass that is not transposed.
 cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, cudaStream_t s) {
@@ -366,7 +370,7 @@ cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, 
     const cudaError_t e = decay_uses_tc(a)          ? decay_tc_ends(p, recs, s)
                           : a.dtype == LIZARD_F32 ? run_ends<float>(p, recs, s)
                                                   : run_ends<__nv_bfloat16>(p, recs, s);
-    if (e != cudaSuccess || shift_of(p) != 0) return e;
+    if (e != cudaSuccess || p.parts > 0) return e;
     return run_join(p, recs, s);
 }
 
@@ -415,7 +419,7 @@ DecayPass base_pass(const DecayArgs& a) {
     p.header = a.header;
     p.in_scale = p.out_scale = 1.0f;
     cut(a, &p);
-    p.rec_shift = shift_of(p);
+    p.parts = parts_of(a, p);
     return p;
 }
 
@@ -448,7 +452,6 @@ DecayPass dv_pass(const DecayArgs& a) {
     p.dx = (int)a.dk, p.dz = (int)a.dv;
     p.gx = 1, p.gy = (int)(a.Hq / a.Hkv);
     p.rev = true;
-    p.rec_shift = shift_of(p);
     p.in_scale = a.scale;
     p.init = a.ds_out;
     p.fin = a.ds0;

@@ -102,7 +102,7 @@ __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
     Seg s;
     s.unit = blockIdx.x % p.units;
     s.seg = (int)(blockIdx.x / p.units);
-    if (ENDS) s.seg = ending_segment(p, s.seg);
+    if (ENDS) s.seg = ending_segment(p, p.parts > 0 ? 0 : s.seg);
     s.b = s.unit / p.Hkv;
     s.h = s.unit - s.b * p.Hkv;
     s.lo = (int64_t)s.seg * p.seg_len;
@@ -161,8 +161,9 @@ __device__ __forceinline__ void mma_bf16_ts_one(bool leader, uint32_t d_tmem, ui
 }
 
 // S += Y~^T Z over a tile's 64 tokens, both parts; by a warp.
+template <int UNROLL>
 __device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, uint32_t zs, uint32_t idesc, bool fresh) {
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int j = 0; j < 8; ++j)
         mma_bf16_one(leader, d, mndesc(kt + (j >> 2) * 2 * kBox + (j & 3) * 2048, kBox), mndesc(zs + (j & 3) * 2048, kBox), idesc, fresh && j == 0 ? 0u : 1u);
 }
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             for (int q = 0; q < ny; ++q, ++yi) {
                 if (!wait.all(kt_full, yi & 1, 109)) { ok = false; break; }
                 tc_fence_after();
-                state_mmas(leader, tH, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), id_h, false);
+                state_mmas<1>(leader, tH, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), id_h, false);
                 if (leader) {
                     mma_commit(h_done);
                     mma_commit(&yz_free[yi % YST]);
@@ -420,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     if (row < p.dx && c + i < z1) *reinterpret_cast<float4*>(to + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
         };
-        // a state from memory
-        auto fetch = [&](const float* from) {
+        // a state from memory, or added to what is there
+        auto fetch = [&](const float* from, bool add) {
 #pragma unroll 1
             for (int c = z0; c < z0 + 64; c += 32) {
                 float v[32];
@@ -438,6 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                         v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
                     }
                 }
+                if (add) {
+                    float old[32];
+                    tmem_ld32(at + c, old);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += old[i];
+                }
                 tmem_st32(at + c, v);
             }
             tmem_wait_st();
@@ -448,10 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tc_fence_after();
                 if (was_last) leave(was_seq);
             }
-            if (t.first || ci == 0)
-                fetch(!t.first            ? first_state(p, w.unit, w.seg)
-                      : p.init == nullptr ? nullptr
-                                          : p.init + (t.seq * p.Hkv + w.h) * size);
+            if (t.first || ci == 0) {
+                const float* from = !t.first            ? first_state(p, w.unit, w.seg)
+                                    : p.init == nullptr ? nullptr
+                                                        : p.init + (t.seq * p.Hkv + w.h) * size;
+                const int parts = t.first || p.parts < 2 ? 1 : 2;
+#pragma unroll 1
+                for (int k = 0; k < parts; ++k) fetch(k == 0 ? from : from + size, k > 0);
+            }
             const float keep = pw[t.n], seen = !slow ? 1.0f : rev ? power(l2, t.n - 1 - mid) : pw[mid + 1];
             const f2 keep2 = pack(keep, keep), seen2 = pack(seen, seen);
 #pragma unroll 1
@@ -706,7 +718,13 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
     const uint32_t tb = *tmem_slot;
     const Waiter wait{abort, p.header};
     const int nhx = (p.dx + 63) / 64, nhz = (p.dz + 63) / 64, nz = (p.dz + 15) / 16 * 16;
-    const Reach r = reach(p.seqs, w.b, w.lo, w.hi, rev);
+    Reach r = reach(p.seqs, w.b, w.lo, w.hi, rev);
+    const int64_t end = r.to, begin = r.from;  // of the tokens that reach the state
+    if (p.parts == 2) {                        // this CTA's half of them
+        const int64_t cut = r.from + ((r.to - r.from + 2 * kTile - 1) / (2 * kTile)) * kTile;
+        if (blockIdx.x < p.units) r.to = min64(cut, end);
+        else r.from = min64(cut, end), r.whole = false;
+    }
     const uint32_t items = (uint32_t)((r.to - r.from + kTile - 1) / kTile) * p.gy;
 
     if (warp == 16) {
@@ -740,7 +758,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             const int k = it & 1;
             if (!wait.all(&kt_full[k], (it >> 1) & 1, 121)) break;
             tc_fence_after();
-            state_mmas(leader, tb, uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), id_h,
+            state_mmas<8>(leader, tb, uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), id_h,
                        it == 0);
             if (leader) {
                 mma_commit(&kt_free[k]);
@@ -760,7 +778,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 const int s = it % kEndsStages;
                 if (!wait.all(&yz_full[s], (it / kEndsStages) & 1, 122)) { ok = false; break; }
                 if (it >= 2 && !wait.all(&kt_free[group], ((it >> 1) & 1) ^ 1, 123)) { ok = false; break; }
-                const float f = tok < n ? power(l2, rev ? t0 + tok - r.from + 1 : r.to - 1 - t0 - tok) * p.in_scale : 0.0f;
+                const float f = tok < n ? power(l2, rev ? t0 + tok - begin + 1 : end - 1 - t0 - tok) * p.in_scale : 0.0f;
                 const uint32_t ya = base + EndsSmem::YZ + s * 4 * kBox;
                 scale_rows<4, 4>(ya, ya + 2 * kBox, base + EndsSmem::KT + group * 4 * kBox, n, f, in);
                 fence_async_smem();
@@ -771,13 +789,17 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             tc_fence_after();
             const int row = 32 * (warp & 3) + lane;
             const int64_t size = (int64_t)p.dx * p.dz;
-            float* to = recs + (w.unit * p.nseg + w.seg) * size + (int64_t)row * p.dz;
+            float* to = recs + (w.unit * p.nseg + (p.parts > 0 ? (int)(blockIdx.x / p.units) : w.seg)) * size + (int64_t)row * p.dz;
             const float* from = r.whole && p.init != nullptr ? p.init + (r.seq * p.Hkv + w.h) * size + (int64_t)row * p.dz : nullptr;
-            const float f = from != nullptr ? power(l2, r.to - r.from) : 0.0f;
+            const float f = from != nullptr ? power(l2, end - begin) : 0.0f;
             const int c = 32 * (warp >> 2);  // 32 of the row's columns
             float v[32];
             tmem_ld32(tb + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
             tmem_wait_ld();
+            if (items == 0) {  // a half without tokens
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+            }
             if (row < p.dx) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
@@ -835,7 +857,7 @@ cudaError_t go_ends(const TcArgs& a, float* recs, cudaStream_t s) {
     const auto kernel = decay_tc_ends_kernel<rev>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)EndsSmem::BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.p.units * (a.p.nseg - 1)), kEndsThreads, EndsSmem::BYTES, s>>>(a, recs);
+    kernel<<<(unsigned)(a.p.units * (a.p.parts > 0 ? a.p.parts : a.p.nseg - 1)), kEndsThreads, EndsSmem::BYTES, s>>>(a, recs);
     return cudaGetLastError();
 }
 

@@ -77,9 +77,11 @@ struct DecayPass {
     float out_scale, in_scale;
     const float *log_decay, *init;
     float* fin;
-    const float* recs;  // a segment's first state is entry seg + rec_shift of [units, nseg, dk, dv]
+    // The segments' first states, [units, nseg, dk, dv]; with `parts` (two segments of a dense batch, where the
+    // one's end is the other's beginning) the sum of a unit's first `parts` entries.
+    const float* recs;
     int64_t units, Hkv, seg_len;
-    int nseg, rec_shift;
+    int nseg, parts;
     Seqs seqs;
     WsHeader* header;
 };
