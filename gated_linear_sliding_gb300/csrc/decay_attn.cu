@@ -500,8 +500,19 @@ __global__ void __launch_bounds__(SNT) decay_step_kernel(const DecayArgs a) {
             if (c0 + e % SW < dv) lz::st(out + (int64_t)(e / SW) * dv + c0 + e % SW, 0.0f);
         return;
     }
-    const float keep = power(log2_decay(a.log_decay, h), 1);
     float* S = a.state + (slot * a.Hkv + h) * dk * dv;
+    float s[R][V];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = r0 + r * RG;
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[r][i] = 0.0f;
+            if (on && row < dk) Vec<V>::ld(S + (int64_t)row * dv + c, s[r]);
+        }
+    };
+    fetch(rg);  // before anything else: these loads are what the time goes to
+    const float keep = power(log2_decay(a.log_decay, h), 1);
     float v[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
@@ -514,14 +525,7 @@ __global__ void __launch_bounds__(SNT) decay_step_kernel(const DecayArgs a) {
         __syncthreads();
         float acc[GH][V] = {};
         for (int r0 = rg; r0 < dk; r0 += RG * R) {
-            float s[R][V];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int row = r0 + r * RG;
-#pragma unroll
-                for (int i = 0; i < V; ++i) s[r][i] = 0.0f;
-                if (on && row < dk) Vec<V>::ld(S + (int64_t)row * dv + c, s[r]);
-            }
+            if (g0 > 0 || r0 > rg) fetch(r0);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = r0 + r * RG;

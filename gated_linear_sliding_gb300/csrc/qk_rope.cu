@@ -3,13 +3,14 @@
 //   n = w x / sqrt(mean(x^2) + eps),   (y1, y2) = (n1 cos a - n2 sin a, n2 cos a + n1 sin a)
 //   dn = the rotation of dy by -a,   dw = sum dn xhat,   dx = rs (w dn - xhat mean(w dn xhat)),  xhat = rs x
 //
-// Bound by HBM: each value is read and written once.  A warp takes one token and walks its heads, so that
-// the angles, which depend on the token alone, stay in registers; a lane holds the same pairs of each
-// head (2 E values: both members of a pair, so the rotation needs no exchange), and as few lanes as
-// that allows make a head, so that its sum of squares takes three steps for 128 values.
+// Bound by HBM: each value is read and written once.  A warp takes one token and walks its heads.  The token's
+// cosines and sines are made by the warp's lanes once, lie in shared memory, and go to registers for all heads; a
+// lane holds the same pairs of each head (both members, so the rotation needs no exchange), and as few lanes as that
+// allows make a head, so that its sum of squares takes three steps for 128 values.  What a lane does is in pairs of
+// fp32 registers, and the norm's factor goes into cosine and sine.
 //
 // Angles.  A frequency is kept as a 64-bit fraction of a turn (2^64 freq / 2 pi, made from the fp32 mantissa
-// by integer products), so a position times it modulo 2^64 is the angle's fraction of a turn with an
+// by integer products, once a CTA), so a position times it modulo 2^64 is the angle's fraction of a turn with an
 // error of |position| 2^-64 turns, at any position; its upper 32 bits go through sincospi.
 #include "heads.h"
 
@@ -65,44 +66,92 @@ RopePlan plan_of(const RopeArgs& a, int64_t want_items) {
     return p;
 }
 
+// A pair's frequency.
+struct Freq {
+    uint64_t turn;
+    float wild;  // NaN for a frequency that is not finite, else 0
+    int axis;
+};
+
+// E pairs of a head, the first members and the second ones, as pairs of registers.
+template <int E>
+struct Pairs {
+    f2 a[E / 2], b[E / 2];
+};
+// From a lane's pieces as they lie in memory: piece 2 g holds the first members and 2 g + 1 the second ones, or
+// (NEAR) the two hold neighbours.
+template <int V, int NG, bool NEAR>
+__device__ __forceinline__ Pairs<V * NG> sorted(const float* v) {
+    Pairs<V * NG> r;
+#pragma unroll
+    for (int e = 0; e < V * NG; e += 2) {
+        const int i = 2 * (e / V) * V, m = e % V;
+        if (V == 1) {
+            r.a[e / 2] = pack(v[2 * e], v[2 * e + 2]);
+            r.b[e / 2] = pack(v[2 * e + 1], v[2 * e + 3]);
+        } else if (NEAR) {
+            r.a[e / 2] = pack(v[i + 2 * m], v[i + 2 * m + 2]);
+            r.b[e / 2] = pack(v[i + 2 * m + 1], v[i + 2 * m + 3]);
+        } else {
+            r.a[e / 2] = pack(v[i + m], v[i + m + 1]);
+            r.b[e / 2] = pack(v[i + V + m], v[i + V + m + 1]);
+        }
+    }
+    return r;
+}
+template <int V, int NG, bool NEAR>
+__device__ __forceinline__ void unsorted(const Pairs<V * NG>& r, float* v) {
+#pragma unroll
+    for (int e = 0; e < V * NG; e += 2) {
+        const int i = 2 * (e / V) * V, m = e % V;
+        if (V == 1) {
+            unpack(r.a[e / 2], v[2 * e], v[2 * e + 2]);
+            unpack(r.b[e / 2], v[2 * e + 1], v[2 * e + 3]);
+        } else if (NEAR) {
+            unpack(r.a[e / 2], v[i + 2 * m], v[i + 2 * m + 2]);
+            unpack(r.b[e / 2], v[i + 2 * m + 1], v[i + 2 * m + 3]);
+        } else {
+            unpack(r.a[e / 2], v[i + m], v[i + m + 1]);
+            unpack(r.b[e / 2], v[i + V + m], v[i + V + m + 1]);
+        }
+    }
+}
+
 // NEAR: pairs of neighbours.  U heads are under way in a lane at a time.
 template <typename T, int V, int NG, bool NEAR, bool BWD, int U>
-__global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const RopePlan p) {
-    constexpr int E = V * NG;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(256, BWD ? 2 : 3) rope_kernel(const RopeArgs a, const RopePlan p) {
+    constexpr int E = V * NG, H = E / 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.rot / 2;
     const int hpw = 32 / p.lph, slot = lane / p.lph, in = lane % p.lph;
     const float inv_d = 1.0f / (float)a.d;
-    // the places of this lane's pieces in a head, and their frequencies
+    Freq* freqs = reinterpret_cast<Freq*>(smem);                            // [half]
+    float2* trig = reinterpret_cast<float2*>(freqs + half) + warp * half;  // cosine and sine of the warp's token
+    for (int i = threadIdx.x; i < half; i += 256) {
+        const float f = a.freqs[i];
+        Freq q;
+        q.turn = turns(f);
+        q.wild = isfinite(f) ? 0.0f : __int_as_float(0x7fc00000);
+        q.axis = a.axes == 1 ? 0 : (i >= a.section[0]) + (i >= a.section[1]) + (i >= a.section[2]);
+        freqs[i] = q;
+    }
+    __syncthreads();
+    // the places of this lane's pieces in a head, and of its pairs among the angles
     int at1[NG], at2[NG];
     bool has1[NG], has2[NG], turn[NG];
-    uint64_t freq[E];
-    unsigned wild = 0;  // frequencies that are not finite
-    int axis[E];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         const int i = in + p.lph * g;
         turn[g] = i < p.rot_groups;
         at1[g] = turn[g] ? (NEAR ? 2 * V * i : V * i) : a.rot + 2 * V * (i - p.rot_groups);
-        at2[g] = turn[g] && !NEAR ? a.rot / 2 + V * i : at1[g] + V;
+        at2[g] = turn[g] && !NEAR ? half + V * i : at1[g] + V;
         has1[g] = i < p.groups;
         has2[g] = has1[g] && at2[g] < a.d;
-#pragma unroll
-        for (int m = 0; m < V; ++m) {
-            const int e = g * V + m, pair = V * i + m;
-            freq[e] = 0;
-            axis[e] = 0;
-            if (turn[g]) {
-                const float f = a.freqs[pair];
-                if (!isfinite(f)) wild |= 1u << e;
-                freq[e] = turns(f);
-                axis[e] = a.axes == 1 ? 0 : (pair >= a.section[0]) + (pair >= a.section[1]) + (pair >= a.section[2]);
-            }
-        }
     }
-    float dw[BWD ? 2 : 1][2 * E];  // sums of dn xhat: queries, keys
+    Pairs<E> dw[BWD ? 2 : 1];  // sums of dn xhat: queries, keys
     if constexpr (BWD) {
 #pragma unroll
-        for (int e = 0; e < 2 * E; ++e) dw[0][e] = dw[1][e] = 0.0f;
+        for (int e = 0; e < H; ++e) dw[0].a[e] = dw[0].b[e] = dw[1].a[e] = dw[1].b[e] = pack(0.0f, 0.0f);
     }
 
     const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 5);
@@ -110,20 +159,28 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
         const int64_t tok = item / p.blocks;
         const int h0 = (int)(item - tok * p.blocks) * p.heads;
         const int h1 = h0 + p.heads < a.Hq + a.Hkv ? h0 + p.heads : (int)(a.Hq + a.Hkv);
-        float cs[E], sn[E];
-        int64_t pos[4];
-        if (a.positions != nullptr) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pos[x] = x < a.axes ? a.positions[tok * a.axes + x] : 0;
-        } else {
-            pos[0] = pos[1] = pos[2] = pos[3] = a.start + tok % a.L;
+        __syncwarp();
+        for (int i = lane; i < half; i += 32) {
+            const Freq q = freqs[i];
+            const int64_t at = a.positions != nullptr ? a.positions[tok * a.axes + q.axis] : a.start + tok % a.L;
+            const int64_t frac = (int64_t)((uint64_t)at * q.turn);
+            float2 t;
+            sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &t.y, &t.x);  // 2^-31
+            t.x += q.wild, t.y += q.wild;
+            trig[i] = t;
         }
+        __syncwarp();
+        f2 cs[H], sn[H];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int64_t at = axis[e] == 0 ? pos[0] : axis[e] == 1 ? pos[1] : axis[e] == 2 ? pos[2] : pos[3];
-            const int64_t frac = (int64_t)((uint64_t)at * freq[e]);
-            sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31
-            if ((wild >> e) & 1u) cs[e] = sn[e] = __int_as_float(0x7fc00000);
+        for (int e = 0; e < E; e += 2) {
+            float2 t[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int g = (e + k) / V, m = (e + k) % V;
+                t[k] = turn[g] ? trig[V * (in + p.lph * g) + m] : make_float2(1.0f, 0.0f);
+            }
+            cs[e / 2] = pack(t[0].x, t[1].x);
+            sn[e / 2] = BWD ? pack(-t[0].y, -t[1].y) : pack(t[0].y, t[1].y);
         }
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -141,14 +198,18 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                 out = (T*)(part == 0 ? a.q_out : a.k_out) + tok * (part == 0 ? a.ldqo : a.ldko) - first * a.d;
             }
             const float* w = part == 0 ? a.w_q : a.w_k;
-            float wv[2 * E];
+            Pairs<E> wp;
+            {
+                float wv[2 * E];
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int m = 0; m < V; ++m) {
-                    wv[2 * g * V + m] = w != nullptr && has1[g] ? w[at1[g] + m] : 1.0f;
-                    wv[(2 * g + 1) * V + m] = w != nullptr && has2[g] ? w[at2[g] + m] : 1.0f;
-                }
+                    for (int m = 0; m < V; ++m) {
+                        wv[2 * g * V + m] = w != nullptr && has1[g] ? w[at1[g] + m] : 1.0f;
+                        wv[(2 * g + 1) * V + m] = w != nullptr && has2[g] ? w[at2[g] + m] : 1.0f;
+                    }
+                wp = sorted<V, NG, NEAR>(wv);
+            }
             for (int hb = lo + slot; hb - slot < hi; hb += U * hpw) {
                 Pack<T, V> rx[U][2 * NG], ry[BWD ? U : 1][2 * NG];
 #pragma unroll
@@ -176,54 +237,74 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                     float v[2 * E], rs = 1.0f;
 #pragma unroll
                     for (int i = 0; i < 2 * NG; ++i) rx[u][i].get(v + i * V);
+                    const Pairs<E> xp = sorted<V, NG, NEAR>(v);
                     if (a.norm) {
-                        float ss = 0.0f;
+                        f2 s2 = mul2(xp.a[0], xp.a[0]);
+                        s2 = fma2(xp.b[0], xp.b[0], s2);
 #pragma unroll
-                        for (int e = 0; e < 2 * E; ++e) ss = fmaf(v[e], v[e], ss);
+                        for (int e = 1; e < H; ++e) s2 = fma2(xp.b[e], xp.b[e], fma2(xp.a[e], xp.a[e], s2));
+                        float ss = sum2(s2);
                         for (int o = p.lph / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
                         rs = rsqrtf(fmaf(ss, inv_d, a.eps));
                     }
-                    float y[2 * E];
-                    if constexpr (!BWD) {
+                    const f2 rs2 = pack(rs, rs);
+                    Pairs<E> n;  // what turns
+                    if constexpr (BWD) {
 #pragma unroll
-                        for (int e = 0; e < 2 * E; ++e) v[e] = v[e] * rs * wv[e];
+                        for (int i = 0; i < 2 * NG; ++i) ry[u][i].get(v + i * V);
+                        n = sorted<V, NG, NEAR>(v);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 2 * NG; ++i) ry[u][i].get(y + i * V);
+                        for (int e = 0; e < H; ++e) n.a[e] = mul2(xp.a[e], wp.a[e]), n.b[e] = mul2(xp.b[e], wp.b[e]);
                     }
-                    float* n = BWD ? y : v;  // what turns
+                    Pairs<E> y;  // turned, times rs
 #pragma unroll
-                    for (int g = 0; g < NG; ++g)
+                    for (int e = 0; e < H; ++e) {
+                        const f2 c = mul2(cs[e], rs2), s = mul2(sn[e], rs2);
+                        const f2 t1 = fma2(n.a[e], c, mul2(mul2(n.b[e], s), pack(-1.0f, -1.0f))), t2 = fma2(n.b[e], c, mul2(n.a[e], s));
+                        y.a[e] = t1;
+                        y.b[e] = t2;
+                    }
+                    if (p.rot_groups < p.groups) {  // beyond the rotation: not by cosine 1 and sine 0, 0 times infinity is NaN
 #pragma unroll
-                        for (int m = 0; m < V; ++m) {
-                            const int e = g * V + m, i1 = 2 * g * V + (NEAR ? 2 * m : m), i2 = i1 + (NEAR ? 1 : V);
-                            const float s = BWD ? -sn[e] : sn[e], n1 = n[i1], n2 = n[i2];
-                            const float t1 = fmaf(n1, cs[e], -n2 * s), t2 = fmaf(n2, cs[e], n1 * s);
-                            n[i1] = turn[g] ? t1 : n1;  // not by cos 1, sin 0: 0 times infinity is NaN
-                            n[i2] = turn[g] ? t2 : n2;
+                        for (int e = 0; e < E; e += 2) {
+                            float t[4], k[4];
+                            unpack(y.a[e / 2], t[0], t[1]);
+                            unpack(y.b[e / 2], t[2], t[3]);
+                            unpack(mul2(n.a[e / 2], rs2), k[0], k[1]);
+                            unpack(mul2(n.b[e / 2], rs2), k[2], k[3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) t[i] = turn[(e + (i & 1)) / V] ? t[i] : k[i];
+                            y.a[e / 2] = pack(t[0], t[1]);
+                            y.b[e / 2] = pack(t[2], t[3]);
                         }
+                    }
                     if constexpr (BWD) {
-                        if (a.norm) {
-                            float c = 0.0f;
+                        if (a.norm) {  // y is rs dn: dw += y x, u = y w, dx = u - x rs^2 mean(u x)
+                            f2 c2 = pack(0.0f, 0.0f);
 #pragma unroll
-                            for (int e = 0; e < 2 * E; ++e) {
-                                v[e] *= rs;  // xhat
-                                dw[part][e] = fmaf(y[e], v[e], dw[part][e]);
-                                y[e] *= wv[e];
-                                c = fmaf(y[e], v[e], c);
+                            for (int e = 0; e < H; ++e) {
+                                dw[part].a[e] = fma2(y.a[e], xp.a[e], dw[part].a[e]);
+                                dw[part].b[e] = fma2(y.b[e], xp.b[e], dw[part].b[e]);
+                                y.a[e] = mul2(y.a[e], wp.a[e]);
+                                y.b[e] = mul2(y.b[e], wp.b[e]);
+                                c2 = fma2(y.b[e], xp.b[e], fma2(y.a[e], xp.a[e], c2));
                             }
+                            float c = sum2(c2);
                             for (int o = p.lph / 2; o > 0; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
-                            c *= inv_d;
+                            c *= -inv_d * rs * rs;
+                            const f2 cc = pack(c, c);
 #pragma unroll
-                            for (int e = 0; e < 2 * E; ++e) y[e] = rs * fmaf(-v[e], c, y[e]);
+                            for (int e = 0; e < H; ++e) y.a[e] = fma2(xp.a[e], cc, y.a[e]), y.b[e] = fma2(xp.b[e], cc, y.b[e]);
                         }
                     }
                     if (h < hi) {
+                        unsorted<V, NG, NEAR>(y, v);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             const int64_t off = (int64_t)h * a.d;
-                            if (has1[g]) Vec<V>::st(out + off + at1[g], n + 2 * g * V);
-                            if (has2[g]) Vec<V>::st(out + off + at2[g], n + (2 * g + 1) * V);
+                            if (has1[g]) Vec<V>::st(out + off + at1[g], v + 2 * g * V);
+                            if (has2[g]) Vec<V>::st(out + off + at2[g], v + (2 * g + 1) * V);
                         }
                     }
                 }
@@ -233,20 +314,22 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
     if constexpr (BWD) {
         if (a.dw_q == nullptr && a.dw_k == nullptr) return;
         // the CTA's sums, warps and their heads in a fixed order
-        extern __shared__ float sums[];  // [8 warps][32 / lph][d] at most 8 * 512
+        float* sums = reinterpret_cast<float*>(smem);  // [8 warps][d]
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
+            float v[2 * E];
+            unsorted<V, NG, NEAR>(dw[part], v);
 #pragma unroll
             for (int e = 0; e < 2 * E; ++e)
-                for (int o = p.lph; o < 32; o <<= 1) dw[part][e] += __shfl_xor_sync(~0u, dw[part][e], o);
+                for (int o = p.lph; o < 32; o <<= 1) v[e] += __shfl_xor_sync(~0u, v[e], o);
             __syncthreads();
             if (slot == 0) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
 #pragma unroll
                     for (int m = 0; m < V; ++m) {
-                        if (has1[g]) sums[warp * a.d + at1[g] + m] = dw[part][2 * g * V + m];
-                        if (has2[g]) sums[warp * a.d + at2[g] + m] = dw[part][(2 * g + 1) * V + m];
+                        if (has1[g]) sums[warp * a.d + at1[g] + m] = v[2 * g * V + m];
+                        if (has2[g]) sums[warp * a.d + at2[g] + m] = v[(2 * g + 1) * V + m];
                     }
             }
             __syncthreads();
@@ -276,10 +359,11 @@ cudaError_t go(const RopeArgs& a, cudaStream_t s) {
     constexpr int U = BWD ? 1 : 2;
     // eight warps a CTA; blocks of heads where the tokens alone do not make 16 warps a SM
     const RopePlan p = plan_of<V, NG>(a, 152 * 16);
-    const int64_t ctas = (p.items + 7) / 8, most = BWD ? rope_bwd_ctas(a) : 152 * 8;
-    const size_t sm = BWD ? sizeof(float) * 8 * (size_t)a.d : 0;
+    const int64_t ctas = (p.items + 7) / 8, most = BWD ? rope_bwd_ctas(a) : 152 * 3;
+    const size_t half = (size_t)a.rot / 2, table = half * (sizeof(Freq) + 8 * sizeof(float2));
+    const size_t sums = BWD ? sizeof(float) * 8 * (size_t)a.d : 0;
     const int64_t grid = BWD ? most : ctas < most ? ctas : most;
-    rope_kernel<T, V, NG, NEAR, BWD, U><<<(unsigned)grid, 256, sm, s>>>(a, p);
+    rope_kernel<T, V, NG, NEAR, BWD, U><<<(unsigned)grid, 256, table > sums ? table : sums, s>>>(a, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || (a.dw_q == nullptr && a.dw_k == nullptr)) return e;
     rope_sum_kernel<<<dim3((unsigned)((a.d + 31) / 32), 2), 1024, 0, s>>>(a, grid);
