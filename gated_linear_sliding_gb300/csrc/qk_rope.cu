@@ -119,7 +119,7 @@ __device__ __forceinline__ void unsorted(const Pairs<V * NG>& r, float* v) {
 
 // NEAR: pairs of neighbours.  U heads are under way in a lane at a time.
 template <typename T, int V, int NG, bool NEAR, bool BWD, int U>
-__global__ void __launch_bounds__(256, BWD ? 2 : 3) rope_kernel(const RopeArgs a, const RopePlan p) {
+__global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const RopePlan p) {
     constexpr int E = V * NG, H = E / 2;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.rot / 2;
@@ -356,10 +356,10 @@ constexpr int64_t kBwdCtas = 304;  // two of 256 threads a SM
 
 template <typename T, int V, int NG, bool NEAR, bool BWD>
 cudaError_t go(const RopeArgs& a, cudaStream_t s) {
-    constexpr int U = BWD ? 1 : 2;
+    constexpr int U = BWD ? 1 : 4;  // heads under way: registers for loads beat more warps (39 against 42 us with three CTAs of two)
     // eight warps a CTA; blocks of heads where the tokens alone do not make 16 warps a SM
     const RopePlan p = plan_of<V, NG>(a, 152 * 16);
-    const int64_t ctas = (p.items + 7) / 8, most = BWD ? rope_bwd_ctas(a) : 152 * 3;
+    const int64_t ctas = (p.items + 7) / 8, most = BWD ? rope_bwd_ctas(a) : 152 * 2;
     const size_t half = (size_t)a.rot / 2, table = half * (sizeof(Freq) + 8 * sizeof(float2));
     const size_t sums = BWD ? sizeof(float) * 8 * (size_t)a.d : 0;
     const int64_t grid = BWD ? most : ctas < most ? ctas : most;
