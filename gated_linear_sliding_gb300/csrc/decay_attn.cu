@@ -447,7 +447,8 @@ DecayPass dq_pass(const DecayArgs& a) {
 
 DecayPass dv_pass(const DecayArgs& a) {
     DecayPass p = base_pass(a);
-    p.x = a.k, p.y = a.q, p.z = a.d_o, p.out = a.dv_;
+    p.x = a.k, p.y = a.q, p.z = a.d_o, p.v = a.v, p.out = a.dv_;
+    p.ldv = a.ldv;
     p.ldx = a.ldk, p.ldy = a.ldq, p.ldz = a.ldo, p.ldout = a.lddv;
     p.dx = (int)a.dk, p.dz = (int)a.dv;
     p.gx = 1, p.gy = (int)(a.Hq / a.Hkv);
@@ -613,6 +614,7 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t s) {
     // dk reads ds_out: before dv, which may overwrite it with ds0
     if ((e = own_first_states(a, &v, recs + records(v), s)) != cudaSuccess) return e;
     if ((e = segment_states(a, v, recs, s)) != cudaSuccess) return e;
+    if (decay_uses_tc(a)) return decay_tc_grads(v, a.dk_, a.lddk, s);
     if ((e = outputs(a, k, s)) != cudaSuccess) return e;
     return outputs(a, v, s);
 }

@@ -20,39 +20,23 @@
 // Warps: 0-7 the pairs' weights and the outputs (a thread holds one row's 32 of 64 pairs and 64 of 128 output
 // columns); 8-15 the state (half a row of S to a thread; Y~); 16 the copies; 17 the MMAs of the scores, 18 of
 // the state, 19 of the outputs.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "decay.cuh"
-#include "sm100.cuh"
-#include "tc_util.cuh"
+#include "decay_tc.cuh"
 
 namespace lz {
 namespace {
-
-using namespace sm100;
-using tc::kdesc;
-using tc::mndesc;
-
-constexpr int kMathWarps = 8;
-constexpr int kStateWarps = 8;
-constexpr int kThreads = 32 * 20;
-constexpr uint32_t kBox = 8192;  // a box of 64 rows x 64 columns of bf16
 
 struct TcArgs {
     CUtensorMap x, y, z, out;
     DecayPass p;
 };
 
-// Shared memory: XST stages of x, YST of y and z, Y~, the state's operand copy, and rows of the output on
-// their way out (OWN), which otherwise go through the stage that x came in.
-template <int XST_, int YST_, bool OWN_, bool REV_>
+// Shared memory: XST stages of x, rows of the output on their way out, YST of y and z, Y~, the state's operand copy.
+template <int XST_, int YST_>
 struct Layout {
     static constexpr int XST = XST_, YST = YST_;
-    static constexpr bool OWN = OWN_, REV = REV_;
     static constexpr uint32_t X = 0;
     static constexpr uint32_t OUT = XST * 4 * kBox;
-    static constexpr uint32_t YZ = OUT + (OWN ? 4 * kBox : 0);
+    static constexpr uint32_t YZ = OUT + 4 * kBox;
     static constexpr uint32_t KT = YZ + YST * 4 * kBox;  // high part, low part
     static constexpr uint32_t ST = KT + 4 * kBox;
     static constexpr uint32_t TABLE = ST + 4 * kBox;     // powers 0 .. 128, and the columns' factors
@@ -60,130 +44,15 @@ struct Layout {
     static constexpr uint32_t BYTES = BARS + 304 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
-// several tiles of x for each of y and z; one of each; several of y and z for each of x (a sum over heads).
-// One stage of x is enough where its last reader is done long before the chunk is, and leaves room for a third
-// of y and z, whose copies otherwise wait for the chunk before.
-using Wide = Layout<2, 2, true, false>;
-template <bool REV>
-using Even = Layout<1, 3, true, REV>;
-using Deep = Layout<2, 3, false, true>;
-
-// Waits with a limit.  When one runs out it is reported once and every role leaves.  What happens while a
-// wait lasts is one function for all of them: in line, the waits would fill the instruction cache.
-__device__ __noinline__ bool spin(uint64_t* bar, uint32_t parity, unsigned where, volatile int* abort, WsHeader* header) {
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort) return false;
-        if (clock64() - t0 > tc::kTimeout) {
-            if (atomicExch((int*)abort, 1) == 0) report(header, LIZARD_ERR_TIMEOUT, where);
-            return false;
-        }
-    }
-    return true;
-}
-struct Waiter {
-    volatile int* abort;
-    WsHeader* header;
-    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, unsigned where) const {
-        return mbar_try_wait(bar, parity) || spin(bar, parity, where, abort, header);
-    }
-    // by all lanes of a warp: one answer
-    __device__ __forceinline__ bool all(uint64_t* bar, uint32_t parity, unsigned where) const {
-        return __all_sync(~0u, (*this)(bar, parity, where));
-    }
-};
-
-struct Seg {
-    int64_t unit, b, h, lo, hi;
-    int seg;
-};
-template <bool ENDS>
-__device__ __forceinline__ Seg seg_of(const DecayPass& p) {
-    Seg s;
-    s.unit = blockIdx.x % p.units;
-    s.seg = (int)(blockIdx.x / p.units);
-    if (ENDS) s.seg = ending_segment(p, p.parts > 0 ? 0 : s.seg);
-    s.b = s.unit / p.Hkv;
-    s.h = s.unit - s.b * p.Hkv;
-    s.lo = (int64_t)s.seg * p.seg_len;
-    s.hi = min64(s.lo + p.seg_len, p.seqs.L);
-    return s;
-}
-
-// The tile of Y~ from y's, as high and low parts, by 64 PARTS threads (token, part of the columns); and rows
-// of z behind the tile's last token become zeros: 0 times what lies there may be NaN.
-template <int PARTS, int UNROLL>
-__device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t zs, uint32_t kt, int n, float f, int tid) {
-    const int tok = tid & 63, part = tid >> 6;
-    const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
-#pragma unroll UNROLL
-    for (int c = 16 / PARTS * part; c < 16 / PARTS * (part + 1); ++c) {
-        const uint32_t off = (c >> 3) * kBox + sw128(tok, c & 7);
-        uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
-        if (tok < n) ld_shared_v4(ys + off, w[0], w[1], w[2], w[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float a, b;
-            const f2 v = mul2(pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), ff);
-            unpack(v, a, b);
-            hi[i] = pack_bf16(a, b);
-            unpack(fma2(pack(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xffff0000u)), minus, v), a, b);
-            lo[i] = pack_bf16(a, b);
-        }
-        st_shared_v4(kt + off, hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(kt + 2 * kBox + off, lo[0], lo[1], lo[2], lo[3]);
-        if (tok >= n) st_shared_v4(zs + off, 0, 0, 0, 0);
-    }
-}
-
-// A value that all lanes of a warp hold, as one the compiler knows to be such: operands of an MMA that are
-// known to be uniform cost a fraction of the issue time.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(~0u, v, 0); }
-
-// An MMA by the lane for which `leader` holds, in code that the whole warp runs.
-__device__ __forceinline__ void mma_bf16_one(bool leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)leader)
-        : "memory");
-}
-__device__ __forceinline__ void mma_bf16_ts_one(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)leader)
-        : "memory");
-}
-
-// S += Y~^T Z over a tile's 64 tokens, both parts; by a warp.
-template <int UNROLL>
-__device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, uint32_t zs, uint32_t idesc, bool fresh) {
-#pragma unroll UNROLL
-    for (int j = 0; j < 8; ++j)
-        mma_bf16_one(leader, d, mndesc(kt + (j >> 2) * 2 * kBox + (j & 3) * 2048, kBox), mndesc(zs + (j & 3) * 2048, kBox), idesc, fresh && j == 0 ? 0u : 1u);
-}
-
-// Eight values of a row times f as bf16.
-__device__ __forceinline__ void st_scaled8(uint32_t to, const float* v, f2 f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        unpack(mul2(pack(v[2 * i], v[2 * i + 1]), f), a, b);
-        w[i] = pack_bf16(a, b);
-    }
-    st_shared_v4(to, w[0], w[1], w[2], w[3]);
-}
+// Several tiles of x for each of y and z, or one.  Then one stage of x is enough (its last reader is done long before
+// the chunk is) and leaves room for a third of y and z, whose copies otherwise wait for the chunk before (16 heads of
+// 64 and 128, 16384 tokens: 391 -> 371 us forwards and backwards).
+using Wide = Layout<2, 2>;
+using Even = Layout<1, 3>;
 
 template <typename SM>
 __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs g) {
     constexpr int XST = SM::XST, YST = SM::YST;
-    constexpr bool rev = SM::REV, own = SM::OWN;
     extern __shared__ uint8_t smem_raw[];
     const DecayPass& p = g.p;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -206,12 +75,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     const bool slow = l2 * (float)chunk >= -64.0f;  // factors of rows and columns (see above)
     for (int i = tid; i < 129; i += kThreads) {
         pw[i] = power(l2, i);
-        if (i < 128) col[i] = p.in_scale * power(l2, rev ? i - mid : mid - i);
+        if (i < 128) col[i] = p.in_scale * power(l2, mid - i);
     }
     if (tid == 0) {
         for (int i = 0; i < XST; ++i) {
             mbar_init(&x_full[i], 1);
-            mbar_init(&x_free[i], own ? 2 : kMathWarps);  // scores and X S, or the outputs' last warps
+            mbar_init(&x_free[i], 2);  // scores and X S
         }
         for (int i = 0; i < YST; ++i) {
             mbar_init(&yz_full[i], 1);
@@ -247,9 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     const int kx = (p.dx + 15) / 16;                 // K steps over dx
     const int nz = (p.dz + 15) / 16 * 16;            // N over dz
     const int ntx = (p.gx + 1) / 2;                  // tiles of x heads
-    constexpr uint32_t kHalf = 2 * kBox;             // from the first 64 columns of x, or of S, to the next
 
-    Walk walk(p.seqs, w.b, w.lo, w.hi, rev, chunk);
+    Walk walk(p.seqs, w.b, w.lo, w.hi, false, chunk);
     Tile t;
 
     if (warp == 16) {
@@ -261,11 +129,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             bool ok = true;
             while (ok && walk.next(p.seqs, w.b, &t)) {
                 const int row = (int)(w.b * p.seqs.L + t.t0);
-                const int nsub = t.n > 64 ? 2 : 1, ny = p.gy * nsub;
+                const int ny = t.n > 64 ? 2 : 1;
                 for (int a = 0; a < ntx && ok; ++a) {
                     for (int q = 0; q < ny && ok; ++q) {
                         if (a == 0) {
-                            const int s = yi % YST, head = (int)(w.h * p.gy) + q / nsub, at = row + 64 * (q % nsub);
+                            const int s = yi % YST, head = (int)w.h, at = row + 64 * q;
                             if (yi >= YST && !wait(&yz_free[s], ((yi / YST) & 1) ^ 1, 100)) {
                                 ok = false;
                                 break;
@@ -277,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                             ++yi;
                         }
                         if (q == 0) {
-                            const int s = xt % XST, parts = tall ? nsub : p.gx - 2 * a < 2 ? 1 : 2;
+                            const int s = xt % XST, parts = tall ? ny : p.gx - 2 * a < 2 ? 1 : 2;
                             if (xt >= XST && !wait(&x_free[s], ((xt / XST) & 1) ^ 1, 101)) {
                                 ok = false;
                                 break;
@@ -305,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         uint32_t it = 0, xt = 0, yi = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
-            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            const int ny = t.n > 64 ? 2 : 1;
             for (int a = 0; a < ntx && ok; ++a) {
                 for (int q = 0; q < ny && ok; ++q, ++it) {
                     const int s = it & 1, xs = xt % XST;
@@ -321,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                         mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
                     if (leader) {
                         mma_commit(&s_full[s]);
-                        if (own && q == ny - 1) mma_commit(&x_free[xs]);
+                        if (q == ny - 1) mma_commit(&x_free[xs]);
                     }
                     if (q == ny - 1) ++xt;
                 }
@@ -338,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         uint32_t it = 0, xt = 0, yi = 0, ci = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
-            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            const int ny = t.n > 64 ? 2 : 1;
             for (int a = 0; a < ntx && ok; ++a) {
                 for (int q = 0; q < ny && ok; ++q, ++it) {
                     const int s = it & 1, xs = xt % XST;
@@ -356,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                             mma_bf16_one(leader, to, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), mndesc(base + SM::ST + k * 2048, kHalf), id_o, k > 0);
                         if (leader) {
                             if (!slow) mma_commit(&xs_full[xt & 1]);
-                            if (own) mma_commit(&x_free[xs]);
+                            mma_commit(&x_free[xs]);
                             if (a == ntx - 1) mma_commit(xs_done);
                         }
                     }
@@ -386,11 +254,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         uint32_t yi = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
-            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            const int ny = t.n > 64 ? 2 : 1;
             for (int q = 0; q < ny; ++q, ++yi) {
                 if (!wait.all(kt_full, yi & 1, 109)) { ok = false; break; }
                 tc_fence_after();
-                state_mmas<1>(leader, tH, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), id_h, false);
+                state_mmas<1>(leader, tH, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), kBox, id_h, false);
                 if (leader) {
                     mma_commit(h_done);
                     mma_commit(&yz_free[yi % YST]);
@@ -399,96 +267,32 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         }
         if (!ok && yi > 0) mbar_wait(h_done, (yi - 1) & 1, tc::kTimeout);
     } else if (warp >= 8) {
-        // the state: row `row` of S, one half of its columns
-        const int in = tid - 32 * kMathWarps, row = in & 127, z0 = (in >> 7) * 64, z1 = min(z0 + 64, p.dz);
-        const uint32_t at = tH + ((uint32_t)(32 * (warp & 3)) << 16);
-        const int64_t size = (int64_t)p.dx * p.dz;
+        // the state: half a row of S to a thread
+        const StateRow sr = state_row(p, tH, tid - 32 * kMathWarps);
         uint32_t yi = 0, ci = 0;
         bool ok = true, was_last = false;
         int was_seq = 0;
         grid_dep_wait();
-        // the state behind a sequence's last tile (a pass whose states are transposed leaves none)
-        auto leave = [&](int seq) {
-            if (p.fin == nullptr) return;
-            float* to = p.fin + (seq * p.Hkv + w.h) * size + (int64_t)row * p.dz;
-#pragma unroll 1
-            for (int c = z0; c < z1; c += 16) {
-                float v[16];
-                tmem_ld16(at + c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    if (row < p.dx && c + i < z1) *reinterpret_cast<float4*>(to + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            }
-        };
-        // a state from memory, or added to what is there
-        auto fetch = [&](const float* from, bool add) {
-#pragma unroll 1
-            for (int c = z0; c < z0 + 64; c += 32) {
-                float v[32];
-                if (p.transposed) {
-                    const float* f = from + (int64_t)c * p.dx + row;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = from != nullptr && row < p.dx && c + (i & ~7) < z1 ? f[i * p.dx] : 0.0f;
-                } else {
-                    const float* f = from + (int64_t)row * p.dz + c;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (from != nullptr && row < p.dx && c + i < z1) u = *reinterpret_cast<const float4*>(f + i);
-                        v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
-                    }
-                }
-                if (add) {
-                    float old[32];
-                    tmem_ld32(at + c, old);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += old[i];
-                }
-                tmem_st32(at + c, v);
-            }
-            tmem_wait_st();
-        };
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (ci > 0) {
                 if (!wait.all(h_done, (yi - 1) & 1, 110) || !wait.all(xs_done, (ci - 1) & 1, 111)) { ok = false; break; }
                 tc_fence_after();
-                if (was_last) leave(was_seq);
+                if (was_last) leave_state(p, sr, w.h, was_seq);
             }
-            if (t.first || ci == 0) {
-                const float* from = !t.first            ? first_state(p, w.unit, w.seg)
-                                    : p.init == nullptr ? nullptr
-                                                        : p.init + (t.seq * p.Hkv + w.h) * size;
-                const int parts = t.first || p.parts < 2 ? 1 : 2;
-#pragma unroll 1
-                for (int k = 0; k < parts; ++k) fetch(k == 0 ? from : from + size, k > 0);
-            }
-            const float keep = pw[t.n], seen = !slow ? 1.0f : rev ? power(l2, t.n - 1 - mid) : pw[mid + 1];
-            const f2 keep2 = pack(keep, keep), seen2 = pack(seen, seen);
-#pragma unroll 1
-            for (int c = z0; c < z0 + 64 && c < nz; c += 16) {
-                float v[16];
-                tmem_ld16(at + c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) st_scaled8(base + SM::ST + (c >> 6) * kHalf + sw128(row, ((c & 63) >> 3) + i), v + 8 * i, seen2);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) unpack(mul2(pack(v[2 * i], v[2 * i + 1]), keep2), v[2 * i], v[2 * i + 1]);
-                tmem_st16(at + c, reinterpret_cast<const uint32_t*>(v));
-            }
-            tmem_wait_st();
+            if (t.first || ci == 0) begin_state(p, sr, w, t);
+            pass_state(sr, base + SM::ST, nz, slow ? pw[mid + 1] : 1.0f, pw[t.n]);
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(st_full);
-            const int nsub = t.n > 64 ? 2 : 1, ny = p.gy * nsub;
+            const int ny = t.n > 64 ? 2 : 1;
             for (int q = 0; q < ny; ++q, ++yi) {
-                const int ys = yi % YST, j0 = 64 * (q % nsub);
+                const int ys = yi % YST, j0 = 64 * q, m = min(64, t.n - j0);
                 if (!wait.all(&yz_full[ys], (yi / YST) & 1, 112)) { ok = false; break; }
                 if (q > 0 && !wait.all(h_done, (yi - 1) & 1, 113)) { ok = false; break; }
-                const int m = min(64, t.n - j0), tok = in & 63, far = rev ? j0 + tok + 1 : t.n - 1 - j0 - tok;
+                const int tok = sr.in & 63;
                 const uint32_t ya = base + SM::YZ + ys * 4 * kBox;
-                scale_rows<4, 1>(ya, ya + 2 * kBox, base + SM::KT, m, tok < m ? pw[far] * p.in_scale : 0.0f, in);
+                if (m < 64) clear_rows<32 * kStateWarps>(ya + 2 * kBox, kBox, m, sr.in);
+                scale_rows<4, 1>(ya, kBox, base + SM::KT, 2 * kx, m, tok < m ? pw[t.n - 1 - j0 - tok] : 0.0f, sr.in);
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&zz_full[ys]);
@@ -501,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         if (ok && ci > 0 && was_last && p.fin != nullptr) {
             if (wait.all(h_done, (yi - 1) & 1, 114)) {
                 tc_fence_after();
-                leave(was_seq);
+                leave_state(p, sr, w.h, was_seq);
             }
         }
     } else {
@@ -512,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         const int slot = tall ? 0 : quad >> 1;                  // head of the two
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         const bool z_on = 64 * half < p.dz;
-        const float rowf = p.out_scale * (slow ? power(l2, rev ? mid - i : i - mid) : 1.0f);
+        const float rowf = p.out_scale * (slow ? power(l2, i - mid) : 1.0f);
         const f2 rowf2 = pack(rowf, rowf);
         const uint32_t c0 = base + SM::TABLE + 132 * 4;
         bool have = walk.next(p.seqs, w.b, &t);
@@ -523,19 +327,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         int held_n = 0, held_head = 0, held_t0 = 0;
         // an item's weights, then the outputs of the tile of x before, whose products end meanwhile
         while (true) {
-            const int ny = p.gy * (t.n > 64 ? 2 : 1);
+            const int ny = t.n > 64 ? 2 : 1;
             const bool live = tall ? 32 * tq < t.n : 2 * a + slot < p.gx;
             if (have) {
-                const int s = it & 1, cb = 2 * (t.n > 64 ? q & 1 : 0) + half;  // block of the columns
+                const int s = it & 1, cb = 2 * q + half;  // block of the columns
                 if (!wait.all(&s_full[s], (it >> 1) & 1, 116)) break;
                 tc_fence_after();
                 if (live) {
                     const uint32_t at = tS + s * 64 + lanes + half * 32;
-                    const bool none = rev ? tq > cb : tq < cb, some = tq == cb || (rev && 32 * cb + 32 > t.n);
-#pragma unroll 1
+                    #pragma unroll 1
                     for (int c = 0; c < 32; c += 16) {
                         uint32_t o[8];
-                        if (none) {
+                        if (tq < cb) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) o[k] = 0;
                         } else {
@@ -555,15 +358,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) {
-                                    const int d = rev ? 32 * cb + c + k - i : i - 32 * cb - c - k;
+                                    const int d = i - 32 * cb - c - k;
                                     v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
                                 }
                             }
-                            if (some) {
-                                // places on the wrong side, and of tokens behind the last one, are left out whatever they hold
-                                const int lo = (rev && tq == cb ? lane : 0) - c, hi = (rev ? t.n - 32 * cb - 1 : lane) - c;
+                            if (tq == cb) {  // tokens behind this one are left out whatever they hold
+                                const int last = lane - c;
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) v[k] = (!rev || k >= lo) && k <= hi ? v[k] : 0.0f;
+                                for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
                             }
 #pragma unroll
                             for (int k = 0; k < 8; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
@@ -575,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) break;
                     tc_fence_after();
                     if (live && z_on) {
-                        const float f = i < t.n ? pw[rev ? t.n - 1 - i : i + 1] : 0.0f;
+                        const float f = i < t.n ? pw[i + 1] : 0.0f;
 #pragma unroll 1
                         for (int c = 0; c < 64; c += 16) {
                             float v[16];
@@ -595,11 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 const uint32_t hx = xt - 1, hi = it - 1;
                 if (!wait.all(&pv_done[hi & 1], (hi >> 1) & 1, 115)) break;
                 tc_fence_after();
-                const uint32_t off = own ? SM::OUT : SM::X + (hx % XST) * 4 * kBox;
-                const uint32_t stage = base + off + half * kHalf + quad * 4096;
+                const uint32_t stage = base + SM::OUT + half * kHalf + quad * 4096;
                 const bool out_live = held_live && z_on;  // one answer for a warp
                 if (out_live) {
-                    if (own && lane == 0) bulk_wait_read();  // the rows before have left
+                    if (lane == 0) bulk_wait_read();  // the rows before have left
                     __syncwarp();
 #pragma unroll 1
                     for (int c = 0; c < 64; c += 16) {
@@ -617,9 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (out_live) {
                     if (32 * tq + 32 <= held_n) {
                         if (lane == 0) {
-                            tma_store_3d(&g.out, sm + off + half * kHalf + quad * 4096, 64 * half, held_head, (int)(w.b * p.seqs.L) + held_t0 + 32 * tq);
+                            tma_store_3d(&g.out, sm + SM::OUT + half * kHalf + quad * 4096, 64 * half, held_head, (int)(w.b * p.seqs.L) + held_t0 + 32 * tq);
                             bulk_commit();
-                            if (!own) bulk_wait_read();
                         }
                     } else if (32 * tq < held_n) {
                         const int c = lane & 7;
@@ -633,11 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                                 if (tok < held_n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
                             }
                         }
-                        fence_async_smem();
                     }
                 }
-                __syncwarp();
-                if (!own && lane == 0) mbar_arrive(&x_free[hx % XST]);
                 held = false;
             }
             if (!have) break;
@@ -758,7 +555,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             const int k = it & 1;
             if (!wait.all(&kt_full[k], (it >> 1) & 1, 121)) break;
             tc_fence_after();
-            state_mmas<8>(leader, tb, uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), id_h,
+            state_mmas<8>(leader, tb, uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
                        it == 0);
             if (leader) {
                 mma_commit(&kt_free[k]);
@@ -780,7 +577,8 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 if (it >= 2 && !wait.all(&kt_free[group], ((it >> 1) & 1) ^ 1, 123)) { ok = false; break; }
                 const float f = tok < n ? power(l2, rev ? t0 + tok - begin + 1 : end - 1 - t0 - tok) * p.in_scale : 0.0f;
                 const uint32_t ya = base + EndsSmem::YZ + s * 4 * kBox;
-                scale_rows<4, 4>(ya, ya + 2 * kBox, base + EndsSmem::KT + group * 4 * kBox, n, f, in);
+                if (n < 64) clear_rows<256>(ya + 2 * kBox, kBox, n, in);
+                scale_rows<4, 4>(ya, kBox, base + EndsSmem::KT + group * 4 * kBox, 2 * ((p.dx + 15) / 16), n, f, in);
                 fence_async_smem();
                 mbar_arrive(&kt_full[group]);
             }
@@ -820,14 +618,6 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
         tc_fence_after();
         tmem_dealloc(tb, 128);
     }
-}
-
-// [rows, heads, width] of a tensor with token distance ld, boxes of `box_rows` x 64 columns of one head.
-bool map_of(CUtensorMap* m, const void* ptr, int64_t rows, int64_t heads, int64_t width, int64_t ld, int box_rows = 64) {
-    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
-    return tc::make_map(m, ptr, 3, dims, strides, box);
 }
 
 bool args_of(const DecayPass& p, TcArgs* a) {
@@ -879,9 +669,7 @@ cudaError_t decay_tc_ends(const DecayPass& p, float* recs, cudaStream_t s) {
 cudaError_t decay_tc_pass(const DecayPass& p, cudaStream_t s) {
     TcArgs a;
     if (!args_of(p, &a)) return cudaErrorInvalidValue;
-    if (p.gx > 1) return go<Wide>(a, s);
-    if (p.gy > 1) return go<Deep>(a, s);
-    return p.rev ? go<Even<true>>(a, s) : go<Even<false>>(a, s);
+    return p.gx > 1 ? go<Wide>(a, s) : go<Even>(a, s);
 }
 
 }  // namespace lz

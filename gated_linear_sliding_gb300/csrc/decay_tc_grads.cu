@@ -1,0 +1,456 @@
+// Gradients of keys and values of the linear attention with a decay for each head, on the tensor cores (tcgen05,
+// TMEM and TMA, sm_103a).
+//
+//   dS[t] = e^l dS[t+1] + scale sum over query heads of q[t] do[t]^T,   dk[t] = dS[t] v[t],   dv[t] = dS[t]^T k[t]
+// A CTA walks a segment of one state head backwards in chunks of 64 tokens.  With E the state behind a chunk as its
+// last token sees it, and for two query heads at a time the 128 rows (head, i) of Q and dO,
+//   P  = scale (Q K^T) (.) e^(l (i - j)),   P' = scale (dO V^T) (.) e^(l (i - j)),   masked to i >= j      [128 x 64]
+//   dv^T = E^T K^T (.) e^(l (n-1-j)) + dO^T P,    dk^T = E V^T (.) e^(l (n-1-j)) + Q^T P'                 [128 x 64]
+//   E' = e^l (what is before the chunk sees) = e^(l n) E + Q~^T dO,   Q~[i] = scale e^(l (i+1)) Q[i]
+// Both gradients share the copies of Q, dO, K, V, the state and its updates, and both are made transposed, so that the
+// MMAs' 128 rows are two heads' tokens or a head's values.  As two passes of the outputs' form (one with dS, one with
+// its transpose) they took 204 us for a training step of 8 x 2048 tokens, 32 heads on 8, 128 values.
+//
+// The decay of a pair is e^(l (i-r)) e^(l (r-j)), r in the middle of the chunk: a factor of the rows of P and one of the
+// finished columns; heads that decay by more than a half a token take each pair's power (see the outputs' kernel, also
+// for the roundings).
+//
+// Warps: 0-7 pairs and gradients; 8-15 the state (half a row to a thread) and Q~; 16 the copies; 17 the MMAs of the
+// scores, 18 those into the state, 19 those of the gradients.  TMEM: two scores of 64 columns, twice two gradients of
+// 64, the state 128.
+#include "decay_tc.cuh"
+
+namespace lz {
+namespace {
+
+struct GradArgs {
+    CUtensorMap q, d_o, k, v, dk, dv;
+    DecayPass p;  // the pass of dv: x = k, y = q, z = d_o
+    void *dk_out, *dv_out;
+    int64_t lddk, lddv;
+};
+
+constexpr int kRing = 3;  // tiles of 128 rows of Q and dO in turn: both of one item and the next one's Q
+struct GradSmem {
+    static constexpr uint32_t RING = 0;
+    static constexpr uint32_t KV = kRing * 4 * kBox;  // K, V: 64 rows each
+    static constexpr uint32_t PP = KV + 4 * kBox;     // P, P' [128 x 64]; then dv and dk [64 x 128] on their way out
+    static constexpr uint32_t KT = PP + 4 * kBox;     // Q~: high part, low part
+    static constexpr uint32_t ST = KT + 4 * kBox;
+    static constexpr uint32_t TABLE = ST + 4 * kBox;  // powers 0 .. 64, and the columns' factors
+    static constexpr uint32_t BARS = TABLE + (68 + 64) * 4;
+    static constexpr uint32_t BYTES = BARS + 304 + 1024;
+    static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
+};
+
+__global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __grid_constant__ GradArgs g) {
+    using SM = GradSmem;
+    extern __shared__ uint8_t smem_raw[];
+    const DecayPass& p = g.p;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
+    float* pw = reinterpret_cast<float*>(sm + SM::TABLE);  // powers of the decay
+    float* col = pw + 68;                                  // factors of the finished columns
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BARS);
+    uint64_t *b_full = bar, *b_free = bar + 3, *kv_full = bar + 6, *kv_free = bar + 7, *s_full = bar + 8, *p_full = bar + 9, *pv_done = bar + 10,
+             *xs_full = bar + 11, *o_free = bar + 13, *zz_full = bar + 15, *kt_full = bar + 17, *h_done = bar + 18, *st_full = bar + 19,
+             *xs_done = bar + 20, *staged = bar + 21, *left = bar + 22, *drained = bar + 23;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 26);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool leader = lane == 0;
+    const Seg w = seg_of<false>(p);
+    check_offsets(p.seqs, p.header);
+    constexpr int mid = 31;
+    const float l2 = log2_decay(p.log_decay, w.h);
+    const bool slow = l2 >= -1.0f;
+    for (int i = tid; i <= 64; i += kThreads) {
+        pw[i] = power(l2, i);
+        if (i < 64) col[i] = slow ? power(l2, mid - i) : 1.0f;
+    }
+    const int nhx = (p.dx + 63) / 64, nhz = (p.dz + 63) / 64;
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_free[i], 2);  // the gradients' and the state's MMAs
+        }
+        mbar_init(kv_full, 1);
+        mbar_init(kv_free, 2);  // the scores and the state's parts
+        mbar_init(s_full, 1);
+        mbar_init(p_full, 32 * kMathWarps);
+        mbar_init(pv_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&xs_full[i], 1);
+            mbar_init(&o_free[i], 32 * kMathWarps);
+            mbar_init(&zz_full[i], 32 * kStateWarps);
+        }
+        mbar_init(kt_full, 32 * kStateWarps);
+        mbar_init(h_done, 1);
+        mbar_init(st_full, 32 * kStateWarps);
+        mbar_init(xs_done, 1);
+        mbar_init(staged, 32 * kMathWarps);
+        mbar_init(left, kMathWarps);
+        for (int i = 0; i < 3; ++i) mbar_init(&drained[i], 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 17) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *tmem_slot;
+    const uint32_t tS = tb, tO = tb + 128, tH = tb + 384;
+    const Waiter wait{abort, p.header};
+    const int kx = (p.dx + 15) / 16, kz = (p.dz + 15) / 16, nz = 16 * kz;
+    const int nt = (p.gy + 1) / 2;  // items of a chunk: two query heads, or one
+
+    Walk walk(p.seqs, w.b, w.lo, w.hi, true, 64);
+    Tile t;
+
+    if (warp == 16) {
+        if (lane == 0) {
+            prefetch_tmap(&g.q);
+            prefetch_tmap(&g.d_o);
+            prefetch_tmap(&g.k);
+            prefetch_tmap(&g.v);
+            uint32_t bi = 0, ci = 0;
+            bool ok = true;
+            while (ok && walk.next(p.seqs, w.b, &t)) {
+                const int row = (int)(w.b * p.seqs.L) + t.t0;
+                for (int a = 0; a < nt && ok; ++a) {
+                    const int heads = p.gy - 2 * a < 2 ? 1 : 2, head = (int)(w.h * p.gy) + 2 * a;
+                    for (int e = 0; e < 2; ++e, ++bi) {  // Q, then dO
+                        const int s = bi % kRing, nh = e == 0 ? nhx : nhz;
+                        if (bi >= kRing && !wait(&b_free[s], ((bi / kRing) & 1) ^ 1, 130)) { ok = false; break; }
+                        uint8_t* to = sm + SM::RING + s * 4 * kBox;
+                        mbar_arrive_expect_tx(&b_full[s], heads * nh * kBox);
+                        for (int k = 0; k < heads; ++k)
+                            for (int h = 0; h < nh; ++h) tma_load_3d(to + h * kHalf + k * kBox, e == 0 ? &g.q : &g.d_o, &b_full[s], 64 * h, head + k, row);
+                        if (a == 0 && e == 0) {  // K and V of the chunk, behind the first Q, which need not wait for their place
+                            if (ci >= 1 && !wait(kv_free, (ci & 1) ^ 1, 131)) { ok = false; ++bi; break; }
+                            mbar_arrive_expect_tx(kv_full, (nhx + nhz) * kBox);
+                            for (int h = 0; h < nhx; ++h) tma_load_3d(sm + SM::KV + h * kBox, &g.k, kv_full, 64 * h, (int)w.h, row);
+                            for (int h = 0; h < nhz; ++h) tma_load_3d(sm + SM::KV + (2 + h) * kBox, &g.v, kv_full, 64 * h, (int)w.h, row);
+                            ++ci;
+                        }
+                    }
+                }
+            }
+            if (!ok) {  // let the copies under way land before the CTA leaves
+                for (uint32_t q = bi > kRing ? bi - kRing : 0; q < bi; ++q) mbar_wait(&b_full[q % kRing], (q / kRing) & 1, tc::kTimeout);
+                if (ci > 0) mbar_wait(kv_full, (ci - 1) & 1, tc::kTimeout);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 17) {
+        // scores: Q K^T and dO V^T
+        const uint32_t id_s = idesc_bf16(128, 64, false, false);
+        uint32_t it = 0, ci = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            if (!wait.all(kv_full, ci & 1, 132)) { ok = false; break; }
+            for (int a = 0; a < nt; ++a, ++it) {
+                const uint32_t q = 2 * it, o = q + 1;
+                if (!wait.all(&b_full[q % kRing], (q / kRing) & 1, 133) || !wait.all(&b_full[o % kRing], (o / kRing) & 1, 134) ||
+                    (it >= 1 && !wait.all(p_full, (it & 1) ^ 1, 135))) {  // the scores before have been read
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t xa = uniform(base + SM::RING + ((q + e) % kRing) * 4 * kBox), ya = uniform(base + SM::KV + e * 2 * kBox);
+#pragma unroll 1
+                    for (int k = 0; k < (e == 0 ? kx : kz); ++k)
+                        mma_bf16_one(leader, tS + 64 * e, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
+                }
+                if (leader) {
+                    mma_commit(s_full);
+                    if (a == nt - 1) mma_commit(kv_free);
+                }
+            }
+            ++ci;
+        }
+        if (!ok) {  // every MMA that was issued ends before the CTA leaves: they read shared memory
+            if (leader) mma_commit(&drained[0]);
+            mbar_wait(&drained[0], 0, tc::kTimeout);
+        }
+    } else if (warp == 19) {
+        // gradients, transposed: the state's parts, and the pairs' on top
+        const uint32_t id_v = idesc_bf16(128, 64, true, false), id_k = idesc_bf16(128, 64, false, false), id_p = idesc_bf16(128, 64, true, true);
+        uint32_t it = 0, ci = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            const uint32_t to = uniform(tO + (ci & 1) * 128);
+            if (!wait.all(kv_full, ci & 1, 136) || (ci >= 2 && !wait.all(&o_free[ci & 1], ((ci >> 1) & 1) ^ 1, 137)) || !wait.all(st_full, ci & 1, 138)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < kx; ++k)  // E^T K^T
+                mma_bf16_one(leader, to, mndesc(base + SM::ST + k * 2048, kHalf), kdesc(base + SM::KV + (k >> 2) * kBox + (k & 3) * 32), id_v, k > 0);
+#pragma unroll 1
+            for (int k = 0; k < kz; ++k)  // E V^T
+                mma_bf16_one(leader, to + 64, kdesc(base + SM::ST + (k >> 2) * kHalf + (k & 3) * 32), kdesc(base + SM::KV + (2 + (k >> 2)) * kBox + (k & 3) * 32),
+                             id_k, k > 0);
+            if (leader) {
+                if (!slow) mma_commit(&xs_full[ci & 1]);
+                mma_commit(xs_done);
+                mma_commit(kv_free);
+            }
+            for (int a = 0; a < nt; ++a, ++it) {
+                const uint32_t q = 2 * it;
+                const int steps = p.gy - 2 * a < 2 ? 4 : 8;  // of 16 rows
+                if (!wait.all(&zz_full[it & 1], (it >> 1) & 1, 139) || !wait.all(p_full, it & 1, 140)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {  // dO^T P, Q^T P'
+                    const uint32_t xa = uniform(base + SM::RING + ((q + 1 - e) % kRing) * 4 * kBox), pa = uniform(base + SM::PP + e * 2 * kBox);
+#pragma unroll 1
+                    for (int k = 0; k < steps; ++k)
+                        mma_bf16_one(leader, to + 64 * e, mndesc(xa + k * 2048, kHalf), mndesc(pa + k * 2048, kHalf), id_p, 1u);
+                }
+                if (leader) {
+                    mma_commit(pv_done);
+                    mma_commit(&b_free[q % kRing]);
+                    mma_commit(&b_free[(q + 1) % kRing]);
+                }
+            }
+            ++ci;
+        }
+        if (!ok) {
+            if (leader) mma_commit(&drained[1]);
+            mbar_wait(&drained[1], 0, tc::kTimeout);
+        }
+    } else if (warp == 18) {
+        const uint32_t id_h = idesc_bf16(128, nz, true, true);
+        uint32_t it = 0, ui = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            for (int a = 0; a < nt && ok; ++a, ++it) {
+                const uint32_t q = 2 * it, oa = uniform(base + SM::RING + ((q + 1) % kRing) * 4 * kBox);
+                const int heads = p.gy - 2 * a < 2 ? 1 : 2;
+                if (!wait.all(&b_full[(q + 1) % kRing], ((q + 1) / kRing) & 1, 154)) { ok = false; break; }
+                for (int k = 0; k < heads; ++k, ++ui) {
+                    if (!wait.all(kt_full, ui & 1, 141)) { ok = false; break; }
+                    tc_fence_after();
+                    state_mmas<1>(leader, tH, base + SM::KT, oa + k * kBox, kHalf, id_h, false);
+                    if (leader) mma_commit(h_done);
+                }
+                if (ok && leader) {
+                    mma_commit(&b_free[q % kRing]);
+                    mma_commit(&b_free[(q + 1) % kRing]);
+                }
+            }
+        }
+        if (!ok) {
+            if (leader) mma_commit(&drained[2]);
+            mbar_wait(&drained[2], 0, tc::kTimeout);
+        }
+    } else if (warp >= kMathWarps) {
+        // the state: half a row of E to a thread
+        const StateRow sr = state_row(p, tH, tid - 32 * kMathWarps);
+        uint32_t it = 0, ui = 0, ci = 0;
+        bool ok = true, was_last = false;
+        int was_seq = 0;
+        grid_dep_wait();
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            if (ci > 0) {
+                if (!wait.all(h_done, (ui - 1) & 1, 142) || !wait.all(xs_done, (ci - 1) & 1, 143)) { ok = false; break; }
+                tc_fence_after();
+                if (was_last) leave_state(p, sr, w.h, was_seq);
+            }
+            if (t.first || ci == 0) begin_state(p, sr, w, t);
+            pass_state(sr, base + SM::ST, nz, slow ? power(l2, t.n - 1 - mid) : 1.0f, pw[t.n]);
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(st_full);
+            for (int a = 0; a < nt && ok; ++a, ++it) {
+                const uint32_t q = 2 * it, qs = q % kRing, os = (q + 1) % kRing;
+                const uint32_t qa = base + SM::RING + qs * 4 * kBox, oa = base + SM::RING + os * 4 * kBox;
+                const int heads = p.gy - 2 * a < 2 ? 1 : 2, tok = sr.in & 63;
+                if (!wait.all(&b_full[qs], (q / kRing) & 1, 144)) { ok = false; break; }
+                if (t.n < 64) {  // rows behind the last token are factors of the products over rows
+                    if (!wait.all(&b_full[os], ((q + 1) / kRing) & 1, 145)) { ok = false; break; }
+                    for (int k = 0; k < heads; ++k) {
+                        clear_rows<32 * kStateWarps>(qa + k * kBox, kHalf, t.n, sr.in);
+                        clear_rows<32 * kStateWarps>(oa + k * kBox, kHalf, t.n, sr.in);
+                    }
+                    fence_async_smem();
+                }
+                mbar_arrive(&zz_full[it & 1]);
+                for (int k = 0; k < heads; ++k, ++ui) {
+                    // the first of a chunk: waited for before the state's copy
+                    if ((a > 0 || k > 0) && !wait.all(h_done, (ui - 1) & 1, 146)) { ok = false; break; }
+                    scale_rows<4, 1>(qa + k * kBox, kHalf, base + SM::KT, 2 * kx, t.n, tok < t.n ? pw[tok + 1] * p.in_scale : 0.0f, sr.in);
+                    fence_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(kt_full);
+                }
+            }
+            was_last = t.last;
+            was_seq = t.seq;
+            ++ci;
+        }
+        if (ok && ci > 0 && was_last && p.fin != nullptr) {
+            if (wait.all(h_done, (ui - 1) & 1, 147)) {
+                tc_fence_after();
+                leave_state(p, sr, w.h, was_seq);
+            }
+        }
+    } else {
+        // pairs: row r = (head, token i) of an item; gradients: value r, 32 of the chunk's tokens
+        const int quad = warp & 3, half = warp >> 2, r = 32 * quad + lane, i = r & 63, tq = quad & 1;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const float rowf = p.in_scale * (slow ? power(l2, i - mid) : 1.0f);
+        uint32_t it = 0, ci = 0;
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
+            const uint32_t acc = tO + (ci & 1) * 128 + lanes + 32 * half;
+            if (!slow) {  // e^(l (n-1-j)) on the state's parts
+                if (!wait.all(&xs_full[ci & 1], (ci >> 1) & 1, 148)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                    if ((c & 63) >= 32) continue;
+                    float v[16];
+                    tmem_ld16(acc + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int far = t.n - 1 - 32 * half - (c & 63) - k;
+                        v[k] = far >= 0 ? v[k] * pw[far] : 0.0f;
+                    }
+                    tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(v));
+                }
+                tmem_wait_st();
+            }
+            for (int a = 0; a < nt; ++a, ++it) {
+                const bool on = 2 * a + (quad >> 1) < p.gy;
+                if (!wait.all(s_full, it & 1, 149)) { ok = false; break; }
+                // the place of P is free: its MMAs are done, and a chunk's gradients have left it
+                if (it >= 1 && !wait.all(pv_done, (it - 1) & 1, 150)) { ok = false; break; }
+                if (a == 0 && ci >= 1 && !wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
+                tc_fence_after();
+                if (on) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {  // 32 columns of P, then of P'
+                        if ((c & 63) >= 32) continue;
+                        const int j = 32 * half + (c & 63);
+                        const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox;
+                        float v[16];
+                        tmem_ld16(tS + lanes + 32 * half + c, v);
+                        tmem_wait_ld();
+                        if (!slow) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] *= pw[i - j - k < 0 ? 0 : i - j - k];
+                        }
+                        if (tq <= half || t.n < 64) {  // tokens before the column's, and behind the last one, are left out whatever they hold
+                            const int last = i < t.n ? i - j : -1;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
+                        }
+                        const f2 f = pack(rowf, rowf);
+                        st_scaled8(to + sw128(r, (j >> 3)), v, f);
+                        st_scaled8(to + sw128(r, (j >> 3) + 1), v + 8, f);
+                    }
+                    fence_async_smem();
+                }
+                tc_fence_before();
+                mbar_arrive(p_full);
+            }
+            if (!ok) break;
+            // the chunk's gradients: value r of tokens 32 half .. + 31, to rows of 128 values
+            if (!wait.all(pv_done, (it - 1) & 1, 152)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {
+                if ((c & 63) >= 32) continue;
+                const int j = 32 * half + (c & 63);
+                const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 6) * 2;
+                float v[16];
+                tmem_ld16(acc + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    // a neighbour's value of the same token: even lanes store token j + k, odd ones j + k + 1
+                    const float a = v[k] * col[j + k], b = v[k + 1] * col[j + k + 1];
+                    const float got = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
+                    const int tok = j + k + (lane & 1);
+                    const uint32_t word = lane & 1 ? pack_bf16(got, b) : pack_bf16(a, got);
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + sw128(tok, (r & 63) >> 3)), "r"(word) : "memory");
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(&o_free[ci & 1]);
+            mbar_arrive(staged);
+            if (!wait.all(staged, ci & 1, 153)) { ok = false; break; }
+            // a warp to each 64 values of dv and dk, or, of fewer than 64 tokens, rows by all of them
+            const int row = (int)(w.b * p.seqs.L) + t.t0;
+            if (t.n == 64) {
+                const int e = warp >> 1, h = warp & 1;
+                if (warp < 4 && h < (e == 0 ? nhz : nhx) && lane == 0) {
+                    tma_store_3d(e == 0 ? &g.dv : &g.dk, sm + SM::PP + e * 2 * kBox + h * kBox, 64 * h, (int)w.h, row);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                    const int d = e == 0 ? p.dz : p.dx;
+                    const int64_t ld = e == 0 ? g.lddv : g.lddk;
+                    __nv_bfloat16* out = (__nv_bfloat16*)(e == 0 ? g.dv_out : g.dk_out) + (w.b * p.seqs.L + t.t0) * ld + w.h * d;
+#pragma unroll 1
+                    for (int c = tid; c < t.n * 16; c += 32 * kMathWarps) {
+                        const int tok = c >> 4, piece = c & 15;
+                        uint32_t v[4];
+                        ld_shared_v4(base + SM::PP + e * 2 * kBox + (piece >> 3) * kBox + sw128(tok, piece & 7), v[0], v[1], v[2], v[3]);
+                        if (8 * piece < d) *reinterpret_cast<uint4*>(out + tok * ld + 8 * piece) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(left);
+            ++ci;
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tb, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t decay_tc_grads(const DecayPass& p, void* dk, int64_t lddk, cudaStream_t s) {
+    GradArgs a;
+    a.p = p;
+    a.dk_out = dk;
+    a.dv_out = p.out;
+    a.lddk = lddk;
+    a.lddv = p.ldout;
+    const int64_t rows = p.units / p.Hkv * p.seqs.L;
+    if (!map_of(&a.q, p.y, rows, p.Hkv * p.gy, p.dx, p.ldy) || !map_of(&a.d_o, p.z, rows, p.Hkv * p.gy, p.dz, p.ldz) ||
+        !map_of(&a.k, p.x, rows, p.Hkv, p.dx, p.ldx) || !map_of(&a.v, p.v, rows, p.Hkv, p.dz, p.ldv) || !map_of(&a.dk, dk, rows, p.Hkv, p.dx, lddk) ||
+        !map_of(&a.dv, p.out, rows, p.Hkv, p.dz, p.ldout))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(decay_tc_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradSmem::BYTES);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.units * p.nseg));
+    if (p.nseg > 1) {  // its set-up overlaps the segments' ends
+        e = launch_dependent(decay_tc_grads_kernel, grid, dim3(kThreads), GradSmem::BYTES, s, a);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    decay_tc_grads_kernel<<<grid, kThreads, GradSmem::BYTES, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace lz

@@ -70,8 +70,9 @@ cudaError_t launch_decay_step(const DecayArgs& a, cudaStream_t s);
 // the token before a sequence's first one would see: ds_out enters undecayed and ds0 leaves that way.
 struct DecayPass {
     const void *x, *y, *z;
+    const void* v;  // the pass of dv: what the pass of dk has for x
     void* out;
-    int64_t ldx, ldy, ldz, ldout;
+    int64_t ldx, ldy, ldz, ldv, ldout;
     int dx, dz, gx, gy;
     bool rev, transposed;  // transposed: states in memory are [dz][dx]
     float out_scale, in_scale;
@@ -88,5 +89,7 @@ struct DecayPass {
 // On the tensor cores: the segments' own end states (of a pass that is not transposed), and a pass.
 cudaError_t decay_tc_ends(const DecayPass& p, float* recs, cudaStream_t s);
 cudaError_t decay_tc_pass(const DecayPass& p, cudaStream_t s);
+// dv and dk at once, from the pass of dv.
+cudaError_t decay_tc_grads(const DecayPass& p, void* dk, int64_t lddk, cudaStream_t s);
 
 }  // namespace lz
