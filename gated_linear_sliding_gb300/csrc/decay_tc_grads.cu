@@ -30,10 +30,13 @@ struct GradArgs {
     int64_t lddk, lddv;
 };
 
-constexpr int kRing = 3;  // tiles of 128 rows of Q and dO in turn: both of one item and the next one's Q
+// Tiles of Q and dO take turns in three places of 128 rows, or, with one query head a state, in six of 64.  With two
+// items or more in a chunk the last one's dO goes where the state's operand copy was, which is read at a chunk's
+// beginning and written behind its last item: three places alone had dO wait for the item before (164 us for the
+// training step above).
 struct GradSmem {
     static constexpr uint32_t RING = 0;
-    static constexpr uint32_t KV = kRing * 4 * kBox;  // K, V: 64 rows each
+    static constexpr uint32_t KV = 12 * kBox;         // K, V: 64 rows each
     static constexpr uint32_t PP = KV + 4 * kBox;     // P, P' [128 x 64]; then dv and dk [64 x 128] on their way out
     static constexpr uint32_t KT = PP + 4 * kBox;     // Q~: high part, low part
     static constexpr uint32_t ST = KT + 4 * kBox;
@@ -52,10 +55,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     float* pw = reinterpret_cast<float*>(sm + SM::TABLE);  // powers of the decay
     float* col = pw + 68;                                  // factors of the finished columns
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BARS);
-    uint64_t *b_full = bar, *b_free = bar + 3, *kv_full = bar + 6, *kv_free = bar + 7, *s_full = bar + 8, *p_full = bar + 9, *pv_done = bar + 10,
-             *xs_full = bar + 11, *o_free = bar + 13, *zz_full = bar + 15, *kt_full = bar + 17, *h_done = bar + 18, *st_full = bar + 19,
-             *xs_done = bar + 20, *staged = bar + 21, *left = bar + 22, *drained = bar + 23;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 26);
+    uint64_t *b_full = bar, *b_free = bar + 6, *kv_full = bar + 12, *kv_free = bar + 13, *s_full = bar + 14, *p_full = bar + 15, *pv_done = bar + 16,
+             *xs_full = bar + 17, *o_free = bar + 19, *zz_full = bar + 21, *kt_full = bar + 23, *h_done = bar + 24, *st_full = bar + 25,
+             *xs_done = bar + 26, *staged = bar + 27, *left = bar + 28, *late = bar + 29, *drained = bar + 30;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 33);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
@@ -70,11 +73,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     }
     const int nhx = (p.dx + 63) / 64, nhz = (p.dz + 63) / 64;
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < 6; ++i) {
             mbar_init(&b_full[i], 1);
             mbar_init(&b_free[i], 2);  // the gradients' and the state's MMAs
         }
         mbar_init(kv_full, 1);
+        mbar_init(late, 1);
         mbar_init(kv_free, 2);  // the scores and the state's parts
         mbar_init(s_full, 1);
         mbar_init(p_full, 32 * kMathWarps);
@@ -106,6 +110,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     const Waiter wait{abort, p.header};
     const int kx = (p.dx + 15) / 16, kz = (p.dz + 15) / 16, nz = 16 * kz;
     const int nt = (p.gy + 1) / 2;  // items of a chunk: two query heads, or one
+    const bool single = p.gy == 1;
+    const uint32_t places = single ? 6 : 3, place = single ? 2 * kBox : 4 * kBox, apart = single ? kBox : kHalf;
+    // of item a, whose Q is tile b of the ring: where its dO is
+    auto is_late = [&](int a) { return nt > 1 && a == nt - 1; };
+    auto tile = [&](uint32_t b) { return base + SM::RING + (b % places) * place; };
+    auto d_o_at = [&](int a, uint32_t b) { return is_late(a) ? base + SM::ST : tile(b + 1); };
 
     Walk walk(p.seqs, w.b, w.lo, w.hi, true, 64);
     Tile t;
@@ -116,45 +126,53 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
             prefetch_tmap(&g.d_o);
             prefetch_tmap(&g.k);
             prefetch_tmap(&g.v);
-            uint32_t bi = 0, ci = 0;
+            uint32_t bi = 0, ci = 0, li = 0;
             bool ok = true;
             while (ok && walk.next(p.seqs, w.b, &t)) {
                 const int row = (int)(w.b * p.seqs.L) + t.t0;
                 for (int a = 0; a < nt && ok; ++a) {
                     const int heads = p.gy - 2 * a < 2 ? 1 : 2, head = (int)(w.h * p.gy) + 2 * a;
-                    for (int e = 0; e < 2; ++e, ++bi) {  // Q, then dO
-                        const int s = bi % kRing, nh = e == 0 ? nhx : nhz;
-                        if (bi >= kRing && !wait(&b_free[s], ((bi / kRing) & 1) ^ 1, 130)) { ok = false; break; }
-                        uint8_t* to = sm + SM::RING + s * 4 * kBox;
-                        mbar_arrive_expect_tx(&b_full[s], heads * nh * kBox);
+                    for (int e = 0; e < 2; ++e) {  // Q, then dO
+                        const bool behind = e == 1 && is_late(a);
+                        const uint32_t s = bi % places;
+                        const int nh = e == 0 ? nhx : nhz;
+                        if (behind ? !wait(xs_done, ci & 1, 155) : bi >= places && !wait(&b_free[s], ((bi / places) & 1) ^ 1, 130)) { ok = false; break; }
+                        uint64_t* full = behind ? late : &b_full[s];
+                        uint8_t* to = sm + (behind ? SM::ST : SM::RING + s * place);
+                        mbar_arrive_expect_tx(full, heads * nh * kBox);
                         for (int k = 0; k < heads; ++k)
-                            for (int h = 0; h < nh; ++h) tma_load_3d(to + h * kHalf + k * kBox, e == 0 ? &g.q : &g.d_o, &b_full[s], 64 * h, head + k, row);
+                            for (int h = 0; h < nh; ++h) tma_load_3d(to + h * apart + k * kBox, e == 0 ? &g.q : &g.d_o, full, 64 * h, head + k, row);
+                        if (behind) ++li;
+                        else ++bi;
                         if (a == 0 && e == 0) {  // K and V of the chunk, behind the first Q, which need not wait for their place
-                            if (ci >= 1 && !wait(kv_free, (ci & 1) ^ 1, 131)) { ok = false; ++bi; break; }
+                            if (ci >= 1 && !wait(kv_free, (ci & 1) ^ 1, 131)) { ok = false; break; }
                             mbar_arrive_expect_tx(kv_full, (nhx + nhz) * kBox);
                             for (int h = 0; h < nhx; ++h) tma_load_3d(sm + SM::KV + h * kBox, &g.k, kv_full, 64 * h, (int)w.h, row);
                             for (int h = 0; h < nhz; ++h) tma_load_3d(sm + SM::KV + (2 + h) * kBox, &g.v, kv_full, 64 * h, (int)w.h, row);
-                            ++ci;
                         }
                     }
                 }
+                if (ok) ++ci;
             }
             if (!ok) {  // let the copies under way land before the CTA leaves
-                for (uint32_t q = bi > kRing ? bi - kRing : 0; q < bi; ++q) mbar_wait(&b_full[q % kRing], (q / kRing) & 1, tc::kTimeout);
+                for (uint32_t q = bi > places ? bi - places : 0; q < bi; ++q) mbar_wait(&b_full[q % places], (q / places) & 1, tc::kTimeout);
                 if (ci > 0) mbar_wait(kv_full, (ci - 1) & 1, tc::kTimeout);
+                mbar_wait(kv_full, ci & 1, tc::kTimeout / 4);  // perhaps under way
+                if (li > 0) mbar_wait(late, (li - 1) & 1, tc::kTimeout);
             }
         }
         __syncwarp();
     } else if (warp == 17) {
         // scores: Q K^T and dO V^T
         const uint32_t id_s = idesc_bf16(128, 64, false, false);
-        uint32_t it = 0, ci = 0;
+        uint32_t it = 0, ci = 0, q = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (!wait.all(kv_full, ci & 1, 132)) { ok = false; break; }
             for (int a = 0; a < nt; ++a, ++it) {
-                const uint32_t q = 2 * it, o = q + 1;
-                if (!wait.all(&b_full[q % kRing], (q / kRing) & 1, 133) || !wait.all(&b_full[o % kRing], (o / kRing) & 1, 134) ||
+                const uint32_t o = q + 1;
+                if (!wait.all(&b_full[q % places], (q / places) & 1, 133) ||
+                    !(is_late(a) ? wait.all(late, ci & 1, 134) : wait.all(&b_full[o % places], (o / places) & 1, 134)) ||
                     (it >= 1 && !wait.all(p_full, (it & 1) ^ 1, 135))) {  // the scores before have been read
                     ok = false;
                     break;
@@ -162,11 +180,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 tc_fence_after();
 #pragma unroll 1
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t xa = uniform(base + SM::RING + ((q + e) % kRing) * 4 * kBox), ya = uniform(base + SM::KV + e * 2 * kBox);
+                    const uint32_t xa = uniform(e == 0 ? tile(q) : d_o_at(a, q)), ya = uniform(base + SM::KV + e * 2 * kBox);
 #pragma unroll 1
                     for (int k = 0; k < (e == 0 ? kx : kz); ++k)
-                        mma_bf16_one(leader, tS + 64 * e, kdesc(xa + (k >> 2) * kHalf + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
+                        mma_bf16_one(leader, tS + 64 * e, kdesc(xa + (k >> 2) * apart + (k & 3) * 32), kdesc(ya + (k >> 2) * kBox + (k & 3) * 32), id_s, k > 0);
                 }
+                q += is_late(a) ? 1 : 2;
                 if (leader) {
                     mma_commit(s_full);
                     if (a == nt - 1) mma_commit(kv_free);
@@ -181,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     } else if (warp == 19) {
         // gradients, transposed: the state's parts, and the pairs' on top
         const uint32_t id_v = idesc_bf16(128, 64, true, false), id_k = idesc_bf16(128, 64, false, false), id_p = idesc_bf16(128, 64, true, true);
-        uint32_t it = 0, ci = 0;
+        uint32_t it = 0, ci = 0, q = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
             const uint32_t to = uniform(tO + (ci & 1) * 128);
@@ -203,22 +222,22 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 mma_commit(kv_free);
             }
             for (int a = 0; a < nt; ++a, ++it) {
-                const uint32_t q = 2 * it;
                 const int steps = p.gy - 2 * a < 2 ? 4 : 8;  // of 16 rows
                 if (!wait.all(&zz_full[it & 1], (it >> 1) & 1, 139) || !wait.all(p_full, it & 1, 140)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll 1
                 for (int e = 0; e < 2; ++e) {  // dO^T P, Q^T P'
-                    const uint32_t xa = uniform(base + SM::RING + ((q + 1 - e) % kRing) * 4 * kBox), pa = uniform(base + SM::PP + e * 2 * kBox);
+                    const uint32_t xa = uniform(e == 0 ? d_o_at(a, q) : tile(q)), pa = uniform(base + SM::PP + e * 2 * kBox);
 #pragma unroll 1
                     for (int k = 0; k < steps; ++k)
-                        mma_bf16_one(leader, to + 64 * e, mndesc(xa + k * 2048, kHalf), mndesc(pa + k * 2048, kHalf), id_p, 1u);
+                        mma_bf16_one(leader, to + 64 * e, mndesc(xa + k * 2048, apart), mndesc(pa + k * 2048, kHalf), id_p, 1u);
                 }
                 if (leader) {
                     mma_commit(pv_done);
-                    mma_commit(&b_free[q % kRing]);
-                    mma_commit(&b_free[(q + 1) % kRing]);
+                    mma_commit(&b_free[q % places]);
+                    if (!is_late(a)) mma_commit(&b_free[(q + 1) % places]);
                 }
+                q += is_late(a) ? 1 : 2;
             }
             ++ci;
         }
@@ -228,24 +247,26 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         }
     } else if (warp == 18) {
         const uint32_t id_h = idesc_bf16(128, nz, true, true);
-        uint32_t it = 0, ui = 0;
+        uint32_t ui = 0, ci = 0, q = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
-            for (int a = 0; a < nt && ok; ++a, ++it) {
-                const uint32_t q = 2 * it, oa = uniform(base + SM::RING + ((q + 1) % kRing) * 4 * kBox);
+            for (int a = 0; a < nt && ok; ++a) {
+                const uint32_t oa = uniform(d_o_at(a, q)), o = q + 1;
                 const int heads = p.gy - 2 * a < 2 ? 1 : 2;
-                if (!wait.all(&b_full[(q + 1) % kRing], ((q + 1) / kRing) & 1, 154)) { ok = false; break; }
+                if (!(is_late(a) ? wait.all(late, ci & 1, 154) : wait.all(&b_full[o % places], (o / places) & 1, 154))) { ok = false; break; }
                 for (int k = 0; k < heads; ++k, ++ui) {
                     if (!wait.all(kt_full, ui & 1, 141)) { ok = false; break; }
                     tc_fence_after();
-                    state_mmas<1>(leader, tH, base + SM::KT, oa + k * kBox, kHalf, id_h, false);
+                    state_mmas<1>(leader, tH, base + SM::KT, oa + k * kBox, apart, id_h, false);
                     if (leader) mma_commit(h_done);
                 }
                 if (ok && leader) {
-                    mma_commit(&b_free[q % kRing]);
-                    mma_commit(&b_free[(q + 1) % kRing]);
+                    mma_commit(&b_free[q % places]);
+                    if (!is_late(a)) mma_commit(&b_free[o % places]);
                 }
+                q += is_late(a) ? 1 : 2;
             }
+            ++ci;
         }
         if (!ok) {
             if (leader) mma_commit(&drained[2]);
@@ -254,13 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     } else if (warp >= kMathWarps) {
         // the state: half a row of E to a thread
         const StateRow sr = state_row(p, tH, tid - 32 * kMathWarps);
-        uint32_t it = 0, ui = 0, ci = 0;
+        uint32_t it = 0, ui = 0, ci = 0, q = 0;
         bool ok = true, was_last = false;
         int was_seq = 0;
         grid_dep_wait();
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (ci > 0) {
-                if (!wait.all(h_done, (ui - 1) & 1, 142) || !wait.all(xs_done, (ci - 1) & 1, 143)) { ok = false; break; }
+                // (a late dO lies where the state's copy goes: the gradients' products are done with it)
+                if (!wait.all(h_done, (ui - 1) & 1, 142) || !wait.all(xs_done, (ci - 1) & 1, 143) || !wait.all(pv_done, (it - 1) & 1, 156)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 if (was_last) leave_state(p, sr, w.h, was_seq);
             }
@@ -270,15 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
             tc_fence_before();
             mbar_arrive(st_full);
             for (int a = 0; a < nt && ok; ++a, ++it) {
-                const uint32_t q = 2 * it, qs = q % kRing, os = (q + 1) % kRing;
-                const uint32_t qa = base + SM::RING + qs * 4 * kBox, oa = base + SM::RING + os * 4 * kBox;
+                const uint32_t qa = tile(q), oa = d_o_at(a, q), o = q + 1;
                 const int heads = p.gy - 2 * a < 2 ? 1 : 2, tok = sr.in & 63;
-                if (!wait.all(&b_full[qs], (q / kRing) & 1, 144)) { ok = false; break; }
+                if (!wait.all(&b_full[q % places], (q / places) & 1, 144)) { ok = false; break; }
                 if (t.n < 64) {  // rows behind the last token are factors of the products over rows
-                    if (!wait.all(&b_full[os], ((q + 1) / kRing) & 1, 145)) { ok = false; break; }
+                    if (!(is_late(a) ? wait.all(late, ci & 1, 145) : wait.all(&b_full[o % places], (o / places) & 1, 145))) { ok = false; break; }
                     for (int k = 0; k < heads; ++k) {
-                        clear_rows<32 * kStateWarps>(qa + k * kBox, kHalf, t.n, sr.in);
-                        clear_rows<32 * kStateWarps>(oa + k * kBox, kHalf, t.n, sr.in);
+                        clear_rows<32 * kStateWarps>(qa + k * kBox, apart, t.n, sr.in);
+                        clear_rows<32 * kStateWarps>(oa + k * kBox, apart, t.n, sr.in);
                     }
                     fence_async_smem();
                 }
@@ -286,11 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 for (int k = 0; k < heads; ++k, ++ui) {
                     // the first of a chunk: waited for before the state's copy
                     if ((a > 0 || k > 0) && !wait.all(h_done, (ui - 1) & 1, 146)) { ok = false; break; }
-                    scale_rows<4, 1>(qa + k * kBox, kHalf, base + SM::KT, 2 * kx, t.n, tok < t.n ? pw[tok + 1] * p.in_scale : 0.0f, sr.in);
+                    scale_rows<4, 1>(qa + k * kBox, apart, base + SM::KT, 2 * kx, t.n, tok < t.n ? pw[tok + 1] * p.in_scale : 0.0f, sr.in);
                     fence_async_smem();
                     tc_fence_before();
                     mbar_arrive(kt_full);
                 }
+                q += is_late(a) ? 1 : 2;
             }
             was_last = t.last;
             was_seq = t.seq;
@@ -307,6 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         const int quad = warp & 3, half = warp >> 2, r = 32 * quad + lane, i = r & 63, tq = quad & 1;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         const float rowf = p.in_scale * (slow ? power(l2, i - mid) : 1.0f);
+        const uint32_t c0 = base + SM::TABLE + 68 * 4;
+        uint32_t sw[8];  // places of a value's 16 bytes in rows of the swizzle
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sw[k] = (((r & 63) >> 3) ^ k) << 4;
         uint32_t it = 0, ci = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
@@ -334,7 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 if (!wait.all(s_full, it & 1, 149)) { ok = false; break; }
                 // the place of P is free: its MMAs are done, and a chunk's gradients have left it
                 if (it >= 1 && !wait.all(pv_done, (it - 1) & 1, 150)) { ok = false; break; }
-                if (a == 0 && ci >= 1 && !wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
+                if (a == 0 && ci >= 1) {
+                    if (lane == 0) {
+                        bulk_wait_read();
+                        mbar_arrive(left);
+                    }
+                    if (!wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
+                }
                 tc_fence_after();
                 if (on) {
 #pragma unroll 1
@@ -371,18 +406,19 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
             for (int c = 0; c < 128; c += 16) {
                 if ((c & 63) >= 32) continue;
                 const int j = 32 * half + (c & 63);
-                const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 6) * 2;
+                const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 7) * 2 + j * 128;
                 float v[16];
                 tmem_ld16(acc + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    // a neighbour's value of the same token: even lanes store token j + k, odd ones j + k + 1
-                    const float a = v[k] * col[j + k], b = v[k + 1] * col[j + k + 1];
-                    const float got = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
-                    const int tok = j + k + (lane & 1);
-                    const uint32_t word = lane & 1 ? pack_bf16(got, b) : pack_bf16(a, got);
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + sw128(tok, (r & 63) >> 3)), "r"(word) : "memory");
+                for (int k = 0; k < 16; k += 4) {  // single values: 32 lanes make half a row
+                    uint32_t f[4];
+                    ld_shared_v4(c0 + (j + k) * 4, f[0], f[1], f[2], f[3]);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v[k + m] * __uint_as_float(f[m])));
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + sw[(k + m) & 7] + (k + m) * 128), "h"(h) : "memory");
+                    }
                 }
             }
             fence_async_smem();
@@ -397,7 +433,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 if (warp < 4 && h < (e == 0 ? nhz : nhx) && lane == 0) {
                     tma_store_3d(e == 0 ? &g.dv : &g.dk, sm + SM::PP + e * 2 * kBox + h * kBox, 64 * h, (int)w.h, row);
                     bulk_commit();
-                    bulk_wait_read();
                 }
             } else {
 #pragma unroll 1
@@ -414,8 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(left);
             ++ci;
         }
         if (lane == 0) bulk_wait_all();
