@@ -30,14 +30,16 @@ struct GradArgs {
     int64_t lddk, lddv;
 };
 
-// Tiles of Q and dO take turns in three places of 128 rows, or, with one query head a state, in six of 64.  With two
+// Tiles of Q and dO take turns in three places of 128 rows, or, with one query head a state, in four of 64.  With two
 // items or more in a chunk the last one's dO goes where the state's operand copy was, which is read at a chunk's
 // beginning and written behind its last item: three places alone had dO wait for the item before (164 us for the
-// training step above).
+// training step above).  With one query head the gradients leave through a place of their own, after the next chunk's
+// pairs have been weighed; otherwise through that of P, before.
 struct GradSmem {
     static constexpr uint32_t RING = 0;
     static constexpr uint32_t KV = 12 * kBox;         // K, V: 64 rows each
-    static constexpr uint32_t PP = KV + 4 * kBox;     // P, P' [128 x 64]; then dv and dk [64 x 128] on their way out
+    static constexpr uint32_t OWN = RING + 8 * kBox;  // dv and dk [64 x 128] on their way out, one query head a state
+    static constexpr uint32_t PP = KV + 4 * kBox;     // P, P' [128 x 64]; else dv and dk
     static constexpr uint32_t KT = PP + 4 * kBox;     // Q~: high part, low part
     static constexpr uint32_t ST = KT + 4 * kBox;
     static constexpr uint32_t TABLE = ST + 4 * kBox;  // powers 0 .. 64, and the columns' factors
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     const int kx = (p.dx + 15) / 16, kz = (p.dz + 15) / 16, nz = 16 * kz;
     const int nt = (p.gy + 1) / 2;  // items of a chunk: two query heads, or one
     const bool single = p.gy == 1;
-    const uint32_t places = single ? 6 : 3, place = single ? 2 * kBox : 4 * kBox, apart = single ? kBox : kHalf;
+    const uint32_t places = single ? 4 : 3, place = single ? 2 * kBox : 4 * kBox, apart = single ? kBox : kHalf;
     // of item a, whose Q is tile b of the ring: where its dO is
     auto is_late = [&](int a) { return nt > 1 && a == nt - 1; };
     auto tile = [&](uint32_t b) { return base + SM::RING + (b % places) * place; };
@@ -337,119 +339,145 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
 #pragma unroll
         for (int k = 0; k < 8; ++k) sw[k] = (((r & 63) >> 3) ^ k) << 4;
         uint32_t it = 0, ci = 0;
-        bool ok = true;
-        while (ok && walk.next(p.seqs, w.b, &t)) {
-            const uint32_t acc = tO + (ci & 1) * 128 + lanes + 32 * half;
-            if (!slow) {  // e^(l (n-1-j)) on the state's parts
-                if (!wait.all(&xs_full[ci & 1], (ci >> 1) & 1, 148)) { ok = false; break; }
+        int held_t0 = 0, held_n = 0;  // the chunk whose gradients are still to leave
+        const uint32_t stage = single ? SM::OWN : SM::PP;
+        bool have = true, held = false;
+        // this warp's part of the gradients before has left the place that is written next
+        auto vacant = [&]() {
+            __syncwarp();
+            if (lane == 0) {
+                bulk_wait_read();
+                mbar_arrive(left);
+            }
+        };
+        uint32_t out = 0;  // chunks whose gradients have left
+        while (true) {
+            have = walk.next(p.seqs, w.b, &t);
+            if (have) {
+                const uint32_t acc = tO + (ci & 1) * 128 + lanes + 32 * half;
+                if (!slow) {  // e^(l (n-1-j)) on the state's parts
+                    if (!wait.all(&xs_full[ci & 1], (ci >> 1) & 1, 148)) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {
+                        if ((c & 63) >= 32) continue;
+                        float v[16];
+                        tmem_ld16(acc + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int far = t.n - 1 - 32 * half - (c & 63) - k;
+                            v[k] = far >= 0 ? v[k] * pw[far] : 0.0f;
+                        }
+                        tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(v));
+                    }
+                    tmem_wait_st();
+                }
+                bool ok = true;
+                for (int a = 0; a < nt; ++a, ++it) {
+                    const bool on = 2 * a + (quad >> 1) < p.gy;
+                    if (!wait.all(s_full, it & 1, 149)) { ok = false; break; }
+                    // the place of P is free: its MMAs are done, and a chunk's gradients have left it
+                    if (it >= 1 && !wait.all(pv_done, (it - 1) & 1, 150)) { ok = false; break; }
+                    if (!single && a == 0 && ci >= 1) {
+                        vacant();
+                        if (!wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
+                    }
+                    tc_fence_after();
+                    if (on) {
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 16) {  // 32 columns of P, then of P'
+                            if ((c & 63) >= 32) continue;
+                            const int j = 32 * half + (c & 63);
+                            const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox;
+                            float v[16];
+                            tmem_ld16(tS + lanes + 32 * half + c, v);
+                            tmem_wait_ld();
+                            if (!slow) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) v[k] *= pw[i - j - k < 0 ? 0 : i - j - k];
+                            }
+                            if (tq <= half || t.n < 64) {  // tokens before the column's, and behind the last one, are left out whatever they hold
+                                const int last = i < t.n ? i - j : -1;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
+                            }
+                            const f2 f = pack(rowf, rowf);
+                            st_scaled8(to + sw128(r, (j >> 3)), v, f);
+                            st_scaled8(to + sw128(r, (j >> 3) + 1), v + 8, f);
+                        }
+                        fence_async_smem();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(p_full);
+                }
+                if (!ok) break;
+                ++ci;
+            }
+            // a chunk's gradients: value r of tokens 32 half .. + 31, to rows of 128 values
+            const bool leaves = single ? held : have;
+            if (leaves) {
+                if (!single) held_t0 = t.t0, held_n = t.n;
+                // (its products: with the next chunk's pairs weighed, they have been waited for)
+                if (!(single && have) && !wait.all(pv_done, (it - 1) & 1, 152)) break;
+                if (single && out >= 1) {
+                    vacant();
+                    if (!wait.all(left, (out - 1) & 1, 157)) break;
+                }
                 tc_fence_after();
+                const uint32_t acc = tO + (out & 1) * 128 + lanes + 32 * half;
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 16) {
                     if ((c & 63) >= 32) continue;
+                    const int j = 32 * half + (c & 63);
+                    const uint32_t to = base + stage + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 7) * 2 + j * 128;
                     float v[16];
                     tmem_ld16(acc + c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int far = t.n - 1 - 32 * half - (c & 63) - k;
-                        v[k] = far >= 0 ? v[k] * pw[far] : 0.0f;
-                    }
-                    tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(v));
-                }
-                tmem_wait_st();
-            }
-            for (int a = 0; a < nt; ++a, ++it) {
-                const bool on = 2 * a + (quad >> 1) < p.gy;
-                if (!wait.all(s_full, it & 1, 149)) { ok = false; break; }
-                // the place of P is free: its MMAs are done, and a chunk's gradients have left it
-                if (it >= 1 && !wait.all(pv_done, (it - 1) & 1, 150)) { ok = false; break; }
-                if (a == 0 && ci >= 1) {
-                    if (lane == 0) {
-                        bulk_wait_read();
-                        mbar_arrive(left);
-                    }
-                    if (!wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
-                }
-                tc_fence_after();
-                if (on) {
-#pragma unroll 1
-                    for (int c = 0; c < 128; c += 16) {  // 32 columns of P, then of P'
-                        if ((c & 63) >= 32) continue;
-                        const int j = 32 * half + (c & 63);
-                        const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox;
-                        float v[16];
-                        tmem_ld16(tS + lanes + 32 * half + c, v);
-                        tmem_wait_ld();
-                        if (!slow) {
+                    for (int k = 0; k < 16; k += 4) {  // single values: 32 lanes make half a row
+                        uint32_t f[4];
+                        ld_shared_v4(c0 + (j + k) * 4, f[0], f[1], f[2], f[3]);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] *= pw[i - j - k < 0 ? 0 : i - j - k];
+                        for (int m = 0; m < 4; ++m) {
+                            const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v[k + m] * __uint_as_float(f[m])));
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + sw[(k + m) & 7] + (k + m) * 128), "h"(h) : "memory");
                         }
-                        if (tq <= half || t.n < 64) {  // tokens before the column's, and behind the last one, are left out whatever they hold
-                            const int last = i < t.n ? i - j : -1;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
-                        }
-                        const f2 f = pack(rowf, rowf);
-                        st_scaled8(to + sw128(r, (j >> 3)), v, f);
-                        st_scaled8(to + sw128(r, (j >> 3) + 1), v + 8, f);
                     }
-                    fence_async_smem();
                 }
+                fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(p_full);
-            }
-            if (!ok) break;
-            // the chunk's gradients: value r of tokens 32 half .. + 31, to rows of 128 values
-            if (!wait.all(pv_done, (it - 1) & 1, 152)) { ok = false; break; }
-            tc_fence_after();
+                mbar_arrive(&o_free[out & 1]);
+                mbar_arrive(staged);
+                if (!wait.all(staged, out & 1, 153)) break;
+                // a warp to each 64 values of dv and dk, or, of fewer than 64 tokens, rows by all of them
+                const int row = (int)(w.b * p.seqs.L) + held_t0;
+                if (held_n == 64) {
+                    const int e = warp >> 1, h = warp & 1;
+                    if (warp < 4 && h < (e == 0 ? nhz : nhx) && lane == 0) {
+                        tma_store_3d(e == 0 ? &g.dv : &g.dk, sm + stage + e * 2 * kBox + h * kBox, 64 * h, (int)w.h, row);
+                        bulk_commit();
+                    }
+                } else {
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-                if ((c & 63) >= 32) continue;
-                const int j = 32 * half + (c & 63);
-                const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 7) * 2 + j * 128;
-                float v[16];
-                tmem_ld16(acc + c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) {  // single values: 32 lanes make half a row
-                    uint32_t f[4];
-                    ld_shared_v4(c0 + (j + k) * 4, f[0], f[1], f[2], f[3]);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v[k + m] * __uint_as_float(f[m])));
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + sw[(k + m) & 7] + (k + m) * 128), "h"(h) : "memory");
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = e == 0 ? p.dz : p.dx;
+                        const int64_t ld = e == 0 ? g.lddv : g.lddk;
+                        __nv_bfloat16* out = (__nv_bfloat16*)(e == 0 ? g.dv_out : g.dk_out) + (w.b * p.seqs.L + held_t0) * ld + w.h * d;
+#pragma unroll 1
+                        for (int c = tid; c < held_n * 16; c += 32 * kMathWarps) {
+                            const int tok = c >> 4, piece = c & 15;
+                            uint32_t v[4];
+                            ld_shared_v4(base + stage + e * 2 * kBox + (piece >> 3) * kBox + sw128(tok, piece & 7), v[0], v[1], v[2], v[3]);
+                            if (8 * piece < d) *reinterpret_cast<uint4*>(out + tok * ld + 8 * piece) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
                     }
                 }
+                ++out;
             }
-            fence_async_smem();
-            tc_fence_before();
-            mbar_arrive(&o_free[ci & 1]);
-            mbar_arrive(staged);
-            if (!wait.all(staged, ci & 1, 153)) { ok = false; break; }
-            // a warp to each 64 values of dv and dk, or, of fewer than 64 tokens, rows by all of them
-            const int row = (int)(w.b * p.seqs.L) + t.t0;
-            if (t.n == 64) {
-                const int e = warp >> 1, h = warp & 1;
-                if (warp < 4 && h < (e == 0 ? nhz : nhx) && lane == 0) {
-                    tma_store_3d(e == 0 ? &g.dv : &g.dk, sm + SM::PP + e * 2 * kBox + h * kBox, 64 * h, (int)w.h, row);
-                    bulk_commit();
-                }
-            } else {
-#pragma unroll 1
-                for (int e = 0; e < 2; ++e) {
-                    const int d = e == 0 ? p.dz : p.dx;
-                    const int64_t ld = e == 0 ? g.lddv : g.lddk;
-                    __nv_bfloat16* out = (__nv_bfloat16*)(e == 0 ? g.dv_out : g.dk_out) + (w.b * p.seqs.L + t.t0) * ld + w.h * d;
-#pragma unroll 1
-                    for (int c = tid; c < t.n * 16; c += 32 * kMathWarps) {
-                        const int tok = c >> 4, piece = c & 15;
-                        uint32_t v[4];
-                        ld_shared_v4(base + SM::PP + e * 2 * kBox + (piece >> 3) * kBox + sw128(tok, piece & 7), v[0], v[1], v[2], v[3]);
-                        if (8 * piece < d) *reinterpret_cast<uint4*>(out + tok * ld + 8 * piece) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-            }
-            ++ci;
+            if (!have) break;
+            held = true;
+            held_t0 = t.t0, held_n = t.n;
         }
         if (lane == 0) bulk_wait_all();
     }
