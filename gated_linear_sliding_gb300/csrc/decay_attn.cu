@@ -17,12 +17,75 @@ constexpr int NT = 256;
 constexpr int ZS = 64;       // columns of z a CTA works on
 constexpr int PS = kTile + 4;  // row of pair weights in shared memory
 
+// A thread's pieces of a tile's rows: piece c of row r, then dr rows and dc of a row's n pieces on.
+struct Pieces {
+    int r, c, dr, dc, n;
+};
+__device__ __forceinline__ Pieces pieces_of(int n) {
+    Pieces q;
+    q.n = n;
+    q.r = threadIdx.x / n;
+    q.c = threadIdx.x - q.r * n;
+    q.dr = NT / n;
+    q.dc = NT - q.dr * n;
+    return q;
+}
+
 // Rows [0, n) of a tile of `cols` columns as fp32 with row distance `ld` in shared memory; other places 0.
-template <typename T>
-__device__ __forceinline__ void load_rows(float* to, int ld, const T* from, int64_t dist, int n, int cols, int width) {
-    for (int e = threadIdx.x; e < kTile * width; e += NT) {
-        const int r = e / width, c = e - r * width;
-        to[r * ld + c] = r < n && c < cols ? lz::ld(from + r * dist + c) : 0.0f;
+// Pieces of V values, eight of a thread under way; a function of its own for each kind, not one for each use.
+template <typename T, int V>
+__device__ __noinline__ void load_pieces(float* to, int ld, const T* from, int64_t dist, int n, int cols, Pieces q) {
+    while (q.r < kTile) {
+        float v[8][V];
+        int at[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[u][i] = 0.0f;
+            if (q.r < n && q.c * V < cols) Vec<V>::ld(from + q.r * dist + q.c * V, v[u]);
+            at[u] = q.r < kTile ? q.r * ld + q.c * V : -1;
+            q.r += q.dr;
+            q.c += q.dc;
+            if (q.c >= q.n) q.c -= q.n, ++q.r;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (at[u] >= 0) Vec<V>::st(to + at[u], v[u]);
+    }
+}
+__device__ __forceinline__ void load_rows(const DecayPass& p, float* to, int ld, const void* base, int64_t at, int64_t dist, int n, int cols, const Pieces& q) {
+    if (p.f32) {
+        if (p.fours) load_pieces<float, 4>(to, ld, (const float*)base + at, dist, n, cols, q);
+        else load_pieces<float, 1>(to, ld, (const float*)base + at, dist, n, cols, q);
+    } else {
+        if (p.fours) load_pieces<__nv_bfloat16, 4>(to, ld, (const __nv_bfloat16*)base + at, dist, n, cols, q);
+        else load_pieces<__nv_bfloat16, 1>(to, ld, (const __nv_bfloat16*)base + at, dist, n, cols, q);
+    }
+}
+
+// acc += sum over rows j of f[j] y[j] z[j]^T: rows 4 (ty + 16 m) .. + 3 of the sum and columns 4 tx .. + 3.
+template <int M>
+__device__ __forceinline__ void add_products(float (&acc)[M][4][4], const float* ys, int ldx, const float* zs, const float* f, int n, int dxp) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        float4 z = *reinterpret_cast<const float4*>(zs + j * ZS + tx * 4);
+        const float w = f[j];
+        z.x *= w, z.y *= w, z.z *= w, z.w *= w;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int row = 4 * (ty + 16 * m);
+            if (row >= dxp) continue;
+            const float4 y4 = *reinterpret_cast<const float4*>(ys + j * ldx + row);
+            const float y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[m][i][0] = fmaf(y[i], z.x, acc[m][i][0]);
+                acc[m][i][1] = fmaf(y[i], z.y, acc[m][i][1]);
+                acc[m][i][2] = fmaf(y[i], z.z, acc[m][i][2]);
+                acc[m][i][3] = fmaf(y[i], z.w, acc[m][i][3]);
+            }
+        }
     }
 }
 
@@ -52,62 +115,56 @@ __device__ __forceinline__ int64_t state_at(const DecayPass& p, int i, int j) {
 }
 
 // A segment's own contribution to the state that leaves it (always [dk][dv]: never transposed).
-template <typename T, int NI>
+template <int M>
 __global__ void __launch_bounds__(NT) decay_ends_kernel(const DecayPass p, float* recs) {
     extern __shared__ float sm[];
     const int slices = (p.dz + ZS - 1) / ZS;
     const Where w = where_of<true>(p, slices);
     check_offsets(p.seqs, p.header);
-    const int ldx = (p.dx + 3) / 4 * 4 + 4;
-    float *ys = sm, *zs = ys + kTile * ldx;
+    const int dxp = (p.dx + 3) / 4 * 4, ldx = dxp + 4;
+    float *ys = sm, *zs = ys + kTile * ldx, *fs = zs + kTile * ZS;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int z0 = w.slice * ZS, zn = min(ZS, p.dz - z0);
     const float l2 = log2_decay(p.log_decay, w.h);
-    float acc[NI][4] = {};
+    const int v = p.fours ? 4 : 1;
+    const Pieces qy = pieces_of(dxp / v), qz = pieces_of(ZS / v);
+    float acc[M][4][4] = {};
     const Reach r = reach(p.seqs, w.b, w.lo, w.hi, p.rev);
     if (r.whole && p.init != nullptr) {
         const float f = power(l2, r.to - r.from);
         const float* s = p.init + (r.seq * p.Hkv + w.h) * p.dx * p.dz;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+        for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int row = ty + 16 * i, col = tx * 4 + c;
-                if (row < p.dx && col < zn) acc[i][c] = f * s[state_at(p, row, z0 + col)];
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int row = 4 * (ty + 16 * m) + i, col = tx * 4 + c;
+                    if (row < p.dx && col < zn) acc[m][i][c] = f * s[state_at(p, row, z0 + col)];
+                }
     }
     for (int64_t t0 = r.from; t0 < r.to; t0 += kTile) {
         const int n = (int)min64(kTile, r.to - t0);
         for (int g = 0; g < p.gy; ++g) {
             __syncthreads();
             const int64_t row = w.b * p.seqs.L + t0, head = w.h * p.gy + g;
-            load_rows(ys, ldx, (const T*)p.y + row * p.ldy + head * p.dx, p.ldy, n, p.dx, ldx);
-            load_rows(zs, ZS, (const T*)p.z + row * p.ldz + head * p.dz + z0, p.ldz, n, zn, ZS);
+            load_rows(p, ys, ldx, p.y, row * p.ldy + head * p.dx, p.ldy, n, p.dx, qy);
+            load_rows(p, zs, ZS, p.z, row * p.ldz + head * p.dz + z0, p.ldz, n, zn, qz);
+            if (g == 0 && threadIdx.x < n) fs[threadIdx.x] = power(l2, p.rev ? t0 + threadIdx.x - r.from + 1 : r.to - 1 - t0 - threadIdx.x) * p.in_scale;
             __syncthreads();
-            for (int j = 0; j < n; ++j) {
-                const int64_t dist = p.rev ? t0 + j - r.from + 1 : r.to - 1 - t0 - j;
-                const float f = power(l2, dist) * p.in_scale;
-                float4 z = *reinterpret_cast<const float4*>(zs + j * ZS + tx * 4);
-                z.x *= f, z.y *= f, z.z *= f, z.w *= f;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const float y = ys[j * ldx + min(ty + 16 * i, p.dx)];
-                    acc[i][0] = fmaf(y, z.x, acc[i][0]);
-                    acc[i][1] = fmaf(y, z.y, acc[i][1]);
-                    acc[i][2] = fmaf(y, z.z, acc[i][2]);
-                    acc[i][3] = fmaf(y, z.w, acc[i][3]);
-                }
-            }
+            add_products<M>(acc, ys, ldx, zs, fs, n, dxp);
         }
     }
     float* out = recs + (w.unit * p.nseg + (p.parts > 0 ? 0 : w.seg)) * p.dx * p.dz;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int row = ty + 16 * i, col = tx * 4 + c;
-            if (row < p.dx && col < zn) out[(int64_t)row * p.dz + z0 + col] = acc[i][c];
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int row = 4 * (ty + 16 * m) + i, col = tx * 4 + c;
+                if (row < p.dx && col < zn) out[(int64_t)row * p.dz + z0 + col] = acc[m][i][c];
+            }
 }
 
 // The states in front of the segments from their own contributions, in place: an element a thread,
@@ -150,8 +207,8 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
     }
 }
 
-// One pass over a segment's tiles, 64 columns of z to a CTA.
-template <typename T>
+// One pass over a segment's tiles, 64 columns of z to a CTA; M: rows of the state by 64.
+template <int M, bool REV>
 __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     extern __shared__ float sm[];
     const int slices = (p.dz + ZS - 1) / ZS;
@@ -164,14 +221,17 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     float* ps = zs + kTile * ZS;     // [64][PS]
     float* st = ps + kTile * PS;     // [dxp][ZS]
     float* pw = st + dxp * ZS;       // powers 0 .. 64 of the decay
+    float* fs = pw + kTile + 4;      // [64]: factors of the tile's rows on their way into the state
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int z0 = w.slice * ZS, zn = min(ZS, p.dz - z0);
     const int64_t size = (int64_t)p.dx * p.dz;
     const float l2 = log2_decay(p.log_decay, w.h);
+    const int v = p.fours ? 4 : 1;
+    const Pieces qx = pieces_of(dxp / v), qz = pieces_of(ZS / v);
     for (int i = threadIdx.x; i <= kTile; i += NT) pw[i] = power(l2, i);
     grid_dep_wait();
 
-    Walk walk(p.seqs, w.b, w.lo, w.hi, p.rev);
+    Walk walk(p.seqs, w.b, w.lo, w.hi, REV);
     Tile t;
     bool begun = false;
     while (walk.next(p.seqs, w.b, &t)) {
@@ -179,26 +239,28 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
         if (t.first || !begun) {
             const float* from = t.first ? (p.init == nullptr ? nullptr : p.init + (t.seq * p.Hkv + w.h) * size)
                                         : first_state(p, w.unit, w.seg);
+#pragma unroll 8
             for (int e = threadIdx.x; e < dxp * ZS; e += NT) {
                 const int i = e / ZS, j = e % ZS;
                 st[e] = from != nullptr && i < p.dx && j < zn ? from[state_at(p, i, z0 + j)] : 0.0f;
             }
             begun = true;
         }
+        if (threadIdx.x < t.n) fs[threadIdx.x] = pw[REV ? threadIdx.x + 1 : t.n - 1 - threadIdx.x] * p.in_scale;
         const int64_t row = w.b * p.seqs.L + t.t0;
         for (int a = 0; a < p.gx; ++a) {
             float o[4][4] = {};
             for (int g = 0; g < p.gy; ++g) {
                 const int64_t head = w.h * p.gy + g;
-                if (g == 0)
-                    load_rows(xs, ldx, (const T*)p.x + row * p.ldx + (w.h * p.gx + a) * p.dx, p.ldx, t.n, p.dx, ldx);
+                if (g == 0) load_rows(p, xs, ldx, p.x, row * p.ldx + (w.h * p.gx + a) * p.dx, p.ldx, t.n, p.dx, qx);
                 if (a == 0) {
-                    load_rows(ys, ldx, (const T*)p.y + row * p.ldy + head * p.dx, p.ldy, t.n, p.dx, ldx);
-                    load_rows(zs, ZS, (const T*)p.z + row * p.ldz + head * p.dz + z0, p.ldz, t.n, zn, ZS);
+                    load_rows(p, ys, ldx, p.y, row * p.ldy + head * p.dx, p.ldy, t.n, p.dx, qx);
+                    load_rows(p, zs, ZS, p.z, row * p.ldz + head * p.dz + z0, p.ldz, t.n, zn, qz);
                 }
                 __syncthreads();
-                // the pairs of the tile: rows ty + 16 i, columns tx + 16 j
+                // the pairs of the tile: rows ty + 16 i, columns tx + 16 j; blocks that are all masked are left out
                 float s[4][4] = {};
+#pragma unroll 2
                 for (int k = 0; k < dxp; k += 4) {
                     float4 xv[4], yv[4];
 #pragma unroll
@@ -210,6 +272,7 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
+                            if (REV ? j < i : j > i) continue;
                             s[i][j] = fmaf(xv[i].x, yv[j].x, s[i][j]);
                             s[i][j] = fmaf(xv[i].y, yv[j].y, s[i][j]);
                             s[i][j] = fmaf(xv[i].z, yv[j].z, s[i][j]);
@@ -220,10 +283,12 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int r = ty + 16 * i, c = tx + 16 * j, dist = p.rev ? c - r : r - c;
+                        if (REV ? j < i : j > i) continue;
+                        const int r = ty + 16 * i, c = tx + 16 * j, dist = REV ? c - r : r - c;
                         ps[r * PS + c] = dist >= 0 ? s[i][j] * pw[dist] * p.in_scale : 0.0f;
                     }
                 if (g == 0) {  // the state's part
+#pragma unroll 2
                     for (int k = 0; k < dxp; k += 4) {
                         float4 xv[4], sv[4];
 #pragma unroll
@@ -245,58 +310,79 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = ty + 16 * i, far = p.rev ? t.n - 1 - r : r + 1;
+                        const int r = ty + 16 * i, far = REV ? t.n - 1 - r : r + 1;
                         const float f = r < t.n ? pw[far] : 0.0f;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) o[i][c] *= f;
                     }
                 }
                 __syncthreads();
-                for (int k = 0; k < kTile; k += 4) {
-                    float4 pv[4], zv[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        pv[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * PS + k);
-                        zv[i] = *reinterpret_cast<const float4*>(zs + (k + i) * ZS + tx * 4);
-                    }
+                for (int kb = 0; kb < 4; ++kb)
+#pragma unroll 2
+                    for (int k = 16 * kb; k < 16 * kb + 16; k += 4) {
+                        float4 pv[4], zv[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float pk[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
+                        for (int i = 0; i < 4; ++i) {
+                            if (REV ? kb >= i : kb <= i) pv[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * PS + k);
+                            zv[i] = *reinterpret_cast<const float4*>(zs + (k + i) * ZS + tx * 4);
+                        }
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            o[i][0] = fmaf(pk[m], zv[m].x, o[i][0]);
-                            o[i][1] = fmaf(pk[m], zv[m].y, o[i][1]);
-                            o[i][2] = fmaf(pk[m], zv[m].z, o[i][2]);
-                            o[i][3] = fmaf(pk[m], zv[m].w, o[i][3]);
+                        for (int i = 0; i < 4; ++i) {
+                            if (REV ? kb < i : kb > i) continue;
+                            const float pk[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                o[i][0] = fmaf(pk[m], zv[m].x, o[i][0]);
+                                o[i][1] = fmaf(pk[m], zv[m].y, o[i][1]);
+                                o[i][2] = fmaf(pk[m], zv[m].z, o[i][2]);
+                                o[i][3] = fmaf(pk[m], zv[m].w, o[i][3]);
+                            }
                         }
                     }
-                }
                 if (a == p.gx - 1) {  // every reader of the state is past the barrier above
                     const float keep = g == 0 ? pw[t.n] : 1.0f;
-                    for (int i = ty; i < dxp; i += 16) {
-                        float4 v = *reinterpret_cast<const float4*>(st + i * ZS + tx * 4);
-                        v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
-                        for (int j = 0; j < t.n; ++j) {
-                            const float f = ys[j * ldx + i] * pw[p.rev ? j + 1 : t.n - 1 - j] * p.in_scale;
-                            const float4 z = *reinterpret_cast<const float4*>(zs + j * ZS + tx * 4);
-                            v.x = fmaf(f, z.x, v.x);
-                            v.y = fmaf(f, z.y, v.y);
-                            v.z = fmaf(f, z.z, v.z);
-                            v.w = fmaf(f, z.w, v.w);
+                    float acc[M][4][4];
+#pragma unroll
+                    for (int m = 0; m < M; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 4 * (ty + 16 * m) + i;
+                            float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (r < dxp) u = *reinterpret_cast<const float4*>(st + r * ZS + tx * 4);
+                            acc[m][i][0] = u.x * keep, acc[m][i][1] = u.y * keep, acc[m][i][2] = u.z * keep, acc[m][i][3] = u.w * keep;
                         }
-                        *reinterpret_cast<float4*>(st + i * ZS + tx * 4) = v;
-                    }
+                    add_products<M>(acc, ys, ldx, zs, fs, t.n, dxp);
+#pragma unroll
+                    for (int m = 0; m < M; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 4 * (ty + 16 * m) + i;
+                            if (r < dxp) *reinterpret_cast<float4*>(st + r * ZS + tx * 4) = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
+                        }
                 }
                 __syncthreads();
             }
-            T* out = (T*)p.out + row * p.ldout + (w.h * p.gx + a) * p.dz + z0;
+            const int64_t to = row * p.ldout + (w.h * p.gx + a) * p.dz + z0 + tx * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = ty + 16 * i;
-                if (r < t.n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (tx * 4 + c < zn) lz::st(out + r * p.ldout + tx * 4 + c, o[i][c] * p.out_scale);
+                for (int c = 0; c < 4; ++c) o[i][c] *= p.out_scale;
+                if (r >= t.n) continue;
+                const int64_t at = to + r * p.ldout;
+                if (p.fours) {
+                    if (tx * 4 >= zn) continue;
+                    if (p.f32) Vec<4>::st((float*)p.out + at, o[i]);
+                    else Vec<4>::st((__nv_bfloat16*)p.out + at, o[i]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (tx * 4 + c >= zn) continue;
+                        if (p.f32) lz::st((float*)p.out + at + c, o[i][c]);
+                        else lz::st((__nv_bfloat16*)p.out + at + c, o[i][c]);
+                    }
+                }
             }
         }
         if (t.last && p.fin != nullptr) {
@@ -322,31 +408,30 @@ __global__ void __launch_bounds__(256) decay_empty_kernel(const Seqs s, const fl
     }
 }
 
-size_t ends_smem(int dx) { return sizeof(float) * (size_t)(kTile * ((dx + 3) / 4 * 4 + 4) + kTile * ZS); }
+size_t ends_smem(int dx) { return sizeof(float) * (size_t)(kTile * ((dx + 3) / 4 * 4 + 4) + kTile * ZS + kTile); }
 size_t pass_smem(int dx) {
     const int dxp = (dx + 3) / 4 * 4;
-    return sizeof(float) * (size_t)(2 * kTile * (dxp + 4) + kTile * ZS + kTile * PS + dxp * ZS + kTile + 4);
+    return sizeof(float) * (size_t)(2 * kTile * (dxp + 4) + kTile * ZS + kTile * PS + dxp * ZS + 2 * kTile + 4);
 }
-constexpr size_t kMostSmem = sizeof(float) * (2 * kTile * (192 + 4) + kTile * ZS + kTile * PS + 192 * ZS + kTile + 4);
+constexpr size_t kMostSmem = sizeof(float) * (2 * kTile * (192 + 4) + kTile * ZS + kTile * PS + 192 * ZS + 2 * kTile + 4);
 static_assert(kMostSmem <= 226 * 1024, "within a SM's shared memory");
 
-template <typename T>
 cudaError_t run_ends(const DecayPass& p, float* recs, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.units * (p.nseg - 1) * ((p.dz + ZS - 1) / ZS));
-    const auto kernel = p.dx <= 64 ? decay_ends_kernel<T, 4> : p.dx <= 128 ? decay_ends_kernel<T, 8> : decay_ends_kernel<T, 12>;
-    const size_t sm = ends_smem(p.dx);
+    const auto kernel = p.dx <= 64 ? decay_ends_kernel<1> : p.dx <= 128 ? decay_ends_kernel<2> : decay_ends_kernel<3>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ends_smem(192));
     if (e != cudaSuccess) return e;
-    kernel<<<grid, NT, sm, s>>>(p, recs);
+    kernel<<<grid, NT, ends_smem(p.dx), s>>>(p, recs);
     return cudaGetLastError();
 }
 
-template <typename T>
+template <bool REV>
 cudaError_t run_pass(const DecayPass& p, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.units * p.nseg * ((p.dz + ZS - 1) / ZS));
-    const cudaError_t e = cudaFuncSetAttribute(decay_pass_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
+    const auto kernel = p.dx <= 64 ? decay_pass_kernel<1, REV> : p.dx <= 128 ? decay_pass_kernel<2, REV> : decay_pass_kernel<3, REV>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (e != cudaSuccess) return e;
-    decay_pass_kernel<T><<<grid, NT, pass_smem(p.dx), s>>>(p);
+    kernel<<<grid, NT, pass_smem(p.dx), s>>>(p);
     return cudaGetLastError();
 }
 
@@ -358,25 +443,23 @@ cudaError_t run_join(const DecayPass& p, float* recs, cudaStream_t s) {
 }
 
 // Of two segments of a dense batch the one's end state is the other's first: nothing to join.  On the tensor
-// cores two CTAs share such a segment where that keeps within a CTA a SM.
+// cores two CTAs share such a segment (two segments are cut where there are CTAs for at most half the SMs).
 int parts_of(const DecayArgs& a, const DecayPass& p) {
     if (p.nseg != 2 || a.seqs.cu != nullptr) return 0;
-    return decay_uses_tc(a) && p.units <= 76 ? 2 : 1;
+    return decay_uses_tc(a) ? 2 : 1;
 }
 
 // The states in front of the segments, [units, nseg, dk, dv], from a pass that is not transposed.
 cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, cudaStream_t s) {
     if (p.nseg == 1) return cudaSuccess;
-    const cudaError_t e = decay_uses_tc(a)          ? decay_tc_ends(p, recs, s)
-                          : a.dtype == LIZARD_F32 ? run_ends<float>(p, recs, s)
-                                                  : run_ends<__nv_bfloat16>(p, recs, s);
+    const cudaError_t e = decay_uses_tc(a) ? decay_tc_ends(p, recs, s) : run_ends(p, recs, s);
     if (e != cudaSuccess || p.parts > 0) return e;
     return run_join(p, recs, s);
 }
 
 cudaError_t outputs(const DecayArgs& a, const DecayPass& p, cudaStream_t s) {
     if (decay_uses_tc(a)) return decay_tc_pass(p, s);
-    return a.dtype == LIZARD_F32 ? run_pass<float>(p, s) : run_pass<__nv_bfloat16>(p, s);
+    return p.rev ? run_pass<true>(p, s) : run_pass<false>(p, s);
 }
 
 cudaError_t empty_states(const DecayArgs& a, const float* init, float* fin, cudaStream_t s) {
@@ -397,12 +480,13 @@ cudaError_t own_first_states(const DecayArgs& a, DecayPass* p, float* copy, cuda
     return e;
 }
 
-// Segments of whole tiles: one where sequences, heads and slices already make a CTA a SM, else as many
-// as that takes (fp32 arithmetic: two CTAs a SM).
+// Segments of whole tiles: as many as keep the CTAs, of sequences, heads and slices, within what is resident at
+// a time (fp32 arithmetic: two CTAs a SM where their shared memory allows).
 void cut(const DecayArgs& a, DecayPass* p) {
     const bool tensor = decay_uses_tc(a);
     const int64_t ctas = tensor ? p->units : p->units * ((a.dv + ZS - 1) / ZS), tiles = (a.seqs.L + kTile - 1) / kTile;
-    int64_t n = tensor ? 152 / ctas : ctas >= 152 ? 1 : 304 / ctas;
+    const int64_t room = tensor || 2 * pass_smem((int)(a.dk > a.dv ? a.dk : a.dv)) > 226 * 1024 ? 152 : 304;
+    int64_t n = room / ctas;
     n = n < tiles ? n : tiles;
     n = n < 1 ? 1 : n;
     const int64_t per = (tiles + n - 1) / n;
@@ -418,6 +502,8 @@ DecayPass base_pass(const DecayArgs& a) {
     p.log_decay = a.log_decay;
     p.header = a.header;
     p.in_scale = p.out_scale = 1.0f;
+    p.f32 = a.dtype == LIZARD_F32;
+    p.fours = ((a.dk | a.dv | a.ldq | a.ldk | a.ldv | a.ldo | a.lddq | a.lddk | a.lddv) & 3) == 0;
     cut(a, &p);
     p.parts = parts_of(a, p);
     return p;

@@ -1,17 +1,18 @@
 // Linear attention with a decay for each head on the tensor cores (tcgen05, TMEM and TMA, sm_103a): bf16,
-// keys and values of up to 128 values.
+// keys and values of up to 128 values.  Here are the passes forwards in time, of the outputs and of dq, and the
+// segments' end states; dk and dv have a kernel of their own.
 //
-// One kernel runs every pass (DecayPass: the outputs, dq, and backwards in time dv and dk).  A CTA walks a
-// segment of one state head in chunks.  128 rows of x make an item with 64 of y and z: two query heads of
-// a chunk of 64 tokens, or one head of a chunk of 128 tokens where a state has one head of x (so that the MMAs'
-// 128 rows are used), with 64 of the chunk's tokens of y and z in turn.  With S the state in front of the chunk
-//   P = (X Y^T) (.) e^(l |i - j|), masked to the tokens before (rev: behind),   O = e^(l (i+1)) X S + P Z
+// A CTA walks a segment of one state head in chunks.  128 rows of x make an item with 64 of y and z: two query
+// heads of a chunk of 64 tokens, or one head of a chunk of 128 tokens where a state has one head of x (so that the
+// MMAs' 128 rows are used), with 64 of the chunk's tokens of y and z in turn.  With S the state in front of the chunk
+//   P = (X Y^T) (.) e^(l (i - j)), masked to the tokens up to i,   O = e^(l (i+1)) X S + P Z
 // and a chunk of n tokens moves the state on:  S' = e^(l n) S + Y~^T Z,  Y~[j] = e^(l (n-1-j)) Y[j].
 //
 // The decay of a pair is e^(l (i-r)) e^(l (r-j)) with r in the middle of the chunk: the second factor is a
 // constant for each column of P, the first one scales the finished row of O, and the operand copy of S takes
 // e^(l (r+1)).  Where all of these lie within 2^32 of 1, as they do while a token keeps 0.71 of the state (a
-// half, in chunks of 64), nothing else is needed.  Heads that decay faster take each pair's power of the difference (at most 1) and scale X S before P Z is added.
+// half, in chunks of 64), nothing else is needed.  Heads that decay faster (or grow that much) take each pair's
+// power of the difference and scale X S before P Z is added.
 //
 // Roundings: P and the operand copy of S are bf16 (a relative 2^-8 of the terms, as the output's own).  S itself
 // stays in fp32 in TMEM, and Y~ goes in as a high and a low bf16 part (2^-17), since S leaves the call in fp32
@@ -20,6 +21,12 @@
 // Warps: 0-7 the pairs' weights and the outputs (a thread holds one row's 32 of 64 pairs and 64 of 128 output
 // columns); 8-15 the state (half a row of S to a thread; Y~); 16 the copies; 17 the MMAs of the scores, 18 of
 // the state, 19 of the outputs.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
+//
+// Bound by the chain of a chunk (state out, X S, P Z, state on) and by what its warps issue in it: with 32 query heads
+// on 8 of 128 the walk of 8192 tokens takes 36 us, where its bytes take 25, and that of 65536 takes 214 us, where they
+// take 201.  The loops over a product's steps stay rolled: unrolled by four the
+// longer one takes 39 us more (the code of seven roles shares the SM's instruction cache), and the waits' slow path
+// is one function for the same reason.
 #include "decay_tc.cuh"
 
 namespace lz {
@@ -72,10 +79,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     const bool tall = p.gx == 1;                 // a tile of x: 128 tokens of a head, or 64 of two
     const int chunk = tall ? 128 : 64, mid = chunk / 2 - 1;
     const float l2 = log2_decay(p.log_decay, w.h);
-    const bool slow = l2 * (float)chunk >= -64.0f;  // factors of rows and columns (see above)
+    const bool slow = fabsf(l2) * (float)chunk <= 64.0f;  // factors of rows and columns (see above)
     for (int i = tid; i < 129; i += kThreads) {
         pw[i] = power(l2, i);
-        if (i < 128) col[i] = p.in_scale * power(l2, mid - i);
+        if (i < 128) col[i] = power(l2, mid - i);
     }
     if (tid == 0) {
         for (int i = 0; i < XST; ++i) {
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) {
                                     const int d = i - 32 * cb - c - k;
-                                    v[k] *= pw[d < 0 ? 0 : d] * p.in_scale;
+                                    v[k] *= pw[d < 0 ? 0 : d];
                                 }
                             }
                             if (tq == cb) {  // tokens behind this one are left out whatever they hold

@@ -9,10 +9,11 @@
 //   E' = e^l (what is before the chunk sees) = e^(l n) E + Q~^T dO,   Q~[i] = scale e^(l (i+1)) Q[i]
 // Both gradients share the copies of Q, dO, K, V, the state and its updates, and both are made transposed, so that the
 // MMAs' 128 rows are two heads' tokens or a head's values.  As two passes of the outputs' form (one with dS, one with
-// its transpose) they took 204 us for a training step of 8 x 2048 tokens, 32 heads on 8, 128 values.
+// its transpose) they took 204 us for a training step of 8 x 2048 tokens, 32 heads on 8, 128 values; together 135, of
+// which their bytes take 64: bound by the chain of a chunk and by what the SM's warps issue in it.
 //
 // The decay of a pair is e^(l (i-r)) e^(l (r-j)), r in the middle of the chunk: a factor of the rows of P and one of the
-// finished columns; heads that decay by more than a half a token take each pair's power (see the outputs' kernel, also
+// finished columns; heads that lose more than a half a token take each pair's power (see the outputs' kernel, also
 // for the roundings).
 //
 // Warps: 0-7 pairs and gradients; 8-15 the state (half a row to a thread) and Q~; 16 the copies; 17 the MMAs of the
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     check_offsets(p.seqs, p.header);
     constexpr int mid = 31;
     const float l2 = log2_decay(p.log_decay, w.h);
-    const bool slow = l2 >= -1.0f;
+    const bool slow = fabsf(l2) <= 1.0f;
     for (int i = tid; i <= 64; i += kThreads) {
         pw[i] = power(l2, i);
         if (i < 64) col[i] = slow ? power(l2, mid - i) : 1.0f;

@@ -75,6 +75,7 @@ struct DecayPass {
     int64_t ldx, ldy, ldz, ldv, ldout;
     int dx, dz, gx, gy;
     bool rev, transposed;  // transposed: states in memory are [dz][dx]
+    bool f32, fours;       // fp32 arithmetic: the type, and whether rows allow pieces of four values
     float out_scale, in_scale;
     const float *log_decay, *init;
     float* fin;

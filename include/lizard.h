@@ -618,13 +618,15 @@ size_t lizard_decay_attn_fwd_workspace(const lizard_decay_dims* dims);
  *   S[t] = exp(log_decay[h]) S[t-1] + k[t] v[t]^T,      o[t] = scale q[t] S[t].
  *   q [B, L, Hq, dk];  k [B, L, Hkv, dk];  v [B, L, Hkv, dv];  o [B, L, Hq, dv];
  *   log_decay [Hkv] fp32, at most 0 (constants of the model; minus infinity: a token sees itself
- *            only; above 0 states grow and may overflow);
+ *            only; above 0 states grow, and what overflows is not finite);
  *   s0       [B or nseq, Hkv, dk, dv] fp32 or NULL (zero): the state before each first token;
  *   s_out    likewise or NULL: the state after the last token (s0's, or zero, for an empty
  *            sequence); may be the same array as s0;
  *   workspace, ws_bytes >= lizard_decay_attn_fwd_workspace(dims).
- * A value that is not finite reaches results of its own sequence and state head only, and there
- * those of up to 63 tokens before it (all products of a chunk of 64 tokens are formed). */
+ * A value that is not finite reaches results of its own sequence and state head only, but there also
+ * those of up to 127 tokens before it (all products of a chunk of tokens are formed): what pads a
+ * batch has to be finite.  On the tensor cores terms carry factors of up to 2^32 either way in between:
+ * states and scores beyond 1e28 may overflow there. */
 lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q, const void* k,
                                     const void* v, const float* log_decay, const float* s0,
                                     const int64_t* cu_seqlens, void* o, float* s_out,
