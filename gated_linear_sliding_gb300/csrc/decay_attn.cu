@@ -32,9 +32,10 @@ __device__ __forceinline__ Pieces pieces_of(int n) {
 }
 
 // Rows [0, n) of a tile of `cols` columns as fp32 with row distance `ld` in shared memory; other places 0.
-// Pieces of V values, eight of a thread under way; a function of its own for each kind, not one for each use.
+// Pieces of V values, eight of a thread under way.  (In line: as a function its callers spill, 16 heads on 8 of 128 in
+// fp32, 8 x 1024 tokens, forward and gradients: 2266 against 1949 us.)
 template <typename T, int V>
-__device__ __noinline__ void load_pieces(float* to, int ld, const T* from, int64_t dist, int n, int cols, Pieces q) {
+__device__ __forceinline__ void load_pieces(float* to, int ld, const T* from, int64_t dist, int n, int cols, Pieces q) {
     while (q.r < kTile) {
         float v[8][V];
         int at[8];
@@ -207,7 +208,9 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
     }
 }
 
-// One pass over a segment's tiles, 64 columns of z to a CTA; M: rows of the state by 64.
+// One pass over a segment's tiles, 64 columns of z to a CTA; M: rows of the state by 64.  Bound by the fp32 pipes and
+// the latency between barriers: a thread has 4 x 4 pairs, 4 x 4 outputs and 4 M x 4 of the state, 16 products for each
+// two or three 16-byte reads of shared memory.  8192 tokens of 16 heads on 8, 128 values, fp32: 593 us forwards.
 template <int M, bool REV>
 __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     extern __shared__ float sm[];
