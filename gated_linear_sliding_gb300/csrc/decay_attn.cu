@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
                     for (int j = 0; j < 4; ++j) {
                         if (REV ? j < i : j > i) continue;
                         const int r = ty + 16 * i, c = tx + 16 * j, dist = REV ? c - r : r - c;
-                        ps[r * PS + c] = dist >= 0 ? s[i][j] * pw[dist] * p.in_scale : 0.0f;
+                        // (a token behind the tile's last one is 0 and its power may overflow where a state grows)
+                        ps[r * PS + c] = dist >= 0 && (!REV || c < t.n) ? s[i][j] * pw[dist] * p.in_scale : 0.0f;
                     }
                 if (g == 0) {  // the state's part
 #pragma unroll 2
