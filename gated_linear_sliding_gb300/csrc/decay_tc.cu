@@ -20,7 +20,7 @@
 //
 // Warps: 0-7 the pairs' weights and the outputs (a thread holds one row's 32 of 64 pairs and 64 of 128 output
 // columns); 8-15 the state (half a row of S to a thread; Y~); 16 the copies; 17 the MMAs of the scores, 18 of
-// the state, 19 of the outputs.  TMEM: P and its scores two of 64 columns, O two of 128, S 128.
+// the state, 19 of the outputs.  TMEM: P and its scores two of 64 columns, O 128, S 128, a chunk's part of S 128.
 //
 // Bound by the chain of a chunk (state out, X S, P Z, state on) and by what its warps issue in it: with 32 query heads
 // on 8 of 128 the walk of 8192 tokens takes 36 us, where its bytes take 25, and that of 65536 takes 214 us, where they
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             mbar_init(&p_full[i], 32 * kMathWarps);
             mbar_init(&xs_full[i], 1);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&o_free[i], 32 * kMathWarps);
         }
+        mbar_init(o_free, 32 * kMathWarps);
         mbar_init(kt_full, 32 * kStateWarps);
         mbar_init(h_done, 1);
         mbar_init(st_full, 32 * kStateWarps);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = *tmem_slot;
-    const uint32_t tS = tb, tO = tb + 128, tH = tb + 384;
+    const uint32_t tS = tb, tO = tb + 128, tD = tb + 256, tH = tb + 384;
     const Waiter wait{abort, p.header};
     const int nhx = (p.dx + 63) / 64, nhz = (p.dz + 63) / 64;
     const int kx = (p.dx + 15) / 16;                 // K steps over dx
@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     const int s = it & 1, xs = xt % XST;
                     const uint32_t y = yi + q;
                     const int ys = y % YST;
-                    const uint32_t to = uniform(tO + (xt & 1) * 128);
+                    const uint32_t to = uniform(tO);
                     if (q == 0) {
                         if (!wait.all(&x_full[xs], (xt / XST) & 1, 107)) { ok = false; break; }
-                        if (xt >= 2 && !wait.all(&o_free[xt & 1], ((xt >> 1) & 1) ^ 1, 119)) { ok = false; break; }
+                        if (xt >= 1 && !wait.all(o_free, (xt & 1) ^ 1, 119)) { ok = false; break; }
                         if (a == 0 && !wait.all(st_full, ci & 1, 108)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t xa = uniform(base + SM::X + xs * 4 * kBox);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             for (int q = 0; q < ny; ++q, ++yi) {
                 if (!wait.all(kt_full, yi & 1, 109)) { ok = false; break; }
                 tc_fence_after();
-                state_mmas<1>(leader, tH, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), kBox, id_h, false);
+                state_mmas<1>(leader, tD, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), kBox, id_h, q == 0);
                 if (leader) {
                     mma_commit(h_done);
                     mma_commit(&yz_free[yi % YST]);
@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         if (!ok && yi > 0) mbar_wait(h_done, (yi - 1) & 1, tc::kTimeout);
     } else if (warp >= 8) {
         // the state: half a row of S to a thread
-        const StateRow sr = state_row(p, tH, tid - 32 * kMathWarps);
+        const StateRow sr = state_row(p, tH, tD, tid - 32 * kMathWarps);
+        float keep = 1.0f;  // of the chunk before
         uint32_t yi = 0, ci = 0;
         bool ok = true, was_last = false;
         int was_seq = 0;
@@ -284,10 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             if (ci > 0) {
                 if (!wait.all(h_done, (yi - 1) & 1, 110) || !wait.all(xs_done, (ci - 1) & 1, 111)) { ok = false; break; }
                 tc_fence_after();
-                if (was_last) leave_state(p, sr, w.h, was_seq);
+                if (was_last) leave_state(p, sr, w.h, was_seq, keep);
             }
-            if (t.first || ci == 0) begin_state(p, sr, w, t);
-            pass_state(sr, base + SM::ST, nz, slow ? pw[mid + 1] : 1.0f, pw[t.n]);
+            const bool fresh = t.first || ci == 0;
+            if (fresh) begin_state(p, sr, w, t);
+            pass_state(sr, base + SM::ST, nz, slow ? pw[mid + 1] : 1.0f, fresh, keep);
+            keep = pw[t.n];
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(st_full);
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         if (ok && ci > 0 && was_last && p.fin != nullptr) {
             if (wait.all(h_done, (yi - 1) & 1, 114)) {
                 tc_fence_after();
-                leave_state(p, sr, w.h, was_seq);
+                leave_state(p, sr, w.h, was_seq, keep);
             }
         }
     } else {
@@ -326,137 +329,117 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         const float rowf = p.out_scale * (slow ? power(l2, i - mid) : 1.0f);
         const f2 rowf2 = pack(rowf, rowf);
         const uint32_t c0 = base + SM::TABLE + 132 * 4;
-        bool have = walk.next(p.seqs, w.b, &t);
+        // an item's weights; the outputs of a tile of x as soon as its products are done, since the next one's X S waits for
+        // their place (65536 tokens: 284 us, 308 with the next item's weights before them)
         uint32_t it = 0, xt = 0;
-        int a = 0, q = 0;
-        // the tile whose outputs are still to be stored
-        bool held = false, held_live = false;
-        int held_n = 0, held_head = 0, held_t0 = 0;
-        // an item's weights, then the outputs of the tile of x before, whose products end meanwhile
-        while (true) {
+        bool ok = true;
+        while (ok && walk.next(p.seqs, w.b, &t)) {
             const int ny = t.n > 64 ? 2 : 1;
-            const bool live = tall ? 32 * tq < t.n : 2 * a + slot < p.gx;
-            if (have) {
-                const int s = it & 1, cb = 2 * q + half;  // block of the columns
-                if (!wait.all(&s_full[s], (it >> 1) & 1, 116)) break;
-                tc_fence_after();
-                if (live) {
-                    const uint32_t at = tS + s * 64 + lanes + half * 32;
-                    #pragma unroll 1
-                    for (int c = 0; c < 32; c += 16) {
-                        uint32_t o[8];
-                        if (tq < cb) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = 0;
-                        } else {
-                            float v[16];
-                            tmem_ld16(at + c, v);
-                            tmem_wait_ld();
-                            if (slow) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    uint32_t f[4];
-                                    ld_shared_v4(c0 + (32 * cb + c + 4 * k) * 4, f[0], f[1], f[2], f[3]);
-#pragma unroll
-                                    for (int m = 0; m < 2; ++m)
-                                        unpack(mul2(pack(v[4 * k + 2 * m], v[4 * k + 2 * m + 1]), pack(__uint_as_float(f[2 * m]), __uint_as_float(f[2 * m + 1]))),
-                                               v[4 * k + 2 * m], v[4 * k + 2 * m + 1]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    const int d = i - 32 * cb - c - k;
-                                    v[k] *= pw[d < 0 ? 0 : d];
-                                }
-                            }
-                            if (tq == cb) {  // tokens behind this one are left out whatever they hold
-                                const int last = lane - c;
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-                        }
-                        tmem_st8(at + c / 2, o);  // over scores that this thread has read
-                    }
-                }
-                if (!slow && q == 0) {  // e^(l (i+1)) X S
-                    if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) break;
+            for (int a = 0; a < ntx && ok; ++a, ++xt) {
+                const bool live = tall ? 32 * tq < t.n : 2 * a + slot < p.gx;
+                const int head = (int)(w.h * p.gx) + (tall ? 0 : 2 * a + slot);
+                for (int q = 0; q < ny; ++q, ++it) {
+                    const int s = it & 1, cb = 2 * q + half;  // block of the columns
+                    if (!wait.all(&s_full[s], (it >> 1) & 1, 116)) { ok = false; break; }
                     tc_fence_after();
-                    if (live && z_on) {
-                        const float f = i < t.n ? pw[i + 1] : 0.0f;
+                    if (live) {
+                        const uint32_t at = tS + s * 64 + lanes + half * 32;
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 16) {
-                            float v[16];
-                            tmem_ld16(tO + (xt & 1) * 128 + lanes + 64 * half + c, v);
-                            tmem_wait_ld();
+                        for (int c = 0; c < 32; c += 16) {
+                            uint32_t o[8];
+                            if (tq < cb) {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] *= f;
-                            tmem_st16(tO + (xt & 1) * 128 + lanes + 64 * half + c, reinterpret_cast<const uint32_t*>(v));
+                                for (int k = 0; k < 8; ++k) o[k] = 0;
+                            } else {
+                                float v[16];
+                                tmem_get16(at + c, v);
+                                if (slow) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        uint32_t f[4];
+                                        ld_shared_v4(c0 + (32 * cb + c + 4 * k) * 4, f[0], f[1], f[2], f[3]);
+#pragma unroll
+                                        for (int m = 0; m < 2; ++m)
+                                            unpack(mul2(pack(v[4 * k + 2 * m], v[4 * k + 2 * m + 1]), pack(__uint_as_float(f[2 * m]), __uint_as_float(f[2 * m + 1]))),
+                                                   v[4 * k + 2 * m], v[4 * k + 2 * m + 1]);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        const int d = i - 32 * cb - c - k;
+                                        v[k] *= pw[d < 0 ? 0 : d];
+                                    }
+                                }
+                                if (tq == cb) {  // tokens behind this one are left out whatever they hold
+                                    const int last = lane - c;
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
+                                }
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) o[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+                            }
+                            tmem_st8(at + c / 2, o);  // over scores that this thread has read
                         }
                     }
+                    if (!slow && q == 0) {  // e^(l (i+1)) X S
+                        if (!wait.all(&xs_full[xt & 1], (xt >> 1) & 1, 117)) { ok = false; break; }
+                        tc_fence_after();
+                        if (live && z_on) {
+                            const float f = i < t.n ? pw[i + 1] : 0.0f;
+#pragma unroll 1
+                            for (int c = 0; c < 64; c += 16) {
+                                float v[16];
+                                tmem_get16(tO + lanes + 64 * half + c, v);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) v[k] *= f;
+                                tmem_st16(tO + lanes + 64 * half + c, reinterpret_cast<const uint32_t*>(v));
+                            }
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[s]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&p_full[s]);
-            }
-            if (held) {  // item it - 1 was the last of tile xt - 1
-                const uint32_t hx = xt - 1, hi = it - 1;
-                if (!wait.all(&pv_done[hi & 1], (hi >> 1) & 1, 115)) break;
+                if (!ok) break;
+                const uint32_t last = it - 1;  // of the tile's items
+                if (!wait.all(&pv_done[last & 1], (last >> 1) & 1, 115)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t stage = base + SM::OUT + half * kHalf + quad * 4096;
-                const bool out_live = held_live && z_on;  // one answer for a warp
+                const bool out_live = live && z_on;  // one answer for a warp
                 if (out_live) {
                     if (lane == 0) bulk_wait_read();  // the rows before have left
                     __syncwarp();
 #pragma unroll 1
                     for (int c = 0; c < 64; c += 16) {
                         float v[16];
-                        tmem_ld16(tO + (hx & 1) * 128 + lanes + 64 * half + c, v);
-                        tmem_wait_ld();
+                        tmem_get16(tO + lanes + 64 * half + c, v);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) st_scaled8(stage + sw128(lane, (c >> 3) + k), v + 8 * k, rowf2);
                     }
                     fence_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(&o_free[hx & 1]);
+                mbar_arrive(o_free);
                 __syncwarp();
                 if (out_live) {
-                    if (32 * tq + 32 <= held_n) {
+                    if (32 * tq + 32 <= t.n) {
                         if (lane == 0) {
-                            tma_store_3d(&g.out, sm + SM::OUT + half * kHalf + quad * 4096, 64 * half, held_head, (int)(w.b * p.seqs.L) + held_t0 + 32 * tq);
+                            tma_store_3d(&g.out, sm + SM::OUT + half * kHalf + quad * 4096, 64 * half, head, (int)(w.b * p.seqs.L) + t.t0 + 32 * tq);
                             bulk_commit();
                         }
-                    } else if (32 * tq < held_n) {
+                    } else if (32 * tq < t.n) {
                         const int c = lane & 7;
-                        __nv_bfloat16* out = (__nv_bfloat16*)p.out + (w.b * p.seqs.L + held_t0) * p.ldout + (int64_t)held_head * p.dz + 64 * half + 8 * c;
+                        __nv_bfloat16* out = (__nv_bfloat16*)p.out + (w.b * p.seqs.L + t.t0) * p.ldout + (int64_t)head * p.dz + 64 * half + 8 * c;
                         if (64 * half + 8 * c < p.dz) {
 #pragma unroll 1
                             for (int k = 0; k < 8; ++k) {
                                 const int row = 4 * k + (lane >> 3), tok = 32 * tq + row;
                                 uint32_t v[4];
                                 ld_shared_v4(stage + sw128(row, c), v[0], v[1], v[2], v[3]);
-                                if (tok < held_n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
+                                if (tok < t.n) *reinterpret_cast<uint4*>(out + tok * p.ldout) = make_uint4(v[0], v[1], v[2], v[3]);
                             }
                         }
                     }
-                }
-                held = false;
-            }
-            if (!have) break;
-            ++it;
-            if (++q == ny) {
-                q = 0;
-                held = true;
-                held_live = live;
-                held_n = t.n;
-                held_head = (int)(w.h * p.gx) + (tall ? 0 : 2 * a + slot);
-                held_t0 = t.t0;
-                ++xt;
-                if (++a == ntx) {
-                    a = 0;
-                    have = walk.next(p.seqs, w.b, &t);
                 }
             }
         }
@@ -473,9 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 // ------------------------------------------------------------------------- segments' end states
 
 // A segment's own contribution to the state that leaves it, from all tokens that reach it, each with its
-// whole power of the decay: S stays in TMEM and nothing is scaled on the way.  Two groups of eight warps make
-// Y~ in turn, warp 16 copies, warp 17 issues the MMAs.
-constexpr int kEndsThreads = 576, kEndsStages = 4;
+// whole power of the decay: nothing is scaled on the way.  Two groups of eight warps make Y~ in turn, warp 16
+// copies, warp 17 issues the MMAs; they sum four tiles from zero in one of two places in TMEM, and all sixteen warps
+// add that to the sum in their registers (see StateRow) two places later.
+constexpr int kEndsThreads = 576, kEndsStages = 4, kEndsBatch = 4;
 struct EndsSmem {
     static constexpr uint32_t YZ = 0;
     static constexpr uint32_t KT = kEndsStages * 4 * kBox;
@@ -491,8 +475,8 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + EndsSmem::BARS);
-    uint64_t *yz_full = bar, *yz_free = bar + 4, *kt_full = bar + 8, *kt_free = bar + 10, *done = bar + 12;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 13);
+    uint64_t *yz_full = bar, *yz_free = bar + 4, *kt_full = bar + 8, *kt_free = bar + 10, *summed = bar + 12, *taken = bar + 14, *drained = bar + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 17);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Seg w = seg_of<true>(p);
@@ -506,13 +490,15 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
         for (int i = 0; i < 2; ++i) {
             mbar_init(&kt_full[i], 256);
             mbar_init(&kt_free[i], 1);
+            mbar_init(&summed[i], 1);
+            mbar_init(&taken[i], 512);
         }
-        mbar_init(done, 1);
+        mbar_init(drained, 1);
         *abort = 0;
         fence_mbar_init();
     }
     if (warp == 17) {
-        tmem_alloc(tmem_slot, 128);
+        tmem_alloc(tmem_slot, 256);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -560,24 +546,44 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
         uint32_t it = 0;
         for (; it < items; ++it) {
             const int k = it & 1;
+            const uint32_t b = it / kEndsBatch, at = it % kEndsBatch;
             if (!wait.all(&kt_full[k], (it >> 1) & 1, 121)) break;
+            if (at == 0 && b >= 2 && !wait.all(&taken[b & 1], ((b >> 1) & 1) ^ 1, 125)) break;
             tc_fence_after();
-            state_mmas<8>(leader, tb, uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
-                       it == 0);
+            state_mmas<8>(leader, uniform(tb + (b & 1) * 128), uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
+                       at == 0);
             if (leader) {
                 mma_commit(&kt_free[k]);
                 mma_commit(&yz_free[it % kEndsStages]);
+                if (at == kEndsBatch - 1 || it == items - 1) mma_commit(&summed[b & 1]);
             }
         }
-        if (leader) mma_commit(done);
-        if (it < items) mbar_wait(done, 0, tc::kTimeout);
+        if (it < items) {
+            if (leader) mma_commit(drained);
+            mbar_wait(drained, 0, tc::kTimeout);
+        }
     } else {
         const int group = warp >> 3, in = tid & 255, tok = in & 63;
-        uint32_t it = 0;
+        const int c = 32 * (warp >> 2);  // 32 of a row's columns
+        float sum[32] = {};
+        uint32_t it = 0, b = 0;  // items, batches added to the sum
+        auto take = [&]() {
+            if (!wait.all(&summed[b & 1], (b >> 1) & 1, 124)) return false;
+            tc_fence_after();
+            float v[32];
+            tmem_get32(tb + (b & 1) * 128 + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sum[k] += v[k];
+            tc_fence_before();
+            mbar_arrive(&taken[b & 1]);
+            ++b;
+            return true;
+        };
         bool ok = true;
         for (int64_t t0 = r.from; t0 < r.to && ok; t0 += kTile) {
             const int n = (int)min64(kTile, r.to - t0);
             for (int gh = 0; gh < p.gy; ++gh, ++it) {
+                if (it >= (b + 2) * kEndsBatch && !take()) { ok = false; break; }
                 if ((int)(it & 1) != group) continue;
                 const int s = it % kEndsStages;
                 if (!wait.all(&yz_full[s], (it / kEndsStages) & 1, 122)) { ok = false; break; }
@@ -585,31 +591,23 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 const float f = tok < n ? power(l2, rev ? t0 + tok - begin + 1 : end - 1 - t0 - tok) * p.in_scale : 0.0f;
                 const uint32_t ya = base + EndsSmem::YZ + s * 4 * kBox;
                 if (n < 64) clear_rows<256>(ya + 2 * kBox, kBox, n, in);
-                scale_rows<4, 4>(ya, kBox, base + EndsSmem::KT + group * 4 * kBox, 2 * ((p.dx + 15) / 16), n, f, in);
+                scale_rows<4, 2>(ya, kBox, base + EndsSmem::KT + group * 4 * kBox, 2 * ((p.dx + 15) / 16), n, f, in);
                 fence_async_smem();
                 mbar_arrive(&kt_full[group]);
             }
         }
-        if (ok && wait.all(done, 0, 124)) {
-            tc_fence_after();
+        while (ok && b * kEndsBatch < items) ok = take();
+        if (ok) {
             const int row = 32 * (warp & 3) + lane;
             const int64_t size = (int64_t)p.dx * p.dz;
             float* to = recs + (w.unit * p.nseg + (p.parts > 0 ? (int)(blockIdx.x / p.units) : w.seg)) * size + (int64_t)row * p.dz;
             const float* from = r.whole && p.init != nullptr ? p.init + (r.seq * p.Hkv + w.h) * size + (int64_t)row * p.dz : nullptr;
             const float f = from != nullptr ? power(l2, end - begin) : 0.0f;
-            const int c = 32 * (warp >> 2);  // 32 of the row's columns
-            float v[32];
-            tmem_ld32(tb + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
-            tmem_wait_ld();
-            if (items == 0) {  // a half without tokens
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = 0.0f;
-            }
             if (row < p.dx) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     if (c + k >= p.dz) continue;
-                    float4 u = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    float4 u = make_float4(sum[k], sum[k + 1], sum[k + 2], sum[k + 3]);
                     if (from != nullptr) {
                         const float4 i = *reinterpret_cast<const float4*>(from + c + k);
                         u.x = fmaf(f, i.x, u.x), u.y = fmaf(f, i.y, u.y), u.z = fmaf(f, i.z, u.z), u.w = fmaf(f, i.w, u.w);
@@ -623,7 +621,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
     __syncthreads();
     if (warp == 17) {
         tc_fence_after();
-        tmem_dealloc(tb, 128);
+        tmem_dealloc(tb, 256);
     }
 }
 

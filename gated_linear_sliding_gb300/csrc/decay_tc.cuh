@@ -118,7 +118,7 @@ __device__ __forceinline__ void mma_bf16_ts_one(bool leader, uint32_t d_tmem, ui
         : "memory");
 }
 
-// S += Y~^T Z over a tile's 64 tokens, both parts; by a warp.  z's second 64 columns lie `apart` bytes behind the first.
+// D += Y~^T Z over a tile's 64 tokens, both parts; by a warp.  z's second 64 columns lie `apart` bytes behind the first.
 template <int UNROLL>
 __device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, uint32_t zs, uint32_t apart, uint32_t idesc, bool fresh) {
 #pragma unroll UNROLL
@@ -138,30 +138,43 @@ __device__ __forceinline__ void st_scaled8(uint32_t to, const float* v, f2 f) {
     st_shared_v4(to, w[0], w[1], w[2], w[3]);
 }
 
-// A thread of the state's warps: row `row` of S, columns [z0, z1) of its half, at `at` in TMEM.
+// The MMAs cut an fp32 accumulator off (towards zero) with every 16 rows that they add: a state they added to directly
+// lost 3e-4 of its size in 65536 tokens without a decay.  So a chunk's products are summed from zero (D), and fp32
+// instructions, which round to nearest, add them to the state: S' = e^(l n) S + D.
+//
+// A thread of the state's warps: row `row` of S, columns [z0, z1) of its half, at `at` in TMEM; D's at `sum`.
 struct StateRow {
     int in, row, z0, z1;
-    uint32_t at;
+    uint32_t at, sum;
 };
-__device__ __forceinline__ StateRow state_row(const DecayPass& p, uint32_t tH, int in) {
+__device__ __forceinline__ StateRow state_row(const DecayPass& p, uint32_t tH, uint32_t tD, int in) {
     StateRow r;
     r.in = in;
     r.row = in & 127;
     r.z0 = (in >> 7) * 64;
     r.z1 = min(r.z0 + 64, p.dz);
     r.at = tH + ((uint32_t)(in & 96) << 16);
+    r.sum = r.at + tD - tH;
     return r;
 }
 
+// 16 columns of the state behind a chunk that keeps `keep` of the state in front of it.
+__device__ __forceinline__ void state_behind(const StateRow& r, int c, f2 keep, float* v) {
+    float d[16];
+    tmem_get16(r.at + c, v);
+    tmem_get16(r.sum + c, d);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) unpack(fma2(pack(v[i], v[i + 1]), keep, pack(d[i], d[i + 1])), v[i], v[i + 1]);
+}
+
 // The state behind a sequence's last tile (a pass whose states are transposed leaves none).
-__device__ __forceinline__ void leave_state(const DecayPass& p, const StateRow& r, int64_t h, int seq) {
+__device__ __forceinline__ void leave_state(const DecayPass& p, const StateRow& r, int64_t h, int seq, float keep) {
     if (p.fin == nullptr) return;
     float* to = p.fin + ((seq * p.Hkv + h) * p.dx + r.row) * (int64_t)p.dz;
 #pragma unroll 1
     for (int c = r.z0; c < r.z1; c += 16) {
         float v[16];
-        tmem_ld16(r.at + c, v);
-        tmem_wait_ld();
+        state_behind(r, c, pack(keep, keep), v);
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
             if (r.row < p.dx && c + i < r.z1) *reinterpret_cast<float4*>(to + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -189,8 +202,7 @@ __device__ __forceinline__ void fetch_state(const DecayPass& p, const StateRow& 
         }
         if (add) {
             float old[32];
-            tmem_ld32(r.at + c, old);
-            tmem_wait_ld();
+            tmem_get32(r.at + c, old);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] += old[i];
         }
@@ -210,19 +222,21 @@ __device__ __forceinline__ void begin_state(const DecayPass& p, const StateRow& 
     for (int k = 0; k < parts; ++k) fetch_state(p, r, k == 0 ? from : from + size, k > 0);
 }
 
-// The operand copy of the state (times `seen`) to shared memory, and the state decayed over the tile's tokens.
-__device__ __forceinline__ void pass_state(const StateRow& r, uint32_t st, int nz, float seen, float keep) {
+// The state in front of a chunk (fresh: as it was fetched, else behind the chunk before), and its operand copy (times
+// `seen`) to shared memory.
+__device__ __forceinline__ void pass_state(const StateRow& r, uint32_t st, int nz, float seen, bool fresh, float keep) {
     const f2 keep2 = pack(keep, keep), seen2 = pack(seen, seen);
 #pragma unroll 1
     for (int c = r.z0; c < r.z0 + 64 && c < nz; c += 16) {
         float v[16];
-        tmem_ld16(r.at + c, v);
-        tmem_wait_ld();
+        if (fresh) {
+            tmem_get16(r.at + c, v);
+        } else {
+            state_behind(r, c, keep2, v);
+            tmem_st16(r.at + c, reinterpret_cast<const uint32_t*>(v));
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) st_scaled8(st + (c >> 6) * kHalf + sw128(r.row, ((c & 63) >> 3) + i), v + 8 * i, seen2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) unpack(mul2(pack(v[2 * i], v[2 * i + 1]), keep2), v[2 * i], v[2 * i + 1]);
-        tmem_st16(r.at + c, reinterpret_cast<const uint32_t*>(v));
     }
     tmem_wait_st();
 }

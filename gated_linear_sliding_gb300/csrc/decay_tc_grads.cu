@@ -17,8 +17,8 @@
 // for the roundings).
 //
 // Warps: 0-7 pairs and gradients; 8-15 the state (half a row to a thread) and Q~; 16 the copies; 17 the MMAs of the
-// scores, 18 those into the state, 19 those of the gradients.  TMEM: two scores of 64 columns, twice two gradients of
-// 64, the state 128.
+// scores, 18 those into the state, 19 those of the gradients.  TMEM: two scores of 64 columns, two gradients of 64, the
+// state 128, a chunk's part of it 128.
 #include "decay_tc.cuh"
 
 namespace lz {
@@ -34,8 +34,8 @@ struct GradArgs {
 // Tiles of Q and dO take turns in three places of 128 rows, or, with one query head a state, in four of 64.  With two
 // items or more in a chunk the last one's dO goes where the state's operand copy was, which is read at a chunk's
 // beginning and written behind its last item: three places alone had dO wait for the item before (164 us for the
-// training step above).  With one query head the gradients leave through a place of their own, after the next chunk's
-// pairs have been weighed; otherwise through that of P, before.
+// training step above).  With one query head the gradients leave through a place of their own, otherwise through that
+// of P.
 struct GradSmem {
     static constexpr uint32_t RING = 0;
     static constexpr uint32_t KV = 12 * kBox;         // K, V: 64 rows each
@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BARS);
     uint64_t *b_full = bar, *b_free = bar + 6, *kv_full = bar + 12, *kv_free = bar + 13, *s_full = bar + 14, *p_full = bar + 15, *pv_done = bar + 16,
              *xs_full = bar + 17, *o_free = bar + 19, *zz_full = bar + 21, *kt_full = bar + 23, *h_done = bar + 24, *st_full = bar + 25,
-             *xs_done = bar + 26, *staged = bar + 27, *left = bar + 28, *late = bar + 29, *drained = bar + 30;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 33);
+             *xs_done = bar + 26, *staged = bar + 27, *left = bar + 28, *late = bar + 29, *drained = bar + 30, *chunk_done = bar + 33;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 34);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
@@ -86,11 +86,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         mbar_init(s_full, 1);
         mbar_init(p_full, 32 * kMathWarps);
         mbar_init(pv_done, 1);
+        mbar_init(chunk_done, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&xs_full[i], 1);
-            mbar_init(&o_free[i], 32 * kMathWarps);
             mbar_init(&zz_full[i], 32 * kStateWarps);
         }
+        mbar_init(o_free, 32 * kMathWarps);
         mbar_init(kt_full, 32 * kStateWarps);
         mbar_init(h_done, 1);
         mbar_init(st_full, 32 * kStateWarps);
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = *tmem_slot;
-    const uint32_t tS = tb, tO = tb + 128, tH = tb + 384;
+    const uint32_t tS = tb, tO = tb + 128, tD = tb + 256, tH = tb + 384;
     const Waiter wait{abort, p.header};
     const int kx = (p.dx + 15) / 16, kz = (p.dz + 15) / 16, nz = 16 * kz;
     const int nt = (p.gy + 1) / 2;  // items of a chunk: two query heads, or one
@@ -206,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         uint32_t it = 0, ci = 0, q = 0;
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
-            const uint32_t to = uniform(tO + (ci & 1) * 128);
-            if (!wait.all(kv_full, ci & 1, 136) || (ci >= 2 && !wait.all(&o_free[ci & 1], ((ci >> 1) & 1) ^ 1, 137)) || !wait.all(st_full, ci & 1, 138)) {
+            const uint32_t to = uniform(tO);
+            if (!wait.all(kv_full, ci & 1, 136) || (ci >= 1 && !wait.all(o_free, (ci & 1) ^ 1, 137)) || !wait.all(st_full, ci & 1, 138)) {
                 ok = false;
                 break;
             }
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 }
                 if (leader) {
                     mma_commit(pv_done);
+                    if (a == nt - 1) mma_commit(chunk_done);
                     mma_commit(&b_free[q % places]);
                     if (!is_late(a)) mma_commit(&b_free[(q + 1) % places]);
                 }
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 for (int k = 0; k < heads; ++k, ++ui) {
                     if (!wait.all(kt_full, ui & 1, 141)) { ok = false; break; }
                     tc_fence_after();
-                    state_mmas<1>(leader, tH, base + SM::KT, oa + k * kBox, apart, id_h, false);
+                    state_mmas<1>(leader, tD, base + SM::KT, oa + k * kBox, apart, id_h, a == 0 && k == 0);
                     if (leader) mma_commit(h_done);
                 }
                 if (ok && leader) {
@@ -277,23 +279,28 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         }
     } else if (warp >= kMathWarps) {
         // the state: half a row of E to a thread
-        const StateRow sr = state_row(p, tH, tid - 32 * kMathWarps);
+        const StateRow sr = state_row(p, tH, tD, tid - 32 * kMathWarps);
+        float keep = 1.0f;  // of the chunk before
         uint32_t it = 0, ui = 0, ci = 0, q = 0;
         bool ok = true, was_last = false;
         int was_seq = 0;
         grid_dep_wait();
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (ci > 0) {
-                // (a late dO lies where the state's copy goes: the gradients' products are done with it)
-                if (!wait.all(h_done, (ui - 1) & 1, 142) || !wait.all(xs_done, (ci - 1) & 1, 143) || !wait.all(pv_done, (it - 1) & 1, 156)) {
+                // (a late dO lies where the state's copy goes: the gradients' products are done with it.  A wait names
+                // one of a barrier's last two phases, so these warps, which do not see every item's, have a barrier of
+                // the chunks.)
+                if (!wait.all(h_done, (ui - 1) & 1, 142) || !wait.all(xs_done, (ci - 1) & 1, 143) || !wait.all(chunk_done, (ci - 1) & 1, 156)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (was_last) leave_state(p, sr, w.h, was_seq);
+                if (was_last) leave_state(p, sr, w.h, was_seq, keep);
             }
-            if (t.first || ci == 0) begin_state(p, sr, w, t);
-            pass_state(sr, base + SM::ST, nz, slow ? power(l2, t.n - 1 - mid) : 1.0f, pw[t.n]);
+            const bool fresh = t.first || ci == 0;
+            if (fresh) begin_state(p, sr, w, t);
+            pass_state(sr, base + SM::ST, nz, slow ? power(l2, t.n - 1 - mid) : 1.0f, fresh, keep);
+            keep = pw[t.n];
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(st_full);
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         if (ok && ci > 0 && was_last && p.fin != nullptr) {
             if (wait.all(h_done, (ui - 1) & 1, 147)) {
                 tc_fence_after();
-                leave_state(p, sr, w.h, was_seq);
+                leave_state(p, sr, w.h, was_seq, keep);
             }
         }
     } else {
@@ -340,9 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
 #pragma unroll
         for (int k = 0; k < 8; ++k) sw[k] = (((r & 63) >> 3) ^ k) << 4;
         uint32_t it = 0, ci = 0;
-        int held_t0 = 0, held_n = 0;  // the chunk whose gradients are still to leave
         const uint32_t stage = single ? SM::OWN : SM::PP;
-        bool have = true, held = false;
         // this warp's part of the gradients before has left the place that is written next
         auto vacant = [&]() {
             __syncwarp();
@@ -351,134 +356,117 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 mbar_arrive(left);
             }
         };
-        uint32_t out = 0;  // chunks whose gradients have left
-        while (true) {
-            have = walk.next(p.seqs, w.b, &t);
-            if (have) {
-                const uint32_t acc = tO + (ci & 1) * 128 + lanes + 32 * half;
-                if (!slow) {  // e^(l (n-1-j)) on the state's parts
-                    if (!wait.all(&xs_full[ci & 1], (ci >> 1) & 1, 148)) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 128; c += 16) {
-                        if ((c & 63) >= 32) continue;
-                        float v[16];
-                        tmem_ld16(acc + c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int far = t.n - 1 - 32 * half - (c & 63) - k;
-                            v[k] = far >= 0 ? v[k] * pw[far] : 0.0f;
-                        }
-                        tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(v));
-                    }
-                    tmem_wait_st();
-                }
-                bool ok = true;
-                for (int a = 0; a < nt; ++a, ++it) {
-                    const bool on = 2 * a + (quad >> 1) < p.gy;
-                    if (!wait.all(s_full, it & 1, 149)) { ok = false; break; }
-                    // the place of P is free: its MMAs are done, and a chunk's gradients have left it
-                    if (it >= 1 && !wait.all(pv_done, (it - 1) & 1, 150)) { ok = false; break; }
-                    if (!single && a == 0 && ci >= 1) {
-                        vacant();
-                        if (!wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
-                    }
-                    tc_fence_after();
-                    if (on) {
-#pragma unroll 1
-                        for (int c = 0; c < 128; c += 16) {  // 32 columns of P, then of P'
-                            if ((c & 63) >= 32) continue;
-                            const int j = 32 * half + (c & 63);
-                            const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox;
-                            float v[16];
-                            tmem_ld16(tS + lanes + 32 * half + c, v);
-                            tmem_wait_ld();
-                            if (!slow) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) v[k] *= pw[i - j - k < 0 ? 0 : i - j - k];
-                            }
-                            if (tq <= half || t.n < 64) {  // tokens before the column's, and behind the last one, are left out whatever they hold
-                                const int last = i < t.n ? i - j : -1;
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
-                            }
-                            const f2 f = pack(rowf, rowf);
-                            st_scaled8(to + sw128(r, (j >> 3)), v, f);
-                            st_scaled8(to + sw128(r, (j >> 3) + 1), v + 8, f);
-                        }
-                        fence_async_smem();
-                    }
-                    tc_fence_before();
-                    mbar_arrive(p_full);
-                }
-                if (!ok) break;
-                ++ci;
-            }
-            // a chunk's gradients: value r of tokens 32 half .. + 31, to rows of 128 values
-            const bool leaves = single ? held : have;
-            if (leaves) {
-                if (!single) held_t0 = t.t0, held_n = t.n;
-                // (its products: with the next chunk's pairs weighed, they have been waited for)
-                if (!(single && have) && !wait.all(pv_done, (it - 1) & 1, 152)) break;
-                if (single && out >= 1) {
-                    vacant();
-                    if (!wait.all(left, (out - 1) & 1, 157)) break;
-                }
+        const uint32_t acc = tO + lanes + 32 * half;
+        while (walk.next(p.seqs, w.b, &t)) {
+            if (!slow) {  // e^(l (n-1-j)) on the state's parts
+                if (!wait.all(&xs_full[ci & 1], (ci >> 1) & 1, 148)) break;
                 tc_fence_after();
-                const uint32_t acc = tO + (out & 1) * 128 + lanes + 32 * half;
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 16) {
                     if ((c & 63) >= 32) continue;
-                    const int j = 32 * half + (c & 63);
-                    const uint32_t to = base + stage + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 7) * 2 + j * 128;
                     float v[16];
-                    tmem_ld16(acc + c, v);
-                    tmem_wait_ld();
+                    tmem_get16(acc + c, v);
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {  // single values: 32 lanes make half a row
-                        uint32_t f[4];
-                        ld_shared_v4(c0 + (j + k) * 4, f[0], f[1], f[2], f[3]);
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v[k + m] * __uint_as_float(f[m])));
-                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + sw[(k + m) & 7] + (k + m) * 128), "h"(h) : "memory");
-                        }
+                    for (int k = 0; k < 16; ++k) {
+                        const int far = t.n - 1 - 32 * half - (c & 63) - k;
+                        v[k] = far >= 0 ? v[k] * pw[far] : 0.0f;
                     }
+                    tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(v));
                 }
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(&o_free[out & 1]);
-                mbar_arrive(staged);
-                if (!wait.all(staged, out & 1, 153)) break;
-                // a warp to each 64 values of dv and dk, or, of fewer than 64 tokens, rows by all of them
-                const int row = (int)(w.b * p.seqs.L) + held_t0;
-                if (held_n == 64) {
-                    const int e = warp >> 1, h = warp & 1;
-                    if (warp < 4 && h < (e == 0 ? nhz : nhx) && lane == 0) {
-                        tma_store_3d(e == 0 ? &g.dv : &g.dk, sm + stage + e * 2 * kBox + h * kBox, 64 * h, (int)w.h, row);
-                        bulk_commit();
-                    }
-                } else {
-#pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
-                        const int d = e == 0 ? p.dz : p.dx;
-                        const int64_t ld = e == 0 ? g.lddv : g.lddk;
-                        __nv_bfloat16* out = (__nv_bfloat16*)(e == 0 ? g.dv_out : g.dk_out) + (w.b * p.seqs.L + held_t0) * ld + w.h * d;
-#pragma unroll 1
-                        for (int c = tid; c < held_n * 16; c += 32 * kMathWarps) {
-                            const int tok = c >> 4, piece = c & 15;
-                            uint32_t v[4];
-                            ld_shared_v4(base + stage + e * 2 * kBox + (piece >> 3) * kBox + sw128(tok, piece & 7), v[0], v[1], v[2], v[3]);
-                            if (8 * piece < d) *reinterpret_cast<uint4*>(out + tok * ld + 8 * piece) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    }
-                }
-                ++out;
+                tmem_wait_st();
             }
-            if (!have) break;
-            held = true;
-            held_t0 = t.t0, held_n = t.n;
+            bool ok = true;
+            for (int a = 0; a < nt; ++a, ++it) {
+                const bool on = 2 * a + (quad >> 1) < p.gy;
+                if (!wait.all(s_full, it & 1, 149)) { ok = false; break; }
+                // the place of P is free: its MMAs are done, and a chunk's gradients have left it
+                if (it >= 1 && !wait.all(pv_done, (it - 1) & 1, 150)) { ok = false; break; }
+                if (!single && a == 0 && ci >= 1) {
+                    vacant();
+                    if (!wait.all(left, (ci - 1) & 1, 151)) { ok = false; break; }
+                }
+                tc_fence_after();
+                if (on) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {  // 32 columns of P, then of P'
+                        if ((c & 63) >= 32) continue;
+                        const int j = 32 * half + (c & 63);
+                        const uint32_t to = base + SM::PP + (c >> 6) * 2 * kBox;
+                        float v[16];
+                        tmem_get16(tS + lanes + 32 * half + c, v);
+                        if (!slow) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] *= pw[i - j - k < 0 ? 0 : i - j - k];
+                        }
+                        if (tq <= half || t.n < 64) {  // tokens before the column's, and behind the last one, are left out whatever they hold
+                            const int last = i < t.n ? i - j : -1;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = k <= last ? v[k] : 0.0f;
+                        }
+                        const f2 f = pack(rowf, rowf);
+                        st_scaled8(to + sw128(r, (j >> 3)), v, f);
+                        st_scaled8(to + sw128(r, (j >> 3) + 1), v + 8, f);
+                    }
+                    fence_async_smem();
+                }
+                tc_fence_before();
+                mbar_arrive(p_full);
+            }
+            if (!ok) break;
+            // a chunk's gradients: value r of tokens 32 half .. + 31, to rows of 128 values
+            if (!wait.all(pv_done, (it - 1) & 1, 152)) break;
+            if (single && ci >= 1) {
+                vacant();
+                if (!wait.all(left, (ci - 1) & 1, 157)) break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {
+                if ((c & 63) >= 32) continue;
+                const int j = 32 * half + (c & 63);
+                const uint32_t to = base + stage + (c >> 6) * 2 * kBox + (r >> 6) * kBox + (r & 7) * 2 + j * 128;
+                float v[16];
+                tmem_get16(acc + c, v);
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {  // single values: 32 lanes make half a row
+                    uint32_t f[4];
+                    ld_shared_v4(c0 + (j + k) * 4, f[0], f[1], f[2], f[3]);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v[k + m] * __uint_as_float(f[m])));
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + sw[(k + m) & 7] + (k + m) * 128), "h"(h) : "memory");
+                    }
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(o_free);
+            mbar_arrive(staged);
+            if (!wait.all(staged, ci & 1, 153)) break;
+            // a warp to each 64 values of dv and dk, or, of fewer than 64 tokens, rows by all of them
+            const int row = (int)(w.b * p.seqs.L) + t.t0;
+            if (t.n == 64) {
+                const int e = warp >> 1, h = warp & 1;
+                if (warp < 4 && h < (e == 0 ? nhz : nhx) && lane == 0) {
+                    tma_store_3d(e == 0 ? &g.dv : &g.dk, sm + stage + e * 2 * kBox + h * kBox, 64 * h, (int)w.h, row);
+                    bulk_commit();
+                }
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                    const int d = e == 0 ? p.dz : p.dx;
+                    const int64_t ld = e == 0 ? g.lddv : g.lddk;
+                    __nv_bfloat16* out = (__nv_bfloat16*)(e == 0 ? g.dv_out : g.dk_out) + (w.b * p.seqs.L + t.t0) * ld + w.h * d;
+#pragma unroll 1
+                    for (int c = tid; c < t.n * 16; c += 32 * kMathWarps) {
+                        const int tok = c >> 4, piece = c & 15;
+                        uint32_t v[4];
+                        ld_shared_v4(base + stage + e * 2 * kBox + (piece >> 3) * kBox + sw128(tok, piece & 7), v[0], v[1], v[2], v[3]);
+                        if (8 * piece < d) *reinterpret_cast<uint4*>(out + tok * ld + 8 * piece) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            ++ci;
         }
         if (lane == 0) bulk_wait_all();
     }

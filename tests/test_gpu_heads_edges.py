@@ -552,3 +552,52 @@ def test_refusals(lz):
               lambda: step(q[0], k[0], v[0], l, state), lambda: step(q[:, 0], k[:, 0], v[:, 0], l, state, slots=torch.zeros(2, dtype=torch.int64, device="cuda"))):
         with pytest.raises(bad):
             f()
+
+
+# --------------------------------------------------------------------- long sums, repeated calls
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("H,L", [(160, 20000), (3, 20000)])
+def test_states_of_long_sequences_do_not_drift(lz, dtype, G, H, L):
+    """With next to no decay and positive terms a state is a sum of L of them: rounded to nearest its errors do not
+    add up in one direction.  Uncut (160 states) and in segments.  A sum's L / 64 additions err by 2^-24 each at random,
+    16 times that at most in 20000 tokens' 313; the split of the terms (2^-16) at random over L of them is below 2^-22.
+    The power of a tile's length, which is the same for every tile, is within two units of the exact one (exp2f's bound:
+    2^-23 below 1), and a term passes L / 128 of them on average: 1.9e-5 in one direction.  (Cut off after every addition
+    of 16 rows, the states would be 8e-5 too small.)  fp32 arithmetic adds token by token, G L of them: an error of at
+    most 2^-24 of a sum that grows in proportion has a deviation of 2^-24 / 3 of the last one, six deviations of all are
+    2^-23 sqrt(G L)."""
+    D = Draw(14, dtype)
+    d, power = 16, L / 128 * 2.0 ** -23
+    most = power + (2.0 ** -17 if dtype == "bf16" else 2.0 ** -23 * (G * L) ** 0.5)
+    k, v = (torch.rand(1, L, H, d, device="cuda", generator=torch.Generator("cuda").manual_seed(i)).add(0.5).to(D.dtype) for i in (1, 2))
+    q = torch.zeros(1, L, G * H, d, dtype=D.dtype, device="cuda")
+    s, l = torch.empty(1, H, d, d, device="cuda"), torch.full((H,), -1e-9, device="cuda")
+    lz.lizard_decay_attn_fwd(q, k, v, l, s_out=s)
+    ref = torch.einsum("lhi,lhj->hij", k[0].double(), v[0].double())
+    err = (s[0].double() - ref) / ref + 0.5e-9 * L  # the decay's own: half of L of it on average
+    assert err.mean().abs() < 2.0 ** -21 + power and err.abs().max() < most
+    # backwards: dS = sum of q do^T
+    g0 = torch.empty_like(s)
+    lz.lizard_decay_attn_bwd(k.repeat_interleave(G, 2), k, v, l, v.repeat_interleave(G, 2), scale=1.0, ds0=g0)
+    err = (g0[0].double() - G * ref) / (G * ref) + 0.5e-9 * L
+    assert err.mean().abs() < 2.0 ** -21 + power and err.abs().max() < most
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,L", [(6, 2, 64, 130), (12, 3, 128, 300), (5, 1, 64, 700), (4, 4, 128, 400)])
+@pytest.mark.parametrize("fast", [True, False])
+def test_many_calls_give_the_same_bits(lz, Hq, Hkv, d, L, fast):
+    """Whatever the memory held before."""
+    D = Draw(15, "bf16")
+    q, k, v, do = (D(2, L, h, d)[0] for h in (Hq, Hkv, Hkv, Hq))
+    l, s0, want = D.dev(np.full(Hkv, -1e6 if fast else -0.01))[0], D(2, Hkv, d, d, dtype=torch.float32)[0], None
+    for _ in range(40):
+        torch.full((16 << 20,), float("nan"), device="cuda")
+        s, ds = torch.empty_like(s0), torch.empty_like(s0)
+        o = lz.lizard_decay_attn_fwd(q, k, v, l, s0=s0, s_out=s)
+        g = lz.lizard_decay_attn_bwd(q, k, v, l, do, s0=s0, ds_out=s0, ds0=ds)
+        got = [o, s, g["dq"], g["dk"], g["dv"], ds]
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
