@@ -61,8 +61,8 @@ struct Walk {
     }
 };
 
-// Segments whose end state another one begins with: all but the last in the order of time.
-__device__ __forceinline__ int ending_segment(const DecayPass& p, int i) { return p.rev ? i + 1 : i; }
+// Segments whose end state is wanted: those that another one begins with, all but the last in the order of time; or all.
+__device__ __forceinline__ int ending_segment(const DecayPass& p, int i) { return p.rev && !p.all_ends ? i + 1 : i; }
 __device__ __forceinline__ const float* first_state(const DecayPass& p, int64_t unit, int seg) {
     return p.recs + (unit * p.nseg + (p.parts > 0 ? 0 : seg)) * p.dx * p.dz;
 }

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int s = p.rev ? p.nseg - 1 - s0 - k : s0 + k;
-            if (s0 + k < p.nseg - 1) own[k] = r[s * size];  // the last segment's is nobody's first state
+            if (s0 + k < p.nseg - 1 + p.all_ends) own[k] = r[s * size];  // the last segment's is nobody's first state
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
@@ -202,10 +202,11 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
             if (s0 + k < p.nseg) {
                 r[s * size] = carry;
                 // a sequence that begins in the segment lets nothing pass, not even NaN
-                if (s0 + k < p.nseg - 1) carry = pass[s] < 0.0f ? own[k] : fmaf(pass[s], carry, own[k]);
+                if (s0 + k < p.nseg - 1 + p.all_ends) carry = pass[s] < 0.0f ? own[k] : fmaf(pass[s], carry, own[k]);
             }
         }
     }
+    if (p.all_ends) p.fin[unit * size + e] = carry;  // (of a dense batch: units are states)
 }
 
 // One pass over a segment's tiles, 64 columns of z to a CTA; M: rows of the state by 64.  Bound by the fp32 pipes and
@@ -453,12 +454,18 @@ int parts_of(const DecayArgs& a, const DecayPass& p) {
     return decay_uses_tc(a) ? 2 : 1;
 }
 
-// The states in front of the segments, [units, nseg, dk, dv], from a pass that is not transposed.
-cudaError_t segment_states(const DecayArgs& a, const DecayPass& p, float* recs, cudaStream_t s) {
+// The states in front of the segments, [units, nseg, dk, dv], from a pass that is not transposed.  On the tensor cores
+// the join of a dense batch also leaves its last states, and the pass, which then needs no third part of its products
+// into the state, has none to leave (65536 tokens: 276 us, else 309).
+cudaError_t segment_states(const DecayArgs& a, DecayPass* pass, float* recs, cudaStream_t s) {
+    DecayPass& p = *pass;
     if (p.nseg == 1) return cudaSuccess;
+    p.all_ends = decay_uses_tc(a) && a.seqs.cu == nullptr && p.parts == 0 && p.fin != nullptr;
     const cudaError_t e = decay_uses_tc(a) ? decay_tc_ends(p, recs, s) : run_ends(p, recs, s);
     if (e != cudaSuccess || p.parts > 0) return e;
-    return run_join(p, recs, s);
+    const cudaError_t j = run_join(p, recs, s);
+    if (p.all_ends) p.fin = nullptr;
+    return j;
 }
 
 cudaError_t outputs(const DecayArgs& a, const DecayPass& p, cudaStream_t s) {
@@ -685,7 +692,7 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t s) {
     DecayPass p = output_pass(a);
     p.recs = a.ws;
     if ((e = own_first_states(a, &p, a.ws + records(p), s)) != cudaSuccess) return e;
-    e = segment_states(a, p, a.ws, s);
+    e = segment_states(a, &p, a.ws, s);
     return e != cudaSuccess ? e : outputs(a, p, s);
 }
 
@@ -699,11 +706,11 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t s) {
     float* recs = a.ws + records(v);
     q.recs = a.ws;
     v.recs = k.recs = recs;
-    if ((e = segment_states(a, o, a.ws, s)) != cudaSuccess) return e;
+    if ((e = segment_states(a, &o, a.ws, s)) != cudaSuccess) return e;
     if ((e = outputs(a, q, s)) != cudaSuccess) return e;
     // dk reads ds_out: before dv, which may overwrite it with ds0
     if ((e = own_first_states(a, &v, recs + records(v), s)) != cudaSuccess) return e;
-    if ((e = segment_states(a, v, recs, s)) != cudaSuccess) return e;
+    if ((e = segment_states(a, &v, recs, s)) != cudaSuccess) return e;
     if (decay_uses_tc(a)) return decay_tc_grads(v, a.dk_, a.lddk, s);
     if ((e = outputs(a, k, s)) != cudaSuccess) return e;
     return outputs(a, v, s);

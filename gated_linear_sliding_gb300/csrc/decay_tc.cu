@@ -15,18 +15,17 @@
 // power of the difference and scale X S before P Z is added.
 //
 // Roundings: P and the operand copy of S are bf16 (a relative 2^-8 of the terms, as the output's own).  S itself
-// stays in fp32 in TMEM, and Y~ goes in as a high and a low bf16 part (2^-17), since S leaves the call in fp32
-// and what is rounded there would stay for the rest of the sequence.
+// stays in fp32, and Y~ goes in as two bf16 parts (2^-16), or three (2^-24) where S leaves the call: what is rounded
+// there would stay for the rest of the sequence.
 //
 // Warps: 0-7 the pairs' weights and the outputs (a thread holds one row's 32 of 64 pairs and 64 of 128 output
 // columns); 8-15 the state (half a row of S to a thread; Y~); 16 the copies; 17 the MMAs of the scores, 18 of
 // the state, 19 of the outputs.  TMEM: P and its scores two of 64 columns, O 128, S 128, a chunk's part of S 128.
 //
 // Bound by the chain of a chunk (state out, X S, P Z, state on) and by what its warps issue in it: with 32 query heads
-// on 8 of 128 the walk of 8192 tokens takes 36 us, where its bytes take 25, and that of 65536 takes 214 us, where they
-// take 201.  The loops over a product's steps stay rolled: unrolled by four the
-// longer one takes 39 us more (the code of seven roles shares the SM's instruction cache), and the waits' slow path
-// is one function for the same reason.
+// on 8 of 128 the walk of 8192 tokens takes 38 us, where its bytes take 25, and that of 65536 takes 220 us, where they
+// take 201.  The loops over a product's steps stay rolled: unrolled by four the longer one takes 39 us more (the code of
+// seven roles shares the SM's instruction cache), and the waits' slow path is one function for the same reason.
 #include "decay_tc.cuh"
 
 namespace lz {
@@ -44,11 +43,11 @@ struct Layout {
     static constexpr uint32_t X = 0;
     static constexpr uint32_t OUT = XST * 4 * kBox;
     static constexpr uint32_t YZ = OUT + 4 * kBox;
-    static constexpr uint32_t KT = YZ + YST * 4 * kBox;  // high part, low part
+    static constexpr uint32_t KT = YZ + YST * 4 * kBox;  // two parts of Y~ (a third takes the first's place)
     static constexpr uint32_t ST = KT + 4 * kBox;
     static constexpr uint32_t TABLE = ST + 4 * kBox;     // powers 0 .. 128, and the columns' factors
     static constexpr uint32_t BARS = TABLE + (132 + 128) * 4;
-    static constexpr uint32_t BYTES = BARS + 304 + 1024;
+    static constexpr uint32_t BYTES = BARS + 400 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 // Several tiles of x for each of y and z, or one.  Then one stage of x is enough (its last reader is done long before
@@ -57,7 +56,8 @@ struct Layout {
 using Wide = Layout<2, 2>;
 using Even = Layout<1, 3>;
 
-template <typename SM>
+// three: parts of Y~ (with a stage of x less and all three at once the walk of 65536 tokens takes 36 us more).
+template <typename SM, bool three>
 __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs g) {
     constexpr int XST = SM::XST, YST = SM::YST;
     extern __shared__ uint8_t smem_raw[];
@@ -69,8 +69,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BARS);
     uint64_t *x_full = bar, *x_free = bar + 3, *yz_full = bar + 6, *yz_free = bar + 10, *zz_full = bar + 14, *s_full = bar + 18,
              *p_full = bar + 20, *xs_full = bar + 22, *pv_done = bar + 24, *o_free = bar + 26, *kt_full = bar + 28,
-             *h_done = bar + 29, *st_full = bar + 30, *xs_done = bar + 31, *drained = bar + 32;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 34);
+             *h_done = bar + 29, *st_full = bar + 30, *xs_done = bar + 31, *drained = bar + 32,
+             *first_free = bar + 35, *third_full = bar + 36;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 38);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
@@ -105,7 +106,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         mbar_init(h_done, 1);
         mbar_init(st_full, 32 * kStateWarps);
         mbar_init(xs_done, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&drained[i], 1);
+        mbar_init(first_free, 1);
+        mbar_init(third_full, 32 * kStateWarps);
+        for (int i = 0; i < 3; ++i) mbar_init(&drained[i], 1);
         *abort = 0;
         fence_mbar_init();
     }
@@ -262,17 +265,29 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         bool ok = true;
         while (ok && walk.next(p.seqs, w.b, &t)) {
             const int ny = t.n > 64 ? 2 : 1;
-            for (int q = 0; q < ny; ++q, ++yi) {
+            for (int q = 0; q < ny && ok; ++q, ++yi) {
                 if (!wait.all(kt_full, yi & 1, 109)) { ok = false; break; }
                 tc_fence_after();
-                state_mmas<1>(leader, tD, base + SM::KT, uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox), kBox, id_h, q == 0);
+                const uint32_t za = uniform(base + SM::YZ + ((yi % YST) * 4 + 2) * kBox);
+                if (!three) state_mmas<1>(leader, tD, base + SM::KT, 2, za, kBox, id_h, q == 0);
+                if (three) {
+                    state_mmas<1>(leader, tD, base + SM::KT, 1, za, kBox, id_h, q == 0);
+                    if (leader) mma_commit(first_free);
+                    state_mmas<1>(leader, tD, base + SM::KT + 2 * kBox, 1, za, kBox, id_h, false);
+                    if (!wait.all(third_full, yi & 1, 118)) { ok = false; break; }
+                    tc_fence_after();
+                    state_mmas<1>(leader, tD, base + SM::KT, 1, za, kBox, id_h, false);
+                }
                 if (leader) {
                     mma_commit(h_done);
                     mma_commit(&yz_free[yi % YST]);
                 }
             }
         }
-        if (!ok && yi > 0) mbar_wait(h_done, (yi - 1) & 1, tc::kTimeout);
+        if (!ok) {
+            if (leader) mma_commit(&drained[2]);
+            mbar_wait(&drained[2], 0, tc::kTimeout);
+        }
     } else if (warp >= 8) {
         // the state: half a row of S to a thread
         const StateRow sr = state_row(p, tH, tD, tid - 32 * kMathWarps);
@@ -301,12 +316,23 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (q > 0 && !wait.all(h_done, (yi - 1) & 1, 113)) { ok = false; break; }
                 const int tok = sr.in & 63;
                 const uint32_t ya = base + SM::YZ + ys * 4 * kBox;
-                if (m < 64) clear_rows<32 * kStateWarps>(ya + 2 * kBox, kBox, m, sr.in);
-                scale_rows<4, 1>(ya, kBox, base + SM::KT, 2 * kx, m, tok < m ? pw[t.n - 1 - j0 - tok] : 0.0f, sr.in);
+                const float f = tok < m ? pw[t.n - 1 - j0 - tok] : 0.0f;
+                if (m < 64) {
+                    clear_rows<32 * kStateWarps>(ya + 2 * kBox, kBox, m, sr.in);
+                    fence_async_smem();
+                }
+                mbar_arrive(&zz_full[ys]);
+                scale_rows<false, 1>(ya, kBox, base + SM::KT, 2 * kx, m, f, sr.in);
                 fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(&zz_full[ys]);
                 mbar_arrive(kt_full);
+                if (three) {
+                    if (!wait.all(first_free, yi & 1, 126)) { ok = false; break; }
+                    third_of_rows(ya, kBox, base + SM::KT, 2 * kx, m, f, sr.in);
+                    fence_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(third_full);
+                }
             }
             was_last = t.last;
             was_seq = t.seq;
@@ -460,21 +486,24 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 // copies, warp 17 issues the MMAs; they sum four tiles from zero in one of two places in TMEM, and all sixteen warps
 // add that to the sum in their registers (see StateRow) two places later.
 constexpr int kEndsThreads = 576, kEndsStages = 4, kEndsBatch = 4;
+template <bool three>
 struct EndsSmem {
     static constexpr uint32_t YZ = 0;
     static constexpr uint32_t KT = kEndsStages * 4 * kBox;
-    static constexpr uint32_t BARS = KT + 2 * 4 * kBox;
+    static constexpr uint32_t BARS = KT + 2 * (three ? 6 : 4) * kBox;
     static constexpr uint32_t BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 
-template <bool rev>
+template <bool rev, bool three>
 __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __grid_constant__ TcArgs g, float* recs) {
+    using SM = EndsSmem<three>;
+    constexpr uint32_t kGroup = (three ? 6 : 4) * kBox;  // a group's Y~
     extern __shared__ uint8_t smem_raw[];
     const DecayPass& p = g.p;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + EndsSmem::BARS);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BARS);
     uint64_t *yz_full = bar, *yz_free = bar + 4, *kt_full = bar + 8, *kt_free = bar + 10, *summed = bar + 12, *taken = bar + 14, *drained = bar + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 17);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -528,7 +557,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 for (int gh = 0; gh < p.gy; ++gh, ++it) {
                     const int s = it % kEndsStages;
                     if (it >= kEndsStages && !wait(&yz_free[s], ((it / kEndsStages) & 1) ^ 1, 120)) { ok = false; break; }
-                    uint8_t* to = sm + EndsSmem::YZ + s * 4 * kBox;
+                    uint8_t* to = sm + SM::YZ + s * 4 * kBox;
                     mbar_arrive_expect_tx(&yz_full[s], (nhx + nhz) * kBox);
                     const int head = (int)(w.h * p.gy + gh);
                     for (int h = 0; h < nhx; ++h) tma_load_3d(to + h * kBox, &g.y, &yz_full[s], 64 * h, head, row);
@@ -550,7 +579,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             if (!wait.all(&kt_full[k], (it >> 1) & 1, 121)) break;
             if (at == 0 && b >= 2 && !wait.all(&taken[b & 1], ((b >> 1) & 1) ^ 1, 125)) break;
             tc_fence_after();
-            state_mmas<8>(leader, uniform(tb + (b & 1) * 128), uniform(base + EndsSmem::KT + k * 4 * kBox), uniform(base + EndsSmem::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
+            state_mmas<three ? 4 : 8>(leader, uniform(tb + (b & 1) * 128), uniform(base + SM::KT + k * kGroup), three ? 3 : 2, uniform(base + SM::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
                        at == 0);
             if (leader) {
                 mma_commit(&kt_free[k]);
@@ -589,9 +618,9 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
                 if (!wait.all(&yz_full[s], (it / kEndsStages) & 1, 122)) { ok = false; break; }
                 if (it >= 2 && !wait.all(&kt_free[group], ((it >> 1) & 1) ^ 1, 123)) { ok = false; break; }
                 const float f = tok < n ? power(l2, rev ? t0 + tok - begin + 1 : end - 1 - t0 - tok) * p.in_scale : 0.0f;
-                const uint32_t ya = base + EndsSmem::YZ + s * 4 * kBox;
+                const uint32_t ya = base + SM::YZ + s * 4 * kBox;
                 if (n < 64) clear_rows<256>(ya + 2 * kBox, kBox, n, in);
-                scale_rows<4, 2>(ya, kBox, base + EndsSmem::KT + group * 4 * kBox, 2 * ((p.dx + 15) / 16), n, f, in);
+                scale_rows<three, 2>(ya, kBox, base + SM::KT + group * kGroup, 2 * ((p.dx + 15) / 16), n, f, in);
                 fence_async_smem();
                 mbar_arrive(&kt_full[group]);
             }
@@ -633,9 +662,9 @@ bool args_of(const DecayPass& p, TcArgs* a) {
            (p.out == nullptr || map_of(&a->out, p.out, rows, p.Hkv * p.gx, p.dz, p.ldout, 32));
 }
 
-template <typename SM>
+template <typename SM, bool three>
 cudaError_t go(const TcArgs& a, cudaStream_t s) {
-    const auto kernel = decay_tc_kernel<SM>;
+    const auto kernel = decay_tc_kernel<SM, three>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::BYTES);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.p.units * a.p.nseg));
@@ -647,12 +676,13 @@ cudaError_t go(const TcArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <bool rev>
+template <bool rev, bool three>
 cudaError_t go_ends(const TcArgs& a, float* recs, cudaStream_t s) {
-    const auto kernel = decay_tc_ends_kernel<rev>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)EndsSmem::BYTES);
+    using SM = EndsSmem<three>;
+    const auto kernel = decay_tc_ends_kernel<rev, three>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.p.units * (a.p.parts > 0 ? a.p.parts : a.p.nseg - 1)), kEndsThreads, EndsSmem::BYTES, s>>>(a, recs);
+    kernel<<<(unsigned)(a.p.units * (a.p.parts > 0 ? a.p.parts : a.p.nseg - 1 + a.p.all_ends)), kEndsThreads, SM::BYTES, s>>>(a, recs);
     return cudaGetLastError();
 }
 
@@ -668,13 +698,15 @@ bool decay_uses_tc(const DecayArgs& a) {
 cudaError_t decay_tc_ends(const DecayPass& p, float* recs, cudaStream_t s) {
     TcArgs a;
     if (!args_of(p, &a)) return cudaErrorInvalidValue;
-    return p.rev ? go_ends<true>(a, recs, s) : go_ends<false>(a, recs, s);
+    if (three_parts(p)) return p.rev ? go_ends<true, true>(a, recs, s) : go_ends<false, true>(a, recs, s);
+    return p.rev ? go_ends<true, false>(a, recs, s) : go_ends<false, false>(a, recs, s);
 }
 
 cudaError_t decay_tc_pass(const DecayPass& p, cudaStream_t s) {
     TcArgs a;
     if (!args_of(p, &a)) return cudaErrorInvalidValue;
-    return p.gx > 1 ? go<Wide>(a, s) : go<Even>(a, s);
+    if (three_parts(p)) return p.gx > 1 ? go<Wide, true>(a, s) : go<Even, true>(a, s);
+    return p.gx > 1 ? go<Wide, false>(a, s) : go<Even, false>(a, s);
 }
 
 }  // namespace lz

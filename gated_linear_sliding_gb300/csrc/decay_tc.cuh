@@ -63,28 +63,64 @@ __device__ __forceinline__ Seg seg_of(const DecayPass& p) {
     return s;
 }
 
-// The tile of Y~ from y's 64 rows, as high and low parts, by 64 PARTS threads (token, every PARTSth of `pieces`
-// pieces of eight columns); y's second 64 columns lie `apart` bytes behind the first.
-template <int PARTS, int UNROLL>
+// Y~ enters the MMAs as bf16 parts, each the rounded remainder of those before: two (2^-16 of a term at most) where the
+// state only meets outputs of bf16, three (fp32's 24 bits) where it leaves the call in fp32 (8192 tokens in eight
+// sequences: 85 and 91 us).
+inline bool three_parts(const DecayPass& p) { return p.fin != nullptr; }
+
+// The tile's first two or all three parts from y's 64 rows, by 256 threads (token, every fourth of `pieces` pieces of
+// eight columns), one part 16 KB behind another; y's second 64 columns lie `apart` bytes behind the first.
+template <bool ALL, int UNROLL>
 __device__ __forceinline__ void scale_rows(uint32_t ys, uint32_t apart, uint32_t kt, int pieces, int n, float f, int tid) {
-    const int tok = tid & 63, part = tid >> 6;
+    const int tok = tid & 63;
     const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
 #pragma unroll UNROLL
-    for (int c = part; c < pieces; c += PARTS) {
+    for (int c = tid >> 6; c < pieces; c += 4) {
         const uint32_t off = sw128(tok, c & 7);
         uint32_t w[4] = {0, 0, 0, 0}, hi[4], lo[4];
         if (tok < n) ld_shared_v4(ys + (c >> 3) * apart + off, w[0], w[1], w[2], w[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float a, b;
-            const f2 v = mul2(pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), ff);
+            f2 v = mul2(pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), ff);
             unpack(v, a, b);
             hi[i] = pack_bf16(a, b);
-            unpack(fma2(pack(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xffff0000u)), minus, v), a, b);
+            v = fma2(pack(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xffff0000u)), minus, v);
+            unpack(v, a, b);
             lo[i] = pack_bf16(a, b);
+            if (ALL) {
+                unpack(fma2(pack(__uint_as_float(lo[i] << 16), __uint_as_float(lo[i] & 0xffff0000u)), minus, v), a, b);
+                w[i] = pack_bf16(a, b);
+            }
         }
         st_shared_v4(kt + (c >> 3) * kBox + off, hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(kt + (c >> 3) * kBox + 2 * kBox + off, lo[0], lo[1], lo[2], lo[3]);
+        if (ALL) st_shared_v4(kt + (c >> 3) * kBox + 4 * kBox + off, w[0], w[1], w[2], w[3]);
+    }
+}
+// The third part alone, in the place of the first, whose MMAs are done.
+__device__ __forceinline__ void third_of_rows(uint32_t ys, uint32_t apart, uint32_t kt, int pieces, int n, float f, int tid) {
+    const int tok = tid & 63;
+    const f2 ff = pack(f, f), minus = pack(-1.0f, -1.0f);
+#pragma unroll 1
+    for (int c = tid >> 6; c < pieces; c += 4) {
+        const uint32_t off = sw128(tok, c & 7);
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (tok < n) ld_shared_v4(ys + (c >> 3) * apart + off, w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2 v = mul2(pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), ff);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                unpack(v, a, b);
+                const uint32_t h = pack_bf16(a, b);
+                v = fma2(pack(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), minus, v);
+            }
+            unpack(v, a, b);
+            w[i] = pack_bf16(a, b);
+        }
+        st_shared_v4(kt + (c >> 3) * kBox + off, w[0], w[1], w[2], w[3]);
     }
 }
 // Rows behind a tile's last token become zeros: 0 times what lies there may be NaN.
@@ -118,11 +154,11 @@ __device__ __forceinline__ void mma_bf16_ts_one(bool leader, uint32_t d_tmem, ui
         : "memory");
 }
 
-// D += Y~^T Z over a tile's 64 tokens, both parts; by a warp.  z's second 64 columns lie `apart` bytes behind the first.
+// D += Y~^T Z over a tile's 64 tokens, `parts` of Y~'s; by a warp.  z's second 64 columns lie `apart` bytes behind the first.
 template <int UNROLL>
-__device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, uint32_t zs, uint32_t apart, uint32_t idesc, bool fresh) {
+__device__ __forceinline__ void state_mmas(bool leader, uint32_t d, uint32_t kt, const int parts, uint32_t zs, uint32_t apart, uint32_t idesc, bool fresh) {
 #pragma unroll UNROLL
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4 * parts; ++j)
         mma_bf16_one(leader, d, mndesc(kt + (j >> 2) * 2 * kBox + (j & 3) * 2048, kBox), mndesc(zs + (j & 3) * 2048, apart), idesc, fresh && j == 0 ? 0u : 1u);
 }
 

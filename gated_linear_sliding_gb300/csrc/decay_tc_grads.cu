@@ -41,14 +41,15 @@ struct GradSmem {
     static constexpr uint32_t KV = 12 * kBox;         // K, V: 64 rows each
     static constexpr uint32_t OWN = RING + 8 * kBox;  // dv and dk [64 x 128] on their way out, one query head a state
     static constexpr uint32_t PP = KV + 4 * kBox;     // P, P' [128 x 64]; else dv and dk
-    static constexpr uint32_t KT = PP + 4 * kBox;     // Q~: high part, low part
+    static constexpr uint32_t KT = PP + 4 * kBox;     // Q~: its first part, later its third; the second
     static constexpr uint32_t ST = KT + 4 * kBox;
     static constexpr uint32_t TABLE = ST + 4 * kBox;  // powers 0 .. 64, and the columns' factors
     static constexpr uint32_t BARS = TABLE + (68 + 64) * 4;
-    static constexpr uint32_t BYTES = BARS + 304 + 1024;
+    static constexpr uint32_t BYTES = BARS + 400 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 
+template <bool three>
 __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __grid_constant__ GradArgs g) {
     using SM = GradSmem;
     extern __shared__ uint8_t smem_raw[];
@@ -61,7 +62,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     uint64_t *b_full = bar, *b_free = bar + 6, *kv_full = bar + 12, *kv_free = bar + 13, *s_full = bar + 14, *p_full = bar + 15, *pv_done = bar + 16,
              *xs_full = bar + 17, *o_free = bar + 19, *zz_full = bar + 21, *kt_full = bar + 23, *h_done = bar + 24, *st_full = bar + 25,
              *xs_done = bar + 26, *staged = bar + 27, *left = bar + 28, *late = bar + 29, *drained = bar + 30, *chunk_done = bar + 33;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 34);
+    uint64_t *first_free = bar + 34, *third_full = bar + 35;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 36);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
@@ -93,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         }
         mbar_init(o_free, 32 * kMathWarps);
         mbar_init(kt_full, 32 * kStateWarps);
+        mbar_init(first_free, 1);
+        mbar_init(third_full, 32 * kStateWarps);
         mbar_init(h_done, 1);
         mbar_init(st_full, 32 * kStateWarps);
         mbar_init(xs_done, 1);
@@ -262,7 +266,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 for (int k = 0; k < heads; ++k, ++ui) {
                     if (!wait.all(kt_full, ui & 1, 141)) { ok = false; break; }
                     tc_fence_after();
-                    state_mmas<1>(leader, tD, base + SM::KT, oa + k * kBox, apart, id_h, a == 0 && k == 0);
+                    if (!three) state_mmas<1>(leader, tD, base + SM::KT, 2, oa + k * kBox, apart, id_h, a == 0 && k == 0);
+                    if (three) {
+                        state_mmas<1>(leader, tD, base + SM::KT, 1, oa + k * kBox, apart, id_h, a == 0 && k == 0);
+                        if (leader) mma_commit(first_free);
+                        state_mmas<1>(leader, tD, base + SM::KT + 2 * kBox, 1, oa + k * kBox, apart, id_h, false);
+                        if (!wait.all(third_full, ui & 1, 158)) { ok = false; break; }
+                        tc_fence_after();
+                        state_mmas<1>(leader, tD, base + SM::KT, 1, oa + k * kBox, apart, id_h, false);
+                    }
                     if (leader) mma_commit(h_done);
                 }
                 if (ok && leader) {
@@ -320,10 +332,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                 for (int k = 0; k < heads; ++k, ++ui) {
                     // the first of a chunk: waited for before the state's copy
                     if ((a > 0 || k > 0) && !wait.all(h_done, (ui - 1) & 1, 146)) { ok = false; break; }
-                    scale_rows<4, 1>(qa + k * kBox, apart, base + SM::KT, 2 * kx, t.n, tok < t.n ? pw[tok + 1] * p.in_scale : 0.0f, sr.in);
+                    const float f = tok < t.n ? pw[tok + 1] * p.in_scale : 0.0f;
+                    scale_rows<false, 1>(qa + k * kBox, apart, base + SM::KT, 2 * kx, t.n, f, sr.in);
                     fence_async_smem();
                     tc_fence_before();
                     mbar_arrive(kt_full);
+                    if (three) {
+                        if (!wait.all(first_free, ui & 1, 159)) { ok = false; break; }
+                        third_of_rows(qa + k * kBox, apart, base + SM::KT, 2 * kx, t.n, f, sr.in);
+                        fence_async_smem();
+                        tc_fence_before();
+                        mbar_arrive(third_full);
+                    }
                 }
                 q += is_late(a) ? 1 : 2;
             }
@@ -478,6 +498,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     }
 }
 
+template <bool three>
+cudaError_t go(const GradArgs& a, cudaStream_t s) {
+    const auto kernel = decay_tc_grads_kernel<three>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradSmem::BYTES);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(a.p.units * a.p.nseg));
+    if (a.p.nseg > 1) {  // its set-up overlaps the segments' ends
+        e = launch_dependent(kernel, grid, dim3(kThreads), GradSmem::BYTES, s, a);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    kernel<<<grid, kThreads, GradSmem::BYTES, s>>>(a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t decay_tc_grads(const DecayPass& p, void* dk, int64_t lddk, cudaStream_t s) {
@@ -492,15 +526,7 @@ cudaError_t decay_tc_grads(const DecayPass& p, void* dk, int64_t lddk, cudaStrea
         !map_of(&a.k, p.x, rows, p.Hkv, p.dx, p.ldx) || !map_of(&a.v, p.v, rows, p.Hkv, p.dz, p.ldv) || !map_of(&a.dk, dk, rows, p.Hkv, p.dx, lddk) ||
         !map_of(&a.dv, p.out, rows, p.Hkv, p.dz, p.ldout))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(decay_tc_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradSmem::BYTES);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.units * p.nseg));
-    if (p.nseg > 1) {  // its set-up overlaps the segments' ends
-        e = launch_dependent(decay_tc_grads_kernel, grid, dim3(kThreads), GradSmem::BYTES, s, a);
-        return e != cudaSuccess ? e : cudaGetLastError();
-    }
-    decay_tc_grads_kernel<<<grid, kThreads, GradSmem::BYTES, s>>>(a);
-    return cudaGetLastError();
+    return three_parts(p) ? go<true>(a, s) : go<false>(a, s);
 }
 
 }  // namespace lz

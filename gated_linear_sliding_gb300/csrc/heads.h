@@ -82,6 +82,7 @@ struct DecayPass {
     // The segments' first states, [units, nseg, dk, dv]; with `parts` (two segments of a dense batch, where the
     // one's end is the other's beginning) the sum of a unit's first `parts` entries.
     const float* recs;
+    bool all_ends;  // the segments' end states are wanted of the last one too: the join leaves `fin`
     int64_t units, Hkv, seg_len;
     int nseg, parts;
     Seqs seqs;
