@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
             if (!wait.all(&kt_full[k], (it >> 1) & 1, 121)) break;
             if (at == 0 && b >= 2 && !wait.all(&taken[b & 1], ((b >> 1) & 1) ^ 1, 125)) break;
             tc_fence_after();
-            state_mmas<three ? 4 : 8>(leader, uniform(tb + (b & 1) * 128), uniform(base + SM::KT + k * kGroup), three ? 3 : 2, uniform(base + SM::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
+            state_mmas<three ? 12 : 8>(leader, uniform(tb + (b & 1) * 128), uniform(base + SM::KT + k * kGroup), three ? 3 : 2, uniform(base + SM::YZ + ((it % kEndsStages) * 4 + 2) * kBox), kBox, id_h,
                        at == 0);
             if (leader) {
                 mma_commit(&kt_free[k]);
@@ -599,10 +599,13 @@ __global__ void __launch_bounds__(kEndsThreads, 1) decay_tc_ends_kernel(const __
         auto take = [&]() {
             if (!wait.all(&summed[b & 1], (b >> 1) & 1, 124)) return false;
             tc_fence_after();
-            float v[32];
-            tmem_get32(tb + (b & 1) * 128 + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) sum[k] += v[k];
+            for (int h = 0; h < 32; h += 16) {
+                float v[16];
+                tmem_get16(tb + (b & 1) * 128 + ((uint32_t)(32 * (warp & 3)) << 16) + c + h, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sum[h + k] += v[k];
+            }
             tc_fence_before();
             mbar_arrive(&taken[b & 1]);
             ++b;
