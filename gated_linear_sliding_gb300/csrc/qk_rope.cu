@@ -205,12 +205,14 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
             {
                 float wv[2 * E];
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
+                for (int e = 0; e < 2 * E; ++e) wv[e] = 1.0f;
+                if (w != nullptr) {
 #pragma unroll
-                    for (int m = 0; m < V; ++m) {
-                        wv[2 * g * V + m] = w != nullptr && has1[g] ? w[at1[g] + m] : 1.0f;
-                        wv[(2 * g + 1) * V + m] = w != nullptr && has2[g] ? w[at2[g] + m] : 1.0f;
+                    for (int g = 0; g < NG; ++g) {
+                        if (has1[g]) Vec<V>::ld(w + at1[g], wv + 2 * g * V);
+                        if (has2[g]) Vec<V>::ld(w + at2[g], wv + (2 * g + 1) * V);
                     }
+                }
                 wp = sorted<V, NG, NEAR>(wv);
             }
             for (int hb = lo + slot; hb - slot < hi; hb += U * hpw) {
@@ -247,7 +249,10 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
 #pragma unroll
                         for (int e = 1; e < H; ++e) s2 = fma2(xp.b[e], xp.b[e], fma2(xp.a[e], xp.a[e], s2));
                         float ss = sum2(s2);
-                        for (int o = p.lph / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                        
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            if (o < p.lph) ss += __shfl_xor_sync(~0u, ss, o);
                         rs = rsqrtf(fmaf(ss, inv_d, a.eps));
                     }
                     const f2 rs2 = pack(rs, rs);
@@ -294,7 +299,10 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                                 c2 = fma2(y.b[e], xp.b[e], fma2(y.a[e], xp.a[e], c2));
                             }
                             float c = sum2(c2);
-                            for (int o = p.lph / 2; o > 0; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+                            
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            if (o < p.lph) c += __shfl_xor_sync(~0u, c, o);
                             c *= -inv_d * rs * rs;
                             const f2 cc = pack(c, c);
 #pragma unroll
@@ -360,7 +368,7 @@ constexpr int64_t kBwdCtas = 304;  // two of 256 threads a SM
 template <typename T, int V, int NG, bool NEAR, bool BWD>
 cudaError_t go(const RopeArgs& a, cudaStream_t s) {
     // heads under way: registers for loads beat more warps (forwards 39 us against 42 with three CTAs of two heads;
-    // with the gradients 189 against 193 with one head, 231 with three CTAs)
+    // with the gradients 187 against 191 with one head, 231 with three CTAs)
     constexpr int U = BWD ? 2 : 4;
     // eight warps a CTA; blocks of heads where the tokens alone do not make 16 warps a SM
     const RopePlan p = plan_of<V, NG>(a, 152 * 16);
