@@ -1055,6 +1055,11 @@ def lizard_block_norm_bwd(o, *, dr_out=None, dn_out=None, gate=None, r=None, w_p
 # ---- queries and keys in front of a mixer, and linear attention with a decay for each head ----------
 
 
+def _dense(t):
+    """A dense tensor like t (new_empty takes twice as long)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _qk_rope_inputs(q, k, freqs, positions, sections, start, w_q, w_k, norm, eps, neighbours):
     """lizard_rope_dims of the inputs, the shapes of q and k, and the addresses of w_q, w_k, freqs,
     positions."""
@@ -1092,7 +1097,7 @@ def lizard_qk_rope_fwd(q, k, freqs, *, positions=None, sections=None, start: int
     tp = q.dtype
     dims.ldq = _ld(q, "q", shape, tp)
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = _dense(q)
     else:
         dims.ldqo = _ld(q_out, "q_out", shape, tp)
     if k is None:
@@ -1101,7 +1106,7 @@ def lizard_qk_rope_fwd(q, k, freqs, *, positions=None, sections=None, start: int
     else:
         dims.ldk = _ld(k, "k", kshape, tp)
         if k_out is None:
-            k_out = q.new_empty(kshape)
+            k_out = _dense(k)
         else:
             dims.ldko = _ld(k_out, "k_out", kshape, tp)
     st = load().lizard_qk_rope_fwd(ctypes.byref(dims), q.data_ptr(), _ptr(k), *params, q_out.data_ptr(),
@@ -1127,13 +1132,13 @@ def lizard_qk_rope_bwd(q, k, freqs, dq_out, dk_out, *, positions=None, sections=
         raise ValueError("dk_out and dk go with k")
     dims.ldq, dims.ldqo = _ld(q, "q", shape, tp), _ld(dq_out, "dq_out", shape, tp)
     if dq is None:
-        dq = q.new_empty(shape)
+        dq = _dense(q)
     else:
         dims.lddq = _ld(dq, "dq", shape, tp)
     if k is not None:
         dims.ldk, dims.ldko = _ld(k, "k", kshape, tp), _ld(dk_out, "dk_out", kshape, tp)
         if dk is None:
-            dk = q.new_empty(kshape)
+            dk = _dense(k)
         else:
             dims.lddk = _ld(dk, "dk", kshape, tp)
     dw_q = None if w_q is None else torch.empty_like(w_q)
@@ -1186,7 +1191,7 @@ def lizard_decay_attn_fwd(q, k, v, log_decay, *, scale=None, s0=None, s_out=None
     dims, ptrs = _decay_inputs(q, k, v, log_decay, scale, nseq)
     shape = (B, L, dims.Hq, dims.dv)
     if o is None:
-        o = q.new_empty(shape)
+        o = _dense(q) if q.shape == shape else q.new_empty(shape)
     else:
         dims.ldo = _ld(o, "o", shape, q.dtype)
     states = (nseq or B, dims.Hkv, dims.dk, dims.dv)
@@ -1215,7 +1220,7 @@ def lizard_decay_attn_bwd(q, k, v, log_decay, do, *, scale=None, s0=None, ds_out
 
     def out(t, name, like):
         shape = tuple(like.shape)
-        return (like.new_empty(shape), 0) if t is None else (t, _ld(t, name, shape, tp))
+        return (_dense(like), 0) if t is None else (t, _ld(t, name, shape, tp))
 
     dq, dims.lddq = out(dq, "dq", q)
     dk, dims.lddk = out(dk, "dk", k)
@@ -1241,7 +1246,7 @@ def lizard_decay_attn_step(q, k, v, log_decay, state, *, scale=None, slots=None,
     dims, ptrs = _decay_inputs(q, k, v, log_decay, scale, 0)
     B = dims.B
     if o is None:
-        o = q.new_empty((B, dims.Hq, dims.dv))
+        o = _dense(q) if dims.dk == dims.dv else q.new_empty((B, dims.Hq, dims.dv))
     else:
         dims.ldo = _ld(o, "o", (B, dims.Hq, dims.dv), q.dtype, 1)
     nslots = state.shape[0]
