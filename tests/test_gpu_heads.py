@@ -11,7 +11,7 @@ Decays: a term passes two products of d values, one of them in sums over 64 toke
 every tile, and powers of up to 87 / ln 2 = 126 in the exponent, each rounded twice (2 ln 2 126 = 175 at
 most where the term is not 0): n = 400 + 2 (dk + dv) + 4 L / 64 + 64.
 Tensor cores round a pair's weight or the state to bf16 once (2^-8 of the term) on its way into an output of
-bf16, and split it in two parts (2^-17) on its way into a state.
+bf16; on its way into a state that leaves the call it keeps its 24 bits in three parts (2^-17 is allowed).
 """
 import numpy as np
 import pytest
