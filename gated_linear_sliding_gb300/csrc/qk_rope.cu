@@ -254,6 +254,8 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                         for (int o = 16; o > 0; o >>= 1)
                             if (o < p.lph) ss += __shfl_xor_sync(~0u, ss, o);
                         rs = rsqrtf(fmaf(ss, inv_d, a.eps));
+                        // (a lane behind the last head holds zeros: with eps 0 the weights' sums would take 0 times infinity)
+                        if (BWD && h >= hi) rs = 0.0f;
                     }
                     const f2 rs2 = pack(rs, rs);
                     Pairs<E> n;  // what turns
