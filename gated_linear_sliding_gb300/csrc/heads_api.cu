@@ -35,7 +35,7 @@ bool rope_args(const lizard_rope_dims* d, RopeArgs* a) {
     a->L = d->L;
     a->Hq = d->Hq;
     a->Hkv = d->Hkv;
-    a->d = (int)d->d;
+    a->d = (int)d->d;  // of sizes that rope_compiled refuses nothing else is read
     a->rot = (int)d->rot;
     a->axes = (int)d->axes;
     a->start = d->start;
@@ -46,8 +46,8 @@ bool rope_args(const lizard_rope_dims* d, RopeArgs* a) {
     return true;
 }
 
-// Heads the kernels are compiled for, counted in 32 bits.
-bool rope_compiled(const RopeArgs& a) { return a.d <= 512 && a.Hq + a.Hkv <= 1 << 24; }
+// Heads the kernels are compiled for, counted in 32 bits (asked of the caller's sizes, which have 64).
+bool rope_compiled(const lizard_rope_dims& d) { return d.d <= 512 && d.Hq + d.Hkv <= 1 << 24; }
 
 bool rope_params(const RopeArgs& a, const float* w_q, const float* w_k, const float* freqs) {
     return (a.norm || (w_q == nullptr && w_k == nullptr)) && (w_k == nullptr || a.Hkv > 0) && (a.rot == 0 || freqs != nullptr);
@@ -106,7 +106,7 @@ lizard_status lizard_qk_rope_fwd(const lizard_rope_dims* dims, const void* q, co
         return LIZARD_ERR_INVALID_ARG;
     const void* ptrs[] = {q, k, w_q, w_k, freqs, q_out, k_out};
     if (!all_aligned(ptrs) || ((uintptr_t)positions & 7u) != 0) return LIZARD_ERR_INVALID_ARG;
-    if (!rope_compiled(a)) return LIZARD_ERR_UNSUPPORTED;
+    if (!rope_compiled(*dims)) return LIZARD_ERR_UNSUPPORTED;
     const lizard_status st = device_status();
     if (st != LIZARD_OK) return st;
     if (!some) return LIZARD_OK;
@@ -123,7 +123,7 @@ lizard_status lizard_qk_rope_fwd(const lizard_rope_dims* dims, const void* q, co
 
 size_t lizard_qk_rope_bwd_workspace(const lizard_rope_dims* dims) {
     RopeArgs a;
-    if (!rope_args(dims, &a)) return 0;
+    if (!rope_args(dims, &a) || !rope_compiled(*dims)) return 0;
     return kHeaderBytes + sizeof(float) * (size_t)(rope_bwd_ctas(a) * 2 * a.d);
 }
 
@@ -141,7 +141,7 @@ lizard_status lizard_qk_rope_bwd(const lizard_rope_dims* dims, const void* q, co
     if ((w_q == nullptr) != (dw_q == nullptr) || (w_k == nullptr) != (dw_k == nullptr)) return LIZARD_ERR_INVALID_ARG;
     const void* ptrs[] = {q, k, w_q, w_k, freqs, dq_out, dk_out, dq, dk, dw_q, dw_k, workspace};
     if (!all_aligned(ptrs) || ((uintptr_t)positions & 7u) != 0) return LIZARD_ERR_INVALID_ARG;
-    if (!rope_compiled(a)) return LIZARD_ERR_UNSUPPORTED;
+    if (!rope_compiled(*dims)) return LIZARD_ERR_UNSUPPORTED;
     if (workspace == nullptr || ws_bytes < lizard_qk_rope_bwd_workspace(dims)) return LIZARD_ERR_WORKSPACE;
     const lizard_status st = device_status();
     if (st != LIZARD_OK) return st;
