@@ -20,6 +20,7 @@ __device__ __forceinline__ float power(float l2, int64_t n) { return exp2f(l2 * 
 struct Tile {
     int t0, n;
     bool first, last;  // the walk enters the sequence with this tile, leaves it after it
+    bool leaves;       // the sequence goes on in the walk's next segment
     int seq;
 };
 
@@ -42,6 +43,7 @@ struct Walk {
         if (rev ? at <= lo : at >= hi) return false;
         if (rev ? at <= begin : at >= end) enter(s, b);
         t->seq = seq;
+        t->leaves = rev ? begin < lo : end > hi;
         if (!rev) {
             const int to = min(min(at + tile, end), hi);
             t->t0 = at;
@@ -65,6 +67,15 @@ struct Walk {
 __device__ __forceinline__ int ending_segment(const DecayPass& p, int i) { return p.rev && !p.all_ends ? i + 1 : i; }
 __device__ __forceinline__ const float* first_state(const DecayPass& p, int64_t unit, int seg) {
     return p.recs + (unit * p.nseg + (p.parts > 0 ? 0 : seg)) * p.dx * p.dz;
+}
+
+// The state of head h that a sequence begins with, in the segment where it does (null: zero).  Only a sequence that
+// goes on in another segment may have had it overwritten by then.
+__device__ __forceinline__ const float* sequence_state(const DecayPass& p, const Tile& t, int64_t h, int seg) {
+    if (p.init == nullptr) return nullptr;
+    const int64_t size = (int64_t)p.dx * p.dz;
+    if (p.kept != nullptr && t.leaves) return p.kept + ((p.rev ? seg - 1 : seg) * p.Hkv + h) * size;
+    return p.init + (t.seq * p.Hkv + h) * size;
 }
 
 // The part of a segment whose tokens reach the state that leaves it: tokens [from, to), and whether

@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     while (walk.next(p.seqs, w.b, &t)) {
         __syncthreads();
         if (t.first || !begun) {
-            const float* from = t.first ? (p.init == nullptr ? nullptr : p.init + (t.seq * p.Hkv + w.h) * size)
-                                        : first_state(p, w.unit, w.seg);
+            const float* from = t.first ? sequence_state(p, t, w.h, w.seg) : first_state(p, w.unit, w.seg);
 #pragma unroll 8
             for (int e = threadIdx.x; e < dxp * ZS; e += NT) {
                 const int i = e / ZS, j = e % ZS;
@@ -413,6 +412,19 @@ __global__ void __launch_bounds__(256) decay_empty_kernel(const Seqs s, const fl
     }
 }
 
+// The first states of the sequences that hold the tokens behind the cuts.  1024 elements to a CTA.
+__global__ void __launch_bounds__(256) decay_keep_kernel(const DecayPass p, float* kept) {
+    const int64_t size = (int64_t)p.dx * p.dz, blocks = (size + 1023) / 1024;
+    const int64_t state = blockIdx.x / blocks, cut = state / p.Hkv, h = state - cut * p.Hkv;
+    const float* from = p.init + (seq_at(p.seqs, 0, (cut + 1) * p.seg_len).seq * p.Hkv + h) * size;
+    const int64_t first = blockIdx.x % blocks * 1024;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t e = first + k * 256 + threadIdx.x;
+        if (e < size) kept[state * size + e] = from[e];
+    }
+}
+
 size_t ends_smem(int dx) { return sizeof(float) * (size_t)(kTile * ((dx + 3) / 4 * 4 + 4) + kTile * ZS + kTile); }
 size_t pass_smem(int dx) {
     const int dxp = (dx + 3) / 4 * 4;
@@ -482,9 +494,20 @@ cudaError_t empty_states(const DecayArgs& a, const float* init, float* fin, cuda
 size_t records(const DecayPass& p) { return p.nseg == 1 ? 0 : (size_t)(p.units * p.nseg) * p.dx * p.dz; }
 
 // Where the last states overwrite the first ones, another segment's CTA may write one before a CTA has
-// read it: such a pass reads a copy.
+// read it: such a pass reads a copy.  Only a sequence that lies across a cut is in danger, so of many packed sequences
+// those at the cuts are copied (all of them, 8192 with 8 heads of 128 x 128, would take 4 GiB), else all.
+bool keeps_by_cut(const DecayArgs& a, const DecayPass& p) { return a.seqs.nseq > p.nseg - 1; }
+size_t kept_states(const DecayArgs& a, const DecayPass& p) {
+    return (size_t)((keeps_by_cut(a, p) ? p.nseg - 1 : a.nstate) * a.Hkv * a.dk * a.dv);
+}
+
 cudaError_t own_first_states(const DecayArgs& a, DecayPass* p, float* copy, cudaStream_t s) {
     if (p->nseg == 1 || p->init == nullptr || p->init != p->fin) return cudaSuccess;
+    if (keeps_by_cut(a, *p)) {
+        decay_keep_kernel<<<(unsigned)((p->nseg - 1) * a.Hkv * ((a.dk * a.dv + 1023) / 1024)), 256, 0, s>>>(*p, copy);
+        p->kept = copy;
+        return cudaGetLastError();
+    }
     const size_t bytes = sizeof(float) * (size_t)(a.nstate * a.Hkv * a.dk * a.dv);
     const cudaError_t e = cudaMemcpyAsync(copy, p->init, bytes, cudaMemcpyDeviceToDevice, s);
     p->init = copy;
@@ -679,11 +702,11 @@ cudaError_t step_typed(const DecayArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Forward: the states of its segments; backward: those of S and of dS.  Behind them, with segments, a
-// copy of the sequences' first states for calls whose last states overwrite them.
+// Forward: the states of its segments; backward: those of S and of dS.  Behind them, with segments, what
+// own_first_states copies in calls whose last states overwrite the first ones.
 size_t decay_ws_floats(const DecayArgs& a, bool bwd) {
     const DecayPass p = base_pass(a);
-    return p.nseg == 1 ? 0 : (size_t)((p.units * p.nseg * (bwd ? 2 : 1) + a.nstate * a.Hkv) * a.dk * a.dv);
+    return p.nseg == 1 ? 0 : (size_t)(p.units * p.nseg * (bwd ? 2 : 1) * a.dk * a.dv) + kept_states(a, p);
 }
 
 cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t s) {

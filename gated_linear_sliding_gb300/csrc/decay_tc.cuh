@@ -250,9 +250,7 @@ __device__ __forceinline__ void fetch_state(const DecayPass& p, const StateRow& 
 // The state a walk begins with: the sequence's own, or the segment's.
 __device__ __forceinline__ void begin_state(const DecayPass& p, const StateRow& r, const Seg& w, const Tile& t) {
     const int64_t size = (int64_t)p.dx * p.dz;
-    const float* from = !t.first            ? first_state(p, w.unit, w.seg)
-                        : p.init == nullptr ? nullptr
-                                            : p.init + (t.seq * p.Hkv + w.h) * size;
+    const float* from = t.first ? sequence_state(p, t, w.h, w.seg) : first_state(p, w.unit, w.seg);
     const int parts = t.first || p.parts < 2 ? 1 : 2;
 #pragma unroll 1
     for (int k = 0; k < parts; ++k) fetch_state(p, r, k == 0 ? from : from + size, k > 0);

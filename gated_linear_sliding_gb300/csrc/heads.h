@@ -79,6 +79,9 @@ struct DecayPass {
     float out_scale, in_scale;
     const float *log_decay, *init;
     float* fin;
+    // Where `fin` overwrites `init`, of a packed batch of many sequences: copies of the first states of the sequences
+    // that lie across the cuts between segments, [nseg - 1, Hkv, dk, dv] (null: there are none, read `init`).
+    const float* kept;
     // The segments' first states, [units, nseg, dk, dv]; with `parts` (two segments of a dense batch, where the
     // one's end is the other's beginning) the sum of a unit's first `parts` entries.
     const float* recs;

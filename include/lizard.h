@@ -611,7 +611,9 @@ int lizard_decay_attn_kernel(const lizard_decay_dims* dims);
 
 /* Bytes of device workspace lizard_decay_attn_fwd needs (0 for invalid dims): the status word, plus,
  * where there are too few sequences and heads to fill the GPU and the time axis is cut into segments,
- * one fp32 state for each of them. */
+ * one fp32 state for each of them and for each of the first states that a call with s_out == s0 has to
+ * copy (those of a dense batch, or of the packed sequences that may lie across a cut: fewer than there
+ * are segments). */
 size_t lizard_decay_attn_fwd_workspace(const lizard_decay_dims* dims);
 
 /* For each sequence and state head h, with query heads q of that state:
@@ -632,7 +634,8 @@ lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q
                                     const int64_t* cu_seqlens, void* o, float* s_out,
                                     void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of device workspace lizard_decay_attn_bwd needs (0 for invalid dims). */
+/* Bytes of device workspace lizard_decay_attn_bwd needs (0 for invalid dims): the status word, plus, with
+ * segments, two fp32 states for each of them, and the copies as above for ds0 == ds_out. */
 size_t lizard_decay_attn_bwd_workspace(const lizard_decay_dims* dims);
 
 /* Exact gradient of lizard_decay_attn_fwd's o (and of s_out) from its inputs (nothing is kept by the

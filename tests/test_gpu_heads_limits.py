@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import heads as H
-from test_gpu_heads import Draw, check
+from test_gpu_heads import Draw, check, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,46 @@ def test_rope_without_epsilon(lz, dtype, Hq, Hkv, d, rot):
         (rdx, rdw), (mdx, mdw) = (H.rope_bwd(xn, w, a, False, True, 0.0, dyn, absolute=t) for t in (False, True))
         check(g["d" + n].reshape(xn.shape), rdx, mdx, 2 * rounds, "d" + n)
         check(g["dw_" + n], rdw, mdw, rounds + B * L * xn.shape[1], "dw_" + n)
+
+
+# ----------------------------------------------------------------------------------- decays
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 2])
+def test_states_in_place_of_many_sequences(lz, dtype, G):
+    """More sequences than cuts, some over one cut or several, some that begin or end at one, empty ones among
+    them: states in place give the bits of two arrays."""
+    D = Draw(14 + G, dtype)
+    lens = [64, 0, 30, 34, 0, 1, 126, 1, 64, 320, 63, 2] + [3] * 100 + [0, 200, 64, 90]
+    L, Hkv, d, cu = sum(lens), 2, 64, offsets(lens)
+    q, k, v, do = (D(1, L, h, d)[0] for h in (G * Hkv, Hkv, Hkv, G * Hkv))
+    l = D.dev([-0.003, -0.9])[0]
+    s0, ds = (D(len(lens), Hkv, d, d, dtype=torch.float32)[0] for _ in range(2))
+    two, dtwo = torch.full_like(s0, 77.0), torch.full_like(s0, 77.0)
+    o = lz.lizard_decay_attn_fwd(q, k, v, l, s0=s0, s_out=two, cu_seqlens=cu)
+    g = lz.lizard_decay_attn_bwd(q, k, v, l, do, s0=s0, ds_out=ds, ds0=dtwo, cu_seqlens=cu)
+    for _ in range(5):
+        one, done = s0.clone(), ds.clone()
+        o1 = lz.lizard_decay_attn_fwd(q, k, v, l, s0=one, s_out=one, cu_seqlens=cu)
+        g1 = lz.lizard_decay_attn_bwd(q, k, v, l, do, s0=s0, ds_out=done, ds0=done, cu_seqlens=cu)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o1) and torch.equal(one, two) and torch.equal(done, dtwo)
+        assert all(torch.equal(g[n], g1[n]) for n in ("dq", "dk", "dv"))
+
+
+def test_a_workspace_of_just_the_bytes_asked_for(lz):
+    """Many sequences with states in place: nothing behind the workspace's last byte is written."""
+    D = Draw(16, "bf16")
+    lens = [5] * 300 + [1000]
+    L, d, cu = sum(lens), 64, offsets(lens)
+    q, k, v, do = (D(1, L, h, d)[0] for h in (2, 1, 1, 2))
+    l = D.dev([-0.003])[0]
+    s0 = D(len(lens), 1, d, d, dtype=torch.float32)[0]
+    dims = lz.lizard_decay_dims(1, L, 2, 1, d, d, len(lens), scale=1.0, dtype=lz.LIZARD_BF16)
+    for need, call in ((lz.lizard_decay_attn_fwd_workspace(dims), lambda s, w: lz.lizard_decay_attn_fwd(q, k, v, l, s0=s, s_out=s, cu_seqlens=cu, workspace=w)),
+                       (lz.lizard_decay_attn_bwd_workspace(dims), lambda s, w: lz.lizard_decay_attn_bwd(q, k, v, l, do, ds_out=s, ds0=s, cu_seqlens=cu, workspace=w))):
+        ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        call(s0.clone(), ws[:need])
+        assert lz.lizard_read_device_status(ws) == 0 and (ws[need:] == 0x5A).all()
