@@ -31,11 +31,11 @@ __device__ __forceinline__ Pieces pieces_of(int n) {
     return q;
 }
 
-// Rows [0, n) of a tile of `cols` columns as fp32 with row distance `ld` in shared memory; other places 0.
-// Pieces of V values, eight of a thread under way.  (In line: as a function its callers spill, 16 heads on 8 of 128 in
+// Rows [0, n) of a tile of `cols` columns as fp32 with row distance `ld` in shared memory; other places 0.  *zero, if
+// asked for, becomes NaN when this thread's values are not all finite.  Pieces of V values, eight of a thread under way.  (In line: as a function its callers spill, 16 heads on 8 of 128 in
 // fp32, 8 x 1024 tokens, forward and gradients: 2266 against 1949 us.)
 template <typename T, int V>
-__device__ __forceinline__ void load_pieces(float* to, int ld, const T* from, int64_t dist, int n, int cols, Pieces q) {
+__device__ __forceinline__ void load_pieces(float* to, int ld, const T* from, int64_t dist, int n, int cols, Pieces q, float* zero) {
     while (q.r < kTile) {
         float v[8][V];
         int at[8];
@@ -52,15 +52,22 @@ __device__ __forceinline__ void load_pieces(float* to, int ld, const T* from, in
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (at[u] >= 0) Vec<V>::st(to + at[u], v[u]);
+        if (zero != nullptr) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) *zero = fmaf(v[u][i], 0.0f, *zero);
+        }
     }
 }
-__device__ __forceinline__ void load_rows(const DecayPass& p, float* to, int ld, const void* base, int64_t at, int64_t dist, int n, int cols, const Pieces& q) {
+__device__ __forceinline__ void load_rows(const DecayPass& p, float* to, int ld, const void* base, int64_t at, int64_t dist, int n, int cols, const Pieces& q,
+                                          float* zero = nullptr) {
     if (p.f32) {
-        if (p.fours) load_pieces<float, 4>(to, ld, (const float*)base + at, dist, n, cols, q);
-        else load_pieces<float, 1>(to, ld, (const float*)base + at, dist, n, cols, q);
+        if (p.fours) load_pieces<float, 4>(to, ld, (const float*)base + at, dist, n, cols, q, zero);
+        else load_pieces<float, 1>(to, ld, (const float*)base + at, dist, n, cols, q, zero);
     } else {
-        if (p.fours) load_pieces<__nv_bfloat16, 4>(to, ld, (const __nv_bfloat16*)base + at, dist, n, cols, q);
-        else load_pieces<__nv_bfloat16, 1>(to, ld, (const __nv_bfloat16*)base + at, dist, n, cols, q);
+        if (p.fours) load_pieces<__nv_bfloat16, 4>(to, ld, (const __nv_bfloat16*)base + at, dist, n, cols, q, zero);
+        else load_pieces<__nv_bfloat16, 1>(to, ld, (const __nv_bfloat16*)base + at, dist, n, cols, q, zero);
     }
 }
 
@@ -211,7 +218,9 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayPass p, floa
 
 // One pass over a segment's tiles, 64 columns of z to a CTA; M: rows of the state by 64.  Bound by the fp32 pipes and
 // the latency between barriers: a thread has 4 x 4 pairs, 4 x 4 outputs and 4 M x 4 of the state, 16 products for each
-// two or three 16-byte reads of shared memory.  8192 tokens of 16 heads on 8, 128 values, fp32: 593 us forwards.
+// two or three 16-byte reads of shared memory.  8192 tokens of 16 heads on 8, 128 values, fp32: 595 us forwards.
+// A masked pair adds 0 times its z, so a tile whose z is not all finite takes its pairs one by one (looking for that
+// costs up to 1.6 %: gradients of 8 x 1024 tokens 1485 -> 1510 us).
 template <int M, bool REV>
 __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
     extern __shared__ float sm[];
@@ -251,6 +260,7 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
         }
         if (threadIdx.x < t.n) fs[threadIdx.x] = pw[REV ? threadIdx.x + 1 : t.n - 1 - threadIdx.x] * p.in_scale;
         const int64_t row = w.b * p.seqs.L + t.t0;
+        float zero = 0.0f;  // NaN where z has a value that is not finite
         for (int a = 0; a < p.gx; ++a) {
             float o[4][4] = {};
             for (int g = 0; g < p.gy; ++g) {
@@ -258,7 +268,8 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
                 if (g == 0) load_rows(p, xs, ldx, p.x, row * p.ldx + (w.h * p.gx + a) * p.dx, p.ldx, t.n, p.dx, qx);
                 if (a == 0) {
                     load_rows(p, ys, ldx, p.y, row * p.ldy + head * p.dx, p.ldy, t.n, p.dx, qx);
-                    load_rows(p, zs, ZS, p.z, row * p.ldz + head * p.dz + z0, p.ldz, t.n, zn, qz);
+                    zero = 0.0f;
+                    load_rows(p, zs, ZS, p.z, row * p.ldz + head * p.dz + z0, p.ldz, t.n, zn, qz, &zero);
                 }
                 __syncthreads();
                 // the pairs of the tile: rows ty + 16 i, columns tx + 16 j; blocks that are all masked are left out
@@ -320,30 +331,46 @@ __global__ void __launch_bounds__(NT) decay_pass_kernel(const DecayPass p) {
                         for (int c = 0; c < 4; ++c) o[i][c] *= f;
                     }
                 }
-                __syncthreads();
+                const bool finite = __syncthreads_and(zero == 0.0f);
+                if (finite) {
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb)
+                    for (int kb = 0; kb < 4; ++kb)
 #pragma unroll 2
-                    for (int k = 16 * kb; k < 16 * kb + 16; k += 4) {
-                        float4 pv[4], zv[4];
+                        for (int k = 16 * kb; k < 16 * kb + 16; k += 4) {
+                            float4 pv[4], zv[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (REV ? kb >= i : kb <= i) pv[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * PS + k);
-                            zv[i] = *reinterpret_cast<const float4*>(zs + (k + i) * ZS + tx * 4);
-                        }
+                            for (int i = 0; i < 4; ++i) {
+                                if (REV ? kb >= i : kb <= i) pv[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * PS + k);
+                                zv[i] = *reinterpret_cast<const float4*>(zs + (k + i) * ZS + tx * 4);
+                            }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (REV ? kb < i : kb > i) continue;
-                            const float pk[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
+                            for (int i = 0; i < 4; ++i) {
+                                if (REV ? kb < i : kb > i) continue;
+                                const float pk[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
 #pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                o[i][0] = fmaf(pk[m], zv[m].x, o[i][0]);
-                                o[i][1] = fmaf(pk[m], zv[m].y, o[i][1]);
-                                o[i][2] = fmaf(pk[m], zv[m].z, o[i][2]);
-                                o[i][3] = fmaf(pk[m], zv[m].w, o[i][3]);
+                                for (int m = 0; m < 4; ++m) {
+                                    o[i][0] = fmaf(pk[m], zv[m].x, o[i][0]);
+                                    o[i][1] = fmaf(pk[m], zv[m].y, o[i][1]);
+                                    o[i][2] = fmaf(pk[m], zv[m].z, o[i][2]);
+                                    o[i][3] = fmaf(pk[m], zv[m].w, o[i][3]);
+                                }
                             }
                         }
+                } else {  // 0 times such a value would be NaN: masked pairs are left out one by one
+#pragma unroll 1
+                    for (int k = 0; k < kTile; ++k) {
+                        const float4 z = *reinterpret_cast<const float4*>(zs + k * ZS + tx * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (REV ? k < ty + 16 * i : k > ty + 16 * i) continue;
+                            const float w = ps[(ty + 16 * i) * PS + k];
+                            o[i][0] = fmaf(w, z.x, o[i][0]);
+                            o[i][1] = fmaf(w, z.y, o[i][1]);
+                            o[i][2] = fmaf(w, z.z, o[i][2]);
+                            o[i][3] = fmaf(w, z.w, o[i][3]);
+                        }
                     }
+                }
                 if (a == p.gx - 1) {  // every reader of the state is past the barrier above
                     const float keep = g == 0 ? pw[t.n] : 1.0f;
                     float acc[M][4][4];

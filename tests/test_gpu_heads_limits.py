@@ -93,3 +93,61 @@ def test_a_workspace_of_just_the_bytes_asked_for(lz):
         ws[:256] = 0
         call(s0.clone(), ws[:need])
         assert lz.lizard_read_device_status(ws) == 0 and (ws[need:] == 0x5A).all()
+
+
+def same_where_finite(got, ref, mag, n, what, part):
+    """The definition's values where it has them; where it has none (infinity, NaN), none either."""
+    at = np.isfinite(ref)
+    assert not np.isfinite(got.double().cpu().numpy()[~at]).any(), f"{what}: finite where the definition is not"
+    keep = torch.from_numpy(at).cuda()
+    check(got[keep], ref[at], mag[at], n, what, part)
+
+
+NOT_FINITE = [
+    # dtype, B, L, Hq, Hkv, dk, dv, log_decay: fp32 arithmetic
+    ("f32", 1, 150, 4, 2, 40, 72, [-0.02, -0.9]),
+    ("f32", 1, 150, 3, 3, 33, 57, [-0.02, -0.9, 0.0]),
+    ("bf16", 1, 200, 2, 1, 136, 24, [-0.1]),
+]
+
+
+@pytest.mark.parametrize("kind", [float("nan"), float("inf")])
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("dtype,B,L,Hq,Hkv,dk,dv,decay", NOT_FINITE)
+def test_values_that_are_not_finite_reach_what_the_definition_says(lz, dtype, B, L, Hq, Hkv, dk, dv, decay, which, kind):
+    """One value of q, k, v or do that is not finite, early and late in a chunk: results that the definition
+    leaves finite (tokens before v's, tokens after do's, other heads) have its values."""
+    D = Draw(L + dk, dtype)
+    x = {n: D(B, L, h, d) for n, h, d in (("q", Hq, dk), ("k", Hkv, dk), ("v", Hkv, dv), ("do", Hq, dv))}
+    l, ln = D.dev(np.asarray(decay))
+    (s0, s0n), (ds, dsn) = (D(B, Hkv, dk, dv, dtype=torch.float32) for _ in range(2))
+    dims = lz.lizard_decay_dims(B, L, Hq, Hkv, dk, dv, dtype=lz.LIZARD_F32 if dtype == "f32" else lz.LIZARD_BF16)
+    tensor = lz.lizard_decay_attn_kernel(dims) == 1
+    part = 2.0 ** -8 + 2.0 ** -16 if tensor else 0.0
+    rounds, scale = 464 + 2 * (dk + dv) + L // 16, 0.37
+    for t in (0, 1, 62, 64, 127, 131, L - 1):
+        b, h = t % B, t % Hkv
+        ends = {n: (a.clone(), w.copy()) for n, (a, w) in x.items()}
+        dev, host = ends[which]
+        head = h * (dev.shape[2] // Hkv) + t % (dev.shape[2] // Hkv)
+        dev[b, t, head, t % dev.shape[3]] = kind
+        host[b, t, head, t % dev.shape[3]] = kind
+        s_out, ds0 = torch.empty_like(s0), torch.empty_like(s0)
+        args = [ends[n][0] for n in ("q", "k", "v")]
+        o = lz.lizard_decay_attn_fwd(*args, l, scale=scale, s0=s0, s_out=s_out)
+        g = lz.lizard_decay_attn_bwd(*args, l, ends["do"][0], scale=scale, s0=s0, ds_out=ds, ds0=ds0)
+        # the row that holds the value, and the state heads around it
+        heads = slice(max(0, h - 1), h + 2)
+        G = Hq // Hkv
+        qheads = slice(heads.start * G, min(heads.stop, Hkv) * G)
+        q, k, v, do = (ends[n][1][b][:, qheads if n in ("q", "do") else heads] for n in ("q", "k", "v", "do"))
+        one = (q, k, v, ln[heads], s0n[b, heads], scale)
+        with np.errstate(invalid="ignore"):
+            (ro, rs), (mo, ms) = (H.decay_fwd(*one, absolute=a) for a in (False, True))
+            rg, mg = (H.decay_bwd(*one, do, dsn[b, heads], absolute=a) for a in (False, True))
+        same_where_finite(o[b, :, qheads], ro, mo, rounds, f"o {t}", part)
+        same_where_finite(s_out[b, heads], rs, ms, rounds, f"s_out {t}", 2.0 ** -17 if tensor else 0.0)
+        for n, r, m in zip(("dq", "dk", "dv"), rg, mg):
+            same_where_finite(g[n][b][:, qheads if n == "dq" else heads], r, m, rounds, f"{n} {t}", part)
+        same_where_finite(ds0[b, heads], rg[3], mg[3], rounds, f"ds0 {t}", 2.0 ** -17 if tensor else 0.0)
+
