@@ -32,8 +32,9 @@ __device__ __forceinline__ Pieces pieces_of(int n) {
 }
 
 // Rows [0, n) of a tile of `cols` columns as fp32 with row distance `ld` in shared memory; other places 0.  *zero, if
-// asked for, becomes NaN when this thread's values are not all finite.  Pieces of V values, eight of a thread under way.  (In line: as a function its callers spill, 16 heads on 8 of 128 in
-// fp32, 8 x 1024 tokens, forward and gradients: 2266 against 1949 us.)
+// asked for, becomes NaN when this thread's values are not all finite.  Pieces of V values, eight of a thread under way.
+// (In line: as a function its callers spill, 16 heads on 8 of 128 in fp32, 8 x 1024 tokens, forward and gradients: 2266
+// against 1949 us.)
 template <typename T, int V>
 __device__ __forceinline__ void load_pieces(float* to, int ld, const T* from, int64_t dist, int n, int cols, Pieces q, float* zero) {
     while (q.r < kTile) {

@@ -47,8 +47,8 @@ struct Layout {
     static constexpr uint32_t ST = KT + 4 * kBox;
     static constexpr uint32_t TABLE = ST + 4 * kBox;     // powers 0 .. 128, and the columns' factors
     static constexpr uint32_t BARS = TABLE + (132 + 128) * 4;
-    static constexpr uint32_t BYTES = BARS + 400 + 1024;
-    static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
+    static constexpr uint32_t BYTES = BARS + 376 + 4 * kMostNoted + 1024;
+    static_assert(BYTES <= 227 * 1024 && kByTokensBytes <= TABLE, "shared memory of a CTA");
 };
 // Several tiles of x for each of y and z, or one.  Then one stage of x is enough (its last reader is done long before
 // the chunk is) and leaves room for a third of y and z, whose copies otherwise wait for the chunk before (16 heads of
@@ -70,9 +70,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     uint64_t *x_full = bar, *x_free = bar + 3, *yz_full = bar + 6, *yz_free = bar + 10, *zz_full = bar + 14, *s_full = bar + 18,
              *p_full = bar + 20, *xs_full = bar + 22, *pv_done = bar + 24, *o_free = bar + 26, *kt_full = bar + 28,
              *h_done = bar + 29, *st_full = bar + 30, *xs_done = bar + 31, *drained = bar + 32,
-             *first_free = bar + 35, *third_full = bar + 36;
+             *first_free = bar + 35, *third_full = bar + 36, *agreed = bar + 37;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 38);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    Seg* seg = reinterpret_cast<Seg*>(bar + 41);  // (for walk_by_tokens: in registers till then it makes the roles spill)
+    const Notes notes{abort + 1, abort + 2, abort + 3, abort + 17, agreed};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
     const Seg w = seg_of<false>(p);
@@ -108,8 +110,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         mbar_init(xs_done, 1);
         mbar_init(first_free, 1);
         mbar_init(third_full, 32 * kStateWarps);
+        mbar_init(agreed, 32 * kStateWarps);
         for (int i = 0; i < 3; ++i) mbar_init(&drained[i], 1);
         *abort = 0;
+        *seg = w;
+        *notes.found = 0;
+        *notes.count = 0;
         fence_mbar_init();
     }
     if (warp == 17) {
@@ -294,17 +300,19 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         float keep = 1.0f;  // of the chunk before
         uint32_t yi = 0, ci = 0;
         bool ok = true, was_last = false;
-        int was_seq = 0;
+        int was_seq = 0, ends = 1;  // the sequence under way is the ends-th
         grid_dep_wait();
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (ci > 0) {
                 if (!wait.all(h_done, (yi - 1) & 1, 110) || !wait.all(xs_done, (ci - 1) & 1, 111)) { ok = false; break; }
                 tc_fence_after();
-                if (was_last) leave_state(p, sr, w.h, was_seq, keep);
+                if (was_last && may_leave(notes, wait, sr, nz, ends++, &ok)) leave_state(p, sr, w.h, was_seq, keep);
+                if (!ok) break;
             }
             const bool fresh = t.first || ci == 0;
             if (fresh) begin_state(p, sr, w, t);
-            pass_state(sr, base + SM::ST, nz, slow ? pw[mid + 1] : 1.0f, fresh, keep);
+            if (!pass_state(sr, base + SM::ST, nz, slow ? pw[mid + 1] : 1.0f, fresh, keep)) *notes.found = ends;
+            if (sr.in == 0) *notes.entered = max(walk.begin, walk.lo);
             keep = pw[t.n];
             fence_async_smem();
             tc_fence_before();
@@ -338,11 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             was_seq = t.seq;
             ++ci;
         }
-        if (ok && ci > 0 && was_last && p.fin != nullptr) {
-            if (wait.all(h_done, (yi - 1) & 1, 114)) {
-                tc_fence_after();
-                leave_state(p, sr, w.h, was_seq, keep);
-            }
+        if (ok && ci > 0 && wait.all(h_done, (yi - 1) & 1, 114)) {
+            tc_fence_after();
+            if (may_leave(notes, wait, sr, nz, ends, &ok) && was_last) leave_state(p, sr, w.h, was_seq, keep);
         }
     } else {
         // weights of pairs and outputs: row `r` of the tile of x
@@ -477,6 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
+    if (*abort != 0) return;
+    for (int i = 0; i < *notes.count; ++i) walk_by_tokens<false>(p, *seg, reinterpret_cast<float*>(sm), notes.at[i], i == kMostNoted - 1);
 }
 
 // ------------------------------------------------------------------------- segments' end states

@@ -45,8 +45,8 @@ struct GradSmem {
     static constexpr uint32_t ST = KT + 4 * kBox;
     static constexpr uint32_t TABLE = ST + 4 * kBox;  // powers 0 .. 64, and the columns' factors
     static constexpr uint32_t BARS = TABLE + (68 + 64) * 4;
-    static constexpr uint32_t BYTES = BARS + 400 + 1024;
-    static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
+    static constexpr uint32_t BYTES = BARS + 376 + 4 * kMostNoted + 1024;
+    static_assert(BYTES <= 227 * 1024 && kByTokensBytes <= TABLE, "shared memory of a CTA");
 };
 
 template <bool three>
@@ -62,9 +62,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     uint64_t *b_full = bar, *b_free = bar + 6, *kv_full = bar + 12, *kv_free = bar + 13, *s_full = bar + 14, *p_full = bar + 15, *pv_done = bar + 16,
              *xs_full = bar + 17, *o_free = bar + 19, *zz_full = bar + 21, *kt_full = bar + 23, *h_done = bar + 24, *st_full = bar + 25,
              *xs_done = bar + 26, *staged = bar + 27, *left = bar + 28, *late = bar + 29, *drained = bar + 30, *chunk_done = bar + 33;
-    uint64_t *first_free = bar + 34, *third_full = bar + 35;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 36);
+    uint64_t *first_free = bar + 34, *third_full = bar + 35, *agreed = bar + 36;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 38);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    Seg* seg = reinterpret_cast<Seg*>(bar + 41);  // (for walk_by_tokens: in registers till then it makes the roles spill)
+    const Notes notes{abort + 1, abort + 2, abort + 3, abort + 17, agreed};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool leader = lane == 0;
     const Seg w = seg_of<false>(p);
@@ -102,8 +104,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         mbar_init(xs_done, 1);
         mbar_init(staged, 32 * kMathWarps);
         mbar_init(left, kMathWarps);
+        mbar_init(agreed, 32 * kStateWarps);
         for (int i = 0; i < 3; ++i) mbar_init(&drained[i], 1);
         *abort = 0;
+        *seg = w;
+        *notes.found = 0;
+        *notes.count = 0;
         fence_mbar_init();
     }
     if (warp == 17) {
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
         float keep = 1.0f;  // of the chunk before
         uint32_t it = 0, ui = 0, ci = 0, q = 0;
         bool ok = true, was_last = false;
-        int was_seq = 0;
+        int was_seq = 0, ends = 1;  // the sequence under way is the ends-th
         grid_dep_wait();
         while (ok && walk.next(p.seqs, w.b, &t)) {
             if (ci > 0) {
@@ -307,11 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
                     break;
                 }
                 tc_fence_after();
-                if (was_last) leave_state(p, sr, w.h, was_seq, keep);
+                if (was_last && may_leave(notes, wait, sr, nz, ends++, &ok)) leave_state(p, sr, w.h, was_seq, keep);
+                if (!ok) break;
             }
             const bool fresh = t.first || ci == 0;
             if (fresh) begin_state(p, sr, w, t);
-            pass_state(sr, base + SM::ST, nz, slow ? power(l2, t.n - 1 - mid) : 1.0f, fresh, keep);
+            if (!pass_state(sr, base + SM::ST, nz, slow ? power(l2, t.n - 1 - mid) : 1.0f, fresh, keep)) *notes.found = ends;
+            if (sr.in == 0) *notes.entered = min(walk.end, walk.hi);
             keep = pw[t.n];
             fence_async_smem();
             tc_fence_before();
@@ -351,11 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
             was_seq = t.seq;
             ++ci;
         }
-        if (ok && ci > 0 && was_last && p.fin != nullptr) {
-            if (wait.all(h_done, (ui - 1) & 1, 147)) {
-                tc_fence_after();
-                leave_state(p, sr, w.h, was_seq, keep);
-            }
+        if (ok && ci > 0 && wait.all(h_done, (ui - 1) & 1, 147)) {
+            tc_fence_after();
+            if (may_leave(notes, wait, sr, nz, ends, &ok) && was_last) leave_state(p, sr, w.h, was_seq, keep);
         }
     } else {
         // pairs: row r = (head, token i) of an item; gradients: value r, 32 of the chunk's tokens
@@ -495,6 +501,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_grads_kernel(const __gri
     if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tb, 512);
+    }
+    if (*abort != 0 || *notes.count == 0) return;
+    DecayPass k = p;  // dk's: the same with x and y from the other side of the state.  First, since dv's may overwrite `init`.
+    k.x = p.v, k.y = p.z, k.z = p.y, k.out = g.dk_out;
+    k.ldx = p.ldv, k.ldy = p.ldz, k.ldz = p.ldy, k.ldout = g.lddk;
+    k.dx = p.dz, k.dz = p.dx;
+    k.transposed = true;
+    k.fin = nullptr;
+    for (int i = 0; i < *notes.count; ++i) {
+        walk_by_tokens<true>(k, *seg, reinterpret_cast<float*>(sm), notes.at[i], i == kMostNoted - 1);
+        walk_by_tokens<true>(p, *seg, reinterpret_cast<float*>(sm), notes.at[i], i == kMostNoted - 1);
     }
 }
 

@@ -625,10 +625,11 @@ size_t lizard_decay_attn_fwd_workspace(const lizard_decay_dims* dims);
  *   s_out    likewise or NULL: the state after the last token (s0's, or zero, for an empty
  *            sequence); may be the same array as s0;
  *   workspace, ws_bytes >= lizard_decay_attn_fwd_workspace(dims).
- * A value that is not finite reaches results of its own sequence and state head only: those that the
- * formula says, but on the tensor cores also those of up to 127 tokens before it (all products of a
- * chunk of tokens are formed): there what pads a batch has to be finite.  On the tensor cores terms carry factors of up to 2^32 either way in between:
- * states and scores beyond 1e28 may overflow there. */
+ * A value that is not finite reaches the results that the formula says and no others, so padding may
+ * hold anything (NaN may stand where the formula gives an infinity).  On the tensor cores a sequence
+ * with such a value is done again in fp32, token by token, where it shares a segment of the time axis
+ * with it: microseconds for each token.  Terms carry factors of up to 2^32 either way in between
+ * there: states and scores beyond 1e28 may overflow. */
 lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q, const void* k,
                                     const void* v, const float* log_decay, const float* s0,
                                     const int64_t* cu_seqlens, void* o, float* s_out,

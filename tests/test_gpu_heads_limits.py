@@ -104,10 +104,18 @@ def same_where_finite(got, ref, mag, n, what, part):
 
 
 NOT_FINITE = [
-    # dtype, B, L, Hq, Hkv, dk, dv, log_decay: fp32 arithmetic
+    # dtype, B, L, Hq, Hkv, dk, dv, log_decay: fp32 arithmetic, then tensor cores with two heads to a tile, an odd number
+    # of them, and one (chunks of 128 tokens), decays within the split of their factors and beyond it, segments of one
+    # chunk and of several
     ("f32", 1, 150, 4, 2, 40, 72, [-0.02, -0.9]),
     ("f32", 1, 150, 3, 3, 33, 57, [-0.02, -0.9, 0.0]),
     ("bf16", 1, 200, 2, 1, 136, 24, [-0.1]),
+    ("bf16", 1, 150, 4, 2, 64, 128, [-0.02, -0.9]),
+    ("bf16", 1, 150, 10, 2, 40, 72, [-0.9, -0.02]),
+    ("bf16", 1, 150, 20, 2, 64, 64, [-0.02, -0.9]),
+    ("bf16", 1, 300, 2, 2, 128, 64, [-0.02, -0.9]),
+    ("bf16", 1, 450, 76, 76, 32, 32, np.resize([-0.02, -0.9], 76)),
+    ("bf16", 4, 200, 60, 20, 32, 32, np.resize([-0.02, -0.9], 20)),
 ]
 
 
@@ -151,3 +159,87 @@ def test_values_that_are_not_finite_reach_what_the_definition_says(lz, dtype, B,
             same_where_finite(g[n][b][:, qheads if n == "dq" else heads], r, m, rounds, f"{n} {t}", part)
         same_where_finite(ds0[b, heads], rg[3], mg[3], rounds, f"ds0 {t}", 2.0 ** -17 if tensor else 0.0)
 
+
+@pytest.mark.parametrize("G", [1, 2])
+def test_padding_that_is_not_finite(lz, G):
+    """A dense batch of ragged rows whose padding was never written: every token in front of it has the
+    definition's value."""
+    D = Draw(13, "bf16")
+    B, L, Hkv, d, lens = 3, 400, 2, 64, (130, 400, 1)
+    x, xn = zip(*(D(B, L, h, d) for h in (G * Hkv, Hkv, Hkv)))
+    l, ln = D.dev([-0.02, -0.9])
+    for b, n in enumerate(lens):
+        for t in x:
+            t[b, n:] = float("nan")
+    got = lz.lizard_decay_attn_fwd(*x, l)
+    for b, n in enumerate(lens):
+        one = (*(t[b, :n] for t in xn), ln, np.zeros((Hkv, d, d)), d ** -0.5)
+        ro, mo = (H.decay_fwd(*one, absolute=t)[0] for t in (False, True))
+        check(got[b, :n], ro, mo, 464 + 4 * d + n // 16, f"o {b}", 2.0 ** -8 + 2.0 ** -16)
+
+
+@pytest.mark.parametrize("G,Hkv", [(1, 2), (2, 2), (1, 80), (2, 80)])
+def test_states_in_place_around_values_that_are_not_finite(lz, G, Hkv):
+    """Sequences of which two hold such values, in segments and in one, states in place: the others keep their bits, and
+    all have those of two arrays."""
+    D = Draw(17 + G, "bf16")
+    lens = [70, 64, 0, 200, 130, 50]
+    L, d, cu = sum(lens), 64, offsets(lens)
+    q, k, v, do = (D(1, L, h, d)[0] for h in (G * Hkv, Hkv, Hkv, G * Hkv))
+    l = D.dev(np.resize([-0.003, -0.9], Hkv))[0]
+    s0, ds = (D(len(lens), Hkv, d, d, dtype=torch.float32)[0] for _ in range(2))
+    bv, bdo = v.clone(), do.clone()
+    bv[0, 300, :, 3] = float("nan")  # of sequence 3, tokens 134 to 333
+    bdo[0, 150, :, 5] = float("inf")
+    bv[0, 69, :, 1] = bdo[0, 69, :, 1] = float("inf")  # of sequence 0, tokens 0 to 69
+
+    def run(v, do, in_place):
+        a, b = s0.clone(), ds.clone()
+        a1, b1 = (a, b) if in_place else (torch.full_like(a, 77.0), torch.full_like(b, 77.0))
+        o = lz.lizard_decay_attn_fwd(q, k, v, l, s0=a, s_out=a1, cu_seqlens=cu)
+        g = lz.lizard_decay_attn_bwd(q, k, v, l, do, s0=s0, ds_out=b, ds0=b1, cu_seqlens=cu)
+        torch.cuda.synchronize()
+        return [o, g["dq"], g["dk"], g["dv"]], [a1, b1]
+
+    clean, states = run(v, do, False)
+    two, two_s = run(bv, bdo, False)
+    one, one_s = run(bv, bdo, True)
+    rows = torch.ones(L, dtype=torch.bool, device="cuda")
+    rows[134:334] = rows[:70] = False
+    others = [1, 2, 4, 5]
+    for a, b, c in zip(clean, two, one):
+        assert torch.equal(b.nan_to_num(99.0), c.nan_to_num(99.0)) and torch.equal(b.isnan(), c.isnan())
+        assert not torch.isfinite(b[:, 134:334]).all() and not torch.isfinite(b[:, :70]).all()
+        assert torch.equal(a[:, rows], b[:, rows])
+    for a, b, c in zip(states, two_s, one_s):
+        assert torch.equal(b.nan_to_num(99.0), c.nan_to_num(99.0)) and torch.equal(b.isnan(), c.isnan())
+        assert torch.equal(a[others], b[others]) and not torch.isfinite(b[3]).all() and not torch.isfinite(b[0]).all()
+
+
+def test_many_sequences_with_values_that_are_not_finite(lz):
+    """More of them in a segment than are noted one by one, states in place: the definition's values, infinities among
+    them, for all."""
+    D = Draw(19, "bf16")
+    G, Hkv, d, n, each = 2, 80, 32, 150, 3  # one segment a head
+    L, cu = n * each, offsets([each] * n)
+    (q, qn), (k, kn), (v, vn), (do, don) = (D(1, L, h, d) for h in (G * Hkv, Hkv, Hkv, G * Hkv))
+    l, ln = D.dev(np.resize([-0.003, -0.9], Hkv))
+    (s0, s0n), (ds, dsn) = (D(n, Hkv, d, d, dtype=torch.float32) for _ in range(2))
+    for t, a in ((v, vn), (do, don)):
+        t[0, 1:-30:each, :, 3] = float("inf")
+        a[0, 1:-30:each, :, 3] = np.inf
+    s, e = s0.clone(), ds.clone()
+    o = lz.lizard_decay_attn_fwd(q, k, v, l, scale=0.37, s0=s, s_out=s, cu_seqlens=cu)
+    g = lz.lizard_decay_attn_bwd(q, k, v, l, do, scale=0.37, s0=s0, ds_out=e, ds0=e, cu_seqlens=cu)
+    part = 2.0 ** -8 + 2.0 ** -16
+    for i in (0, 1, 63, 64, 65, 139, 140, 149):
+        at, heads = slice(each * i, each * i + each), slice(0, 3)
+        one = (qn[0, at, :3 * G], kn[0, at, heads], vn[0, at, heads], ln[heads], s0n[i, heads], 0.37)
+        with np.errstate(invalid="ignore"):
+            (ro, rs), (mo, ms) = (H.decay_fwd(*one, absolute=a) for a in (False, True))
+            rg, mg = (H.decay_bwd(*one, don[0, at, :3 * G], dsn[i, heads], absolute=a) for a in (False, True))
+        same_where_finite(o[0, at, :3 * G], ro, mo, 600, f"o {i}", part)
+        same_where_finite(s[i, heads], rs, ms, 600, f"s_out {i}", 2.0 ** -17)
+        for name, r, m in zip(("dq", "dk", "dv"), rg, mg):
+            same_where_finite(g[name][0, at, :3 * G] if name == "dq" else g[name][0, at, heads], r, m, 600, f"{name} {i}", part)
+        same_where_finite(e[i, heads], rg[3], mg[3], 600, f"ds0 {i}", 2.0 ** -17)
