@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import heads as H
-from test_gpu_heads import Draw, check, offsets
+from test_gpu_heads import U32, Draw, check, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +243,61 @@ def test_many_sequences_with_values_that_are_not_finite(lz):
         for name, r, m in zip(("dq", "dk", "dv"), rg, mg):
             same_where_finite(g[name][0, at, :3 * G] if name == "dq" else g[name][0, at, heads], r, m, 600, f"{name} {i}", part)
         same_where_finite(e[i, heads], rg[3], mg[3], 600, f"ds0 {i}", 2.0 ** -17)
+
+
+WHOLE = [
+    # B, L, Hq, Hkv, lens, token: states that leave from the walk itself (a packed batch; one segment; two that share an
+    # end), and from the ends and their join; with several query heads a state and with one
+    (1, 40, 2, 1, None, 3),
+    (1, 40, 1, 1, None, 3),
+    (1, 60, 2, 1, [20, 40], 25),
+    (2, 128, 80, 40, None, 70),
+    (2, 128, 40, 40, None, 70),
+    (1, 128, 2, 1, None, 5),
+    (1, 190, 2, 1, None, 70),
+    (1, 190, 1, 1, None, 70),
+]
+
+
+@pytest.mark.parametrize("B,L,Hq,Hkv,lens,token", WHOLE)
+def test_states_that_leave_keep_their_24_bits(lz, B, L, Hq, Hkv, lens, token):
+    """States of one token's product, on the tensor cores: every entry is a power of the decay times two values,
+    which two bf16 parts of the scaled row miss by up to 2^-17, three by up to 2^-26.
+    Roundings, in units of 2^-24 of the entry: the decay's log2 (a rounding and its constant's, of an exponent of
+    up to 0.19) 0.3, its product with a distance 0.2, the power (two units in the last place) 4, the row times it 1 and times
+    the scale 1, two cut-off additions of the parts 4: 11.  For each tile of 64 tokens that the state passes then (three
+    at most), and for its join, a power as the one above, its product and an addition: 7.  Together 39.  Two parts miss
+    the largest remainders by about 100, which is shown on the same row."""
+    d, l = 128, -0.003
+    rng = np.random.default_rng(L + Hq)
+    ln = np.float64(np.float32(l))
+    decay = torch.full((Hkv,), l, device="cuda")
+    n, cu = len(lens or []) or B, offsets(lens)
+    begin, end = (0, L) if lens is None else (lens[0], L)
+    G, h, b = Hq // Hkv, Hkv // 2, B - 1
+    seq = b if lens is None else 1
+    y, z = (torch.from_numpy(rng.normal(size=d).astype(np.float32)).to("cuda", torch.bfloat16) for _ in range(2))
+    units = 11 + 7 * 4
+    outer = torch.outer(y.double(), z.double()).cpu().numpy()
+
+    def close(got, far, scale):
+        ref = scale * np.exp(ln * far) * outer
+        off = np.abs(got.double().cpu().numpy() / ref - 1)
+        assert off.max() < units * U32, off.max() / U32
+        # the same from two parts of the row
+        row = (y.double() * scale * np.exp(ln * far)).float().cpu()
+        hi = row.bfloat16().float()
+        two = hi.double() + (row - hi).bfloat16().double()
+        assert (two / row.double() - 1).abs().max() > units * U32
+
+    q, k, v, do = (torch.zeros(B, L, m, d, dtype=torch.bfloat16, device="cuda") for m in (Hq, Hkv, Hkv, Hq))
+    k[b, token, h], v[b, token, h] = y, z
+    q[b, token, h * G], do[b, token, h * G] = y, z
+    s_out, ds0 = (torch.full((n, Hkv, d, d), 77.0, device="cuda") for _ in range(2))
+    assert lz.lizard_decay_attn_kernel(lz.lizard_decay_dims(B, L, Hq, Hkv, d, d, dtype=lz.LIZARD_BF16)) == 1
+    lz.lizard_decay_attn_fwd(q, k, v, decay, s_out=s_out, cu_seqlens=cu)
+    lz.lizard_decay_attn_bwd(q, k, v, decay, do, scale=0.37, ds0=ds0, cu_seqlens=cu)
+    close(s_out[seq, h], end - 1 - token, 1.0)
+    close(ds0[seq, h], token + 1 - begin, np.float64(np.float32(0.37)))
+    s_out[seq, h] = ds0[seq, h] = 0
+    assert not s_out.any() and not ds0.any()
