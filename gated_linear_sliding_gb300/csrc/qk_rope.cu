@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
 #pragma unroll
                         for (int e = 1; e < H; ++e) s2 = fma2(xp.b[e], xp.b[e], fma2(xp.a[e], xp.a[e], s2));
                         float ss = sum2(s2);
-                        
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1)
                             if (o < p.lph) ss += __shfl_xor_sync(~0u, ss, o);
@@ -301,10 +300,9 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                                 c2 = fma2(y.b[e], xp.b[e], fma2(y.a[e], xp.a[e], c2));
                             }
                             float c = sum2(c2);
-                            
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            if (o < p.lph) c += __shfl_xor_sync(~0u, c, o);
+                            for (int o = 16; o > 0; o >>= 1)
+                                if (o < p.lph) c += __shfl_xor_sync(~0u, c, o);
                             c *= -inv_d * rs * rs;
                             const f2 cc = pack(c, c);
 #pragma unroll
