@@ -253,8 +253,6 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                         for (int o = 16; o > 0; o >>= 1)
                             if (o < p.lph) ss += __shfl_xor_sync(~0u, ss, o);
                         rs = rsqrtf(fmaf(ss, inv_d, a.eps));
-                        // (a lane behind the last head holds zeros: with eps 0 the weights' sums would take 0 times infinity)
-                        if (BWD && h >= hi) rs = 0.0f;
                     }
                     const f2 rs2 = pack(rs, rs);
                     Pairs<E> n;  // what turns
@@ -293,8 +291,10 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const RopeArgs a, const Ro
                             f2 c2 = pack(0.0f, 0.0f);
 #pragma unroll
                             for (int e = 0; e < H; ++e) {
-                                dw[part].a[e] = fma2(y.a[e], xp.a[e], dw[part].a[e]);
-                                dw[part].b[e] = fma2(y.b[e], xp.b[e], dw[part].b[e]);
+                                if (h < hi) {  // (behind the last head lie zeros, and with eps 0 rs is infinite there)
+                                    dw[part].a[e] = fma2(y.a[e], xp.a[e], dw[part].a[e]);
+                                    dw[part].b[e] = fma2(y.b[e], xp.b[e], dw[part].b[e]);
+                                }
                                 y.a[e] = mul2(y.a[e], wp.a[e]);
                                 y.b[e] = mul2(y.b[e], wp.b[e]);
                                 c2 = fma2(y.b[e], xp.b[e], fma2(y.a[e], xp.a[e], c2));
