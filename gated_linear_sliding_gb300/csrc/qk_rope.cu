@@ -6,6 +6,7 @@
 // Each value is read and written once: 8192 tokens of 32 + 8 heads of 128 take 39 us, of which HBM needs 25; what else
 // it is bound by is the issue of instructions, 54 % of the slots, with 16 warps a SM, and the wait for a token's loads.
 // Weights folded into cosine and sine take fewer instructions and more registers, and 41 us.
+// The gradients' kernels spill (112 bytes a thread in the main form): a warp holds the weights' sums of queries and of keys.
 // A warp takes one token and walks its heads.  The token's
 // cosines and sines are made by the warp's lanes once, lie in shared memory, and go to registers for all heads; a
 // lane holds the same pairs of each head (both members, so the rotation needs no exchange), and as few lanes as that

@@ -605,8 +605,11 @@ typedef struct {
 } lizard_decay_dims;
 
 /* Which kernels serve these sizes: 1 = tensor cores (bf16, dk and dv multiples of 8 up to 128, token
- * distances multiples of 8), 0 = fp32 arithmetic (every other shape), -1 = invalid sizes.  Pure host
- * query. */
+ * distances multiples of 8), 0 = fp32 arithmetic (every other shape; 5 to 20 times the time: rows that
+ * are no multiple of 8 values apart are worth copying), -1 = invalid sizes.  On the tensor cores the
+ * weights of pairs of tokens and a copy of the state are rounded to bf16 on their way into o, dq, dk
+ * and dv (2^-8 of the terms; in the mean 2.35e-3 of a result, 1.66e-3 of which is its own rounding);
+ * states are fp32 throughout and keep their 24 bits.  Pure host query. */
 int lizard_decay_attn_kernel(const lizard_decay_dims* dims);
 
 /* Bytes of device workspace lizard_decay_attn_fwd needs (0 for invalid dims): the status word, plus,
