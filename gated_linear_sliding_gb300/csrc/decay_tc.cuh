@@ -184,7 +184,7 @@ __device__ __forceinline__ void st_scaled8(uint32_t to, const float* v, f2 f) {
 // sequences; when the CTA is through, it does these again by the recurrence (walk_by_tokens).
 //
 // A thread of the state's warps: row `row` of S, columns [z0, z1) of its half, at `at` in TMEM; D's at `sum`.  `watch`: of
-// its half's four times 16 columns of D those that the thread looks at; the rows that S has share them.
+// its half's four times 16 columns of D those that the thread looks at; the rows that S has share them, and each has some.
 struct StateRow {
     int in, row, z0, z1;
     uint32_t at, sum, watch;
@@ -197,10 +197,12 @@ __device__ __forceinline__ StateRow state_row(const DecayPass& p, uint32_t tH, u
     r.z1 = min(r.z0 + 64, p.dz);
     r.at = tH + ((uint32_t)(in & 96) << 16);
     r.sum = r.at + tD - tH;
-    const int quads = (p.dx + 31) / 32;
+    const int quads = (p.dx + 31) / 32, quad = r.row >> 5;
     r.watch = 0;
-    if (r.row < p.dx)
-        for (int k = r.row >> 5; k < 4; k += quads) r.watch |= 1u << k;
+    if (r.row < p.dx) {
+        for (int k = quad; k < 4; k += quads) r.watch |= 1u << k;
+        if (r.z0 + 16 * quad >= p.dz) r.watch |= 1u;  // (columns that there are)
+    }
     return r;
 }
 

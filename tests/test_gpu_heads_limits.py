@@ -113,6 +113,8 @@ NOT_FINITE = [
     ("bf16", 1, 150, 4, 2, 64, 128, [-0.02, -0.9]),
     ("bf16", 1, 150, 10, 2, 40, 72, [-0.9, -0.02]),
     ("bf16", 1, 150, 20, 2, 64, 64, [-0.02, -0.9]),
+    ("bf16", 1, 150, 4, 2, 120, 24, [-0.02, -0.9]),
+    ("bf16", 1, 150, 2, 2, 16, 128, [-0.02, -1e6]),
     ("bf16", 1, 300, 2, 2, 128, 64, [-0.02, -0.9]),
     ("bf16", 1, 450, 76, 76, 32, 32, np.resize([-0.02, -0.9], 76)),
     ("bf16", 4, 200, 60, 20, 32, 32, np.resize([-0.02, -0.9], 20)),
@@ -138,8 +140,9 @@ def test_values_that_are_not_finite_reach_what_the_definition_says(lz, dtype, B,
         ends = {n: (a.clone(), w.copy()) for n, (a, w) in x.items()}
         dev, host = ends[which]
         head = h * (dev.shape[2] // Hkv) + t % (dev.shape[2] // Hkv)
-        dev[b, t, head, t % dev.shape[3]] = kind
-        host[b, t, head, t % dev.shape[3]] = kind
+        at = -1 - 5 * t % dev.shape[3]
+        dev[b, t, head, at] = kind
+        host[b, t, head, at] = kind
         s_out, ds0 = torch.empty_like(s0), torch.empty_like(s0)
         args = [ends[n][0] for n in ("q", "k", "v")]
         o = lz.lizard_decay_attn_fwd(*args, l, scale=scale, s0=s0, s_out=s_out)
